@@ -24,6 +24,7 @@ FA_ERR_MISALIGNED = 3
 FA_ERR_TOO_LARGE = 4
 FA_ERR_CUDA = 5
 FA_ERR_TIMEOUT = 6
+FA_ERR_BAD_INDEX = 7
 
 FA_BF16 = 0
 FA_FP16 = 1
@@ -35,6 +36,7 @@ FA_SCALE_TENSOR = 2
 # Every symbol include/fa.h declares (checked by the tests).
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_gqa_packed", "fa_fwd_ext", "fa_fwd_splitkv", "fa_splitkv_workspace_floats",
            "fa_splitkv_auto", "fa_quantize_fp8", "fa_quantize_fp8_granular", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_bwd", "fa_bwd_ext", "fa_bwd_noalloc",
+           "fa_paged_append", "fa_fwd_paged", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
            "fa_check_status", "fa_status_detail", "fa_selftest_wait_timeout",
            "fa_status_string", "fa_version")
 
@@ -87,6 +89,17 @@ def load():
     lib.fa_bwd_ext.restype = i
     lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i, vp]
     lib.fa_bwd_noalloc.restype = i
+    ll = ctypes.c_longlong
+    lib.fa_paged_append.argtypes = [vp] * 7 + [i] * 7 + [ll, ll, vp]
+    lib.fa_paged_append.restype = i
+    lib.fa_fwd_paged.argtypes = [vp] * 9 + [i] * 9 + [ll, ll, f, i, i, i, i, vp]
+    lib.fa_fwd_paged.restype = i
+    lib.fa_paged_workspace_bytes.argtypes = [i]
+    lib.fa_paged_workspace_bytes.restype = ll
+    lib.fa_paged_scores.argtypes = [vp] * 8 + [i] * 10 + [ll, ll, f, i, i, i, i, vp]
+    lib.fa_paged_scores.restype = i
+    lib.fa_paged_evict.argtypes = [vp] * 9 + [i] * 8 + [ll, i, i, i, vp]
+    lib.fa_paged_evict.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [vp, vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_check_status.argtypes = [vp]
@@ -386,6 +399,283 @@ def attention_backward(q, k, v, o, lse, dout, causal: bool = False,
     if rc != FA_OK:
         raise FaError(rc, "fa_bwd")
     return dq, dk, dv
+
+
+# ---- paged key/value cache (see include/fa.h) ----
+
+def fa_paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, B: int, H_kv: int, d: int,
+                    total_q: int, page_size: int, n_pages: int, table_width: int, kv_stride: int,
+                    page_stride: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h)."""
+    return load().fa_paged_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
+                                  _ptr(block_table), _ptr(kv_len), _ptr(cu_q), B, H_kv, d, total_q,
+                                  page_size, n_pages, table_width, kv_stride, page_stride,
+                                  _stream(stream))
+
+
+def fa_fwd_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, o, lse, workspace, B: int, H: int,
+                 H_kv: int, total_q: int, max_q: int, d: int, page_size: int, n_pages: int,
+                 table_width: int, q_stride: int, page_stride: int, alpha: float, window_left: int,
+                 window_right: int, first: int, dtype: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``lse`` may be None."""
+    return load().fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                               _ptr(kv_len), _ptr(cu_q), _ptr(o), _ptr(lse), _ptr(workspace), B, H,
+                               H_kv, total_q, max_q, d, page_size, n_pages, table_width, q_stride,
+                               page_stride, alpha, window_left, window_right, first, dtype,
+                               _stream(stream))
+
+
+def fa_paged_workspace_bytes(d: int) -> int:
+    return load().fa_paged_workspace_bytes(int(d))
+
+
+def fa_paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, scores_in, scores, B: int, H: int,
+                    H_kv: int, total_q: int, max_q: int, d: int, page_size: int, n_pages: int,
+                    table_width: int, score_width: int, q_stride: int, page_stride: int,
+                    alpha: float, window_left: int, window_right: int, first: int, dtype: int,
+                    stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``scores_in`` may
+    be None."""
+    return load().fa_paged_scores(_ptr(q), _ptr(lse), _ptr(k_pages), _ptr(block_table),
+                                  _ptr(kv_len), _ptr(cu_q), _ptr(scores_in), _ptr(scores), B, H,
+                                  H_kv, total_q, max_q, d, page_size, n_pages, table_width,
+                                  score_width, q_stride, page_stride, alpha, window_left,
+                                  window_right, first, dtype, _stream(stream))
+
+
+def fa_paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, kept, scores_out,
+                   new_len, B: int, H_kv: int, d: int, page_size: int, n_pages: int,
+                   table_width: int, dst_width: int, score_width: int, page_stride: int, keep: int,
+                   first: int, recent: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``scores_out`` may
+    be None."""
+    return load().fa_paged_evict(_ptr(k_pages), _ptr(v_pages), _ptr(scores), _ptr(block_table),
+                                 _ptr(kv_len), _ptr(dst_table), _ptr(kept), _ptr(scores_out),
+                                 _ptr(new_len), B, H_kv, d, page_size, n_pages, table_width,
+                                 dst_width, score_width, page_stride, keep, first, recent,
+                                 _stream(stream))
+
+
+def _check_paged(device, pools, ints, tensors=()):
+    """The layout that the C entry points are told by sizes and strides: pools
+    [n_pages, page_size, H_kv, d] of one 16-bit type with whole rows, int32
+    index tensors without gaps, everything on one device.  ``tensors``:
+    (tensor, shape, dtype or None) that must be contiguous."""
+    import torch
+    k = pools[0]
+    if k.dim() != 4:
+        raise ValueError("pages are [n_pages, page_size, H_kv, d]")
+    if k.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    n, ps, hk, d = k.shape
+    for x in pools:
+        if x.dtype != k.dtype or x.shape != k.shape or x.stride() != k.stride():
+            raise ValueError("k_pages and v_pages differ in type, shape or strides")
+        if x.stride()[1:] != (hk * d, d, 1) and x.numel():
+            raise ValueError("a page's rows [page_size, H_kv, d] must be contiguous")
+        if x.device != device:
+            raise ValueError("tensors on different devices")
+    for x, shape in ints:
+        if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous():
+            raise ValueError(f"index tensors are contiguous int32; expected {tuple(shape)}, got "
+                             f"{x.dtype} {tuple(x.shape)}")
+        if x.device != device:
+            raise ValueError("tensors on different devices")
+    for x, shape, dt in tensors:
+        if x.shape != shape or x.dtype != dt or not x.is_contiguous():
+            raise ValueError(f"expected a contiguous {dt} {tuple(shape)}, got {x.dtype} "
+                             f"{tuple(x.shape)}")
+        if x.device != device:
+            raise ValueError("tensors on different devices")
+
+
+def _packed_stride(x, name: str) -> int:
+    """The elements between the tokens of a packed [T, heads, d] tensor, whose
+    rows are whole (a slice of wider rows is fine)."""
+    if x.dim() != 3 or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+        raise ValueError(f"{name} is [T, heads, d] with contiguous [heads, d] rows")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+class _launch_on:
+    """Makes the tensors' device current and the launch stream the one that
+    torch allocates for, so that what a call allocates is reused only behind
+    its kernels: for a raw cudaStream_t, a torch stream, or None (the
+    device's current stream).  Gives the raw stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = device
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                      else torch.cuda.default_stream(device))
+        self.ctx = torch.cuda.stream(stream) if stream is not None else None
+        self.guard = (torch.cuda.device(device)
+                      if device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        import torch
+        if self.guard is not None:
+            self.guard.__enter__()
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def paged_workspace(d: int, device="cuda"):
+    """A workspace for ``attention_paged`` at head dim d (uint8 tensor); calls
+    that may overlap in time need one each."""
+    import torch
+    with torch.cuda.device(device):
+        n = fa_paged_workspace_bytes(d)
+        if n < 0:
+            raise FaError(FA_ERR_UNSUPPORTED, "fa_paged_workspace_bytes")
+        return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, stream=None) -> None:
+    """Writes the new tokens' K and V (packed [T, H_kv, d], rows of a wider
+    tensor allowed) into their pages [n_pages, page_size, H_kv, d]; kv_len
+    counts them already."""
+    B, W = block_table.shape
+    n, ps, hk, d = k_pages.shape
+    _check_paged(k.device, (k_pages, v_pages),
+                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))))
+    ks = _packed_stride(k, "k")
+    if (k.shape != v.shape or k.dtype != v.dtype or _packed_stride(v, "v") != ks
+            or v.device != k.device):
+        raise ValueError("k and v differ in type, shape, strides or device")
+    if k.dtype != k_pages.dtype or k.shape[1:] != (hk, d):
+        raise ValueError("k, v and the pages differ in type, heads or head dim")
+    with _launch_on(k.device, stream) as st:
+        rc = fa_paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, B, hk, d,
+                             k.shape[0], ps, n, W, ks, k_pages.stride(0), st)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_paged_append")
+
+
+def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, window=(-1, 0),
+                    first: int = 0, alpha: float | None = None, out=None, lse=None,
+                    want_lse: bool = True, workspace=None, stream=None):
+    """Attention of the new tokens (packed q [T, H, d], sequence b's in rows
+    cu_q[b] .. cu_q[b + 1]) over the cache that holds them: causal by default,
+    window = (left, right) key bounds around a token's position (-1: none),
+    the first ``first`` tokens visible beside a left bound.  ``max_q``: the
+    most new tokens of one sequence.  Returns (O [T, H, d], LSE [H, T] or
+    None)."""
+    import torch
+    T, H, d = q.shape
+    B, W = block_table.shape
+    n, ps, hk, dk = k_pages.shape
+    tensors = []
+    if out is not None:
+        tensors.append((out, q.shape, q.dtype))
+    if lse is not None:
+        tensors.append((lse, (H, T), torch.float32))
+    _check_paged(q.device, (k_pages, v_pages),
+                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))), tensors)
+    qs = _packed_stride(q, "q")
+    if q.dtype != k_pages.dtype or dk != d:
+        raise ValueError("q and the pages differ in type or head dim")
+    if alpha is None:
+        alpha = 1.0 / math.sqrt(d)
+    with _launch_on(q.device, stream) as st:
+        if out is None:
+            out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        need = fa_paged_workspace_bytes(d)
+        if workspace is None:
+            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
+        elif workspace.device != q.device or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"the workspace is {need} bytes on {q.device}")
+        rc = fa_fwd_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, out, lse, workspace, B, H,
+                          hk, T, int(max_q), d, ps, n, W, qs, k_pages.stride(0), alpha,
+                          int(window[0]), int(window[1]), int(first),
+                          FA_BF16 if q.dtype == torch.bfloat16 else FA_FP16, st)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged")
+    return out, lse
+
+
+def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=None,
+                 window=(-1, 0), first: int = 0, alpha: float | None = None, out=None, stream=None):
+    """The attention weight that every cached token gets from the new ones,
+    per K/V head, added to ``scores`` (float32 [B, H_kv, L], None: zeros); q,
+    lse, window, first and alpha as in ``attention_paged``.  ``out`` may be
+    ``scores``; entries behind kv_len are left as they were (zeros where it
+    is allocated here).  Returns out."""
+    import torch
+    T, H, d = q.shape
+    B, W = block_table.shape
+    n, ps, hk, dk = k_pages.shape
+    L = W * ps if scores is None else scores.shape[2]
+    if scores is None and out is not None:
+        L = out.shape[2]
+    tensors = [(lse, (H, T), torch.float32)]
+    for x in (scores, out):
+        if x is not None:
+            tensors.append((x, (B, hk, L), torch.float32))
+    _check_paged(q.device, (k_pages,),
+                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))), tensors)
+    qs = _packed_stride(q, "q")
+    if q.dtype != k_pages.dtype or dk != d:
+        raise ValueError("q and the pages differ in type or head dim")
+    if alpha is None:
+        alpha = 1.0 / math.sqrt(d)
+    with _launch_on(q.device, stream) as st:
+        if out is None:
+            out = torch.zeros((B, hk, L), dtype=torch.float32, device=q.device)
+        rc = fa_paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, scores, out, B, H, hk, T,
+                             int(max_q), d, ps, n, W, L, qs, k_pages.stride(0), alpha,
+                             int(window[0]), int(window[1]), int(first),
+                             FA_BF16 if q.dtype == torch.bfloat16 else FA_FP16, st)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_paged_scores")
+    return out
+
+
+def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: int, first: int = 0,
+                recent: int = 0, kept=None, scores_out=None, new_len=None, stream=None):
+    """Cuts every sequence to its ``keep`` most important tokens per K/V head
+    (the first ``first``, the last ``recent``, the others by ``scores``) and
+    writes them, in their order, into the pages of ``dst_table``.  Returns
+    (kept positions [B, H_kv, keep], their scores, new lengths); entries
+    behind a new length are left as they were (-1 and 0 where they are
+    allocated here)."""
+    import torch
+    B, W = block_table.shape
+    n, ps, hk, d = k_pages.shape
+    L, Wd, keep = scores.shape[2], dst_table.shape[1], int(keep)
+    ints = [(block_table, (B, W)), (kv_len, (B,)), (dst_table, (B, Wd))]
+    if kept is not None:
+        ints.append((kept, (B, hk, keep)))
+    if new_len is not None:
+        ints.append((new_len, (B,)))
+    tensors = [(scores, (B, hk, L), torch.float32)]
+    if scores_out is not None:
+        tensors.append((scores_out, (B, hk, keep), torch.float32))
+    _check_paged(scores.device, (k_pages, v_pages), ints, tensors)
+    dev = scores.device
+    with _launch_on(dev, stream) as st:
+        if kept is None:
+            kept = torch.full((B, hk, max(keep, 0)), -1, dtype=torch.int32, device=dev)
+        if scores_out is None:
+            scores_out = torch.zeros((B, hk, max(keep, 0)), dtype=torch.float32, device=dev)
+        if new_len is None:
+            new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        rc = fa_paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, kept,
+                            scores_out, new_len, B, hk, d, ps, n, W, Wd, L, k_pages.stride(0), keep,
+                            int(first), int(recent), st)
+    if rc != FA_OK:
+        raise FaError(rc, "fa_paged_evict")
+    return kept, scores_out, new_len
 
 
 def fa_selftest_wait_timeout(result, stream=None) -> int:

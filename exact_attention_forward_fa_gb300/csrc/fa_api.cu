@@ -11,13 +11,14 @@
 
 #include "fa.h"
 #include "fa_launch.cuh"
+#include "fa_paged.cuh"
 
 namespace {
 
 constexpr int kVersion = 100;   // 0.1.0
 
-// Set by kernels whose bounded waits give up: [0] code, [1] role,
-// [2] wait site, [3] block index.  One instance per device context.
+// Set by kernels whose bounded waits give up or that meet an index out of
+// range: [0] code, [1] role, [2] site, [3] block index.  One instance per device context.
 __device__ uint32_t g_fa_status[4];
 
 struct DeviceInfo {
@@ -139,6 +140,7 @@ const char *fa_status_string(fa_status s) {
         case FA_ERR_TOO_LARGE: return "FA_ERR_TOO_LARGE";
         case FA_ERR_CUDA: return "FA_ERR_CUDA";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
+        case FA_ERR_BAD_INDEX: return "FA_ERR_BAD_INDEX";
     }
     return "FA_ERR_UNKNOWN";
 }
@@ -728,6 +730,216 @@ fa_status fa_bwd_noalloc(const void *q, const void *k, const void *v, const void
                   stream);
 }
 
+// ---- paged key/value cache ----
+
+// What every entry point on a paged cache checks of its sizes; *ps_log2 gets
+// log2(page_size).
+static fa_status paged_checks(int B, int H_kv, int d, int page_size, int n_pages, int table_width,
+                              long long page_stride, const void *table, const void *kv_len,
+                              int *ps_log2) {
+    if (B < 1 || H_kv < 1 || d < 1 || page_size < 1 || n_pages < 1 || table_width < 1)
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (page_size < 8 || (page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+    if (page_stride < static_cast<long long>(page_size) * H_kv * d) return FA_ERR_INVALID_ARG;
+    if (page_stride % 8 != 0) return FA_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(table) & 3u) || (reinterpret_cast<uintptr_t>(kv_len) & 3u))
+        return FA_ERR_MISALIGNED;
+    // TMA: every global stride < 2^40 bytes; B and H_kv are grid dimensions
+    if (page_stride >= (1ll << 39) || B > 65535 || H_kv > 65535) return FA_ERR_TOO_LARGE;
+    int l = 0;
+    while ((1 << l) < page_size) ++l;
+    *ps_log2 = l;
+    return FA_OK;
+}
+
+fa_status fa_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                          const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q,
+                          int B, int H_kv, int d, int total_q, int page_size, int n_pages,
+                          int table_width, long long kv_stride, long long page_stride,
+                          void *stream) {
+    if (!k_pages || !v_pages || !block_table || !kv_len || !cu_q) return FA_ERR_INVALID_ARG;
+    if (total_q < 0 || (total_q > 0 && (!k || !v))) return FA_ERR_INVALID_ARG;
+    fa::PagedAppendArgs a;
+    fa_status st = paged_checks(B, H_kv, d, page_size, n_pages, table_width, page_stride, block_table,
+                                kv_len, &a.ps_log2);
+    if (st != FA_OK) return st;
+    if (kv_stride < static_cast<long long>(H_kv) * d) return FA_ERR_INVALID_ARG;
+    if (kv_stride % 8 != 0 || !aligned16(k) || !aligned16(v) || !aligned16(k_pages) ||
+        !aligned16(v_pages) || (reinterpret_cast<uintptr_t>(cu_q) & 3u))
+        return FA_ERR_MISALIGNED;
+    if (kv_stride >= (1ll << 39)) return FA_ERR_TOO_LARGE;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    if (total_q == 0) return FA_OK;
+    a.k = k;
+    a.v = v;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.table = block_table;
+    a.kv_len = kv_len;
+    a.cu_q = cu_q;
+    a.status = dev->status;
+    a.kv_stride = kv_stride;
+    a.page_stride = page_stride;
+    a.B = B;
+    a.T = total_q;
+    a.W = table_width;
+    a.n_pages = n_pages;
+    a.row_vecs = H_kv * (d / 8);
+    return fa::launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                       : FA_ERR_CUDA;
+}
+
+// The arguments that fa_fwd_paged and fa_paged_scores share, checked and laid
+// out (pointers that differ are the caller's).
+static fa_status paged_attn_args(fa::PagedArgs *a, const void *q, const void *k_pages,
+                                 const int32_t *block_table, const int32_t *kv_len,
+                                 const int32_t *cu_q, const float *lse, int B, int H, int H_kv,
+                                 int total_q, int max_q, int d, int page_size, int n_pages,
+                                 int table_width, long long q_stride, long long page_stride,
+                                 float alpha, int window_left, int window_right, int first,
+                                 fa_dtype dtype) {
+    std::memset(a, 0, sizeof(*a));
+    if (!k_pages || !block_table || !kv_len || !cu_q) return FA_ERR_INVALID_ARG;
+    if (total_q < 0 || (total_q > 0 && !q) || max_q < 1 || first < 0 || H < 1) return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1 || !std::isfinite(alpha)) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    fa_status st = paged_checks(B, H_kv, d, page_size, n_pages, table_width, page_stride, block_table,
+                                kv_len, &a->ps_log2);
+    if (st != FA_OK) return st;
+    if (H % H_kv != 0 || q_stride < static_cast<long long>(H) * d) return FA_ERR_INVALID_ARG;
+    if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;      // a tile holds the heads of a group
+    if (q_stride % 8 != 0 || !aligned16(q) || !aligned16(k_pages) ||
+        (reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return FA_ERR_MISALIGNED;
+    if (q_stride >= (1ll << 39)) return FA_ERR_TOO_LARGE;
+    a->q = q;
+    a->k_pages = k_pages;
+    a->table = block_table;
+    a->kv_len = kv_len;
+    a->cu_q = cu_q;
+    a->q_stride = q_stride;
+    a->page_stride = page_stride;
+    a->B = B;
+    a->H = H;
+    a->H_kv = H_kv;
+    a->group = H / H_kv;
+    a->T = total_q;
+    a->W = table_width;
+    a->n_pages = n_pages;
+    a->wl = window_left;
+    a->wr = window_right;
+    a->first = first;
+    a->scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    return FA_OK;
+}
+
+long long fa_paged_workspace_bytes(int d) {
+    if (d != 64 && d != 128) return -1;
+    DeviceInfo *dev = nullptr;
+    if (get_device(&dev) != FA_OK) return -1;
+    return 256;
+}
+
+fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
+                       const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q,
+                       void *o, float *lse, void *workspace, int B, int H, int H_kv, int total_q,
+                       int max_q, int d, int page_size, int n_pages, int table_width,
+                       long long q_stride, long long page_stride, float alpha, int window_left,
+                       int window_right, int first, fa_dtype dtype, void *stream) {
+    if (!v_pages || !workspace || (total_q > 0 && !o)) return FA_ERR_INVALID_ARG;
+    fa::PagedArgs a;
+    fa_status st = paged_attn_args(&a, q, k_pages, block_table, kv_len, cu_q, lse, B, H, H_kv, total_q,
+                                   max_q, d, page_size, n_pages, table_width, q_stride, page_stride,
+                                   alpha, window_left, window_right, first, dtype);
+    if (st != FA_OK) return st;
+    if (!aligned16(v_pages) || !aligned16(o) || !aligned16(workspace)) return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    if (total_q == 0) return FA_OK;
+    a.v_pages = v_pages;
+    a.o = o;
+    a.lse = lse;
+    a.status = dev->status;
+    return fa::launch_fwd_paged(a, d, dtype == FA_BF16, dev->sm_count,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
+                          const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q,
+                          const float *scores_in, float *scores, int B, int H, int H_kv, int total_q,
+                          int max_q, int d, int page_size, int n_pages, int table_width,
+                          int score_width, long long q_stride, long long page_stride, float alpha,
+                          int window_left, int window_right, int first, fa_dtype dtype,
+                          void *stream) {
+    if (!scores || score_width < 1 || (total_q > 0 && !lse)) return FA_ERR_INVALID_ARG;
+    fa::PagedScoresArgs g;
+    fa_status st = paged_attn_args(&g.p, q, k_pages, block_table, kv_len, cu_q, lse, B, H, H_kv,
+                                   total_q, max_q, d, page_size, n_pages, table_width, q_stride,
+                                   page_stride, alpha, window_left, window_right, first, dtype);
+    if (st != FA_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(scores_in) & 3u) || (reinterpret_cast<uintptr_t>(scores) & 3u))
+        return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    g.p.lse = const_cast<float *>(lse);
+    g.p.status = dev->status;
+    g.in = scores_in;
+    g.out = scores;
+    g.L = score_width;
+    return fa::launch_paged_scores(g, d, dtype == FA_BF16, dev->sm_count,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
+                         const int32_t *block_table, const int32_t *kv_len,
+                         const int32_t *dst_table, int32_t *kept, float *scores_out,
+                         int32_t *new_len, int B, int H_kv, int d, int page_size, int n_pages,
+                         int table_width, int dst_width, int score_width, long long page_stride,
+                         int keep, int first, int recent, void *stream) {
+    if (!k_pages || !v_pages || !scores || !block_table || !kv_len || !dst_table || !kept || !new_len)
+        return FA_ERR_INVALID_ARG;
+    fa::PagedEvictArgs a;
+    fa_status st = paged_checks(B, H_kv, d, page_size, n_pages, table_width, page_stride, block_table,
+                                kv_len, &a.ps_log2);
+    if (st != FA_OK) return st;
+    if (keep < 1 || first < 0 || recent < 0 || first > keep || recent > keep - first || dst_width < 1 ||
+        score_width < 1)
+        return FA_ERR_INVALID_ARG;
+    if ((static_cast<long long>(dst_width) << a.ps_log2) < keep) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(scores) & 3u) || (reinterpret_cast<uintptr_t>(dst_table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(kept) & 3u) || (reinterpret_cast<uintptr_t>(scores_out) & 3u) ||
+        (reinterpret_cast<uintptr_t>(new_len) & 3u))
+        return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.scores = scores;
+    a.table = block_table;
+    a.kv_len = kv_len;
+    a.dst_table = dst_table;
+    a.kept = kept;
+    a.scores_out = scores_out;
+    a.new_len = new_len;
+    a.status = dev->status;
+    a.page_stride = page_stride;
+    a.B = B;
+    a.H_kv = H_kv;
+    a.d = d;
+    a.W = table_width;
+    a.dst_W = dst_width;
+    a.n_pages = n_pages;
+    a.L = score_width;
+    a.keep = keep;
+    a.first = first;
+    a.recent = recent;
+    return fa::launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                      : FA_ERR_CUDA;
+}
+
 fa_status fa_check_status(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
     DeviceInfo *dev = nullptr;
@@ -744,7 +956,7 @@ fa_status fa_check_status(void *stream) {
     const uint32_t zero[4] = {0, 0, 0, 0};
     if (cudaMemcpy(dev->status, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
         return FA_ERR_CUDA;
-    return FA_ERR_TIMEOUT;
+    return h[0] == fa::kStatusBadIndex ? FA_ERR_BAD_INDEX : FA_ERR_TIMEOUT;
 }
 
 fa_status fa_selftest_wait_timeout(uint32_t *result, void *stream) {

@@ -19,17 +19,21 @@
  *                                 element (b,n,h,c) at ((b*N + n)*H + h)*d + c
  *     LSE        : [B][H][N]      float32, element (b,h,n) at (b*H + h)*N + n
  *     FP8 scales : [B][H][ceil(N/128)] float32, one per 128-row tile of a head
+ *     paged cache: pools of pages with their own strides (see "Paged
+ *                  key/value cache" below)
  *
  * Conventions for every entry point:
- *   * Pointers named q, k, v, o, lse, x, x8, *_scale are DEVICE pointers
- *     owned by the caller; the library never frees or keeps them.
+ *   * Pointers named q, k, v, o, lse, x, x8, *_scale, *_pages, *_table,
+ *     scores*, kv_len, cu_q, kept, new_len are DEVICE pointers owned by the
+ *     caller; the library never frees or keeps them.
  *   * `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Calls are asynchronous: they validate, launch and return.
  *   * Arguments are validated on the host before anything is launched; a
  *     failed check returns an error code and launches nothing.
  *   * The library allocates no device memory per call.  It owns one small
  *     per-device status word in a static __device__ variable that kernels
- *     set when a bounded wait gives up; fa_check_status reads it.
+ *     set when a bounded wait gives up or a device-side index is out of
+ *     range; fa_check_status reads it.
  *   * Results are deterministic for fixed inputs: fixed reduction order, no
  *     atomics on outputs.
  *   * Thread safety: entry points may be called from several host threads;
@@ -51,7 +55,9 @@ typedef enum {
     FA_ERR_MISALIGNED = 3,   /* a tensor pointer is not 16-byte aligned (TMA rule) */
     FA_ERR_TOO_LARGE = 4,    /* a size exceeds the TMA descriptor limits */
     FA_ERR_CUDA = 5,         /* a CUDA runtime/driver call or the launch failed */
-    FA_ERR_TIMEOUT = 6       /* a kernel's bounded wait gave up (fa_check_status) */
+    FA_ERR_TIMEOUT = 6,      /* a kernel's bounded wait gave up (fa_check_status) */
+    FA_ERR_BAD_INDEX = 7     /* a page id, length or offset in device memory was out of
+                                range; the access was skipped (fa_check_status) */
 } fa_status;
 
 typedef enum {
@@ -347,21 +353,162 @@ fa_status fa_bwd_noalloc(const void *q, const void *k, const void *v,
                          void *stream);
 
 /*
+ * Paged key/value cache: the entry points that answer from a cache of past
+ * keys and values instead of dense tensors with Nq = Nk.
+ *
+ * The cache.  k_pages and v_pages are pools of pages, element (page, slot,
+ * K/V head, c) at page * page_stride + (slot * H_kv + head) * d + c in
+ * `dtype`: page_size slots of H_kv x d, page_stride >= page_size * H_kv * d
+ * elements from page to page (one pool with K and V side by side in a page
+ * has twice that), a multiple of 8.  page_size is a power of two >= 8.
+ * Token p of sequence b is slot p % page_size of page
+ * block_table[b * table_width + p / page_size]; kv_len[b] tokens are cached.
+ * Sequences may share pages that none of them writes.
+ *
+ * The new tokens of a call are packed: rows cu_q[b] .. cu_q[b + 1] (cu_q has
+ * B + 1 entries, ascending) of tensors with total_q rows are sequence b's
+ * last cached tokens, kv_len[b] counts them, and row cu_q[b] + i has position
+ * kv_len[b] - (cu_q[b + 1] - cu_q[b]) + i.  A sequence may have none.  Rows
+ * at and behind cu_q[B] are neither read nor written.  With total_q = 0 the
+ * packed tensors may be NULL.
+ *
+ * block_table, kv_len and cu_q are device int32, so lengths may change from
+ * one replay of a captured graph to the next.  What is out of range there (a
+ * page id a call needs outside [0, n_pages), kv_len outside [0, table_width *
+ * page_size], cu_q outside [0, total_q] or falling) is cut off: that access is
+ * skipped, the row's result is undefined, and the next fa_check_status
+ * returns FA_ERR_BAD_INDEX.  Entries of block_table that no visible token
+ * needs are not looked at, and slots at and behind kv_len may hold anything
+ * (NaN included).
+ *
+ * d in {64, 128}, other head dims and page sizes give FA_ERR_UNSUPPORTED;
+ * B, H_kv <= 65535.
+ */
+
+/*
+ * fa_paged_append -- writes the new tokens' keys and values into their pages.
+ *   k, v : device, total_q rows of [H_kv][d], kv_stride elements from row to
+ *          row (>= H_kv * d, a multiple of 8: a slice of a fused projection's
+ *          rows is fine), 16-byte aligned.
+ * Tokens with a negative position (more new tokens than kv_len counts) are
+ * dropped.  Any 16-bit element type.
+ */
+fa_status fa_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                          const int32_t *block_table, const int32_t *kv_len,
+                          const int32_t *cu_q, int B, int H_kv, int d, int total_q,
+                          int page_size, int n_pages, int table_width, long long kv_stride,
+                          long long page_stride, void *stream);
+
+/*
+ * fa_fwd_paged -- exact attention of the new tokens over the cache (which
+ * already holds them), with grouped K/V heads as in fa_fwd_gqa:
+ *     S = alpha * q K^T over the visible keys, O = softmax(S) V,
+ *     LSE = log sum exp(S).
+ * Key j is visible to the row at position p when j < kv_len and
+ *     j <= p + window_right            (window_right >= 0; -1: no bound), and
+ *     j >= p - window_left  or  j < first   (window_left >= 0; -1: no bound):
+ * (-1, 0) is causal, (-1, -1) no mask, and with a left bound the first
+ * `first` tokens of the sequence stay visible beside the sliding window.  A
+ * row that sees no key gives O = 0, LSE = -inf.
+ *   q    : device, total_q rows of [H][d], q_stride elements from row to row
+ *          (>= H * d, a multiple of 8), 16-byte aligned.
+ *   o    : device, [total_q][H][d], 16-byte aligned (written).
+ *   lse  : device, float [H][total_q], or NULL to skip.
+ *   workspace : device, fa_paged_workspace_bytes(d) bytes, 16-byte aligned,
+ *          caller-owned; nothing in it needs to start at zero.  Calls that
+ *          may overlap in time need one each.
+ *   max_q : the most new tokens of one sequence, >= 1; it only chooses tile
+ *          shapes (a larger sequence is still computed in full).
+ *   H / H_kv <= 128, else FA_ERR_UNSUPPORTED.
+ * Accumulation is FP32, P is rounded to `dtype` before the P V product.
+ * The key ranges of all rows together are cut into equal shares for the SMs
+ * and the shares' results joined in a fixed order: the same call repeats its
+ * bits, but where a sequence is cut depends on the whole batch's lengths.
+ */
+fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
+                       const int32_t *block_table, const int32_t *kv_len,
+                       const int32_t *cu_q, void *o, float *lse, void *workspace, int B,
+                       int H, int H_kv, int total_q, int max_q, int d, int page_size,
+                       int n_pages, int table_width, long long q_stride,
+                       long long page_stride, float alpha, int window_left,
+                       int window_right, int first, fa_dtype dtype, void *stream);
+
+/* fa_paged_workspace_bytes -- workspace of fa_fwd_paged on the current
+ * device, whatever the problem's other sizes; -1 for a head dim without a
+ * kernel or without an sm_103 device. */
+long long fa_paged_workspace_bytes(int d);
+
+/*
+ * fa_paged_scores -- the attention weight that every cached token gets from
+ * the new ones, summed over the rows and over the query heads of each K/V
+ * head, on top of what it had:
+ *     scores[b][h][j] = (j older than the new tokens ? scores_in[b][h][j] : 0)
+ *                       + sum over rows i that see j, heads of group h, of
+ *                         exp(alpha q_i . k_j - LSE_i)
+ * for j < kv_len[b]; the rest of scores is left as it was.
+ *   lse    : device, float [H][total_q], from fa_fwd_paged with the same
+ *            arguments (rows with LSE = -inf add nothing).
+ *   scores_in, scores : device, float [B][H_kv][score_width]; scores_in may
+ *            be scores itself, or NULL for zeros.  score_width >= every
+ *            kv_len (longer ones are cut off: FA_ERR_BAD_INDEX).
+ * Summed in FP32 in a fixed order, without atomics.  Other arguments as
+ * fa_fwd_paged.
+ */
+fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
+                          const int32_t *block_table, const int32_t *kv_len,
+                          const int32_t *cu_q, const float *scores_in, float *scores, int B,
+                          int H, int H_kv, int total_q, int max_q, int d, int page_size,
+                          int n_pages, int table_width, int score_width, long long q_stride,
+                          long long page_stride, float alpha, int window_left,
+                          int window_right, int first, fa_dtype dtype, void *stream);
+
+/*
+ * fa_paged_evict -- cuts every sequence of the cache to its `keep` most
+ * important tokens, for each K/V head by itself: the first `first`, the last
+ * `recent`, and of the others those with the largest score (equal scores: the
+ * lower position; NaN ranks above +inf).  The kept tokens go, in their order,
+ * to positions 0, 1, ... of the pages of dst_table (their slots then hold
+ * different tokens for different heads); a sequence of at most `keep` tokens
+ * keeps all.  The old pages are left as they were: other sequences may share
+ * them, and the caller frees them.
+ *   scores : device, float [B][H_kv][score_width] (fa_paged_scores).
+ *   dst_table : device, int32 [B][dst_width], pages of the same pools that no
+ *            sequence of the call reads and no two entries name twice;
+ *            dst_width * page_size >= keep.
+ *   kept   : device, int32 [B][H_kv][keep] (written): the kept tokens' old
+ *            positions, ascending; entries at and behind new_len[b] are left.
+ *   scores_out : device, float [B][H_kv][keep], their scores (as kept), or
+ *            NULL.  Not scores itself.
+ *   new_len : device, int32 [B] (written): min(kv_len[b], keep).
+ *   keep >= 1, first, recent >= 0, first + recent <= keep.
+ * Any 16-bit element type.  kv_len beyond score_width is cut off.
+ */
+fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
+                         const int32_t *block_table, const int32_t *kv_len,
+                         const int32_t *dst_table, int32_t *kept, float *scores_out,
+                         int32_t *new_len, int B, int H_kv, int d, int page_size,
+                         int n_pages, int table_width, int dst_width, int score_width,
+                         long long page_stride, int keep, int first, int recent,
+                         void *stream);
+
+/*
  * fa_check_status -- synchronizes `stream`, then reports and clears the
  * device status word of the current device.  Returns FA_ERR_TIMEOUT if a
  * kernel launched since the last check gave up on a bounded wait (its
- * outputs are then undefined), FA_ERR_CUDA if the synchronization failed,
- * FA_OK otherwise.
+ * outputs are then undefined), FA_ERR_BAD_INDEX if one met an index out of
+ * range in device memory, FA_ERR_CUDA if the synchronization failed, FA_OK
+ * otherwise.  (The first of several events is the one reported.)
  */
 fa_status fa_check_status(void *stream);
 
 /*
  * fa_status_detail -- the status word captured by the last fa_check_status
- * that returned FA_ERR_TIMEOUT: out[0] code, out[1] role that gave up
- * (1/2 softmax group L/H, 3 producer, 4 MMA issuer, 6 FP8 pre-pass,
- * 7 self-test),
- * out[2] wait site,
- * out[3] block index.  Zeros if no timeout was ever reported.
+ * that returned FA_ERR_TIMEOUT or FA_ERR_BAD_INDEX: out[0] code, out[1] role
+ * that gave up (1/2 softmax group L/H, 3 producer, 4 MMA issuer, 6 FP8
+ * pre-pass, 7 self-test, 8 paged cache),
+ * out[2] wait site (bad index: 1 kv_len or cu_q, 2 page id, 3 kv_len beyond
+ * the scores),
+ * out[3] block index.  Zeros if nothing was ever reported.
  */
 void fa_status_detail(uint32_t out[4]);
 
