@@ -803,7 +803,10 @@ static fa_status paged_attn_args(fa::PagedArgs *a, const void *q, const void *k_
     std::memset(a, 0, sizeof(*a));
     if (!k_pages || !block_table || !kv_len || !cu_q) return FA_ERR_INVALID_ARG;
     if (total_q < 0 || (total_q > 0 && !q) || max_q < 1 || first < 0 || H < 1) return FA_ERR_INVALID_ARG;
-    if (window_left < -1 || window_right < -1 || !std::isfinite(alpha)) return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+    // a hidden score is -inf before it is scaled, and the largest stays the largest
+    const float scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    if (!std::isnormal(scale_log2) || scale_log2 < 0.f) return FA_ERR_INVALID_ARG;
     if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
     fa_status st = paged_checks(B, H_kv, d, page_size, n_pages, table_width, page_stride, block_table,
                                 kv_len, &a->ps_log2);
@@ -831,7 +834,7 @@ static fa_status paged_attn_args(fa::PagedArgs *a, const void *q, const void *k_
     a->wl = window_left;
     a->wr = window_right;
     a->first = first;
-    a->scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    a->scale_log2 = scale_log2;
     return FA_OK;
 }
 
@@ -839,7 +842,39 @@ long long fa_paged_workspace_bytes(int d) {
     if (d != 64 && d != 128) return -1;
     DeviceInfo *dev = nullptr;
     if (get_device(&dev) != FA_OK) return -1;
-    return 256;
+    // per CTA: one descriptor of 8 ints, two parts of 2 x 128 rows of O and LSE
+    return static_cast<long long>(dev->sm_count) * (32 + 2 * 256 * 4 * (1 + d));
+}
+
+// The pool of pages as {d, H_kv, page_size, n_pages}: a box is up to 128 slots
+// of one head in one page; pages beyond the pool read as zero.
+static fa_status encode_pages(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt,
+                              const fa::PagedArgs &a, int d) {
+    const cuuint64_t ps = 1ull << a.ps_log2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.H_kv), ps,
+                          static_cast<cuuint64_t>(a.n_pages)};
+    cuuint64_t strides[3] = {2ull * d, 2ull * d * a.H_kv, 2ull * static_cast<cuuint64_t>(a.page_stride)};
+    cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(ps < 128 ? ps : 128), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, dt, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// The packed queries as {d, H, T, 1}: a box is R positions of one group's heads.
+static fa_status encode_packed_q(CUtensorMap *m, CUtensorMapDataType dt, const fa::PagedArgs &a,
+                                 int d, int R) {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.H),
+                          static_cast<cuuint64_t>(a.T), 1};
+    const cuuint64_t tok = 2ull * static_cast<cuuint64_t>(a.q_stride);
+    cuuint64_t strides[3] = {2ull * d, tok, tok};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.group), static_cast<cuuint32_t>(R), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, dt, 4, const_cast<void *>(a.q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
@@ -849,12 +884,15 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
                        long long q_stride, long long page_stride, float alpha, int window_left,
                        int window_right, int first, fa_dtype dtype, void *stream) {
     if (!v_pages || !workspace || (total_q > 0 && !o)) return FA_ERR_INVALID_ARG;
-    fa::PagedArgs a;
+    fa::PagedFwdLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    fa::PagedArgs &a = L.a;
     fa_status st = paged_attn_args(&a, q, k_pages, block_table, kv_len, cu_q, lse, B, H, H_kv, total_q,
                                    max_q, d, page_size, n_pages, table_width, q_stride, page_stride,
                                    alpha, window_left, window_right, first, dtype);
     if (st != FA_OK) return st;
-    if (!aligned16(v_pages) || !aligned16(o) || !aligned16(workspace)) return FA_ERR_MISALIGNED;
+    if (!aligned16(v_pages) || !aligned16(o) || (reinterpret_cast<uintptr_t>(workspace) & 31u))
+        return FA_ERR_MISALIGNED;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
     if (total_q == 0) return FA_OK;
@@ -862,8 +900,31 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     a.o = o;
     a.lse = lse;
     a.status = dev->status;
-    return fa::launch_fwd_paged(a, d, dtype == FA_BF16, dev->sm_count,
-                                static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    L.d = d;
+    L.bf16 = dtype == FA_BF16;
+    L.stream = static_cast<cudaStream_t>(stream);
+    // Q tiles of R positions: as many as fit 128 rows, fewer when no sequence
+    // has that many (a single token's box is then one position).
+    const int fit = 128 / a.group;
+    L.R = max_q < fit ? max_q : fit;
+    const CUtensorMapDataType dt =
+        L.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if ((st = encode_packed_q(&L.q, dt, a, d, L.R)) != FA_OK) return st;
+    if ((st = encode_pages(&L.k, k_pages, dt, a, d)) != FA_OK) return st;
+    if ((st = encode_pages(&L.v, v_pages, dt, a, d)) != FA_OK) return st;
+    // CTAs: one per SM, fewer when even the longest cache has not q_min steps
+    // for each.
+    L.q_min = 2;
+    const uint64_t units = static_cast<uint64_t>(B) + static_cast<uint64_t>(total_q) / (2 * L.R);
+    const uint64_t tiles = ((static_cast<uint64_t>(table_width) << a.ps_log2) + 127) / 128;
+    const uint64_t share = (units * tiles + L.q_min - 1) / L.q_min;     // shares of one K/V head
+    const uint64_t sm = static_cast<uint64_t>(dev->sm_count);
+    L.grid = static_cast<int>(share >= sm ? sm : share * H_kv < sm ? share * H_kv : sm);
+    L.w.desc = static_cast<int *>(workspace);
+    L.w.lse = reinterpret_cast<float *>(L.w.desc + 8 * dev->sm_count);
+    L.w.o = L.w.lse + static_cast<size_t>(dev->sm_count) * 2 * 256;
+    const cudaError_t e = d == 64 ? fa::launch_fwd_paged_d64(L) : fa::launch_fwd_paged_d128(L);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,

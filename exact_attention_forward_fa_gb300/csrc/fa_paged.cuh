@@ -128,8 +128,25 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t stream);
 
-cudaError_t launch_fwd_paged(const PagedArgs &a, int d, bool bf16, int sm_count,
-                             cudaStream_t stream);
+// The workspace of the attention: what the parts of cut units leave.
+struct PagedWork {
+    int *desc;          // [CTAs][8]: the cut unit that starts in a CTA's share
+    float *lse;         // [2 * CTAs][2][128], log2 units
+    float *o;           // [2 * CTAs][2][128][d], normalised
+};
+struct PagedFwdLaunch {
+    CUtensorMap q;      // {d, H, T, 1}, box {64, group, R, 1}, 128-byte swizzle
+    CUtensorMap k, v;   // {d, H_kv, page_size, n_pages}, box {64, 1, min(page_size, 128), 1}
+    PagedArgs a;
+    PagedWork w;
+    int R;              // positions per Q tile
+    int q_min;          // fewest steps of a share
+    int grid, d;
+    bool bf16;
+    cudaStream_t stream;
+};
+cudaError_t launch_fwd_paged_d64(const PagedFwdLaunch &L);
+cudaError_t launch_fwd_paged_d128(const PagedFwdLaunch &L);
 
 struct PagedScoresArgs {
     PagedArgs p;                   // lse: read here

@@ -1,0 +1,856 @@
+// fa_paged_fwd_kernel.cuh -- attention of new tokens over a paged cache on
+// sm_103a (tcgen05 + TMA), one kernel from single tokens to long chunks.
+//
+// Rows.  The g = H / H_kv query heads of a K/V head share each Q tile: tile
+// row p holds the tile's position p / g, head p % g, R positions a tile
+// (R g <= 128), so one pass over a K/V head's pages serves the group.
+//
+// Units.  A unit is a pair of Q tiles (L, H) of one (sequence, K/V head).  Its
+// steps are the 128-key tiles that any of its rows sees, from the last to the
+// first, the sliding window's first and then those of the first tokens.
+//   * Two tiles: both softmax groups walk every step, each for its own tile
+//     (the schedule of fa_fwd_kernel.cuh): 256 rows per K/V tile read.
+//   * One tile (single tokens and short chunks): the groups take the steps in
+//     turn, each with an accumulator of its own, joined in TMEM at the end.
+//     The chain QK -> softmax -> PV of a step is as long as two K/V tiles
+//     take from HBM, so two chains side by side keep the loads going.
+//
+// Shares.  Lengths are known on the device only.  Every CTA adds up the
+// steps of all units (a scan over the sequences by all its threads), takes
+// the share [c Q, (c + 1) Q) of them, Q = ceil(total / CTAs), and walks it:
+// whole units are written to O; of a unit that a share's border cuts, each
+// part leaves its normalised O and LSE in the workspace (at most two parts a
+// CTA) and fa_paged_combine_kernel joins them in order.  Shares differ by one
+// step at most, whatever the lengths.
+//
+// Warps: 0-3 and 4-7 the softmax groups, 8 the TMA producer (all lanes: one
+// box of a page each), 9 the MMA issuer, 10 walks the share and posts its
+// pieces in a ring that the others read.
+//
+// Pages.  A 128-key tile is 128 / page_size boxes (or part of one page).  A
+// page that no row of the unit sees, or a bad id, is loaded from beyond the
+// pool, which TMA fills with zeros.  In a tile that the unit sees in part, the
+// rows of V outside are set to zero in shared memory before the product:
+// their probabilities are 0, but 0 times a NaN left in a slot is not.
+// Every mbarrier wait is bounded (fa_device.cuh).
+#pragma once
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+template <int D, bool kBF16>
+struct PagedCfg {
+    static constexpr int NCH = D / 64;                    // 128-byte column chunks
+    static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
+    static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
+    static constexpr int NSTAGE = D == 64 ? 8 : 4;        // powers of two
+    static constexpr int NQ = 3;
+    static constexpr int QK_STEPS = D / 16, PV_STEPS = 8;
+    static constexpr int NTHREADS = 384;
+    static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
+    static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register budget");
+    static constexpr int RING = 4;                        // pieces ahead
+    static constexpr uint32_t Q_OFF = 0;
+    static constexpr uint32_t KV_OFF = NQ * TILE_BYTES;
+    static constexpr uint32_t X_OFF = KV_OFF + NSTAGE * TILE_BYTES;   // group H's LSE, 1 / l
+    static constexpr uint32_t RING_OFF = X_OFF + 2 * 128 * 4;
+    static constexpr uint32_t BAR_OFF = RING_OFF + RING * 64;
+    static constexpr int B_QFULL = 0, B_QEMPTY = NQ, B_KVFULL = 2 * NQ, B_KVEMPTY = B_KVFULL + NSTAGE,
+                         B_SFULL = B_KVEMPTY + NSTAGE, B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 2,
+                         B_OEMPTY = B_OFULL + 2, B_XFULL = B_OEMPTY + 2, B_XEMPTY = B_XFULL + 1,
+                         B_MMADONE = B_XEMPTY + 1, B_PIECE = B_MMADONE + 1, B_FREE = B_PIECE + RING,
+                         NBAR = B_FREE + RING;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
+    static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+    static constexpr uint32_t TMEM_COLS = 512;
+    __host__ __device__ static constexpr uint32_t col_s(int x) { return x ? 128u : 0u; }
+    __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + (x ? D : 0u); }
+    static constexpr uint32_t IDESC_QK = idesc_f16(128, 128, kBF16, false, false);
+    static constexpr uint32_t IDESC_PV = idesc_f16(128, D, kBF16, false, true);
+    // fa_fwd_kernel.cuh: the conditional rescale, tau in log2 units, and the
+    // row sum below which a tile's P against the old reference is kept.
+    static constexpr float TAU = 8.0f, KEEP_SUM = 65536.0f;
+};
+
+// One piece of a share, as posted in the ring.
+struct __align__(16) PagedPiece {
+    int qrow;           // packed row of tile L's first position; -1: no more pieces
+    int nl, nh;         // positions in tiles L and H (nh = 0: one tile)
+    int pos;            // cache position of tile L's first position
+    int n, b, h;        // cached tokens, sequence, K/V head
+    int hi, nw, T;      // one past the last key tile, steps in the window, all steps
+    int t0, t1;         // this piece's steps
+    int skip;           // steps that tile L does not see
+    int slot;           // part in the workspace, or -1: the whole unit
+    int vlo, vhi;       // keys of the window that any row sees
+};
+static_assert(sizeof(PagedPiece) == 64, "piece ring");
+
+// The key tile of step t.
+__device__ __forceinline__ int paged_tile(const PagedPiece &p, int t) {
+    return t < p.nw ? p.hi - 1 - t : (p.T - 1) - t;
+}
+
+// Key tiles that rows at positions pa .. pb (of n cached tokens) see.
+struct PagedTiles { int hi, nw, T; };
+__device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, const PagedArgs &a) {
+    const int khi = paged_hi(pb, n, a.wr);
+    PagedTiles t;
+    t.hi = (khi >> 7) + ((khi & 127) != 0);
+    const int lo = min(paged_lo(pa, a.wl) >> 7, t.hi);
+    const int f = min(a.first, khi);
+    t.nw = t.hi - lo;
+    t.T = max(1, t.nw + min((f >> 7) + ((f & 127) != 0), lo));   // an empty unit still writes O = 0
+    return t;
+}
+// Steps of unit p of a sequence (2 R positions a unit).
+__device__ __forceinline__ int paged_unit_steps(const PagedSeq &s, int p, int R, const PagedArgs &a) {
+    const int i0 = p * 2 * R;
+    return paged_tiles(s.n - s.m + i0, s.n - s.m + min(s.m, i0 + 2 * R) - 1, s.n, a).T;
+}
+__device__ __forceinline__ int paged_units(const PagedSeq &s, int R) {
+    return static_cast<int>((static_cast<long long>(s.m) + 2 * R - 1) / (2 * R));
+}
+// Steps of all units of a sequence, by the whole warp.
+__device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int R, const PagedArgs &a) {
+    const int np = paged_units(s, R);
+    long long sum = 0;
+    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s, p, R, a);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(384, 1)
+fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
+                    const int R, const int q_min) {
+    using C = PagedCfg<D, kBF16>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) -> uint32_t { return base + C::BAR_OFF + 8u * i; };
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF + 4);
+    PagedPiece *ring = reinterpret_cast<PagedPiece *>(gbase + C::RING_OFF);
+
+    // ---- prologue: TMEM (warp 9), barriers (thread 0), this CTA's share ----
+    if (warp == 9) tmem_alloc(base + C::MISC_OFF, C::TMEM_COLS);
+    if (tid == 0) {
+        *abort_flag = 0u;
+        for (int q = 0; q < C::NQ; ++q) {
+            mbar_init(bar(C::B_QFULL + q), 1);
+            mbar_init(bar(C::B_QEMPTY + q), 1);
+        }
+        for (int s = 0; s < C::NSTAGE; ++s) {
+            mbar_init(bar(C::B_KVFULL + s), 1);
+            mbar_init(bar(C::B_KVEMPTY + s), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(C::B_SFULL + x), 1);
+            mbar_init(bar(C::B_PFULL + x), 4);
+            mbar_init(bar(C::B_OFULL + x), 1);
+            mbar_init(bar(C::B_OEMPTY + x), 4);
+        }
+        mbar_init(bar(C::B_XFULL), 4);
+        mbar_init(bar(C::B_XEMPTY), 4);
+        mbar_init(bar(C::B_MMADONE), 1);
+        for (int q = 0; q < C::RING; ++q) {
+            mbar_init(bar(C::B_PIECE + q), 1);
+            mbar_init(bar(C::B_FREE + q), 10);            // producer, MMA, 8 softmax warps
+        }
+        fence_barrier_init();
+    }
+    // Scan: thread i owns sequences [i k, (i + 1) k).  Scratch lies in the
+    // K/V ring, which no copy uses yet.
+    long long *scan = reinterpret_cast<long long *>(gbase + C::KV_OFF);   // [12], then the start
+    const int k = (a.B + C::NTHREADS - 1) / C::NTHREADS;
+    long long mine = 0;
+    for (int i = 0; i < k; ++i) {
+        const int b = tid * k + i;
+        PagedSeq s{0, 0, 0, false};
+        if (b < a.B) s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
+        if (s.bad && blockIdx.x == 0) report_bad_index(a.status, 1);
+        const int np = paged_units(s, R);
+        if (np <= 2)
+            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s, p, R, a);
+        for (unsigned big = __ballot_sync(0xffffffffu, np > 2); big != 0; big &= big - 1) {
+            const int src = __ffs(big) - 1;
+            PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
+            const long long sum = paged_seq_steps_warp(t, R, a);
+            if (lane == src) mine += sum;
+        }
+    }
+    mine *= a.H_kv;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < 12; ++w) {
+        const long long v = scan[w];
+        before += w < warp ? v : 0;
+        total += v;
+    }
+    const long long G = gridDim.x, c = blockIdx.x;
+    const long long quota = max((total + G - 1) / G, static_cast<long long>(q_min));
+    const long long w0 = c * quota, w1 = min(total, w0 + quota);
+    if (w0 < w1 && before + incl - mine <= w0 && w0 < before + incl) {
+        scan[12] = before + incl - mine;
+        scan[13] = static_cast<long long>(tid) * k;
+    }
+    fence_proxy_async_smem();                              // the scratch is overwritten by TMA
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    const long long scan_w = scan[12], scan_b = scan[13];
+    __syncthreads();                                       // the scratch is free again
+
+    // Reads piece number i (every role keeps its own count), whole warp; the
+    // caller releases it.
+    auto take = [&](uint32_t i, const WaitCtx &w, uint32_t where, PagedPiece &p) __attribute__((always_inline)) -> bool {
+        const uint32_t q = i % C::RING;
+        if (!mbar_wait_warp(bar(C::B_PIECE + q), (i / C::RING) & 1u, w, where)) return false;
+        p = ring[q];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_FREE + q));
+        return p.qrow >= 0;
+    };
+
+    if (warp >= 8) {
+      regs_shrink<C::REGS_LOW>();
+      if (warp == 10) {
+        // =================== scheduler (whole warp) ===================
+        WaitCtx w{abort_flag, a.status, kRolePaged};
+        uint32_t np_out = 0;
+        auto post = [&](const PagedPiece &p) __attribute__((always_inline)) -> bool {
+            const uint32_t q = np_out % C::RING;
+            if (!mbar_wait_warp(bar(C::B_FREE + q), ((np_out / C::RING) & 1u) ^ 1u, w, 30)) return false;
+            if (lane == 0) {
+                ring[q] = p;
+                mbar_arrive(bar(C::B_PIECE + q));
+            }
+            __syncwarp();
+            ++np_out;
+            return true;
+        };
+        int *desc = wk.desc + 8 * blockIdx.x;
+        if (lane == 0) desc[0] = 0;
+        bool ok = true;
+        if (w0 < w1) {
+            int b = static_cast<int>(scan_b);
+            long long at = scan_w, per = 0;                // steps before sequence b; of one K/V head
+            PagedSeq s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
+            for (;;) {
+                per = paged_seq_steps_warp(s, R, a);
+                if (w0 < at + per * a.H_kv || b + 1 >= a.B) break;
+                at += per * a.H_kv;
+                s = paged_seq(a.cu_q, a.kv_len, ++b, a.T, a.W, a.ps_log2);
+            }
+            int h = static_cast<int>((w0 - at) / per);
+            long long rem = (w0 - at) - h * per;           // steps into this head's units
+            int np = paged_units(s, R), p = 0;
+            for (int p0 = 0; p0 < np; p0 += 32) {
+                const long long mine_t = p0 + lane < np ? paged_unit_steps(s, p0 + lane, R, a) : 0;
+                long long inc = mine_t;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += v;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
+                if (past != 0) {
+                    const int l = __ffs(past) - 1;
+                    p = p0 + l;
+                    rem -= __shfl_sync(0xffffffffu, inc - mine_t, l);
+                    break;
+                }
+                rem -= __shfl_sync(0xffffffffu, inc, 31);
+            }
+            int t0 = static_cast<int>(rem);
+            for (long long at_w = w0; ok && at_w < w1;) {
+                PagedPiece pc;
+                const int i0 = p * 2 * R, left = s.m - i0;
+                pc.qrow = s.q0 + i0;
+                pc.nl = min(left, R);
+                pc.nh = min(max(left - R, 0), R);
+                pc.pos = s.n - s.m + i0;
+                pc.n = s.n;
+                pc.b = b;
+                pc.h = h;
+                const int last = pc.pos + pc.nl + pc.nh - 1;
+                const PagedTiles tl = paged_tiles(pc.pos, last, s.n, a);
+                pc.hi = tl.hi;
+                pc.nw = tl.nw;
+                pc.T = tl.T;
+                pc.vlo = paged_lo(pc.pos, a.wl);
+                pc.vhi = paged_hi(last, s.n, a.wr);
+                const int khl = paged_hi(pc.pos + pc.nl - 1, s.n, a.wr);
+                pc.skip = min(tl.T - 1, max(0, min(tl.nw, tl.hi - ((khl >> 7) + ((khl & 127) != 0)))));
+                pc.t0 = t0;
+                pc.t1 = static_cast<int>(min(static_cast<long long>(tl.T), t0 + (w1 - at_w)));
+                const bool cont = pc.t1 < tl.T;
+                pc.slot = t0 > 0 ? 2 * static_cast<int>(c) : cont ? 2 * static_cast<int>(c) + 1 : -1;
+                if (t0 == 0 && cont && lane == 0) {        // a cut unit that starts here
+                    desc[1] = pc.qrow;
+                    desc[2] = pc.nl;
+                    desc[3] = pc.nh;
+                    desc[4] = h;
+                    desc[0] = static_cast<int>((at_w + tl.T - 1) / quota - c + 1);   // its parts
+                }
+                ok = post(pc);
+                at_w += pc.t1 - t0;
+                t0 = 0;
+                if (++p == np) {
+                    p = 0;
+                    if (++h == a.H_kv) {
+                        h = 0;
+                        do {
+                            if (++b >= a.B) break;
+                            s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
+                            np = paged_units(s, R);
+                        } while (np == 0);
+                        if (b >= a.B) break;
+                    }
+                }
+            }
+        }
+        if (ok) {
+            PagedPiece end{};
+            end.qrow = -1;
+            post(end);
+        }
+      } else if (warp == 8) {
+        // =================== TMA producer (whole warp) ===================
+        WaitCtx w{abort_flag, a.status, kRoleProducer};
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
+        uint32_t qc = 0, kv = 0, pi = 0;                   // Q tiles, K/V tiles, pieces so far
+        uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
+        bool ok = true;
+        // this lane's box of a tile: rows [box_row, box_row + box), column chunk box_c
+        const int ps = 1 << a.ps_log2, box = min(ps, 128);
+        const int n_box = (128 / box) * C::NCH;
+        const int box_row = (lane / C::NCH) * box, box_c = lane % C::NCH;
+        const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
+        PagedPiece p;
+        while (ok && take(pi, w, 31, p)) {
+            ++pi;
+            for (int x = 0; x < (p.nh > 0 ? 2 : 1) && ok; ++x) {
+                const uint32_t qs = qc % C::NQ, qph = (qc / C::NQ) & 1u;
+                ok = mbar_wait_warp(bar(C::B_QEMPTY + qs), qph ^ 1u, w, 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QFULL + qs), q_bytes);
+                __syncwarp();
+                if (lane < C::NCH)
+                    tma_load_4d(&tm_q, base + C::Q_OFF + qs * C::TILE_BYTES + lane * C::CHUNK_BYTES,
+                                bar(C::B_QFULL + qs), lane * 64, p.h * a.group, p.qrow + x * R, 0);
+                qarmed |= 1u << qs;
+                qarmed_par = (qarmed_par & ~(1u << qs)) | (qph << qs);
+                ++qc;
+            }
+            const int *tb = a.table + static_cast<long long>(p.b) * a.W;
+            const int nf = min(a.first, p.vhi);
+            auto page_of = [&](int t) __attribute__((always_inline)) -> int {
+                const int tok = paged_tile(p, t) * 128 + box_row;
+                if (lane >= n_box || !((tok < p.vhi && tok + box > p.vlo) || tok < nf)) return a.n_pages;
+                return tb[tok >> a.ps_log2];
+            };
+            int page = p.t0 < p.t1 ? page_of(p.t0) : 0;
+            for (int t = p.t0; t < p.t1 && ok; ++t) {
+                const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;
+                if (static_cast<unsigned>(page) > static_cast<unsigned>(a.n_pages)) {
+                    report_bad_index(a.status, 2);
+                    page = a.n_pages;
+                } else if (page == a.n_pages && lane < n_box) {
+                    // beyond the pool: no row sees it, or its id is one too large
+                    const int tok = paged_tile(p, t) * 128 + box_row;
+                    if ((tok < p.vhi && tok + box > p.vlo) || tok < nf) report_bad_index(a.status, 2);
+                }
+                const int row0 = (paged_tile(p, t) * 128 + box_row) & (ps - 1);
+                for (int v = 0; v < 2; ++v, ++kv) {
+                    const uint32_t slot = kv % C::NSTAGE, ph = (kv / C::NSTAGE) & 1u;
+                    ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
+                    __syncwarp();
+                    if (lane < n_box)
+                        tma_load_4d(v ? &tm_v : &tm_k,
+                                    base + C::KV_OFF + slot * C::TILE_BYTES + box_c * C::CHUNK_BYTES + box_row * 128u,
+                                    bar(C::B_KVFULL + slot), box_c * 64, p.h, row0, page);
+                    armed |= 1u << slot;
+                    armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                }
+                page = next;
+            }
+        }
+        // Every issued copy lands before the CTA may end (bounded).
+        for (int s = 0; s < C::NSTAGE; ++s)
+            if (armed & (1u << s)) mbar_wait_quiet(bar(C::B_KVFULL + s), (armed_par >> s) & 1u, 500000000ull);
+        for (int q = 0; q < C::NQ; ++q)
+            if (qarmed & (1u << q)) mbar_wait_quiet(bar(C::B_QFULL + q), (qarmed_par >> q) & 1u, 500000000ull);
+        __syncwarp();
+      } else if (warp == 9) {
+        // =================== MMA issuer (whole warp, one elected lane issues) ===================
+        WaitCtx w{abort_flag, a.status, kRoleMma};
+        uint32_t qc = 0, kv = 0, pi = 0;
+        uint32_t un0 = 0, un1 = 0, pp0 = 0, pp1 = 0;       // accumulator uses, P tiles, per group
+        bool ok = true;
+        auto pv = [&](const int x, const uint32_t idx, const bool begin, const bool end, const bool v_wait,
+                      const uint32_t un, uint32_t &pp) __attribute__((always_inline)) -> bool {
+            const uint32_t slot = idx % C::NSTAGE;
+            if (v_wait && !mbar_wait_warp(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 10)) return false;
+            if (begin && !mbar_wait_warp(bar(C::B_OEMPTY + x), (un & 1u) ^ 1u, w, 11)) return false;
+            if (!mbar_wait_warp(bar(C::B_PFULL + x), pp & 1u, w, 12)) return false;
+            ++pp;
+            tc_fence_after();
+            const uint64_t vd = smem_desc_sw128(base + C::KV_OFF + slot * C::TILE_BYTES, C::CHUNK_BYTES, 1024u);
+#pragma unroll
+            for (int kk = 0; kk < C::PV_STEPS; ++kk)
+                mma_ts_f16_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u, vd + ((kk * 16 * 128u) >> 4),
+                                 C::IDESC_PV, (!begin || kk > 0) ? 1u : 0u);
+            if (end) mma_commit_elect(bar(C::B_OFULL + x));
+            return true;
+        };
+        auto qk = [&](const int x, const uint32_t qi, const bool q_wait, const uint32_t idx,
+                      const bool k_wait) __attribute__((always_inline)) -> bool {
+            const uint32_t slot = idx % C::NSTAGE, qs = qi % C::NQ;
+            if (k_wait && !mbar_wait_warp(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 13)) return false;
+            if (q_wait && !mbar_wait_warp(bar(C::B_QFULL + qs), (qi / C::NQ) & 1u, w, 14)) return false;
+            tc_fence_after();
+            const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::TILE_BYTES, 16u, 1024u);
+            const uint64_t kd = smem_desc_sw128(base + C::KV_OFF + slot * C::TILE_BYTES, 16u, 1024u);
+#pragma unroll
+            for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                mma_ss_f16_elect(tbase + C::col_s(x), qd + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_elect(bar(C::B_SFULL + x));
+            return true;
+        };
+        PagedPiece p;
+        while (ok && take(pi, w, 32, p)) {
+            ++pi;
+            const int ns = p.t1 - p.t0;
+            if (p.nh == 0) {
+                // one tile: step i belongs to group i & 1
+                for (int i = 0; i < ns + 2 && ok; ++i) {
+                    if (i >= 2) {
+                        const uint32_t idx = kv + 2 * (i - 2) + 1;
+                        ok = (i & 1) ? pv(1, idx, i == 3, i >= ns, true, un1, pp1)
+                                     : pv(0, idx, i == 2, i >= ns, true, un0, pp0);
+                        if (!ok) break;
+                        mma_commit_elect(bar(C::B_KVEMPTY + idx % C::NSTAGE));
+                    }
+                    if (i < ns) {
+                        const uint32_t idx = kv + 2 * i;
+                        ok = (i & 1) ? qk(1, qc, false, idx, true) : qk(0, qc, i == 0, idx, true);
+                        if (!ok) break;
+                        mma_commit_elect(bar(C::B_KVEMPTY + idx % C::NSTAGE));
+                        if (i == ns - 1) mma_commit_elect(bar(C::B_QEMPTY + qc % C::NQ));
+                    }
+                }
+                ++qc;
+                ++un0;
+                un1 += ns >= 2 ? 1u : 0u;
+            } else {
+                const int s0 = max(p.t0, p.skip) - p.t0;    // first step of tile L (ns or more: none)
+                // (an unused Q tile still has to land before its slot is released)
+                if (s0 >= ns) ok = mbar_wait_warp(bar(C::B_QFULL + qc % C::NQ), (qc / C::NQ) & 1u, w, 15);
+                for (int i = 0; i <= ns && ok; ++i) {
+                    const uint32_t vi = kv + 2 * (i - 1) + 1, ki = kv + 2 * i;
+                    const bool l_v = i - 1 >= s0, l_k = i < ns && i >= s0;
+                    if (l_v) ok = pv(0, vi, i - 1 == s0, i == ns, true, un0, pp0);
+                    if (ok && l_k) ok = qk(0, qc, i == s0, ki, true);
+                    if (ok && i > 0) ok = pv(1, vi, i == 1, i == ns, !l_v, un1, pp1);
+                    if (ok && i < ns) ok = qk(1, qc + 1, i == 0, ki, !l_k);
+                    if (!ok) break;
+                    if (i == ns - 1) {
+                        mma_commit_elect(bar(C::B_QEMPTY + qc % C::NQ));
+                        mma_commit_elect(bar(C::B_QEMPTY + (qc + 1) % C::NQ));
+                    }
+                    if (i < ns) mma_commit_elect(bar(C::B_KVEMPTY + ki % C::NSTAGE));
+                    if (i > 0) mma_commit_elect(bar(C::B_KVEMPTY + vi % C::NSTAGE));
+                }
+                qc += 2;
+                un0 += s0 < ns ? 1u : 0u;
+                ++un1;
+            }
+            kv += 2 * ns;
+        }
+        // Drain: every issued MMA completes before TMEM is released.
+        mma_commit_elect(bar(C::B_MMADONE));
+        mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
+        __syncwarp();
+      }
+    } else {
+        regs_grow<C::REGS_HIGH>();
+        // =================== softmax group x ===================
+        const int x = warp >> 2;
+        const int row = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tbase + lane_off + C::col_s(x);
+        const uint32_t tO = tbase + lane_off + C::col_o(x);
+        WaitCtx w{abort_flag, a.status, x ? kRoleSoftmax1 : kRoleSoftmax0};
+        const float sl2 = a.scale_log2;
+        float *xch = reinterpret_cast<float *>(gbase + C::X_OFF);
+        const bool v8ok = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+        uint32_t pi = 0, kv = 0, sph = 0;
+        uint32_t un0 = 0, un1 = 0, nx = 0;                 // accumulator uses per group, exchanges
+        bool ok = true;
+        const int my_pos = row / a.group;                  // this row's position within a tile
+        const int my_head = row - my_pos * a.group;
+        PagedPiece p;
+        while (ok && take(pi, w, 24, p)) {
+            ++pi;
+            const bool one = p.nh == 0;
+            const int ns = p.t1 - p.t0;
+            const int tile = one ? 0 : x;                  // the Q tile this group works on
+            const int npos = tile ? p.nh : p.nl;
+            const int s0 = one ? x : x ? 0 : max(p.t0, p.skip) - p.t0;   // its first step
+            const int ds = one ? 2 : 1;
+            const bool valid = my_pos < npos;
+            const bool live_warp = __any_sync(0xffffffffu, valid);
+            const int pos = p.pos + tile * R + my_pos;
+            const int klo = paged_lo(pos, a.wl), khi = paged_hi(pos, p.n, a.wr), kf = min(a.first, khi);
+            const int nf = min(a.first, p.vhi);            // first tokens that any row sees
+            // r: reference point (log2 units); le: row sum of the FP32
+            // exponentials (LSE); lr: of the same rounded as P (normalises O).
+            // Rows that hold no token never ask for a new reference.
+            float r = valid ? -INFINITY : 0.f, le = 0.f, lr = 0.f;
+            for (int i = s0; i < ns; i += ds) {
+                const int k0 = paged_tile(p, p.t0 + i) * 128;
+                ok = mbar_wait(bar(C::B_SFULL + x), sph, w, 20);
+                if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                sph ^= 1;
+                // ---- a tile that the unit sees in part: its other V rows become 0 ----
+                if (!((k0 >= p.vlo && k0 + 128 <= p.vhi) || k0 + 128 <= nf)) {
+                    const uint32_t idx = kv + 2 * i + 1, slot = idx % C::NSTAGE;
+                    ok = mbar_wait(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 22);
+                    if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                    const int kk = k0 + row;
+                    if (!((kk >= p.vlo && kk < p.vhi) || kk < nf)) {
+                        uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + row * 128;
+#pragma unroll
+                        for (int ch = 0; ch < C::NCH; ++ch)
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                *reinterpret_cast<uint4 *>(vr + ch * C::CHUNK_BYTES + q * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (!live_warp) {
+                    if (lane == 0) mbar_arrive(bar(C::B_PFULL + x));
+                    continue;
+                }
+                tc_fence_after();
+                uint32_t s[128];
+                float *sf = reinterpret_cast<float *>(s);
+                const int lim = khi - k0, llo = klo - k0, lf = kf - k0;
+                auto load_s = [&]() __attribute__((always_inline)) {
+                    tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                    tmem_ld_wait();
+                    if (valid && lim < 128) {
+#pragma unroll
+                        for (int cc = 0; cc < 128; ++cc) if (cc >= lim) sf[cc] = -INFINITY;
+                    }
+                    if (valid && llo > 0 && lf < 128) {
+#pragma unroll
+                        for (int cc = 0; cc < 128; ++cc) if (cc < llo && cc >= lf) sf[cc] = -INFINITY;
+                    }
+                };
+                load_s();
+                float rn = r, corr = 1.f;
+                bool need = false;
+                float2 e_a, e_b;
+                uint32_t pk[64];
+                const float2 c2 = make_float2(sl2, sl2);
+                auto exps = [&](const float rs) __attribute__((always_inline)) {
+                    const float2 nr2 = make_float2(-rs, -rs);
+                    e_a = make_float2(0.f, 0.f);
+                    e_b = e_a;
+#pragma unroll
+                    for (int cc = 0; cc < 128; cc += 4) {
+                        const float2 x01 = __ffma2_rn(make_float2(sf[cc + 0], sf[cc + 1]), c2, nr2);
+                        const float2 x23 = __ffma2_rn(make_float2(sf[cc + 2], sf[cc + 3]), c2, nr2);
+                        const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                        const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                        pk[cc / 2] = pack2<kBF16>(e01.x, e01.y);
+                        pk[cc / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                        e_a = __fadd2_rn(e_a, e01);
+                        e_b = __fadd2_rn(e_b, e23);
+                    }
+                };
+                // P against the current reference first; the maximum only on the
+                // first tile or when the row's sum got too large (fa_fwd_kernel.cuh)
+                bool keep = __all_sync(0xffffffffu, r != -INFINITY);
+                if (keep) {
+                    exps(r);
+                    const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                    keep = __all_sync(0xffffffffu, !valid || ts <= C::KEEP_SUM);
+                    if (!keep) load_s();
+                }
+                if (!keep) {
+                    float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
+#pragma unroll
+                    for (int cc = 4; cc < 128; cc += 8) {
+                        m0 = max3(m0, sf[cc + 0], sf[cc + 4]);
+                        m1 = max3(m1, sf[cc + 1], sf[cc + 5]);
+                        m2 = max3(m2, sf[cc + 2], sf[cc + 6]);
+                        m3 = max3(m3, sf[cc + 3], sf[cc + 7]);
+                    }
+                    const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+                    if (valid) {
+                        if (r == -INFINITY) rn = bnew;
+                        else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
+                        need = (r != -INFINITY) && (rn != r);
+                    }
+                    exps((rn == -INFINITY) ? 0.f : rn);
+                }
+                tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                // ---- correction of O (its previous PV completed before S_FULL) ----
+                if (__any_sync(0xffffffffu, need)) {
+                    const float2 cc2 = make_float2(corr, corr);
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + ch * 32, ov);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 32; q += 2) {
+                            const float2 v2 = __fmul2_rn(
+                                make_float2(__uint_as_float(ov[q]), __uint_as_float(ov[q + 1])), cc2);
+                            ov[q] = __float_as_uint(v2.x);
+                            ov[q + 1] = __float_as_uint(v2.y);
+                        }
+                        tmem_st32(tO + ch * 32, ov);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_PFULL + x));
+                // ---- row sums, after P is published ----
+                le = __fmaf_rn(le, corr, (e_a.x + e_a.y) + (e_b.x + e_b.y));
+                float2 r_a = make_float2(0.f, 0.f), r_b = r_a;
+#pragma unroll
+                for (int q = 0; q < 64; q += 2) {
+                    add_pair<kBF16>(r_a.x, r_a.y, pk[q]);
+                    add_pair<kBF16>(r_b.x, r_b.y, pk[q + 1]);
+                }
+                lr = __fmaf_rn(lr, corr, (r_a.x + r_a.y) + (r_b.x + r_b.y));
+                r = rn;
+            }
+            if (!ok) break;
+            kv += 2 * ns;
+            // ---- this group's normaliser and LSE (log2 units) ----
+            const bool some = s0 < ns;
+            const bool live = some && le > 0.f && lr > 0.f;
+            float inv = live ? 1.f / lr : 0.f;
+            float lse2 = live ? r + log2f(le) : -INFINITY;
+            const bool joined = one && ns >= 2;            // group H has a share of this tile
+            if (one && x == 1) {
+                if (joined) {
+                    ok = mbar_wait_warp(bar(C::B_XEMPTY), (nx & 1u) ^ 1u, w, 25);
+                    if (!ok) break;
+                    xch[row] = lse2;
+                    xch[128 + row] = inv;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_XFULL));
+                    ++nx;
+                    ++un1;
+                }
+                ++un0;
+                continue;
+            }
+            const uint32_t my_un = x ? un1 : un0;
+            if (some) {
+                ok = mbar_wait_warp(bar(C::B_OFULL + x), my_un & 1u, w, 21);
+                if (!ok) break;
+            }
+            float inv_h = 0.f;
+            if (joined) {
+                ok = mbar_wait_warp(bar(C::B_XFULL), nx & 1u, w, 26) &&
+                     mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 27);
+                if (!ok) break;
+                const float l_h = xch[row];
+                const float m = fmaxf(lse2, l_h);
+                if (m != -INFINITY) {
+                    const float w_l = ex2_approx(lse2 - m), w_h = ex2_approx(l_h - m);
+                    const float n2 = 1.f / (w_l + w_h);
+                    inv *= w_l * n2;
+                    inv_h = xch[128 + row] * w_h * n2;
+                    lse2 = m + log2f(w_l + w_h);
+                }
+            }
+            tc_fence_after();
+            uint32_t ov[D];
+            if (some && live_warp) {
+#pragma unroll
+                for (int ch = 0; ch < D / 32; ++ch)
+                    tmem_ld32(tO + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&ov[ch * 32]));
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < D; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * inv);
+                if (joined) {
+#pragma unroll
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t oh[32];
+                        tmem_ld32(tbase + lane_off + C::col_o(1) + ch * 32, oh);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            ov[ch * 32 + q] = __float_as_uint(
+                                fmaf(__uint_as_float(oh[q]), inv_h, __uint_as_float(ov[ch * 32 + q])));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < D; ++q) ov[q] = 0u;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (some) mbar_arrive(bar(C::B_OEMPTY + x));
+                if (joined) {
+                    mbar_arrive(bar(C::B_OEMPTY + 1));
+                    mbar_arrive(bar(C::B_XEMPTY));
+                }
+            }
+            if (one) {
+                ++un0;
+                if (joined) { ++un1; ++nx; }
+            } else {
+                un0 += max(p.t0, p.skip) - p.t0 < ns ? 1u : 0u;
+                ++un1;
+            }
+            if (!valid) continue;
+            if (p.slot >= 0) {
+                // a part of the unit: normalised O and LSE to the workspace
+                const size_t part = (static_cast<size_t>(p.slot) * 2 + tile) * 128 + row;
+                wk.lse[part] = lse2;
+                if (some) {
+                    float *prow = wk.o + part * D;
+#pragma unroll
+                    for (int ch = 0; ch < D / 8; ++ch) st_global_v8(prow + 8 * ch, &ov[8 * ch]);
+                }
+                continue;
+            }
+            const int tok = p.qrow + tile * R + my_pos, qh = p.h * a.group + my_head;
+            uint16_t *orow = reinterpret_cast<uint16_t *>(a.o) + (static_cast<size_t>(tok) * a.H + qh) * D;
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) {
+                uint32_t pk[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    pk[q] = pack2<kBF16>(__uint_as_float(ov[16 * ch + 2 * q]), __uint_as_float(ov[16 * ch + 2 * q + 1]));
+                if (v8ok) {
+                    st_global_v8(orow + 16 * ch, pk);
+                } else {
+                    reinterpret_cast<uint4 *>(orow)[2 * ch] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    reinterpret_cast<uint4 *>(orow)[2 * ch + 1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
+            }
+            if (a.lse != nullptr) a.lse[static_cast<size_t>(qh) * a.T + tok] = lse2 * 0.69314718055994530942f;
+        }
+    }
+
+    // ---- teardown ----
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tbase, C::TMEM_COLS);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Joins the parts of the units that the shares' borders cut: LSE = log sum_s
+// exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  CTA (c, y) takes rows y, y +
+// gridDim.y, ... of the cut unit that starts in share c; its part 0 is slot
+// 2 c + 1, part s > 0 slot 2 (c + s).  A row's parts are split over the eight
+// warps (part s to warp s % 8) and the warps' sums added in order.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedArgs a, const PagedWork wk, const int R) {
+    constexpr int E = D / 32;
+    __shared__ float s_acc[8][D];
+    __shared__ float s_m[8], s_l[8];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int *desc = wk.desc + 8 * c;
+    const int parts = desc[0];
+    if (parts == 0) return;
+    const int qrow = desc[1], nl = desc[2], nh = desc[3], h = desc[4];
+    for (int rr = blockIdx.y; rr < (nl + nh) * a.group; rr += gridDim.y) {
+        const int tile = rr >= nl * a.group ? 1 : 0;
+        const int row = tile ? rr - nl * a.group : rr;
+        float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int s = warp; s < parts; s += 8) {
+            const size_t part = (static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 2 + tile) * 128 + row;
+            const float z = wk.lse[part];
+            if (z == -INFINITY) continue;                 // the part saw nothing (its O may be unwritten)
+            const float *src = wk.o + part * D + lane * E;
+            float v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = src[e];
+            const float mn = fmaxf(m, z);
+            const float k = ex2_approx(m - mn), wt = ex2_approx(z - mn);
+            l = fmaf(l, k, wt);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], k, wt * v[e]);
+            m = mn;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+        if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+        __syncthreads();
+        if (warp == 0) {
+            float M = s_m[0], L = 0.f;
+#pragma unroll
+            for (int q = 1; q < 8; ++q) M = fmaxf(M, s_m[q]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = 0.f;
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float k = ex2_approx(s_m[q] - M);
+                    L = fmaf(s_l[q], k, L);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[q][lane * E + e], k, acc[e]);
+                }
+            }
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const int tok = qrow + tile * R + row / a.group, qh = h * a.group + row % a.group;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.o) +
+                                                         (static_cast<size_t>(tok) * a.H + qh) * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
+            if (a.lse != nullptr && lane == 0)
+                a.lse[static_cast<size_t>(qh) * a.T + tok] =
+                    L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace fa

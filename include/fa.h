@@ -414,11 +414,12 @@ fa_status fa_paged_append(const void *k, const void *v, void *k_pages, void *v_p
  *          (>= H * d, a multiple of 8), 16-byte aligned.
  *   o    : device, [total_q][H][d], 16-byte aligned (written).
  *   lse  : device, float [H][total_q], or NULL to skip.
- *   workspace : device, fa_paged_workspace_bytes(d) bytes, 16-byte aligned,
+ *   workspace : device, fa_paged_workspace_bytes(d) bytes, 32-byte aligned,
  *          caller-owned; nothing in it needs to start at zero.  Calls that
  *          may overlap in time need one each.
  *   max_q : the most new tokens of one sequence, >= 1; it only chooses tile
  *          shapes (a larger sequence is still computed in full).
+ *   alpha : the score scale, positive.
  *   H / H_kv <= 128, else FA_ERR_UNSUPPORTED.
  * Accumulation is FP32, P is rounded to `dtype` before the P V product.
  * The key ranges of all rows together are cut into equal shares for the SMs

@@ -195,7 +195,7 @@ def test_attention_large_scores(gpu_lib):
     check_attention(c, o, lse)
 
 
-@pytest.mark.parametrize("alpha", [0.0, -0.125])
+@pytest.mark.parametrize("alpha", [1e-6, 0.01, 2.0])
 def test_attention_alpha(gpu_lib, alpha):
     c = Cache([3, 140], [50, 200], seed=1)
     o, lse = attend(gpu_lib, c, alpha=alpha)

@@ -54,6 +54,7 @@ ATTN = [
     (dict(q=None), INV), (dict(cu=None), INV), (dict(T=-1), INV), (dict(mq=0), INV), (dict(H=5), INV),
     (dict(H=0), INV), (dict(qst=4 * 128 - 8), INV), (dict(wl=-2), INV), (dict(wr=-2), INV),
     (dict(first=-1), INV), (dict(alpha=float("nan")), INV), (dict(alpha=float("inf")), INV), (dict(dt=2), INV),
+    (dict(alpha=0.0), INV), (dict(alpha=-0.1), INV), (dict(alpha=1e-40), INV), (dict(alpha=3e38), INV),
     (dict(H=258, qst=1 << 20), UNS), (dict(q=A + 8), MIS), (dict(cu=A + 2), MIS), (dict(lse=A + 2), MIS),
     (dict(qst=4 * 128 + 4), MIS), (dict(qst=1 << 39), BIG),
 ]
@@ -61,7 +62,7 @@ ATTN = [
 
 @pytest.mark.parametrize("kw,code", SHARED + ATTN + [
     (dict(vp=None), INV), (dict(o=None), INV), (dict(ws=None), INV), (dict(vp=A + 8), MIS), (dict(o=A + 8), MIS),
-    (dict(ws=A + 8), MIS),
+    (dict(ws=A + 8), MIS), (dict(ws=A + 16), MIS),
 ])
 def test_attention_codes(lib, kw, code):
     assert _attend(lib, **kw) == code
