@@ -935,8 +935,10 @@ fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
                           int window_left, int window_right, int first, fa_dtype dtype,
                           void *stream) {
     if (!scores || score_width < 1 || (total_q > 0 && !lse)) return FA_ERR_INVALID_ARG;
-    fa::PagedScoresArgs g;
-    fa_status st = paged_attn_args(&g.p, q, k_pages, block_table, kv_len, cu_q, lse, B, H, H_kv,
+    fa::PagedScoresLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    fa::PagedArgs &a = L.a;
+    fa_status st = paged_attn_args(&a, q, k_pages, block_table, kv_len, cu_q, lse, B, H, H_kv,
                                    total_q, max_q, d, page_size, n_pages, table_width, q_stride,
                                    page_stride, alpha, window_left, window_right, first, dtype);
     if (st != FA_OK) return st;
@@ -944,13 +946,30 @@ fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
         return FA_ERR_MISALIGNED;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
-    g.p.lse = const_cast<float *>(lse);
-    g.p.status = dev->status;
-    g.in = scores_in;
-    g.out = scores;
-    g.L = score_width;
-    return fa::launch_paged_scores(g, d, dtype == FA_BF16, dev->sm_count,
-                                   static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    a.lse = const_cast<float *>(lse);
+    a.status = dev->status;
+    L.in = scores_in;
+    L.out = scores;
+    L.L = score_width;
+    L.d = d;
+    L.bf16 = dtype == FA_BF16;
+    L.stream = static_cast<cudaStream_t>(stream);
+    const int fit = 128 / a.group;
+    L.R = max_q < fit ? max_q : fit;
+    const CUtensorMapDataType dt =
+        L.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    fa::PagedArgs qa = a;
+    if (total_q == 0) {                 // no row is loaded: any address will do
+        qa.q = k_pages;
+        qa.T = 1;
+    }
+    if ((st = encode_packed_q(&L.q, dt, qa, d, L.R)) != FA_OK) return st;
+    if ((st = encode_pages(&L.k, k_pages, dt, a, d)) != FA_OK) return st;
+    // units: pairs of 128-token tiles of each (sequence, K/V head)
+    const uint64_t most = ((static_cast<uint64_t>(table_width) << a.ps_log2) + 255) / 256;
+    const uint64_t units = most * static_cast<uint64_t>(B) * static_cast<uint64_t>(H_kv);
+    L.grid = static_cast<int>(units < static_cast<uint64_t>(dev->sm_count) ? units : dev->sm_count);
+    return fa::launch_paged_scores(L) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,

@@ -87,6 +87,27 @@ __device__ __forceinline__ int paged_hi(int p, int n, int wr) {
     return hi < 0 ? 0 : hi < n ? static_cast<int>(hi) : n;
 }
 
+// A lane's part of a 128-token tile: TMA boxes of min(page_size, 128) slots by
+// one 128-byte column chunk, kChunks chunks a row; lanes at and behind n_box
+// have none.  row: the box's first token in the tile, c: its chunk.
+template <int kChunks>
+struct PagedBox {
+    int box, n_box, row, c;
+    __device__ __forceinline__ explicit PagedBox(int ps_log2) {
+        const int lane = threadIdx.x & 31;
+        box = min(1 << ps_log2, 128);
+        n_box = (128 / box) * kChunks;
+        row = (lane / kChunks) * box;
+        c = lane % kChunks;
+    }
+    // The page that this lane's box of tile j needs, when a row sees tokens
+    // [vlo, vhi) or [0, nf); otherwise n_pages, which TMA reads as zeros.
+    __device__ __forceinline__ bool needs(int j, int vlo, int vhi, int nf) const {
+        const int tok = j * 128 + row;
+        return (threadIdx.x & 31) < n_box && ((tok < vhi && tok + box > vlo) || tok < nf);
+    }
+};
+
 // The page that holds token j of sequence b, or -1 (reported) for an id
 // outside the pool.
 __device__ __forceinline__ int paged_page(const int *table_b, int j, int ps_log2, int n_pages,
@@ -148,14 +169,17 @@ struct PagedFwdLaunch {
 cudaError_t launch_fwd_paged_d64(const PagedFwdLaunch &L);
 cudaError_t launch_fwd_paged_d128(const PagedFwdLaunch &L);
 
-struct PagedScoresArgs {
-    PagedArgs p;                   // lse: read here
-    const float *in;               // [B][H_kv][L] or nullptr
-    float *out;                    // [B][H_kv][L]
+struct PagedScoresLaunch {
+    CUtensorMap q, k;   // as in PagedFwdLaunch
+    PagedArgs a;        // lse: read here
+    const float *in;    // [B][H_kv][L] or nullptr
+    float *out;         // [B][H_kv][L]
     int L;
+    int R, grid, d;
+    bool bf16;
+    cudaStream_t stream;
 };
-cudaError_t launch_paged_scores(const PagedScoresArgs &a, int d, bool bf16, int sm_count,
-                                cudaStream_t stream);
+cudaError_t launch_paged_scores(const PagedScoresLaunch &L);
 
 struct PagedEvictArgs {
     void *k_pages, *v_pages;

@@ -341,10 +341,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         uint32_t qc = 0, kv = 0, pi = 0;                   // Q tiles, K/V tiles, pieces so far
         uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        // this lane's box of a tile: rows [box_row, box_row + box), column chunk box_c
-        const int ps = 1 << a.ps_log2, box = min(ps, 128);
-        const int n_box = (128 / box) * C::NCH;
-        const int box_row = (lane / C::NCH) * box, box_c = lane % C::NCH;
+        const PagedBox<C::NCH> bx(a.ps_log2);
         const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
         PagedPiece p;
         while (ok && take(pi, w, 31, p)) {
@@ -364,33 +361,30 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             const int *tb = a.table + static_cast<long long>(p.b) * a.W;
             const int nf = min(a.first, p.vhi);
+            // the page id of this lane's box of step t (loaded a step ahead)
             auto page_of = [&](int t) __attribute__((always_inline)) -> int {
-                const int tok = paged_tile(p, t) * 128 + box_row;
-                if (lane >= n_box || !((tok < p.vhi && tok + box > p.vlo) || tok < nf)) return a.n_pages;
-                return tb[tok >> a.ps_log2];
+                const int j = paged_tile(p, t);
+                return bx.needs(j, p.vlo, p.vhi, nf) ? tb[(j * 128 + bx.row) >> a.ps_log2] : a.n_pages;
             };
             int page = p.t0 < p.t1 ? page_of(p.t0) : 0;
             for (int t = p.t0; t < p.t1 && ok; ++t) {
                 const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;
-                if (static_cast<unsigned>(page) > static_cast<unsigned>(a.n_pages)) {
-                    report_bad_index(a.status, 2);
-                    page = a.n_pages;
-                } else if (page == a.n_pages && lane < n_box) {
-                    // beyond the pool: no row sees it, or its id is one too large
-                    const int tok = paged_tile(p, t) * 128 + box_row;
-                    if ((tok < p.vhi && tok + box > p.vlo) || tok < nf) report_bad_index(a.status, 2);
+                const int j = paged_tile(p, t);
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
+                    if (bx.needs(j, p.vlo, p.vhi, nf)) report_bad_index(a.status, 2);
+                    page = a.n_pages;                      // beyond the pool: zeros
                 }
-                const int row0 = (paged_tile(p, t) * 128 + box_row) & (ps - 1);
+                const int row0 = (j * 128 + bx.row) & ((1 << a.ps_log2) - 1);
                 for (int v = 0; v < 2; ++v, ++kv) {
                     const uint32_t slot = kv % C::NSTAGE, ph = (kv / C::NSTAGE) & 1u;
                     ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
                     __syncwarp();
-                    if (lane < n_box)
+                    if (lane < bx.n_box)
                         tma_load_4d(v ? &tm_v : &tm_k,
-                                    base + C::KV_OFF + slot * C::TILE_BYTES + box_c * C::CHUNK_BYTES + box_row * 128u,
-                                    bar(C::B_KVFULL + slot), box_c * 64, p.h, row0, page);
+                                    base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
+                                    bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, page);
                     armed |= 1u << slot;
                     armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
                 }

@@ -1,63 +1,451 @@
 // fa_paged_scores.cu -- the attention weight that each cached token of a
-// paged cache gets from the new tokens.
+// paged cache gets from the new tokens, on sm_103a (tcgen05 + TMA):
+//     A[b][h][j] += sum_i exp(alpha q_i . k_j - LSE_i)
+// over the rows i that see token j and the query heads of K/V head h.
+//
+// The sum runs over rows, so the product is formed transposed, S^T = K Q^T:
+// a TMEM lane, and with it a thread, holds one cached token, its columns are
+// the rows of a Q tile (R positions x g heads, packed as in
+// fa_paged_fwd_kernel.cuh).  A token's sum then stays in one thread's
+// registers from the first row to the last: no reduction between threads, no
+// atomics, and the order of the terms is fixed.
+//
+// A unit is a pair of 128-token tiles of one (sequence, K/V head), one for
+// each of the two groups of four warps; their K tiles stay in shared memory
+// while the Q tiles that see them stream past, so a Q tile that is read once
+// serves 256 tokens.  S^T is double-buffered per group in TMEM (4 x 128
+// columns).  With few rows a Q tile is narrow (the product has N = 32 for a
+// single token of up to 32 heads a group) and the kernel reads K at the rate of HBM;
+// with long chunks it is bound by the exponentials (one per row and token
+// against 2 d flops, 32 a clock and SM).
+//
+// Units are dealt to the CTAs in turn, back and forth; warp 10 finds a
+// unit's sequence by a prefix sum over 32 sequences at a time.  The log-sum-
+// exps of a Q tile go through shared memory, where all threads of a group
+// read the same one at a time.  Columns of other sequences (a Q tile reads
+// past its sequence's end) and rows that see nothing are dropped by
+// selection, never by multiplying with zero.
 #include "fa_paged.cuh"
 
 namespace fa {
 
-template <bool kBF16>
-__device__ __forceinline__ float to_f32(uint16_t x) {
-    float lo, hi;
-    unpack2<kBF16>(x, lo, hi);
-    return lo;
-}
-
-// One warp per (sequence, K/V head, cached token): the rows that see it, one
-// by one, in a fixed order.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(256) fa_paged_scores_kernel(const PagedScoresArgs g) {
-    constexpr int E = D / 32;
-    const PagedArgs &a = g.p;
-    const int lane = threadIdx.x & 31;
-    const int j = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int hk = blockIdx.y, b = blockIdx.z;
-    const PagedSeq s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-    if (s.bad && lane == 0) report_bad_index(a.status, 1);
-    if (s.n > g.L && lane == 0) report_bad_index(a.status, 3);
-    if (j >= s.n || j >= g.L) return;
-    const int page = paged_page(a.table + static_cast<long long>(b) * a.W, j, a.ps_log2, a.n_pages, a.status);
-    const long long at = page * a.page_stride +
-        (static_cast<long long>(j & ((1 << a.ps_log2) - 1)) * a.H_kv + hk) * D + lane * E;
-    float k[E];
-    for (int e = 0; e < E; ++e)
-        k[e] = page < 0 ? 0.f : to_f32<kBF16>(reinterpret_cast<const uint16_t *>(a.k_pages)[at + e]);
-    const int old = s.n - s.m;
-    float sum = 0.f;
-    for (int i = 0; i < s.m; ++i) {
-        const int p = old + i;
-        if (j >= paged_hi(p, s.n, a.wr) || (j < paged_lo(p, a.wl) && j >= a.first)) continue;
-        for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
-            const uint16_t *qr = reinterpret_cast<const uint16_t *>(a.q) + (s.q0 + i) * a.q_stride + h * D + lane * E;
-            float x = 0.f;
-            for (int e = 0; e < E; ++e) x += to_f32<kBF16>(qr[e]) * k[e];
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            const float z = a.lse[static_cast<long long>(h) * a.T + s.q0 + i];
-            if (z != -INFINITY) sum += exp2f(fmaf(x, a.scale_log2, -z * 1.44269504088896340736f));
+struct ScoresCfg {
+    static constexpr int NCH = D / 64;
+    static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
+    static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
+    static constexpr int NK = D == 64 ? 8 : 4;            // K tiles in flight
+    static constexpr int NQ = D == 64 ? 6 : 3;            // Q tiles in flight
+    static constexpr int NTHREADS = 384;
+    static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
+    static constexpr int RING = 4;
+    static constexpr uint32_t K_OFF = 0;
+    static constexpr uint32_t Q_OFF = NK * TILE_BYTES;
+    static constexpr uint32_t L_OFF = Q_OFF + NQ * TILE_BYTES;        // [2 groups][128] floats
+    static constexpr uint32_t RING_OFF = L_OFF + 2 * 128 * 4;
+    static constexpr uint32_t BAR_OFF = RING_OFF + RING * 32;
+    static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_QFULL = 2 * NK, B_QEMPTY = B_QFULL + NQ,
+                         B_SFULL = B_QEMPTY + NQ, B_SEMPTY = B_SFULL + 4, B_MMADONE = B_SEMPTY + 4,
+                         B_UNIT = B_MMADONE + 1, B_FREE = B_UNIT + RING, NBAR = B_FREE + RING;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
+    static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+    static constexpr uint32_t TMEM_COLS = 512;
+    __host__ __device__ static constexpr uint32_t col_s(int x, int buf) { return 256u * x + 128u * buf; }
+};
+
+struct __align__(16) ScoresUnit {
+    int k0;             // first token of the pair; -1: no more units
+    int n, q0, m;       // cached tokens, first packed row, new tokens
+    int qa, qb;         // Q tiles that see any of the pair's tokens
+    int b, h;
+};
+static_assert(sizeof(ScoresUnit) == 32, "unit ring");
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(384, 1)
+fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const PagedArgs a, const float *in, float *out, const int L, const int R,
+                       const uint32_t idesc) {
+    using C = ScoresCfg<D, kBF16>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) -> uint32_t { return base + C::BAR_OFF + 8u * i; };
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF + 4);
+    ScoresUnit *ring = reinterpret_cast<ScoresUnit *>(gbase + C::RING_OFF);
+
+    if (warp == 9) tmem_alloc(base + C::MISC_OFF, C::TMEM_COLS);
+    if (tid == 0) {
+        *abort_flag = 0u;
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(bar(C::B_KFULL + s), 1);
+            mbar_init(bar(C::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < C::NQ; ++s) {
+            mbar_init(bar(C::B_QFULL + s), 1);
+            mbar_init(bar(C::B_QEMPTY + s), 1);
+        }
+        for (int s = 0; s < 4; ++s) {                     // 2 x group + buffer
+            mbar_init(bar(C::B_SFULL + s), 1);
+            mbar_init(bar(C::B_SEMPTY + s), 4);
+        }
+        mbar_init(bar(C::B_MMADONE), 1);
+        for (int q = 0; q < C::RING; ++q) {
+            mbar_init(bar(C::B_UNIT + q), 1);
+            mbar_init(bar(C::B_FREE + q), 10);            // producer, MMA, 8 group warps
+        }
+        fence_barrier_init();
+    }
+    // The rows of the Q tiles that no box fills are columns of the product:
+    // zeros there keep the scores finite, and a log-sum-exp of +inf their
+    // terms zero.
+    const int box_rows = R * a.group;
+    for (int i = tid; i < C::NQ * C::NCH * (128 - box_rows) * 8; i += C::NTHREADS) {
+        const int chunk = i / ((128 - box_rows) * 8), r = i % ((128 - box_rows) * 8);
+        *reinterpret_cast<uint4 *>(gbase + C::Q_OFF + chunk * C::CHUNK_BYTES + box_rows * 128 + r * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+
+    auto take = [&](uint32_t i, const WaitCtx &w, uint32_t where, ScoresUnit &u) __attribute__((always_inline)) -> bool {
+        const uint32_t q = i % C::RING;
+        if (!mbar_wait_warp(bar(C::B_UNIT + q), (i / C::RING) & 1u, w, where)) return false;
+        u = ring[q];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_FREE + q));
+        return u.k0 >= 0;
+    };
+
+    if (warp >= 8) {
+      regs_shrink<C::REGS_LOW>();
+      if (warp == 10) {
+        // =================== scheduler (whole warp) ===================
+        WaitCtx w{abort_flag, a.status, kRolePaged};
+        uint32_t sent = 0;
+        bool ok = true;
+        auto post = [&](const ScoresUnit &u) __attribute__((always_inline)) {
+            const uint32_t q = sent % C::RING;
+            ok = mbar_wait_warp(bar(C::B_FREE + q), ((sent / C::RING) & 1u) ^ 1u, w, 30);
+            if (ok && lane == 0) {
+                ring[q] = u;
+                mbar_arrive(bar(C::B_UNIT + q));
+            }
+            __syncwarp();
+            ++sent;
+        };
+        // lane l holds sequence b0 + l; units [first, end) of the window
+        int b0 = -32;
+        long long end = 0, incl = 0;
+        PagedSeq s{0, 0, 0, false};
+        long long u = blockIdx.x, st = 2ll * gridDim.x - 1 - 2ll * blockIdx.x;
+        while (ok) {
+            while (u >= end && b0 + 32 < a.B) {
+                b0 += 32;
+                s = PagedSeq{0, 0, 0, false};
+                if (b0 + lane < a.B) s = paged_seq(a.cu_q, a.kv_len, b0 + lane, a.T, a.W, a.ps_log2);
+                if (blockIdx.x == 0) {
+                    if (s.bad) report_bad_index(a.status, 1);
+                    if (s.n > L) report_bad_index(a.status, 3);
+                }
+                s.n = min(s.n, L);                        // (reported: the cached tokens end there)
+                incl = static_cast<long long>((s.n + 255) >> 8) * a.H_kv;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                incl += end;
+                end = __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (u >= end) break;
+            const int l = __ffs(__ballot_sync(0xffffffffu, incl > u)) - 1;
+            ScoresUnit o;
+            o.n = __shfl_sync(0xffffffffu, s.n, l);
+            o.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+            o.m = __shfl_sync(0xffffffffu, s.m, l);
+            o.b = b0 + l;
+            const int pairs = (o.n + 255) >> 8;
+            const long long r = u - (__shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(pairs) * a.H_kv);
+            o.h = static_cast<int>(r / pairs);
+            o.k0 = static_cast<int>(r - static_cast<long long>(o.h) * pairs) * 256;
+            // Q tiles t (positions [t R, t R + R) of the new tokens) that see a
+            // token of [k0, k0 + 256): from the first whose last row reaches k0,
+            // to the last whose first row's window still holds one
+            const int old = o.n - o.m;
+            const int tiles = (o.m + R - 1) / R;
+            o.qa = 0;
+            if (a.wr >= 0) {
+                const long long need = static_cast<long long>(o.k0) - a.wr - old;   // first row with hi > k0
+                o.qa = need <= 0 ? 0 : static_cast<int>(min(need / R, static_cast<long long>(tiles)));
+            }
+            o.qb = tiles;
+            if (a.wl >= 0 && o.k0 >= a.first) {
+                const long long last = static_cast<long long>(o.k0) + 255 + a.wl - old;   // last row with lo <= k0 + 255
+                o.qb = last < 0 ? 0 : static_cast<int>(min(last / R + 1, static_cast<long long>(tiles)));
+            }
+            post(o);
+            u += st;
+            st = 2ll * gridDim.x - st;
+        }
+        if (ok) {
+            ScoresUnit stop{};
+            stop.k0 = -1;
+            post(stop);
+        }
+      } else if (warp == 8) {
+        // =================== TMA producer (whole warp) ===================
+        WaitCtx w{abort_flag, a.status, kRoleProducer};
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(&tm_k);
+        }
+        const PagedBox<C::NCH> bx(a.ps_log2);
+        const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
+        uint32_t kc = 0, qc = 0, ui = 0;
+        uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
+        bool ok = true;
+        ScoresUnit u;
+        while (ok && take(ui, w, 31, u)) {
+            ++ui;
+            if (u.qa >= u.qb) continue;                   // no row sees the pair
+            const int *tb = a.table + static_cast<long long>(u.b) * a.W;
+            const int old = u.n - u.m;
+            const int vlo = paged_lo(old, a.wl), vhi = paged_hi(u.n - 1, u.n, a.wr), nf = min(a.first, vhi);
+            const int nk = u.k0 + 128 < u.n ? 2 : 1;
+            int page[2];
+            for (int x = 0; x < 2; ++x) {
+                const int j = (u.k0 >> 7) + x;
+                page[x] = x < nk && bx.needs(j, vlo, vhi, nf) ? tb[(j * 128 + bx.row) >> a.ps_log2] : a.n_pages;
+            }
+            for (int x = 0; x < nk && ok; ++x, ++kc) {
+                const int j = (u.k0 >> 7) + x;
+                int pg = x ? page[1] : page[0];
+                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
+                    if (bx.needs(j, vlo, vhi, nf)) report_bad_index(a.status, 2);
+                    pg = a.n_pages;
+                }
+                const uint32_t slot = kc % C::NK, ph = (kc / C::NK) & 1u;
+                ok = mbar_wait_warp(bar(C::B_KEMPTY + slot), ph ^ 1u, w, 2);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + slot), C::TILE_BYTES);
+                __syncwarp();
+                if (lane < bx.n_box)
+                    tma_load_4d(&tm_k, base + C::K_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
+                                bar(C::B_KFULL + slot), bx.c * 64, u.h,
+                                (j * 128 + bx.row) & ((1 << a.ps_log2) - 1), pg);
+                armed |= 1u << slot;
+                armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+            }
+            for (int t = u.qa; t < u.qb && ok; ++t, ++qc) {
+                const uint32_t slot = qc % C::NQ, ph = (qc / C::NQ) & 1u;
+                ok = mbar_wait_warp(bar(C::B_QEMPTY + slot), ph ^ 1u, w, 1);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QFULL + slot), q_bytes);
+                __syncwarp();
+                if (lane < C::NCH)
+                    tma_load_4d(&tm_q, base + C::Q_OFF + slot * C::TILE_BYTES + lane * C::CHUNK_BYTES,
+                                bar(C::B_QFULL + slot), lane * 64, u.h * a.group, u.q0 + t * R, 0);
+                qarmed |= 1u << slot;
+                qarmed_par = (qarmed_par & ~(1u << slot)) | (ph << slot);
+            }
+        }
+        for (int s = 0; s < C::NK; ++s)
+            if (armed & (1u << s)) mbar_wait_quiet(bar(C::B_KFULL + s), (armed_par >> s) & 1u, 500000000ull);
+        for (int s = 0; s < C::NQ; ++s)
+            if (qarmed & (1u << s)) mbar_wait_quiet(bar(C::B_QFULL + s), (qarmed_par >> s) & 1u, 500000000ull);
+        __syncwarp();
+      } else if (warp == 9) {
+        // =================== MMA issuer ===================
+        WaitCtx w{abort_flag, a.status, kRoleMma};
+        uint32_t kc = 0, qc = 0, ui = 0, sc0 = 0, sc1 = 0;
+        bool ok = true;
+        auto mma = [&](const int x, const uint32_t kslot, const uint32_t qslot,
+                       uint32_t &sc) __attribute__((always_inline)) -> bool {
+            const int buf = sc & 1u;
+            if (!mbar_wait_warp(bar(C::B_SEMPTY + 2 * x + buf), ((sc >> 1) & 1u) ^ 1u, w, 11)) return false;
+            ++sc;
+            tc_fence_after();
+            const uint64_t kd = smem_desc_sw128(base + C::K_OFF + kslot * C::TILE_BYTES, 16u, 1024u);
+            const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qslot * C::TILE_BYTES, 16u, 1024u);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                mma_ss_f16_elect(tbase + C::col_s(x, buf), kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit_elect(bar(C::B_SFULL + 2 * x + buf));
+            return true;
+        };
+        ScoresUnit u;
+        while (ok && take(ui, w, 32, u)) {
+            ++ui;
+            if (u.qa >= u.qb) continue;
+            const int nk = u.k0 + 128 < u.n ? 2 : 1;
+            const uint32_t k0s = kc % C::NK, k1s = (kc + 1) % C::NK;
+            for (int t = u.qa; t < u.qb && ok; ++t, ++qc) {
+                const uint32_t qs = qc % C::NQ;
+                ok = mbar_wait_warp(bar(C::B_QFULL + qs), (qc / C::NQ) & 1u, w, 14);
+                if (ok && t == u.qa) ok = mbar_wait_warp(bar(C::B_KFULL + k0s), (kc / C::NK) & 1u, w, 13);
+                if (ok) ok = mma(0, k0s, qs, sc0);
+                if (ok && nk == 2) {
+                    if (t == u.qa) ok = mbar_wait_warp(bar(C::B_KFULL + k1s), ((kc + 1) / C::NK) & 1u, w, 13);
+                    if (ok) ok = mma(1, k1s, qs, sc1);
+                }
+                if (!ok) break;
+                mma_commit_elect(bar(C::B_QEMPTY + qs));
+            }
+            if (!ok) break;
+            mma_commit_elect(bar(C::B_KEMPTY + k0s));
+            if (nk == 2) mma_commit_elect(bar(C::B_KEMPTY + k1s));
+            kc += nk;
+        }
+        mma_commit_elect(bar(C::B_MMADONE));
+        mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
+        __syncwarp();
+      }
+    } else {
+        regs_grow<C::REGS_HIGH>();
+        // =================== group x: one cached token a thread ===================
+        const int x = warp >> 2, row = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        WaitCtx w{abort_flag, a.status, x ? kRoleSoftmax1 : kRoleSoftmax0};
+        float *nl = reinterpret_cast<float *>(gbase + C::L_OFF) + x * 128;   // -LSE log2(e) of the columns
+        const float sl2 = a.scale_log2;
+        const float2 c2 = make_float2(sl2, sl2);
+        const int my_pos = row / a.group, my_head = row - my_pos * a.group;  // of column `row`
+        uint32_t ui = 0, sc = 0;
+        bool ok = true;
+        ScoresUnit u;
+        while (ok && take(ui, w, 24, u)) {
+            ++ui;
+            const int kk = u.k0 + x * 128 + row;                             // this thread's token
+            if (u.k0 + x * 128 >= u.n) continue;
+            const int old = u.n - u.m;
+            const size_t at = (static_cast<size_t>(u.b) * a.H_kv + u.h) * L + kk;
+            const float had = in != nullptr && kk < old ? in[at] : 0.f;
+            // rows [ra, rb) of the new tokens see this one
+            long long ra = a.wr >= 0 ? static_cast<long long>(kk) - a.wr - old : 0;
+            long long rb = a.wl >= 0 && kk >= a.first ? static_cast<long long>(kk) + a.wl - old + 1 : u.m;
+            ra = max(ra, 0ll);
+            rb = min(rb, static_cast<long long>(u.m));
+            // -LSE of column `row` of Q tile t, -inf for none (the term is then 0)
+            const float *lrow = a.lse + static_cast<size_t>(u.h * a.group + my_head) * a.T + u.q0;
+            auto column = [&](int t) __attribute__((always_inline)) -> float {
+                const int i = t * R + my_pos;
+                if (my_pos >= R || i >= u.m) return -INFINITY;
+                const float z = lrow[i];
+                return z == -INFINITY ? -INFINITY : z * -1.44269504088896340736f;
+            };
+            float sum = 0.f;
+            float next = u.qa < u.qb ? column(u.qa) : 0.f;
+            for (int t = u.qa; t < u.qb; ++t) {
+                const int nc = min(R, u.m - t * R) * a.group;                // columns of this sequence
+                asm volatile("bar.sync %0, 128;" :: "r"(1 + x) : "memory");  // the last tile's are read
+                nl[row] = next;
+                asm volatile("bar.sync %0, 128;" :: "r"(1 + x) : "memory");
+                if (t + 1 < u.qb) next = column(t + 1);
+                const int buf = sc & 1u;
+                ok = mbar_wait(bar(C::B_SFULL + 2 * x + buf), (sc >> 1) & 1u, w, 20);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++sc;
+                tc_fence_after();
+                const uint32_t tS = tbase + lane_off + C::col_s(x, buf);
+                // columns [ca, cb) see this token
+                const int ca = static_cast<int>(min(max(ra - static_cast<long long>(t) * R, 0ll), static_cast<long long>(R))) * a.group;
+                const int cb = min(nc, static_cast<int>(min(max(rb - static_cast<long long>(t) * R, 0ll), static_cast<long long>(R))) * a.group);
+                const bool all = __all_sync(0xffffffffu, ca == 0 && cb == box_rows);
+                float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
+                auto add = [&](const uint32_t (&s)[32], const int c0) __attribute__((always_inline)) {
+                    const float4 *l4 = reinterpret_cast<const float4 *>(nl + c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 l = l4[c / 4];
+                        const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                                      c2, make_float2(l.x, l.y));
+                        const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                                                      c2, make_float2(l.z, l.w));
+                        float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                        float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                        if (!all) {
+                            if (c0 + c < ca || c0 + c >= cb) e01.x = 0.f;
+                            if (c0 + c + 1 < ca || c0 + c + 1 >= cb) e01.y = 0.f;
+                            if (c0 + c + 2 < ca || c0 + c + 2 >= cb) e23.x = 0.f;
+                            if (c0 + c + 3 < ca || c0 + c + 3 >= cb) e23.y = 0.f;
+                        }
+                        e_a = __fadd2_rn(e_a, e01);
+                        e_b = __fadd2_rn(e_b, e23);
+                    }
+                };
+                uint32_t s0[32];
+                if (nc <= 32) {
+                    tmem_ld32(tS, s0);
+                    tmem_ld_wait();
+                } else {
+                    uint32_t s1[32], s2[32], s3[32];
+                    tmem_ld32(tS, s0);
+                    tmem_ld32(tS + 32, s1);
+                    tmem_ld32(tS + 64, s2);
+                    tmem_ld32(tS + 96, s3);
+                    tmem_ld_wait();
+                    add(s1, 32);
+                    if (nc > 64) {
+                        add(s2, 64);
+                        add(s3, 96);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + 2 * x + buf));
+                add(s0, 0);
+                sum += (e_a.x + e_a.y) + (e_b.x + e_b.y);
+            }
+            if (!ok) break;
+            if (kk < u.n) out[at] = had + sum;
         }
     }
-    const long long w = (static_cast<long long>(b) * a.H_kv + hk) * g.L + j;
-    if (lane == 0) g.out[w] = (g.in != nullptr && j < old ? g.in[w] : 0.f) + sum;
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tbase, C::TMEM_COLS);
+    }
 }
 
-cudaError_t launch_paged_scores(const PagedScoresArgs &g, int d, bool bf16, int, cudaStream_t stream) {
-    const long long most = min(static_cast<long long>(g.L), static_cast<long long>(g.p.W) << g.p.ps_log2);
-    const dim3 grid(static_cast<unsigned>((most + 7) / 8), g.p.H_kv, g.p.B);
-    if (d == 64)
-        bf16 ? fa_paged_scores_kernel<64, true><<<grid, 256, 0, stream>>>(g)
-             : fa_paged_scores_kernel<64, false><<<grid, 256, 0, stream>>>(g);
-    else
-        bf16 ? fa_paged_scores_kernel<128, true><<<grid, 256, 0, stream>>>(g)
-             : fa_paged_scores_kernel<128, false><<<grid, 256, 0, stream>>>(g);
+template <int D, bool kBF16>
+static cudaError_t launch_scores_inst(const PagedScoresLaunch &L) {
+    using C = ScoresCfg<D, kBF16>;
+    auto kern = fa_paged_scores_kernel<D, kBF16>;
+    static unsigned long long configured = 0ull;   // bit per device id (< 64)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(C::SMEM_BYTES));
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&configured, bit, __ATOMIC_ACQ_REL);
+    }
+    // N of the product: as many columns as the groups may read at once
+    const int rows = L.R * L.a.group;
+    const uint32_t cols = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.a, L.in, L.out, L.L, L.R,
+                                                           idesc_f16(128, cols, kBF16, false, false));
     return cudaGetLastError();
+}
+
+cudaError_t launch_paged_scores(const PagedScoresLaunch &L) {
+    if (L.d == 64) return L.bf16 ? launch_scores_inst<64, true>(L) : launch_scores_inst<64, false>(L);
+    return L.bf16 ? launch_scores_inst<128, true>(L) : launch_scores_inst<128, false>(L);
 }
 
 }  // namespace fa
