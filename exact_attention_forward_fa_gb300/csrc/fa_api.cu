@@ -847,7 +847,8 @@ long long fa_paged_workspace_bytes(int d) {
 }
 
 // The pool of pages as {d, H_kv, page_size, n_pages}: a box is up to 128 slots
-// of one head in one page; pages beyond the pool read as zero.
+// of one head in one page; pages beyond the pool read as zero.  At d = 64 a
+// head's row is 128 bytes and the next 128 another head's: no wider promotion.
 static fa_status encode_pages(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt,
                               const fa::PagedArgs &a, int d) {
     const cuuint64_t ps = 1ull << a.ps_log2;
@@ -858,7 +859,7 @@ static fa_status encode_pages(CUtensorMap *m, const void *ptr, CUtensorMapDataTy
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(m, dt, 4, const_cast<void *>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -49,6 +49,25 @@ __device__ __forceinline__ void report_bad_index(uint32_t *status, uint32_t wher
     }
 }
 
+// mbar_wait_warp for a warp whose answer is not urgent: it sleeps between its
+// polls.  A polling warp takes issue slots and shared-memory bandwidth from
+// the warps that work.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, const WaitCtx &w,
+                                               uint32_t where) {
+    bool ok = mbar_try_wait(bar, parity);
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xffffffffu, ok)) {
+        __nanosleep(100);
+        ok = mbar_try_wait(bar, parity);
+        if (*w.abort_flag) return false;
+        if (!ok && globaltimer_ns() - t0 > kWaitLimitNs) {
+            report_timeout(w.abort_flag, w.status, w.role, where);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Sequence b: its first packed row, its new tokens and its cached tokens,
 // forced into the ranges that the buffers have; `bad` tells whether they
 // were outside.

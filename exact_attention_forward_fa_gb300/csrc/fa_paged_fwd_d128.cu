@@ -3,6 +3,6 @@
 
 namespace fa {
 cudaError_t launch_fwd_paged_d128(const PagedFwdLaunch &L) {
-    return L.bf16 ? launch_fwd_paged_inst<128, true>(L) : launch_fwd_paged_inst<128, false>(L);
+    return launch_fwd_paged_dispatch<128>(L);
 }
 }  // namespace fa

@@ -3,6 +3,6 @@
 
 namespace fa {
 cudaError_t launch_fwd_paged_d64(const PagedFwdLaunch &L) {
-    return L.bf16 ? launch_fwd_paged_inst<64, true>(L) : launch_fwd_paged_inst<64, false>(L);
+    return launch_fwd_paged_dispatch<64>(L);
 }
 }  // namespace fa

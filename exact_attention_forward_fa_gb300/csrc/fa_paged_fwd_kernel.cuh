@@ -39,20 +39,27 @@
 
 namespace fa {
 
-template <int D, bool kBF16>
+// kNarrow: Q tiles of at most 32 rows (single tokens).  Their slots hold 32
+// rows -- the product reads 128, whatever lies behind them, into rows that
+// nobody reads -- and the K/V ring takes the space: 6 (12) tiles instead of 4
+// (8).  Bytes in flight are what such calls live on.
+template <int D, bool kBF16, bool kNarrow>
 struct PagedCfg {
     static constexpr int NCH = D / 64;                    // 128-byte column chunks
     static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
     static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
-    static constexpr int NSTAGE = D == 64 ? 8 : 4;        // powers of two
+    static constexpr uint32_t Q_CHUNK = (kNarrow ? 32u : 128u) * 128u;
+    static constexpr uint32_t Q_BYTES = NCH * Q_CHUNK;
+    static constexpr int NSTAGE = (D == 64 ? 2 : 1) * (kNarrow ? 6 : 4);
     static constexpr int NQ = 3;
+    static constexpr int LIVE = kNarrow ? 1 : 4;          // warps of a group that may hold rows
     static constexpr int QK_STEPS = D / 16, PV_STEPS = 8;
     static constexpr int NTHREADS = 384;
     static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
     static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register budget");
     static constexpr int RING = 4;                        // pieces ahead
     static constexpr uint32_t Q_OFF = 0;
-    static constexpr uint32_t KV_OFF = NQ * TILE_BYTES;
+    static constexpr uint32_t KV_OFF = NQ * Q_BYTES;
     static constexpr uint32_t X_OFF = KV_OFF + NSTAGE * TILE_BYTES;   // group H's LSE, 1 / l
     static constexpr uint32_t RING_OFF = X_OFF + 2 * 128 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 64;
@@ -123,12 +130,12 @@ __device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int
     return sum;
 }
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kNarrow>
 __global__ void __launch_bounds__(384, 1)
 fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
                     const int R, const int q_min) {
-    using C = PagedCfg<D, kBF16>;
+    using C = PagedCfg<D, kBF16, kNarrow>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -153,16 +160,16 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(C::B_SFULL + x), 1);
-            mbar_init(bar(C::B_PFULL + x), 4);
+            mbar_init(bar(C::B_PFULL + x), C::LIVE);
             mbar_init(bar(C::B_OFULL + x), 1);
-            mbar_init(bar(C::B_OEMPTY + x), 4);
+            mbar_init(bar(C::B_OEMPTY + x), C::LIVE);
         }
-        mbar_init(bar(C::B_XFULL), 4);
-        mbar_init(bar(C::B_XEMPTY), 4);
+        mbar_init(bar(C::B_XFULL), C::LIVE);
+        mbar_init(bar(C::B_XEMPTY), C::LIVE);
         mbar_init(bar(C::B_MMADONE), 1);
         for (int q = 0; q < C::RING; ++q) {
             mbar_init(bar(C::B_PIECE + q), 1);
-            mbar_init(bar(C::B_FREE + q), 10);            // producer, MMA, 8 softmax warps
+            mbar_init(bar(C::B_FREE + q), 2 + 2 * C::LIVE);   // producer, MMA, softmax warps
         }
         fence_barrier_init();
     }
@@ -235,7 +242,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         uint32_t np_out = 0;
         auto post = [&](const PagedPiece &p) __attribute__((always_inline)) -> bool {
             const uint32_t q = np_out % C::RING;
-            if (!mbar_wait_warp(bar(C::B_FREE + q), ((np_out / C::RING) & 1u) ^ 1u, w, 30)) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait_idle(bar(C::B_FREE + q), ((np_out / C::RING) & 1u) ^ 1u, w, 30)))
+                return false;
             if (lane == 0) {
                 ring[q] = p;
                 mbar_arrive(bar(C::B_PIECE + q));
@@ -338,14 +346,28 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        uint32_t qc = 0, kv = 0, pi = 0;                   // Q tiles, K/V tiles, pieces so far
+        uint32_t qc = 0, pi = 0, slot = 0, ph = 0;         // Q tiles, pieces; K/V slot and its phase
         uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
         bool ok = true;
         const PagedBox<C::NCH> bx(a.ps_log2);
         const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
-        PagedPiece p;
-        while (ok && take(pi, w, 31, p)) {
-            ++pi;
+        // The page ids of a step are read PF steps ahead, and a piece's first
+        // ones while the piece before it still loads: an id comes from L2 or
+        // HBM, and a step may not wait for that.
+        constexpr int PF = 4;
+        auto page_of = [&](const PagedPiece &p, int t) __attribute__((always_inline)) -> int {
+            if (t >= p.t1) return a.n_pages;
+            const int j = paged_tile(p, t);
+            return bx.needs(j, p.vlo, p.vhi, min(a.first, p.vhi))
+                       ? a.table[static_cast<long long>(p.b) * a.W + ((j * 128 + bx.row) >> a.ps_log2)]
+                       : a.n_pages;
+        };
+        PagedPiece p, nx;
+        int page[PF], page_n[PF];
+        bool more = take(pi++, w, 31, p), more_n = false;
+#pragma unroll
+        for (int u = 0; u < PF; ++u) page[u] = more ? page_of(p, p.t0 + u) : 0;
+        while (ok && more) {
             for (int x = 0; x < (p.nh > 0 ? 2 : 1) && ok; ++x) {
                 const uint32_t qs = qc % C::NQ, qph = (qc / C::NQ) & 1u;
                 ok = mbar_wait_warp(bar(C::B_QEMPTY + qs), qph ^ 1u, w, 1);
@@ -353,43 +375,48 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QFULL + qs), q_bytes);
                 __syncwarp();
                 if (lane < C::NCH)
-                    tma_load_4d(&tm_q, base + C::Q_OFF + qs * C::TILE_BYTES + lane * C::CHUNK_BYTES,
+                    tma_load_4d(&tm_q, base + C::Q_OFF + qs * C::Q_BYTES + lane * C::Q_CHUNK,
                                 bar(C::B_QFULL + qs), lane * 64, p.h * a.group, p.qrow + x * R, 0);
                 qarmed |= 1u << qs;
                 qarmed_par = (qarmed_par & ~(1u << qs)) | (qph << qs);
                 ++qc;
             }
-            const int *tb = a.table + static_cast<long long>(p.b) * a.W;
-            const int nf = min(a.first, p.vhi);
-            // the page id of this lane's box of step t (loaded a step ahead)
-            auto page_of = [&](int t) __attribute__((always_inline)) -> int {
-                const int j = paged_tile(p, t);
-                return bx.needs(j, p.vlo, p.vhi, nf) ? tb[(j * 128 + bx.row) >> a.ps_log2] : a.n_pages;
-            };
-            int page = p.t0 < p.t1 ? page_of(p.t0) : 0;
+#pragma unroll 1
             for (int t = p.t0; t < p.t1 && ok; ++t) {
-                const int next = t + 1 < p.t1 ? page_of(t + 1) : 0;
                 const int j = paged_tile(p, t);
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
-                    if (bx.needs(j, p.vlo, p.vhi, nf)) report_bad_index(a.status, 2);
-                    page = a.n_pages;                      // beyond the pool: zeros
+                int pg = page[0];
+#pragma unroll
+                for (int u = 0; u + 1 < PF; ++u) page[u] = page[u + 1];
+                page[PF - 1] = page_of(p, t + PF);
+                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
+                    if (bx.needs(j, p.vlo, p.vhi, min(a.first, p.vhi))) report_bad_index(a.status, 2);
+                    pg = a.n_pages;                        // beyond the pool: zeros
                 }
                 const int row0 = (j * 128 + bx.row) & ((1 << a.ps_log2) - 1);
-                for (int v = 0; v < 2; ++v, ++kv) {
-                    const uint32_t slot = kv % C::NSTAGE, ph = (kv / C::NSTAGE) & 1u;
+                const CUtensorMap *tm = &tm_k;
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v, tm = &tm_v) {
                     ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
                     __syncwarp();
                     if (lane < bx.n_box)
-                        tma_load_4d(v ? &tm_v : &tm_k,
-                                    base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
-                                    bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, page);
+                        tma_load_4d(tm, base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
+                                    bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, pg);
                     armed |= 1u << slot;
                     armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                    if (++slot == C::NSTAGE) { slot = 0; ph ^= 1u; }
                 }
-                page = next;
+                if (t == p.t0 && ok) {
+                    more_n = take(pi++, w, 31, nx);
+#pragma unroll
+                    for (int u = 0; u < PF; ++u) page_n[u] = more_n ? page_of(nx, nx.t0 + u) : 0;
+                }
             }
+            p = nx;
+            more = more_n;
+#pragma unroll
+            for (int u = 0; u < PF; ++u) page[u] = page_n[u];
         }
         // Every issued copy lands before the CTA may end (bounded).
         for (int s = 0; s < C::NSTAGE; ++s)
@@ -399,99 +426,97 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         __syncwarp();
       } else if (warp == 9) {
         // =================== MMA issuer (whole warp, one elected lane issues) ===================
+        // Step i multiplies Q with its K tile, and P of step i - lag with that
+        // step's V tile: with two Q tiles for both of them (lag 1), with one
+        // for the group whose turn it is (lag 2).  Everything that a
+        // descriptor depends on is kept warp-uniform (uniform()): tcgen05.mma
+        // takes uniform registers.
         WaitCtx w{abort_flag, a.status, kRoleMma};
-        uint32_t qc = 0, kv = 0, pi = 0;
-        uint32_t un0 = 0, un1 = 0, pp0 = 0, pp1 = 0;       // accumulator uses, P tiles, per group
+        auto uniform = [](int v) __attribute__((always_inline)) -> int { return __shfl_sync(0xffffffffu, v, 0); };
+        uint32_t qs = 0, qph = 0, ks = 0, kph = 0, vs = 1, vph = 0, pi = 0;   // slots and their phases
+        uint32_t un = 0, pp = 0;                           // bit x: phase of group x's accumulator, of its P
         bool ok = true;
-        auto pv = [&](const int x, const uint32_t idx, const bool begin, const bool end, const bool v_wait,
-                      const uint32_t un, uint32_t &pp) __attribute__((always_inline)) -> bool {
-            const uint32_t slot = idx % C::NSTAGE;
-            if (v_wait && !mbar_wait_warp(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 10)) return false;
-            if (begin && !mbar_wait_warp(bar(C::B_OEMPTY + x), (un & 1u) ^ 1u, w, 11)) return false;
-            if (!mbar_wait_warp(bar(C::B_PFULL + x), pp & 1u, w, 12)) return false;
-            ++pp;
-            tc_fence_after();
-            const uint64_t vd = smem_desc_sw128(base + C::KV_OFF + slot * C::TILE_BYTES, C::CHUNK_BYTES, 1024u);
-#pragma unroll
-            for (int kk = 0; kk < C::PV_STEPS; ++kk)
-                mma_ts_f16_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u, vd + ((kk * 16 * 128u) >> 4),
-                                 C::IDESC_PV, (!begin || kk > 0) ? 1u : 0u);
-            if (end) mma_commit_elect(bar(C::B_OFULL + x));
-            return true;
-        };
-        auto qk = [&](const int x, const uint32_t qi, const bool q_wait, const uint32_t idx,
-                      const bool k_wait) __attribute__((always_inline)) -> bool {
-            const uint32_t slot = idx % C::NSTAGE, qs = qi % C::NQ;
-            if (k_wait && !mbar_wait_warp(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 13)) return false;
-            if (q_wait && !mbar_wait_warp(bar(C::B_QFULL + qs), (qi / C::NQ) & 1u, w, 14)) return false;
-            tc_fence_after();
-            const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::TILE_BYTES, 16u, 1024u);
-            const uint64_t kd = smem_desc_sw128(base + C::KV_OFF + slot * C::TILE_BYTES, 16u, 1024u);
-#pragma unroll
-            for (int kk = 0; kk < C::QK_STEPS; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
-                mma_ss_f16_elect(tbase + C::col_s(x), qd + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
-            }
-            mma_commit_elect(bar(C::B_SFULL + x));
-            return true;
-        };
         PagedPiece p;
         while (ok && take(pi, w, 32, p)) {
             ++pi;
-            const int ns = p.t1 - p.t0;
-            if (p.nh == 0) {
-                // one tile: step i belongs to group i & 1
-                for (int i = 0; i < ns + 2 && ok; ++i) {
-                    if (i >= 2) {
-                        const uint32_t idx = kv + 2 * (i - 2) + 1;
-                        ok = (i & 1) ? pv(1, idx, i == 3, i >= ns, true, un1, pp1)
-                                     : pv(0, idx, i == 2, i >= ns, true, un0, pp0);
+            const int ns = uniform(p.t1 - p.t0);
+            const bool one = uniform(p.nh) == 0;
+            const int lag = one ? 2 : 1;
+            const int s0l = one ? 0 : uniform(max(p.t0, p.skip) - p.t0);       // tile L's first step
+            uint32_t q1 = qs + 1, q1ph = qph;              // tile H's slot
+            if (q1 == C::NQ) { q1 = 0; q1ph ^= 1u; }
+            // (an unused Q tile still has to land before its slot is released)
+            if (s0l >= ns) ok = mbar_wait_warp(bar(C::B_QFULL + qs), qph, w, 15);
+#pragma unroll 1
+            for (int i = 0; i < ns + lag && ok; ++i) {
+                const int iv = i - lag;
+#pragma unroll 1
+                for (int x = one ? i & 1 : 0; x < 2; ++x) {
+                    const int s0 = one ? x : x ? 0 : s0l;
+                    const uint32_t d_s = tbase + (x ? C::col_s(1) : C::col_s(0));
+                    if (iv >= s0) {
+                        const uint32_t d_o = tbase + (x ? C::col_o(1) : C::col_o(0));
+                        const bool begin = iv == s0;
+                        ok = mbar_wait_warp(bar(C::B_KVFULL + vs), vph, w, 10);
+                        if (ok && begin) ok = mbar_wait_warp(bar(C::B_OEMPTY + x), ((un >> x) & 1u) ^ 1u, w, 11);
+                        if (ok) ok = mbar_wait_warp(bar(C::B_PFULL + x), (pp >> x) & 1u, w, 12);
                         if (!ok) break;
-                        mma_commit_elect(bar(C::B_KVEMPTY + idx % C::NSTAGE));
+                        pp ^= 1u << x;
+                        tc_fence_after();
+                        const uint64_t vd = smem_desc_sw128(base + C::KV_OFF + vs * C::TILE_BYTES, C::CHUNK_BYTES, 1024u);
+#pragma unroll
+                        for (int kk = 0; kk < C::PV_STEPS; ++kk)
+                            mma_ts_f16_elect(d_o, d_s + kk * 8u, vd + ((kk * 16 * 128u) >> 4), C::IDESC_PV,
+                                             (!begin || kk > 0) ? 1u : 0u);
+                        if (iv + lag >= ns) {              // its last step
+                            mma_commit_elect(bar(C::B_OFULL + x));
+                            un ^= 1u << x;
+                        }
                     }
-                    if (i < ns) {
-                        const uint32_t idx = kv + 2 * i;
-                        ok = (i & 1) ? qk(1, qc, false, idx, true) : qk(0, qc, i == 0, idx, true);
+                    if (i < ns && i >= s0) {
+                        const uint32_t qx = one || x == 0 ? qs : q1, qxp = one || x == 0 ? qph : q1ph;
+                        ok = mbar_wait_warp(bar(C::B_KVFULL + ks), kph, w, 13);
+                        if (ok && i == s0) ok = mbar_wait_warp(bar(C::B_QFULL + qx), qxp, w, 14);
                         if (!ok) break;
-                        mma_commit_elect(bar(C::B_KVEMPTY + idx % C::NSTAGE));
-                        if (i == ns - 1) mma_commit_elect(bar(C::B_QEMPTY + qc % C::NQ));
+                        tc_fence_after();
+                        const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qx * C::Q_BYTES, 16u, 1024u);
+                        const uint64_t kd = smem_desc_sw128(base + C::KV_OFF + ks * C::TILE_BYTES, 16u, 1024u);
+#pragma unroll
+                        for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+                            const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
+                            const uint32_t ko = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                            mma_ss_f16_elect(d_s, qd + qo, kd + ko, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                        }
+                        mma_commit_elect(bar(C::B_SFULL + x));
                     }
+                    if (one) break;
                 }
-                ++qc;
-                ++un0;
-                un1 += ns >= 2 ? 1u : 0u;
-            } else {
-                const int s0 = max(p.t0, p.skip) - p.t0;    // first step of tile L (ns or more: none)
-                // (an unused Q tile still has to land before its slot is released)
-                if (s0 >= ns) ok = mbar_wait_warp(bar(C::B_QFULL + qc % C::NQ), (qc / C::NQ) & 1u, w, 15);
-                for (int i = 0; i <= ns && ok; ++i) {
-                    const uint32_t vi = kv + 2 * (i - 1) + 1, ki = kv + 2 * i;
-                    const bool l_v = i - 1 >= s0, l_k = i < ns && i >= s0;
-                    if (l_v) ok = pv(0, vi, i - 1 == s0, i == ns, true, un0, pp0);
-                    if (ok && l_k) ok = qk(0, qc, i == s0, ki, true);
-                    if (ok && i > 0) ok = pv(1, vi, i == 1, i == ns, !l_v, un1, pp1);
-                    if (ok && i < ns) ok = qk(1, qc + 1, i == 0, ki, !l_k);
-                    if (!ok) break;
-                    if (i == ns - 1) {
-                        mma_commit_elect(bar(C::B_QEMPTY + qc % C::NQ));
-                        mma_commit_elect(bar(C::B_QEMPTY + (qc + 1) % C::NQ));
-                    }
-                    if (i < ns) mma_commit_elect(bar(C::B_KVEMPTY + ki % C::NSTAGE));
-                    if (i > 0) mma_commit_elect(bar(C::B_KVEMPTY + vi % C::NSTAGE));
+                if (!ok) break;
+                if (i == ns - 1) {
+                    mma_commit_elect(bar(C::B_QEMPTY + qs));
+                    if (!one) mma_commit_elect(bar(C::B_QEMPTY + q1));
                 }
-                qc += 2;
-                un0 += s0 < ns ? 1u : 0u;
-                ++un1;
+                if (i < ns) {
+                    mma_commit_elect(bar(C::B_KVEMPTY + ks));
+                    ks += 2;
+                    if (ks >= C::NSTAGE) { ks = 0; kph ^= 1u; }
+                }
+                if (iv >= 0) {
+                    mma_commit_elect(bar(C::B_KVEMPTY + vs));
+                    vs += 2;
+                    if (vs >= C::NSTAGE) { vs = 1; vph ^= 1u; }
+                }
             }
-            kv += 2 * ns;
+            qs = one ? qs + 1 : q1 + 1;
+            qph = one ? qph : q1ph;
+            if (qs == C::NQ) { qs = 0; qph ^= 1u; }
         }
         // Drain: every issued MMA completes before TMEM is released.
         mma_commit_elect(bar(C::B_MMADONE));
         mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
         __syncwarp();
       }
-    } else {
-        regs_grow<C::REGS_HIGH>();
+    } else if (regs_grow<C::REGS_HIGH>(); (warp & 3) < C::LIVE) {
         // =================== softmax group x ===================
         const int x = warp >> 2;
         const int row = tid & 127;
@@ -535,9 +560,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const uint32_t idx = kv + 2 * i + 1, slot = idx % C::NSTAGE;
                     ok = mbar_wait(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 22);
                     if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
-                    const int kk = k0 + row;
-                    if (!((kk >= p.vlo && kk < p.vhi) || kk < nf)) {
-                        uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + row * 128;
+#pragma unroll 1
+                    for (int vrow = row; vrow < 128; vrow += 32 * C::LIVE) {
+                        const int kk = k0 + vrow;
+                        if ((kk >= p.vlo && kk < p.vhi) || kk < nf) continue;
+                        uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + vrow * 128;
 #pragma unroll
                         for (int ch = 0; ch < C::NCH; ++ch)
 #pragma unroll
@@ -554,29 +581,52 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc_fence_after();
                 uint32_t s[128];
                 float *sf = reinterpret_cast<float *>(s);
-                const int lim = khi - k0, llo = klo - k0, lf = kf - k0;
-                auto load_s = [&]() __attribute__((always_inline)) {
-                    tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
-                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-                    tmem_ld_wait();
-                    if (valid && lim < 128) {
-#pragma unroll
-                        for (int cc = 0; cc < 128; ++cc) if (cc >= lim) sf[cc] = -INFINITY;
-                    }
-                    if (valid && llo > 0 && lf < 128) {
-#pragma unroll
-                        for (int cc = 0; cc < 128; ++cc) if (cc < llo && cc >= lf) sf[cc] = -INFINITY;
-                    }
-                };
-                load_s();
+                // visible columns: c < lim, and c >= llo or c < lf
+                const int lim = valid ? khi - k0 : 128, llo = valid ? klo - k0 : 0, lf = kf - k0;
+                const bool masked = __any_sync(0xffffffffu, lim < 128 || (llo > 0 && lf < 128));
                 float rn = r, corr = 1.f;
                 bool need = false;
                 float2 e_a, e_b;
                 uint32_t pk[64];
                 const float2 c2 = make_float2(sl2, sl2);
-                auto exps = [&](const float rs) __attribute__((always_inline)) {
+                // P against the current reference first; the maximum only on the
+                // first tile or when a row's sum got too large (fa_fwd_kernel.cuh)
+                bool keep = __all_sync(0xffffffffu, r != -INFINITY);
+#pragma unroll 1
+                for (;;) {
+                    tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                    tmem_ld_wait();
+                    if (masked) {
+#pragma unroll
+                        for (int w32 = 0; w32 < 4; ++w32) {
+                            // bit c of m: column 32 w32 + c is visible
+                            auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                            const uint32_t m = below(lim - 32 * w32) & (~below(llo - 32 * w32) | below(lf - 32 * w32));
+#pragma unroll
+                            for (int cc = 0; cc < 32; ++cc)
+                                if (!(m & (1u << cc))) sf[32 * w32 + cc] = -INFINITY;
+                        }
+                    }
+                    if (!keep) {
+                        float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
+#pragma unroll
+                        for (int cc = 4; cc < 128; cc += 8) {
+                            m0 = max3(m0, sf[cc + 0], sf[cc + 4]);
+                            m1 = max3(m1, sf[cc + 1], sf[cc + 5]);
+                            m2 = max3(m2, sf[cc + 2], sf[cc + 6]);
+                            m3 = max3(m3, sf[cc + 3], sf[cc + 7]);
+                        }
+                        const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+                        if (valid) {
+                            if (r == -INFINITY) rn = bnew;
+                            else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
+                            need = (r != -INFINITY) && (rn != r);
+                        }
+                    }
+                    const float rs = rn == -INFINITY ? 0.f : rn;
                     const float2 nr2 = make_float2(-rs, -rs);
                     e_a = make_float2(0.f, 0.f);
                     e_b = e_a;
@@ -591,32 +641,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         e_a = __fadd2_rn(e_a, e01);
                         e_b = __fadd2_rn(e_b, e23);
                     }
-                };
-                // P against the current reference first; the maximum only on the
-                // first tile or when the row's sum got too large (fa_fwd_kernel.cuh)
-                bool keep = __all_sync(0xffffffffu, r != -INFINITY);
-                if (keep) {
-                    exps(r);
+                    if (!keep) break;
                     const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
-                    keep = __all_sync(0xffffffffu, !valid || ts <= C::KEEP_SUM);
-                    if (!keep) load_s();
-                }
-                if (!keep) {
-                    float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
-#pragma unroll
-                    for (int cc = 4; cc < 128; cc += 8) {
-                        m0 = max3(m0, sf[cc + 0], sf[cc + 4]);
-                        m1 = max3(m1, sf[cc + 1], sf[cc + 5]);
-                        m2 = max3(m2, sf[cc + 2], sf[cc + 6]);
-                        m3 = max3(m3, sf[cc + 3], sf[cc + 7]);
-                    }
-                    const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
-                    if (valid) {
-                        if (r == -INFINITY) rn = bnew;
-                        else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
-                        need = (r != -INFINITY) && (rn != r);
-                    }
-                    exps((rn == -INFINITY) ? 0.f : rn);
+                    if (__all_sync(0xffffffffu, !valid || ts <= C::KEEP_SUM)) break;
+                    keep = false;
                 }
                 tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
                 tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
@@ -778,70 +806,118 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 }
 
 // Joins the parts of the units that the shares' borders cut: LSE = log sum_s
-// exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  CTA (c, y) takes rows y, y +
-// gridDim.y, ... of the cut unit that starts in share c; its part 0 is slot
-// 2 c + 1, part s > 0 slot 2 (c + s).  A row's parts are split over the eight
-// warps (part s to warp s % 8) and the warps' sums added in order.
+// exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  CTA (c, y) works on the cut unit
+// that starts in share c; its part 0 is slot 2 c + 1, part s > 0 slot 2 (c + s).
+// A part with LSE = -inf saw nothing and its O may be unwritten: it is not
+// read.  Up to eight parts (a chunk's unit has two or three): one warp a row,
+// all loads of the row at once.  More (single tokens against a long cache, a
+// part for every SM): the CTA takes a row, each warp every eighth part, and
+// the warps' sums are added in order.
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedArgs a, const PagedWork wk, const int R) {
     constexpr int E = D / 32;
     __shared__ float s_acc[8][D];
-    __shared__ float s_m[8], s_l[8];
+    __shared__ float s_l[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int *desc = wk.desc + 8 * c;
-    const int parts = desc[0];
+    const int4 *d4 = reinterpret_cast<const int4 *>(wk.desc + 8 * c);
+    const int4 d0 = d4[0], d1 = d4[1];
+    const int parts = d0.x, qrow = d0.y, nl = d0.z, nh = d0.w, h = d1.x;
     if (parts == 0) return;
-    const int qrow = desc[1], nl = desc[2], nh = desc[3], h = desc[4];
-    for (int rr = blockIdx.y; rr < (nl + nh) * a.group; rr += gridDim.y) {
-        const int tile = rr >= nl * a.group ? 1 : 0;
-        const int row = tile ? rr - nl * a.group : rr;
-        float m = -INFINITY, l = 0.f, acc[E];
+    const int rows = (nl + nh) * a.group;
+    auto slot = [&](int s, int tile, int row) __attribute__((always_inline)) -> size_t {
+        return (static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 2 + tile) * 128 + row;
+    };
+    auto write = [&](int tile, int row, const float (&acc)[E], float M, float L) __attribute__((always_inline)) {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int tok = qrow + tile * R + row / a.group, qh = h * a.group + row % a.group;
+        uint32_t pk[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) pk[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
+        uint16_t *dst = reinterpret_cast<uint16_t *>(a.o) + (static_cast<size_t>(tok) * a.H + qh) * D + lane * E;
+        if constexpr (E == 2) *reinterpret_cast<uint32_t *>(dst) = pk[0];
+        else *reinterpret_cast<uint2 *>(dst) = make_uint2(pk[0], pk[1]);
+        if (a.lse != nullptr && lane == 0)
+            a.lse[static_cast<size_t>(qh) * a.T + tok] =
+                L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    };
+    auto load = [&](size_t part, float (&v)[E]) __attribute__((always_inline)) {
+        const float *src = wk.o + part * D + lane * E;
+        if constexpr (E == 2) {
+            const float2 t = *reinterpret_cast<const float2 *>(src);
+            v[0] = t.x; v[1] = t.y;
+        } else {
+            const float4 t = *reinterpret_cast<const float4 *>(src);
+            v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+        }
+    };
+    if (parts <= 8) {
+        for (int rr = blockIdx.y * 8 + warp; rr < rows; rr += gridDim.y * 8) {
+            const int tile = rr >= nl * a.group ? 1 : 0, row = tile ? rr - nl * a.group : rr;
+            float z[8], v[8][E], acc[E];
+#pragma unroll
+            for (int s = 0; s < 8; ++s) z[s] = s < parts ? wk.lse[slot(s, tile, row)] : -INFINITY;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < parts) load(slot(s, tile, row), v[s]);
+            float M = z[0], L = 0.f;
+#pragma unroll
+            for (int s = 1; s < 8; ++s) M = fmaxf(M, z[s]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                if (z[s] == -INFINITY) continue;
+                const float wt = ex2_approx(z[s] - M);
+                L += wt;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[s][e], acc[e]);
+            }
+            write(tile, row, acc, M, L);
+        }
+        return;
+    }
+    for (int rr = blockIdx.y; rr < rows; rr += gridDim.y) {
+        const int tile = rr >= nl * a.group ? 1 : 0, row = tile ? rr - nl * a.group : rr;
+        float M = -INFINITY;
+        for (int s = lane; s < parts; s += 32) M = fmaxf(M, wk.lse[slot(s, tile, row)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int s = warp; s < parts; s += 8) {
-            const size_t part = (static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 2 + tile) * 128 + row;
-            const float z = wk.lse[part];
-            if (z == -INFINITY) continue;                 // the part saw nothing (its O may be unwritten)
-            const float *src = wk.o + part * D + lane * E;
-            float v[E];
+        for (int s0 = warp; s0 < parts; s0 += 32) {
+            float z[4], v[4][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = src[e];
-            const float mn = fmaxf(m, z);
-            const float k = ex2_approx(m - mn), wt = ex2_approx(z - mn);
-            l = fmaf(l, k, wt);
+            for (int u = 0; u < 4; ++u) {
+                const int s = s0 + 8 * u;
+                z[u] = s < parts ? wk.lse[slot(s, tile, row)] : -INFINITY;
+                if (s < parts) load(slot(s, tile, row), v[u]);
+            }
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], k, wt * v[e]);
-            m = mn;
+            for (int u = 0; u < 4; ++u) {
+                if (z[u] == -INFINITY) continue;
+                const float wt = ex2_approx(z[u] - M);
+                l += wt;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[u][e], acc[e]);
+            }
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-        if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+        if (lane == 0) s_l[warp] = l;
         __syncthreads();
         if (warp == 0) {
-            float M = s_m[0], L = 0.f;
-#pragma unroll
-            for (int q = 1; q < 8; ++q) M = fmaxf(M, s_m[q]);
+            float L = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = 0.f;
-            if (M != -INFINITY) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float k = ex2_approx(s_m[q] - M);
-                    L = fmaf(s_l[q], k, L);
+            for (int q = 0; q < 8; ++q) {
+                L += s_l[q];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[q][lane * E + e], k, acc[e]);
-                }
+                for (int e = 0; e < E; ++e) acc[e] += s_acc[q][lane * E + e];
             }
-            const float inv = L > 0.f ? 1.f / L : 0.f;
-            const int tok = qrow + tile * R + row / a.group, qh = h * a.group + row % a.group;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.o) +
-                                                         (static_cast<size_t>(tok) * a.H + qh) * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
-            if (a.lse != nullptr && lane == 0)
-                a.lse[static_cast<size_t>(qh) * a.T + tok] =
-                    L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+            write(tile, row, acc, M, L);
         }
         __syncthreads();
     }

@@ -6,10 +6,10 @@
 
 namespace fa {
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kNarrow>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
-    using C = PagedCfg<D, kBF16>;
-    auto kern = fa_paged_fwd_kernel<D, kBF16>;
+    using C = PagedCfg<D, kBF16, kNarrow>;
+    auto kern = fa_paged_fwd_kernel<D, kBF16, kNarrow>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -37,6 +37,13 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16>, L.a, L.w, L.R);
+}
+
+template <int D>
+cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
+    if (L.R * L.a.group <= 32)
+        return L.bf16 ? launch_fwd_paged_inst<D, true, true>(L) : launch_fwd_paged_inst<D, false, true>(L);
+    return L.bf16 ? launch_fwd_paged_inst<D, true, false>(L) : launch_fwd_paged_inst<D, false, false>(L);
 }
 
 }  // namespace fa

@@ -212,25 +212,31 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         uint32_t kc = 0, qc = 0, ui = 0;
         uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        ScoresUnit u;
-        while (ok && take(ui, w, 31, u)) {
-            ++ui;
+        // page ids of a unit's two tiles, read while the unit before it loads
+        auto page_of = [&](const ScoresUnit &u, int x) __attribute__((always_inline)) -> int {
+            const int j = (u.k0 >> 7) + x, vhi = paged_hi(u.n - 1, u.n, a.wr);
+            if (u.qa >= u.qb || !bx.needs(j, paged_lo(u.n - u.m, a.wl), vhi, min(a.first, vhi))) return a.n_pages;
+            return a.table[static_cast<long long>(u.b) * a.W + ((j * 128 + bx.row) >> a.ps_log2)];
+        };
+        ScoresUnit u, nx;
+        bool more = take(ui++, w, 31, u);
+        int page[2] = {0, 0};
+        if (more) { page[0] = page_of(u, 0); page[1] = page_of(u, 1); }
+        for (; ok && more; u = nx) {
+            int mine[2] = {page[0], page[1]};
+            more = take(ui++, w, 31, nx);
+            if (more) { page[0] = page_of(nx, 0); page[1] = page_of(nx, 1); }
             if (u.qa >= u.qb) continue;                   // no row sees the pair
-            const int *tb = a.table + static_cast<long long>(u.b) * a.W;
-            const int old = u.n - u.m;
-            const int vlo = paged_lo(old, a.wl), vhi = paged_hi(u.n - 1, u.n, a.wr), nf = min(a.first, vhi);
             const int nk = u.k0 + 128 < u.n ? 2 : 1;
-            int page[2];
+#pragma unroll
             for (int x = 0; x < 2; ++x) {
+                if (x >= nk || !ok) break;
                 const int j = (u.k0 >> 7) + x;
-                page[x] = x < nk && bx.needs(j, vlo, vhi, nf) ? tb[(j * 128 + bx.row) >> a.ps_log2] : a.n_pages;
-            }
-            for (int x = 0; x < nk && ok; ++x, ++kc) {
-                const int j = (u.k0 >> 7) + x;
-                int pg = x ? page[1] : page[0];
+                int pg = mine[x];
                 if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
-                    if (bx.needs(j, vlo, vhi, nf)) report_bad_index(a.status, 2);
-                    pg = a.n_pages;
+                    const int vhi = paged_hi(u.n - 1, u.n, a.wr);
+                    if (bx.needs(j, paged_lo(u.n - u.m, a.wl), vhi, min(a.first, vhi))) report_bad_index(a.status, 2);
+                    pg = a.n_pages;                       // beyond the pool: zeros
                 }
                 const uint32_t slot = kc % C::NK, ph = (kc / C::NK) & 1u;
                 ok = mbar_wait_warp(bar(C::B_KEMPTY + slot), ph ^ 1u, w, 2);
@@ -243,6 +249,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                                 (j * 128 + bx.row) & ((1 << a.ps_log2) - 1), pg);
                 armed |= 1u << slot;
                 armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                ++kc;
             }
             for (int t = u.qa; t < u.qb && ok; ++t, ++qc) {
                 const uint32_t slot = qc % C::NQ, ph = (qc / C::NQ) & 1u;
