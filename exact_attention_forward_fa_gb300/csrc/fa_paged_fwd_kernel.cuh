@@ -10,7 +10,7 @@
 // first, the sliding window's first and then those of the first tokens.
 //   * Two tiles: both softmax groups walk every step, each for its own tile
 //     (the schedule of fa_fwd_kernel.cuh): 256 rows per K/V tile read.
-//   * One tile (single tokens and short chunks): the groups take the steps in
+//   * One tile (single tokens, short chunks; always in the narrow kernel): the groups take the steps in
 //     turn, each with an accumulator of its own, joined in TMEM at the end.
 //     The chain QK -> softmax -> PV of a step is as long as two K/V tiles
 //     take from HBM, so two chains side by side keep the loads going.
@@ -23,9 +23,16 @@
 // CTA) and fa_paged_combine_kernel joins them in order.  Shares differ by one
 // step at most, whatever the lengths.
 //
-// Warps: 0-3 and 4-7 the softmax groups, 8 the TMA producer (all lanes: one
-// box of a page each), 9 the MMA issuer, 10 walks the share and posts its
-// pieces in a ring that the others read.
+// Warps: 0-3 and 4-7 the softmax groups, 8 and 11 the TMA producers of K and V
+// (all lanes: one box of a page each), 9 the MMA issuer, 10 walks the share and
+// posts its pieces in a ring that the others read.
+//
+// Code size.  Twelve warps run five different roles, and what their loops
+// execute has to stay in the instruction cache: with two copies of the softmax
+// step, four of each product and non-uniform descriptors (184 KB of code) every
+// role ran at a third of its speed; as it is (one copy each, ~105 KB, most of
+// it outside the loops) single tokens at d = 64 went from 120 to 66 us (512
+// sequences of 2048).
 //
 // Pages.  A 128-key tile is 128 / page_size boxes (or part of one page).  A
 // page that no row of the unit sees, or a bad id, is loaded from beyond the
@@ -112,19 +119,19 @@ __device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, const P
     t.T = max(1, t.nw + min((f >> 7) + ((f & 127) != 0), lo));   // an empty unit still writes O = 0
     return t;
 }
-// Steps of unit p of a sequence (2 R positions a unit).
-__device__ __forceinline__ int paged_unit_steps(const PagedSeq &s, int p, int R, const PagedArgs &a) {
-    const int i0 = p * 2 * R;
-    return paged_tiles(s.n - s.m + i0, s.n - s.m + min(s.m, i0 + 2 * R) - 1, s.n, a).T;
+// Steps of unit p of a sequence (U positions a unit).
+__device__ __forceinline__ int paged_unit_steps(const PagedSeq &s, int p, int U, const PagedArgs &a) {
+    const int i0 = p * U;
+    return paged_tiles(s.n - s.m + i0, s.n - s.m + min(s.m, i0 + U) - 1, s.n, a).T;
 }
-__device__ __forceinline__ int paged_units(const PagedSeq &s, int R) {
-    return static_cast<int>((static_cast<long long>(s.m) + 2 * R - 1) / (2 * R));
+__device__ __forceinline__ int paged_units(const PagedSeq &s, int U) {
+    return static_cast<int>((static_cast<long long>(s.m) + U - 1) / U);
 }
 // Steps of all units of a sequence, by the whole warp.
-__device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int R, const PagedArgs &a) {
-    const int np = paged_units(s, R);
+__device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int U, const PagedArgs &a) {
+    const int np = paged_units(s, U);
     long long sum = 0;
-    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s, p, R, a);
+    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s, p, U, a);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
@@ -169,10 +176,11 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         mbar_init(bar(C::B_MMADONE), 1);
         for (int q = 0; q < C::RING; ++q) {
             mbar_init(bar(C::B_PIECE + q), 1);
-            mbar_init(bar(C::B_FREE + q), 2 + 2 * C::LIVE);   // producer, MMA, softmax warps
+            mbar_init(bar(C::B_FREE + q), 3 + 2 * C::LIVE);   // producers, MMA, softmax warps
         }
         fence_barrier_init();
     }
+    const int U = kNarrow ? R : 2 * R;                     // positions of a unit
     // Scan: thread i owns sequences [i k, (i + 1) k).  Scratch lies in the
     // K/V ring, which no copy uses yet.
     long long *scan = reinterpret_cast<long long *>(gbase + C::KV_OFF);   // [12], then the start
@@ -183,13 +191,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         PagedSeq s{0, 0, 0, false};
         if (b < a.B) s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
         if (s.bad && blockIdx.x == 0) report_bad_index(a.status, 1);
-        const int np = paged_units(s, R);
+        const int np = paged_units(s, U);
         if (np <= 2)
-            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s, p, R, a);
+            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s, p, U, a);
         for (unsigned big = __ballot_sync(0xffffffffu, np > 2); big != 0; big &= big - 1) {
             const int src = __ffs(big) - 1;
             PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
-            const long long sum = paged_seq_steps_warp(t, R, a);
+            const long long sum = paged_seq_steps_warp(t, U, a);
             if (lane == src) mine += sum;
         }
     }
@@ -260,16 +268,16 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             long long at = scan_w, per = 0;                // steps before sequence b; of one K/V head
             PagedSeq s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
             for (;;) {
-                per = paged_seq_steps_warp(s, R, a);
+                per = paged_seq_steps_warp(s, U, a);
                 if (w0 < at + per * a.H_kv || b + 1 >= a.B) break;
                 at += per * a.H_kv;
                 s = paged_seq(a.cu_q, a.kv_len, ++b, a.T, a.W, a.ps_log2);
             }
             int h = static_cast<int>((w0 - at) / per);
             long long rem = (w0 - at) - h * per;           // steps into this head's units
-            int np = paged_units(s, R), p = 0;
+            int np = paged_units(s, U), p = 0;
             for (int p0 = 0; p0 < np; p0 += 32) {
-                const long long mine_t = p0 + lane < np ? paged_unit_steps(s, p0 + lane, R, a) : 0;
+                const long long mine_t = p0 + lane < np ? paged_unit_steps(s, p0 + lane, U, a) : 0;
                 long long inc = mine_t;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -288,10 +296,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             int t0 = static_cast<int>(rem);
             for (long long at_w = w0; ok && at_w < w1;) {
                 PagedPiece pc;
-                const int i0 = p * 2 * R, left = s.m - i0;
+                const int i0 = p * U, left = s.m - i0;
                 pc.qrow = s.q0 + i0;
                 pc.nl = min(left, R);
-                pc.nh = min(max(left - R, 0), R);
+                pc.nh = kNarrow ? 0 : min(max(left - R, 0), R);
                 pc.pos = s.n - s.m + i0;
                 pc.n = s.n;
                 pc.b = b;
@@ -326,7 +334,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         do {
                             if (++b >= a.B) break;
                             s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-                            np = paged_units(s, R);
+                            np = paged_units(s, U);
                         } while (np == 0);
                         if (b >= a.B) break;
                     }
@@ -338,15 +346,21 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             end.qrow = -1;
             post(end);
         }
-      } else if (warp == 8) {
-        // =================== TMA producer (whole warp) ===================
+      } else if (warp != 9) {
+        // =================== TMA producers (whole warps) ===================
+        // Warp 8 loads Q and K, warp 11 V, each into its half of the ring (K
+        // tiles in the even slots).  The lanes of a warp issue their boxes one
+        // after the other, ~55 cycles each: with 16-token pages a K/V tile pair
+        // is 64 of them, which one warp could not issue in the time that HBM
+        // takes for the pair.
         WaitCtx w{abort_flag, a.status, kRoleProducer};
+        const bool is_v = warp == 11;
+        const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
         if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
+            if (!is_v) tma_prefetch_desc(&tm_q);
+            tma_prefetch_desc(tm);
         }
-        uint32_t qc = 0, pi = 0, slot = 0, ph = 0;         // Q tiles, pieces; K/V slot and its phase
+        uint32_t qc = 0, pi = 0, slot = is_v, ph = 0;      // Q tiles, pieces; ring slot and its phase
         uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
         bool ok = true;
         const PagedBox<C::NCH> bx(a.ps_log2);
@@ -368,7 +382,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll
         for (int u = 0; u < PF; ++u) page[u] = more ? page_of(p, p.t0 + u) : 0;
         while (ok && more) {
-            for (int x = 0; x < (p.nh > 0 ? 2 : 1) && ok; ++x) {
+            for (int x = is_v ? 2 : 0; x < (p.nh > 0 ? 2 : 1) && ok; ++x) {
                 const uint32_t qs = qc % C::NQ, qph = (qc / C::NQ) & 1u;
                 ok = mbar_wait_warp(bar(C::B_QEMPTY + qs), qph ^ 1u, w, 1);
                 if (!ok) break;
@@ -393,20 +407,17 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     pg = a.n_pages;                        // beyond the pool: zeros
                 }
                 const int row0 = (j * 128 + bx.row) & ((1 << a.ps_log2) - 1);
-                const CUtensorMap *tm = &tm_k;
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v, tm = &tm_v) {
-                    ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
-                    __syncwarp();
-                    if (lane < bx.n_box)
-                        tma_load_4d(tm, base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
-                                    bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, pg);
-                    armed |= 1u << slot;
-                    armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
-                    if (++slot == C::NSTAGE) { slot = 0; ph ^= 1u; }
-                }
+                ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
+                __syncwarp();
+                if (lane < bx.n_box)
+                    tma_load_4d(tm, base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
+                                bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, pg);
+                armed |= 1u << slot;
+                armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                slot += 2;
+                if (slot >= C::NSTAGE) { slot = is_v; ph ^= 1u; }
                 if (t == p.t0 && ok) {
                     more_n = take(pi++, w, 31, nx);
 #pragma unroll
@@ -440,7 +451,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         while (ok && take(pi, w, 32, p)) {
             ++pi;
             const int ns = uniform(p.t1 - p.t0);
-            const bool one = uniform(p.nh) == 0;
+            const bool one = kNarrow || uniform(p.nh) == 0;
             const int lag = one ? 2 : 1;
             const int s0l = one ? 0 : uniform(max(p.t0, p.skip) - p.t0);       // tile L's first step
             uint32_t q1 = qs + 1, q1ph = qph;              // tile H's slot
@@ -535,7 +546,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         PagedPiece p;
         while (ok && take(pi, w, 24, p)) {
             ++pi;
-            const bool one = p.nh == 0;
+            const bool one = kNarrow || p.nh == 0;
             const int ns = p.t1 - p.t0;
             const int tile = one ? 0 : x;                  // the Q tile this group works on
             const int npos = tile ? p.nh : p.nl;
