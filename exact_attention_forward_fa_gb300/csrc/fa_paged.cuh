@@ -54,16 +54,15 @@ __device__ __forceinline__ void report_bad_index(uint32_t *status, uint32_t wher
 // the warps that work.
 __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, const WaitCtx &w,
                                                uint32_t where) {
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
     const uint64_t t0 = globaltimer_ns();
-    while (!__all_sync(0xffffffffu, ok)) {
+    while (!ok) {
         __nanosleep(100);
-        ok = mbar_try_wait(bar, parity);
-        if (*w.abort_flag) return false;
-        if (!ok && globaltimer_ns() - t0 > kWaitLimitNs) {
-            report_timeout(w.abort_flag, w.status, w.role, where);
-            return false;
-        }
+        ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+        if (ok) break;
+        const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+        if (late) report_timeout(w.abort_flag, w.status, w.role, where);
+        if (__any_sync(0xffffffffu, late || *w.abort_flag != 0u)) return false;   // all lanes together
     }
     return true;
 }

@@ -42,31 +42,27 @@
 // Every mbarrier wait is bounded (fa_device.cuh).
 #pragma once
 
-#include "fa_paged.cuh"
+#include "fa_paged_share.cuh"
 
 namespace fa {
 
-// kNarrow: Q tiles of at most 32 rows (single tokens).  Their slots hold 32
-// rows -- the product reads 128, whatever lies behind them, into rows that
-// nobody reads -- and the K/V ring takes the space: 6 (12) tiles instead of 4
-// (8).  Bytes in flight are what such calls live on.
-template <int D, bool kBF16, bool kNarrow>
+template <int D, bool kBF16>
 struct PagedCfg {
     static constexpr int NCH = D / 64;                    // 128-byte column chunks
     static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
     static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
-    static constexpr uint32_t Q_CHUNK = (kNarrow ? 32u : 128u) * 128u;
-    static constexpr uint32_t Q_BYTES = NCH * Q_CHUNK;
-    static constexpr int NSTAGE = (D == 64 ? 2 : 1) * (kNarrow ? 6 : 4);
+    static constexpr int NSTAGE = D == 64 ? 8 : 4;
+    static constexpr bool kByStep = false;                // K in the even slots, V in the odd ones
+    static constexpr int NRING = NSTAGE;
     static constexpr int NQ = 3;
-    static constexpr int LIVE = kNarrow ? 1 : 4;          // warps of a group that may hold rows
     static constexpr int QK_STEPS = D / 16, PV_STEPS = 8;
     static constexpr int NTHREADS = 384;
     static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
     static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register budget");
     static constexpr int RING = 4;                        // pieces ahead
+    static constexpr uint32_t Q_CHUNK = CHUNK_BYTES, Q_BYTES = TILE_BYTES;
     static constexpr uint32_t Q_OFF = 0;
-    static constexpr uint32_t KV_OFF = NQ * Q_BYTES;
+    static constexpr uint32_t KV_OFF = NQ * TILE_BYTES;
     static constexpr uint32_t X_OFF = KV_OFF + NSTAGE * TILE_BYTES;   // group H's LSE, 1 / l
     static constexpr uint32_t RING_OFF = X_OFF + 2 * 128 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 64;
@@ -88,61 +84,12 @@ struct PagedCfg {
     static constexpr float TAU = 8.0f, KEEP_SUM = 65536.0f;
 };
 
-// One piece of a share, as posted in the ring.
-struct __align__(16) PagedPiece {
-    int qrow;           // packed row of tile L's first position; -1: no more pieces
-    int nl, nh;         // positions in tiles L and H (nh = 0: one tile)
-    int pos;            // cache position of tile L's first position
-    int n, b, h;        // cached tokens, sequence, K/V head
-    int hi, nw, T;      // one past the last key tile, steps in the window, all steps
-    int t0, t1;         // this piece's steps
-    int skip;           // steps that tile L does not see
-    int slot;           // part in the workspace, or -1: the whole unit
-    int vlo, vhi;       // keys of the window that any row sees
-};
-static_assert(sizeof(PagedPiece) == 64, "piece ring");
-
-// The key tile of step t.
-__device__ __forceinline__ int paged_tile(const PagedPiece &p, int t) {
-    return t < p.nw ? p.hi - 1 - t : (p.T - 1) - t;
-}
-
-// Key tiles that rows at positions pa .. pb (of n cached tokens) see.
-struct PagedTiles { int hi, nw, T; };
-__device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, const PagedArgs &a) {
-    const int khi = paged_hi(pb, n, a.wr);
-    PagedTiles t;
-    t.hi = (khi >> 7) + ((khi & 127) != 0);
-    const int lo = min(paged_lo(pa, a.wl) >> 7, t.hi);
-    const int f = min(a.first, khi);
-    t.nw = t.hi - lo;
-    t.T = max(1, t.nw + min((f >> 7) + ((f & 127) != 0), lo));   // an empty unit still writes O = 0
-    return t;
-}
-// Steps of unit p of a sequence (U positions a unit).
-__device__ __forceinline__ int paged_unit_steps(const PagedSeq &s, int p, int U, const PagedArgs &a) {
-    const int i0 = p * U;
-    return paged_tiles(s.n - s.m + i0, s.n - s.m + min(s.m, i0 + U) - 1, s.n, a).T;
-}
-__device__ __forceinline__ int paged_units(const PagedSeq &s, int U) {
-    return static_cast<int>((static_cast<long long>(s.m) + U - 1) / U);
-}
-// Steps of all units of a sequence, by the whole warp.
-__device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int U, const PagedArgs &a) {
-    const int np = paged_units(s, U);
-    long long sum = 0;
-    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s, p, U, a);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-}
-
-template <int D, bool kBF16, bool kNarrow>
+template <int D, bool kBF16>
 __global__ void __launch_bounds__(384, 1)
 fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
                     const int R, const int q_min) {
-    using C = PagedCfg<D, kBF16, kNarrow>;
+    using C = PagedCfg<D, kBF16>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -167,69 +114,24 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(C::B_SFULL + x), 1);
-            mbar_init(bar(C::B_PFULL + x), C::LIVE);
+            mbar_init(bar(C::B_PFULL + x), 4);
             mbar_init(bar(C::B_OFULL + x), 1);
-            mbar_init(bar(C::B_OEMPTY + x), C::LIVE);
+            mbar_init(bar(C::B_OEMPTY + x), 4);
         }
-        mbar_init(bar(C::B_XFULL), C::LIVE);
-        mbar_init(bar(C::B_XEMPTY), C::LIVE);
+        mbar_init(bar(C::B_XFULL), 4);
+        mbar_init(bar(C::B_XEMPTY), 4);
         mbar_init(bar(C::B_MMADONE), 1);
         for (int q = 0; q < C::RING; ++q) {
             mbar_init(bar(C::B_PIECE + q), 1);
-            mbar_init(bar(C::B_FREE + q), 3 + 2 * C::LIVE);   // producers, MMA, softmax warps
+            mbar_init(bar(C::B_FREE + q), 11);              // producers, MMA, softmax warps
         }
         fence_barrier_init();
     }
-    const int U = kNarrow ? R : 2 * R;                     // positions of a unit
-    // Scan: thread i owns sequences [i k, (i + 1) k).  Scratch lies in the
-    // K/V ring, which no copy uses yet.
-    long long *scan = reinterpret_cast<long long *>(gbase + C::KV_OFF);   // [12], then the start
-    const int k = (a.B + C::NTHREADS - 1) / C::NTHREADS;
-    long long mine = 0;
-    for (int i = 0; i < k; ++i) {
-        const int b = tid * k + i;
-        PagedSeq s{0, 0, 0, false};
-        if (b < a.B) s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-        if (s.bad && blockIdx.x == 0) report_bad_index(a.status, 1);
-        const int np = paged_units(s, U);
-        if (np <= 2)
-            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s, p, U, a);
-        for (unsigned big = __ballot_sync(0xffffffffu, np > 2); big != 0; big &= big - 1) {
-            const int src = __ffs(big) - 1;
-            PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
-            const long long sum = paged_seq_steps_warp(t, U, a);
-            if (lane == src) mine += sum;
-        }
-    }
-    mine *= a.H_kv;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < 12; ++w) {
-        const long long v = scan[w];
-        before += w < warp ? v : 0;
-        total += v;
-    }
-    const long long G = gridDim.x, c = blockIdx.x;
-    const long long quota = max((total + G - 1) / G, static_cast<long long>(q_min));
-    const long long w0 = c * quota, w1 = min(total, w0 + quota);
-    if (w0 < w1 && before + incl - mine <= w0 && w0 < before + incl) {
-        scan[12] = before + incl - mine;
-        scan[13] = static_cast<long long>(tid) * k;
-    }
-    fence_proxy_async_smem();                              // the scratch is overwritten by TMA
+    // (the scratch lies in the K/V ring, which no copy uses yet)
     tc_fence_before();
-    __syncthreads();
+    const PagedShare share = paged_share<C::NTHREADS>(a, 2 * R, q_min, gbase + C::KV_OFF);
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const long long scan_w = scan[12], scan_b = scan[13];
-    __syncthreads();                                       // the scratch is free again
 
     // Reads piece number i (every role keeps its own count), whole warp; the
     // caller releases it.
@@ -250,7 +152,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         uint32_t np_out = 0;
         auto post = [&](const PagedPiece &p) __attribute__((always_inline)) -> bool {
             const uint32_t q = np_out % C::RING;
-            if (!__all_sync(0xffffffffu, mbar_wait_idle(bar(C::B_FREE + q), ((np_out / C::RING) & 1u) ^ 1u, w, 30)))
+            if (!mbar_wait_idle(bar(C::B_FREE + q), ((np_out / C::RING) & 1u) ^ 1u, w, 30))
                 return false;
             if (lane == 0) {
                 ring[q] = p;
@@ -260,181 +162,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             ++np_out;
             return true;
         };
-        int *desc = wk.desc + 8 * blockIdx.x;
-        if (lane == 0) desc[0] = 0;
-        bool ok = true;
-        if (w0 < w1) {
-            int b = static_cast<int>(scan_b);
-            long long at = scan_w, per = 0;                // steps before sequence b; of one K/V head
-            PagedSeq s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-            for (;;) {
-                per = paged_seq_steps_warp(s, U, a);
-                if (w0 < at + per * a.H_kv || b + 1 >= a.B) break;
-                at += per * a.H_kv;
-                s = paged_seq(a.cu_q, a.kv_len, ++b, a.T, a.W, a.ps_log2);
-            }
-            int h = static_cast<int>((w0 - at) / per);
-            long long rem = (w0 - at) - h * per;           // steps into this head's units
-            int np = paged_units(s, U), p = 0;
-            for (int p0 = 0; p0 < np; p0 += 32) {
-                const long long mine_t = p0 + lane < np ? paged_unit_steps(s, p0 + lane, U, a) : 0;
-                long long inc = mine_t;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += v;
-                }
-                const unsigned past = __ballot_sync(0xffffffffu, inc > rem);
-                if (past != 0) {
-                    const int l = __ffs(past) - 1;
-                    p = p0 + l;
-                    rem -= __shfl_sync(0xffffffffu, inc - mine_t, l);
-                    break;
-                }
-                rem -= __shfl_sync(0xffffffffu, inc, 31);
-            }
-            int t0 = static_cast<int>(rem);
-            for (long long at_w = w0; ok && at_w < w1;) {
-                PagedPiece pc;
-                const int i0 = p * U, left = s.m - i0;
-                pc.qrow = s.q0 + i0;
-                pc.nl = min(left, R);
-                pc.nh = kNarrow ? 0 : min(max(left - R, 0), R);
-                pc.pos = s.n - s.m + i0;
-                pc.n = s.n;
-                pc.b = b;
-                pc.h = h;
-                const int last = pc.pos + pc.nl + pc.nh - 1;
-                const PagedTiles tl = paged_tiles(pc.pos, last, s.n, a);
-                pc.hi = tl.hi;
-                pc.nw = tl.nw;
-                pc.T = tl.T;
-                pc.vlo = paged_lo(pc.pos, a.wl);
-                pc.vhi = paged_hi(last, s.n, a.wr);
-                const int khl = paged_hi(pc.pos + pc.nl - 1, s.n, a.wr);
-                pc.skip = min(tl.T - 1, max(0, min(tl.nw, tl.hi - ((khl >> 7) + ((khl & 127) != 0)))));
-                pc.t0 = t0;
-                pc.t1 = static_cast<int>(min(static_cast<long long>(tl.T), t0 + (w1 - at_w)));
-                const bool cont = pc.t1 < tl.T;
-                pc.slot = t0 > 0 ? 2 * static_cast<int>(c) : cont ? 2 * static_cast<int>(c) + 1 : -1;
-                if (t0 == 0 && cont && lane == 0) {        // a cut unit that starts here
-                    desc[1] = pc.qrow;
-                    desc[2] = pc.nl;
-                    desc[3] = pc.nh;
-                    desc[4] = h;
-                    desc[0] = static_cast<int>((at_w + tl.T - 1) / quota - c + 1);   // its parts
-                }
-                ok = post(pc);
-                at_w += pc.t1 - t0;
-                t0 = 0;
-                if (++p == np) {
-                    p = 0;
-                    if (++h == a.H_kv) {
-                        h = 0;
-                        do {
-                            if (++b >= a.B) break;
-                            s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-                            np = paged_units(s, U);
-                        } while (np == 0);
-                        if (b >= a.B) break;
-                    }
-                }
-            }
-        }
-        if (ok) {
+        if (paged_walk<true>(share, a, R, wk.desc + 8 * blockIdx.x, post)) {
             PagedPiece end{};
             end.qrow = -1;
             post(end);
         }
       } else if (warp != 9) {
         // =================== TMA producers (whole warps) ===================
-        // Warp 8 loads Q and K, warp 11 V, each into its half of the ring (K
-        // tiles in the even slots).  The lanes of a warp issue their boxes one
-        // after the other, ~55 cycles each: with 16-token pages a K/V tile pair
-        // is 64 of them, which one warp could not issue in the time that HBM
-        // takes for the pair.
-        WaitCtx w{abort_flag, a.status, kRoleProducer};
-        const bool is_v = warp == 11;
-        const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
-        if (lane == 0) {
-            if (!is_v) tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(tm);
-        }
-        uint32_t qc = 0, pi = 0, slot = is_v, ph = 0;      // Q tiles, pieces; ring slot and its phase
-        uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
-        bool ok = true;
-        const PagedBox<C::NCH> bx(a.ps_log2);
-        const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
-        // The page ids of a step are read PF steps ahead, and a piece's first
-        // ones while the piece before it still loads: an id comes from L2 or
-        // HBM, and a step may not wait for that.
-        constexpr int PF = 4;
-        auto page_of = [&](const PagedPiece &p, int t) __attribute__((always_inline)) -> int {
-            if (t >= p.t1) return a.n_pages;
-            const int j = paged_tile(p, t);
-            return bx.needs(j, p.vlo, p.vhi, min(a.first, p.vhi))
-                       ? a.table[static_cast<long long>(p.b) * a.W + ((j * 128 + bx.row) >> a.ps_log2)]
-                       : a.n_pages;
-        };
-        PagedPiece p, nx;
-        int page[PF], page_n[PF];
-        bool more = take(pi++, w, 31, p), more_n = false;
-#pragma unroll
-        for (int u = 0; u < PF; ++u) page[u] = more ? page_of(p, p.t0 + u) : 0;
-        while (ok && more) {
-            for (int x = is_v ? 2 : 0; x < (p.nh > 0 ? 2 : 1) && ok; ++x) {
-                const uint32_t qs = qc % C::NQ, qph = (qc / C::NQ) & 1u;
-                ok = mbar_wait_warp(bar(C::B_QEMPTY + qs), qph ^ 1u, w, 1);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QFULL + qs), q_bytes);
-                __syncwarp();
-                if (lane < C::NCH)
-                    tma_load_4d(&tm_q, base + C::Q_OFF + qs * C::Q_BYTES + lane * C::Q_CHUNK,
-                                bar(C::B_QFULL + qs), lane * 64, p.h * a.group, p.qrow + x * R, 0);
-                qarmed |= 1u << qs;
-                qarmed_par = (qarmed_par & ~(1u << qs)) | (qph << qs);
-                ++qc;
-            }
-#pragma unroll 1
-            for (int t = p.t0; t < p.t1 && ok; ++t) {
-                const int j = paged_tile(p, t);
-                int pg = page[0];
-#pragma unroll
-                for (int u = 0; u + 1 < PF; ++u) page[u] = page[u + 1];
-                page[PF - 1] = page_of(p, t + PF);
-                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
-                    if (bx.needs(j, p.vlo, p.vhi, min(a.first, p.vhi))) report_bad_index(a.status, 2);
-                    pg = a.n_pages;                        // beyond the pool: zeros
-                }
-                const int row0 = (j * 128 + bx.row) & ((1 << a.ps_log2) - 1);
-                ok = mbar_wait_warp(bar(C::B_KVEMPTY + slot), ph ^ 1u, w, 2);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
-                __syncwarp();
-                if (lane < bx.n_box)
-                    tma_load_4d(tm, base + C::KV_OFF + slot * C::TILE_BYTES + bx.c * C::CHUNK_BYTES + bx.row * 128u,
-                                bar(C::B_KVFULL + slot), bx.c * 64, p.h, row0, pg);
-                armed |= 1u << slot;
-                armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
-                slot += 2;
-                if (slot >= C::NSTAGE) { slot = is_v; ph ^= 1u; }
-                if (t == p.t0 && ok) {
-                    more_n = take(pi++, w, 31, nx);
-#pragma unroll
-                    for (int u = 0; u < PF; ++u) page_n[u] = more_n ? page_of(nx, nx.t0 + u) : 0;
-                }
-            }
-            p = nx;
-            more = more_n;
-#pragma unroll
-            for (int u = 0; u < PF; ++u) page[u] = page_n[u];
-        }
-        // Every issued copy lands before the CTA may end (bounded).
-        for (int s = 0; s < C::NSTAGE; ++s)
-            if (armed & (1u << s)) mbar_wait_quiet(bar(C::B_KVFULL + s), (armed_par >> s) & 1u, 500000000ull);
-        for (int q = 0; q < C::NQ; ++q)
-            if (qarmed & (1u << q)) mbar_wait_quiet(bar(C::B_QFULL + q), (qarmed_par >> q) & 1u, 500000000ull);
-        __syncwarp();
+        paged_produce<C>(warp == 11, tm_q, tm_k, tm_v, a, R, base, take,
+                         WaitCtx{abort_flag, a.status, kRoleProducer});
       } else if (warp == 9) {
         // =================== MMA issuer (whole warp, one elected lane issues) ===================
         // Step i multiplies Q with its K tile, and P of step i - lag with that
@@ -451,7 +187,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         while (ok && take(pi, w, 32, p)) {
             ++pi;
             const int ns = uniform(p.t1 - p.t0);
-            const bool one = kNarrow || uniform(p.nh) == 0;
+            const bool one = uniform(p.nh) == 0;
             const int lag = one ? 2 : 1;
             const int s0l = one ? 0 : uniform(max(p.t0, p.skip) - p.t0);       // tile L's first step
             uint32_t q1 = qs + 1, q1ph = qph;              // tile H's slot
@@ -490,13 +226,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         if (ok && i == s0) ok = mbar_wait_warp(bar(C::B_QFULL + qx), qxp, w, 14);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qx * C::Q_BYTES, 16u, 1024u);
+                        const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qx * C::TILE_BYTES, 16u, 1024u);
                         const uint64_t kd = smem_desc_sw128(base + C::KV_OFF + ks * C::TILE_BYTES, 16u, 1024u);
 #pragma unroll
                         for (int kk = 0; kk < C::QK_STEPS; ++kk) {
-                            const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
-                            const uint32_t ko = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
-                            mma_ss_f16_elect(d_s, qd + qo, kd + ko, C::IDESC_QK, kk > 0 ? 1u : 0u);
+                            const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                            mma_ss_f16_elect(d_s, qd + off, kd + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
                         }
                         mma_commit_elect(bar(C::B_SFULL + x));
                     }
@@ -527,7 +262,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
         __syncwarp();
       }
-    } else if (regs_grow<C::REGS_HIGH>(); (warp & 3) < C::LIVE) {
+    } else {
+        regs_grow<C::REGS_HIGH>();
         // =================== softmax group x ===================
         const int x = warp >> 2;
         const int row = tid & 127;
@@ -546,7 +282,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         PagedPiece p;
         while (ok && take(pi, w, 24, p)) {
             ++pi;
-            const bool one = kNarrow || p.nh == 0;
+            const bool one = p.nh == 0;
             const int ns = p.t1 - p.t0;
             const int tile = one ? 0 : x;                  // the Q tile this group works on
             const int npos = tile ? p.nh : p.nl;
@@ -571,11 +307,9 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const uint32_t idx = kv + 2 * i + 1, slot = idx % C::NSTAGE;
                     ok = mbar_wait(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 22);
                     if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
-#pragma unroll 1
-                    for (int vrow = row; vrow < 128; vrow += 32 * C::LIVE) {
-                        const int kk = k0 + vrow;
-                        if ((kk >= p.vlo && kk < p.vhi) || kk < nf) continue;
-                        uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + vrow * 128;
+                    const int kk = k0 + row;
+                    if (!((kk >= p.vlo && kk < p.vhi) || kk < nf)) {
+                        uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + row * 128;
 #pragma unroll
                         for (int ch = 0; ch < C::NCH; ++ch)
 #pragma unroll
@@ -814,124 +548,6 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         tmem_dealloc(tbase, C::TMEM_COLS);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Joins the parts of the units that the shares' borders cut: LSE = log sum_s
-// exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s.  CTA (c, y) works on the cut unit
-// that starts in share c; its part 0 is slot 2 c + 1, part s > 0 slot 2 (c + s).
-// A part with LSE = -inf saw nothing and its O may be unwritten: it is not
-// read.  Up to eight parts (a chunk's unit has two or three): one warp a row,
-// all loads of the row at once.  More (single tokens against a long cache, a
-// part for every SM): the CTA takes a row, each warp every eighth part, and
-// the warps' sums are added in order.
-template <int D, bool kBF16>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedArgs a, const PagedWork wk, const int R) {
-    constexpr int E = D / 32;
-    __shared__ float s_acc[8][D];
-    __shared__ float s_l[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 *d4 = reinterpret_cast<const int4 *>(wk.desc + 8 * c);
-    const int4 d0 = d4[0], d1 = d4[1];
-    const int parts = d0.x, qrow = d0.y, nl = d0.z, nh = d0.w, h = d1.x;
-    if (parts == 0) return;
-    const int rows = (nl + nh) * a.group;
-    auto slot = [&](int s, int tile, int row) __attribute__((always_inline)) -> size_t {
-        return (static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * 2 + tile) * 128 + row;
-    };
-    auto write = [&](int tile, int row, const float (&acc)[E], float M, float L) __attribute__((always_inline)) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        const int tok = qrow + tile * R + row / a.group, qh = h * a.group + row % a.group;
-        uint32_t pk[E / 2];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) pk[e / 2] = pack2<kBF16>(acc[e] * inv, acc[e + 1] * inv);
-        uint16_t *dst = reinterpret_cast<uint16_t *>(a.o) + (static_cast<size_t>(tok) * a.H + qh) * D + lane * E;
-        if constexpr (E == 2) *reinterpret_cast<uint32_t *>(dst) = pk[0];
-        else *reinterpret_cast<uint2 *>(dst) = make_uint2(pk[0], pk[1]);
-        if (a.lse != nullptr && lane == 0)
-            a.lse[static_cast<size_t>(qh) * a.T + tok] =
-                L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
-    };
-    auto load = [&](size_t part, float (&v)[E]) __attribute__((always_inline)) {
-        const float *src = wk.o + part * D + lane * E;
-        if constexpr (E == 2) {
-            const float2 t = *reinterpret_cast<const float2 *>(src);
-            v[0] = t.x; v[1] = t.y;
-        } else {
-            const float4 t = *reinterpret_cast<const float4 *>(src);
-            v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-        }
-    };
-    if (parts <= 8) {
-        for (int rr = blockIdx.y * 8 + warp; rr < rows; rr += gridDim.y * 8) {
-            const int tile = rr >= nl * a.group ? 1 : 0, row = tile ? rr - nl * a.group : rr;
-            float z[8], v[8][E], acc[E];
-#pragma unroll
-            for (int s = 0; s < 8; ++s) z[s] = s < parts ? wk.lse[slot(s, tile, row)] : -INFINITY;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                if (s < parts) load(slot(s, tile, row), v[s]);
-            float M = z[0], L = 0.f;
-#pragma unroll
-            for (int s = 1; s < 8; ++s) M = fmaxf(M, z[s]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                if (z[s] == -INFINITY) continue;
-                const float wt = ex2_approx(z[s] - M);
-                L += wt;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[s][e], acc[e]);
-            }
-            write(tile, row, acc, M, L);
-        }
-        return;
-    }
-    for (int rr = blockIdx.y; rr < rows; rr += gridDim.y) {
-        const int tile = rr >= nl * a.group ? 1 : 0, row = tile ? rr - nl * a.group : rr;
-        float M = -INFINITY;
-        for (int s = lane; s < parts; s += 32) M = fmaxf(M, wk.lse[slot(s, tile, row)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float l = 0.f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        for (int s0 = warp; s0 < parts; s0 += 32) {
-            float z[4], v[4][E];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int s = s0 + 8 * u;
-                z[u] = s < parts ? wk.lse[slot(s, tile, row)] : -INFINITY;
-                if (s < parts) load(slot(s, tile, row), v[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (z[u] == -INFINITY) continue;
-                const float wt = ex2_approx(z[u] - M);
-                l += wt;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[u][e], acc[e]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-        if (lane == 0) s_l[warp] = l;
-        __syncthreads();
-        if (warp == 0) {
-            float L = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                L += s_l[q];
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += s_acc[q][lane * E + e];
-            }
-            write(tile, row, acc, M, L);
-        }
-        __syncthreads();
-    }
 }
 
 }  // namespace fa

@@ -2,14 +2,21 @@
 // kernel that joins its parts.
 #pragma once
 
+#include <type_traits>
+
+#include "fa_paged_combine.cuh"
 #include "fa_paged_fwd_kernel.cuh"
+#include "fa_paged_token_kernel.cuh"
 
 namespace fa {
 
-template <int D, bool kBF16, bool kNarrow>
+// kN: the kernel for few rows, with products of kN columns; 0: the one for chunks.
+template <int D, bool kBF16, int kN>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
-    using C = PagedCfg<D, kBF16, kNarrow>;
-    auto kern = fa_paged_fwd_kernel<D, kBF16, kNarrow>;
+    using C = std::conditional_t<kN != 0, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
+    void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedArgs, PagedWork, int, int);
+    if constexpr (kN != 0) kern = fa_paged_token_kernel<D, kBF16, kN>;
+    else kern = fa_paged_fwd_kernel<D, kBF16>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -26,7 +33,7 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     if (e != cudaSuccess || L.grid == 1) return e;  // one share: nothing is cut
     // The joining kernel's CTAs are brought up while the attention's last ones
     // run; it waits for their results itself (griddepcontrol.wait).
-    const int rows = 2 * L.R * L.a.group;
+    const int rows = (kN ? 1 : 2) * L.R * L.a.group;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.grid, rows < 16 ? rows : 16);
     cfg.blockDim = dim3(256);
@@ -39,11 +46,15 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16>, L.a, L.w, L.R);
 }
 
+// Up to 32 rows a tile: few rows against each K/V tile, bound by HBM.
 template <int D>
 cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
-    if (L.R * L.a.group <= 32)
-        return L.bf16 ? launch_fwd_paged_inst<D, true, true>(L) : launch_fwd_paged_inst<D, false, true>(L);
-    return L.bf16 ? launch_fwd_paged_inst<D, true, false>(L) : launch_fwd_paged_inst<D, false, false>(L);
+    const int rows = L.R * L.a.group;
+    if (rows <= 16)
+        return L.bf16 ? launch_fwd_paged_inst<D, true, 16>(L) : launch_fwd_paged_inst<D, false, 16>(L);
+    if (rows <= 32)
+        return L.bf16 ? launch_fwd_paged_inst<D, true, 32>(L) : launch_fwd_paged_inst<D, false, 32>(L);
+    return L.bf16 ? launch_fwd_paged_inst<D, true, 0>(L) : launch_fwd_paged_inst<D, false, 0>(L);
 }
 
 }  // namespace fa
