@@ -10,7 +10,7 @@
 
 namespace fa {
 
-// kN: the kernel for few rows, with products of kN columns; 0: the one for chunks.
+// kN: the kernel for few rows, up to kN of them; 0: the one for chunks.
 template <int D, bool kBF16, int kN>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     using C = std::conditional_t<kN != 0, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
@@ -50,8 +50,8 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
 template <int D>
 cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
     const int rows = L.R * L.a.group;
-    if (rows <= 16)
-        return L.bf16 ? launch_fwd_paged_inst<D, true, 16>(L) : launch_fwd_paged_inst<D, false, 16>(L);
+    if (rows <= 8)
+        return L.bf16 ? launch_fwd_paged_inst<D, true, 8>(L) : launch_fwd_paged_inst<D, false, 8>(L);
     if (rows <= 32)
         return L.bf16 ? launch_fwd_paged_inst<D, true, 32>(L) : launch_fwd_paged_inst<D, false, 32>(L);
     return L.bf16 ? launch_fwd_paged_inst<D, true, 0>(L) : launch_fwd_paged_inst<D, false, 0>(L);

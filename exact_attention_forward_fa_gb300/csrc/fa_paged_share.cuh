@@ -39,20 +39,21 @@ __device__ __forceinline__ int paged_tile(const PagedPiece &p, int t) {
 
 // Key tiles that rows at positions pa .. pb (of n cached tokens) see.
 struct PagedTiles { int hi, nw, T; };
-__device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, const PagedArgs &a) {
-    const int khi = paged_hi(pb, n, a.wr);
+__device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, int wl, int wr, int first) {
+    const int khi = paged_hi(pb, n, wr);
     PagedTiles t;
     t.hi = (khi >> 7) + ((khi & 127) != 0);
-    const int lo = min(paged_lo(pa, a.wl) >> 7, t.hi);
-    const int f = min(a.first, khi);
+    const int lo = min(paged_lo(pa, wl) >> 7, t.hi);
+    const int f = min(first, khi);
     t.nw = t.hi - lo;
     t.T = max(1, t.nw + min((f >> 7) + ((f & 127) != 0), lo));   // an empty unit still writes O = 0
     return t;
 }
-// Steps of unit p of a sequence (U positions a unit).
-__device__ __forceinline__ int paged_unit_steps(const PagedSeq &s, int p, int U, const PagedArgs &a) {
+// Steps of unit p of a sequence (U positions a unit).  Not inlined: the code
+// before a CTA's first load comes from L2, line by line.
+static __device__ __noinline__ int paged_unit_steps(int m, int n, int p, int U, int wl, int wr, int first) {
     const int i0 = p * U;
-    return paged_tiles(s.n - s.m + i0, s.n - s.m + min(s.m, i0 + U) - 1, s.n, a).T;
+    return paged_tiles(n - m + i0, n - m + min(m, i0 + U) - 1, n, wl, wr, first).T;
 }
 __device__ __forceinline__ int paged_units(const PagedSeq &s, int U) {
     return static_cast<int>((static_cast<long long>(s.m) + U - 1) / U);
@@ -61,7 +62,7 @@ __device__ __forceinline__ int paged_units(const PagedSeq &s, int U) {
 __device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int U, const PagedArgs &a) {
     const int np = paged_units(s, U);
     long long sum = 0;
-    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s, p, U, a);
+    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s.m, s.n, p, U, a.wl, a.wr, a.first);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
@@ -96,9 +97,8 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, int
         if (b < a.B) s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
         if (s.bad && blockIdx.x == 0) report_bad_index(a.status, 1);
         const int np = paged_units(s, U);
-        if (np <= 2)
-            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s, p, U, a);
-        for (unsigned big = __ballot_sync(0xffffffffu, np > 2); big != 0; big &= big - 1) {
+        if (np == 1) mine += paged_unit_steps(s.m, s.n, 0, U, a.wl, a.wr, a.first);
+        for (unsigned big = __ballot_sync(0xffffffffu, np > 1); big != 0; big &= big - 1) {
             const int src = __ffs(big) - 1;
             PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
             const long long sum = paged_seq_steps_warp(t, U, a);
@@ -175,7 +175,7 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
         }
         int np = paged_units(s, U), p = 0;
         for (int p0 = 0; p0 < np; p0 += 32) {
-            const long long mine_t = p0 + lane < np ? paged_unit_steps(s, p0 + lane, U, a) : 0;
+            const long long mine_t = p0 + lane < np ? paged_unit_steps(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
             long long inc = mine_t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -203,7 +203,7 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
             pc.b = b;
             pc.h = h;
             const int last = pc.pos + pc.nl + pc.nh - 1;
-            const PagedTiles tl = paged_tiles(pc.pos, last, s.n, a);
+            const PagedTiles tl = paged_tiles(pc.pos, last, s.n, a.wl, a.wr, a.first);
             pc.hi = tl.hi;
             pc.nw = tl.nw;
             pc.T = tl.T;

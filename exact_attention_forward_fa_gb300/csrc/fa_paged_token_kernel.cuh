@@ -48,13 +48,14 @@ struct TokenCfg {
     static constexpr bool kByStep = true;
     static constexpr int NQ = 2;
     static constexpr int NTHREADS = 416;
-    static constexpr int RING = 4;
+    static constexpr int RING = 2;
     static constexpr uint32_t KV_OFF = 0;
     static constexpr uint32_t Q_OFF = NSTAGE * TILE_BYTES;
     static constexpr uint32_t P_OFF = Q_OFF + NQ * Q_BYTES;
     static constexpr uint32_t R_OFF = P_OFF + 2 * P_BYTES;            // [2 groups][32] references
-    static constexpr uint32_t X_OFF = R_OFF + 2 * 32 * 4;             // group 1's LSE and 1 / l, [2][32]
-    static constexpr uint32_t RING_OFF = X_OFF + 2 * 32 * 4;
+    static constexpr uint32_t X_OFF = R_OFF + 2 * 32 * 4;             // group 1's LSE and 1 / l, the factors: [4][32]
+    static constexpr uint32_t RED_OFF = X_OFF + 4 * 32 * 4;           // sums of 8 rows: [2 groups][2][4 warps][8]
+    static constexpr uint32_t RING_OFF = RED_OFF + 2 * 64 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 64;
     static constexpr int B_QFULL = 0, B_QEMPTY = NQ, B_KVFULL = 2 * NQ, B_KVEMPTY = B_KVFULL + NSTAGE,
                          B_SFULL = B_KVEMPTY + NSTAGE, B_SEMPTY = B_SFULL + 4, B_PFULL = B_SEMPTY + 4,
@@ -71,16 +72,24 @@ struct TokenCfg {
     static constexpr float CAP = 15.0f;                   // and has to when a P would pass 2^15
 };
 
+// TMEM: eight 32-bit columns of the warp's lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Adds (or takes the maximum of) v[n] over the 32 lanes of a warp, for every n:
-// lane l gets that of v[l % kN].  31 exchanges instead of 5 for each n.
+// lane l gets that of v[l % kN].  31 exchanges for 32 values instead of 160.
 template <int kN, bool kMax = false>
 __device__ __forceinline__ float warp_reduce_transposed(float (&v)[kN]) {
     const int lane = threadIdx.x & 31;
     auto both = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
-    if constexpr (kN == 16) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = both(v[i], __shfl_xor_sync(0xffffffffu, v[i], 16));
-    }
 #pragma unroll
     for (int w = kN / 2; w > 0; w >>= 1) {
         const bool up = (lane & w) != 0;
@@ -91,6 +100,8 @@ __device__ __forceinline__ float warp_reduce_transposed(float (&v)[kN]) {
             v[i] = both(mine, __shfl_xor_sync(0xffffffffu, send, w));
         }
     }
+#pragma unroll
+    for (int w = kN; w < 32; w <<= 1) v[0] = both(v[0], __shfl_xor_sync(0xffffffffu, v[0], w));
     return v[0];
 }
 
@@ -103,7 +114,10 @@ __device__ __forceinline__ bool group_any(int x, bool v) {
     return r != 0;
 }
 
-// kN: columns of the products, 16 or 32.
+// kN: rows that the groups work on, 8 or 32 (the products have 16 or 32
+// columns).  One token of up to 8 heads a group is the common call, and the
+// code of a piece's beginning and end, which runs once a piece and by then has
+// left the instruction cache, is a quarter as long for 8 rows.
 template <int D, bool kBF16, int kN>
 __global__ void __launch_bounds__(416, 1)
 fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -194,8 +208,8 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // a step ahead of O^T += V^T P^T.
         WaitCtx w{abort_flag, a.status, kRoleMma};
         const int x = __shfl_sync(0xffffffffu, warp - 10, 0);
-        constexpr uint32_t idesc_s = idesc_f16(128, kN, kBF16, false, false);
-        constexpr uint32_t idesc_o = idesc_f16(128, kN, kBF16, true, false);
+        constexpr uint32_t idesc_s = idesc_f16(128, kN < 16 ? 16 : kN, kBF16, false, false);
+        constexpr uint32_t idesc_o = idesc_f16(128, kN < 16 ? 16 : kN, kBF16, true, false);
         uint32_t kc = 0, vc = 1;                           // this group's next K and V tile, counted together
         uint32_t pc = 0, sc = 0, un = 0, pp = 0;           // pieces, S tiles, accumulators, P tiles so far
         bool ok = true;
@@ -323,7 +337,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 tc_fence_after();
                 uint32_t s[kN];
                 const uint32_t tS = tbase + lane_off + C::col_s(0, 0) + 64u * x + 32u * buf;
-                if constexpr (kN == 16) tmem_ld16(tS, s);
+                if constexpr (kN == 8) tmem_ld8(tS, s);
                 else tmem_ld32(tS, s);
                 tmem_ld_wait();
                 tc_fence_before();
@@ -364,7 +378,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll
                     for (int n = 0; n < kN; ++n) m[n] = n < nr ? __uint_as_float(s[n]) : -INFINITY;
                     const float top = warp_reduce_transposed<kN, true>(m);
-                    scratch[gwarp * 32 + lane] = top;
+                    if (lane < kN) scratch[gwarp * kN + lane] = top;
                     group_any(x, false);
                     bad = bad || scratch[128] + scratch[129] + scratch[130] + scratch[131] != 0.f;
                     bool moved = false;
@@ -375,7 +389,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         if (n >= nr) continue;
                         const bool first_seen = (unseen & (1u << n)) != 0;
                         const float o = first_seen ? 0.f : ref[n];
-                        const float mx = fmaxf(fmaxf(scratch[n], scratch[32 + n]), fmaxf(scratch[64 + n], scratch[96 + n])) + o;
+                        const float mx = fmaxf(fmaxf(scratch[n], scratch[kN + n]), fmaxf(scratch[2 * kN + n], scratch[3 * kN + n])) + o;
                         float rn = o, corr = 1.f;
                         if (first_seen) {
                             if (mx != -INFINITY) { rn = mx; unseen &= ~(1u << n); }
@@ -395,12 +409,12 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         const uint32_t tO = tbase + lane_off + C::col_o(0) + 32u * x;
                         uint32_t ov[kN];
                         tc_fence_after();
-                        if constexpr (kN == 16) tmem_ld16(tO, ov);
+                        if constexpr (kN == 8) tmem_ld8(tO, ov);
                         else tmem_ld32(tO, ov);
                         tmem_ld_wait();
 #pragma unroll
                         for (int n = 0; n < kN; ++n) ov[n] = __float_as_uint(__uint_as_float(ov[n]) * m[n]);
-                        if constexpr (kN == 16) tmem_st16(tO, ov);
+                        if constexpr (kN == 8) tmem_st8(tO, ov);
                         else tmem_st32(tO, ov);
                         tmem_st_wait();
                         tc_fence_before();
@@ -433,44 +447,46 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
             const bool some = x < ns, joined = ns >= 2;
             // ---- row n's sums over all keys of the group, in thread n ----
-            if (some && !bad) bad = !mbar_wait_warp(bar(C::B_OFULL + x), (x ? un1 : un0) & 1u, w, 21);
+            if (kN == 32 && some && !bad) bad = !mbar_wait_warp(bar(C::B_OFULL + x), (x ? un1 : un0) & 1u, w, 21);
+            const float le_w = warp_reduce_transposed<kN>(le), lr_w = warp_reduce_transposed<kN>(lr);
+            if (kN == 32 && group_any(x, bad)) break;     // the sums of 32 rows go through P's buffer
+            float *sums = kN == 32 ? scratch : reinterpret_cast<float *>(gbase + C::RED_OFF) + 64 * x;
+            if (lane < kN) {
+                sums[gwarp * kN + lane] = le_w;
+                sums[(4 + gwarp) * kN + lane] = lr_w;
+            }
             if (group_any(x, bad)) break;
-            float lse2 = -INFINITY, inv = 0.f;                               // of row n = row (threads < 32)
-            if (some) {
-                scratch[gwarp * 32 + lane] = warp_reduce_transposed<kN>(le);
-                scratch[128 + gwarp * 32 + lane] = warp_reduce_transposed<kN>(lr);
-                group_any(x, false);
-                if (row < nr) {
-                    const float e = (scratch[row] + scratch[32 + row]) + (scratch[64 + row] + scratch[96 + row]);
-                    const float q = (scratch[128 + row] + scratch[160 + row]) + (scratch[192 + row] + scratch[224 + row]);
-                    if (e > 0.f && q > 0.f) {
-                        lse2 = ref[row] + log2f(e);
-                        inv = 1.f / q;
-                    }
+            float lse2 = -INFINITY, inv = 0.f;                               // of row n = lane (warp 0)
+            if (gwarp == 0 && some && lane < nr) {
+                const float e = (sums[lane] + sums[kN + lane]) + (sums[2 * kN + lane] + sums[3 * kN + lane]);
+                const float q = (sums[4 * kN + lane] + sums[5 * kN + lane]) + (sums[6 * kN + lane] + sums[7 * kN + lane]);
+                if (e > 0.f && q > 0.f) {
+                    lse2 = ref[lane] + log2f(e);
+                    inv = 1.f / q;
                 }
             }
             if (x == 1) {
-                ++un0;
-                if (!joined) continue;
-                ++un1;
-                if (gwarp == 0) {
-                    bad = !mbar_wait_warp(bar(C::B_XEMPTY), (nx & 1u) ^ 1u, w, 25);
-                    xch[lane] = lse2;
-                    xch[32 + lane] = inv;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_XFULL));
+                if (joined) {
+                    if (gwarp == 0) {
+                        bad = !mbar_wait_warp(bar(C::B_XEMPTY), (nx & 1u) ^ 1u, w, 25);
+                        xch[lane] = lse2;
+                        xch[32 + lane] = inv;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_XFULL));
+                    }
+                    if (kN == 8) bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 21) || bad;
+                    ++nx;
+                    ++un1;
                 }
-                ++nx;
+                ++un0;
                 continue;
             }
             // ---- group 0: join the halves, write the rows ----
-            if (joined) {
-                bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 27);
-                if (gwarp == 0) bad = !mbar_wait_warp(bar(C::B_XFULL), nx & 1u, w, 26) || bad;
-            }
+            float *fac = xch + 64;                                           // the rows' factors, [2][32]
             if (gwarp == 0) {
                 float inv1 = 0.f;
                 if (joined) {
+                    bad = !mbar_wait_warp(bar(C::B_XFULL), nx & 1u, w, 26);
                     const float l1 = xch[lane], m = fmaxf(lse2, l1);
                     inv1 = xch[32 + lane];
                     __syncwarp();
@@ -482,9 +498,8 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         lse2 = m + log2f(w0 + w1);
                     }
                 }
-                // (scratch [0, 256) may still be read: the factors go behind it)
-                scratch[256 + lane] = inv;
-                scratch[288 + lane] = inv1;
+                fac[lane] = inv;
+                fac[32 + lane] = inv1;
                 if (lane < nr) {
                     if (p.slot >= 0) {
                         wk.lse[static_cast<size_t>(p.slot) * 256 + lane] = lse2;
@@ -494,34 +509,35 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                 }
             }
+            if (kN == 8) bad = !mbar_wait_warp(bar(C::B_OFULL), un0 & 1u, w, 21) || bad;
+            if (joined) bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 27) || bad;
             if (group_any(0, bad)) break;
             tc_fence_after();
-            uint32_t o0[kN], o1[kN];
-            if constexpr (kN == 16) {
-                tmem_ld16(tbase + lane_off + C::col_o(0), o0);
-                tmem_ld16(tbase + lane_off + C::col_o(1), o1);
-            } else {
-                tmem_ld32(tbase + lane_off + C::col_o(0), o0);
-                tmem_ld32(tbase + lane_off + C::col_o(1), o1);
-            }
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(C::B_OEMPTY));
-                if (joined) mbar_arrive(bar(C::B_OEMPTY + 1));
-            }
-            ++un0;
-            if (joined) { ++un1; ++nx; }
-            if (row < D) {
-                int tok = p.qrow, hd = 0;
-                float *part = wk.o + static_cast<size_t>(max(p.slot, 0)) * 256 * D + row;
-                uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + static_cast<size_t>(p.h) * a.group * D + row;
+            const uint32_t tO = tbase + lane_off + C::col_o(0);
+            int tok = p.qrow, hd = 0;
+            float *part = wk.o + static_cast<size_t>(max(p.slot, 0)) * 256 * D + row;
+            uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + static_cast<size_t>(p.h) * a.group * D + row;
+#pragma unroll 1
+            for (int n8 = 0; n8 < nr; n8 += 8) {
+                uint32_t o0[8], o1[8];
+                tmem_ld8(tO + n8, o0);
+                tmem_ld8(tO + (C::col_o(1) - C::col_o(0)) + n8, o1);
+                tmem_ld_wait();
+                if (n8 + 8 >= nr) {                                          // the accumulators are read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(C::B_OEMPTY));
+                        if (joined) mbar_arrive(bar(C::B_OEMPTY + 1));
+                    }
+                }
+                if (row >= D) continue;                                      // (d = 64: lanes that hold nothing)
 #pragma unroll
-                for (int n = 0; n < kN; ++n) {
+                for (int q = 0; q < 8; ++q) {
+                    const int n = n8 + q;
                     if (n >= nr) continue;
-                    float v = __uint_as_float(o0[n]) * scratch[256 + n];
-                    if (joined) v = fmaf(__uint_as_float(o1[n]), scratch[288 + n], v);
+                    float v = __uint_as_float(o0[q]) * fac[n];
+                    if (joined) v = fmaf(__uint_as_float(o1[q]), fac[32 + n], v);
                     if (p.slot >= 0)
                         part[n * D] = v;
                     else
@@ -529,6 +545,8 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     if (++hd == a.group) { hd = 0; ++tok; }
                 }
             }
+            ++un0;
+            if (joined) { ++un1; ++nx; }
         }
     }
 
