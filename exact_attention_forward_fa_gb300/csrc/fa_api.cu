@@ -913,9 +913,10 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     if ((st = encode_packed_q(&L.q, dt, a, d, L.R)) != FA_OK) return st;
     if ((st = encode_pages(&L.k, k_pages, dt, a, d)) != FA_OK) return st;
     if ((st = encode_pages(&L.v, v_pages, dt, a, d)) != FA_OK) return st;
-    // CTAs: one per SM, fewer when even the longest cache has not q_min steps
-    // for each.
-    L.q_min = 2;
+    // CTAs: one per SM, fewer when even the longest cache has not a step for
+    // each (two steps a share made a short conversation's call 14.3 us instead of
+    // 11: a share then holds the end of one unit and the start of the next).
+    L.q_min = 1;
     const uint64_t units = static_cast<uint64_t>(B) + static_cast<uint64_t>(total_q) / (2 * L.R);
     const uint64_t tiles = ((static_cast<uint64_t>(table_width) << a.ps_log2) + 127) / 128;
     const uint64_t share = (units * tiles + L.q_min - 1) / L.q_min;     // shares of one K/V head

@@ -71,6 +71,11 @@ struct PagedCfg {
                          B_OEMPTY = B_OFULL + 2, B_XFULL = B_OEMPTY + 2, B_XEMPTY = B_XFULL + 1,
                          B_MMADONE = B_XEMPTY + 1, B_PIECE = B_MMADONE + 1, B_FREE = B_PIECE + RING,
                          NBAR = B_FREE + RING;
+    // Arrivals that complete a phase: a group's four warps; producers, MMA issuer
+    // and the groups' warps.
+    __device__ static uint32_t arrivals(int i) {
+        return i == B_PFULL || i == B_PFULL + 1 || (i >= B_OEMPTY && i < B_MMADONE) ? 4u : i >= B_FREE ? 11u : 1u;
+    }
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -102,30 +107,15 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
     // ---- prologue: TMEM (warp 9), barriers (thread 0), this CTA's share ----
     if (warp == 9) tmem_alloc(base + C::MISC_OFF, C::TMEM_COLS);
-    if (tid == 0) {
-        *abort_flag = 0u;
-        for (int q = 0; q < C::NQ; ++q) {
-            mbar_init(bar(C::B_QFULL + q), 1);
-            mbar_init(bar(C::B_QEMPTY + q), 1);
-        }
-        for (int s = 0; s < C::NSTAGE; ++s) {
-            mbar_init(bar(C::B_KVFULL + s), 1);
-            mbar_init(bar(C::B_KVEMPTY + s), 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(C::B_SFULL + x), 1);
-            mbar_init(bar(C::B_PFULL + x), 4);
-            mbar_init(bar(C::B_OFULL + x), 1);
-            mbar_init(bar(C::B_OEMPTY + x), 4);
-        }
-        mbar_init(bar(C::B_XFULL), 4);
-        mbar_init(bar(C::B_XEMPTY), 4);
-        mbar_init(bar(C::B_MMADONE), 1);
-        for (int q = 0; q < C::RING; ++q) {
-            mbar_init(bar(C::B_PIECE + q), 1);
-            mbar_init(bar(C::B_FREE + q), 11);              // producers, MMA, softmax warps
-        }
+    if (tid == 0) *abort_flag = 0u;
+    if (warp == 11) {
+        for (int i = lane; i < C::NBAR; i += 32) mbar_init(bar(i), C::arrivals(i));
         fence_barrier_init();
+    }
+    if (tid == 8 * 32) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
     // (the scratch lies in the K/V ring, which no copy uses yet)
     tc_fence_before();

@@ -174,7 +174,7 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
             rem -= h * per;
         }
         int np = paged_units(s, U), p = 0;
-        for (int p0 = 0; p0 < np; p0 += 32) {
+        for (int p0 = 0; np > 1 && p0 < np; p0 += 32) {
             const long long mine_t = p0 + lane < np ? paged_unit_steps(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
             long long inc = mine_t;
 #pragma unroll
@@ -260,11 +260,6 @@ __device__ __forceinline__ void paged_produce(const int wp, const CUtensorMap &t
                                               const uint32_t base, Take &&take, const WaitCtx w) {
     const int lane = threadIdx.x & 31;
     auto bar = [&](int i) -> uint32_t { return base + C::BAR_OFF + 8u * i; };
-    if (lane == 0) {
-        if (wp == 0) tma_prefetch_desc(&tm_q);
-        if (C::kByStep || wp == 0) tma_prefetch_desc(&tm_k);
-        if (C::kByStep || wp == 1) tma_prefetch_desc(&tm_v);
-    }
     constexpr int kStride = C::kByStep ? 2 : 1;        // between this warp's steps
     const uint32_t slot0 = C::kByStep ? wp * C::NRING : wp, slot1 = C::kByStep ? slot0 + C::NRING : C::NSTAGE;
     uint32_t qc = 0, pi = 0, slot = slot0, ph = 0;     // Q tiles, pieces; ring slot and its phase

@@ -62,6 +62,12 @@ struct TokenCfg {
                          B_PEMPTY = B_PFULL + 2, B_OFULL = B_PEMPTY + 2, B_OEMPTY = B_OFULL + 2,
                          B_XFULL = B_OEMPTY + 2, B_XEMPTY = B_XFULL + 1, B_DONE = B_XEMPTY + 1,
                          B_PIECE = B_DONE + 2, B_FREE = B_PIECE + RING, NBAR = B_FREE + RING;
+    // Arrivals that complete a phase: a group's four warps; both groups' last
+    // product with a Q tile; producers, MMA issuers and the groups' warps.
+    __device__ static uint32_t arrivals(int i) {
+        return (i >= B_SEMPTY && i < B_PEMPTY) || i == B_OEMPTY || i == B_OEMPTY + 1 ? 4u
+               : i >= B_QEMPTY && i < B_KVFULL ? 2u : i >= B_FREE ? 12u : 1u;
+    }
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -135,34 +141,15 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     PagedPiece *ring = reinterpret_cast<PagedPiece *>(gbase + C::RING_OFF);
 
     if (warp == 10) tmem_alloc(base + C::MISC_OFF, C::TMEM_COLS);
-    if (tid == 0) {
-        *abort_flag = 0u;
-        for (int q = 0; q < C::NQ; ++q) {
-            mbar_init(bar(C::B_QFULL + q), 1);
-            mbar_init(bar(C::B_QEMPTY + q), 2);           // both groups' last product with it
-        }
-        for (int s = 0; s < C::NSTAGE; ++s) {
-            mbar_init(bar(C::B_KVFULL + s), 1);
-            mbar_init(bar(C::B_KVEMPTY + s), 1);
-        }
-        for (int s = 0; s < 4; ++s) {                     // 2 x group + buffer
-            mbar_init(bar(C::B_SFULL + s), 1);
-            mbar_init(bar(C::B_SEMPTY + s), 4);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(bar(C::B_PFULL + x), 4);
-            mbar_init(bar(C::B_PEMPTY + x), 1);
-            mbar_init(bar(C::B_OFULL + x), 1);
-            mbar_init(bar(C::B_OEMPTY + x), 4);
-            mbar_init(bar(C::B_DONE + x), 1);
-        }
-        mbar_init(bar(C::B_XFULL), 1);
-        mbar_init(bar(C::B_XEMPTY), 1);
-        for (int q = 0; q < C::RING; ++q) {
-            mbar_init(bar(C::B_PIECE + q), 1);
-            mbar_init(bar(C::B_FREE + q), 12);            // producers, MMA issuers, 8 group warps
-        }
+    if (tid == 0) *abort_flag = 0u;
+    if (warp == 11) {
+        for (int i = lane; i < C::NBAR; i += 32) mbar_init(bar(i), C::arrivals(i));
         fence_barrier_init();
+    }
+    if (tid == 8 * 32) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
     tc_fence_before();
     const PagedShare share = paged_share<C::NTHREADS>(a, R, q_min, gbase + C::KV_OFF);
