@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfa.so")
@@ -456,52 +457,66 @@ def fa_paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, kep
                                  _stream(stream))
 
 
-def _check_paged(device, pools, ints, tensors=()):
+def _check_paged(device, dtype, pools, ints, shapes) -> None:
     """The layout that the C entry points are told by sizes and strides: pools
-    [n_pages, page_size, H_kv, d] of one 16-bit type with whole rows, int32
-    index tensors without gaps, everything on one device.  ``tensors``:
-    (tensor, shape, dtype or None) that must be contiguous."""
+    [n_pages, page_size, H_kv, d] of ``dtype`` with whole rows, int32 index
+    tensors of ``shapes`` without gaps, everything on one GPU."""
     import torch
     k = pools[0]
     if k.dim() != 4:
         raise ValueError("pages are [n_pages, page_size, H_kv, d]")
-    if k.dtype not in (torch.bfloat16, torch.float16):
+    if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
         raise TypeError(f"unsupported dtype {k.dtype}")
-    n, ps, hk, d = k.shape
-    for x in pools:
-        if x.dtype != k.dtype or x.shape != k.shape or x.stride() != k.stride():
-            raise ValueError("k_pages and v_pages differ in type, shape or strides")
-        if x.stride()[1:] != (hk * d, d, 1) and x.numel():
-            raise ValueError("a page's rows [page_size, H_kv, d] must be contiguous")
-        if x.device != device:
-            raise ValueError("tensors on different devices")
-    for x, shape in ints:
-        if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous():
+    if k.dtype is not dtype:
+        raise ValueError("the pages and the new tokens differ in type")
+    n, ps, hk, d = shape = k.shape
+    st = k.stride()
+    if st[3] != 1 or st[2] != d or st[1] != hk * d:
+        raise ValueError("a page's rows [page_size, H_kv, d] must be contiguous")
+    if k.device != device:
+        raise ValueError("tensors on different devices")
+    if len(pools) == 2:
+        v = pools[1]
+        if v.dtype is not dtype or v.shape != shape or v.stride() != st or v.device != device:
+            raise ValueError("k_pages and v_pages differ in type, shape, strides or device")
+    _check_ints(device, ints, shapes)
+    if device.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+
+
+def _check_ints(device, ints, shapes) -> None:
+    import torch
+    for x, shape in zip(ints, shapes):
+        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous():
             raise ValueError(f"index tensors are contiguous int32; expected {tuple(shape)}, got "
                              f"{x.dtype} {tuple(x.shape)}")
         if x.device != device:
             raise ValueError("tensors on different devices")
-    for x, shape, dt in tensors:
-        if x.shape != shape or x.dtype != dt or not x.is_contiguous():
-            raise ValueError(f"expected a contiguous {dt} {tuple(shape)}, got {x.dtype} "
-                             f"{tuple(x.shape)}")
-        if x.device != device:
-            raise ValueError("tensors on different devices")
+
+
+def _check_float(x, shape, device) -> None:
+    import torch
+    if (x.dtype is not torch.float32 or x.shape != shape or not x.is_contiguous()
+            or x.device != device):
+        raise ValueError(f"expected a contiguous float32 {tuple(shape)} on {device}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
 
 
 def _packed_stride(x, name: str) -> int:
     """The elements between the tokens of a packed [T, heads, d] tensor, whose
     rows are whole (a slice of wider rows is fine)."""
-    if x.dim() != 3 or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+    T, heads, d = x.shape
+    s = x.stride()
+    if s[2] != 1 or s[1] != d:
         raise ValueError(f"{name} is [T, heads, d] with contiguous [heads, d] rows")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return s[0] if T > 1 else heads * d
 
 
 class _launch_on:
-    """Makes the tensors' device current and the launch stream the one that
-    torch allocates for, so that what a call allocates is reused only behind
-    its kernels: for a raw cudaStream_t, a torch stream, or None (the
-    device's current stream).  Gives the raw stream."""
+    """Makes the tensors' device current and ``stream`` (a raw cudaStream_t, a
+    torch stream, or None: the device's current one) the stream that torch
+    allocates for and launches on: what a call allocates is then reused only
+    behind its kernels."""
 
     def __init__(self, device, stream):
         import torch
@@ -514,12 +529,10 @@ class _launch_on:
                       if device.index != torch.cuda.current_device() else None)
 
     def __enter__(self):
-        import torch
         if self.guard is not None:
             self.guard.__enter__()
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -528,34 +541,54 @@ class _launch_on:
             self.guard.__exit__(*exc)
 
 
+# The workspace of attention_paged's calls on a device's legacy default stream,
+# by (device index, d): that stream is never destroyed nor captured, so its
+# calls run one after the other.  The lock keeps the launches of one call
+# together when several host threads call.
+_paged_ws: dict = {}
+_paged_ws_lock = threading.Lock()
+
+
+def _new_paged_workspace(d: int, device):
+    """A new workspace on ``device``, which is current."""
+    import torch
+    n = fa_paged_workspace_bytes(d)
+    if n < 0:
+        raise FaError(FA_ERR_UNSUPPORTED, "fa_paged_workspace_bytes")
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
 def paged_workspace(d: int, device="cuda"):
     """A workspace for ``attention_paged`` at head dim d (uint8 tensor); calls
     that may overlap in time need one each."""
     import torch
     with torch.cuda.device(device):
-        n = fa_paged_workspace_bytes(d)
-        if n < 0:
-            raise FaError(FA_ERR_UNSUPPORTED, "fa_paged_workspace_bytes")
-        return torch.empty((n,), dtype=torch.uint8, device=device)
+        return _new_paged_workspace(d, torch.device("cuda", torch.cuda.current_device()))
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, stream=None) -> None:
     """Writes the new tokens' K and V (packed [T, H_kv, d], rows of a wider
     tensor allowed) into their pages [n_pages, page_size, H_kv, d]; kv_len
     counts them already."""
+    import torch
+    dev = k.device
+    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
+        with _launch_on(dev, stream):
+            return paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q)
     B, W = block_table.shape
-    n, ps, hk, d = k_pages.shape
-    _check_paged(k.device, (k_pages, v_pages),
-                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))))
+    T, hk, d = k.shape
+    _check_paged(dev, k.dtype, (k_pages, v_pages), (block_table, kv_len, cu_q),
+                 ((B, W), (B,), (B + 1,)))
+    n, ps, hp, dp = k_pages.shape
     ks = _packed_stride(k, "k")
-    if (k.shape != v.shape or k.dtype != v.dtype or _packed_stride(v, "v") != ks
-            or v.device != k.device):
+    if k.shape != v.shape or k.dtype != v.dtype or v.device != dev or _packed_stride(v, "v") != ks:
         raise ValueError("k and v differ in type, shape, strides or device")
-    if k.dtype != k_pages.dtype or k.shape[1:] != (hk, d):
-        raise ValueError("k, v and the pages differ in type, heads or head dim")
-    with _launch_on(k.device, stream) as st:
-        rc = fa_paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, B, hk, d,
-                             k.shape[0], ps, n, W, ks, k_pages.stride(0), st)
+    if hk != hp or d != dp:
+        raise ValueError("k, v and the pages differ in heads or head dim")
+    rc = load().fa_paged_append(
+        k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        kv_len.data_ptr(), cu_q.data_ptr(), B, hk, d, T, ps, n, W, ks, k_pages.stride(0),
+        torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_append")
 
@@ -570,35 +603,50 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
     most new tokens of one sequence.  Returns (O [T, H, d], LSE [H, T] or
     None)."""
     import torch
+    dev, dtype = q.device, q.dtype
+    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
+        with _launch_on(dev, stream):
+            return attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q, window, first,
+                                   alpha, out, lse, want_lse, workspace)
     T, H, d = q.shape
     B, W = block_table.shape
+    _check_paged(dev, dtype, (k_pages, v_pages), (block_table, kv_len, cu_q), ((B, W), (B,), (B + 1,)))
     n, ps, hk, dk = k_pages.shape
-    tensors = []
-    if out is not None:
-        tensors.append((out, q.shape, q.dtype))
-    if lse is not None:
-        tensors.append((lse, (H, T), torch.float32))
-    _check_paged(q.device, (k_pages, v_pages),
-                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))), tensors)
     qs = _packed_stride(q, "q")
-    if q.dtype != k_pages.dtype or dk != d:
-        raise ValueError("q and the pages differ in type or head dim")
+    if dk != d:
+        raise ValueError("q and the pages differ in head dim")
     if alpha is None:
         alpha = 1.0 / math.sqrt(d)
-    with _launch_on(q.device, stream) as st:
-        if out is None:
-            out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-        need = fa_paged_workspace_bytes(d)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=dtype, device=dev)
+    elif (out.shape != q.shape or out.dtype != dtype or out.device != dev
+            or not out.is_contiguous()):
+        raise ValueError(f"out is a contiguous {dtype} {tuple(q.shape)} on {dev}")
+    if lse is not None:
+        _check_float(lse, (H, T), dev)
+    elif want_lse:
+        lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    shared = workspace is None and raw == 0
+    if shared:
+        workspace = _paged_ws.get((dev.index, d))
         if workspace is None:
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
-        elif workspace.device != q.device or workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"the workspace is {need} bytes on {q.device}")
-        rc = fa_fwd_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, out, lse, workspace, B, H,
-                          hk, T, int(max_q), d, ps, n, W, qs, k_pages.stride(0), alpha,
-                          int(window[0]), int(window[1]), int(first),
-                          FA_BF16 if q.dtype == torch.bfloat16 else FA_FP16, st)
+            workspace = _paged_ws.setdefault((dev.index, d), _new_paged_workspace(d, dev))
+        _paged_ws_lock.acquire()
+    elif workspace is None:
+        workspace = _new_paged_workspace(d, dev)
+    elif (workspace.device != dev
+            or workspace.numel() * workspace.element_size() < fa_paged_workspace_bytes(d)):
+        raise ValueError(f"the workspace is {fa_paged_workspace_bytes(d)} bytes on {dev}")
+    try:
+        rc = load().fa_fwd_paged(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+            kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+            workspace.data_ptr(), B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha,
+            window[0], window[1], first, FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
+    finally:
+        if shared:
+            _paged_ws_lock.release()
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_paged")
     return out, lse
@@ -612,30 +660,34 @@ def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=
     ``scores``; entries behind kv_len are left as they were (zeros where it
     is allocated here).  Returns out."""
     import torch
+    dev, dtype = q.device, q.dtype
+    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
+        with _launch_on(dev, stream):
+            return paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q, scores, window, first,
+                                alpha, out)
     T, H, d = q.shape
     B, W = block_table.shape
+    _check_paged(dev, dtype, (k_pages,), (block_table, kv_len, cu_q), ((B, W), (B,), (B + 1,)))
     n, ps, hk, dk = k_pages.shape
-    L = W * ps if scores is None else scores.shape[2]
-    if scores is None and out is not None:
-        L = out.shape[2]
-    tensors = [(lse, (H, T), torch.float32)]
-    for x in (scores, out):
-        if x is not None:
-            tensors.append((x, (B, hk, L), torch.float32))
-    _check_paged(q.device, (k_pages,),
-                 ((block_table, (B, W)), (kv_len, (B,)), (cu_q, (B + 1,))), tensors)
     qs = _packed_stride(q, "q")
-    if q.dtype != k_pages.dtype or dk != d:
-        raise ValueError("q and the pages differ in type or head dim")
+    if dk != d:
+        raise ValueError("q and the pages differ in head dim")
+    like = scores if scores is not None else out
+    shape = (B, hk, W * ps if like is None else like.shape[2])
+    _check_float(lse, (H, T), dev)
+    if scores is not None:
+        _check_float(scores, shape, dev)
+    if out is None:
+        out = torch.zeros(shape, dtype=torch.float32, device=dev)
+    else:
+        _check_float(out, shape, dev)
     if alpha is None:
         alpha = 1.0 / math.sqrt(d)
-    with _launch_on(q.device, stream) as st:
-        if out is None:
-            out = torch.zeros((B, hk, L), dtype=torch.float32, device=q.device)
-        rc = fa_paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, scores, out, B, H, hk, T,
-                             int(max_q), d, ps, n, W, L, qs, k_pages.stride(0), alpha,
-                             int(window[0]), int(window[1]), int(first),
-                             FA_BF16 if q.dtype == torch.bfloat16 else FA_FP16, st)
+    rc = load().fa_paged_scores(
+        q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(),
+        cu_q.data_ptr(), None if scores is None else scores.data_ptr(), out.data_ptr(), B, H, hk, T,
+        max_q, d, ps, n, W, shape[2], qs, k_pages.stride(0), alpha, window[0], window[1], first,
+        FA_BF16 if dtype is torch.bfloat16 else FA_FP16, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_scores")
     return out
@@ -650,29 +702,36 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
     behind a new length are left as they were (-1 and 0 where they are
     allocated here)."""
     import torch
-    B, W = block_table.shape
-    n, ps, hk, d = k_pages.shape
-    L, Wd, keep = scores.shape[2], dst_table.shape[1], int(keep)
-    ints = [(block_table, (B, W)), (kv_len, (B,)), (dst_table, (B, Wd))]
-    if kept is not None:
-        ints.append((kept, (B, hk, keep)))
-    if new_len is not None:
-        ints.append((new_len, (B,)))
-    tensors = [(scores, (B, hk, L), torch.float32)]
-    if scores_out is not None:
-        tensors.append((scores_out, (B, hk, keep), torch.float32))
-    _check_paged(scores.device, (k_pages, v_pages), ints, tensors)
     dev = scores.device
-    with _launch_on(dev, stream) as st:
-        if kept is None:
-            kept = torch.full((B, hk, max(keep, 0)), -1, dtype=torch.int32, device=dev)
-        if scores_out is None:
-            scores_out = torch.zeros((B, hk, max(keep, 0)), dtype=torch.float32, device=dev)
-        if new_len is None:
-            new_len = torch.empty((B,), dtype=torch.int32, device=dev)
-        rc = fa_paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, kept,
-                            scores_out, new_len, B, hk, d, ps, n, W, Wd, L, k_pages.stride(0), keep,
-                            int(first), int(recent), st)
+    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
+        with _launch_on(dev, stream):
+            return paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep, first,
+                               recent, kept, scores_out, new_len)
+    B, W = block_table.shape
+    Wd = dst_table.shape[1]
+    _check_paged(dev, k_pages.dtype, (k_pages, v_pages), (block_table, kv_len, dst_table),
+                 ((B, W), (B,), (B, Wd)))
+    n, ps, hk, d = k_pages.shape
+    L = scores.shape[2]
+    _check_float(scores, (B, hk, L), dev)
+    room = (B, hk, max(keep, 0))
+    if kept is None:
+        kept = torch.full(room, -1, dtype=torch.int32, device=dev)
+    else:
+        _check_ints(dev, (kept,), (room,))
+    if scores_out is None:
+        scores_out = torch.zeros(room, dtype=torch.float32, device=dev)
+    else:
+        _check_float(scores_out, room, dev)
+    if new_len is None:
+        new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _check_ints(dev, (new_len,), ((B,),))
+    rc = load().fa_paged_evict(
+        k_pages.data_ptr(), v_pages.data_ptr(), scores.data_ptr(), block_table.data_ptr(),
+        kv_len.data_ptr(), dst_table.data_ptr(), kept.data_ptr(), scores_out.data_ptr(),
+        new_len.data_ptr(), B, hk, d, ps, n, W, Wd, L, k_pages.stride(0), keep, first, recent,
+        torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_evict")
     return kept, scores_out, new_len
