@@ -19,34 +19,45 @@
 // with long chunks it is bound by the exponentials (one per row and token
 // against 2 d flops, 32 a clock and SM).
 //
-// Units are dealt to the CTAs in turn, back and forth; warp 10 finds a
-// unit's sequence by a prefix sum over 32 sequences at a time.  The log-sum-
-// exps of a Q tile go through shared memory, where all threads of a group
-// read the same one at a time.  Columns of other sequences (a Q tile reads
-// past its sequence's end) and rows that see nothing are dropped by
-// selection, never by multiplying with zero.
+// Units are dealt to the CTAs in turn, back and forth; warp 10 finds a unit's
+// sequence by a prefix sum over 32 sequences at a time.  Warp 8 loads the K
+// tiles (page ids a unit ahead) and the Q tiles, warp 11 puts the log-sum-exps
+// of a Q tile's rows beside it, warp 9 issues the products.  Columns of other
+// sequences (a Q tile reads past its sequence's end) are dropped by selection,
+// never by multiplying with zero.
+//
+// kN = 32: Q tiles of at most 32 rows take 8 KB instead of 32 and leave room for
+// six K tiles instead of four (d = 128): the bytes in flight of a decoding step.
 #include "fa_paged.cuh"
 
 namespace fa {
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int kN>
 struct ScoresCfg {
     static constexpr int NCH = D / 64;
     static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
     static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
-    static constexpr int NK = D == 64 ? 8 : 4;            // K tiles in flight
-    static constexpr int NQ = D == 64 ? 6 : 3;            // Q tiles in flight
+    static constexpr uint32_t Q_CHUNK = kN * 128u, Q_BYTES = NCH * Q_CHUNK;
+    static constexpr int NK = (D == 64 ? 2 : 1) * (kN == 32 ? 6 : 4);   // K tiles in flight
+    static constexpr int NQ = D == 64 && kN == 128 ? 5 : 3;             // Q tiles in flight
     static constexpr int NTHREADS = 384;
     static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
     static constexpr int RING = 4;
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = NK * TILE_BYTES;
-    static constexpr uint32_t L_OFF = Q_OFF + NQ * TILE_BYTES;        // [2 groups][128] floats
-    static constexpr uint32_t RING_OFF = L_OFF + 2 * 128 * 4;
+    static constexpr uint32_t L_OFF = Q_OFF + NQ * Q_BYTES;             // -LSE log2(e): [NQ][128] floats
+    static constexpr uint32_t RING_OFF = L_OFF + NQ * 128 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 32;
     static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_QFULL = 2 * NK, B_QEMPTY = B_QFULL + NQ,
                          B_SFULL = B_QEMPTY + NQ, B_SEMPTY = B_SFULL + 4, B_MMADONE = B_SEMPTY + 4,
                          B_UNIT = B_MMADONE + 1, B_FREE = B_UNIT + RING, NBAR = B_FREE + RING;
+    // Arrivals that complete a phase: Q full by the copy and warp 11, Q empty by
+    // the products and the 8 group warps, S empty by a group's warps, units by
+    // the producers, MMA issuer and the groups.
+    __device__ static uint32_t arrivals(int i) {
+        return i >= B_QFULL && i < B_QEMPTY ? 2u : i >= B_QEMPTY && i < B_SFULL ? 9u
+               : i >= B_SEMPTY && i < B_MMADONE ? 4u : i >= B_FREE ? 11u : 1u;
+    }
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -62,12 +73,12 @@ struct __align__(16) ScoresUnit {
 };
 static_assert(sizeof(ScoresUnit) == 32, "unit ring");
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int kN>
 __global__ void __launch_bounds__(384, 1)
 fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const PagedArgs a, const float *in, float *out, const int L, const int R,
-                       const uint32_t idesc) {
-    using C = ScoresCfg<D, kBF16>;
+                       const PagedArgs a, const float *in, float *out, const int L, const int R) {
+    using C = ScoresCfg<D, kBF16, kN>;
+    constexpr uint32_t idesc = idesc_f16(128, kN, kBF16, false, false);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -79,34 +90,22 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     ScoresUnit *ring = reinterpret_cast<ScoresUnit *>(gbase + C::RING_OFF);
 
     if (warp == 9) tmem_alloc(base + C::MISC_OFF, C::TMEM_COLS);
-    if (tid == 0) {
-        *abort_flag = 0u;
-        for (int s = 0; s < C::NK; ++s) {
-            mbar_init(bar(C::B_KFULL + s), 1);
-            mbar_init(bar(C::B_KEMPTY + s), 1);
-        }
-        for (int s = 0; s < C::NQ; ++s) {
-            mbar_init(bar(C::B_QFULL + s), 1);
-            mbar_init(bar(C::B_QEMPTY + s), 1);
-        }
-        for (int s = 0; s < 4; ++s) {                     // 2 x group + buffer
-            mbar_init(bar(C::B_SFULL + s), 1);
-            mbar_init(bar(C::B_SEMPTY + s), 4);
-        }
-        mbar_init(bar(C::B_MMADONE), 1);
-        for (int q = 0; q < C::RING; ++q) {
-            mbar_init(bar(C::B_UNIT + q), 1);
-            mbar_init(bar(C::B_FREE + q), 10);            // producer, MMA, 8 group warps
-        }
+    if (tid == 0) *abort_flag = 0u;
+    if (warp == 11) {
+        for (int i = lane; i < C::NBAR; i += 32) mbar_init(bar(i), C::arrivals(i));
         fence_barrier_init();
+    }
+    if (tid == 8 * 32) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
     }
     // The rows of the Q tiles that no box fills are columns of the product:
     // zeros there keep the scores finite, and a log-sum-exp of +inf their
     // terms zero.
     const int box_rows = R * a.group;
-    for (int i = tid; i < C::NQ * C::NCH * (128 - box_rows) * 8; i += C::NTHREADS) {
-        const int chunk = i / ((128 - box_rows) * 8), r = i % ((128 - box_rows) * 8);
-        *reinterpret_cast<uint4 *>(gbase + C::Q_OFF + chunk * C::CHUNK_BYTES + box_rows * 128 + r * 16) =
+    for (int i = tid; i < C::NQ * C::NCH * (kN - box_rows) * 8; i += C::NTHREADS) {
+        const int chunk = i / ((kN - box_rows) * 8), r = i % ((kN - box_rows) * 8);
+        *reinterpret_cast<uint4 *>(gbase + C::Q_OFF + chunk * C::Q_CHUNK + box_rows * 128 + r * 16) =
             make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -133,7 +132,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         bool ok = true;
         auto post = [&](const ScoresUnit &u) __attribute__((always_inline)) {
             const uint32_t q = sent % C::RING;
-            ok = mbar_wait_warp(bar(C::B_FREE + q), ((sent / C::RING) & 1u) ^ 1u, w, 30);
+            ok = mbar_wait_idle(bar(C::B_FREE + q), ((sent / C::RING) & 1u) ^ 1u, w, 30);
             if (ok && lane == 0) {
                 ring[q] = u;
                 mbar_arrive(bar(C::B_UNIT + q));
@@ -203,10 +202,6 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
       } else if (warp == 8) {
         // =================== TMA producer (whole warp) ===================
         WaitCtx w{abort_flag, a.status, kRoleProducer};
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_k);
-        }
         const PagedBox<C::NCH> bx(a.ps_log2);
         const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
         uint32_t kc = 0, qc = 0, ui = 0;
@@ -258,7 +253,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 if (lane == 0) mbar_arrive_expect_tx(bar(C::B_QFULL + slot), q_bytes);
                 __syncwarp();
                 if (lane < C::NCH)
-                    tma_load_4d(&tm_q, base + C::Q_OFF + slot * C::TILE_BYTES + lane * C::CHUNK_BYTES,
+                    tma_load_4d(&tm_q, base + C::Q_OFF + slot * C::Q_BYTES + lane * C::Q_CHUNK,
                                 bar(C::B_QFULL + slot), lane * 64, u.h * a.group, u.q0 + t * R, 0);
                 qarmed |= 1u << slot;
                 qarmed_par = (qarmed_par & ~(1u << slot)) | (ph << slot);
@@ -269,49 +264,104 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         for (int s = 0; s < C::NQ; ++s)
             if (qarmed & (1u << s)) mbar_wait_quiet(bar(C::B_QFULL + s), (qarmed_par >> s) & 1u, 500000000ull);
         __syncwarp();
-      } else if (warp == 9) {
-        // =================== MMA issuer ===================
-        WaitCtx w{abort_flag, a.status, kRoleMma};
-        uint32_t kc = 0, qc = 0, ui = 0, sc0 = 0, sc1 = 0;
+      } else if (warp == 11) {
+        // =================== log-sum-exps (whole warp) ===================
+        // -LSE log2(e) of a Q tile's rows, -inf (a term of zero) for columns
+        // that are none or rows that see nothing; read a tile ahead.
+        WaitCtx w{abort_flag, a.status, kRoleProducer};
+        uint32_t qc = 0, ui = 0;
         bool ok = true;
-        auto mma = [&](const int x, const uint32_t kslot, const uint32_t qslot,
-                       uint32_t &sc) __attribute__((always_inline)) -> bool {
-            const int buf = sc & 1u;
-            if (!mbar_wait_warp(bar(C::B_SEMPTY + 2 * x + buf), ((sc >> 1) & 1u) ^ 1u, w, 11)) return false;
-            ++sc;
-            tc_fence_after();
-            const uint64_t kd = smem_desc_sw128(base + C::K_OFF + kslot * C::TILE_BYTES, 16u, 1024u);
-            const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qslot * C::TILE_BYTES, 16u, 1024u);
+        constexpr int kEach = kN / 32;
+        int pos[kEach], head[kEach];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
-                mma_ss_f16_elect(tbase + C::col_s(x, buf), kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+        for (int i = 0; i < kEach; ++i) {
+            pos[i] = (lane + 32 * i) / a.group;
+            head[i] = (lane + 32 * i) % a.group;
+        }
+        auto read = [&](const ScoresUnit &u, int t, float (&v)[kEach]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int row = t * R + pos[i];
+                v[i] = -INFINITY;
+                if (pos[i] < R && t < u.qb && row < u.m)
+                    v[i] = a.lse[static_cast<size_t>(u.h * a.group + head[i]) * a.T + u.q0 + row];
             }
-            mma_commit_elect(bar(C::B_SFULL + 2 * x + buf));
-            return true;
         };
+        ScoresUnit u, nx;
+        float val[kEach], val_n[kEach];
+        bool more = take(ui++, w, 33, u);
+        if (more) read(u, u.qa, val);
+        while (ok && more) {
+            more = take(ui++, w, 33, nx);
+            if (more) read(nx, nx.qa, val_n);
+            for (int t = u.qa; t < u.qb; ++t, ++qc) {
+                const uint32_t slot = qc % C::NQ, ph = (qc / C::NQ) & 1u;
+                float cur[kEach];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) cur[i] = val[i];
+                read(u, t + 1, val);
+                ok = mbar_wait_warp(bar(C::B_QEMPTY + slot), ph ^ 1u, w, 3);
+                if (!ok) break;
+                float *nl = reinterpret_cast<float *>(gbase + C::L_OFF) + slot * 128;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    nl[lane + 32 * i] = cur[i] == -INFINITY ? -INFINITY : cur[i] * -1.44269504088896340736f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_QFULL + slot));
+            }
+            u = nx;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) val[i] = val_n[i];
+        }
+        __syncwarp();
+      } else {
+        // =================== MMA issuer (whole warp, one elected lane issues) ===================
+        WaitCtx w{abort_flag, a.status, kRoleMma};
+        auto uniform = [](int v) __attribute__((always_inline)) -> int { return __shfl_sync(0xffffffffu, v, 0); };
+        uint32_t ks = 0, kph = 0, qs = 0, qph = 0, ui = 0; // slots and their phases
+        uint32_t sc = 0, sph = 0;                          // bit x: group x's S buffer, its phase
+        bool ok = true;
         ScoresUnit u;
         while (ok && take(ui, w, 32, u)) {
             ++ui;
-            if (u.qa >= u.qb) continue;
-            const int nk = u.k0 + 128 < u.n ? 2 : 1;
-            const uint32_t k0s = kc % C::NK, k1s = (kc + 1) % C::NK;
-            for (int t = u.qa; t < u.qb && ok; ++t, ++qc) {
-                const uint32_t qs = qc % C::NQ;
-                ok = mbar_wait_warp(bar(C::B_QFULL + qs), (qc / C::NQ) & 1u, w, 14);
-                if (ok && t == u.qa) ok = mbar_wait_warp(bar(C::B_KFULL + k0s), (kc / C::NK) & 1u, w, 13);
-                if (ok) ok = mma(0, k0s, qs, sc0);
-                if (ok && nk == 2) {
-                    if (t == u.qa) ok = mbar_wait_warp(bar(C::B_KFULL + k1s), ((kc + 1) / C::NK) & 1u, w, 13);
-                    if (ok) ok = mma(1, k1s, qs, sc1);
+            const int tiles = uniform(u.qb - u.qa);
+            if (tiles <= 0) continue;
+            const int nk = uniform(u.k0 + 128 < u.n ? 2 : 1);
+            uint32_t k1 = ks + 1, k1ph = kph;
+            if (k1 == C::NK) { k1 = 0; k1ph ^= 1u; }
+#pragma unroll 1
+            for (int t = 0; t < tiles && ok; ++t) {
+                ok = mbar_wait_warp(bar(C::B_QFULL + qs), qph, w, 14);
+#pragma unroll 1
+                for (int x = 0; x < nk && ok; ++x) {
+                    const uint32_t slot = x ? k1 : ks, buf = (sc >> x) & 1u, bx = 2 * x + buf;
+                    if (t == 0) ok = mbar_wait_warp(bar(C::B_KFULL + slot), x ? k1ph : kph, w, 13);
+                    if (ok) ok = mbar_wait_warp(bar(C::B_SEMPTY + bx), ((sph >> bx) & 1u) ^ 1u, w, 11);
+                    if (!ok) break;
+                    sph ^= 1u << bx;
+                    sc ^= 1u << x;
+                    tc_fence_after();
+                    const uint64_t kd = smem_desc_sw128(base + C::K_OFF + slot * C::TILE_BYTES, 16u, 1024u);
+                    const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::Q_BYTES, 16u, 1024u);
+                    const uint32_t d_s = tbase + 256u * x + 128u * buf;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t ko = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                        const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
+                        mma_ss_f16_elect(d_s, kd + ko, qd + qo, idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit_elect(bar(C::B_SFULL + bx));
                 }
                 if (!ok) break;
                 mma_commit_elect(bar(C::B_QEMPTY + qs));
+                if (++qs == C::NQ) { qs = 0; qph ^= 1u; }
             }
             if (!ok) break;
-            mma_commit_elect(bar(C::B_KEMPTY + k0s));
-            if (nk == 2) mma_commit_elect(bar(C::B_KEMPTY + k1s));
-            kc += nk;
+            mma_commit_elect(bar(C::B_KEMPTY + ks));
+            if (nk == 2) mma_commit_elect(bar(C::B_KEMPTY + k1));
+            ks = nk == 2 ? k1 + 1 : ks + 1;
+            kph = nk == 2 ? k1ph : kph;
+            if (ks == C::NK) { ks = 0; kph ^= 1u; }
         }
         mma_commit_elect(bar(C::B_MMADONE));
         mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
@@ -323,99 +373,75 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         WaitCtx w{abort_flag, a.status, x ? kRoleSoftmax1 : kRoleSoftmax0};
-        float *nl = reinterpret_cast<float *>(gbase + C::L_OFF) + x * 128;   // -LSE log2(e) of the columns
         const float sl2 = a.scale_log2;
         const float2 c2 = make_float2(sl2, sl2);
-        const int my_pos = row / a.group, my_head = row - my_pos * a.group;  // of column `row`
-        uint32_t ui = 0, sc = 0;
+        uint32_t ui = 0, sc = 0, qs = 0, qph = 0;
         bool ok = true;
         ScoresUnit u;
         while (ok && take(ui, w, 24, u)) {
             ++ui;
             const int kk = u.k0 + x * 128 + row;                             // this thread's token
-            if (u.k0 + x * 128 >= u.n) continue;
+            const bool none = u.k0 + x * 128 >= u.n;                         // the group has no tile of this unit
             const int old = u.n - u.m;
             const size_t at = (static_cast<size_t>(u.b) * a.H_kv + u.h) * L + kk;
-            const float had = in != nullptr && kk < old ? in[at] : 0.f;
+            const float had = in != nullptr && !none && kk < old ? in[at] : 0.f;
             // rows [ra, rb) of the new tokens see this one
-            long long ra = a.wr >= 0 ? static_cast<long long>(kk) - a.wr - old : 0;
-            long long rb = a.wl >= 0 && kk >= a.first ? static_cast<long long>(kk) + a.wl - old + 1 : u.m;
-            ra = max(ra, 0ll);
-            rb = min(rb, static_cast<long long>(u.m));
-            // -LSE of column `row` of Q tile t, -inf for none (the term is then 0)
-            const float *lrow = a.lse + static_cast<size_t>(u.h * a.group + my_head) * a.T + u.q0;
-            auto column = [&](int t) __attribute__((always_inline)) -> float {
-                const int i = t * R + my_pos;
-                if (my_pos >= R || i >= u.m) return -INFINITY;
-                const float z = lrow[i];
-                return z == -INFINITY ? -INFINITY : z * -1.44269504088896340736f;
-            };
+            const long long ra = a.wr >= 0 ? static_cast<long long>(kk) - a.wr - old : 0;
+            const long long rb = a.wl >= 0 && kk >= a.first ? static_cast<long long>(kk) + a.wl - old + 1 : u.m;
+            const int r0 = static_cast<int>(min(max(ra, 0ll), static_cast<long long>(u.m)));
+            const int r1 = static_cast<int>(min(max(rb, 0ll), static_cast<long long>(u.m)));
             float sum = 0.f;
-            float next = u.qa < u.qb ? column(u.qa) : 0.f;
+#pragma unroll 1
             for (int t = u.qa; t < u.qb; ++t) {
-                const int nc = min(R, u.m - t * R) * a.group;                // columns of this sequence
-                asm volatile("bar.sync %0, 128;" :: "r"(1 + x) : "memory");  // the last tile's are read
-                nl[row] = next;
-                asm volatile("bar.sync %0, 128;" :: "r"(1 + x) : "memory");
-                if (t + 1 < u.qb) next = column(t + 1);
+                const uint32_t slot = qs;
+                ok = mbar_wait_warp(bar(C::B_QFULL + slot), qph, w, 19);     // the LSEs are there
+                if (++qs == C::NQ) { qs = 0; qph ^= 1u; }
+                if (!ok) break;
+                if (none) {
+                    if (lane == 0) mbar_arrive(bar(C::B_QEMPTY + slot));
+                    continue;
+                }
                 const int buf = sc & 1u;
-                ok = mbar_wait(bar(C::B_SFULL + 2 * x + buf), (sc >> 1) & 1u, w, 20);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = mbar_wait_warp(bar(C::B_SFULL + 2 * x + buf), (sc >> 1) & 1u, w, 20);
                 if (!ok) break;
                 ++sc;
                 tc_fence_after();
                 const uint32_t tS = tbase + lane_off + C::col_s(x, buf);
+                const float4 *l4 = reinterpret_cast<const float4 *>(gbase + C::L_OFF) + slot * 32;
                 // columns [ca, cb) see this token
-                const int ca = static_cast<int>(min(max(ra - static_cast<long long>(t) * R, 0ll), static_cast<long long>(R))) * a.group;
-                const int cb = min(nc, static_cast<int>(min(max(rb - static_cast<long long>(t) * R, 0ll), static_cast<long long>(R))) * a.group);
-                const bool all = __all_sync(0xffffffffu, ca == 0 && cb == box_rows);
+                const int ca = min(max(r0 - t * R, 0), R) * a.group;
+                const int cb = min(max(r1 - t * R, 0), R) * a.group;
+                const bool part = __any_sync(0xffffffffu, ca != 0 || cb != box_rows);
                 float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
-                auto add = [&](const uint32_t (&s)[32], const int c0) __attribute__((always_inline)) {
-                    const float4 *l4 = reinterpret_cast<const float4 *>(nl + c0);
+                uint32_t sv[kN];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 l = l4[c / 4];
-                        const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                                      c2, make_float2(l.x, l.y));
-                        const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
-                                                      c2, make_float2(l.z, l.w));
-                        float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
-                        float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
-                        if (!all) {
-                            if (c0 + c < ca || c0 + c >= cb) e01.x = 0.f;
-                            if (c0 + c + 1 < ca || c0 + c + 1 >= cb) e01.y = 0.f;
-                            if (c0 + c + 2 < ca || c0 + c + 2 >= cb) e23.x = 0.f;
-                            if (c0 + c + 3 < ca || c0 + c + 3 >= cb) e23.y = 0.f;
-                        }
-                        e_a = __fadd2_rn(e_a, e01);
-                        e_b = __fadd2_rn(e_b, e23);
-                    }
-                };
-                uint32_t s0[32];
-                if (nc <= 32) {
-                    tmem_ld32(tS, s0);
-                    tmem_ld_wait();
-                } else {
-                    uint32_t s1[32], s2[32], s3[32];
-                    tmem_ld32(tS, s0);
-                    tmem_ld32(tS + 32, s1);
-                    tmem_ld32(tS + 64, s2);
-                    tmem_ld32(tS + 96, s3);
-                    tmem_ld_wait();
-                    add(s1, 32);
-                    if (nc > 64) {
-                        add(s2, 64);
-                        add(s3, 96);
-                    }
-                }
+                for (int c = 0; c < kN; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&sv[c]));
+                tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + 2 * x + buf));
-                add(s0, 0);
+                if (part) {
+                    // hidden columns: a score of -inf (what lies there may be anything)
+#pragma unroll
+                    for (int c = 0; c < kN; ++c)
+                        if (c < ca || c >= cb) sv[c] = 0xff800000u;
+                }
+#pragma unroll
+                for (int c = 0; c < kN; c += 4) {
+                    const float4 l = l4[c / 4];
+                    const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                                                  c2, make_float2(l.x, l.y));
+                    const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])),
+                                                  c2, make_float2(l.z, l.w));
+                    e_a = __fadd2_rn(e_a, make_float2(ex2_approx(x01.x), ex2_approx(x01.y)));
+                    e_b = __fadd2_rn(e_b, make_float2(ex2_approx(x23.x), ex2_approx(x23.y)));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_QEMPTY + slot));
                 sum += (e_a.x + e_a.y) + (e_b.x + e_b.y);
             }
             if (!ok) break;
-            if (kk < u.n) out[at] = had + sum;
+            if (!none && kk < u.n) out[at] = had + sum;
         }
     }
 
@@ -427,10 +453,10 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     }
 }
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, int kN>
 static cudaError_t launch_scores_inst(const PagedScoresLaunch &L) {
-    using C = ScoresCfg<D, kBF16>;
-    auto kern = fa_paged_scores_kernel<D, kBF16>;
+    using C = ScoresCfg<D, kBF16, kN>;
+    auto kern = fa_paged_scores_kernel<D, kBF16, kN>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -442,17 +468,19 @@ static cudaError_t launch_scores_inst(const PagedScoresLaunch &L) {
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, bit, __ATOMIC_ACQ_REL);
     }
-    // N of the product: as many columns as the groups may read at once
-    const int rows = L.R * L.a.group;
-    const uint32_t cols = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.a, L.in, L.out, L.L, L.R,
-                                                           idesc_f16(128, cols, kBF16, false, false));
+    kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.a, L.in, L.out, L.L, L.R);
     return cudaGetLastError();
 }
 
+template <int D>
+static cudaError_t launch_scores_dispatch(const PagedScoresLaunch &L) {
+    if (L.R * L.a.group <= 32)
+        return L.bf16 ? launch_scores_inst<D, true, 32>(L) : launch_scores_inst<D, false, 32>(L);
+    return L.bf16 ? launch_scores_inst<D, true, 128>(L) : launch_scores_inst<D, false, 128>(L);
+}
+
 cudaError_t launch_paged_scores(const PagedScoresLaunch &L) {
-    if (L.d == 64) return L.bf16 ? launch_scores_inst<64, true>(L) : launch_scores_inst<64, false>(L);
-    return L.bf16 ? launch_scores_inst<128, true>(L) : launch_scores_inst<128, false>(L);
+    return L.d == 64 ? launch_scores_dispatch<64>(L) : launch_scores_dispatch<128>(L);
 }
 
 }  // namespace fa
