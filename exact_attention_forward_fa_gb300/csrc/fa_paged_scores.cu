@@ -28,6 +28,9 @@
 //
 // kN = 32: Q tiles of at most 32 rows take 8 KB instead of 32 and leave room for
 // six K tiles instead of four (d = 128): the bytes in flight of a decoding step.
+// A warp of its own (12) then loads group 1's K tiles: a tile of 16-token pages is
+// 16 boxes at ~80 cycles each, and a unit's two tiles come from HBM in ~2900.
+//
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -40,23 +43,25 @@ struct ScoresCfg {
     static constexpr uint32_t Q_CHUNK = kN * 128u, Q_BYTES = NCH * Q_CHUNK;
     static constexpr int NK = (D == 64 ? 2 : 1) * (kN == 32 ? 6 : 4);   // K tiles in flight
     static constexpr int NQ = D == 64 && kN == 128 ? 5 : 3;             // Q tiles in flight
-    static constexpr int NTHREADS = 384;
+    static constexpr int NL = 3;                                        // and their LSEs (held longer)
+    static constexpr int NKX = NK / 2;                                  // slots of a group's K ring
+    static constexpr bool kTwo = kN == 32;                              // a K producer for each group
+    static constexpr int NTHREADS = kTwo ? 416 : 384;
     static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
     static constexpr int RING = 4;
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = NK * TILE_BYTES;
-    static constexpr uint32_t L_OFF = Q_OFF + NQ * Q_BYTES;             // -LSE log2(e): [NQ][128] floats
-    static constexpr uint32_t RING_OFF = L_OFF + NQ * 128 * 4;
+    static constexpr uint32_t L_OFF = Q_OFF + NQ * Q_BYTES;             // -LSE log2(e): [NL][128] floats
+    static constexpr uint32_t RING_OFF = L_OFF + NL * 128 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 32;
     static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_QFULL = 2 * NK, B_QEMPTY = B_QFULL + NQ,
-                         B_SFULL = B_QEMPTY + NQ, B_SEMPTY = B_SFULL + 4, B_MMADONE = B_SEMPTY + 4,
+                         B_LFULL = B_QEMPTY + NQ, B_LEMPTY = B_LFULL + NL, B_SFULL = B_LEMPTY + NL, B_SEMPTY = B_SFULL + 4, B_MMADONE = B_SEMPTY + 4,
                          B_UNIT = B_MMADONE + 1, B_FREE = B_UNIT + RING, NBAR = B_FREE + RING;
-    // Arrivals that complete a phase: Q full by the copy and warp 11, Q empty by
-    // the products and the 8 group warps, S empty by a group's warps, units by
-    // the producers, MMA issuer and the groups.
+    // Arrivals that complete a phase: LSEs read by the 8 group warps, S read by a
+    // group's, units taken by the producers, MMA issuer and groups.
     __device__ static uint32_t arrivals(int i) {
-        return i >= B_QFULL && i < B_QEMPTY ? 2u : i >= B_QEMPTY && i < B_SFULL ? 9u
-               : i >= B_SEMPTY && i < B_MMADONE ? 4u : i >= B_FREE ? 11u : 1u;
+        return i >= B_LEMPTY && i < B_SFULL ? 8u : i >= B_SEMPTY && i < B_MMADONE ? 4u
+               : i >= B_FREE ? (kTwo ? 12u : 11u) : 1u;
     }
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
@@ -74,7 +79,7 @@ struct __align__(16) ScoresUnit {
 static_assert(sizeof(ScoresUnit) == 32, "unit ring");
 
 template <int D, bool kBF16, int kN>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kN == 32 ? 416 : 384, 1)
 fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const PagedArgs a, const float *in, float *out, const int L, const int R) {
     using C = ScoresCfg<D, kBF16, kN>;
@@ -124,7 +129,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     };
 
     if (warp >= 8) {
-      regs_shrink<C::REGS_LOW>();
+      if constexpr (!C::kTwo) regs_shrink<C::REGS_LOW>();
       if (warp == 10) {
         // =================== scheduler (whole warp) ===================
         WaitCtx w{abort_flag, a.status, kRolePaged};
@@ -199,15 +204,18 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             stop.k0 = -1;
             post(stop);
         }
-      } else if (warp == 8) {
-        // =================== TMA producer (whole warp) ===================
+      } else if (warp == 8 || warp == 12) {
+        // =================== TMA producers (whole warps) ===================
+        // K tile x of every unit for x in [xa, xb), each group's in a ring of its
+        // own, and (warp 8) the Q tiles
         WaitCtx w{abort_flag, a.status, kRoleProducer};
+        const int xa = warp == 12 ? 1 : 0, xb = warp == 12 || !C::kTwo ? 2 : 1;
         const PagedBox<C::NCH> bx(a.ps_log2);
         const uint32_t q_bytes = static_cast<uint32_t>(a.group * R) * 128u * C::NCH;
-        uint32_t kc = 0, qc = 0, ui = 0;
+        uint32_t kc0 = 0, kc1 = 0, qc = 0, ui = 0;
         uint32_t qarmed = 0, qarmed_par = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        // page ids of a unit's two tiles, read while the unit before it loads
+        // page ids of a unit's tiles, read while the unit before it loads
         auto page_of = [&](const ScoresUnit &u, int x) __attribute__((always_inline)) -> int {
             const int j = (u.k0 >> 7) + x, vhi = paged_hi(u.n - 1, u.n, a.wr);
             if (u.qa >= u.qb || !bx.needs(j, paged_lo(u.n - u.m, a.wl), vhi, min(a.first, vhi))) return a.n_pages;
@@ -218,22 +226,22 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         int page[2] = {0, 0};
         if (more) { page[0] = page_of(u, 0); page[1] = page_of(u, 1); }
         for (; ok && more; u = nx) {
-            int mine[2] = {page[0], page[1]};
+            const int mine[2] = {page[0], page[1]};
             more = take(ui++, w, 31, nx);
             if (more) { page[0] = page_of(nx, 0); page[1] = page_of(nx, 1); }
             if (u.qa >= u.qb) continue;                   // no row sees the pair
             const int nk = u.k0 + 128 < u.n ? 2 : 1;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (x >= nk || !ok) break;
+#pragma unroll 1
+            for (int x = xa; x < min(xb, nk) && ok; ++x) {
                 const int j = (u.k0 >> 7) + x;
-                int pg = mine[x];
+                int pg = x ? mine[1] : mine[0];
                 if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
                     const int vhi = paged_hi(u.n - 1, u.n, a.wr);
                     if (bx.needs(j, paged_lo(u.n - u.m, a.wl), vhi, min(a.first, vhi))) report_bad_index(a.status, 2);
                     pg = a.n_pages;                       // beyond the pool: zeros
                 }
-                const uint32_t slot = kc % C::NK, ph = (kc / C::NK) & 1u;
+                const uint32_t kc = x ? kc1 : kc0;
+                const uint32_t slot = x * C::NKX + kc % C::NKX, ph = (kc / C::NKX) & 1u;
                 ok = mbar_wait_warp(bar(C::B_KEMPTY + slot), ph ^ 1u, w, 2);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(bar(C::B_KFULL + slot), C::TILE_BYTES);
@@ -244,9 +252,10 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                                 (j * 128 + bx.row) & ((1 << a.ps_log2) - 1), pg);
                 armed |= 1u << slot;
                 armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
-                ++kc;
+                if (x) ++kc1; else ++kc0;
             }
-            for (int t = u.qa; t < u.qb && ok; ++t, ++qc) {
+#pragma unroll 1
+            for (int t = u.qa; t < u.qb && ok && warp == 8; ++t, ++qc) {
                 const uint32_t slot = qc % C::NQ, ph = (qc / C::NQ) & 1u;
                 ok = mbar_wait_warp(bar(C::B_QEMPTY + slot), ph ^ 1u, w, 1);
                 if (!ok) break;
@@ -295,19 +304,19 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             more = take(ui++, w, 33, nx);
             if (more) read(nx, nx.qa, val_n);
             for (int t = u.qa; t < u.qb; ++t, ++qc) {
-                const uint32_t slot = qc % C::NQ, ph = (qc / C::NQ) & 1u;
+                const uint32_t slot = qc % C::NL, ph = (qc / C::NL) & 1u;
                 float cur[kEach];
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) cur[i] = val[i];
                 read(u, t + 1, val);
-                ok = mbar_wait_warp(bar(C::B_QEMPTY + slot), ph ^ 1u, w, 3);
+                ok = mbar_wait_warp(bar(C::B_LEMPTY + slot), ph ^ 1u, w, 3);
                 if (!ok) break;
                 float *nl = reinterpret_cast<float *>(gbase + C::L_OFF) + slot * 128;
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
                     nl[lane + 32 * i] = cur[i] == -INFINITY ? -INFINITY : cur[i] * -1.44269504088896340736f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_QFULL + slot));
+                if (lane == 0) mbar_arrive(bar(C::B_LFULL + slot));
             }
             u = nx;
 #pragma unroll
@@ -318,7 +327,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         // =================== MMA issuer (whole warp, one elected lane issues) ===================
         WaitCtx w{abort_flag, a.status, kRoleMma};
         auto uniform = [](int v) __attribute__((always_inline)) -> int { return __shfl_sync(0xffffffffu, v, 0); };
-        uint32_t ks = 0, kph = 0, qs = 0, qph = 0, ui = 0; // slots and their phases
+        uint32_t ks = 0, kph = 0, k1 = C::NKX, k1ph = 0, qs = 0, qph = 0, ui = 0;   // slots and their phases
         uint32_t sc = 0, sph = 0;                          // bit x: group x's S buffer, its phase
         bool ok = true;
         ScoresUnit u;
@@ -327,8 +336,6 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const int tiles = uniform(u.qb - u.qa);
             if (tiles <= 0) continue;
             const int nk = uniform(u.k0 + 128 < u.n ? 2 : 1);
-            uint32_t k1 = ks + 1, k1ph = kph;
-            if (k1 == C::NK) { k1 = 0; k1ph ^= 1u; }
 #pragma unroll 1
             for (int t = 0; t < tiles && ok; ++t) {
                 ok = mbar_wait_warp(bar(C::B_QFULL + qs), qph, w, 14);
@@ -358,24 +365,25 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             }
             if (!ok) break;
             mma_commit_elect(bar(C::B_KEMPTY + ks));
-            if (nk == 2) mma_commit_elect(bar(C::B_KEMPTY + k1));
-            ks = nk == 2 ? k1 + 1 : ks + 1;
-            kph = nk == 2 ? k1ph : kph;
-            if (ks == C::NK) { ks = 0; kph ^= 1u; }
+            if (++ks == C::NKX) { ks = 0; kph ^= 1u; }
+            if (nk == 2) {
+                mma_commit_elect(bar(C::B_KEMPTY + k1));
+                if (++k1 == C::NK) { k1 = C::NKX; k1ph ^= 1u; }
+            }
         }
         mma_commit_elect(bar(C::B_MMADONE));
         mbar_wait_quiet(bar(C::B_MMADONE), 0, 500000000ull);
         __syncwarp();
       }
     } else {
-        regs_grow<C::REGS_HIGH>();
+        if constexpr (!C::kTwo) regs_grow<C::REGS_HIGH>();
         // =================== group x: one cached token a thread ===================
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         WaitCtx w{abort_flag, a.status, x ? kRoleSoftmax1 : kRoleSoftmax0};
         const float sl2 = a.scale_log2;
         const float2 c2 = make_float2(sl2, sl2);
-        uint32_t ui = 0, sc = 0, qs = 0, qph = 0;
+        uint32_t ui = 0, sc = 0, ls = 0, lph = 0;          // units, S tiles, LSE slot and its phase
         bool ok = true;
         ScoresUnit u;
         while (ok && take(ui, w, 24, u)) {
@@ -391,53 +399,57 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             const int r0 = static_cast<int>(min(max(ra, 0ll), static_cast<long long>(u.m)));
             const int r1 = static_cast<int>(min(max(rb, 0ll), static_cast<long long>(u.m)));
             float sum = 0.f;
+            // the next Q tile's LSEs and (if the group has a tile) scores are there
+            auto arrived = [&]() __attribute__((always_inline)) -> bool {
+                if (!mbar_wait_warp(bar(C::B_LFULL + ls), lph, w, 19)) return false;
+                if (none) return true;
+                if (!mbar_wait_warp(bar(C::B_SFULL + 2 * x + (sc & 1u)), (sc >> 1) & 1u, w, 20)) return false;
+                tc_fence_after();
+                return true;
+            };
 #pragma unroll 1
             for (int t = u.qa; t < u.qb; ++t) {
-                const uint32_t slot = qs;
-                ok = mbar_wait_warp(bar(C::B_QFULL + slot), qph, w, 19);     // the LSEs are there
-                if (++qs == C::NQ) { qs = 0; qph ^= 1u; }
+                ok = arrived();
                 if (!ok) break;
+                const uint32_t slot = ls, buf = sc & 1u;
+                if (++ls == C::NL) { ls = 0; lph ^= 1u; }
                 if (none) {
-                    if (lane == 0) mbar_arrive(bar(C::B_QEMPTY + slot));
+                    if (lane == 0) mbar_arrive(bar(C::B_LEMPTY + slot));
                     continue;
                 }
-                const int buf = sc & 1u;
-                ok = mbar_wait_warp(bar(C::B_SFULL + 2 * x + buf), (sc >> 1) & 1u, w, 20);
-                if (!ok) break;
                 ++sc;
-                tc_fence_after();
-                const uint32_t tS = tbase + lane_off + C::col_s(x, buf);
-                const float4 *l4 = reinterpret_cast<const float4 *>(gbase + C::L_OFF) + slot * 32;
-                // columns [ca, cb) see this token
-                const int ca = min(max(r0 - t * R, 0), R) * a.group;
-                const int cb = min(max(r1 - t * R, 0), R) * a.group;
-                const bool part = __any_sync(0xffffffffu, ca != 0 || cb != box_rows);
-                float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
-                uint32_t sv[kN];
+                uint32_t v[kN];
 #pragma unroll
-                for (int c = 0; c < kN; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&sv[c]));
+                for (int c = 0; c < kN; c += 32)
+                    tmem_ld32(tbase + lane_off + C::col_s(x, 0) + 128u * buf + c,
+                              *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + 2 * x + buf));
-                if (part) {
+                if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + 2 * x + buf));   // the scores are read
+                // columns [ca, cb) see this token
+                const int ca = min(max(r0 - t * R, 0), R) * a.group;
+                const int cb = min(max(r1 - t * R, 0), R) * a.group;
+                if (__any_sync(0xffffffffu, ca != 0 || cb != box_rows)) {
                     // hidden columns: a score of -inf (what lies there may be anything)
 #pragma unroll
                     for (int c = 0; c < kN; ++c)
-                        if (c < ca || c >= cb) sv[c] = 0xff800000u;
+                        if (c < ca || c >= cb) v[c] = 0xff800000u;
                 }
+                const float4 *l4 = reinterpret_cast<const float4 *>(gbase + C::L_OFF) + slot * 32;
+                float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
 #pragma unroll
                 for (int c = 0; c < kN; c += 4) {
                     const float4 l = l4[c / 4];
-                    const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
+                    const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
                                                   c2, make_float2(l.x, l.y));
-                    const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])),
+                    const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
                                                   c2, make_float2(l.z, l.w));
                     e_a = __fadd2_rn(e_a, make_float2(ex2_approx(x01.x), ex2_approx(x01.y)));
                     e_b = __fadd2_rn(e_b, make_float2(ex2_approx(x23.x), ex2_approx(x23.y)));
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_QEMPTY + slot));
+                if (lane == 0) mbar_arrive(bar(C::B_LEMPTY + slot));
                 sum += (e_a.x + e_a.y) + (e_b.x + e_b.y);
             }
             if (!ok) break;
