@@ -1018,8 +1018,8 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
     a.keep = keep;
     a.first = first;
     a.recent = recent;
-    return fa::launch_paged_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
-                                                                                      : FA_ERR_CUDA;
+    return fa::launch_paged_evict(a, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_check_status(void *stream) {

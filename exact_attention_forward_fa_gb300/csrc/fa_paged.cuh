@@ -211,6 +211,6 @@ struct PagedEvictArgs {
     int B, H_kv, d, W, dst_W, ps_log2, n_pages, L;
     int keep, first, recent;
 };
-cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t stream);
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, int sm_count, cudaStream_t stream);
 
 }  // namespace fa

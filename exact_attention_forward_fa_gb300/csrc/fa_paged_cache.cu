@@ -67,12 +67,102 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Evict, first kernel: which tokens stay.  One CTA per (sequence, K/V head).
+// Evict, the rows.
+// ---------------------------------------------------------------------------
+// Cached tokens of sequence b (as far as the table and the scores go).
+__device__ __forceinline__ int evict_tokens(const PagedEvictArgs &a, int b) {
+    const long long cap = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
+    const int n0 = a.kv_len[b];
+    return n0 < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n0), cap));
+}
+__device__ __forceinline__ int evict_len(const PagedEvictArgs &a, int b) { return min(evict_tokens(a, b), a.keep); }
+
+// Row r of (b, h) in the fresh pages is the kept token's row, for rows first,
+// first + step, ... (V 16-byte vectors a row, one a thread; kMoveRows rows of K and
+// V in flight per thread).  Where a row lies takes two dependent loads, its token
+// and that token's page: those of the next rows are read while these are copied.
+constexpr int kMoveRows = 4;
+
+template <int D, int kThreads>
+__device__ __forceinline__ void move_rows(const PagedEvictArgs &a, int b, int h, int first, int step, int len) {
+    constexpr int V = D / 8, R = kThreads / V;
+    const int c = threadIdx.x % V, r0 = threadIdx.x / V;
+    const int *kept = a.kept + (static_cast<long long>(b) * a.H_kv + h) * a.keep;
+    const int mask = (1 << a.ps_log2) - 1;
+    uint4 *kp = reinterpret_cast<uint4 *>(a.k_pages), *vp = reinterpret_cast<uint4 *>(a.v_pages);
+    long long src[kMoveRows], dst[kMoveRows];             // in vectors; dst < 0: none
+    auto find = [&](int at) __attribute__((always_inline)) {
+        int j[kMoveRows];
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i) j[i] = at + r0 + i * R < len ? kept[at + r0 + i * R] : -1;
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i) {
+            const int r = at + r0 + i * R;
+            dst[i] = -1;
+            if (j[i] < 0) continue;
+            const int sp = paged_page(a.table + static_cast<long long>(b) * a.W, j[i], a.ps_log2, a.n_pages, a.status);
+            const int dp = paged_page(a.dst_table + static_cast<long long>(b) * a.dst_W, r, a.ps_log2, a.n_pages,
+                                      a.status);
+            if (sp < 0 || dp < 0) continue;
+            src[i] = static_cast<long long>(sp) * (a.page_stride / 8) +
+                     (static_cast<long long>(j[i] & mask) * a.H_kv + h) * V + c;
+            dst[i] = static_cast<long long>(dp) * (a.page_stride / 8) +
+                     (static_cast<long long>(r & mask) * a.H_kv + h) * V + c;
+        }
+    };
+    if (first < len) find(first);
+#pragma unroll 1
+    for (int at = first; at < len; at += step) {
+        uint4 kr[kMoveRows], vr[kMoveRows];
+        long long to[kMoveRows];
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i) {
+            to[i] = dst[i];
+            if (to[i] < 0) continue;
+            kr[i] = kp[src[i]];
+            vr[i] = vp[src[i]];
+        }
+        if (at + step < len) find(at + step);
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i) {
+            if (to[i] < 0) continue;
+            kp[to[i]] = kr[i];
+            vp[to[i]] = vr[i];
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) fa_paged_move_kernel(const PagedEvictArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");    // the kept positions
+    const int h = blockIdx.y, b = blockIdx.z;
+    constexpr int kRows = 256 / (D / 8) * kMoveRows;
+    move_rows<D, 256>(a, b, h, blockIdx.x * kRows, gridDim.x * kRows, evict_len(a, b));
+}
+
+// ---------------------------------------------------------------------------
+// Evict, which tokens stay.  One CTA per (sequence, K/V head).
 // Of n > keep cached tokens the first `first` and the last `recent` stay, and
 // of the others the keep - first - recent with the largest score; equal
-// scores go to the lower position, NaN ranks above +inf.  The k-th largest
-// score is found by a radix select over an order-preserving 32-bit key, 8
-// bits a pass; the kept positions are written in order.
+// scores go to the lower position, NaN ranks above +inf.
+//
+// The want-th largest score is searched over an order-preserving 32-bit key by
+// digits of 12 bits, from the first bit in which the keys differ, counted with
+// shared-memory atomics.  The digits are wide so that a warp's keys spread over
+// many bins: with 8 bits the first digit is little more than the exponent, and a
+// warp's 32 additions go to a few addresses, one after the other.  Up to
+// kSelStaged tokens the scores are read once and kept in shared memory; longer
+// caches are read again for each digit.
+//
+// What it takes is latency and issue slots, not bytes.  For sixteen caches of 1500
+// to 16384 tokens: 26 us reading the scores again for each digit, 56 us with bins
+// counted by ballots (six votes for 32 keys and five bits; a vote costs ~16 issue
+// cycles), 40 us with keys in registers and unrolled loops (its code comes from L2
+// once a launch), SELECT_US us as it is.
+//
+// The kept positions are written in order: every warp owns a run of 32-token
+// groups and counts its tokens that stay and its ties, a scan over the warps
+// gives where they go, ballots the places within a group.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t score_key(float x) {
     if (x != x) return 0xffffffffu;
@@ -80,24 +170,22 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024, kSelStaged = 24576;     // (96 KB: two CTAs per SM)
 
-__global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const PagedEvictArgs a) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_left;
+// staged: the n scores go to `held`.
+__device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const bool staged, float *held) {
+    __shared__ uint32_t hist[4096];                       // a digit's bins
+    __shared__ uint32_t s_and, s_or, s_digit, s_left;
     __shared__ int w_hi[32], w_eq[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.x, b = blockIdx.y;
-    const long long cap = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
-    const int n0 = a.kv_len[b];
-    const int n = n0 < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n0), cap));
-    if (n != n0 && tid == 0) report_bad_index(a.status, 3);
+    const int n = evict_tokens(a, b);
+    if (tid == 0 && n != a.kv_len[b]) report_bad_index(a.status, 3);
     const long long bh = static_cast<long long>(b) * a.H_kv + h;
     const float *sc = a.scores + bh * a.L;
     int *kept = a.kept + bh * a.keep;
     float *so = a.scores_out ? a.scores_out + bh * a.keep : nullptr;
-    const int len = min(n, a.keep);
-    if (h == 0 && tid == 0) a.new_len[b] = len;
+    if (h == 0 && tid == 0) a.new_len[b] = min(n, a.keep);
     if (n <= a.keep) {
         for (int j = tid; j < n; j += kSelThreads) {
             kept[j] = j;
@@ -107,140 +195,162 @@ __global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const Page
     }
     const int lo = a.first, hi = n - a.recent;            // the tokens that compete
     const uint32_t want = static_cast<uint32_t>(a.keep - a.first - a.recent);
-    if (tid == 0) { s_prefix = 0; s_left = want; }
-    // want = 0: a threshold above every key that competes
-    for (int shift = 24; want != 0 && shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t prefix = s_prefix;
-        const uint32_t above = shift == 24 ? 0u : (0xffffffffu << (shift + 8));
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            const uint32_t k = score_key(sc[j]);
-            if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l owns bins 255 - 8 l down to 248 - 8 l
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) { c[i] = hist[255 - 8 * lane - i]; sum += c[i]; }
-            uint32_t before = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += v;
-            }
-            before -= sum;                                // keys above this lane's bins
-            const uint32_t left = s_left;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (before < left && before + c[i] >= left) {
-                    s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - i) << shift);
-                    s_left = left - before;
-                }
-                before += c[i];
-            }
-        }
-        __syncthreads();
-    }
-    __syncthreads();
-    const uint32_t thr = s_prefix;                        // the want-th largest key
-    const uint32_t ties = want ? s_left : 0u;             // how many of its equals stay
     // every warp owns a run of whole 32-token groups
     const int groups = (n + 31) / 32, per = (groups + 31) / 32;
     const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
-    auto kind = [&](int j) __attribute__((always_inline)) -> int {   // 2 stays, 1 tie, 0 goes
+    auto score = [&](int j) __attribute__((always_inline)) -> float { return staged ? held[j] : sc[j]; };
+    // the key of token j: 0 where none competes (a real key is never 0)
+    auto key_of = [&](int j) __attribute__((always_inline)) -> uint32_t {
+        return j >= lo && j < hi ? score_key(score(j)) : 0u;
+    };
+    if (staged) {
+#pragma unroll 8
+        for (int j = g0 * 32 + lane; j < min(n, g1 * 32); j += 32) held[j] = sc[j];   // (read by this thread only)
+    }
+    uint32_t all = ~0u, any = 0u;
+#pragma unroll 4
+    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
+        const uint32_t k = key_of(j);
+        all &= k != 0u ? k : ~0u;
+        any |= k;
+    }
+    if (tid == 0) { s_and = ~0u; s_or = 0u; }
+    __syncthreads();
+    all = __reduce_and_sync(0xffffffffu, all);
+    any = __reduce_or_sync(0xffffffffu, any);
+    if (lane == 0) { atomicAnd(&s_and, all); atomicOr(&s_or, any); }
+    __syncthreads();
+    int top = 32 - __clz(s_and ^ s_or);                   // bits to decide; the others are common
+    uint32_t prefix = top == 32 ? 0u : (s_or >> top) << top, left = want;
+#pragma unroll 1
+    while (want != 0 && top > 0) {
+        const int low = max(top - 12, 0), bins = 1 << (top - low);
+        for (int i = tid; i < 4096; i += kSelThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
+            const uint32_t k = key_of(j);
+            if (k != 0u && (top == 32 || ((k ^ prefix) >> top) == 0u)) atomicAdd(&hist[(k >> low) & (bins - 1)], 1u);
+        }
+        __syncthreads();
+        // thread t sums bins 4095 - 4 t down to 4092 - 4 t; the digit is the bin
+        // that holds the left-th key from the top
+        uint32_t c[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { c[i] = hist[4095 - 4 * tid - i]; sum += c[i]; }
+        uint32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) w_hi[warp] = static_cast<int>(incl);
+        __syncthreads();
+        uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? w_hi[lane] : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (above < left && above + c[i] >= left) {
+                s_digit = static_cast<uint32_t>(4095 - 4 * tid - i);
+                s_left = left - above;
+            }
+            above += c[i];
+        }
+        __syncthreads();
+        left = s_left;
+        prefix |= s_digit << low;
+        top = low;
+    }
+    const uint32_t thr = prefix;                          // the want-th largest key
+    const uint32_t ties = want ? left : 0u;               // how many of its equals stay
+    auto rank = [&](int j, uint32_t k) __attribute__((always_inline)) -> int {   // 2 stays, 1 tie, 0 goes
         if (j >= n) return 0;
         if (j < lo || j >= hi) return 2;
         if (want == 0) return 0;
-        const uint32_t k = score_key(sc[j]);
         return k > thr ? 2 : k == thr ? 1 : 0;
     };
     int c2 = 0, c1 = 0;
-    for (int g = g0; g < g1; ++g) {
-        const int k = kind(g * 32 + lane);
-        c2 += __popc(__ballot_sync(0xffffffffu, k == 2));
-        c1 += __popc(__ballot_sync(0xffffffffu, k == 1));
+#pragma unroll 4
+    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
+        const int r = rank(j, key_of(j));
+        c2 += r == 2;
+        c1 += r == 1;
     }
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    __syncthreads();                                      // (the scan's sums are read)
     if (lane == 0) { w_hi[warp] = c2; w_eq[warp] = c1; }
     __syncthreads();
-    int at = 0, eq = 0;                                   // stays and ties before this warp
-    for (int w = 0; w < warp; ++w) { at += w_hi[w]; eq += w_eq[w]; }
-    at += min(eq, static_cast<int>(ties));
+    // stays and ties before this warp
+    const int before2 = __reduce_add_sync(0xffffffffu, lane < warp ? w_hi[lane] : 0);
+    int eq = __reduce_add_sync(0xffffffffu, lane < warp ? w_eq[lane] : 0);
+    int at = before2 + min(eq, static_cast<int>(ties));
     const unsigned below = (1u << lane) - 1u;
-    for (int g = g0; g < g1; ++g) {
-        const int j = g * 32 + lane;
-        const int k = kind(j);
-        const unsigned m1 = __ballot_sync(0xffffffffu, k == 1);
-        const bool stay = k == 2 || (k == 1 && eq + __popc(m1 & below) < static_cast<int>(ties));
+#pragma unroll 2
+    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
+        const int r = rank(j, key_of(j));
+        const unsigned m1 = __ballot_sync(0xffffffffu, r == 1);
+        const bool stay = r == 2 || (r == 1 && eq + __popc(m1 & below) < static_cast<int>(ties));
         const unsigned m = __ballot_sync(0xffffffffu, stay);
         if (stay) {
-            const int r = at + __popc(m & below);
-            kept[r] = j;
-            if (so) so[r] = sc[j];
+            kept[at + __popc(m & below)] = j;
+            if (so) so[at + __popc(m & below)] = score(j);
         }
         at += __popc(m);
         eq += __popc(m1);
     }
 }
 
-// Second kernel: row r of (b, h) in the fresh pages is the kept token's row.
-// 16-byte vectors, one per thread and row; kRows rows per thread in flight.
-constexpr int kMoveRows = 4;
-
+// D != 0: the CTA then moves its own rows.
 template <int D>
-__global__ void __launch_bounds__(256) fa_paged_move_kernel(const PagedEvictArgs a) {
-    constexpr int V = D / 8;                              // vectors of a row
-    constexpr int R = 256 / V;                            // rows per pass of the CTA
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int n0 = a.kv_len[b];
-    const long long cap = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
-    const int len = n0 < 0 ? 0 : static_cast<int>(min(min(static_cast<long long>(n0), cap),
-                                                      static_cast<long long>(a.keep)));
-    const int c = threadIdx.x % V, r0 = blockIdx.x * (R * kMoveRows) + threadIdx.x / V;
-    const int *kept = a.kept + (static_cast<long long>(b) * a.H_kv + h) * a.keep;
-    const int mask = (1 << a.ps_log2) - 1;
-    const uint4 *ks = reinterpret_cast<const uint4 *>(a.k_pages);
-    const uint4 *vs = reinterpret_cast<const uint4 *>(a.v_pages);
-    uint4 kr[kMoveRows], vr[kMoveRows];
-    long long dst[kMoveRows];
-#pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-        const int r = r0 + i * R;
-        dst[i] = -1;
-        if (r >= len) continue;
-        const int j = kept[r];
-        const int sp = paged_page(a.table + static_cast<long long>(b) * a.W, j, a.ps_log2, a.n_pages, a.status);
-        const int dp = paged_page(a.dst_table + static_cast<long long>(b) * a.dst_W, r, a.ps_log2, a.n_pages,
-                                  a.status);
-        if (sp < 0 || dp < 0) continue;
-        const long long src = static_cast<long long>(sp) * (a.page_stride / 8) +
-                              (static_cast<long long>(j & mask) * a.H_kv + h) * V + c;
-        dst[i] = static_cast<long long>(dp) * (a.page_stride / 8) +
-                 (static_cast<long long>(r & mask) * a.H_kv + h) * V + c;
-        kr[i] = ks[src];
-        vr[i] = vs[src];
-    }
-#pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-        if (dst[i] < 0) continue;
-        reinterpret_cast<uint4 *>(a.k_pages)[dst[i]] = kr[i];
-        reinterpret_cast<uint4 *>(a.v_pages)[dst[i]] = vr[i];
+__global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const PagedEvictArgs a, const bool staged) {
+    extern __shared__ float held[];
+    select_tokens(a, staged, held);
+    if constexpr (D != 0) {
+        __syncthreads();                                  // the kept positions are written
+        move_rows<D, kSelThreads>(a, blockIdx.y, blockIdx.x, 0, kSelThreads / (D / 8) * kMoveRows,
+                                  evict_len(a, blockIdx.y));
     }
 }
 
-cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t stream) {
-    fa_paged_select_kernel<<<dim3(a.H_kv, a.B), kSelThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+template <int D>
+static cudaError_t launch_select(const PagedEvictArgs &a, cudaStream_t stream) {
+    static unsigned long long configured = 0ull;          // bit per device id (< 64)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(fa_paged_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelStaged * 4);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&configured, bit, __ATOMIC_ACQ_REL);
+    }
+    const long long most = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
+    const bool staged = most <= kSelStaged;
+    fa_paged_select_kernel<D><<<dim3(a.H_kv, a.B), kSelThreads, staged ? most * 4 : 0, stream>>>(a, staged);
+    return cudaGetLastError();
+}
+
+// With a (sequence, K/V head) for most of the SMs the CTA that selects also
+// moves: short caches move while long ones still select.  With few, moving is
+// spread over the whole device by a kernel of its own, whose CTAs come up while the
+// last selections run.
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, int sm_count, cudaStream_t stream) {
+    if (static_cast<long long>(a.B) * a.H_kv * 3 >= 2ll * sm_count)
+        return a.d == 64 ? launch_select<64>(a, stream) : launch_select<128>(a, stream);
+    const cudaError_t e = launch_select<0>(a, stream);
     if (e != cudaSuccess) return e;
     const int rows = (256 / (a.d / 8)) * kMoveRows;
-    const dim3 grid((a.keep + rows - 1) / rows, a.H_kv, a.B);
-    if (a.d == 64)
-        fa_paged_move_kernel<64><<<grid, 256, 0, stream>>>(a);
-    else
-        fa_paged_move_kernel<128><<<grid, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.keep + rows - 1) / rows, a.H_kv, a.B);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return a.d == 64 ? cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<64>, a)
+                     : cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<128>, a);
 }
 
 }  // namespace fa
