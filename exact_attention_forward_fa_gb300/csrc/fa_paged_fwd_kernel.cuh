@@ -187,6 +187,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll 1
             for (int i = 0; i < ns + lag && ok; ++i) {
                 const int iv = i - lag;
+                bool v_here = false, k_here = false;       // (the second tile need not look again)
 #pragma unroll 1
                 for (int x = one ? i & 1 : 0; x < 2; ++x) {
                     const int s0 = one ? x : x ? 0 : s0l;
@@ -194,7 +195,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (iv >= s0) {
                         const uint32_t d_o = tbase + (x ? C::col_o(1) : C::col_o(0));
                         const bool begin = iv == s0;
-                        ok = mbar_wait_warp(bar(C::B_KVFULL + vs), vph, w, 10);
+                        if (!v_here) ok = mbar_wait_warp(bar(C::B_KVFULL + vs), vph, w, 10);
+                        v_here = true;
                         if (ok && begin) ok = mbar_wait_warp(bar(C::B_OEMPTY + x), ((un >> x) & 1u) ^ 1u, w, 11);
                         if (ok) ok = mbar_wait_warp(bar(C::B_PFULL + x), (pp >> x) & 1u, w, 12);
                         if (!ok) break;
@@ -212,7 +214,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                     if (i < ns && i >= s0) {
                         const uint32_t qx = one || x == 0 ? qs : q1, qxp = one || x == 0 ? qph : q1ph;
-                        ok = mbar_wait_warp(bar(C::B_KVFULL + ks), kph, w, 13);
+                        if (!k_here) ok = mbar_wait_warp(bar(C::B_KVFULL + ks), kph, w, 13);
+                        k_here = true;
                         if (ok && i == s0) ok = mbar_wait_warp(bar(C::B_QFULL + qx), qxp, w, 14);
                         if (!ok) break;
                         tc_fence_after();

@@ -35,7 +35,7 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     // run; it waits for their results itself (griddepcontrol.wait).
     const int rows = (kN ? 1 : 2) * L.R * L.a.group;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(L.grid, rows < 16 ? rows : 16);
+    cfg.gridDim = dim3(L.grid, rows < 8 ? rows : 8);
     cfg.blockDim = dim3(256);
     cfg.stream = L.stream;
     cudaLaunchAttribute at[1];
@@ -43,7 +43,7 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16>, L.a, L.w, L.R);
+    return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16, (kN != 0)>, L.a, L.w, L.R);
 }
 
 // Up to 32 rows a tile: few rows against each K/V tile, bound by HBM.
