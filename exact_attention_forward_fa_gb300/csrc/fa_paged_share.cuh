@@ -97,8 +97,10 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, int
         if (b < a.B) s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
         if (s.bad && blockIdx.x == 0) report_bad_index(a.status, 1);
         const int np = paged_units(s, U);
-        if (np == 1) mine += paged_unit_steps(s.m, s.n, 0, U, a.wl, a.wr, a.first);
-        for (unsigned big = __ballot_sync(0xffffffffu, np > 1); big != 0; big &= big - 1) {
+        // a few units by the thread itself, many by its warp
+        if (np <= 8)
+            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s.m, s.n, p, U, a.wl, a.wr, a.first);
+        for (unsigned big = __ballot_sync(0xffffffffu, np > 8); big != 0; big &= big - 1) {
             const int src = __ffs(big) - 1;
             PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
             const long long sum = paged_seq_steps_warp(t, U, a);
