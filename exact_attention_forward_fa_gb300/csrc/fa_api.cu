@@ -916,10 +916,9 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     // CTAs: one per SM, fewer when even the longest cache has not a step for
     // each (two steps a share made a short conversation's call 14.3 us instead of
     // 11: a share then holds the end of one unit and the start of the next).
-    L.q_min = 1;
     const uint64_t units = static_cast<uint64_t>(B) + static_cast<uint64_t>(total_q) / (2 * L.R);
     const uint64_t tiles = ((static_cast<uint64_t>(table_width) << a.ps_log2) + 127) / 128;
-    const uint64_t share = (units * tiles + L.q_min - 1) / L.q_min;     // shares of one K/V head
+    const uint64_t share = units * tiles;              // shares of one K/V head
     const uint64_t sm = static_cast<uint64_t>(dev->sm_count);
     L.grid = static_cast<int>(share >= sm ? sm : share * H_kv < sm ? share * H_kv : sm);
     L.w.desc = static_cast<int *>(workspace);

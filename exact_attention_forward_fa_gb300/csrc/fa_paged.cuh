@@ -179,7 +179,6 @@ struct PagedFwdLaunch {
     PagedArgs a;
     PagedWork w;
     int R;              // positions per Q tile
-    int q_min;          // fewest steps of a share
     int grid, d;
     bool bf16;
     cudaStream_t stream;

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedArgs a
         else *reinterpret_cast<uint2 *>(dst) = make_uint2(pk[0], pk[1]);
         if (a.lse != nullptr && lane == 0)
             a.lse[static_cast<size_t>(qh) * a.T + tok] =
-                L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+                L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
     };
     auto load = [&](size_t part, float (&v)[E]) __attribute__((always_inline)) {
         const float *src = wk.o + part * D + lane * E;
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedArgs a
                                         pack2<kBF16>(acc[f].z * inv, acc[f].w * inv));
             if (a.lse != nullptr && sub == 0)
                 a.lse[static_cast<size_t>(qh) * a.T + tok] =
-                    L > 0.f ? (M + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+                    L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
         }
         return;
     }

@@ -93,7 +93,7 @@ template <int D, bool kBF16>
 __global__ void __launch_bounds__(384, 1)
 fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
-                    const int R, const int q_min) {
+                    const int R) {
     using C = PagedCfg<D, kBF16>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -119,7 +119,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     // (the scratch lies in the K/V ring, which no copy uses yet)
     tc_fence_before();
-    const PagedShare share = paged_share<C::NTHREADS>(a, 2 * R, q_min, gbase + C::KV_OFF);
+    const PagedShare share = paged_share<C::NTHREADS>(a, 2 * R, gbase + C::KV_OFF);
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
 
@@ -423,7 +423,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             kv += 2 * ns;
             // ---- this group's normaliser and LSE (log2 units) ----
             const bool some = s0 < ns;
-            const bool live = some && le > 0.f && lr > 0.f;
+            const bool live = some && !(le <= 0.f);        // (a NaN that the row sees stays one)
             float inv = live ? 1.f / lr : 0.f;
             float lse2 = live ? r + log2f(le) : -INFINITY;
             const bool joined = one && ns >= 2;            // group H has a share of this tile
@@ -453,7 +453,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (!ok) break;
                 const float l_h = xch[row];
                 const float m = fmaxf(lse2, l_h);
-                if (m != -INFINITY) {
+                if (lse2 != -INFINITY || l_h != -INFINITY) {
                     const float w_l = ex2_approx(lse2 - m), w_h = ex2_approx(l_h - m);
                     const float n2 = 1.f / (w_l + w_h);
                     inv *= w_l * n2;

@@ -14,7 +14,7 @@ namespace fa {
 template <int D, bool kBF16, int kN>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     using C = std::conditional_t<kN != 0, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
-    void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedArgs, PagedWork, int, int);
+    void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedArgs, PagedWork, int);
     if constexpr (kN != 0) kern = fa_paged_token_kernel<D, kBF16, kN>;
     else kern = fa_paged_fwd_kernel<D, kBF16>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
@@ -28,7 +28,7 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, bit, __ATOMIC_ACQ_REL);
     }
-    kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.v, L.a, L.w, L.R, L.q_min);
+    kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.v, L.a, L.w, L.R);
     e = cudaGetLastError();
     if (e != cudaSuccess || L.grid == 1) return e;  // one share: nothing is cut
     // The joining kernel's CTAs are brought up while the attention's last ones

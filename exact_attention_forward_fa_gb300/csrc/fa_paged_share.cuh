@@ -82,7 +82,7 @@ constexpr uint32_t kShareScratch = 16 * 8 + 48;
 // By the whole block (kThreads of them); ends with a barrier after which the
 // scratch is free.
 template <int kThreads>
-__device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, int q_min, uint8_t *scratch) {
+__device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, uint8_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long *scan = reinterpret_cast<long long *>(scratch);          // [16]
     long long *found = scan + 16;                                      // at, per
@@ -128,7 +128,6 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, int
     const unsigned G = gridDim.x;
     sh.quota = (total >> 31) == 0 ? static_cast<long long>((static_cast<unsigned>(total) + G - 1) / G)
                                   : (total + G - 1) / G;
-    sh.quota = max(sh.quota, static_cast<long long>(q_min));
     sh.w0 = blockIdx.x * sh.quota;
     sh.w1 = min(total, sh.w0 + sh.quota);
     const long long start = before + incl - mine;

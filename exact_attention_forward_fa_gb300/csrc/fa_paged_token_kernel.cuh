@@ -128,7 +128,7 @@ template <int D, bool kBF16, int kN>
 __global__ void __launch_bounds__(416, 1)
 fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
-                      const int R, const int q_min) {
+                      const int R) {
     using C = TokenCfg<D, kBF16>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -152,7 +152,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tma_prefetch_desc(&tm_v);
     }
     tc_fence_before();
-    const PagedShare share = paged_share<C::NTHREADS>(a, R, q_min, gbase + C::KV_OFF);
+    const PagedShare share = paged_share<C::NTHREADS>(a, R, gbase + C::KV_OFF);
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
 
@@ -447,7 +447,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (gwarp == 0 && some && lane < nr) {
                 const float e = (sums[lane] + sums[kN + lane]) + (sums[2 * kN + lane] + sums[3 * kN + lane]);
                 const float q = (sums[4 * kN + lane] + sums[5 * kN + lane]) + (sums[6 * kN + lane] + sums[7 * kN + lane]);
-                if (e > 0.f && q > 0.f) {
+                if (!(e <= 0.f)) {                                           // (a NaN that the row sees stays one)
                     lse2 = ref[lane] + log2f(e);
                     inv = 1.f / q;
                 }
@@ -478,7 +478,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     inv1 = xch[32 + lane];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_XEMPTY));
-                    if (m != -INFINITY) {
+                    if (lse2 != -INFINITY || l1 != -INFINITY) {
                         const float w0 = ex2_approx(lse2 - m), w1 = ex2_approx(l1 - m), k = 1.f / (w0 + w1);
                         inv *= w0 * k;
                         inv1 *= w1 * k;

@@ -409,7 +409,9 @@ fa_status fa_paged_append(const void *k, const void *v, void *k_pages, void *v_p
  *     j >= p - window_left  or  j < first   (window_left >= 0; -1: no bound):
  * (-1, 0) is causal, (-1, -1) no mask, and with a left bound the first
  * `first` tokens of the sequence stay visible beside the sliding window.  A
- * row that sees no key gives O = 0, LSE = -inf.
+ * row that sees no key gives O = 0, LSE = -inf.  A NaN in q or in a key that a
+ * row sees makes its O and LSE NaN.  An infinity or NaN in a value reaches, as
+ * 0 times it, every row of the K/V head whose tile of rows sees that token.
  *   q    : device, total_q rows of [H][d], q_stride elements from row to row
  *          (>= H * d, a multiple of 8), 16-byte aligned.
  *   o    : device, [total_q][H][d], 16-byte aligned (written).

@@ -202,6 +202,39 @@ def test_attention_alpha(gpu_lib, alpha):
     check_attention(c, o, lse, alpha=alpha)
 
 
+@pytest.mark.parametrize("q_len,H", [([1, 1], 8), ([7, 1], 8), ([200, 90], 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_stays_with_the_rows_that_see_it(gpu_lib, q_len, H, d):
+    # one key of sequence 0 and K/V head 1, in the middle of a long key range
+    # (which is cut and joined), and one that only the later new tokens see
+    c = Cache(q_len, [9000, 500], H, 2, d, 16, seed=d)
+    o, lse = attend(gpu_lib, c)
+    m, g = q_len[0], H // 2
+    for pos in {4321, 9000 - m + m // 2}:
+        key = c.K[0][pos:pos + 1].to(DT[c.dt])
+        bad = key.clone()
+        bad[0, 1, 5] = math.nan
+        c.put(0, pos, bad, c.V[0][pos:pos + 1].to(DT[c.dt]))
+        o2, lse2 = attend(gpu_lib, c)
+        c.put(0, pos, key, c.V[0][pos:pos + 1].to(DT[c.dt]))
+        sees = torch.zeros(c.T, H, dtype=torch.bool, device="cuda")
+        sees[max(0, pos - (9000 - m)):m, g:] = True
+        assert torch.isnan(o2[sees]).all() and torch.isnan(lse2.t()[sees]).all()
+        assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2.t()[~sees], lse.t()[~sees])
+
+
+@pytest.mark.parametrize("q,d", [(1, 128), (4, 128), (1, 64), (70, 128)])
+def test_pieces_of_many_steps_repeat_their_bits(gpu_lib, q, d):
+    # every ring of tiles is passed many times, pieces of odd and even lengths
+    lens = [2000 + 137 * i for i in range(24)]
+    c = Cache([q] * 24, lens, 8, 2, d, 64, seed=q)
+    o, lse = attend(gpu_lib, c)
+    check_attention(c, o, lse)
+    for _ in range(20):
+        o2, lse2 = attend(gpu_lib, c)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_max_q_is_only_a_hint(gpu_lib):
     c = Cache([150, 1], [150, 300], 8, 2, 128, 16, seed=2)
     for hint in (1, 3, 1000):
@@ -482,6 +515,29 @@ def test_two_streams_at_once(gpu_lib):
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_graphs_with_workspaces_of_their_own(gpu_lib):
+    # two captured calls, each with what its capture took, replayed side by side
+    fa = gpu_lib
+    cs = [Cache([1, 1], [15000, 700 + i], 8, 2, 128, 16, seed=i) for i in range(2)]
+    want = [attend(fa, c) for c in cs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in cs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fa.attention_paged(c.q, *c.args(), max_q=1))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_check_status() == fa.FA_OK
+    for (o, lse), (o2, lse2) in zip(want, outs):
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_graph_replays_with_other_lengths(gpu_lib):
