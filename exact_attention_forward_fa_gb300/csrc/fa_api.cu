@@ -62,6 +62,13 @@ fa_status get_device(DeviceInfo **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return FA_ERR_UNSUPPORTED;
+    // cuTensorMapEncodeTiled is a driver call and needs a current context, which a
+    // host thread that has made no runtime call with device work yet lacks.
+    static thread_local int bound = -1;
+    if (bound != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
+        bound = dev;
+    }
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceInfo &d = g_dev[dev];
     if (!d.ready) {

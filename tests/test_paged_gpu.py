@@ -19,6 +19,7 @@ Tolerances, per element, with u the half step of the 16-bit type (2^-8 bf16,
   there, 2^-23 relative.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -515,6 +516,63 @@ def test_two_streams_at_once(gpu_lib):
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_threads_at_once(gpu_lib):
+    # on the default stream (whose calls share a workspace) and on streams of
+    # the threads' own
+    cs = [Cache([1, 3], [6000 + 500 * i, 900], 8, 2, 64, 16, seed=i) for i in range(4)]
+    want = [attend(gpu_lib, c) for c in cs]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in cs], []
+
+    def work(i, own):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream() if own else torch.cuda.default_stream()):
+                for _ in range(25):
+                    got[i].append(gpu_lib.attention_paged(cs[i].q, *cs[i].args(), max_q=3))
+        except Exception as e:          # noqa: BLE001 (reported by the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i, i == 3)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and gpu_lib.fa_check_status() == gpu_lib.FA_OK
+    for (o, lse), outs in zip(want, got):
+        assert len(outs) == 25
+        for o2, lse2 in outs:
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_a_threads_first_call(gpu_lib):
+    # a thread that has not used the device yet, outputs given: nothing but the
+    # call itself makes the device's context current there
+    c = Cache([1], [300], 4, 2, 64, 16)
+    o, lse = attend(gpu_lib, c)
+    o2, lse2, ws = torch.empty_like(o), torch.empty_like(lse), gpu_lib.paged_workspace(64)
+    old = torch.zeros(1, 2, 300, device="cuda")
+    a = gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], max_q=1, scores=old)
+    a2 = torch.empty_like(a)
+    torch.cuda.synchronize()
+    for call in (lambda: gpu_lib.attention_paged(c.q, *c.args(), max_q=1, out=o2, lse=lse2, workspace=ws),
+                 lambda: gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], max_q=1, scores=old, out=a2)):
+        errors = []
+
+        def work():
+            try:
+                call()
+            except Exception as e:      # noqa: BLE001 (reported by the test's own thread)
+                errors.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        assert not errors
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(a, a2)
 
 
 def test_graphs_with_workspaces_of_their_own(gpu_lib):
