@@ -46,6 +46,8 @@ struct ScoresCfg {
     static constexpr int NL = 3;                                        // and their LSEs (held longer)
     static constexpr int NKX = NK / 2;                                  // slots of a group's K ring
     static constexpr bool kTwo = kN == 32;                              // a K producer for each group
+    static constexpr bool kHeld = kN == 128;                            // K tiles held in TMEM
+    static constexpr int NS = kHeld ? 3 : 4;                            // S buffers
     static constexpr int NTHREADS = kTwo ? 416 : 384;
     static constexpr uint32_t REGS_LOW = 96, REGS_HIGH = 200;
     static constexpr int RING = 4;
@@ -55,19 +57,19 @@ struct ScoresCfg {
     static constexpr uint32_t RING_OFF = L_OFF + NL * 128 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 32;
     static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_QFULL = 2 * NK, B_QEMPTY = B_QFULL + NQ,
-                         B_LFULL = B_QEMPTY + NQ, B_LEMPTY = B_LFULL + NL, B_SFULL = B_LEMPTY + NL, B_SEMPTY = B_SFULL + 4, B_MMADONE = B_SEMPTY + 4,
+                         B_LFULL = B_QEMPTY + NQ, B_LEMPTY = B_LFULL + NL, B_SFULL = B_LEMPTY + NL, B_SEMPTY = B_SFULL + NS, B_TFULL = B_SEMPTY + NS, B_MMADONE = B_TFULL + 2,
                          B_UNIT = B_MMADONE + 1, B_FREE = B_UNIT + RING, NBAR = B_FREE + RING;
-    // Arrivals that complete a phase: LSEs read by the 8 group warps, S read by a
-    // group's, units taken by the producers, MMA issuer and groups.
+    // Arrivals that complete a phase: LSEs read by the 8 group warps, S read and K
+    // moved to TMEM by a group's, units taken by the producers, MMA issuer and groups.
     __device__ static uint32_t arrivals(int i) {
-        return i >= B_LEMPTY && i < B_SFULL ? 8u : i >= B_SEMPTY && i < B_MMADONE ? 4u
+        return (kHeld && i >= B_KEMPTY && i < B_QFULL) ? 4u : i >= B_LEMPTY && i < B_SFULL ? 8u : i >= B_SEMPTY && i < B_MMADONE ? 4u
                : i >= B_FREE ? (kTwo ? 12u : 11u) : 1u;
     }
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
     static constexpr uint32_t TMEM_COLS = 512;
-    __host__ __device__ static constexpr uint32_t col_s(int x, int buf) { return 256u * x + 128u * buf; }
+    static constexpr uint32_t COL_S = kHeld ? 128u : 0u;                // S buffers (K tile x: column 64 x)
 };
 
 struct __align__(16) ScoresUnit {
@@ -328,7 +330,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         WaitCtx w{abort_flag, a.status, kRoleMma};
         auto uniform = [](int v) __attribute__((always_inline)) -> int { return __shfl_sync(0xffffffffu, v, 0); };
         uint32_t ks = 0, kph = 0, k1 = C::NKX, k1ph = 0, qs = 0, qph = 0, ui = 0;   // slots and their phases
-        uint32_t sc = 0, sph = 0;                          // bit x: group x's S buffer, its phase
+        uint32_t sb = 0, sph = 0, tph = 0;                 // S buffer(s), their phases, bit x: phase of K tile x in TMEM
         bool ok = true;
         ScoresUnit u;
         while (ok && take(ui, w, 32, u)) {
@@ -339,35 +341,51 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
 #pragma unroll 1
             for (int t = 0; t < tiles && ok; ++t) {
                 ok = mbar_wait_warp(bar(C::B_QFULL + qs), qph, w, 14);
+                const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::Q_BYTES, 16u, 1024u);
 #pragma unroll 1
-                for (int x = 0; x < nk && ok; ++x) {
-                    const uint32_t slot = x ? k1 : ks, buf = (sc >> x) & 1u, bx = 2 * x + buf;
-                    if (t == 0) ok = mbar_wait_warp(bar(C::B_KFULL + slot), x ? k1ph : kph, w, 13);
-                    if (ok) ok = mbar_wait_warp(bar(C::B_SEMPTY + bx), ((sph >> bx) & 1u) ^ 1u, w, 11);
+                for (int x = 0; x < (C::kHeld ? 2 : nk) && ok; ++x) {
+                    // held: the buffers in turn, and group 1's turn comes even if it has no tile
+                    const uint32_t b = C::kHeld ? sb : 2 * x + ((sb >> x) & 1u);
+                    if (t == 0 && x < nk)
+                        ok = C::kHeld ? mbar_wait_warp(bar(C::B_TFULL + x), (tph >> x) & 1u, w, 13)
+                                      : mbar_wait_warp(bar(C::B_KFULL + (x ? k1 : ks)), x ? k1ph : kph, w, 13);
+                    if (ok) ok = mbar_wait_warp(bar(C::B_SEMPTY + b), ((sph >> b) & 1u) ^ 1u, w, 11);
                     if (!ok) break;
-                    sph ^= 1u << bx;
-                    sc ^= 1u << x;
+                    sph ^= 1u << b;
+                    if (!C::kHeld) sb ^= 1u << x;
+                    else if (++sb == C::NS) sb = 0;
                     tc_fence_after();
-                    const uint64_t kd = smem_desc_sw128(base + C::K_OFF + slot * C::TILE_BYTES, 16u, 1024u);
-                    const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::Q_BYTES, 16u, 1024u);
-                    const uint32_t d_s = tbase + 256u * x + 128u * buf;
+                    const uint32_t d_s = tbase + C::COL_S + 128u * b;
+                    if constexpr (C::kHeld) {
+                        if (x < nk) {
+                            const uint32_t tK = tbase + 64u * x;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t ko = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
-                        const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
-                        mma_ss_f16_elect(d_s, kd + ko, qd + qo, idesc, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
+                                mma_ts_f16_elect(d_s, tK + kk * 8u, qd + qo, idesc, kk > 0 ? 1u : 0u);
+                            }
+                        }
+                    } else {
+                        const uint64_t kd = smem_desc_sw128(base + C::K_OFF + (x ? k1 : ks) * C::TILE_BYTES, 16u, 1024u);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t ko = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                            const uint32_t qo = ((kk >> 2) * C::Q_CHUNK + (kk & 3) * 32u) >> 4;
+                            mma_ss_f16_elect(d_s, kd + ko, qd + qo, idesc, kk > 0 ? 1u : 0u);
+                        }
                     }
-                    mma_commit_elect(bar(C::B_SFULL + bx));
+                    mma_commit_elect(bar(C::B_SFULL + b));
                 }
                 if (!ok) break;
                 mma_commit_elect(bar(C::B_QEMPTY + qs));
                 if (++qs == C::NQ) { qs = 0; qph ^= 1u; }
             }
             if (!ok) break;
-            mma_commit_elect(bar(C::B_KEMPTY + ks));
+            tph ^= nk == 2 ? 3u : 1u;
+            if (!C::kHeld) mma_commit_elect(bar(C::B_KEMPTY + ks));
             if (++ks == C::NKX) { ks = 0; kph ^= 1u; }
             if (nk == 2) {
-                mma_commit_elect(bar(C::B_KEMPTY + k1));
+                if (!C::kHeld) mma_commit_elect(bar(C::B_KEMPTY + k1));
                 if (++k1 == C::NK) { k1 = C::NKX; k1ph ^= 1u; }
             }
         }
@@ -383,7 +401,8 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         WaitCtx w{abort_flag, a.status, x ? kRoleSoftmax1 : kRoleSoftmax0};
         const float sl2 = a.scale_log2;
         const float2 c2 = make_float2(sl2, sl2);
-        uint32_t ui = 0, sc = 0, ls = 0, lph = 0;          // units, S tiles, LSE slot and its phase
+        uint32_t ui = 0, ls = 0, lph = 0;                  // units; LSE slot and its phase
+        uint32_t sb = C::kHeld ? x : 2 * x, sph = 0, kc = 0;   // S buffer and its phase; K tiles
         bool ok = true;
         ScoresUnit u;
         while (ok && take(ui, w, 24, u)) {
@@ -402,31 +421,62 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             // the next Q tile's LSEs and (if the group has a tile) scores are there
             auto arrived = [&]() __attribute__((always_inline)) -> bool {
                 if (!mbar_wait_warp(bar(C::B_LFULL + ls), lph, w, 19)) return false;
-                if (none) return true;
-                if (!mbar_wait_warp(bar(C::B_SFULL + 2 * x + (sc & 1u)), (sc >> 1) & 1u, w, 20)) return false;
+                if (none && !C::kHeld) return true;
+                if (!mbar_wait_warp(bar(C::B_SFULL + sb), sph, w, 20)) return false;
                 tc_fence_after();
                 return true;
             };
+            if (C::kHeld && !none && u.qa < u.qb) {
+                // this token's key into TMEM (every product with the group's last one
+                // is complete: its last scores are read)
+                const uint32_t ks = x * C::NKX + kc % C::NKX;
+                ok = mbar_wait_warp(bar(C::B_KFULL + ks), (kc / C::NKX) & 1u, w, 18);
+                if (!ok) break;
+                ++kc;
+                const uint8_t *kr = gbase + C::K_OFF + ks * C::TILE_BYTES + row * 128;
+#pragma unroll
+                for (int ch = 0; ch < C::NCH; ++ch) {
+                    uint32_t kw[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 v4 = *reinterpret_cast<const uint4 *>(kr + ch * C::CHUNK_BYTES + ((q ^ (row & 7)) << 4));
+                        kw[4 * q] = v4.x; kw[4 * q + 1] = v4.y; kw[4 * q + 2] = v4.z; kw[4 * q + 3] = v4.w;
+                    }
+                    tmem_st32(tbase + lane_off + 64u * x + 32u * ch, kw);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_KEMPTY + ks));
+                    mbar_arrive(bar(C::B_TFULL + x));
+                }
+            }
 #pragma unroll 1
             for (int t = u.qa; t < u.qb; ++t) {
                 ok = arrived();
                 if (!ok) break;
-                const uint32_t slot = ls, buf = sc & 1u;
+                const uint32_t slot = ls, buf = sb;
                 if (++ls == C::NL) { ls = 0; lph ^= 1u; }
+                if (C::kHeld || !none) {
+                    if (C::kHeld) sb += 2;
+                    else sb ^= 1u;
+                    if (C::kHeld ? sb >= C::NS : (sb & 1u) == 0) { if (C::kHeld) sb -= C::NS; sph ^= 1u; }
+                }
                 if (none) {
                     if (lane == 0) mbar_arrive(bar(C::B_LEMPTY + slot));
+                    if (C::kHeld && lane == 0) mbar_arrive(bar(C::B_SEMPTY + buf));
                     continue;
                 }
-                ++sc;
                 uint32_t v[kN];
 #pragma unroll
                 for (int c = 0; c < kN; c += 32)
-                    tmem_ld32(tbase + lane_off + C::col_s(x, 0) + 128u * buf + c,
+                    tmem_ld32(tbase + lane_off + C::COL_S + 128u * buf + c,
                               *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + 2 * x + buf));   // the scores are read
+                if (lane == 0) mbar_arrive(bar(C::B_SEMPTY + buf));   // the scores are read
                 // columns [ca, cb) see this token
                 const int ca = min(max(r0 - t * R, 0), R) * a.group;
                 const int cb = min(max(r1 - t * R, 0), R) * a.group;
