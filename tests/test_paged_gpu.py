@@ -330,6 +330,23 @@ def test_scores_long_chunk(gpu_lib):
     check_scores(c, lse, None, a)
 
 
+@pytest.mark.parametrize("kv", [[9000, 7777, 300], [12000, 9000, 300], [12100, 100, 16100], [129, 600, 290]])
+@pytest.mark.parametrize("d,window,first", [(128, (-1, 0), 0), (64, (5000, 0), 200)])
+def test_scores_several_rounds(gpu_lib, kv, d, window, first):
+    # more pairs of key tiles than SMs, the last round full, half full, nearly
+    # empty; and fewer: odd and even numbers of key and of Q tiles
+    c = Cache([40, 90, 290], kv, 16, 4, d, 64, seed=kv[0])
+    _, lse = attend(gpu_lib, c, window, first)
+    kw = dict(max_q=290, window=window, first=first)
+    a = gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], **kw)
+    check_scores(c, lse, None, a, window, first)
+    for _ in range(5):
+        b = gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], **kw)
+        for i, n in enumerate(kv):
+            assert torch.equal(a[i, :, :n], b[i, :, :n])
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+
+
 @pytest.mark.parametrize("dt,d,ps,side", [("bf16", 128, 16, False), ("fp16", 64, 8, True)])
 @pytest.mark.parametrize("H_kv", [1, 2, 5, 40])
 def test_append(gpu_lib, dt, d, ps, side, H_kv):
