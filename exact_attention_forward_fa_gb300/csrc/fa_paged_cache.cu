@@ -77,27 +77,32 @@ __device__ __forceinline__ int evict_tokens(const PagedEvictArgs &a, int b) {
 }
 __device__ __forceinline__ int evict_len(const PagedEvictArgs &a, int b) { return min(evict_tokens(a, b), a.keep); }
 
-// Row r of (b, h) in the fresh pages is the kept token's row, for rows first,
-// first + step, ... (V 16-byte vectors a row, one a thread; kMoveRows rows of K and
-// V in flight per thread).  Where a row lies takes two dependent loads, its token
-// and that token's page: those of the next rows are read while these are copied.
+// Copies rows of (b, h) to the fresh pages: for i = first, first + step, ... below
+// len (each call kThreads / V * kMoveRows of them) row_of(i, r, j) tells the row and
+// the token that goes there.  V 16-byte vectors a row, one a thread; kMoveRows rows
+// of K and V in flight per thread.  Where a row lies takes two dependent loads, its
+// token and that token's page: those of the next rows are read while these are copied.
 constexpr int kMoveRows = 4;
 
-template <int D, int kThreads>
-__device__ __forceinline__ void move_rows(const PagedEvictArgs &a, int b, int h, int first, int step, int len) {
+template <int D, int kThreads, class RowOf>
+__device__ __forceinline__ void move_rows(const PagedEvictArgs &a, int b, int h, int first, int step, int len,
+                                          RowOf &&row_of) {
     constexpr int V = D / 8, R = kThreads / V;
     const int c = threadIdx.x % V, r0 = threadIdx.x / V;
-    const int *kept = a.kept + (static_cast<long long>(b) * a.H_kv + h) * a.keep;
     const int mask = (1 << a.ps_log2) - 1;
     uint4 *kp = reinterpret_cast<uint4 *>(a.k_pages), *vp = reinterpret_cast<uint4 *>(a.v_pages);
     long long src[kMoveRows], dst[kMoveRows];             // in vectors; dst < 0: none
     auto find = [&](int at) __attribute__((always_inline)) {
-        int j[kMoveRows];
-#pragma unroll
-        for (int i = 0; i < kMoveRows; ++i) j[i] = at + r0 + i * R < len ? kept[at + r0 + i * R] : -1;
+        int j[kMoveRows], to[kMoveRows];
 #pragma unroll
         for (int i = 0; i < kMoveRows; ++i) {
-            const int r = at + r0 + i * R;
+            j[i] = -1;
+            to[i] = 0;
+            if (at + r0 + i * R < len) row_of(at + r0 + i * R, to[i], j[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i) {
+            const int r = to[i];
             dst[i] = -1;
             if (j[i] < 0) continue;
             const int sp = paged_page(a.table + static_cast<long long>(b) * a.W, j[i], a.ps_log2, a.n_pages, a.status);
@@ -137,7 +142,9 @@ __global__ void __launch_bounds__(256) fa_paged_move_kernel(const PagedEvictArgs
     asm volatile("griddepcontrol.wait;" ::: "memory");    // the kept positions
     const int h = blockIdx.y, b = blockIdx.z;
     constexpr int kRows = 256 / (D / 8) * kMoveRows;
-    move_rows<D, 256>(a, b, h, blockIdx.x * kRows, gridDim.x * kRows, evict_len(a, b));
+    const int *kept = a.kept + (static_cast<long long>(b) * a.H_kv + h) * a.keep;
+    move_rows<D, 256>(a, b, h, blockIdx.x * kRows, gridDim.x * kRows, evict_len(a, b),
+                      [&](int i, int &r, int &j) { r = i; j = kept[i]; });
 }
 
 // ---------------------------------------------------------------------------
@@ -300,15 +307,32 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
     }
 }
 
-// D != 0: the CTA then moves its own rows.
+// D != 0: the CTA then moves the rows that it chose.  Those that stay anyway need not
+// wait for the choice: CTAs of their own (z = 1) move the first and the last ones,
+// or all of a short cache, meanwhile.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const PagedEvictArgs a, const bool staged) {
     extern __shared__ float held[];
-    select_tokens(a, staged, held);
-    if constexpr (D != 0) {
-        __syncthreads();                                  // the kept positions are written
-        move_rows<D, kSelThreads>(a, blockIdx.y, blockIdx.x, 0, kSelThreads / (D / 8) * kMoveRows,
-                                  evict_len(a, blockIdx.y));
+    if constexpr (D == 0) {
+        select_tokens(a, staged, held);
+    } else {
+        constexpr int kRows = kSelThreads / (D / 8) * kMoveRows;
+        const int h = blockIdx.x, b = blockIdx.y, n = evict_tokens(a, b);
+        if (blockIdx.z == 0) {
+            select_tokens(a, staged, held);
+            if (n <= a.keep) return;
+            __syncthreads();                              // the kept positions are written
+            const int *kept = a.kept + (static_cast<long long>(b) * a.H_kv + h) * a.keep + a.first;
+            move_rows<D, kSelThreads>(a, b, h, 0, kRows, a.keep - a.first - a.recent,
+                                      [&](int i, int &r, int &j) { r = a.first + i; j = kept[i]; });
+        } else {
+            const bool all = n <= a.keep;
+            move_rows<D, kSelThreads>(a, b, h, 0, kRows, all ? n : a.first + a.recent, [&](int i, int &r, int &j) {
+                const bool front = all || i < a.first;
+                r = front ? i : a.keep - a.recent + (i - a.first);
+                j = front ? i : n - a.recent + (i - a.first);
+            });
+        }
     }
 }
 
@@ -326,7 +350,7 @@ static cudaError_t launch_select(const PagedEvictArgs &a, cudaStream_t stream) {
     }
     const long long most = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
     const bool staged = most <= kSelStaged;
-    fa_paged_select_kernel<D><<<dim3(a.H_kv, a.B), kSelThreads, staged ? most * 4 : 0, stream>>>(a, staged);
+    fa_paged_select_kernel<D><<<dim3(a.H_kv, a.B, D ? 2 : 1), kSelThreads, staged ? most * 4 : 0, stream>>>(a, staged);
     return cudaGetLastError();
 }
 
