@@ -71,7 +71,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // Cached tokens of sequence b (as far as the table and the scores go).
 __device__ __forceinline__ int evict_tokens(const PagedEvictArgs &a, int b) {
-    const long long cap = min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L));
+    // (2^31 - 2^20: indices past the end stay within 32 bits)
+    const long long cap = min(min(static_cast<long long>(a.W) << a.ps_log2, static_cast<long long>(a.L)), 0x7ff00000ll);
     const int n0 = a.kv_len[b];
     return n0 < 0 ? 0 : static_cast<int>(min(static_cast<long long>(n0), cap));
 }
@@ -158,18 +159,20 @@ __global__ void __launch_bounds__(256) fa_paged_move_kernel(const PagedEvictArgs
 // shared-memory atomics.  The digits are wide so that a warp's keys spread over
 // many bins: with 8 bits the first digit is little more than the exponent, and a
 // warp's 32 additions go to a few addresses, one after the other.  Up to
-// kSelStaged tokens the scores are read once and kept in shared memory; longer
-// caches are read again for each digit.
+// kSelStaged tokens the scores are read once and their keys kept in shared
+// memory; longer caches are read again for each pass.
 //
-// What it takes is latency and issue slots, not bytes.  For sixteen caches of 1500
-// to 16384 tokens: 26 us reading the scores again for each digit, 56 us with bins
-// counted by ballots (six votes for 32 keys and five bits; a vote costs ~16 issue
-// cycles), 40 us with keys in registers and unrolled loops (its code comes from L2
-// once a launch), SELECT_US us as it is.
+// What it takes is latency and issue slots, not bytes, so a pass does little more
+// than read a key and compare.  Caches of 15400 tokens: 15 us (of which 5 read
+// the scores, 2.5 a digit; it ends at the digit below which all keys of the bin stay);
+// 23 with scores staged instead of keys (whose order is made anew in every pass) and
+// places found by ballots, 26 reading the scores again for each digit, 40 with keys in
+// registers and unrolled loops (their code comes from L2 once a launch), 56 with
+// bins counted by ballots (a vote costs ~16 issue cycles).
 //
-// The kept positions are written in order: every warp owns a run of 32-token
-// groups and counts its tokens that stay and its ties, a scan over the warps
-// gives where they go, ballots the places within a group.
+// The kept positions are written in order: every thread owns a run of tokens (an
+// odd number, so that a warp's reads of its runs fall into different banks) and
+// counts those that stay and its ties; a scan over the threads gives their places.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t score_key(float x) {
     if (x != x) return 0xffffffffu;
@@ -177,14 +180,28 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024, kSelStaged = 24576;     // (96 KB: two CTAs per SM)
+constexpr int kSelThreads = 1024, kSelStaged = 49152;     // (192 KB)
 
-// staged: the n scores go to `held`.
-__device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const bool staged, float *held) {
+// Inclusive sums over the block's threads (kSelThreads of them); `sums`: 32 words of
+// shared memory, read by all when it returns.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    return v + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0u);
+}
+
+// staged: the keys of the n tokens go to `held`.
+__device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const bool staged, uint32_t *held) {
     __shared__ uint32_t hist[4096];                       // a digit's bins
-    __shared__ uint32_t s_and, s_or, s_digit, s_left;
-    __shared__ int w_hi[32], w_eq[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ uint32_t s_and, s_or, s_digit, s_left, s_all;
+    __shared__ uint32_t sums[3][32];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int h = blockIdx.x, b = blockIdx.y;
     const int n = evict_tokens(a, b);
     if (tid == 0 && n != a.kv_len[b]) report_bad_index(a.status, 3);
@@ -202,63 +219,66 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
     }
     const int lo = a.first, hi = n - a.recent;            // the tokens that compete
     const uint32_t want = static_cast<uint32_t>(a.keep - a.first - a.recent);
-    // every warp owns a run of whole 32-token groups
-    const int groups = (n + 31) / 32, per = (groups + 31) / 32;
-    const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
-    auto score = [&](int j) __attribute__((always_inline)) -> float { return staged ? held[j] : sc[j]; };
-    // the key of token j: 0 where none competes (a real key is never 0)
-    auto key_of = [&](int j) __attribute__((always_inline)) -> uint32_t {
-        return j >= lo && j < hi ? score_key(score(j)) : 0u;
-    };
-    if (staged) {
-#pragma unroll 8
-        for (int j = g0 * 32 + lane; j < min(n, g1 * 32); j += 32) held[j] = sc[j];   // (read by this thread only)
-    }
-    uint32_t all = ~0u, any = 0u;
+    // keys(j0, j1, step, f): f(j, key) for j = j0, j0 + step, ... below j1; the key
+    // is 0 (less than any real one) where none competes
+    auto keys = [&](int j0, int j1, int step, auto &&f) __attribute__((always_inline)) {
+        if (staged) {
 #pragma unroll 4
-    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
-        const uint32_t k = key_of(j);
-        all &= k != 0u ? k : ~0u;
-        any |= k;
-    }
+            for (int j = j0; j < j1; j += step) f(j, held[j]);
+        } else {
+#pragma unroll 4
+            for (int j = j0; j < j1; j += step) f(j, j >= lo && j < hi ? score_key(sc[j]) : 0u);
+        }
+    };
+    uint32_t all = ~0u, any = 0u;
     if (tid == 0) { s_and = ~0u; s_or = 0u; }
+#pragma unroll 1
+    for (int j0 = tid; j0 < n; j0 += 8 * kSelThreads) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = j0 + i * kSelThreads < n ? sc[j0 + i * kSelThreads] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * kSelThreads;
+            const bool competes = j >= lo && j < hi;
+            const uint32_t k = competes ? score_key(x[i]) : 0u;
+            if (staged && j < n) held[j] = k;
+            all &= competes ? k : ~0u;
+            any |= k;
+        }
+    }
     __syncthreads();
     all = __reduce_and_sync(0xffffffffu, all);
     any = __reduce_or_sync(0xffffffffu, any);
     if (lane == 0) { atomicAnd(&s_and, all); atomicOr(&s_or, any); }
+    for (int i = tid; i < 4096; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     int top = 32 - __clz(s_and ^ s_or);                   // bits to decide; the others are common
     uint32_t prefix = top == 32 ? 0u : (s_or >> top) << top, left = want;
 #pragma unroll 1
     while (want != 0 && top > 0) {
         const int low = max(top - 12, 0), bins = 1 << (top - low);
-        for (int i = tid; i < 4096; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-#pragma unroll 4
-        for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
-            const uint32_t k = key_of(j);
-            if (k != 0u && (top == 32 || ((k ^ prefix) >> top) == 0u)) atomicAdd(&hist[(k >> low) & (bins - 1)], 1u);
-        }
+        const uint32_t common = top == 32 ? 0u : ~0u << top;
+        keys(tid, n, kSelThreads, [&](int, uint32_t k) __attribute__((always_inline)) {
+            if (((k ^ prefix) & common) == 0u) atomicAdd(&hist[(k >> low) & (bins - 1)], 1u);
+        });
         __syncthreads();
         // thread t sums bins 4095 - 4 t down to 4092 - 4 t; the digit is the bin
         // that holds the left-th key from the top
         uint32_t c[4], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { c[i] = hist[4095 - 4 * tid - i]; sum += c[i]; }
-        uint32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+        for (int i = 0; i < 4; ++i) {
+            c[i] = hist[4095 - 4 * tid - i];
+            hist[4095 - 4 * tid - i] = 0;                 // (for the next digit)
+            sum += c[i];
         }
-        if (lane == 31) w_hi[warp] = static_cast<int>(incl);
-        __syncthreads();
-        uint32_t above = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? w_hi[lane] : 0);
+        uint32_t above = block_scan(sum, sums[0]) - sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (above < left && above + c[i] >= left) {
                 s_digit = static_cast<uint32_t>(4095 - 4 * tid - i);
                 s_left = left - above;
+                s_all = c[i] == left - above;             // all keys of the bin stay
             }
             above += c[i];
         }
@@ -266,44 +286,36 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
         left = s_left;
         prefix |= s_digit << low;
         top = low;
+        if (s_all) break;
     }
+    const uint32_t mask = top == 32 ? 0u : ~0u << top;    // (the bits below decide nothing)
     const uint32_t thr = prefix;                          // the want-th largest key
     const uint32_t ties = want ? left : 0u;               // how many of its equals stay
-    auto rank = [&](int j, uint32_t k) __attribute__((always_inline)) -> int {   // 2 stays, 1 tie, 0 goes
-        if (j >= n) return 0;
+    // 2 stays, 1 tie, 0 goes
+    auto rank = [&](int j, uint32_t k) __attribute__((always_inline)) -> int {
         if (j < lo || j >= hi) return 2;
-        if (want == 0) return 0;
-        return k > thr ? 2 : k == thr ? 1 : 0;
+        return want == 0 ? 0 : (k & mask) > thr ? 2 : (k & mask) == thr ? 1 : 0;
     };
-    int c2 = 0, c1 = 0;
-#pragma unroll 4
-    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
-        const int r = rank(j, key_of(j));
+    const int per = ((n + kSelThreads - 1) / kSelThreads) | 1;
+    const int j0 = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(tid) * per));
+    const int j1 = min(n, j0 + per);
+    uint32_t c2 = 0, c1 = 0;
+    keys(j0, j1, 1, [&](int j, uint32_t k) __attribute__((always_inline)) {
+        const int r = rank(j, k);
         c2 += r == 2;
         c1 += r == 1;
-    }
-    c2 = __reduce_add_sync(0xffffffffu, c2);
-    c1 = __reduce_add_sync(0xffffffffu, c1);
-    __syncthreads();                                      // (the scan's sums are read)
-    if (lane == 0) { w_hi[warp] = c2; w_eq[warp] = c1; }
-    __syncthreads();
-    // stays and ties before this warp
-    const int before2 = __reduce_add_sync(0xffffffffu, lane < warp ? w_hi[lane] : 0);
-    int eq = __reduce_add_sync(0xffffffffu, lane < warp ? w_eq[lane] : 0);
-    int at = before2 + min(eq, static_cast<int>(ties));
-    const unsigned below = (1u << lane) - 1u;
-#pragma unroll 2
-    for (int j = g0 * 32 + lane; j < g1 * 32; j += 32) {
-        const int r = rank(j, key_of(j));
-        const unsigned m1 = __ballot_sync(0xffffffffu, r == 1);
-        const bool stay = r == 2 || (r == 1 && eq + __popc(m1 & below) < static_cast<int>(ties));
-        const unsigned m = __ballot_sync(0xffffffffu, stay);
-        if (stay) {
-            kept[at + __popc(m & below)] = j;
-            if (so) so[at + __popc(m & below)] = score(j);
-        }
-        at += __popc(m);
-        eq += __popc(m1);
+    });
+    uint32_t eq = block_scan(c1, sums[1]) - c1;           // ties, and tokens that stay anyway, before this thread's
+    uint32_t at = block_scan(c2, sums[2]) - c2 + min(eq, ties);
+    keys(j0, j1, 1, [&](int j, uint32_t k) __attribute__((always_inline)) {
+        const int r = rank(j, k);
+        if (r == 2 || (r == 1 && eq < ties)) kept[at++] = j;
+        eq += r == 1;
+    });
+    if (so) {
+        __syncthreads();
+#pragma unroll 4
+        for (int r = tid; r < a.keep; r += kSelThreads) so[r] = sc[kept[r]];
     }
 }
 
@@ -312,7 +324,7 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
 // or all of a short cache, meanwhile.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const PagedEvictArgs a, const bool staged) {
-    extern __shared__ float held[];
+    extern __shared__ uint32_t held[];
     if constexpr (D == 0) {
         select_tokens(a, staged, held);
     } else {
