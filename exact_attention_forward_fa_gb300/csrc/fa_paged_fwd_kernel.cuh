@@ -1,38 +1,41 @@
 // fa_paged_fwd_kernel.cuh -- attention of new tokens over a paged cache on
-// sm_103a (tcgen05 + TMA), one kernel from single tokens to long chunks.
+// sm_103a (tcgen05 + TMA): chunks, more than 32 rows a Q tile (fewer: fa_paged_token_kernel.cuh).
 //
 // Rows.  The g = H / H_kv query heads of a K/V head share each Q tile: tile
 // row p holds the tile's position p / g, head p % g, R positions a tile
 // (R g <= 128), so one pass over a K/V head's pages serves the group.
 //
-// Units.  A unit is a pair of Q tiles (L, H) of one (sequence, K/V head).  Its
-// steps are the 128-key tiles that any of its rows sees, from the last to the
-// first, the sliding window's first and then those of the first tokens.
+// Units.  A unit is a pair of Q tiles (L, H) of one (sequence, K/V head), dealt
+// to the CTAs in equal shares of steps (fa_paged_share.cuh).  A step is one
+// 128-key tile:
 //   * Two tiles: both softmax groups walk every step, each for its own tile
 //     (the schedule of fa_fwd_kernel.cuh): 256 rows per K/V tile read.
-//   * One tile (single tokens, short chunks; always in the narrow kernel): the groups take the steps in
-//     turn, each with an accumulator of its own, joined in TMEM at the end.
-//     The chain QK -> softmax -> PV of a step is as long as two K/V tiles
-//     take from HBM, so two chains side by side keep the loads going.
+//   * One tile (a short or a chunk's last one): the groups take the steps in turn,
+//     each with an accumulator of its own, joined in TMEM at the end: one tile's
+//     chain QK -> softmax -> PV is longer than its tensor work, and two of them
+//     side by side overlap (1850 to 2300 cycles a step).
 //
-// Shares.  Lengths are known on the device only.  Every CTA adds up the
-// steps of all units (a scan over the sequences by all its threads), takes
-// the share [c Q, (c + 1) Q) of them, Q = ceil(total / CTAs), and walks it:
-// whole units are written to O; of a unit that a share's border cuts, each
-// part leaves its normalised O and LSE in the workspace (at most two parts a
-// CTA) and fa_paged_combine_kernel joins them in order.  Shares differ by one
-// step at most, whatever the lengths.
+// Measured.  Bound by the tensor core and each tile's chain QK -> softmax -> PV,
+// whose parts cannot overlap within a tile (S and P share their columns):
+// ~3400 cycles a step of two tiles, 2180 of them tensor work, as in the dense
+// forward (~3090).  Three chunks of 1100 to 1200 tokens on caches of up to 14516
+// (32 heads over 8, d = 128): 550 us, 1300 TFLOP/s.  24 sequences with 1 to 300 new
+// tokens on caches of up to 4096: 89 us, of which ~4 pass before a CTA's first
+// scores and ~11 go to the joining kernel's 152 cut units and its launch.
+// Tried: an issuing warp for each Q tile (750 us for the chunks) and the issuer's
+// loop unrolled for both tiles (608): both are code that pushes the softmax out
+// of the instruction cache; shares weighted by the time of a step with one tile
+// and with two (the batch 99 us: weights are then summed by every CTA at the start).
 //
 // Warps: 0-3 and 4-7 the softmax groups, 8 and 11 the TMA producers of K and V
 // (all lanes: one box of a page each), 9 the MMA issuer, 10 walks the share and
 // posts its pieces in a ring that the others read.
 //
-// Code size.  Twelve warps run five different roles, and what their loops
-// execute has to stay in the instruction cache: with two copies of the softmax
-// step, four of each product and non-uniform descriptors (184 KB of code) every
-// role ran at a third of its speed; as it is (one copy each, ~105 KB, most of
-// it outside the loops) single tokens at d = 64 went from 120 to 66 us (512
-// sequences of 2048).
+// Code size.  Twelve warps run five different roles, and what their loops execute
+// has to stay in the instruction cache: with two copies of the softmax step, four
+// of each product and non-uniform descriptors every role ran at a third of its
+// speed.  So there is one copy of each, and what differs between the two
+// tiles and the two schedules is data.
 //
 // Pages.  A 128-key tile is 128 / page_size boxes (or part of one page).  A
 // page that no row of the unit sees, or a bad id, is loaded from beyond the

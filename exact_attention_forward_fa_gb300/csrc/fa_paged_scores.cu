@@ -11,13 +11,29 @@
 // atomics, and the order of the terms is fixed.
 //
 // A unit is a pair of 128-token tiles of one (sequence, K/V head), one for
-// each of the two groups of four warps; their K tiles stay in shared memory
-// while the Q tiles that see them stream past, so a Q tile that is read once
-// serves 256 tokens.  S^T is double-buffered per group in TMEM (4 x 128
-// columns).  With few rows a Q tile is narrow (the product has N = 32 for a
-// single token of up to 32 heads a group) and the kernel reads K at the rate of HBM;
-// with long chunks it is bound by the exponentials (one per row and token
-// against 2 d flops, 32 a clock and SM).
+// each of the two groups of four warps; their K tiles stay while the Q tiles that
+// see them stream past, so a Q tile that is read once serves 256 tokens.
+//
+// Two forms, by the rows of a Q tile (R positions x g heads).
+//   * kN = 32, up to 32 rows (decoding: one token of up to 32 heads a group).
+//     The product has N = 32, the kernel reads K at the rate of HBM: 50.5 us,
+//     5.5 TB/s, for 32 sequences of up to 8192 tokens (8 K/V heads, d = 128);
+//     launch and first tiles are ~6 us of it.  Small Q tiles leave room for six K tiles
+//     instead of four: the bytes in flight.  Each group's S^T is
+//     double-buffered.  A warp of its own (12) loads group 1's K tiles: a tile of
+//     16-token pages is 16 boxes at ~80 cycles each, and a unit's two tiles come
+//     from HBM in ~2900.
+//   * kN = 128.  A group moves its K tile into TMEM once a unit, where the product
+//     takes it as its A operand.  From shared memory K would be read again for
+//     every Q tile, which with Q's own reads and writes and the log-sum-exps
+//     (32 16-byte loads a warp and tile) fills its 128 bytes a clock: 100 us
+//     against 93.5 (940 TFLOP/s) for chunks of 973 and 742 tokens on caches of
+//     7947 and 5023 (32 heads over 8, d = 128).  TMEM then has room for three S^T
+//     buffers, which the two groups take in turn.
+//     A pair of tiles takes ~2000 cycles: 1090 of tensor work, 1024 of exponentials
+//     (32 a clock and SM), each group's chain of waits, TMEM loads and
+//     exponentials ~1900.  Sixteen warps (half of the columns each, sums joined
+//     through TMEM) took 98 us, barriers looked at ahead of their waits 97.5.
 //
 // Units are dealt to the CTAs in turn, back and forth; warp 10 finds a unit's
 // sequence by a prefix sum over 32 sequences at a time.  Warp 8 loads the K
@@ -25,12 +41,6 @@
 // of a Q tile's rows beside it, warp 9 issues the products.  Columns of other
 // sequences (a Q tile reads past its sequence's end) are dropped by selection,
 // never by multiplying with zero.
-//
-// kN = 32: Q tiles of at most 32 rows take 8 KB instead of 32 and leave room for
-// six K tiles instead of four (d = 128): the bytes in flight of a decoding step.
-// A warp of its own (12) then loads group 1's K tiles: a tile of 16-token pages is
-// 16 boxes at ~80 cycles each, and a unit's two tiles come from HBM in ~2900.
-//
 #include "fa_paged.cuh"
 
 namespace fa {
