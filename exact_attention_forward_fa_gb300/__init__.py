@@ -457,48 +457,59 @@ def fa_paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, kep
                                  _stream(stream))
 
 
-def _check_paged(device, dtype, pools, ints, shapes) -> None:
-    """The layout that the C entry points are told by sizes and strides: pools
-    [n_pages, page_size, H_kv, d] of ``dtype`` with whole rows, int32 index
-    tensors of ``shapes`` without gaps, everything on one GPU."""
+# Single tokens make host time count: the checks below compare device indices
+# (-1: not on a GPU) instead of devices, and the module is looked up once.
+_torch = None
+
+
+def _use_torch():
+    global _torch
     import torch
-    k = pools[0]
-    if k.dim() != 4:
+    _torch = torch
+    return torch
+
+
+def _check_paged(at: int, dtype, k, v, block_table, kv_len, last, last_shape) -> None:
+    """The layout that the C entry points are told by sizes and strides: pools
+    [n_pages, page_size, H_kv, d] of ``dtype`` with whole rows (v may be
+    None), int32 index tensors [B, W], [B] and ``last_shape`` without gaps,
+    everything on GPU ``at``."""
+    torch = _torch or _use_torch()
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("pages are [n_pages, page_size, H_kv, d]")
-    if k.dtype is not torch.bfloat16 and k.dtype is not torch.float16:
-        raise TypeError(f"unsupported dtype {k.dtype}")
-    if k.dtype is not dtype:
+    kt = k.dtype
+    if kt is not torch.bfloat16 and kt is not torch.float16:
+        raise TypeError(f"unsupported dtype {kt}")
+    if kt is not dtype:
         raise ValueError("the pages and the new tokens differ in type")
-    n, ps, hk, d = shape = k.shape
+    n, ps, hk, d = shape
     st = k.stride()
     if st[3] != 1 or st[2] != d or st[1] != hk * d:
         raise ValueError("a page's rows [page_size, H_kv, d] must be contiguous")
-    if k.device != device:
+    if k.get_device() != at:
         raise ValueError("tensors on different devices")
-    if len(pools) == 2:
-        v = pools[1]
-        if v.dtype is not dtype or v.shape != shape or v.stride() != st or v.device != device:
-            raise ValueError("k_pages and v_pages differ in type, shape, strides or device")
-    _check_ints(device, ints, shapes)
-    if device.type != "cuda":
+    if v is not None and (v.dtype is not dtype or v.shape != shape or v.stride() != st or v.get_device() != at):
+        raise ValueError("k_pages and v_pages differ in type, shape, strides or device")
+    table_shape = block_table.shape
+    _check_int(block_table, table_shape, at)
+    _check_int(kv_len, table_shape[:1], at)
+    _check_int(last, last_shape, at)
+    if at < 0:
         raise ValueError("tensors must be on the GPU")
 
 
-def _check_ints(device, ints, shapes) -> None:
-    import torch
-    for x, shape in zip(ints, shapes):
-        if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous():
-            raise ValueError(f"index tensors are contiguous int32; expected {tuple(shape)}, got "
-                             f"{x.dtype} {tuple(x.shape)}")
-        if x.device != device:
-            raise ValueError("tensors on different devices")
+def _check_int(x, shape, at: int) -> None:
+    if x.dtype is not _torch.int32 or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"index tensors are contiguous int32; expected {tuple(shape)}, got "
+                         f"{x.dtype} {tuple(x.shape)}")
+    if x.get_device() != at:
+        raise ValueError("tensors on different devices")
 
 
-def _check_float(x, shape, device) -> None:
-    import torch
-    if (x.dtype is not torch.float32 or x.shape != shape or not x.is_contiguous()
-            or x.device != device):
-        raise ValueError(f"expected a contiguous float32 {tuple(shape)} on {device}, got {x.dtype} "
+def _check_float(x, shape, at: int) -> None:
+    if x.dtype is not _torch.float32 or x.shape != shape or not x.is_contiguous() or x.get_device() != at:
+        raise ValueError(f"expected a contiguous float32 {tuple(shape)} on GPU {at}, got {x.dtype} "
                          f"{tuple(x.shape)} on {x.device}")
 
 
@@ -570,25 +581,24 @@ def paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, stream=None)
     """Writes the new tokens' K and V (packed [T, H_kv, d], rows of a wider
     tensor allowed) into their pages [n_pages, page_size, H_kv, d]; kv_len
     counts them already."""
-    import torch
-    dev = k.device
-    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
-        with _launch_on(dev, stream):
+    torch = _torch or _use_torch()
+    at = k.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(k.device, stream):
             return paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q)
     B, W = block_table.shape
     T, hk, d = k.shape
-    _check_paged(dev, k.dtype, (k_pages, v_pages), (block_table, kv_len, cu_q),
-                 ((B, W), (B,), (B + 1,)))
+    _check_paged(at, k.dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hp, dp = k_pages.shape
     ks = _packed_stride(k, "k")
-    if k.shape != v.shape or k.dtype != v.dtype or v.device != dev or _packed_stride(v, "v") != ks:
+    if k.shape != v.shape or k.dtype != v.dtype or v.get_device() != at or _packed_stride(v, "v") != ks:
         raise ValueError("k and v differ in type, shape, strides or device")
     if hk != hp or d != dp:
         raise ValueError("k, v and the pages differ in heads or head dim")
     rc = load().fa_paged_append(
         k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         kv_len.data_ptr(), cu_q.data_ptr(), B, hk, d, T, ps, n, W, ks, k_pages.stride(0),
-        torch._C._cuda_getCurrentRawStream(dev.index))
+        torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_append")
 
@@ -602,15 +612,15 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
     the first ``first`` tokens visible beside a left bound.  ``max_q``: the
     most new tokens of one sequence.  Returns (O [T, H, d], LSE [H, T] or
     None)."""
-    import torch
-    dev, dtype = q.device, q.dtype
-    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
-        with _launch_on(dev, stream):
+    torch = _torch or _use_torch()
+    at, dtype = q.get_device(), q.dtype
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
             return attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q, window, first,
                                    alpha, out, lse, want_lse, workspace)
     T, H, d = q.shape
     B, W = block_table.shape
-    _check_paged(dev, dtype, (k_pages, v_pages), (block_table, kv_len, cu_q), ((B, W), (B,), (B + 1,)))
+    _check_paged(at, dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
     if dk != d:
@@ -618,26 +628,26 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
     if alpha is None:
         alpha = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((T, H, d), dtype=dtype, device=dev)
-    elif (out.shape != q.shape or out.dtype != dtype or out.device != dev
+        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+    elif (out.shape != q.shape or out.dtype is not dtype or out.get_device() != at
             or not out.is_contiguous()):
-        raise ValueError(f"out is a contiguous {dtype} {tuple(q.shape)} on {dev}")
+        raise ValueError(f"out is a contiguous {dtype} {tuple(q.shape)} on {q.device}")
     if lse is not None:
-        _check_float(lse, (H, T), dev)
+        _check_float(lse, (H, T), at)
     elif want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=dev)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    raw = torch._C._cuda_getCurrentRawStream(at)
     shared = workspace is None and raw == 0
     if shared:
-        workspace = _paged_ws.get((dev.index, d))
+        workspace = _paged_ws.get((at, d))
         if workspace is None:
-            workspace = _paged_ws.setdefault((dev.index, d), _new_paged_workspace(d, dev))
+            workspace = _paged_ws.setdefault((at, d), _new_paged_workspace(d, q.device))
         _paged_ws_lock.acquire()
     elif workspace is None:
-        workspace = _new_paged_workspace(d, dev)
-    elif (workspace.device != dev
+        workspace = _new_paged_workspace(d, q.device)
+    elif (workspace.get_device() != at
             or workspace.numel() * workspace.element_size() < fa_paged_workspace_bytes(d)):
-        raise ValueError(f"the workspace is {fa_paged_workspace_bytes(d)} bytes on {dev}")
+        raise ValueError(f"the workspace is {fa_paged_workspace_bytes(d)} bytes on {q.device}")
     try:
         rc = load().fa_fwd_paged(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
@@ -659,35 +669,35 @@ def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=
     lse, window, first and alpha as in ``attention_paged``.  ``out`` may be
     ``scores``; entries behind kv_len are left as they were (zeros where it
     is allocated here).  Returns out."""
-    import torch
-    dev, dtype = q.device, q.dtype
-    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
-        with _launch_on(dev, stream):
+    torch = _torch or _use_torch()
+    at, dtype = q.get_device(), q.dtype
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
             return paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q, scores, window, first,
                                 alpha, out)
     T, H, d = q.shape
     B, W = block_table.shape
-    _check_paged(dev, dtype, (k_pages,), (block_table, kv_len, cu_q), ((B, W), (B,), (B + 1,)))
+    _check_paged(at, dtype, k_pages, None, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
     if dk != d:
         raise ValueError("q and the pages differ in head dim")
     like = scores if scores is not None else out
     shape = (B, hk, W * ps if like is None else like.shape[2])
-    _check_float(lse, (H, T), dev)
+    _check_float(lse, (H, T), at)
     if scores is not None:
-        _check_float(scores, shape, dev)
+        _check_float(scores, shape, at)
     if out is None:
-        out = torch.zeros(shape, dtype=torch.float32, device=dev)
+        out = torch.zeros(shape, dtype=torch.float32, device=q.device)
     else:
-        _check_float(out, shape, dev)
+        _check_float(out, shape, at)
     if alpha is None:
         alpha = 1.0 / math.sqrt(d)
     rc = load().fa_paged_scores(
         q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(),
         cu_q.data_ptr(), None if scores is None else scores.data_ptr(), out.data_ptr(), B, H, hk, T,
         max_q, d, ps, n, W, shape[2], qs, k_pages.stride(0), alpha, window[0], window[1], first,
-        FA_BF16 if dtype is torch.bfloat16 else FA_FP16, torch._C._cuda_getCurrentRawStream(dev.index))
+        FA_BF16 if dtype is torch.bfloat16 else FA_FP16, torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_scores")
     return out
@@ -701,37 +711,36 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
     (kept positions [B, H_kv, keep], their scores, new lengths); entries
     behind a new length are left as they were (-1 and 0 where they are
     allocated here)."""
-    import torch
-    dev = scores.device
-    if stream is not None or (dev.index is not None and dev.index != torch.cuda.current_device()):
-        with _launch_on(dev, stream):
+    torch = _torch or _use_torch()
+    at = scores.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(scores.device, stream):
             return paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep, first,
                                recent, kept, scores_out, new_len)
     B, W = block_table.shape
     Wd = dst_table.shape[1]
-    _check_paged(dev, k_pages.dtype, (k_pages, v_pages), (block_table, kv_len, dst_table),
-                 ((B, W), (B,), (B, Wd)))
+    _check_paged(at, k_pages.dtype, k_pages, v_pages, block_table, kv_len, dst_table, (B, Wd))
     n, ps, hk, d = k_pages.shape
     L = scores.shape[2]
-    _check_float(scores, (B, hk, L), dev)
+    _check_float(scores, (B, hk, L), at)
     room = (B, hk, max(keep, 0))
     if kept is None:
-        kept = torch.full(room, -1, dtype=torch.int32, device=dev)
+        kept = torch.full(room, -1, dtype=torch.int32, device=scores.device)
     else:
-        _check_ints(dev, (kept,), (room,))
+        _check_int(kept, room, at)
     if scores_out is None:
-        scores_out = torch.zeros(room, dtype=torch.float32, device=dev)
+        scores_out = torch.zeros(room, dtype=torch.float32, device=scores.device)
     else:
-        _check_float(scores_out, room, dev)
+        _check_float(scores_out, room, at)
     if new_len is None:
-        new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_len = torch.empty((B,), dtype=torch.int32, device=scores.device)
     else:
-        _check_ints(dev, (new_len,), ((B,),))
+        _check_int(new_len, (B,), at)
     rc = load().fa_paged_evict(
         k_pages.data_ptr(), v_pages.data_ptr(), scores.data_ptr(), block_table.data_ptr(),
         kv_len.data_ptr(), dst_table.data_ptr(), kept.data_ptr(), scores_out.data_ptr(),
         new_len.data_ptr(), B, hk, d, ps, n, W, Wd, L, k_pages.stride(0), keep, first, recent,
-        torch._C._cuda_getCurrentRawStream(dev.index))
+        torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_evict")
     return kept, scores_out, new_len
