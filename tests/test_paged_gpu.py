@@ -615,6 +615,54 @@ def test_graphs_with_workspaces_of_their_own(gpu_lib):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+def test_results_of_the_call_before(gpu_lib):
+    # chains of calls that read what the last one, another kernel, a copy or
+    # another stream wrote, eager and captured
+    fa = gpu_lib
+    c = Cache([1, 2, 40], [700, 3000, 2000], 8, 2, 128, 16, seed=2)
+    n = c.cu[-1]
+    k, v = torch.randn(2, n, 2, 128, device="cuda").bfloat16()
+    q2 = torch.randn(n, 8, 128, device="cuda").bfloat16()
+    q, lens = torch.empty_like(q2), torch.empty_like(c.kv_len)
+    pool = c.k_pages.clone(), c.v_pages.clone()
+    wide = c.table.shape[1] * 16
+    dst = torch.arange(-(-256 // 16) * 3, device="cuda").reshape(3, -1).int() + c.k_pages.shape[0]
+    big = [torch.cat([x, torch.zeros_like(x[:dst.numel()])]) for x in pool]
+    side = torch.cuda.Stream()
+
+    def chain():
+        out = []
+        for i in range(3):
+            kp, vp = (x.clone() for x in big)                       # (a copy, then the append)
+            lens.copy_(c.kv_len)
+            here = torch.cuda.current_stream()
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                q.copy_(q2)                                         # (another stream, then the attention)
+            fa.paged_append(k, v, kp, vp, c.table, lens, c.cu_q)
+            here.wait_stream(side)
+            o, lse = fa.attention_paged(q, kp, vp, c.table, lens, c.cu_q, max_q=40)
+            a = fa.paged_scores(q, lse, kp, c.table, lens, c.cu_q, max_q=40,
+                                scores=torch.zeros(3, 2, wide, device="cuda"))
+            kept, s, m = fa.paged_evict(kp, vp, a, c.table, lens, dst, 256, 4, 64)
+            o1, lse1 = fa.attention_paged(o, kp, vp, dst, m, c.cu_q, max_q=40)
+            out += [o, lse, a, kept, s, m, o1, lse1]
+        return out
+
+    want = [x.clone() for x in chain()]
+    torch.cuda.synchronize()
+    for i in range(8):                                              # each pass equals the first
+        assert torch.equal(want[i].nan_to_num(9e9), want[i + 8].nan_to_num(9e9))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    for _ in range(20):
+        g.replay()
+        for x, y in zip(want, got):
+            assert torch.equal(x.nan_to_num(9e9), y.nan_to_num(9e9))
+    assert fa.fa_check_status() == fa.FA_OK
+
+
 def test_graph_replays_with_other_lengths(gpu_lib):
     fa = gpu_lib
     c = Cache([1, 1, 1], [400, 300, 2000], 8, 2, 64, 16, seed=3)
