@@ -88,8 +88,9 @@ struct PagedCfg {
     static constexpr uint32_t IDESC_QK = idesc_f16(128, 128, kBF16, false, false);
     static constexpr uint32_t IDESC_PV = idesc_f16(128, D, kBF16, false, true);
     // fa_fwd_kernel.cuh: the conditional rescale, tau in log2 units, and the
-    // row sum below which a tile's P against the old reference is kept.
-    static constexpr float TAU = 8.0f, KEEP_SUM = 65536.0f;
+    // row sum up to which a tile's P against the old reference is kept: fp16's
+    // largest number, so that no term of it becomes infinite.
+    static constexpr float TAU = 8.0f, KEEP_SUM = 65504.0f;
 };
 
 template <int D, bool kBF16>

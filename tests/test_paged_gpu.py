@@ -196,6 +196,26 @@ def test_attention_large_scores(gpu_lib):
     check_attention(c, o, lse)
 
 
+@pytest.mark.parametrize("q_len", [1, 7, 40])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("peak", [14.9999, 15.0001, 15.9985, 15.99975, 15.99995, 16.0001])
+def test_attention_one_score_far_above(gpu_lib, q_len, dt, tile, peak):
+    # 2^peak against a reference of 0 from other tiles: terms at the edge of
+    # fp16's range
+    c = Cache([q_len], [384], 4, 1, 64, 64, dt, seed=1)
+    c.q.zero_()
+    c.q[:, :, 0] = 1
+    k = torch.zeros(384, 1, 64, device="cuda")
+    k[128 * tile:128 * tile + 128, 0, 0] = -10
+    k[128 * tile + 5, 0, 0] = 1
+    c.K[0] = k.double()
+    c.put(0, 0, k.to(DT[dt]), c.V[0].to(DT[dt]))
+    alpha = peak * math.log(2)
+    o, lse = attend(gpu_lib, c, (-1, -1), 0, alpha)
+    check_attention(c, o, lse, (-1, -1), 0, alpha)
+
+
 @pytest.mark.parametrize("alpha", [1e-6, 0.01, 2.0])
 def test_attention_alpha(gpu_lib, alpha):
     c = Cache([3, 140], [50, 200], seed=1)
@@ -501,6 +521,21 @@ def test_empty_calls(gpu_lib):
     old = torch.rand(2, 2, 32, device="cuda")
     a = gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], max_q=1, scores=old)
     assert torch.equal(a[0, :, :5], old[0, :, :5]) and (a[0, :, 5:] == 0).all() and (a[1] == 0).all()
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+
+
+def test_strides_that_no_row_has(gpu_lib):
+    # of an empty tensor, and between the heads of one head
+    c = Cache([0, 0], [5, 0], 1, 1, 64, 16)
+    q = torch.empty(192, device="cuda", dtype=torch.bfloat16).as_strided((0, 1, 64), (1, 1, 1))
+    o, lse = gpu_lib.attention_paged(q, *c.args(), max_q=1)
+    assert o.shape == (0, 1, 64)
+    c = Cache([2, 1], [50, 9], 1, 1, 64, 16)
+    want = attend(gpu_lib, c)
+    wide = torch.zeros(3, 192, device="cuda", dtype=torch.bfloat16)
+    wide[:, :64] = c.q[:, 0]
+    o, lse = gpu_lib.attention_paged(wide.as_strided((3, 1, 64), (192, 1, 1)), *c.args(), max_q=2)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
 
 
