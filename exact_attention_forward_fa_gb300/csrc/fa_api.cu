@@ -925,7 +925,8 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     // 11: a share then holds the end of one unit and the start of the next).
     const uint64_t units = static_cast<uint64_t>(B) + static_cast<uint64_t>(total_q) / (2 * L.R);
     const uint64_t tiles = ((static_cast<uint64_t>(table_width) << a.ps_log2) + 127) / 128;
-    const uint64_t share = units * tiles;              // shares of one K/V head
+    const uint64_t cost = tiles + (L.R * a.group <= fa::kFewRows ? fa::kUnitCostFew : fa::kUnitCostChunk);
+    const uint64_t share = units * cost;              // shares of one K/V head
     const uint64_t sm = static_cast<uint64_t>(dev->sm_count);
     L.grid = static_cast<int>(share >= sm ? sm : share * H_kv < sm ? share * H_kv : sm);
     L.w.desc = static_cast<int *>(workspace);

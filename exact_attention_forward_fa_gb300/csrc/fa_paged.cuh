@@ -167,6 +167,10 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t stream);
 
+// What a unit costs beside its steps, in steps (fa_paged_share.cuh): in the kernel
+// for few rows and in the one for chunks.
+constexpr int kFewRows = 32, kUnitCostFew = 1, kUnitCostChunk = 3;
+
 // The workspace of the attention: what the parts of cut units leave.
 struct PagedWork {
     int *desc;          // [CTAs][8]: the cut unit that starts in a CTA's share

@@ -123,7 +123,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
     // (the scratch lies in the K/V ring, which no copy uses yet)
     tc_fence_before();
-    const PagedShare share = paged_share<C::NTHREADS>(a, 2 * R, gbase + C::KV_OFF);
+    const PagedShare share = paged_share<C::NTHREADS, kUnitCostChunk>(a, 2 * R, gbase + C::KV_OFF);
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
 
@@ -156,7 +156,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             ++np_out;
             return true;
         };
-        if (paged_walk<true>(share, a, R, wk.desc + 8 * blockIdx.x, post)) {
+        if (paged_walk<true, kUnitCostChunk>(share, a, R, wk.desc + 8 * blockIdx.x, post)) {
             PagedPiece end{};
             end.qrow = -1;
             post(end);

@@ -52,7 +52,7 @@ cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
     const int rows = L.R * L.a.group;
     if (rows <= 8)
         return L.bf16 ? launch_fwd_paged_inst<D, true, 8>(L) : launch_fwd_paged_inst<D, false, 8>(L);
-    if (rows <= 32)
+    if (rows <= kFewRows)
         return L.bf16 ? launch_fwd_paged_inst<D, true, 32>(L) : launch_fwd_paged_inst<D, false, 32>(L);
     return L.bf16 ? launch_fwd_paged_inst<D, true, 0>(L) : launch_fwd_paged_inst<D, false, 0>(L);
 }

@@ -5,13 +5,15 @@
 // A unit is U positions of the new tokens of one (sequence, K/V head); its
 // steps are the 128-key tiles that any of its rows sees, from the last to the
 // first, the sliding window's first and then those of the first tokens.
-// Lengths are known on the device only: every CTA adds up the steps of all
+// Lengths are known on the device only: every CTA adds up the cost of all
 // units (a scan over the sequences by all its threads), takes the share
-// [c Q, (c + 1) Q) of them, Q = ceil(total / CTAs), and walks it.  Whole units
-// are written to O; of a unit that a share's border cuts, each part leaves its
-// normalised O and LSE in the workspace (at most two parts a CTA) and
-// fa_paged_combine_kernel joins them in order.  Shares differ by one step at
-// most, whatever the lengths.
+// [c Q, (c + 1) Q) of it, Q = ceil(total / CTAs), and walks it.  A unit costs its
+// steps and, in front of them, kCost for its beginning and end, when the pipeline
+// fills and drains (3 for chunks: 89 -> 85 us for 24 sequences of 1 to 300 new
+// tokens; 1 for few rows: 184 -> 181 us for 64 single tokens; more is worse).
+// Whole units are written to O; of a unit that a share's border cuts, each
+// part leaves its normalised O and LSE in the workspace (at most two parts a
+// CTA) and fa_paged_combine_kernel joins them in order.
 #pragma once
 
 #include "fa_paged.cuh"
@@ -49,29 +51,31 @@ __device__ __forceinline__ PagedTiles paged_tiles(int pa, int pb, int n, int wl,
     t.T = max(1, t.nw + min((f >> 7) + ((f & 127) != 0), lo));   // an empty unit still writes O = 0
     return t;
 }
-// Steps of unit p of a sequence (U positions a unit).  Not inlined: the code
+// Cost of unit p of a sequence (U positions a unit).  Not inlined: the code
 // before a CTA's first load comes from L2, line by line.
-static __device__ __noinline__ int paged_unit_steps(int m, int n, int p, int U, int wl, int wr, int first) {
+template <int kCost>
+static __device__ __noinline__ int paged_unit_cost(int m, int n, int p, int U, int wl, int wr, int first) {
     const int i0 = p * U;
-    return paged_tiles(n - m + i0, n - m + min(m, i0 + U) - 1, n, wl, wr, first).T;
+    return kCost + paged_tiles(n - m + i0, n - m + min(m, i0 + U) - 1, n, wl, wr, first).T;
 }
 __device__ __forceinline__ int paged_units(const PagedSeq &s, int U) {
     return static_cast<int>((static_cast<long long>(s.m) + U - 1) / U);
 }
-// Steps of all units of a sequence, by the whole warp.
-__device__ __forceinline__ long long paged_seq_steps_warp(const PagedSeq &s, int U, const PagedArgs &a) {
+// Cost of all units of a sequence, by the whole warp.
+template <int kCost>
+__device__ __forceinline__ long long paged_seq_cost_warp(const PagedSeq &s, int U, const PagedArgs &a) {
     const int np = paged_units(s, U);
     long long sum = 0;
-    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_steps(s.m, s.n, p, U, a.wl, a.wr, a.first);
+    for (int p = threadIdx.x & 31; p < np; p += 32) sum += paged_unit_cost<kCost>(s.m, s.n, p, U, a.wl, a.wr, a.first);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     return sum;
 }
 
-// A CTA's share [w0, w1) of all steps, in units of `quota`; its first unit
-// belongs to sequence b or one behind it, whose steps start at `at`.
+// A CTA's share [w0, w1) of the whole cost, in units of `quota`; its first unit
+// belongs to sequence b or one behind it, whose units start at `at`.
 struct PagedShare {
-    long long w0, w1, quota, at, per;   // per: steps of one K/V head of sequence b
+    long long w0, w1, quota, at, per;   // per: cost of one K/V head of sequence b
     int b;
     PagedSeq s;                         // sequence b
 };
@@ -81,7 +85,7 @@ constexpr uint32_t kShareScratch = 16 * 8 + 48;
 
 // By the whole block (kThreads of them); ends with a barrier after which the
 // scratch is free.
-template <int kThreads>
+template <int kThreads, int kCost>
 __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, uint8_t *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long *scan = reinterpret_cast<long long *>(scratch);          // [16]
@@ -99,11 +103,11 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, uin
         const int np = paged_units(s, U);
         // a few units by the thread itself, many by its warp
         if (np <= 8)
-            for (int p = 0; p < np; ++p) mine += paged_unit_steps(s.m, s.n, p, U, a.wl, a.wr, a.first);
+            for (int p = 0; p < np; ++p) mine += paged_unit_cost<kCost>(s.m, s.n, p, U, a.wl, a.wr, a.first);
         for (unsigned big = __ballot_sync(0xffffffffu, np > 8); big != 0; big &= big - 1) {
             const int src = __ffs(big) - 1;
             PagedSeq t{0, __shfl_sync(0xffffffffu, s.m, src), __shfl_sync(0xffffffffu, s.n, src), false};
-            const long long sum = paged_seq_steps_warp(t, U, a);
+            const long long sum = paged_seq_cost_warp<kCost>(t, U, a);
             if (lane == src) mine += sum;
         }
         if (i == 0) { s0 = s; per0 = mine; }
@@ -152,7 +156,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, uin
 // The scheduler warp: the pieces of a share, in order, to post(piece) -> bool.
 // kPair: units of two Q tiles of R positions (U = 2 R), otherwise of one.
 // desc: this CTA's descriptor in the workspace.
-template <bool kPair, class Post>
+template <bool kPair, int kCost, class Post>
 __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs &a, int R, int *desc, Post &&post) {
     const int lane = threadIdx.x & 31, U = kPair ? 2 * R : R;
     const long long w0 = sh.w0, w1 = sh.w1;
@@ -160,15 +164,15 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
     bool ok = true;
     if (w0 < w1) {
         int b = sh.b;
-        long long at = sh.at, per = sh.per;            // steps before sequence b; of one K/V head
+        long long at = sh.at, per = sh.per;            // cost before sequence b; of one K/V head
         PagedSeq s = sh.s;
         while (w0 >= at + per * a.H_kv && b + 1 < a.B) {
             at += per * a.H_kv;
             s = paged_seq(a.cu_q, a.kv_len, ++b, a.T, a.W, a.ps_log2);
-            per = paged_seq_steps_warp(s, U, a);
+            per = paged_seq_cost_warp<kCost>(s, U, a);
         }
         int h = 0;
-        long long rem = w0 - at;                       // steps into this head's units
+        long long rem = w0 - at;                       // how far into this head's units
         if (rem >= per) {
             h = (rem >> 31) == 0 ? static_cast<unsigned>(rem) / static_cast<unsigned>(per)
                                  : static_cast<int>(rem / per);
@@ -176,7 +180,7 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
         }
         int np = paged_units(s, U), p = 0;
         for (int p0 = 0; np > 1 && p0 < np; p0 += 32) {
-            const long long mine_t = p0 + lane < np ? paged_unit_steps(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
+            const long long mine_t = p0 + lane < np ? paged_unit_cost<kCost>(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
             long long inc = mine_t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -192,7 +196,7 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
             }
             rem -= __shfl_sync(0xffffffffu, inc, 31);
         }
-        int t0 = static_cast<int>(rem);
+        int v0 = static_cast<int>(rem);                // where the share starts within the unit
         for (long long at_w = w0; ok && at_w < w1;) {
             PagedPiece pc;
             const int i0 = p * U, left = s.m - i0;
@@ -212,20 +216,21 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
             pc.vhi = paged_hi(last, s.n, a.wr);
             const int khl = paged_hi(pc.pos + pc.nl - 1, s.n, a.wr);
             pc.skip = min(tl.T - 1, max(0, min(tl.nw, tl.hi - ((khl >> 7) + ((khl & 127) != 0)))));
-            pc.t0 = t0;
-            pc.t1 = static_cast<int>(min(static_cast<long long>(tl.T), t0 + (w1 - at_w)));
+            const int v1 = static_cast<int>(min(static_cast<long long>(tl.T) + kCost, v0 + (w1 - at_w)));
+            pc.t0 = max(v0 - kCost, 0);
+            pc.t1 = max(v1 - kCost, 0);
             const bool cont = pc.t1 < tl.T;
-            pc.slot = t0 > 0 ? 2 * static_cast<int>(blockIdx.x) : cont ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-            if (t0 == 0 && cont && lane == 0) {        // a cut unit that starts here
+            pc.slot = pc.t0 > 0 ? 2 * static_cast<int>(blockIdx.x) : cont ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+            if (pc.t0 == 0 && pc.t1 > 0 && cont && lane == 0) {        // a cut unit that starts here
                 desc[1] = pc.qrow;
                 desc[2] = pc.nl;
                 desc[3] = pc.nh;
                 desc[4] = h;
-                desc[0] = 1 + static_cast<int>((at_w + tl.T - 1) / sh.quota - blockIdx.x);   // its parts
+                desc[0] = 1 + static_cast<int>((at_w - v0 + kCost + tl.T - 1) / sh.quota - blockIdx.x);   // its parts
             }
-            ok = post(pc);
-            at_w += pc.t1 - t0;
-            t0 = 0;
+            if (pc.t1 > pc.t0) ok = post(pc);
+            at_w += v1 - v0;
+            v0 = 0;
             if (++p == np) {
                 p = 0;
                 if (++h == a.H_kv) {

@@ -160,7 +160,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         tma_prefetch_desc(&tm_v);
     }
     tc_fence_before();
-    const PagedShare share = paged_share<C::NTHREADS>(a, R, gbase + C::KV_OFF);
+    const PagedShare share = paged_share<C::NTHREADS, kUnitCostFew>(a, R, gbase + C::KV_OFF);
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
 
@@ -189,7 +189,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             ++sent;
             return true;
         };
-        if (paged_walk<false>(share, a, R, wk.desc + 8 * blockIdx.x, post)) {
+        if (paged_walk<false, kUnitCostFew>(share, a, R, wk.desc + 8 * blockIdx.x, post)) {
             PagedPiece end{};
             end.qrow = -1;
             post(end);
