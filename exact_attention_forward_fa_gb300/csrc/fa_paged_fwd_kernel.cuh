@@ -20,8 +20,8 @@
 // ~3400 cycles a step of two tiles, 2180 of them tensor work, as in the dense
 // forward (~3090).  Three chunks of 1100 to 1200 tokens on caches of up to 14516
 // (32 heads over 8, d = 128): 550 us, 1300 TFLOP/s.  24 sequences with 1 to 300 new
-// tokens on caches of up to 4096: 89 us, of which ~4 pass before a CTA's first
-// scores and ~11 go to the joining kernel's 152 cut units and its launch.
+// tokens on caches of up to 4096: 85 us, of which ~4 pass before a CTA's first
+// scores and up to 10 go to the joining kernel's 152 cut units and its launch.
 // Tried: an issuing warp for each Q tile (750 us for the chunks) and the issuer's
 // loop unrolled for both tiles (608): both are code that pushes the softmax out
 // of the instruction cache; shares weighted by the time of a step with one tile

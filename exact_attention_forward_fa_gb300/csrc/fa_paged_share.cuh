@@ -180,7 +180,8 @@ __device__ __forceinline__ bool paged_walk(const PagedShare &sh, const PagedArgs
         }
         int np = paged_units(s, U), p = 0;
         for (int p0 = 0; np > 1 && p0 < np; p0 += 32) {
-            const long long mine_t = p0 + lane < np ? paged_unit_cost<kCost>(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
+            const long long mine_t =
+                p0 + lane < np ? paged_unit_cost<kCost>(s.m, s.n, p0 + lane, U, a.wl, a.wr, a.first) : 0;
             long long inc = mine_t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

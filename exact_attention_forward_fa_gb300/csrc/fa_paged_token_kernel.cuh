@@ -29,12 +29,13 @@
 // unit.
 //
 // Measured (32 heads over 8, d = 128, bf16): 64 sequences of up to 8192 tokens
-// 183 us, 6.2 TB/s; two of 115831 and 125872 154 us, 6.4 TB/s; one of 777 11.6 us, all of it
+// 180.5 us, 6.3 TB/s; two of 115831 and 125872 154 us, 6.4 TB/s; one of 777 11.6 us, all of it
 // latency (launch, shares, first tiles, joining kernel).  d = 64, a K/V head for
 // each of 16 heads, 1 to 4 new tokens, 32 caches of which the last 2047 and the first 4 are
-// seen: 59 us, 4.5 TB/s (sixteen times the pieces a byte).  The bytes in flight
-// (192 KB an SM) cover HBM's latency; what is left of the longer ones are the
-// ~6 us at the start and the ~4 us of the joining kernel.
+// seen: 60 us, 4.5 TB/s (32 KB a step, for the same barriers, votes and
+// exponentials).  The bytes in flight (192 KB an SM) cover HBM's latency; what is
+// left of the longer ones are the ~6 us at the start and the ~4 us of the joining
+// kernel.
 //
 // Waits are bounded, and a warp whose wait gave up keeps taking part in its
 // group's barriers until a vote makes the whole group leave.
