@@ -121,13 +121,14 @@ __device__ __forceinline__ PagedShare paged_share(const PagedArgs &a, int U, uin
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long v = scan[w];
-        before += w < warp ? v : 0;
-        total += v;
+    long long sums = lane < kThreads / 32 ? scan[lane] : 0;            // (every warp scans the warps' sums)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += v;
     }
+    const long long total = __shfl_sync(0xffffffffu, sums, 31);
+    const long long before = __shfl_sync(0xffffffffu, sums, warp == 0 ? 31 : warp - 1) - (warp == 0 ? total : 0);
     PagedShare sh;
     const unsigned G = gridDim.x;
     sh.quota = (total >> 31) == 0 ? static_cast<long long>((static_cast<unsigned>(total) + G - 1) / G)
