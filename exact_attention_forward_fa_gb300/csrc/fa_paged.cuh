@@ -9,10 +9,9 @@
 // kv_len[b] cached tokens, so row cu_q[b] + i has position
 // kv_len[b] - (cu_q[b + 1] - cu_q[b]) + i.
 //
-// Visible keys of the row at position p ("FlashAttention-3 on Hopper", sec.
-// 4.7, with the bottom-right diagonal of Nk > Nq): j < kv_len, j <= p + wr
-// (wr >= 0), and j >= p - wl (wl >= 0) or j < first -- a sliding window
-// beside which the first tokens stay visible.
+// Visible keys of the row at position p (the bottom-right diagonal of more keys
+// than queries): j < kv_len, j <= p + wr (wr >= 0), and j >= p - wl (wl >= 0) or
+// j < first -- a sliding window beside which the first tokens stay visible.
 #pragma once
 
 #include <cuda_runtime.h>
