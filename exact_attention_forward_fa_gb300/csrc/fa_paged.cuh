@@ -168,7 +168,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t stream);
 
 // What a unit costs beside its steps, in steps (fa_paged_share.cuh): in the kernel
 // for few rows and in the one for chunks.
-constexpr int kFewRows = 32, kUnitCostFew = 1, kUnitCostChunk = 3;
+constexpr int kFewRows = 8, kUnitCostFew = 1, kUnitCostChunk = 3;
 
 // The workspace of the attention: what the parts of cut units leave.
 struct PagedWork {

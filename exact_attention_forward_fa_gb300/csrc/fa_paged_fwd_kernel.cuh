@@ -1,5 +1,5 @@
 // fa_paged_fwd_kernel.cuh -- attention of new tokens over a paged cache on
-// sm_103a (tcgen05 + TMA): chunks, more than 32 rows a Q tile (fewer: fa_paged_token_kernel.cuh).
+// sm_103a (tcgen05 + TMA): more than 8 rows a Q tile (fewer: fa_paged_token_kernel.cuh).
 //
 // Rows.  The g = H / H_kv query heads of a K/V head share each Q tile: tile
 // row p holds the tile's position p / g, head p % g, R positions a tile

@@ -10,12 +10,12 @@
 
 namespace fa {
 
-// kN: the kernel for few rows, up to kN of them; 0: the one for chunks.
-template <int D, bool kBF16, int kN>
+// kFew: the kernel for few rows, else the one for chunks.
+template <int D, bool kBF16, bool kFew>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
-    using C = std::conditional_t<kN != 0, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
+    using C = std::conditional_t<kFew, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
     void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedArgs, PagedWork, int);
-    if constexpr (kN != 0) kern = fa_paged_token_kernel<D, kBF16, kN>;
+    if constexpr (kFew) kern = fa_paged_token_kernel<D, kBF16>;
     else kern = fa_paged_fwd_kernel<D, kBF16>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
     int dev = 0;
@@ -33,7 +33,7 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     if (e != cudaSuccess || L.grid == 1) return e;  // one share: nothing is cut
     // The joining kernel's CTAs are brought up while the attention's last ones
     // run; it waits for their results itself (griddepcontrol.wait).
-    const int rows = (kN ? 1 : 2) * L.R * L.a.group;
+    const int rows = (kFew ? 1 : 2) * L.R * L.a.group;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.grid, rows < 8 ? rows : 8);
     cfg.blockDim = dim3(256);
@@ -43,18 +43,17 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16, (kN != 0)>, L.a, L.w, L.R);
+    return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D, kBF16, kFew>, L.a, L.w, L.R);
 }
 
-// Up to 32 rows a tile: few rows against each K/V tile, bound by HBM.
+// Up to kFewRows rows a tile: few rows against each K/V tile, bound by HBM.  64
+// single tokens of 4 heads a group (4 rows) 180 us, one on 777 tokens 11.6, 4 rows of
+// d = 64 with a window 60; the chunk kernel with 16 rows 190, 13.6 and 87.
 template <int D>
 cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
-    const int rows = L.R * L.a.group;
-    if (rows <= 8)
-        return L.bf16 ? launch_fwd_paged_inst<D, true, 8>(L) : launch_fwd_paged_inst<D, false, 8>(L);
-    if (rows <= kFewRows)
-        return L.bf16 ? launch_fwd_paged_inst<D, true, 32>(L) : launch_fwd_paged_inst<D, false, 32>(L);
-    return L.bf16 ? launch_fwd_paged_inst<D, true, 0>(L) : launch_fwd_paged_inst<D, false, 0>(L);
+    if (L.R * L.a.group <= kFewRows)
+        return L.bf16 ? launch_fwd_paged_inst<D, true, true>(L) : launch_fwd_paged_inst<D, false, true>(L);
+    return L.bf16 ? launch_fwd_paged_inst<D, true, false>(L) : launch_fwd_paged_inst<D, false, false>(L);
 }
 
 }  // namespace fa

@@ -1,5 +1,5 @@
 // fa_paged_token_kernel.cuh -- attention over a paged cache for few rows
-// (single tokens, drafts of a few: at most 32 rows of R positions x g heads),
+// (single tokens, drafts of two or three: at most 8 rows of R positions x g heads),
 // on sm_103a.
 //
 // Such a call reads each K and V tile for a handful of rows: it is bound by
@@ -7,9 +7,8 @@
 // latency keeps loads from being issued.  Both products are formed transposed:
 //     S^T = K Q^T   (128 keys x N rows; a TMEM lane, and a thread, is a key)
 //     O^T = V^T P^T (d x N; a lane is an output column)
-// so a tile of 128 keys has work for all 128 threads of a group -- N
-// exponentials each, N <= 32 -- and the tensor core's N is the number of rows
-// rounded to 16 or 32 instead of 128.  (With rows as lanes one warp of four
+// so a tile of 128 keys has work for all 128 threads of a group -- an
+// exponential a row each -- and the tensor core's N is 16 instead of 128.  (With rows as lanes one warp of four
 // held all rows: 2000 cycles a step and group, 54 us for 32 caches of 32768 at
 // d = 64 where HBM takes 39.)  P^T goes through shared memory, written in the
 // swizzled layout that the product reads.
@@ -50,6 +49,8 @@ struct TokenCfg {
     static constexpr int NCH = D / 64;                    // 128-byte column chunks
     static constexpr uint32_t CHUNK_BYTES = 128u * 128u;
     static constexpr uint32_t TILE_BYTES = NCH * CHUNK_BYTES;
+    // (32 rows of Q and P where the products read 16: what lies behind the K/V
+    // tiles has to be as long as one of their chunks, see MMA_END)
     static constexpr uint32_t Q_CHUNK = 32u * 128u, Q_BYTES = NCH * Q_CHUNK;
     static constexpr uint32_t P_CHUNK = 32u * 128u, P_BYTES = 2 * P_CHUNK;   // [32 rows][128 keys]
     static constexpr int NSTAGE = D == 64 ? 12 : 6;
@@ -61,9 +62,9 @@ struct TokenCfg {
     static constexpr uint32_t KV_OFF = 0;
     static constexpr uint32_t Q_OFF = NSTAGE * TILE_BYTES;
     static constexpr uint32_t P_OFF = Q_OFF + NQ * Q_BYTES;
-    static constexpr uint32_t R_OFF = P_OFF + 2 * P_BYTES;            // [2 groups][32] references
+    static constexpr uint32_t R_OFF = P_OFF + 2 * P_BYTES;            // [2 groups][32] references (8 used)
     static constexpr uint32_t X_OFF = R_OFF + 2 * 32 * 4;             // group 1's LSE and 1 / l, the factors: [4][32]
-    static constexpr uint32_t RED_OFF = X_OFF + 4 * 32 * 4;           // sums of 8 rows: [2 groups][2][4 warps][8]
+    static constexpr uint32_t RED_OFF = X_OFF + 4 * 32 * 4;           // sums: [2 groups][2][4 warps][8]
     static constexpr uint32_t RING_OFF = RED_OFF + 2 * 64 * 4;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 64;
     static constexpr int B_QFULL = 0, B_QEMPTY = NQ, B_KVFULL = 2 * NQ, B_KVEMPTY = B_KVFULL + NSTAGE,
@@ -80,6 +81,10 @@ struct TokenCfg {
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     static constexpr uint32_t SMEM_BYTES = MISC_OFF + 16 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+    // O^T's product has 128 rows, at d = 64 too: with the last V tile as A it reads
+    // one chunk past the tiles, which must not lie outside shared memory.
+    static constexpr uint32_t MMA_END = KV_OFF + (NSTAGE - 1) * TILE_BYTES + 2 * CHUNK_BYTES;
+    static_assert(MMA_END <= MISC_OFF, "the last V tile's product stays in shared memory");
     static constexpr uint32_t TMEM_COLS = 256;
     __host__ __device__ static constexpr uint32_t col_s(int x, int buf) { return 64u * x + 32u * buf; }
     __host__ __device__ static constexpr uint32_t col_o(int x) { return 128u + 32u * x; }
@@ -100,7 +105,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
 }
 
 // Adds (or takes the maximum of) v[n] over the 32 lanes of a warp, for every n:
-// lane l gets that of v[l % kN].  31 exchanges for 32 values instead of 160.
+// lane l gets that of v[l % kN].  9 exchanges for 8 values instead of 40.
 template <int kN, bool kMax = false>
 __device__ __forceinline__ float warp_reduce_transposed(float (&v)[kN]) {
     const int lane = threadIdx.x & 31;
@@ -129,16 +134,18 @@ __device__ __forceinline__ bool group_any(int x, bool v) {
     return r != 0;
 }
 
-// kN: rows that the groups work on, 8 or 32 (the products have 16 or 32
-// columns).  One token of up to 8 heads a group is the common call, and the
-// code of a piece's beginning and end, which runs once a piece and by then has
-// left the instruction cache, is a quarter as long for 8 rows.
-template <int D, bool kBF16, int kN>
+// More rows are the chunk kernel's (fa_paged_launch.cuh): an instantiation of this
+// one for 32 took 370 us for 64 sequences of four tokens on up to 8192 (16 rows) and
+// 535 of eight (32 rows), where the chunk kernel takes 190, and 22 to 26 us for
+// one sequence of 777 against 14: a thread's unrolled work on 32 rows, most of
+// it at the beginning and end of a piece, comes from L2 each time.
+template <int D, bool kBF16>
 __global__ void __launch_bounds__(416, 1)
 fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
                       const int R) {
     using C = TokenCfg<D, kBF16>;
+    constexpr int kN = kFewRows;                          // rows that the groups work on
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -204,8 +211,8 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // a step ahead of O^T += V^T P^T.
         WaitCtx w{abort_flag, a.status, kRoleMma};
         const int x = __shfl_sync(0xffffffffu, warp - 10, 0);
-        constexpr uint32_t idesc_s = idesc_f16(128, kN < 16 ? 16 : kN, kBF16, false, false);
-        constexpr uint32_t idesc_o = idesc_f16(128, kN < 16 ? 16 : kN, kBF16, true, false);
+        constexpr uint32_t idesc_s = idesc_f16(128, 16, kBF16, false, false);
+        constexpr uint32_t idesc_o = idesc_f16(128, 16, kBF16, true, false);
         uint32_t kc = 0, vc = 1;                           // this group's next K and V tile, counted together
         uint32_t pc = 0, sc = 0, un = 0, pp = 0;           // pieces, S tiles, accumulators, P tiles so far
         bool ok = true;
@@ -333,8 +340,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 tc_fence_after();
                 uint32_t s[kN];
                 const uint32_t tS = tbase + lane_off + C::col_s(0, 0) + 64u * x + 32u * buf;
-                if constexpr (kN == 8) tmem_ld8(tS, s);
-                else tmem_ld32(tS, s);
+                tmem_ld8(tS, s);
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -405,13 +411,11 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         const uint32_t tO = tbase + lane_off + C::col_o(0) + 32u * x;
                         uint32_t ov[kN];
                         tc_fence_after();
-                        if constexpr (kN == 8) tmem_ld8(tO, ov);
-                        else tmem_ld32(tO, ov);
+                        tmem_ld8(tO, ov);
                         tmem_ld_wait();
 #pragma unroll
                         for (int n = 0; n < kN; ++n) ov[n] = __float_as_uint(__uint_as_float(ov[n]) * m[n]);
-                        if constexpr (kN == 8) tmem_st8(tO, ov);
-                        else tmem_st32(tO, ov);
+                        tmem_st8(tO, ov);
                         tmem_st_wait();
                         tc_fence_before();
                     }
@@ -443,10 +447,8 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             }
             const bool some = x < ns, joined = ns >= 2;
             // ---- row n's sums over all keys of the group, in thread n ----
-            if (kN == 32 && some && !bad) bad = !mbar_wait_warp(bar(C::B_OFULL + x), (x ? un1 : un0) & 1u, w, 21);
             const float le_w = warp_reduce_transposed<kN>(le), lr_w = warp_reduce_transposed<kN>(lr);
-            if (kN == 32 && group_any(x, bad)) break;     // the sums of 32 rows go through P's buffer
-            float *sums = kN == 32 ? scratch : reinterpret_cast<float *>(gbase + C::RED_OFF) + 64 * x;
+            float *sums = reinterpret_cast<float *>(gbase + C::RED_OFF) + 64 * x;
             if (lane < kN) {
                 sums[gwarp * kN + lane] = le_w;
                 sums[(4 + gwarp) * kN + lane] = lr_w;
@@ -470,7 +472,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::B_XFULL));
                     }
-                    if (kN == 8) bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 21) || bad;
+                    bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 21) || bad;
                     ++nx;
                     ++un1;
                 }
@@ -505,7 +507,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     }
                 }
             }
-            if (kN == 8) bad = !mbar_wait_warp(bar(C::B_OFULL), un0 & 1u, w, 21) || bad;
+            bad = !mbar_wait_warp(bar(C::B_OFULL), un0 & 1u, w, 21) || bad;
             if (joined) bad = !mbar_wait_warp(bar(C::B_OFULL + 1), un1 & 1u, w, 27) || bad;
             if (group_any(0, bad)) break;
             tc_fence_after();
@@ -513,33 +515,26 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             int tok = p.qrow, hd = 0;
             float *part = wk.o + static_cast<size_t>(max(p.slot, 0)) * 256 * D + row;
             uint16_t *out = reinterpret_cast<uint16_t *>(a.o) + static_cast<size_t>(p.h) * a.group * D + row;
-#pragma unroll 1
-            for (int n8 = 0; n8 < nr; n8 += 8) {
-                uint32_t o0[8], o1[8];
-                tmem_ld8(tO + n8, o0);
-                tmem_ld8(tO + (C::col_o(1) - C::col_o(0)) + n8, o1);
-                tmem_ld_wait();
-                if (n8 + 8 >= nr) {                                          // the accumulators are read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(C::B_OEMPTY));
-                        if (joined) mbar_arrive(bar(C::B_OEMPTY + 1));
-                    }
-                }
-                if (row >= D) continue;                                      // (d = 64: lanes that hold nothing)
+            uint32_t o0[8], o1[8];
+            tmem_ld8(tO, o0);
+            tmem_ld8(tO + (C::col_o(1) - C::col_o(0)), o1);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {                                                 // the accumulators are read
+                mbar_arrive(bar(C::B_OEMPTY));
+                if (joined) mbar_arrive(bar(C::B_OEMPTY + 1));
+            }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int n = n8 + q;
-                    if (n >= nr) continue;
-                    float v = __uint_as_float(o0[q]) * fac[n];
-                    if (joined) v = fmaf(__uint_as_float(o1[q]), fac[32 + n], v);
-                    if (p.slot >= 0)
-                        part[n * D] = v;
-                    else
-                        out[(static_cast<size_t>(tok) * a.H + hd) * D] = static_cast<uint16_t>(pack2<kBF16>(v, 0.f));
-                    if (++hd == a.group) { hd = 0; ++tok; }
-                }
+            for (int n = 0; n < kN; ++n) {
+                if (n >= nr || row >= D) continue;                           // (d = 64: lanes that hold nothing)
+                float v = __uint_as_float(o0[n]) * fac[n];
+                if (joined) v = fmaf(__uint_as_float(o1[n]), fac[32 + n], v);
+                if (p.slot >= 0)
+                    part[n * D] = v;
+                else
+                    out[(static_cast<size_t>(tok) * a.H + hd) * D] = static_cast<uint16_t>(pack2<kBF16>(v, 0.f));
+                if (++hd == a.group) { hd = 0; ++tok; }
             }
             ++un0;
             if (joined) { ++un1; ++nx; }
