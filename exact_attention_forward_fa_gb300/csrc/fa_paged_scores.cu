@@ -544,6 +544,8 @@ static cudaError_t launch_scores_inst(const PagedScoresLaunch &L) {
     return cudaGetLastError();
 }
 
+// Up to 32 rows a Q tile the narrow form: 64 sequences of 4 tokens on up to 8192 97 us
+// (the other 138), of 8 tokens 97.5 (138), one of 4 tokens on 777 7.1 (8.4).
 template <int D>
 static cudaError_t launch_scores_dispatch(const PagedScoresLaunch &L) {
     if (L.R * L.a.group <= 32)
