@@ -40,7 +40,11 @@
 // tiles (page ids a unit ahead) and the Q tiles, warp 11 puts the log-sum-exps
 // of a Q tile's rows beside it, warp 9 issues the products.  Columns of other
 // sequences (a Q tile reads past its sequence's end) are dropped by selection,
-// never by multiplying with zero.
+// never by multiplying with zero.  A row whose log-sum-exp is NaN counts as one that
+// adds nothing, and a bit beside the log-sum-exps makes the tokens that see it NaN:
+// hidden columns stay free of it, at one 16-byte load a tile (selecting the hidden
+// exponents instead of the hidden scores parts the additions from the exponentials:
+// 132 us instead of 88 for chunks).
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -63,8 +67,9 @@ struct ScoresCfg {
     static constexpr int RING = 4;
     static constexpr uint32_t K_OFF = 0;
     static constexpr uint32_t Q_OFF = NK * TILE_BYTES;
-    static constexpr uint32_t L_OFF = Q_OFF + NQ * Q_BYTES;             // -LSE log2(e): [NL][128] floats
-    static constexpr uint32_t RING_OFF = L_OFF + NL * 128 * 4;
+    static constexpr uint32_t L_OFF = Q_OFF + NQ * Q_BYTES;             // [NL]: -LSE log2(e) of 128 columns, and
+    static constexpr uint32_t L_SLOT = 128 * 4 + 16;                    // a bit for each that is NaN
+    static constexpr uint32_t RING_OFF = L_OFF + NL * L_SLOT;
     static constexpr uint32_t BAR_OFF = RING_OFF + RING * 32;
     static constexpr int B_KFULL = 0, B_KEMPTY = NK, B_QFULL = 2 * NK, B_QEMPTY = B_QFULL + NQ,
                          B_LFULL = B_QEMPTY + NQ, B_LEMPTY = B_LFULL + NL, B_SFULL = B_LEMPTY + NL, B_SEMPTY = B_SFULL + NS, B_TFULL = B_SEMPTY + NS, B_MMADONE = B_TFULL + 2,
@@ -288,7 +293,8 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
       } else if (warp == 11) {
         // =================== log-sum-exps (whole warp) ===================
         // -LSE log2(e) of a Q tile's rows, -inf (a term of zero) for columns
-        // that are none or rows that see nothing; read a tile ahead.
+        // that are none, rows that see nothing and NaN, whose bits follow; read a
+        // tile ahead.
         WaitCtx w{abort_flag, a.status, kRoleProducer};
         uint32_t qc = 0, ui = 0;
         bool ok = true;
@@ -323,10 +329,14 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 read(u, t + 1, val);
                 ok = mbar_wait_warp(bar(C::B_LEMPTY + slot), ph ^ 1u, w, 3);
                 if (!ok) break;
-                float *nl = reinterpret_cast<float *>(gbase + C::L_OFF) + slot * 128;
+                float *nl = reinterpret_cast<float *>(gbase + C::L_OFF + slot * C::L_SLOT);
 #pragma unroll
-                for (int i = 0; i < kEach; ++i)
-                    nl[lane + 32 * i] = cur[i] == -INFINITY ? -INFINITY : cur[i] * -1.44269504088896340736f;
+                for (int i = 0; i < kEach; ++i) {
+                    const bool nan = cur[i] != cur[i];
+                    nl[lane + 32 * i] = cur[i] == -INFINITY || nan ? -INFINITY : cur[i] * -1.44269504088896340736f;
+                    const unsigned bits = __ballot_sync(0xffffffffu, nan);
+                    if (lane == i) reinterpret_cast<uint32_t *>(nl)[128 + i] = bits;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_LFULL + slot));
             }
@@ -496,7 +506,10 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     for (int c = 0; c < kN; ++c)
                         if (c < ca || c >= cb) v[c] = 0xff800000u;
                 }
-                const float4 *l4 = reinterpret_cast<const float4 *>(gbase + C::L_OFF) + slot * 32;
+                const float4 *l4 = reinterpret_cast<const float4 *>(gbase + C::L_OFF + slot * C::L_SLOT);
+                uint4 nan = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kN == 32) nan.x = reinterpret_cast<const uint32_t *>(l4)[128];
+                else nan = reinterpret_cast<const uint4 *>(l4)[32];
                 float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
 #pragma unroll
                 for (int c = 0; c < kN; c += 4) {
@@ -511,6 +524,12 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_LEMPTY + slot));
                 sum += (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                if ((nan.x | nan.y | nan.z | nan.w) != 0u) {
+                    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                    auto sees = [&](int c) -> uint32_t { return below(cb - c) & ~below(ca - c); };
+                    if ((nan.x & sees(0)) | (nan.y & sees(32)) | (nan.z & sees(64)) | (nan.w & sees(96)))
+                        sum = __int_as_float(0x7fc00000);
+                }
             }
             if (!ok) break;
             if (!none && kk < u.n) out[at] = had + sum;

@@ -450,7 +450,8 @@ long long fa_paged_workspace_bytes(int d);
  *                         exp(alpha q_i . k_j - LSE_i)
  * for j < kv_len[b]; the rest of scores is left as it was.
  *   lse    : device, float [H][total_q], from fa_fwd_paged with the same
- *            arguments (rows with LSE = -inf add nothing).
+ *            arguments (rows with LSE = -inf add nothing, a NaN makes the
+ *            weights of the tokens that its row sees NaN, and no others).
  *   scores_in, scores : device, float [B][H_kv][score_width]; scores_in may
  *            be scores itself, or NULL for zeros.  score_width >= every
  *            kv_len (longer ones are cut off: FA_ERR_BAD_INDEX).

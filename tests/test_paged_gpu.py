@@ -801,3 +801,30 @@ def test_serving_steps(gpu_lib):
     scores[:, :, :keep] = cut
     step([1, 1])
     step([2, 1])
+
+
+# ---- what a row or a token that is not finite may touch ----
+
+@pytest.mark.parametrize("q_len,H,d,window,first", [
+    ([70, 9], 8, 128, (-1, 0), 0), ([70, 9], 8, 64, (20, 0), 3), ([130, 1], 6, 128, (40, 2), 0),
+    ([5, 1], 4, 64, (-1, 0), 0), ([7, 2], 4, 128, (6, 0), 2)])
+def test_scores_a_nan_row_stays_with_the_tokens_it_sees(gpu_lib, q_len, H, d, window, first):
+    c = Cache(q_len, [400, 150], H, 2, d, 16, seed=d)
+    _, lse = attend(gpu_lib, c, window, first)
+    kw = dict(max_q=max(q_len), window=window, first=first)
+    want = gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], **kw)
+    assert want.isfinite().all()
+    m, n = c.q_len[0], c.kv[0]
+    j = torch.arange(want.shape[2], device="cuda")
+    for i in (0, m // 2, m - 1):
+        bad = lse.clone()
+        bad[H - 1, i] = math.nan                 # a head of K/V head 1
+        got = gpu_lib.paged_scores(c.q, bad, c.k_pages, *c.args()[2:], **kw)
+        p = n - m + i
+        sees = (j < n) & ((j <= p + window[1]) if window[1] >= 0 else (j < n))
+        if window[0] >= 0:
+            sees &= (j >= p - window[0]) | (j < first)
+        assert torch.isnan(got[0, 1, sees]).all()
+        assert torch.equal(got[0, 1, ~sees], want[0, 1, ~sees])
+        assert torch.equal(got[0, 0], want[0, 0]) and torch.equal(got[1], want[1])
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
