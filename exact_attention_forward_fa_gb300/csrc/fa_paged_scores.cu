@@ -45,6 +45,12 @@
 // hidden columns stay free of it, at one 16-byte load a tile (selecting the hidden
 // exponents instead of the hidden scores parts the additions from the exponentials:
 // 132 us instead of 88 for chunks).
+// Columns of a Q tile that are no rows (group sizes that do not divide 128, short
+// calls) hold zeros, and an infinite key times zero is NaN: where a key is not
+// finite (held in TMEM, on its way there) or a sum became NaN (keys in shared
+// memory) they are selected away too. Selecting them in every tile took 81 us
+// instead of 50 for chunks of 3 heads a group at d = 64, 58.5 instead of 56.4 for 32
+// single tokens.
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -446,6 +452,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 tc_fence_after();
                 return true;
             };
+            bool odd = false;                              // (held) the key is not finite and there are columns that are none
             if (C::kHeld && !none && u.qa < u.qb) {
                 // this token's key into TMEM (every product with the group's last one
                 // is complete: its last scores are read)
@@ -454,6 +461,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 if (!ok) break;
                 ++kc;
                 const uint8_t *kr = gbase + C::K_OFF + ks * C::TILE_BYTES + row * 128;
+                uint32_t top = 0u;                         // the largest magnitudes, in halves
 #pragma unroll
                 for (int ch = 0; ch < C::NCH; ++ch) {
                     uint32_t kw[32];
@@ -463,7 +471,13 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         kw[4 * q] = v4.x; kw[4 * q + 1] = v4.y; kw[4 * q + 2] = v4.z; kw[4 * q + 3] = v4.w;
                     }
                     tmem_st32(tbase + lane_off + 64u * x + 32u * ch, kw);
+                    if (box_rows != kN) {
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) top = __vmaxu2(top, kw[q] & 0x7fff7fffu);
+                    }
                 }
+                constexpr uint32_t kInf = kBF16 ? 0x7f80u : 0x7c00u;
+                odd = max(top & 0xffffu, top >> 16) >= kInf;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -500,8 +514,9 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 // columns [ca, cb) see this token
                 const int ca = min(max(r0 - t * R, 0), R) * a.group;
                 const int cb = min(max(r1 - t * R, 0), R) * a.group;
-                if (__any_sync(0xffffffffu, ca != 0 || cb != box_rows)) {
-                    // hidden columns: a score of -inf (what lies there may be anything)
+                if (__any_sync(0xffffffffu, ca != 0 || cb != box_rows || odd)) {
+                    // hidden columns: a score of -inf (what lies there may be anything;
+                    // in a column that is none, an infinite key times its zeros)
 #pragma unroll
                     for (int c = 0; c < kN; ++c)
                         if (c < ca || c >= cb) v[c] = 0xff800000u;
@@ -510,20 +525,32 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 uint4 nan = make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (kN == 32) nan.x = reinterpret_cast<const uint32_t *>(l4)[128];
                 else nan = reinterpret_cast<const uint4 *>(l4)[32];
-                float2 e_a = make_float2(0.f, 0.f), e_b = e_a;
+                float2 e_a, e_b;
+                float ts;
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    e_a = make_float2(0.f, 0.f);
+                    e_b = e_a;
 #pragma unroll
-                for (int c = 0; c < kN; c += 4) {
-                    const float4 l = l4[c / 4];
-                    const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                                                  c2, make_float2(l.x, l.y));
-                    const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
-                                                  c2, make_float2(l.z, l.w));
-                    e_a = __fadd2_rn(e_a, make_float2(ex2_approx(x01.x), ex2_approx(x01.y)));
-                    e_b = __fadd2_rn(e_b, make_float2(ex2_approx(x23.x), ex2_approx(x23.y)));
+                    for (int c = 0; c < kN; c += 4) {
+                        const float4 l = l4[c / 4];
+                        const float2 x01 = __ffma2_rn(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                                      c2, make_float2(l.x, l.y));
+                        const float2 x23 = __ffma2_rn(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                                      c2, make_float2(l.z, l.w));
+                        e_a = __fadd2_rn(e_a, make_float2(ex2_approx(x01.x), ex2_approx(x01.y)));
+                        e_b = __fadd2_rn(e_b, make_float2(ex2_approx(x23.x), ex2_approx(x23.y)));
+                    }
+                    ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                    // (keys in shared memory) NaN, maybe of such a column: once more without them
+                    if (C::kHeld || again || box_rows == kN || !__any_sync(0xffffffffu, ts != ts)) break;
+#pragma unroll
+                    for (int c = 0; c < kN; ++c)
+                        if (c >= cb) v[c] = 0xff800000u;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_LEMPTY + slot));
-                sum += (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                sum += ts;
                 if ((nan.x | nan.y | nan.z | nan.w) != 0u) {
                     auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
                     auto sees = [&](int c) -> uint32_t { return below(cb - c) & ~below(ca - c); };

@@ -828,3 +828,24 @@ def test_scores_a_nan_row_stays_with_the_tokens_it_sees(gpu_lib, q_len, H, d, wi
         assert torch.equal(got[0, 1, ~sees], want[0, 1, ~sees])
         assert torch.equal(got[0, 0], want[0, 0]) and torch.equal(got[1], want[1])
     assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+
+
+@pytest.mark.parametrize("q_len,H,H_kv,d", [([1, 1], 4, 1, 128), ([3, 1], 6, 2, 64), ([90, 40], 6, 2, 128),
+                                            ([90, 40], 8, 2, 64)])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_an_infinite_key_that_nobody_weighs(gpu_lib, q_len, H, H_kv, d, dt):
+    # a score of -inf has weight 0, as one of -30000 / 8 has (2^-5000)
+    c = Cache(q_len, [700, 300], H, H_kv, d, 16, dt, seed=d)
+    c.q[:, :, 0] = -1
+    got = []
+    for far in (30000.0, math.inf):
+        for pos in (3, 500):
+            key = c.K[0][pos:pos + 1].to(DT[dt])
+            key[0, 0, 0] = far
+            c.put(0, pos, key, c.V[0][pos:pos + 1].to(DT[dt]))
+        o, lse = attend(gpu_lib, c)
+        got.append((o, lse, gpu_lib.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], max_q=max(q_len))))
+    for x, y in zip(*got):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+    assert (got[1][2][0, 0, [3, 500]] == 0).all()
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
