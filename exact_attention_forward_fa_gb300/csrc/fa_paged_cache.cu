@@ -38,9 +38,11 @@ __global__ void __launch_bounds__(256) fa_paged_append_kernel(const PagedAppendA
     load(0);
     const int b = paged_find_seq(a.cu_q, a.B, t);
     if (b < 0) return;                                   // behind the last sequence
-    const PagedSeq s = paged_seq(a.cu_q, a.kv_len, b, a.T, a.W, a.ps_log2);
-    const int p = s.n - s.m + (t - s.q0);
-    if (p < 0 || p >= s.n) return;                       // more new tokens than the cache counts
+    // The position as the caller's numbers have it: a length or an offset that is out
+    // of range moves no token into the slot of another.
+    const long long n = a.kv_len[b], at_p = n - a.cu_q[b + 1] + t;
+    if (at_p < 0 || at_p >= min(n, static_cast<long long>(a.W) << a.ps_log2)) return;   // no slot
+    const int p = static_cast<int>(at_p);
     const int page = paged_page(a.table + static_cast<long long>(b) * a.W, p, a.ps_log2, a.n_pages,
                                 a.status);
     if (page < 0) return;

@@ -390,8 +390,10 @@ fa_status fa_bwd_noalloc(const void *q, const void *k, const void *v,
  *   k, v : device, total_q rows of [H_kv][d], kv_stride elements from row to
  *          row (>= H_kv * d, a multiple of 8: a slice of a fused projection's
  *          rows is fine), 16-byte aligned.
- * Tokens with a negative position (more new tokens than kv_len counts) are
- * dropped.  Any 16-bit element type.
+ * Tokens without a slot are dropped and nothing is written in their place: a
+ * negative position (more new tokens than kv_len counts), or one at or behind
+ * table_width * page_size (a full cache; FA_ERR_BAD_INDEX).  Any 16-bit
+ * element type.
  */
 fa_status fa_paged_append(const void *k, const void *v, void *k_pages, void *v_pages,
                           const int32_t *block_table, const int32_t *kv_len,

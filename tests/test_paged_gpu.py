@@ -849,3 +849,32 @@ def test_an_infinite_key_that_nobody_weighs(gpu_lib, q_len, H, H_kv, d, dt):
         assert torch.isfinite(x).all() and torch.equal(x, y)
     assert (got[1][2][0, 0, [3, 500]] == 0).all()
     assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+
+
+# (capacity 80 and 48 tokens) kv_len, cu_q: a full cache, a chunk over the
+# edge, offsets behind the packed rows, lengths of any value
+@pytest.mark.parametrize("kv,cu", [
+    ([81, 40], [0, 1, 4]), ([80, 50], [0, 2, 7]), ([83, 49], [0, 5, 7]), ([70, 48], [0, 3, 11]),
+    ([70, 48], [0, 9, 9]), ([-1, 48], [0, 2, 7]), ([2**31 - 1, 30], [0, 4, 7]), ([60, -2**31], [0, 4, 7]),
+    ([60, 40], [-2, 4, 7])])
+@pytest.mark.parametrize("dt,d", [("bf16", 64), ("fp16", 128)])
+def test_append_skips_what_has_no_slot(gpu_lib, kv, cu, dt, d):
+    c = Cache([1, 1], [80, 48], 2, 2, d, 16, dt, seed=3)
+    table = c.table[:, :5].clone()
+    table[1, 3:] = -1
+    width = (5, 3)                               # pages that exist
+    T = 7
+    k, v = torch.randn(2, T, 2, d, device="cuda").to(DT[dt])
+    want_k, want_v = c.k_pages.clone(), c.v_pages.clone()
+    for b in range(2):
+        for t in range(max(cu[b], 0), min(cu[b + 1], T)):
+            p = kv[b] - cu[b + 1] + t
+            if 0 <= p < 16 * width[b]:
+                page = int(table[b, p // 16])
+                want_k[page, p % 16], want_v[page, p % 16] = k[t], v[t]
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    gpu_lib.paged_append(k, v, c.k_pages, c.v_pages, table, lens, cu_q)
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_ERR_BAD_INDEX
+    for got, want in ((c.k_pages, want_k), (c.v_pages, want_v)):
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
