@@ -182,8 +182,8 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     if (s.bad) report_bad_index(a.status, 1);
                     if (s.n > L) report_bad_index(a.status, 3);
                 }
-                s.n = min(s.n, L);                        // (reported: the cached tokens end there)
-                incl = static_cast<long long>((s.n + 255) >> 8) * a.H_kv;
+                if (s.bad) s.m = 0;                       // what its rows would see is unknown: its weights stay
+                incl = static_cast<long long>((min(s.n, L) + 255) >> 8) * a.H_kv;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -199,7 +199,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             o.q0 = __shfl_sync(0xffffffffu, s.q0, l);
             o.m = __shfl_sync(0xffffffffu, s.m, l);
             o.b = b0 + l;
-            const int pairs = (o.n + 255) >> 8;
+            const int pairs = (min(o.n, L) + 255) >> 8;
             const long long r = u - (__shfl_sync(0xffffffffu, incl, l) - static_cast<long long>(pairs) * a.H_kv);
             o.h = static_cast<int>(r / pairs);
             o.k0 = static_cast<int>(r - static_cast<long long>(o.h) * pairs) * 256;
@@ -253,7 +253,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             more = take(ui++, w, 31, nx);
             if (more) { page[0] = page_of(nx, 0); page[1] = page_of(nx, 1); }
             if (u.qa >= u.qb) continue;                   // no row sees the pair
-            const int nk = u.k0 + 128 < u.n ? 2 : 1;
+            const int nk = u.k0 + 128 < min(u.n, L) ? 2 : 1;
 #pragma unroll 1
             for (int x = xa; x < min(xb, nk) && ok; ++x) {
                 const int j = (u.k0 >> 7) + x;
@@ -363,7 +363,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             ++ui;
             const int tiles = uniform(u.qb - u.qa);
             if (tiles <= 0) continue;
-            const int nk = uniform(u.k0 + 128 < u.n ? 2 : 1);
+            const int nk = uniform(u.k0 + 128 < min(u.n, L) ? 2 : 1);
 #pragma unroll 1
             for (int t = 0; t < tiles && ok; ++t) {
                 ok = mbar_wait_warp(bar(C::B_QFULL + qs), qph, w, 14);
@@ -434,10 +434,11 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         while (ok && take(ui, w, 24, u)) {
             ++ui;
             const int kk = u.k0 + x * 128 + row;                             // this thread's token
-            const bool none = u.k0 + x * 128 >= u.n;                         // the group has no tile of this unit
+            const int end = min(u.n, L);                                     // no room for tokens behind it
+            const bool none = u.k0 + x * 128 >= end;                         // the group has no tile of this unit
             const int old = u.n - u.m;
             const size_t at = (static_cast<size_t>(u.b) * a.H_kv + u.h) * L + kk;
-            const float had = in != nullptr && !none && kk < old ? in[at] : 0.f;
+            const float had = in != nullptr && kk < min(old, end) ? in[at] : 0.f;
             // rows [ra, rb) of the new tokens see this one
             const long long ra = a.wr >= 0 ? static_cast<long long>(kk) - a.wr - old : 0;
             const long long rb = a.wl >= 0 && kk >= a.first ? static_cast<long long>(kk) + a.wl - old + 1 : u.m;
@@ -559,7 +560,7 @@ fa_paged_scores_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 }
             }
             if (!ok) break;
-            if (!none && kk < u.n) out[at] = had + sum;
+            if (kk < end) out[at] = had + sum;
         }
     }
 

@@ -456,7 +456,10 @@ long long fa_paged_workspace_bytes(int d);
  *            weights of the tokens that its row sees NaN, and no others).
  *   scores_in, scores : device, float [B][H_kv][score_width]; scores_in may
  *            be scores itself, or NULL for zeros.  score_width >= every
- *            kv_len (longer ones are cut off: FA_ERR_BAD_INDEX).
+ *            kv_len (of a longer cache the first score_width tokens get their
+ *            weights: FA_ERR_BAD_INDEX).
+ * A sequence whose kv_len or offsets are out of range adds nothing, so that
+ * weights collected in place survive it.
  * Summed in FP32 in a fixed order, without atomics.  Other arguments as
  * fa_fwd_paged.
  */

@@ -878,3 +878,46 @@ def test_append_skips_what_has_no_slot(gpu_lib, kv, cu, dt, d):
     assert gpu_lib.fa_check_status() == gpu_lib.FA_ERR_BAD_INDEX
     for got, want in ((c.k_pages, want_k), (c.v_pages, want_v)):
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("q_len,H", [([1, 1, 2], 4), ([40, 1, 7], 8)])
+def test_scores_of_lengths_out_of_range(gpu_lib, q_len, H):
+    # a sequence whose own numbers are out of range hands out nothing: the
+    # weights that its cache has collected stay
+    fa = gpu_lib
+    c = Cache(q_len, [160, 100, 80], H, 2, 64, 16, seed=4)
+    _, lse = attend(fa, c)
+    table = c.table[:, :10].contiguous()                 # 160 tokens
+    old = torch.rand(3, 2, 170, device="cuda")
+    kw = dict(max_q=max(q_len), scores=old)
+    want = fa.paged_scores(c.q, lse, c.k_pages, table, c.kv_len, c.cu_q, out=old.clone(), **kw)
+    for n0 in (161, 2 ** 31 - 1):
+        lens = c.kv_len.clone()
+        lens[0] = n0
+        got = fa.paged_scores(c.q, lse, c.k_pages, table, lens, c.cu_q, out=old.clone(), **kw)
+        assert fa.fa_check_status() == fa.FA_ERR_BAD_INDEX
+        assert torch.equal(got[0], old[0]) and torch.equal(got[1:], want[1:])
+    cu_q = c.cu_q.clone()
+    cu_q[3] = c.T + 1
+    got = fa.paged_scores(c.q, lse, c.k_pages, table, c.kv_len, cu_q, out=old.clone(), **kw)
+    assert fa.fa_check_status() == fa.FA_ERR_BAD_INDEX
+    assert torch.equal(got[2], old[2]) and torch.equal(got[:2], want[:2])
+
+
+@pytest.mark.parametrize("q_len,H,window,first", [([1, 1], 4, (-1, 0), 0), ([60, 3], 8, (-1, 0), 0),
+                                                  ([60, 3], 8, (30, 2), 5), ([5, 60], 8, (-1, -1), 0)])
+@pytest.mark.parametrize("L", [1, 100, 128, 256, 299])
+def test_scores_narrower_than_the_cache(gpu_lib, q_len, H, window, first, L):
+    # the weights that there is room for are those of the whole cache
+    fa = gpu_lib
+    c = Cache(q_len, [300, 70], H, 2, 64, 16, seed=L)
+    _, lse = attend(fa, c, window, first)
+    kw = dict(max_q=max(q_len), window=window, first=first)
+    old = torch.rand(2, 2, 304, device="cuda")
+    want = fa.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], scores=old, out=old.clone(), **kw)
+    check_scores(c, lse, old, want, window, first)
+    assert fa.fa_check_status() == fa.FA_OK
+    cut = old[:, :, :L].contiguous()
+    fa.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], scores=cut, out=cut, **kw)
+    assert fa.fa_check_status() == fa.FA_ERR_BAD_INDEX
+    assert torch.equal(cut, want[:, :, :L])
