@@ -921,3 +921,77 @@ def test_scores_narrower_than_the_cache(gpu_lib, q_len, H, window, first, L):
     fa.paged_scores(c.q, lse, c.k_pages, *c.args()[2:], scores=cut, out=cut, **kw)
     assert fa.fa_check_status() == fa.FA_ERR_BAD_INDEX
     assert torch.equal(cut, want[:, :, :L])
+
+
+def check_evicted(c, scores, dst, keep, first, recent, before, kept, out, new_len):
+    """Everything that an eviction writes: kept positions, scores, lengths and the rows of both pools."""
+    kv, ps, H_kv = c.kv, c.ps, c.H_kv
+    assert new_len.tolist() == [min(n, keep) for n in kv]
+    kept_l, rows = kept.tolist(), scores.tolist()
+    want_k, want_v = (x.clone() for x in before)
+    for b, n in enumerate(kv):
+        m = min(n, keep)
+        r = torch.arange(m, device="cuda")
+        dp = dst[b].long()[r // ps]
+        for h in range(H_kv):
+            want = _expected_kept(rows[b][h], n, keep, first, recent)
+            assert kept_l[b][h] == want + [-1] * (keep - m)
+            i = torch.tensor(want, device="cuda", dtype=torch.long)
+            if out is not None:
+                assert torch.equal(out[b, h, :m], scores[b, h][i]) and (out[b, h, m:] == 0).all()
+            sp = c.table[b].long()[i // ps]
+            want_k[dp, r % ps, h], want_v[dp, r % ps, h] = before[0][sp, i % ps, h], before[1][sp, i % ps, h]
+    for got, want in ((c.k_pages, want_k), (c.v_pages, want_v)):
+        assert torch.equal(got.contiguous().view(torch.int16), want.contiguous().view(torch.int16))
+
+
+def _evict_case(kv, H_kv, d, ps, dt, keep, seed, side=False):
+    per = -(-keep // ps)
+    c = Cache([1] * len(kv), kv, H_kv, H_kv, d, ps, dt, seed=seed, spare=per * len(kv) + 2, side=side)
+    dst = c.free[:per * len(kv)].reshape(len(kv), per).contiguous()
+    scores = _score_rows("plain", (len(kv), H_kv, c.table.shape[1] * ps), seed)
+    scores[:, :, 1::3] = 0.25                    # equal ones among them
+    return c, dst, scores
+
+
+# B * H_kv at and around the border between choosing and moving in one kernel
+# and in two (102 of them on 152 SMs), far above it and below
+@pytest.mark.parametrize("B,H_kv,d,ps,dt", [(16, 8, 64, 64, "fp16"), (16, 8, 128, 16, "bf16"), (13, 8, 128, 256, "fp16"),
+                                            (51, 2, 64, 8, "bf16"), (101, 1, 64, 16, "fp16"), (40, 5, 128, 32, "fp16"),
+                                            (3, 8, 128, 64, "fp16")])
+@pytest.mark.parametrize("keep,first,recent", [(96, 4, 20), (70, 0, 0), (64, 40, 24), (1, 0, 0), (130, 0, 129)])
+def test_evict_batches(gpu_lib, B, H_kv, d, ps, dt, keep, first, recent):
+    some = [keep - 1, keep, keep + 1, 300, 1, 0, 129, 260]       # below, at and above keep
+    kv = [some[(3 * i) % 8] for i in range(B)]
+    c, dst, scores = _evict_case(kv, H_kv, d, ps, dt, keep, B + keep, side=B == 13)
+    before = c.k_pages.clone(), c.v_pages.clone()
+    kept, out, new_len = gpu_lib.paged_evict(c.k_pages, c.v_pages, scores, c.table, c.kv_len, dst, keep, first, recent)
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+    check_evicted(c, scores, dst, keep, first, recent, before, kept, out, new_len)
+
+
+def test_evict_batch_of_long_caches(gpu_lib):
+    # a table too wide for keys in shared memory, no scores wanted, tables and
+    # scores of different widths
+    fa = gpu_lib
+    kv = [100, 49500, 3000, 1024, 1500, 700] + [600] * 7
+    keep, first, recent, ps, d, H_kv = 1024, 4, 200, 64, 64, 8
+    c, dst, scores = _evict_case(kv, H_kv, d, ps, "bf16", keep, 5)
+    assert c.table.shape[1] * ps > 49152
+    before = c.k_pages.clone(), c.v_pages.clone()
+    kept = torch.full((len(kv), H_kv, keep), -1, dtype=torch.int32, device="cuda")
+    new_len = torch.empty(len(kv), dtype=torch.int32, device="cuda")
+    rc = fa.fa_paged_evict(c.k_pages, c.v_pages, scores, c.table, c.kv_len, dst, kept, None, new_len, len(kv), H_kv, d,
+                           ps, c.k_pages.shape[0], c.table.shape[1], dst.shape[1], scores.shape[2], ps * H_kv * d, keep,
+                           first, recent)
+    assert rc == fa.FA_OK and fa.fa_check_status() == fa.FA_OK
+    check_evicted(c, scores, dst, keep, first, recent, before, kept, None, new_len)
+
+
+@pytest.mark.parametrize("n,keep,d,ps", [(40001, 5000, 128, 64), (70000, 65537, 64, 256)])
+def test_evict_long_moves_its_rows(gpu_lib, n, keep, d, ps):
+    c, dst, scores = _evict_case([n], 1, d, ps, "fp16", keep, n)
+    before = c.k_pages.clone(), c.v_pages.clone()
+    kept, out, new_len = gpu_lib.paged_evict(c.k_pages, c.v_pages, scores, c.table, c.kv_len, dst, keep, 4, 100)
+    assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
+    check_evicted(c, scores, dst, keep, 4, 100, before, kept, out, new_len)
