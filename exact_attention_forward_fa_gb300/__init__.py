@@ -710,7 +710,8 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
     writes them, in their order, into the pages of ``dst_table``.  Returns
     (kept positions [B, H_kv, keep], their scores, new lengths); entries
     behind a new length are left as they were (-1 and 0 where they are
-    allocated here)."""
+    allocated here).  ``new_len`` may be ``kv_len`` itself; ``scores_out`` is
+    no part of ``scores``."""
     torch = _torch or _use_torch()
     at = scores.get_device()
     if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):

@@ -981,6 +981,12 @@ fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
     return fa::launch_paged_scores(L) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Whether two arrays of 4-byte elements share any (a null one shares none).
+static bool overlap(const void *x, size_t nx, const void *y, size_t ny) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return x && y && a < b + 4 * ny && b < a + 4 * nx;
+}
+
 fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
                          const int32_t *block_table, const int32_t *kv_len,
                          const int32_t *dst_table, int32_t *kept, float *scores_out,
@@ -1002,6 +1008,12 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
         (reinterpret_cast<uintptr_t>(kept) & 3u) || (reinterpret_cast<uintptr_t>(scores_out) & 3u) ||
         (reinterpret_cast<uintptr_t>(new_len) & 3u))
         return FA_ERR_MISALIGNED;
+    // kernels read the scores and kv_len while others write: no shared memory, but
+    // for lengths in place (written last)
+    const size_t heads = static_cast<size_t>(B) * H_kv;
+    if (overlap(scores_out, heads * keep, scores, heads * score_width) ||
+        (new_len != kv_len && overlap(new_len, B, kv_len, B)))
+        return FA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
     a.k_pages = k_pages;

@@ -213,7 +213,7 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
     const float *sc = a.scores + bh * a.L;
     int *kept = a.kept + bh * a.keep;
     float *so = a.scores_out ? a.scores_out + bh * a.keep : nullptr;
-    if (h == 0 && tid == 0) a.new_len[b] = min(n, a.keep);
+    if (h == 0 && tid == 0 && a.new_len != a.kv_len) a.new_len[b] = min(n, a.keep);
     if (n <= a.keep) {
         for (int j = tid; j < n; j += kSelThreads) {
             kept[j] = j;
@@ -376,7 +376,7 @@ static cudaError_t launch_select(const PagedEvictArgs &a, cudaStream_t stream) {
 // bound by HBM behind ~10 us of selection that nothing covers).  With few, moving
 // is spread over the whole device by a kernel of its own, whose CTAs come up while
 // the last selections run (two caches cut to 512: 10.7 us, latency, against 14).
-cudaError_t launch_paged_evict(const PagedEvictArgs &a, int sm_count, cudaStream_t stream) {
+static cudaError_t launch_evict_rows(const PagedEvictArgs &a, int sm_count, cudaStream_t stream) {
     if (static_cast<long long>(a.B) * a.H_kv * 3 >= 2ll * sm_count)
         return a.d == 64 ? launch_select<64>(a, stream) : launch_select<128>(a, stream);
     const cudaError_t e = launch_select<0>(a, stream);
@@ -393,6 +393,20 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, int sm_count, cudaStream
     cfg.numAttrs = 1;
     return a.d == 64 ? cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<64>, a)
                      : cudaLaunchKernelEx(&cfg, fa_paged_move_kernel<128>, a);
+}
+
+// New lengths that replace kv_len itself: every CTA that selects or moves reads
+// kv_len, so they are written when the last of these has ended.
+__global__ void __launch_bounds__(256) fa_paged_len_kernel(const PagedEvictArgs a) {
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b < a.B) a.new_len[b] = evict_len(a, b);
+}
+
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, int sm_count, cudaStream_t stream) {
+    const cudaError_t e = launch_evict_rows(a, sm_count, stream);
+    if (e != cudaSuccess || a.new_len != a.kv_len) return e;
+    fa_paged_len_kernel<<<(a.B + 255) / 256, 256, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace fa

@@ -487,8 +487,10 @@ fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,
  *   kept   : device, int32 [B][H_kv][keep] (written): the kept tokens' old
  *            positions, ascending; entries at and behind new_len[b] are left.
  *   scores_out : device, float [B][H_kv][keep], their scores (as kept), or
- *            NULL.  Not scores itself.
- *   new_len : device, int32 [B] (written): min(kv_len[b], keep).
+ *            NULL.  No part of scores, else FA_ERR_INVALID_ARG.
+ *   new_len : device, int32 [B] (written): min(kv_len[b], keep).  It may be
+ *            kv_len itself, but overlap it in no other way
+ *            (FA_ERR_INVALID_ARG).
  *   keep >= 1, first, recent >= 0, first + recent <= keep.
  * Any 16-bit element type.  kv_len beyond score_width is cut off.
  */

@@ -995,3 +995,41 @@ def test_evict_long_moves_its_rows(gpu_lib, n, keep, d, ps):
     kept, out, new_len = gpu_lib.paged_evict(c.k_pages, c.v_pages, scores, c.table, c.kv_len, dst, keep, 4, 100)
     assert gpu_lib.fa_check_status() == gpu_lib.FA_OK
     check_evicted(c, scores, dst, keep, 4, 100, before, kept, out, new_len)
+
+
+@pytest.mark.parametrize("B,H_kv", [(16, 8), (3, 4)])
+def test_evict_in_place_lengths(gpu_lib, B, H_kv):
+    # the new lengths may replace the old ones where they are
+    fa = gpu_lib
+    kv = [(700 * i) % 1500 + 1 for i in range(B)]
+    keep, first, recent = 200, 4, 50
+    c, dst, scores = _evict_case(kv, H_kv, 64, 16, "bf16", keep, B)
+    before = c.k_pages.clone(), c.v_pages.clone()
+    graph, lens, kept, out = torch.cuda.CUDAGraph(), c.kv_len.clone(), None, None
+    for turn in range(6):
+        for x, y in zip((c.k_pages, c.v_pages), before):
+            x.copy_(y)
+        lens.copy_(c.kv_len)
+        if turn < 2:
+            kept, out, m = fa.paged_evict(c.k_pages, c.v_pages, scores, c.table, lens, dst, keep, first, recent,
+                                          new_len=lens)
+        elif turn == 2:
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                kept, out, m = fa.paged_evict(c.k_pages, c.v_pages, scores, c.table, lens, dst, keep, first, recent,
+                                              new_len=lens)
+        if turn >= 2:
+            graph.replay()
+        assert m is lens and fa.fa_check_status() == fa.FA_OK
+        check_evicted(c, scores, dst, keep, first, recent, before, kept, out, m)
+
+
+def test_evict_refuses_outputs_that_lie_in_its_inputs(gpu_lib):
+    fa = gpu_lib
+    c, dst, scores = _evict_case([200, 300], 2, 64, 16, "bf16", 320, 1)
+    scores = scores[:, :, :320].contiguous()
+    lens = torch.tensor([200, 300, 0], dtype=torch.int32, device="cuda")
+    for kw in (dict(scores_out=scores), dict(new_len=lens[1:])):
+        with pytest.raises(fa.FaError):
+            fa.paged_evict(c.k_pages, c.v_pages, scores, c.table, lens[:2], dst, 320, **kw)
+    assert fa.fa_check_status() == fa.FA_OK and lens.tolist() == [200, 300, 0]

@@ -180,3 +180,19 @@ def test_wrappers_refuse_outputs():
 def test_append_wrapper_refuses(k, v):
     with pytest.raises(ValueError):
         fa.paged_append(k, v, **_cache())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=3, nl=A + 4), dict(B=3, kl=A + 8), dict(so=A), dict(so=A + 4 * 63), dict(s=A + 4 * 31, so=A),
+])
+def test_evict_refuses_overlapping_arrays(lib, kw):
+    # [1][2][32] scores, [1][2][16] kept ones; lengths shifted against the old ones
+    assert _evict(lib, **kw) == INV
+
+
+@pytest.mark.parametrize("kw", [dict(B=3, nl=A + 12), dict(B=3, kl=A + 12), dict(so=A + 4 * 64), dict(s=A + 4 * 32, so=A),
+                                dict(B=3)])
+def test_evict_takes_neighbours_and_lengths_in_place(lib, kw):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present; covered by the gpu tests")
+    assert _evict(lib, **kw) in (fa.FA_ERR_CUDA, fa.FA_ERR_UNSUPPORTED)
