@@ -162,10 +162,11 @@ struct FwdCfg {
     static constexpr float TAU = kFP8 ? 4.8f : 8.0f;
     static constexpr float P_OFFSET = kFP8 ? 4.0f : 0.0f;
     // 16-bit P is first formed against the current reference r and kept
-    // when the tile's FP32 row sum is <= 2^16.  The sum bounds every term,
-    // so a kept tile has P <= 2^16; a tile that fails has a term > 2^16/128
-    // = 2^9 > 2^tau, so its row max grew by more than tau and r moves.
-    static constexpr float KEEP_SUM = 65536.0f;
+    // when the tile's FP32 row sum is <= 2^16, in fp16 <= 65504, the largest
+    // number there (a term above 65520 would round to infinity).  The sum
+    // bounds every term of a kept tile; a tile that fails has a term
+    // > 65504/128 > 2^tau, so its row max grew by more than tau and r moves.
+    static constexpr float KEEP_SUM = kBF16 ? 65536.0f : 65504.0f;
 };
 
 // The geometry of one work unit, identical in every role.

@@ -10,6 +10,7 @@ other sweep points are compared on sampled (b, h, row) outputs that the
 oracle computes one by one.  Exact pins: causal row 0 reproduces V[0] bit for bit, a constant V
 gives that constant, and two launches give identical bits.
 """
+import math
 import os
 
 import numpy as np
@@ -453,3 +454,33 @@ def test_sampled_many_units(gpu_lib):
     # B32 H64 N640: 2048 heads, 6144 work units -- many waves of the
     # persistent grid; heads sampled at both ends and in between.
     _sampled(gpu_lib, 32, 64, 640, 64, True, n_heads=4, n_rows=8)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("peak", [14.9999, 15.0001, 15.9985, 15.99975, 15.99995, 16.0001])
+def test_one_score_far_above(gpu_lib, d, dt, tile, peak):
+    # 2^peak against a reference of 0 from other tiles: terms at the edge of
+    # fp16's range.  P is rounded to the type (u, its half step) in numerator
+    # and denominator alike and O once more: |dO| <= u (A + |O|) + u |O|, A the
+    # softmax-weighted |v|; 5 % for second-order terms and the FP32 sums.  LSE
+    # may be that of the rounded terms (d = 64): off by log(1 + u), and 2^-17
+    # for the FP32 scale, exponent (16 log2 units), exp2, log2 and the sums.
+    n, t, u = 384, DT[dt], {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}[dt]
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k = (torch.zeros(1, n, 2, d, dtype=t, device="cuda") for _ in range(2))
+    v = torch.randn(1, n, 2, d, generator=g, device="cuda").to(t)
+    q[..., 0] = 1
+    k[:, 128 * tile:128 * tile + 128, :, 0] = -10
+    k[:, 128 * tile + 5, :, 0] = 1
+    alpha = peak * math.log(2)
+    o, lse = gpu_lib.attention(q, k, v, alpha=alpha)
+    torch.cuda.synchronize()
+    s = alpha * torch.einsum("bihd,bjhd->bhij", q.double(), k.double())
+    w = torch.softmax(s, -1)
+    ref = torch.einsum("bhij,bjhd->bihd", w, v.double())
+    mag = torch.einsum("bhij,bjhd->bihd", w, v.double().abs())
+    assert torch.isfinite(o).all()
+    assert ((o.double() - ref).abs() <= 1.05 * u * (mag + 2 * ref.abs()) + 1e-6).all()
+    assert (lse.double() - torch.logsumexp(s, -1)).abs().max() <= 1.01 * u + 2.0 ** -17
