@@ -507,6 +507,13 @@ def _check_int(x, shape, at: int) -> None:
         raise ValueError("tensors on different devices")
 
 
+def _check_int32(*xs) -> None:
+    """Numbers that a C int holds (ctypes would keep the lowest 32 bits of others)."""
+    for x in xs:
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{x} does not fit 32 bits")
+
+
 def _check_float(x, shape, at: int) -> None:
     if x.dtype is not _torch.float32 or x.shape != shape or not x.is_contiguous() or x.get_device() != at:
         raise ValueError(f"expected a contiguous float32 {tuple(shape)} on GPU {at}, got {x.dtype} "
@@ -620,6 +627,7 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
                                    alpha, out, lse, want_lse, workspace)
     T, H, d = q.shape
     B, W = block_table.shape
+    _check_int32(max_q, window[0], window[1], first)
     _check_paged(at, dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
@@ -677,6 +685,7 @@ def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=
                                 alpha, out)
     T, H, d = q.shape
     B, W = block_table.shape
+    _check_int32(max_q, window[0], window[1], first)
     _check_paged(at, dtype, k_pages, None, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
@@ -720,6 +729,7 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
                                recent, kept, scores_out, new_len)
     B, W = block_table.shape
     Wd = dst_table.shape[1]
+    _check_int32(keep, first, recent)
     _check_paged(at, k_pages.dtype, k_pages, v_pages, block_table, kv_len, dst_table, (B, Wd))
     n, ps, hk, d = k_pages.shape
     L = scores.shape[2]

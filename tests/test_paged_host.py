@@ -196,3 +196,24 @@ def test_evict_takes_neighbours_and_lengths_in_place(lib, kw):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present; covered by the gpu tests")
     assert _evict(lib, **kw) in (fa.FA_ERR_CUDA, fa.FA_ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("kw", [dict(window=(2**32, 0)), dict(window=(-1, 2**32)), dict(first=2**32 + 4),
+                                dict(max_q=2**32 + 1), dict(window=(-2**31 - 1, 0)), dict(window=(2**63, 0))])
+def test_wrappers_refuse_numbers_beyond_32_bits(kw):
+    # ctypes passes their lowest 32 bits: a window of 2**32 tokens would be one of none
+    q, kw = torch.zeros(3, 4, 64, dtype=torch.bfloat16), {"max_q": 3, **kw}
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.attention_paged(q, **_cache(), **kw)
+    c = _cache()
+    c.pop("v_pages")
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.paged_scores(q, torch.zeros(4, 3), **c, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(keep=2**32 + 8), dict(first=2**32), dict(recent=2**32)])
+def test_evict_wrapper_refuses_numbers_beyond_32_bits(kw):
+    c, kw = _cache(), {"keep": 8, **kw}
+    c.pop("cu_q")
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.paged_evict(scores=torch.zeros(1, 2, 32), dst_table=torch.zeros(1, 1, dtype=torch.int32), **c, **kw)
