@@ -542,6 +542,8 @@ class _launch_on:
         if isinstance(stream, int):
             stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                       else torch.cuda.default_stream(device))
+        elif stream is not None and stream.device != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
         self.ctx = torch.cuda.stream(stream) if stream is not None else None
         self.guard = (torch.cuda.device(device)
                       if device.index != torch.cuda.current_device() else None)

@@ -217,3 +217,12 @@ def test_evict_wrapper_refuses_numbers_beyond_32_bits(kw):
     c.pop("cu_q")
     with pytest.raises(ValueError, match="32 bits"):
         fa.paged_evict(scores=torch.zeros(1, 2, 32), dst_table=torch.zeros(1, 1, dtype=torch.int32), **c, **kw)
+
+
+def test_a_stream_of_another_device_is_refused():
+    # (the call would have gone to the current stream of the tensors' device)
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        fa._launch_on(torch.device("cuda", 0), Stream())
