@@ -485,7 +485,7 @@ def _check_paged(at: int, dtype, k, v, block_table, kv_len, last, last_shape) ->
         raise ValueError("the pages and the new tokens differ in type")
     n, ps, hk, d = shape
     st = k.stride()
-    if st[3] != 1 or st[2] != d or st[1] != hk * d:
+    if st[3] != 1 or (st[2] != d and hk > 1) or st[1] != hk * d:
         raise ValueError("a page's rows [page_size, H_kv, d] must be contiguous")
     if k.get_device() != at:
         raise ValueError("tensors on different devices")

@@ -1033,3 +1033,16 @@ def test_evict_refuses_outputs_that_lie_in_its_inputs(gpu_lib):
         with pytest.raises(fa.FaError):
             fa.paged_evict(c.k_pages, c.v_pages, scores, c.table, lens[:2], dst, 320, **kw)
     assert fa.fa_check_status() == fa.FA_OK and lens.tolist() == [200, 300, 0]
+
+
+def test_pages_of_one_head_in_either_order(gpu_lib):
+    c = Cache([2, 1], [100, 33], 4, 1, 64, 16, seed=2)
+    want = attend(gpu_lib, c)
+    for name in ("k_pages", "v_pages"):
+        pages = getattr(c, name)
+        n, ps, hk, d = pages.shape
+        other = torch.empty(n, hk, ps, d, dtype=pages.dtype, device="cuda").transpose(1, 2)
+        setattr(c, name, other.copy_(pages))
+    assert c.k_pages.stride(2) != 64
+    got = attend(gpu_lib, c)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -226,3 +226,14 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="cuda:1"):
         fa._launch_on(torch.device("cuda", 0), Stream())
+
+
+def test_pages_of_one_head_in_either_order():
+    # [n, 1, page_size, d] seen as [n, page_size, 1, d]: whole rows, whatever the
+    # stride between heads that there is only one of
+    c = _cache(hk=1)
+    for name in ("k_pages", "v_pages"):
+        c[name] = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16).transpose(1, 2)
+        assert c[name].stride(2) != 64
+    with pytest.raises(ValueError, match="must be on the GPU"):
+        fa.attention_paged(torch.zeros(3, 4, 64, dtype=torch.bfloat16), max_q=3, **c)
