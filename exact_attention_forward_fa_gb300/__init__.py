@@ -507,11 +507,8 @@ def _check_int(x, shape, at: int) -> None:
         raise ValueError("tensors on different devices")
 
 
-def _check_int32(*xs) -> None:
-    """Numbers that a C int holds (ctypes would keep the lowest 32 bits of others)."""
-    for x in xs:
-        if not -0x80000000 <= x <= 0x7fffffff:
-            raise ValueError(f"{x} does not fit 32 bits")
+# ctypes would keep the lowest 32 bits of a number that a C int does not hold.
+_BEYOND_32 = "windows and counts have to fit 32 bits"
 
 
 def _check_float(x, shape, at: int) -> None:
@@ -629,7 +626,10 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
                                    alpha, out, lse, want_lse, workspace)
     T, H, d = q.shape
     B, W = block_table.shape
-    _check_int32(max_q, window[0], window[1], first)
+    left, right = window
+    if not (-0x80000000 <= max_q <= 0x7fffffff and -0x80000000 <= left <= 0x7fffffff
+            and -0x80000000 <= right <= 0x7fffffff and -0x80000000 <= first <= 0x7fffffff):
+        raise ValueError(_BEYOND_32)
     _check_paged(at, dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
@@ -663,7 +663,7 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
             kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
             workspace.data_ptr(), B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha,
-            window[0], window[1], first, FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
+            left, right, first, FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
     finally:
         if shared:
             _paged_ws_lock.release()
@@ -687,7 +687,10 @@ def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=
                                 alpha, out)
     T, H, d = q.shape
     B, W = block_table.shape
-    _check_int32(max_q, window[0], window[1], first)
+    left, right = window
+    if not (-0x80000000 <= max_q <= 0x7fffffff and -0x80000000 <= left <= 0x7fffffff
+            and -0x80000000 <= right <= 0x7fffffff and -0x80000000 <= first <= 0x7fffffff):
+        raise ValueError(_BEYOND_32)
     _check_paged(at, dtype, k_pages, None, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dk = k_pages.shape
     qs = _packed_stride(q, "q")
@@ -707,7 +710,7 @@ def paged_scores(q, lse, k_pages, block_table, kv_len, cu_q, max_q: int, scores=
     rc = load().fa_paged_scores(
         q.data_ptr(), lse.data_ptr(), k_pages.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(),
         cu_q.data_ptr(), None if scores is None else scores.data_ptr(), out.data_ptr(), B, H, hk, T,
-        max_q, d, ps, n, W, shape[2], qs, k_pages.stride(0), alpha, window[0], window[1], first,
+        max_q, d, ps, n, W, shape[2], qs, k_pages.stride(0), alpha, left, right, first,
         FA_BF16 if dtype is torch.bfloat16 else FA_FP16, torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_scores")
@@ -731,7 +734,9 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
                                recent, kept, scores_out, new_len)
     B, W = block_table.shape
     Wd = dst_table.shape[1]
-    _check_int32(keep, first, recent)
+    if not (-0x80000000 <= keep <= 0x7fffffff and -0x80000000 <= first <= 0x7fffffff
+            and -0x80000000 <= recent <= 0x7fffffff):
+        raise ValueError(_BEYOND_32)
     _check_paged(at, k_pages.dtype, k_pages, v_pages, block_table, kv_len, dst_table, (B, Wd))
     n, ps, hk, d = k_pages.shape
     L = scores.shape[2]
