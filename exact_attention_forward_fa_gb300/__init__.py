@@ -617,7 +617,8 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
     window = (left, right) key bounds around a token's position (-1: none),
     the first ``first`` tokens visible beside a left bound.  ``max_q``: the
     most new tokens of one sequence.  Returns (O [T, H, d], LSE [H, T] or
-    None)."""
+    None); rows behind cu_q[B] (a padded batch) are left as they were,
+    uninitialised where O and LSE are allocated here."""
     torch = _torch or _use_torch()
     at, dtype = q.get_device(), q.dtype
     if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):

@@ -117,8 +117,8 @@ struct PagedBox {
         row = (lane / kChunks) * box;
         c = lane % kChunks;
     }
-    // The page that this lane's box of tile j needs, when a row sees tokens
-    // [vlo, vhi) or [0, nf); otherwise n_pages, which TMA reads as zeros.
+    // Whether this lane has a box of tile j that holds tokens which a row sees,
+    // [vlo, vhi) or [0, nf).  (Others are loaded from page n_pages: TMA gives zeros.)
     __device__ __forceinline__ bool needs(int j, int vlo, int vhi, int nf) const {
         const int tok = j * 128 + row;
         return (threadIdx.x & 31) < n_box && ((tok < vhi && tok + box > vlo) || tok < nf);

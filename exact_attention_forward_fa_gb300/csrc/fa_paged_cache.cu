@@ -11,8 +11,8 @@ namespace fa {
 // One warp per token: its lanes copy the token's 16-byte vectors, all loads
 // of a pass issued before the stores, and the loads of the first pass before
 // the search for the token's sequence, whose latency they hide.  64 single tokens
-// of 8 heads of 128: 2.7 us, the latency of a launch and of three dependent loads;
-// four chunks, 10240 tokens (84 MB in and out): 15.3 us, 5.5 TB/s.
+// of 8 heads of 128: 3.4 us, the latency of a launch and of three dependent loads;
+// four chunks, 10240 tokens (84 MB in and out): 16.2 us, 5.2 TB/s.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) fa_paged_append_kernel(const PagedAppendArgs a) {
     if (blockIdx.x == gridDim.x - 1)                     // the last block only checks
@@ -325,7 +325,8 @@ __device__ __forceinline__ void select_tokens(const PagedEvictArgs &a, const boo
 
 // D != 0: the CTA then moves the rows that it chose.  Those that stay anyway need not
 // wait for the choice: CTAs of their own (z = 1) move the first and the last ones,
-// or all of a short cache, meanwhile.
+// or all of a short cache.  A CTA takes an SM's whole register file (1024 threads of 64),
+// so these run on the SMs that no choosing CTA has, the others behind them.
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) fa_paged_select_kernel(const PagedEvictArgs a, const bool staged) {
     extern __shared__ uint32_t held[];
@@ -372,10 +373,18 @@ static cudaError_t launch_select(const PagedEvictArgs &a, cudaStream_t stream) {
 
 // With a (sequence, K/V head) for most of the SMs the CTA that selects also
 // moves: short caches move while long ones still select (sixteen caches cut to
-// 2048 tokens of 8 heads, 268 MB: 56.5 us, 4.8 TB/s, against 62 with two kernels;
-// bound by HBM behind ~10 us of selection that nothing covers).  With few, moving
-// is spread over the whole device by a kernel of its own, whose CTAs come up while
-// the last selections run (two caches cut to 512: 10.7 us, latency, against 14).
+// 2048 tokens of 8 heads, 268 MB: 57 us, 4.7 TB/s; bound by HBM behind ~10 us of
+// selection that nothing covers).  With few, moving is spread over the whole device
+// by a kernel of its own, launched when the last selection ends (two caches cut to
+// 512: 12.3 us, latency).  The border, two kernels against one, in us: caches of up to
+// 2048 cut to 512, of up to 16384 cut to 2048 (d = 128) and of up to 6000 cut to 1024
+// (d = 64), 8 heads:
+//     16 pairs   11.3 / 14.4    22 / 43    13.3 / 18.4
+//     64         15.5 / 15.5    43 / 48    17.5 / 18.5
+//     96         19.4 / 17.5    55 / 53    21.7 / 20.0
+//     128        24.6 / 21.6    65 / 61    27.5 / 22.6
+//     152        26.6 / 24.7    74 / 76    28.9 / 27.1
+//     256        42.5 / 38.9   119 / 108   46.8 / 42.0
 static cudaError_t launch_evict_rows(const PagedEvictArgs &a, int sm_count, cudaStream_t stream) {
     if (static_cast<long long>(a.B) * a.H_kv * 3 >= 2ll * sm_count)
         return a.d == 64 ? launch_select<64>(a, stream) : launch_select<128>(a, stream);

@@ -15,17 +15,23 @@
 //     chain QK -> softmax -> PV is longer than its tensor work, and two of them
 //     side by side overlap (1850 to 2300 cycles a step).
 //
+// P is rounded to the 16-bit type (fa_paged_token_kernel.cuh tells what that costs).
+//
 // Measured.  Bound by the tensor core and each tile's chain QK -> softmax -> PV,
-// whose parts cannot overlap within a tile (S and P share their columns):
-// ~3400 cycles a step of two tiles, 2180 of them tensor work, as in the dense
-// forward (~3090).  Three chunks of 1100 to 1200 tokens on caches of up to 14516
-// (32 heads over 8, d = 128): 550 us, 1300 TFLOP/s.  24 sequences with 1 to 300 new
-// tokens on caches of up to 4096: 85 us, of which ~4 pass before a CTA's first
-// scores and up to 10 go to the joining kernel's 152 cut units and its launch.
+// whose parts cannot overlap within a tile (S and P share their columns; at d = 128
+// there are no others, at d = 64 128 columns lie idle): ~3400 cycles a step of two
+// tiles, 2180 of them tensor work, as in the dense forward (~3090).  Three chunks of
+// 1100 to 1200 tokens on caches of up to 14516 (32 heads over 8, d = 128): 548 us,
+// 1305 TFLOP/s; 575 to 595 in long runs, under the power cap.  24 sequences with 1 to
+// 300 new tokens on caches of up to 4096: 86 us, of which ~4 pass before a CTA's first
+// scores, up to 10 go to the joining kernel's 152 cut units and its launch, and some
+// to shares that count a step of one tile like one of two.  At d = 128 the epilogue of
+// units with one tile spills (172 bytes: both groups' accumulators are held at once).
 // Tried: an issuing warp for each Q tile (750 us for the chunks) and the issuer's
 // loop unrolled for both tiles (608): both are code that pushes the softmax out
-// of the instruction cache; shares weighted by the time of a step with one tile
-// and with two (the batch 99 us: weights are then summed by every CTA at the start).
+// of the instruction cache; shares in which a step of two tiles counts twice (the
+// batch 99 us; by the cycles it is 3 : 2 to 5 : 3, and units had no cost of their own
+// then).
 //
 // Warps: 0-3 and 4-7 the softmax groups, 8 and 11 the TMA producers of K and V
 // (all lanes: one box of a page each), 9 the MMA issuer, 10 walks the share and

@@ -31,8 +31,9 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     kern<<<L.grid, C::NTHREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.k, L.v, L.a, L.w, L.R);
     e = cudaGetLastError();
     if (e != cudaSuccess || L.grid == 1) return e;  // one share: nothing is cut
-    // The joining kernel's CTAs are brought up while the attention's last ones
-    // run; it waits for their results itself (griddepcontrol.wait).
+    // The joining kernel is launched when every CTA of the attention is at its end
+    // (their last statement lets it come), so that its launch overlaps their
+    // teardown, nothing more; it waits for their results itself (griddepcontrol.wait).
     const int rows = (kFew ? 1 : 2) * L.R * L.a.group;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.grid, rows < 8 ? rows : 8);
@@ -47,8 +48,8 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
 }
 
 // Up to kFewRows rows a tile: few rows against each K/V tile, bound by HBM.  64
-// single tokens of 4 heads a group (4 rows) 180 us, one on 777 tokens 11.6, 4 rows of
-// d = 64 with a window 60; the chunk kernel with 16 rows 190, 13.6 and 87.
+// single tokens of 4 heads a group (4 rows) on up to 8192 188 us, one on 777 tokens 11.8,
+// up to 4 rows of d = 64 with a window 60; the chunk kernel 197, 12.8 and 89 for the same.
 template <int D>
 cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
     if (L.R * L.a.group <= kFewRows)

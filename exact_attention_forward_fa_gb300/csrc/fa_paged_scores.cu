@@ -16,8 +16,8 @@
 //
 // Two forms, by the rows of a Q tile (R positions x g heads).
 //   * kN = 32, up to 32 rows (decoding: one token of up to 32 heads a group).
-//     The product has N = 32, the kernel reads K at the rate of HBM: 50.5 us,
-//     5.5 TB/s, for 32 sequences of up to 8192 tokens (8 K/V heads, d = 128);
+//     The product has N = 32, the kernel reads K at the rate of HBM: 51.9 us,
+//     5.4 TB/s, for 32 sequences of up to 8192 tokens (8 K/V heads, d = 128);
 //     launch and first tiles are ~6 us of it.  Small Q tiles leave room for six K tiles
 //     instead of four: the bytes in flight.  Each group's S^T is
 //     double-buffered.  A warp of its own (12) loads group 1's K tiles: a tile of
@@ -27,7 +27,7 @@
 //     takes it as its A operand.  From shared memory K would be read again for
 //     every Q tile, which with Q's own reads and writes and the log-sum-exps
 //     (32 16-byte loads a warp and tile) fills its 128 bytes a clock: 100 us
-//     against 93.5 (940 TFLOP/s) for chunks of 973 and 742 tokens on caches of
+//     against 94.5 (928 TFLOP/s) for chunks of 973 and 742 tokens on caches of
 //     7947 and 5023 (32 heads over 8, d = 128).  TMEM then has room for three S^T
 //     buffers, which the two groups take in turn.
 //     A pair of tiles takes ~2000 cycles: 1090 of tensor work, 1024 of exponentials
@@ -591,8 +591,8 @@ static cudaError_t launch_scores_inst(const PagedScoresLaunch &L) {
     return cudaGetLastError();
 }
 
-// Up to 32 rows a Q tile the narrow form: 64 sequences of 4 tokens on up to 8192 97 us
-// (the other 138), of 8 tokens 97.5 (138), one of 4 tokens on 777 7.1 (8.4).
+// Up to 32 rows a Q tile the narrow form: 64 sequences of 4 tokens on up to 8192 103 us
+// (the other 154), of 8 tokens 103 (153), one of 4 tokens on 777 6.7 (8.2).
 template <int D>
 static cudaError_t launch_scores_dispatch(const PagedScoresLaunch &L) {
     if (L.R * L.a.group <= 32)

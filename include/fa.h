@@ -369,8 +369,9 @@ fa_status fa_bwd_noalloc(const void *q, const void *k, const void *v,
  * B + 1 entries, ascending) of tensors with total_q rows are sequence b's
  * last cached tokens, kv_len[b] counts them, and row cu_q[b] + i has position
  * kv_len[b] - (cu_q[b + 1] - cu_q[b]) + i.  A sequence may have none.  Rows
- * at and behind cu_q[B] are neither read nor written.  With total_q = 0 the
- * packed tensors may be NULL.
+ * at and behind cu_q[B] may hold anything and are not written (what a call
+ * reads ahead there it drops).  With total_q = 0 the packed tensors may be
+ * NULL.
  *
  * block_table, kv_len and cu_q are device int32, so lengths may change from
  * one replay of a captured graph to the next.  What is out of range there (a
