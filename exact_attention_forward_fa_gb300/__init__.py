@@ -38,6 +38,7 @@ FA_SCALE_TENSOR = 2
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_gqa_packed", "fa_fwd_ext", "fa_fwd_splitkv", "fa_splitkv_workspace_floats",
            "fa_splitkv_auto", "fa_quantize_fp8", "fa_quantize_fp8_granular", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_bwd", "fa_bwd_ext", "fa_bwd_noalloc",
            "fa_paged_append", "fa_fwd_paged", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
+           "fa_rope", "fa_paged_rope_append",
            "fa_check_status", "fa_status_detail", "fa_selftest_wait_timeout",
            "fa_status_string", "fa_version")
 
@@ -101,6 +102,10 @@ def load():
     lib.fa_paged_scores.restype = i
     lib.fa_paged_evict.argtypes = [vp] * 9 + [i] * 8 + [ll, i, i, i, vp]
     lib.fa_paged_evict.restype = i
+    lib.fa_rope.argtypes = [vp] * 6 + [i] * 6 + [ll] * 4 + [f, i, i, i, vp]
+    lib.fa_rope.restype = i
+    lib.fa_paged_rope_append.argtypes = [vp] * 11 + [i] * 9 + [ll] * 4 + [f, i, i, vp]
+    lib.fa_paged_rope_append.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [vp, vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_check_status.argtypes = [vp]
@@ -763,6 +768,211 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_evict")
     return kept, scores_out, new_len
+
+
+# ---- rotary positions (see include/fa.h) ----
+
+def fa_rope(q, k, q_out, k_out, positions, inv_freq, B: int, N: int, H: int, H_kv: int, d: int,
+            rot_dim: int, q_stride: int, k_stride: int, q_out_stride: int, k_out_stride: int,
+            scale: float, interleaved: int, inverse: int, dtype: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``k``, ``k_out``
+    and ``positions`` may be None."""
+    return load().fa_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(positions),
+                          _ptr(inv_freq), B, N, H, H_kv, d, rot_dim, q_stride, k_stride,
+                          q_out_stride, k_out_stride, scale, interleaved, inverse, dtype,
+                          _stream(stream))
+
+
+def fa_paged_rope_append(q, k, v, q_out, k_pages, v_pages, block_table, kv_len, cu_q, offsets,
+                         inv_freq, B: int, H: int, H_kv: int, d: int, rot_dim: int, total_q: int,
+                         page_size: int, n_pages: int, table_width: int, q_stride: int,
+                         kv_stride: int, q_out_stride: int, page_stride: int, scale: float,
+                         interleaved: int, dtype: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``offsets`` may be
+    None."""
+    return load().fa_paged_rope_append(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+        _ptr(kv_len), _ptr(cu_q), _ptr(offsets), _ptr(inv_freq), B, H, H_kv, d, rot_dim, total_q,
+        page_size, n_pages, table_width, q_stride, kv_stride, q_out_stride, page_stride, scale,
+        interleaved, dtype, _stream(stream))
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original: int = 0, beta=(32.0, 1.0), device="cuda"):
+    """(inv_freq, scale) for ``rope`` and ``paged_rope_append``: radians a
+    position for each of the rot_dim / 2 pairs, float64 on ``device``, and the
+    factor of the rotated values.  Contexts ``factor`` times as long as those
+    trained on:
+
+    * None: inv_freq[c] = base ** (-2c / rot_dim);
+    * "linear": positions interpolated, inv_freq / factor;
+    * "ntk": base grown by factor ** (rot_dim / (rot_dim - 2));
+    * "yarn": pairs that turn more than beta[0] times within the first
+      ``original`` positions stay, those that turn less than beta[1] times are
+      interpolated, a ramp between; scale = 0.1 ln(factor) + 1.
+    """
+    import torch
+    if rot_dim < 2 or rot_dim % 2 or not base > 1.0 or not factor >= 1.0:
+        raise ValueError("rot_dim is even and positive, base > 1, factor >= 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
+    w, scale = base ** -i, 1.0
+    if scaling == "linear":
+        w = w / factor
+    elif scaling == "ntk":
+        if rot_dim == 2:
+            raise ValueError("ntk scaling needs more than one pair")
+        w = (base * factor ** (rot_dim / (rot_dim - 2))) ** -i
+    elif scaling == "yarn":
+        if original < 1:
+            raise ValueError("yarn scaling needs the original context length")
+        # the pairs that turn beta times within the original context
+        lo, hi = (rot_dim * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in beta)
+        lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rot_dim - 1)
+        ramp = ((torch.arange(rot_dim // 2, dtype=torch.float64) - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        w = w / factor * ramp + w * (1 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling is not None:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return w.to(device), scale
+
+
+def _check_turns(inv_freq, d: int, at: int) -> int:
+    """rot_dim of a frequency tensor."""
+    if inv_freq.dtype is not _torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq is a contiguous float64 [rot_dim / 2]")
+    if inv_freq.get_device() != at:
+        raise ValueError("tensors on different devices")
+    return 2 * inv_freq.shape[0]
+
+
+def _rows_stride(x, name: str) -> int:
+    """The elements between the tokens of a [B, N, heads, d] or [T, heads, d]
+    tensor whose tokens follow one another at one distance."""
+    s, shape = x.stride(), x.shape
+    heads, d = shape[-2:]
+    if x.numel() and (s[-1] != 1 or (s[-2] != d and heads > 1)):
+        raise ValueError(f"{name} has contiguous [heads, d] rows")
+    if len(shape) == 3:
+        return s[0] if shape[0] > 1 else heads * d
+    B, N = shape[:2]
+    step = s[1] if N > 1 else s[0] if B > 1 else heads * d
+    if B > 1 and N > 1 and s[0] != N * step:
+        raise ValueError(f"{name}: the tokens of all sequences follow at one distance")
+    return step
+
+
+def _dtype_of(x) -> int:
+    if x.dtype is _torch.bfloat16:
+        return FA_BF16
+    if x.dtype is _torch.float16:
+        return FA_FP16
+    raise TypeError(f"unsupported dtype {x.dtype}")
+
+
+def _like(x, ref, name: str) -> None:
+    if x.dtype is not ref.dtype or x.get_device() != ref.get_device():
+        raise ValueError(f"{name} differs in type or device")
+
+
+def rope(q, k, inv_freq, positions=None, scale: float = 1.0, interleaved: bool = False,
+         inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [B, N, H, d] and k [B, N, H_kv, d] (or packed
+    [T, heads, d]; k may be None; slices of wider rows are fine).  inv_freq
+    float64 [rot_dim / 2] radians a position (``rope_frequencies``), positions
+    int32 [B, N] (or [T]; None: a token's place in its sequence), interleaved:
+    pairs of neighbours instead of halves.  ``inverse`` turns back: the gradient
+    of the inputs from that of the outputs.  q_out and k_out may be q and k
+    themselves.  Returns (q_out, k_out or None)."""
+    torch = _torch or _use_torch()
+    at = q.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
+            return rope(q, k, inv_freq, positions, scale, interleaved, inverse, q_out, k_out)
+    dt = _dtype_of(q)
+    shape = q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError("q is [B, N, H, d] or [T, H, d]")
+    lead, (H, d) = shape[:-2], shape[-2:]
+    rot = _check_turns(inv_freq, d, at)
+    if positions is not None:
+        _check_int(positions, lead, at)
+    qs, ks, kos, hk = _rows_stride(q, "q"), 0, 0, 0
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != shape:
+        raise ValueError("q_out differs from q in shape")
+    _like(q_out, q, "q_out")
+    if k is not None:
+        hk = k.shape[-2]
+        if k.shape != (*lead, hk, d):
+            raise ValueError("q and k differ in tokens or head dim")
+        _like(k, q, "k")
+        ks = _rows_stride(k, "k")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out differs from k in shape")
+        _like(k_out, q, "k_out")
+        kos = _rows_stride(k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if at < 0:
+        raise ValueError("tensors must be on the GPU")
+    if 0 in lead:
+        return q_out, k_out
+    B, N = lead if len(lead) == 2 else (1, lead[0])
+    rc = load().fa_rope(
+        q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+        None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
+        inv_freq.data_ptr(), B, N, H, hk, d, rot, qs, ks, _rows_stride(q_out, "q_out"), kos, scale,
+        int(bool(interleaved)), int(bool(inverse)), dt, torch._C._cuda_getCurrentRawStream(at))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_rope")
+    return q_out, k_out
+
+
+def paged_rope_append(q, k, v, k_pages, v_pages, block_table, kv_len, cu_q, inv_freq,
+                      scale: float = 1.0, interleaved: bool = False, offsets=None, q_out=None,
+                      stream=None):
+    """``paged_append`` with rotary positions: rotates the new tokens' q
+    (packed [T, H, d]) into q_out (None: a new tensor; q itself is fine),
+    writes their rotated k and their v (packed [T, H_kv, d]) into their pages.
+    A token at place p of sequence b has position p + offsets[b] (int32 [B],
+    None: zeros); inv_freq, scale, interleaved as in ``rope``.  Returns q_out;
+    its rows behind cu_q[B] are left as they were."""
+    torch = _torch or _use_torch()
+    at, dtype = q.get_device(), q.dtype
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
+            return paged_rope_append(q, k, v, k_pages, v_pages, block_table, kv_len, cu_q, inv_freq,
+                                     scale, interleaved, offsets, q_out)
+    B, W = block_table.shape
+    T, H, d = q.shape
+    _check_paged(at, dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
+    n, ps, hk, dp = k_pages.shape
+    qs, ks = _packed_stride(q, "q"), _packed_stride(k, "k")
+    if (k.shape != v.shape or k.dtype is not dtype or v.dtype is not dtype or k.get_device() != at
+            or v.get_device() != at or _packed_stride(v, "v") != ks):
+        raise ValueError("k and v differ in type, shape, strides or device")
+    if k.shape != (T, hk, d) or d != dp:
+        raise ValueError("q, k, v and the pages differ in tokens, heads or head dim")
+    rot = _check_turns(inv_freq, d, at)
+    if offsets is not None:
+        _check_int(offsets, (B,), at)
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.get_device() != at:
+        raise ValueError("q_out differs from q in type, shape or device")
+    rc = load().fa_paged_rope_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), inv_freq.data_ptr(), B, H, hk, d, rot, T, ps,
+        n, W, qs, ks, _packed_stride(q_out, "q_out"), k_pages.stride(0), scale,
+        int(bool(interleaved)), FA_BF16 if dtype is torch.bfloat16 else FA_FP16,
+        torch._C._cuda_getCurrentRawStream(at))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_paged_rope_append")
+    return q_out
 
 
 def fa_selftest_wait_timeout(result, stream=None) -> int:

@@ -12,6 +12,7 @@
 #include "fa.h"
 #include "fa_launch.cuh"
 #include "fa_paged.cuh"
+#include "fa_rope.cuh"
 
 namespace {
 
@@ -1039,6 +1040,145 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
     a.recent = recent;
     return fa::launch_paged_evict(a, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FA_OK : FA_ERR_CUDA;
+}
+
+// ---- rotary positions ----
+
+// Whether rows of two packed tensors, `w` elements wide and `s` apart, share
+// memory: T rows each; equal strides may interleave (slices of wider rows).
+static bool rows_overlap(const void *x, long long wx, long long sx, const void *y, long long wy,
+                         long long sy, long long T) {
+    if (!x || !y || T < 1) return false;
+    const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
+    if (a >= b + 2 * ((T - 1) * sy + wy) || b >= a + 2 * ((T - 1) * sx + wx)) return false;
+    if (sx != sy) return true;
+    const long long row = 2 * sx, off = ((b - a) % row + row) % row;     // y's columns begin at off
+    return off < 2 * wx || off + 2 * wy > row;
+}
+
+// What both rotary entry points check of sizes and pointers, laid out.
+static fa_status rope_args(fa::RopeArgs *a, const void *q, const void *k, void *q_out,
+                           const double *inv_freq, int T, int H, int H_kv, int d, int rot_dim,
+                           long long q_stride, long long k_stride, long long qo_stride, float scale,
+                           int interleaved, fa_dtype dtype) {
+    std::memset(a, 0, sizeof(*a));
+    if (T < 0 || H < 1 || H_kv < 0 || d < 1 || !inv_freq || (T > 0 && (!q || !q_out)))
+        return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+    if (rot_dim < 1 || rot_dim > d) return FA_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+    const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d;
+    if (q_stride < wq || qo_stride < wq || (H_kv > 0 && k_stride < wk)) return FA_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || qo_stride % 8 != 0 || (H_kv > 0 && k_stride % 8 != 0) || !aligned16(q) ||
+        !aligned16(k) || !aligned16(q_out) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+        return FA_ERR_MISALIGNED;
+    if (q_stride >= (1ll << 39) || qo_stride >= (1ll << 39) || k_stride >= (1ll << 39) ||
+        H > (1 << 20) || H_kv > (1 << 20))
+        return FA_ERR_TOO_LARGE;
+    // in place (each value is read by the lane that writes it), or apart
+    if ((q_out != q || qo_stride != q_stride) && rows_overlap(q_out, wq, qo_stride, q, wq, q_stride, T))
+        return FA_ERR_INVALID_ARG;
+    if (rows_overlap(q_out, wq, qo_stride, k, wk, k_stride, T)) return FA_ERR_INVALID_ARG;
+    a->q = q;
+    a->k = k;
+    a->q_out = q_out;
+    a->inv_freq = inv_freq;
+    a->T = T;
+    a->N = 1;
+    a->H = H;
+    a->H_kv = H_kv;
+    a->V = d / 8;
+    a->rot = rot_dim;
+    a->q_stride = q_stride / 8;
+    a->k_stride = k_stride / 8;
+    a->qo_stride = qo_stride / 8;
+    a->scale = scale;
+    a->interleaved = interleaved != 0;
+    return FA_OK;
+}
+
+fa_status fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int32_t *positions,
+                  const double *inv_freq, int B, int N, int H, int H_kv, int d, int rot_dim,
+                  long long q_stride, long long k_stride, long long q_out_stride,
+                  long long k_out_stride, float scale, int interleaved, int inverse,
+                  fa_dtype dtype, void *stream) {
+    if (B < 1 || N < 1) return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_TOO_LARGE;
+    const int T = B * N;
+    fa::RopeArgs a;
+    fa_status st = rope_args(&a, q, k, q_out, inv_freq, T, H, H_kv, d, rot_dim, q_stride, k_stride,
+                             q_out_stride, scale, interleaved, dtype);
+    if (st != FA_OK) return st;
+    if ((inverse != 0 && inverse != 1) || (H_kv > 0 && (!k || !k_out))) return FA_ERR_INVALID_ARG;
+    const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d;
+    if (H_kv > 0) {
+        if (k_out_stride < wk) return FA_ERR_INVALID_ARG;
+        if (k_out_stride % 8 != 0 || !aligned16(k_out)) return FA_ERR_MISALIGNED;
+        if (k_out_stride >= (1ll << 39)) return FA_ERR_TOO_LARGE;
+        if ((k_out != k || k_out_stride != k_stride) &&
+            rows_overlap(k_out, wk, k_out_stride, k, wk, k_stride, T))
+            return FA_ERR_INVALID_ARG;
+        if (rows_overlap(k_out, wk, k_out_stride, q, wq, q_stride, T) ||
+            rows_overlap(k_out, wk, k_out_stride, q_out, wq, q_out_stride, T))
+            return FA_ERR_INVALID_ARG;
+    }
+    if (reinterpret_cast<uintptr_t>(positions) & 3u) return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    a.k_out = k_out;
+    a.ko_stride = k_out_stride / 8;
+    a.positions = positions;
+    a.N = N;
+    a.inverse = inverse != 0;
+    return fa::launch_rope(a, dtype == FA_BF16, false, dev->sm_count,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_paged_rope_append(const void *q, const void *k, const void *v, void *q_out,
+                               void *k_pages, void *v_pages, const int32_t *block_table,
+                               const int32_t *kv_len, const int32_t *cu_q, const int32_t *offsets,
+                               const double *inv_freq, int B, int H, int H_kv, int d, int rot_dim,
+                               int total_q, int page_size, int n_pages, int table_width,
+                               long long q_stride, long long kv_stride, long long q_out_stride,
+                               long long page_stride, float scale, int interleaved, fa_dtype dtype,
+                               void *stream) {
+    if (!k_pages || !v_pages || !block_table || !kv_len || !cu_q) return FA_ERR_INVALID_ARG;
+    if (total_q < 0 || (total_q > 0 && (!k || !v))) return FA_ERR_INVALID_ARG;
+    int ps_log2 = 0;
+    fa_status st = paged_checks(B, H_kv, d, page_size, n_pages, table_width, page_stride, block_table,
+                                kv_len, &ps_log2);
+    if (st != FA_OK) return st;
+    fa::RopeArgs a;
+    st = rope_args(&a, q, k, q_out, inv_freq, total_q, H, H_kv, d, rot_dim, q_stride, kv_stride,
+                   q_out_stride, scale, interleaved, dtype);
+    if (st != FA_OK) return st;
+    if (!aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        (reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return FA_ERR_MISALIGNED;
+    if (rows_overlap(q_out, static_cast<long long>(H) * d, q_out_stride, v, static_cast<long long>(H_kv) * d,
+                     kv_stride, total_q))
+        return FA_ERR_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+    if (total_q == 0) return FA_OK;
+    a.v = v;
+    a.v_stride = kv_stride / 8;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.table = block_table;
+    a.kv_len = kv_len;
+    a.cu_q = cu_q;
+    a.offsets = offsets;
+    a.status = dev->status;
+    a.page_stride = page_stride / 8;
+    a.B = B;
+    a.W = table_width;
+    a.ps_log2 = ps_log2;
+    a.n_pages = n_pages;
+    return fa::launch_rope(a, dtype == FA_BF16, true, dev->sm_count,
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status fa_check_status(void *stream) {

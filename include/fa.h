@@ -504,6 +504,66 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
                          void *stream);
 
 /*
+ * Rotary positions.  A head's first rot_dim elements are pairs that turn by an
+ * angle proportional to the token's position p:
+ *     y0 = scale (x0 cos t - x1 sin t),  y1 = scale (x1 cos t + x0 sin t),
+ *     t = p * inv_freq[c]
+ * for pair c = 0 .. rot_dim / 2 - 1: elements (c, c + rot_dim / 2), or with
+ * interleaved = 1 elements (2c, 2c + 1).  Elements from rot_dim on are copied.
+ * Contexts are stretched through inv_freq and scale (position interpolation, a
+ * larger base, frequencies kept and stretched by their wavelength: any
+ * per-pair choice).  The angle is formed in 64-bit fixed point from the double
+ * inv_freq, so that it holds at any int32 position (off by |p| 2^-53 relative to
+ * w plus 2^-23 rad); the rotation is FP32, rounded once to `dtype`.
+ *   inv_freq : device, double [rot_dim / 2], finite, radians a position.
+ *   d in {64, 128, 256}, rot_dim <= d a multiple of 16 (else
+ *   FA_ERR_UNSUPPORTED).  Strides are elements between tokens, multiples of 8,
+ *   at least the row's width; a token's [heads][d] is contiguous.  Pointers
+ *   16-byte aligned.  An output is its input itself (same pointer and stride)
+ *   or shares no element with any input or other output, else
+ *   FA_ERR_INVALID_ARG.
+ */
+
+/*
+ * fa_rope -- rotates the queries and keys of B sequences of N tokens in one
+ * launch.
+ *   q, q_out : device, B * N rows of [H][d].
+ *   k, k_out : device, B * N rows of [H_kv][d]; H_kv = 0: none (k NULL).
+ *   positions : device, int32 [B * N] (any value), or NULL: a token's place
+ *          0 .. N - 1 in its sequence.
+ *   inverse : 1 turns by -t: the gradient of the inputs from that of the
+ *          outputs, with the same scale.
+ */
+fa_status fa_rope(const void *q, const void *k, void *q_out, void *k_out,
+                  const int32_t *positions, const double *inv_freq, int B, int N, int H,
+                  int H_kv, int d, int rot_dim, long long q_stride, long long k_stride,
+                  long long q_out_stride, long long k_out_stride, float scale, int interleaved,
+                  int inverse, fa_dtype dtype, void *stream);
+
+/*
+ * fa_paged_rope_append -- fa_paged_append of rotated keys, and the rotated
+ * queries, in one launch: the new tokens' q turns into q_out, k turns and goes
+ * to its page, v goes to its page as it is.
+ *   offsets : device, int32 [B], or NULL for zeros: a token at place p of the
+ *          cache has position p + offsets[b] (after fa_paged_evict the places
+ *          begin anew, positions run on).
+ *   kv_stride : of k and of v.
+ * Tokens without a slot are not cached (fa_paged_append); their q_out is
+ * rotated by the position that the caller's numbers give.  Rows at and behind
+ * cu_q[B] are left as they were.  d in {64, 128}.  Other arguments as
+ * fa_paged_append and fa_rope.
+ */
+fa_status fa_paged_rope_append(const void *q, const void *k, const void *v, void *q_out,
+                               void *k_pages, void *v_pages, const int32_t *block_table,
+                               const int32_t *kv_len, const int32_t *cu_q,
+                               const int32_t *offsets, const double *inv_freq, int B, int H,
+                               int H_kv, int d, int rot_dim, int total_q, int page_size,
+                               int n_pages, int table_width, long long q_stride,
+                               long long kv_stride, long long q_out_stride,
+                               long long page_stride, float scale, int interleaved,
+                               fa_dtype dtype, void *stream);
+
+/*
  * fa_check_status -- synchronizes `stream`, then reports and clears the
  * device status word of the current device.  Returns FA_ERR_TIMEOUT if a
  * kernel launched since the last check gave up on a bounded wait (its
