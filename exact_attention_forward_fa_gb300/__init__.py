@@ -38,7 +38,7 @@ FA_SCALE_TENSOR = 2
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_gqa_packed", "fa_fwd_ext", "fa_fwd_splitkv", "fa_splitkv_workspace_floats",
            "fa_splitkv_auto", "fa_quantize_fp8", "fa_quantize_fp8_granular", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_bwd", "fa_bwd_ext", "fa_bwd_noalloc",
            "fa_paged_append", "fa_fwd_paged", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
-           "fa_rope", "fa_paged_rope_append",
+           "fa_mask_plan", "fa_mask_plan_bytes", "fa_fwd_masked", "fa_rope", "fa_paged_rope_append",
            "fa_check_status", "fa_status_detail", "fa_selftest_wait_timeout",
            "fa_status_string", "fa_version")
 
@@ -102,6 +102,12 @@ def load():
     lib.fa_paged_scores.restype = i
     lib.fa_paged_evict.argtypes = [vp] * 9 + [i] * 8 + [ll, i, i, i, vp]
     lib.fa_paged_evict.restype = i
+    lib.fa_mask_plan.argtypes = [vp] * 4 + [i] * 5 + [vp]
+    lib.fa_mask_plan.restype = i
+    lib.fa_mask_plan_bytes.argtypes = [i, i]
+    lib.fa_mask_plan_bytes.restype = ll
+    lib.fa_fwd_masked.argtypes = [vp] * 8 + [i] * 5 + [ll] * 3 + [f, i, vp]
+    lib.fa_fwd_masked.restype = i
     lib.fa_rope.argtypes = [vp] * 6 + [i] * 6 + [ll] * 4 + [f, i, i, i, vp]
     lib.fa_rope.restype = i
     lib.fa_paged_rope_append.argtypes = [vp] * 11 + [i] * 9 + [ll] * 4 + [f, i, i, vp]
@@ -768,6 +774,143 @@ def paged_evict(k_pages, v_pages, scores, block_table, kv_len, dst_table, keep: 
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_evict")
     return kept, scores_out, new_len
+
+
+# ---- masks of documents and prefixes, distance bias (see include/fa.h) ----
+
+def fa_mask_plan(docs, prefix, plan, positions, B: int, N: int, n_docs: int, window_left: int,
+                 window_right: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``prefix`` and
+    ``positions`` may be None."""
+    return load().fa_mask_plan(_ptr(docs), _ptr(prefix), _ptr(plan), _ptr(positions), B, N, n_docs,
+                               window_left, window_right, _stream(stream))
+
+
+def fa_mask_plan_bytes(B: int, N: int) -> int:
+    return load().fa_mask_plan_bytes(B, N)
+
+
+def fa_fwd_masked(q, k, v, o, lse, plan, slopes, sinks, B: int, H: int, H_kv: int, N: int, d: int,
+                  q_stride: int, k_stride: int, v_stride: int, alpha: float, dtype: int,
+                  stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``lse``,
+    ``slopes`` and ``sinks`` may be None."""
+    return load().fa_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(plan),
+                                _ptr(slopes), _ptr(sinks), B, H, H_kv, N, d, q_stride, k_stride,
+                                v_stride, alpha, dtype, _stream(stream))
+
+
+class MaskPlan:
+    """A mask laid out by ``mask_plan`` for sequences [B, N]; ``positions``
+    int32 [B, N] are the tokens' places in their documents (for ``rope``)."""
+
+    __slots__ = ("B", "N", "window", "data", "positions")
+
+    def __init__(self, B, N, window, data, positions):
+        self.B, self.N, self.window, self.data, self.positions = B, N, window, data, positions
+
+
+def mask_plan(docs, N: int, prefix=None, window=(-1, 0), out: MaskPlan | None = None, stream=None):
+    """The mask of sequences of N tokens packed with documents: docs int32
+    [B, D + 1], document k of sequence b being tokens docs[b, k] ..
+    docs[b, k + 1] (tokens outside all of them are padding), prefix int32 [B, D]
+    the lengths of the documents' prefixes or None, window = (left, right) key
+    bounds around a token (-1: none; (-1, 0) causal).  ``out``: a plan of the
+    same B and N to lay out anew (a captured step whose documents change).
+    Returns a MaskPlan."""
+    torch = _torch or _use_torch()
+    at = docs.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(docs.device, stream):
+            return mask_plan(docs, N, prefix, window, out)
+    if docs.dim() != 2 or docs.shape[1] < 2:
+        raise ValueError("docs is [B, D + 1]")
+    B, D = docs.shape[0], docs.shape[1] - 1
+    left, right = window
+    if not (-0x80000000 <= left <= 0x7fffffff and -0x80000000 <= right <= 0x7fffffff):
+        raise ValueError(_BEYOND_32)
+    _check_int(docs, docs.shape, at)
+    if prefix is not None:
+        _check_int(prefix, (B, D), at)
+    if at < 0:
+        raise ValueError("tensors must be on the GPU")
+    if out is None:
+        n = -1 if not 1 <= N <= 0x7fffffff else fa_mask_plan_bytes(B, N)
+        if n < 0:
+            raise FaError(FA_ERR_TOO_LARGE if N > 0 and B > 0 else FA_ERR_INVALID_ARG, "fa_mask_plan_bytes")
+        out = MaskPlan(B, N, window, torch.empty((n,), dtype=torch.uint8, device=docs.device),
+                       torch.empty((B, N), dtype=torch.int32, device=docs.device))
+    else:
+        if (out.B, out.N) != (B, N) or out.data.get_device() != at:
+            raise ValueError("out is a plan of another shape or device")
+        out.window = window
+    rc = load().fa_mask_plan(docs.data_ptr(), None if prefix is None else prefix.data_ptr(),
+                             out.data.data_ptr(), out.positions.data_ptr(), B, N, D, left, right,
+                             torch._C._cuda_getCurrentRawStream(at))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_mask_plan")
+    return out
+
+
+def _check_masked(q, k, v, plan, slopes, sinks):
+    """What the forward and the backward on a plan are told by sizes and
+    strides: (dtype code, B, N, H, H_kv, d, strides of q, k, v)."""
+    at = q.get_device()
+    dt = _dtype_of(q)
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("q is [B, N, H, d], k and v are [B, N, H_kv, d]")
+    B, N, H, d = q.shape
+    if k.shape[:2] != (B, N) or k.shape[3] != d:
+        raise ValueError("q, k and v differ in tokens or head dim")
+    if (plan.B, plan.N) != (B, N):
+        raise ValueError(f"a plan of [{plan.B}, {plan.N}] for sequences of [{B}, {N}]")
+    _like(k, q, "k")
+    _like(v, q, "v")
+    if plan.data.get_device() != at:
+        raise ValueError("tensors on different devices")
+    for x in (slopes, sinks):
+        if x is not None:
+            _check_float(x, (H,), at)
+    if at < 0:
+        raise ValueError("tensors must be on the GPU")
+    return dt, B, N, H, k.shape[2], d, _rows_stride(q, "q"), _rows_stride(k, "k"), _rows_stride(v, "v")
+
+
+def _check_out(x, shape, ref, name: str) -> None:
+    if x.shape != shape or x.dtype is not ref.dtype or x.get_device() != ref.get_device() or not x.is_contiguous():
+        raise ValueError(f"{name} is a contiguous {ref.dtype} {tuple(shape)} on {ref.device}")
+
+
+def attention_masked(q, k, v, plan: MaskPlan, slopes=None, sinks=None, alpha: float | None = None,
+                     out=None, lse=None, want_lse: bool = True, stream=None):
+    """Attention of q [B, N, H, d] over k, v [B, N, H_kv, d] (slices of wider
+    rows are fine) under the mask of ``plan``; slopes float32 [H]: the scores
+    lose slopes[h] times the distance; sinks as in ``attention_ext``.  Rows
+    that see nothing give O = 0, LSE = -inf.  Returns (O, LSE or None)."""
+    torch = _torch or _use_torch()
+    at = q.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
+            return attention_masked(q, k, v, plan, slopes, sinks, alpha, out, lse, want_lse)
+    dt, B, N, H, hk, d, qs, ks, vs = _check_masked(q, k, v, plan, slopes, sinks)
+    if alpha is None:
+        alpha = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
+    else:
+        _check_out(out, q.shape, q, "out")
+    if lse is not None:
+        _check_float(lse, (B, H, N), at)
+    elif want_lse:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    rc = load().fa_fwd_masked(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        plan.data.data_ptr(), None if slopes is None else slopes.data_ptr(),
+        None if sinks is None else sinks.data_ptr(), B, H, hk, N, d, qs, ks, vs, alpha, dt,
+        torch._C._cuda_getCurrentRawStream(at))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_masked")
+    return out, lse
 
 
 # ---- rotary positions (see include/fa.h) ----

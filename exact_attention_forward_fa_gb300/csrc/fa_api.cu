@@ -100,13 +100,16 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // 4-D map over a [B][N][H][d] tensor: dims {d, H, N, B}, box {128 B of the
 // row, 1, rows, 1}, 128-byte swizzle, rows beyond N read as zero.  2-byte
-// elements (bf16/fp16) or 1-byte e4m3 codes.
+// elements (bf16/fp16) or 1-byte e4m3 codes.  token_stride: elements between
+// tokens (0: contiguous, H d).
 fa_status encode_bshd(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int B,
-                      int H, int N, int d, cuuint32_t rows) {
+                      int H, int N, int d, cuuint32_t rows, long long token_stride = 0) {
     const cuuint64_t esz = dt == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
                           static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(B)};
-    cuuint64_t strides[3] = {esz * d, esz * d * H, esz * d * H * static_cast<cuuint64_t>(N)};
+    const cuuint64_t tok = esz * (token_stride ? static_cast<cuuint64_t>(token_stride)
+                                               : static_cast<cuuint64_t>(d) * H);
+    cuuint64_t strides[3] = {esz * d, tok, tok * static_cast<cuuint64_t>(N)};
     cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / esz), 1, rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = g_encode(m, dt, 4, const_cast<void *>(ptr), dims, strides, box, estr,
@@ -1040,6 +1043,112 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
     a.recent = recent;
     return fa::launch_paged_evict(a, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? FA_OK : FA_ERR_CUDA;
+}
+
+// ---- masks of documents and prefixes ----
+
+long long fa_mask_plan_bytes(int B, int N) {
+    if (B < 1 || N < 1 || B > 65535 || N > (1 << 30)) return -1;
+    return static_cast<long long>(fa::mask_plan_layout(B, N, nullptr, nullptr));
+}
+
+fa_status fa_mask_plan(const int32_t *docs, const int32_t *prefix, void *plan, int32_t *positions,
+                       int B, int N, int n_docs, int window_left, int window_right,
+                       void *stream) {
+    if (!docs || !plan || B < 1 || N < 1 || n_docs < 1) return FA_ERR_INVALID_ARG;
+    if (window_left < -1 || window_right < -1) return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(docs) & 3u) || (reinterpret_cast<uintptr_t>(prefix) & 3u) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u) || !aligned16(plan))
+        return FA_ERR_MISALIGNED;
+    if (B > 65535 || N > (1 << 30) || n_docs > (1 << 30)) return FA_ERR_TOO_LARGE;
+    DeviceInfo *dev = nullptr;
+    fa_status st = get_device(&dev);
+    if (st != FA_OK) return st;
+    fa::MaskPlanArgs a;
+    a.docs = docs;
+    a.prefix = prefix;
+    a.positions = positions;
+    fa::mask_plan_layout(B, N, plan, &a.plan);
+    a.status = dev->status;
+    a.B = B;
+    a.N = N;
+    a.D = n_docs;
+    a.wl = window_left;
+    a.wr = window_right;
+    return fa::launch_mask_plan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                     : FA_ERR_CUDA;
+}
+
+// What the forward and the backward on a mask plan check of their sizes.
+static fa_status masked_checks(const void *plan, const float *slopes, const float *sinks, int B, int H,
+                               int H_kv, int N, int d, long long q_stride, long long k_stride,
+                               long long v_stride, float alpha, fa_dtype dtype) {
+    if (!plan || B < 1 || H < 1 || N < 1 || d < 1) return FA_ERR_INVALID_ARG;
+    if (H_kv < 1 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
+    // a hidden score is -inf before it is scaled, and the largest stays the largest
+    const float scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    if (!std::isnormal(scale_log2) || scale_log2 < 0.f) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d;
+    if (q_stride < wq || k_stride < wk || v_stride < wk) return FA_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned16(plan) ||
+        (reinterpret_cast<uintptr_t>(slopes) & 3u) || (reinterpret_cast<uintptr_t>(sinks) & 3u))
+        return FA_ERR_MISALIGNED;
+    // TMA: every global stride < 2^40 bytes
+    const long long most = (1ll << 39) / N;
+    if (B > 65535 || N > (1 << 30) || q_stride >= most || k_stride >= most || v_stride >= most)
+        return FA_ERR_TOO_LARGE;
+    const uint64_t units = static_cast<uint64_t>(B) * H * ((static_cast<uint64_t>(N) + 127) / 128);
+    if (units > 0x7fffffffull || static_cast<uint64_t>(B) * H * N > 0x7fffffffffffull)
+        return FA_ERR_TOO_LARGE;
+    return FA_OK;
+}
+
+fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, float *lse,
+                        const void *plan, const float *slopes, const float *sinks, int B, int H,
+                        int H_kv, int N, int d, long long q_stride, long long k_stride,
+                        long long v_stride, float alpha, fa_dtype dtype, void *stream) {
+    // ---- host-side validation: nothing is launched on failure ----
+    if (!q || !k || !v || !o) return FA_ERR_INVALID_ARG;
+    fa_status st = masked_checks(plan, slopes, sinks, B, H, H_kv, N, d, q_stride, k_stride, v_stride, alpha,
+                                 dtype);
+    if (st != FA_OK) return st;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+
+    fa::FwdLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    const CUtensorMapDataType dt =
+        dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if ((st = encode_bshd(&L.q, q, dt, B, H, N, d, 128, q_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.k, k, dt, B, H_kv, N, d, 128, k_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.v, v, dt, B, H_kv, N, d, 128, v_stride)) != FA_OK) return st;
+    const uint64_t n_qt = (static_cast<uint64_t>(N) + 127) / 128;
+    const uint64_t units = static_cast<uint64_t>(B) * H * ((n_qt + 1) / 2);
+    L.args.o = o;
+    L.args.lse = lse;
+    L.args.status = dev->status;
+    L.args.B = B;
+    L.args.H = H;
+    L.args.N = N;
+    L.args.n_kv = static_cast<int>(n_qt);
+    L.args.n_pairs = static_cast<int>((n_qt + 1) / 2);
+    L.args.n_units = static_cast<int>(units);
+    L.args.group = H / H_kv;
+    L.args.scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    L.args.sinks = sinks;
+    fa::mask_plan_layout(B, N, plan, &L.args.plan);
+    L.args.slopes = slopes;
+    set_dynamic_order(L, units, B, H, N, d, 2, H / H_kv);
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.bf16 = dtype == FA_BF16;
+    L.d64 = d == 64;
+    const cudaError_t e = slopes ? fa::launch_fwd_mask_bias(L) : fa::launch_fwd_mask(L);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // ---- rotary positions ----

@@ -43,6 +43,7 @@
 #pragma once
 
 #include "fa_device.cuh"
+#include "fa_mask.cuh"
 
 namespace fa {
 
@@ -76,6 +77,10 @@ struct FwdArgs {
     int wl, wr;
     float sc_pre, sc_post;
     const float *sinks;
+    // Interval masks (kVar 3 and 4): the plan's lists and each row's visible
+    // keys; kVar 4: the score loses slopes[h] |i - j|.
+    MaskPlan plan;
+    const float *slopes;
     // FP8 only: one FP32 scale per 128-row tile of each head, [B][H][n_kv]
     const float *q_scale, *k_scale, *v_scale;
 };
@@ -192,9 +197,9 @@ __device__ __forceinline__ int window_hi(int i, const FwdArgs &a) {
 }
 
 // Units whose length falls with their index (longest-first orders).
-template <bool kCausal, bool kExt>
+template <bool kCausal, int kVar>
 __device__ __forceinline__ bool units_longest_first(const FwdArgs &a) {
-    return kExt ? (a.wl < 0 && a.wr >= 0) : kCausal;
+    return kVar ? (a.wl < 0 && a.wr >= 0) : kCausal;
 }
 
 // kSplit: the key range is cut into a.n_splits parts (otherwise one part,
@@ -214,14 +219,39 @@ __device__ __forceinline__ bool units_longest_first(const FwdArgs &a) {
 // group, so the group's K/V stay in L2 while its units run; the shortest
 // pair of every head (one or two key tiles) comes last, over all heads,
 // so that the CTAs finish together.
-template <bool kCausal, bool kSplit, bool kExt, bool kPack>
+// Interval masks (kVar >= 3) take that order too, the pairs of a sequence
+// sorted by the plan: documents make their lengths unlike.
+template <bool kCausal, bool kSplit, int kVar, bool kPack>
 __device__ __forceinline__ constexpr bool dynamic_units() {
-    return kCausal && !kSplit && !kExt && !kPack;
+    return kVar >= 3 || (kCausal && !kSplit && !kVar && !kPack);
 }
 
-template <bool kCausal, bool kSplit, bool kExt = false, bool kPack = false>
+template <bool kCausal, bool kSplit, int kVar = 0, bool kPack = false>
 __device__ __forceinline__ Unit make_unit(int u, const FwdArgs &a) {
     Unit U;
+    constexpr bool kExt = kVar != 0;
+    if constexpr (kVar >= 3) {
+        int i, bh;
+        dynamic_order(u, a.B * a.H, a.n_pairs, a.chunk, i, bh);
+        U.b = bh / a.H;
+        U.h = bh - U.b * a.H;
+        U.s = 0;
+        const int4 *rec = a.plan.pairs + 2 * (static_cast<size_t>(U.b) * a.n_pairs + (a.n_pairs - 1 - i));
+        const int4 r0 = __ldg(rec), r1 = __ldg(rec + 1);
+        const int lo[2] = {r0.y, r1.y}, hi[2] = {r0.z, r1.z};
+        for (int x = 0; x < 2; ++x) {
+            U.m[x] = 2 * r0.x + x;
+            U.act[x] = hi[x] > lo[x];
+        }
+        const int jlo = !U.act[1] ? lo[0] : !U.act[0] ? lo[1] : min(lo[0], lo[1]);
+        U.jhi = !U.act[1] ? hi[0] : !U.act[0] ? hi[1] : max(hi[0], hi[1]);
+        U.T = U.jhi - jlo;                         // 0: neither tile sees a key
+        for (int x = 0; x < 2; ++x) {
+            U.t0[x] = U.act[x] ? U.jhi - hi[x] : U.T;
+            U.t1[x] = U.act[x] ? U.jhi - lo[x] : U.T;
+        }
+        return U;
+    }
     const int HH = kPack ? a.H / a.group : a.H;    // heads the units run over
     const int BH = a.B * HH;
     const int S = kSplit ? a.n_splits : 1;
@@ -229,8 +259,8 @@ __device__ __forceinline__ Unit make_unit(int u, const FwdArgs &a) {
     if (kSplit) u /= S;
     int p, bh;
     // a right bound without a left one makes later pairs longer
-    const bool lpt = units_longest_first<kCausal, kExt>(a);
-    if (dynamic_units<kCausal, kSplit, kExt, kPack>()) {
+    const bool lpt = units_longest_first<kCausal, kVar>(a);
+    if (dynamic_units<kCausal, kSplit, kVar, kPack>()) {
         const int P1 = a.n_pairs - 1;              // pairs per head before the tail
         const int grouped = BH * P1;
         if (u < grouped) {
@@ -302,7 +332,10 @@ __device__ __forceinline__ Unit make_unit(int u, const FwdArgs &a) {
 
 // kVar: the score and mask variants of FwdArgs -- 1: window and sinks,
 // 2: window, sinks and softcap; kCausal is then unused (the causal mask is
-// the window (-1, 0)).
+// the window (-1, 0)).  3: the intervals of a mask plan, and sinks; 4: the
+// same with a distance bias.  There a row may see nothing in a tile that
+// others of its tile see, or nothing at all, and tokens outside every
+// document may hold anything: their V rows become 0 in shared memory.
 template <int D, bool kCausal, bool kBF16, bool kFP8 = false, bool kSplit = false,
           int kVar = 0, bool kPack = false>
 __global__ void __launch_bounds__(384, 1)
@@ -312,6 +345,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     using C = FwdCfg<D, kCausal, kBF16, kFP8>;
     constexpr bool kExt = kVar != 0;
     constexpr bool kCap = kVar == 2;
+    constexpr bool kMask = kVar >= 3, kBias = kVar == 4;
     static_assert(!kExt || (!kFP8 && !kSplit && !kCausal), "variants: 16-bit, one split");
     static_assert(!kPack || (!kExt && !kFP8 && !kSplit), "packed heads: plain or causal, 16-bit");
     extern __shared__ uint8_t smem_raw[];
@@ -322,7 +356,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    const bool snake = units_longest_first<kCausal, kExt>(a);   // unit order (unit_stride0)
+    const bool snake = units_longest_first<kCausal, kVar>(a);   // unit order (unit_stride0)
     // Dynamic order: the grid has one CTA per unit; a CTA starts with its
     // own unit and then takes the units of CTAs it cancels before they
     // launch.  The producer asks for the next unit once it has issued the
@@ -331,7 +365,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     // MMA warp and the 8 softmax warps read it and release the slot.
     // Static order: the persistent stride walk.
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::UNIT_OFF);
-    constexpr bool kDyn = dynamic_units<kCausal, kSplit, kExt, kPack>();
+    constexpr bool kDyn = dynamic_units<kCausal, kSplit, kVar, kPack>();
 
     auto bar = [&](int i) -> uint32_t { return base + C::BAR_OFF + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF);
@@ -431,7 +465,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             };
             for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                      u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const Unit U = make_unit<kCausal, kSplit, kExt, kPack>(u, a);
+                const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 if (U.act[0]) ok = ok && load_q(0, U);
                 if (U.act[1]) ok = ok && load_q(1, U);
                 const int hk = kPack ? U.h : U.h / a.group;   // K/V head of this query head
@@ -485,7 +519,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             };
             for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                      u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const Unit U = make_unit<kCausal, kSplit, kExt, kPack>(u, a);
+                const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 uint32_t qs0 = 0, qp0 = 0, qs1 = 0, qp1 = 0;   // Q slot and parity per tile
                 if (U.act[0]) { qs0 = qc % C::NQ; qp0 = (qc / C::NQ) & 1u; ++qc; }
                 if (U.act[1]) { qs1 = qc % C::NQ; qp1 = (qc / C::NQ) & 1u; ++qc; }
@@ -593,6 +627,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             ((reinterpret_cast<uintptr_t>(kSplit ? static_cast<const void *>(a.o_part) : a.o) & 31u) == 0);
         bool ok = true;
         uint32_t kq = 0;                            // dynamic order: answers read
+        uint32_t kvc = 0;                           // interval masks: K and V tiles of the units so far
         // (a failed wait leaves this loop by break, so ok holds here)
         auto next_dyn = [&]() __attribute__((always_inline)) -> int {
             const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
@@ -606,10 +641,26 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
         };
         for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                      u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const Unit U = make_unit<kCausal, kSplit, kExt, kPack>(u, a);
+            const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
             const bool act = x ? U.act[1] : U.act[0];
-            if (!act) continue;
             const int mt = x ? U.m[1] : U.m[0];
+            const uint32_t kv0 = kvc;                    // K and V tiles before this unit's
+            if constexpr (kMask) {
+                kvc += 2u * static_cast<uint32_t>(U.T);
+                if (!act) {                              // no row of the tile sees a key
+                    const int n = mt * 128 + row;
+                    if (n < a.N) {
+                        uint4 *o4 = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) +
+                                    ((static_cast<size_t>(U.b) * a.N + n) * a.H + U.h) * D);
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) o4[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (a.lse != nullptr)
+                            a.lse[(static_cast<size_t>(U.b) * a.H + U.h) * a.N + n] =
+                                a.sinks != nullptr ? a.sinks[U.h] : -INFINITY;
+                    }
+                }
+            }
+            if (!act) continue;
             // this row's query position and head (packed: the group's heads
             // share the tile, and its rows share one diagonal key tile)
             const int qpos = kPack ? mt * (128 / a.group) + row / a.group : mt * 128 + row;
@@ -618,7 +669,19 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             const int t1 = kExt ? (x ? U.t1[1] : U.t1[0]) : U.T;
             // this row's visible keys (rows past N: any non-empty range)
             int klo = 0, khi = a.N;
-            if constexpr (kExt) {
+            int live_lo = 0, live_hi = a.N;
+            float beta = 0.f;                            // the bias a key of distance, log2 units
+            if constexpr (kMask) {
+                const int2 kr = mt * 128 + row < a.N
+                                    ? __ldg(a.plan.rows + static_cast<size_t>(U.b) * a.N + mt * 128 + row)
+                                    : make_int2(0, 0);
+                klo = kr.x;
+                khi = kr.y;
+                const int4 lv = __ldg(a.plan.live + U.b);
+                live_lo = lv.x;
+                live_hi = lv.y;
+                if constexpr (kBias) beta = a.slopes[U.h] * 1.44269504088896340736f;
+            } else if constexpr (kExt) {
                 const int gr = min(mt * 128 + row, a.N - 1);
                 klo = window_lo(gr, a);
                 khi = window_hi(gr, a);
@@ -672,6 +735,28 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 ok = mbar_wait(bar(C::B_SFULL + x), sph, w, 20);
                 if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
                 sph ^= 1;
+                if constexpr (kMask) {
+                    // ---- a tile that reaches outside the documents: those V rows
+                    //      become 0 (P is 0 there, and 0 x NaN is not); both groups
+                    //      may write them, each before its own P is published ----
+                    if (j * 128 < live_lo || j * 128 + 128 > live_hi) {
+                        const uint32_t idx = kv0 + 2u * static_cast<uint32_t>(t) + 1u, slot = idx % C::NSTAGE;
+                        ok = mbar_wait(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 22);
+                        if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                        const int key = j * 128 + row;
+                        if (key < live_lo || key >= live_hi) {
+                            uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + row * 128;
+#pragma unroll
+                            for (int ch = 0; ch < C::NCH; ++ch)
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    *reinterpret_cast<uint4 *>(vr + ch * C::CHUNK_BYTES + q * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
                 tc_fence_after();
                 uint32_t s[128];
                 float *sf = reinterpret_cast<float *>(s);
@@ -761,8 +846,76 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     //      the max is formed only on the first tile or when
                     //      the tile's sum exceeds KEEP_SUM ----
                     const float2 c2 = make_float2(sl2, sl2);
+                    // Distance bias, -beta |i - j|: in a tile before or behind the
+                    // diagonal one it is linear in the column, b0 + bs c.
+                    const float bs = kBias ? (j < mt ? beta : -beta) : 0.f;
+                    const float b0 = kBias ? bs * static_cast<float>(j * 128 - qpos) : 0.f;
+                    bool scaled = false;                // s holds biased scores in log2 units
+                    auto to_scaled = [&]() __attribute__((always_inline)) {
+                        scaled = true;
+                        if (j != mt) {
+                            const float2 step = make_float2(8.f * bs, 8.f * bs);
+                            float2 bc[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0), __fmaf_rn(bs, 2.f * i + 1.f, b0));
+#pragma unroll
+                            for (int c = 0; c < 128; c += 2) {
+                                float2 &b = bc[(c >> 1) & 3];
+                                const float2 x = __ffma2_rn(make_float2(sf[c], sf[c + 1]), c2, b);
+                                sf[c] = x.x;
+                                sf[c + 1] = x.y;
+                                b = __fadd2_rn(b, step);
+                            }
+                        } else {
+                            const float d0 = static_cast<float>(row);
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                sf[c] = __fmaf_rn(sf[c], sl2, -beta * fabsf(d0 - static_cast<float>(c)));
+                        }
+                    };
                     auto exps = [&](const float rs) __attribute__((always_inline)) {
                         const float2 nr2 = make_float2(-rs, -rs);
+                        if constexpr (kBias) {
+                            // s is raw in a linear tile that keeps its reference, else scaled
+                            e_a = make_float2(0.f, 0.f);
+                            e_b = e_a;
+                            if (!scaled) {
+                                const float2 step = make_float2(8.f * bs, 8.f * bs);
+                                float2 bc[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0 - rs),
+                                                        __fmaf_rn(bs, 2.f * i + 1.f, b0 - rs));
+#pragma unroll
+                                for (int c = 0; c < 128; c += 4) {
+                                    float2 &b01 = bc[(c >> 1) & 3], &b23 = bc[((c >> 1) + 1) & 3];
+                                    const float2 x01 = __ffma2_rn(make_float2(sf[c + 0], sf[c + 1]), c2, b01);
+                                    const float2 x23 = __ffma2_rn(make_float2(sf[c + 2], sf[c + 3]), c2, b23);
+                                    b01 = __fadd2_rn(b01, step);
+                                    b23 = __fadd2_rn(b23, step);
+                                    const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                                    const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                                    p[c / 2] = pack2<kBF16>(e01.x, e01.y);
+                                    p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                                    e_a = __fadd2_rn(e_a, e01);
+                                    e_b = __fadd2_rn(e_b, e23);
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 128; c += 4) {
+                                    const float2 x01 = __fadd2_rn(make_float2(sf[c + 0], sf[c + 1]), nr2);
+                                    const float2 x23 = __fadd2_rn(make_float2(sf[c + 2], sf[c + 3]), nr2);
+                                    const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                                    const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                                    p[c / 2] = pack2<kBF16>(e01.x, e01.y);
+                                    p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                                    e_a = __fadd2_rn(e_a, e01);
+                                    e_b = __fadd2_rn(e_b, e23);
+                                }
+                            }
+                            return;
+                        }
                         e_a = make_float2(0.f, 0.f);
                         e_b = e_a;
 #pragma unroll
@@ -777,15 +930,19 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             e_b = __fadd2_rn(e_b, e23);
                         }
                     };
-                    bool keep = __all_sync(0xffffffffu, r != -INFINITY);
+                    // (interval masks: a row without a reference that sees nothing
+                    // here needs none yet)
+                    bool keep = __all_sync(0xffffffffu, r != -INFINITY || (kMask && (lim <= 0 || llo >= 128)));
                     if (keep) {
-                        exps(r);
+                        if (kBias && j == mt) to_scaled();
+                        exps(kMask && r == -INFINITY ? 0.f : r);
                         const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
                         keep = __all_sync(0xffffffffu, ts <= C::KEEP_SUM);   // NaN: redo
                         if (!keep) load_s();
                     }
                     if (!keep) {
-                        const float bnew = row_max() * sl2;
+                        if constexpr (kBias) to_scaled();
+                        const float bnew = kBias ? row_max() : row_max() * sl2;
                         if (r == -INFINITY) rn = bnew;
                         else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
                         need = (r != -INFINITY) && (rn != r);

@@ -30,6 +30,8 @@ cudaError_t launch_fwd_fp8_d256(const FwdLaunch &L);   // the same at head dim 2
 cudaError_t launch_fwd_split(const FwdLaunch &L);  // split key ranges, d in {64, 128}
 cudaError_t launch_fwd_ext(const FwdLaunch &L);    // window / sinks, d in {64, 128}
 cudaError_t launch_fwd_ext_softcap(const FwdLaunch &L);   // the same with a softcap
+cudaError_t launch_fwd_mask(const FwdLaunch &L);   // interval masks
+cudaError_t launch_fwd_mask_bias(const FwdLaunch &L);   // the same with a distance bias
 // Grouped heads packed into the Q tiles (q map box {64, group, 128 / group, 1}),
 // d in {64, 128}, plain or causal.
 cudaError_t launch_fwd_pack(const FwdLaunch &L);
@@ -180,8 +182,8 @@ cudaError_t launch_fwd_pack_dispatch(const FwdLaunch &L) {
                   : launch_fwd_inst<D, false, false, false, false, 0, true>(L);
 }
 
-// Score and mask variants, d in {64, 128}: kVar 1 (window, sinks) or 2
-// (window, sinks, softcap).
+// Score and mask variants, d in {64, 128}: kVar 1 (window, sinks), 2
+// (window, sinks, softcap), 3 (mask plan, sinks) or 4 (mask plan, sinks, bias).
 template <int D, int kVar>
 cudaError_t launch_fwd_ext_dispatch(const FwdLaunch &L) {
     return L.bf16 ? launch_fwd_inst<D, false, true, false, false, kVar>(L)

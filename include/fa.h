@@ -504,6 +504,70 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
                          void *stream);
 
 /*
+ * Attention over packed documents: masks of documents, prefixes and windows,
+ * and a bias that depends on the distance, forward and backward.
+ *
+ * Sequence b of N tokens is packed with n_docs documents, the k-th of them tokens
+ * docs[b][k] .. docs[b][k + 1] (docs: int32 [B][n_docs + 1], ascending; equal
+ * offsets are empty documents, so that sequences may have fewer).  Token i of
+ * document [s, e) whose first p tokens are its prefix (prefix: int32
+ * [B][n_docs], or NULL for none) sees key j when
+ *     max(s, i - window_left) <= j < min(e, max(i + 1 + window_right, s + p)),
+ * a bound of -1 being none: (-1, 0) is causal, with a prefix the prefix
+ * language model's mask; (-1, -1) both directions.  (A left bound hides the
+ * prefix too; without a right bound a prefix changes nothing.)  Tokens before
+ * docs[b][0] and from docs[b][n_docs] on are padding: they see nothing, nobody
+ * sees them, and q, k, v and dout may hold anything there (NaN included).
+ * Within the documents, an infinity or NaN in a value, key, query or gradient
+ * reaches, as 0 times it, also rows of its 128-token tile that do not see it.
+ *
+ *     S_ij = alpha q_i . k_j - slopes[h] |i - j|
+ *     O = softmax(S) V, LSE = log sum exp(S)      (over the visible keys)
+ *
+ * A row that sees nothing gives O = 0, LSE = -inf, and its gradients are 0.
+ */
+
+/*
+ * fa_mask_plan -- lays a mask out for fa_fwd_masked and fa_bwd_masked: the
+ * visible interval of every token and key, and the tiles that each work unit
+ * needs, the longest units first.  Once a step, for all layers and heads.
+ *   docs, prefix : device; offsets outside [0, N] or falling, prefixes longer
+ *          than their document or negative are cut off
+ *          (FA_ERR_BAD_INDEX; rows of such a document are undefined).
+ *   plan : device, fa_mask_plan_bytes(B, N) bytes, 16-byte aligned (written).
+ *   positions : device, int32 [B][N] (written), or NULL: a token's place in its
+ *          document, as fa_rope takes it; 0 outside.
+ *   N <= 2^30, B <= 65535.
+ */
+fa_status fa_mask_plan(const int32_t *docs, const int32_t *prefix, void *plan,
+                       int32_t *positions, int B, int N, int n_docs, int window_left,
+                       int window_right, void *stream);
+
+/* fa_mask_plan_bytes -- size of a plan; -1 for sizes without one. */
+long long fa_mask_plan_bytes(int B, int N);
+
+/*
+ * fa_fwd_masked -- the forward.  Grouped K/V heads as fa_fwd_gqa.
+ *   q    : device, B * N rows of [H][d], q_stride elements from token to token
+ *          (>= H * d, a multiple of 8); k, v the same with H_kv heads: slices of
+ *          a fused projection's rows are fine.  16-byte aligned.
+ *   o    : device, [B][N][H][d] (written).  lse : float [B][H][N] or NULL.
+ *   plan : from fa_mask_plan for the same B and N.
+ *   slopes : device, float [H], finite, or NULL for no bias.
+ *   sinks : as fa_fwd_ext, or NULL (a row that sees nothing then has
+ *          LSE = sink).
+ *   alpha : positive.  d in {64, 128}.
+ * Accumulation and rounding as fa_fwd.  Key tiles that no row of a Q tile sees
+ * are neither loaded nor computed; units run in a dynamic order as fa_fwd's
+ * causal launches do.
+ */
+fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, float *lse,
+                        const void *plan, const float *slopes, const float *sinks, int B,
+                        int H, int H_kv, int N, int d, long long q_stride,
+                        long long k_stride, long long v_stride, float alpha,
+                        fa_dtype dtype, void *stream);
+
+/*
  * Rotary positions.  A head's first rot_dim elements are pairs that turn by an
  * angle proportional to the token's position p:
  *     y0 = scale (x0 cos t - x1 sin t),  y1 = scale (x1 cos t + x0 sin t),
