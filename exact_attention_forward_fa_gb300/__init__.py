@@ -38,7 +38,7 @@ FA_SCALE_TENSOR = 2
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_gqa_packed", "fa_fwd_ext", "fa_fwd_splitkv", "fa_splitkv_workspace_floats",
            "fa_splitkv_auto", "fa_quantize_fp8", "fa_quantize_fp8_granular", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_bwd", "fa_bwd_ext", "fa_bwd_noalloc",
            "fa_paged_append", "fa_fwd_paged", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
-           "fa_mask_plan", "fa_mask_plan_bytes", "fa_fwd_masked", "fa_rope", "fa_paged_rope_append",
+           "fa_mask_plan", "fa_mask_plan_bytes", "fa_fwd_masked", "fa_bwd_masked", "fa_rope", "fa_paged_rope_append",
            "fa_check_status", "fa_status_detail", "fa_selftest_wait_timeout",
            "fa_status_string", "fa_version")
 
@@ -108,6 +108,8 @@ def load():
     lib.fa_mask_plan_bytes.restype = ll
     lib.fa_fwd_masked.argtypes = [vp] * 8 + [i] * 5 + [ll] * 3 + [f, i, vp]
     lib.fa_fwd_masked.restype = i
+    lib.fa_bwd_masked.argtypes = [vp] * 14 + [i] * 5 + [ll] * 3 + [f, i, vp]
+    lib.fa_bwd_masked.restype = i
     lib.fa_rope.argtypes = [vp] * 6 + [i] * 6 + [ll] * 4 + [f, i, i, i, vp]
     lib.fa_rope.restype = i
     lib.fa_paged_rope_append.argtypes = [vp] * 11 + [i] * 9 + [ll] * 4 + [f, i, i, vp]
@@ -800,6 +802,17 @@ def fa_fwd_masked(q, k, v, o, lse, plan, slopes, sinks, B: int, H: int, H_kv: in
                                 v_stride, alpha, dtype, _stream(stream))
 
 
+def fa_bwd_masked(q, k, v, o, dout, lse, workspace, plan, slopes, sinks, dq, dk, dv, dsinks, B: int,
+                  H: int, H_kv: int, N: int, d: int, q_stride: int, k_stride: int, v_stride: int,
+                  alpha: float, dtype: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``slopes``,
+    ``sinks`` and ``dsinks`` may be None."""
+    return load().fa_bwd_masked(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+                                _ptr(workspace), _ptr(plan), _ptr(slopes), _ptr(sinks), _ptr(dq),
+                                _ptr(dk), _ptr(dv), _ptr(dsinks), B, H, H_kv, N, d, q_stride,
+                                k_stride, v_stride, alpha, dtype, _stream(stream))
+
+
 class MaskPlan:
     """A mask laid out by ``mask_plan`` for sequences [B, N]; ``positions``
     int32 [B, N] are the tokens' places in their documents (for ``rope``)."""
@@ -911,6 +924,38 @@ def attention_masked(q, k, v, plan: MaskPlan, slopes=None, sinks=None, alpha: fl
     if rc != FA_OK:
         raise FaError(rc, "fa_fwd_masked")
     return out, lse
+
+
+def attention_backward_masked(q, k, v, o, lse, dout, plan: MaskPlan, slopes=None, sinks=None,
+                              alpha: float | None = None, stream=None):
+    """Gradients (dQ, dK, dV, dsinks or None) for the forward of
+    ``attention_masked`` on the same inputs; ``o`` and ``lse`` are its
+    outputs.  Tokens outside every document get 0, whatever dout holds there."""
+    torch = _torch or _use_torch()
+    at = q.get_device()
+    if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
+        with _launch_on(q.device, stream):
+            return attention_backward_masked(q, k, v, o, lse, dout, plan, slopes, sinks, alpha)
+    dt, B, N, H, hk, d, qs, ks, vs = _check_masked(q, k, v, plan, slopes, sinks)
+    if alpha is None:
+        alpha = 1.0 / math.sqrt(d)
+    _check_out(o, q.shape, q, "o")
+    _check_out(dout, q.shape, q, "dout")
+    _check_float(lse, (B, H, N), at)
+    dq = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
+    dk = torch.empty((B, N, hk, d), dtype=q.dtype, device=q.device)
+    dv = torch.empty((B, N, hk, d), dtype=q.dtype, device=q.device)
+    ws = torch.empty((bwd_workspace_floats(B, H, N),), dtype=torch.float32, device=q.device)
+    ds = None if sinks is None else torch.empty((H,), dtype=torch.float32, device=q.device)
+    rc = load().fa_bwd_masked(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), plan.data.data_ptr(), None if slopes is None else slopes.data_ptr(),
+        None if sinks is None else sinks.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        None if ds is None else ds.data_ptr(), B, H, hk, N, d, qs, ks, vs, alpha, dt,
+        torch._C._cuda_getCurrentRawStream(at))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_bwd_masked")
+    return dq, dk, dv, ds
 
 
 # ---- rotary positions (see include/fa.h) ----

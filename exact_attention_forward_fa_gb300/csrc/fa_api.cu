@@ -1151,6 +1151,78 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void *o,
+                        const void *dout, const float *lse, float *workspace, const void *plan,
+                        const float *slopes, const float *sinks, void *dq, void *dk, void *dv,
+                        float *dsinks, int B, int H, int H_kv, int N, int d, long long q_stride,
+                        long long k_stride, long long v_stride, float alpha, fa_dtype dtype,
+                        void *stream) {
+    // ---- host-side validation: nothing is launched on failure ----
+    if (!q || !k || !v || !o || !dout || !lse || !workspace || !dq || !dk || !dv)
+        return FA_ERR_INVALID_ARG;
+    if (dsinks && !sinks) return FA_ERR_INVALID_ARG;
+    fa_status st = masked_checks(plan, slopes, sinks, B, H, H_kv, N, d, q_stride, k_stride, v_stride, alpha,
+                                 dtype);
+    if (st != FA_OK) return st;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) ||
+        !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(dsinks) & 3u))
+        return FA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    if ((st = get_device(&dev)) != FA_OK) return st;
+
+    fa::BwdLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    const CUtensorMapDataType dt =
+        dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if ((st = encode_bshd(&L.q, q, dt, B, H, N, d, 128, q_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.k, k, dt, B, H_kv, N, d, 128, k_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.v, v, dt, B, H_kv, N, d, 128, v_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.dout, dout, dt, B, H, N, d, 128)) != FA_OK) return st;
+    const uint64_t n_t = (static_cast<uint64_t>(N) + 127) / 128;
+    const uint64_t units = static_cast<uint64_t>(B) * H * n_t;
+    const uint64_t units_kv = static_cast<uint64_t>(B) * H_kv * n_t;
+    L.args.lse = lse;
+    L.args.ws_d = workspace;
+    L.args.ws_l = workspace + units * 128;
+    L.args.NP = static_cast<int>(n_t * 128);
+    L.args.o = o;
+    L.args.dout = dout;
+    L.args.dq = dq;
+    L.args.dk = dk;
+    L.args.dv = dv;
+    L.args.status = dev->status;
+    L.args.B = B;
+    L.args.H = H;
+    L.args.N = N;
+    L.args.n_t = static_cast<int>(n_t);
+    L.args.n_units = static_cast<int>(units);
+    L.args.n_units_kv = static_cast<int>(units_kv);
+    L.args.group = H / H_kv;
+    L.args.scale_log2 = static_cast<float>(static_cast<double>(alpha) * 1.4426950408889634);
+    L.args.alpha = alpha;
+    fa::mask_plan_layout(B, N, plan, &L.args.plan);
+    L.args.slopes = slopes;
+    // one CTA per unit in both main kernels, in the dynamic order (bwd_impl)
+    L.grid = static_cast<int>(units);
+    L.grid_kv = static_cast<int>(units_kv);
+    const uint64_t per_head = 4ull * static_cast<uint64_t>(N) * d;
+    const uint64_t bh = static_cast<uint64_t>(B) * H;
+    uint64_t c = (32ull << 20) / per_head;
+    c = c < 1 ? 1 : c > bh ? bh : c;
+    L.args.chunk = static_cast<int>(c);
+    const uint64_t rows_per_cta = 8ull * 4ull * (256ull / static_cast<uint64_t>(d));
+    const uint64_t gd = (static_cast<uint64_t>(B) * H * N + rows_per_cta - 1) / rows_per_cta;
+    const uint64_t gcap = 8ull * static_cast<uint64_t>(dev->sm_count);
+    L.grid_delta = static_cast<int>(gd < gcap ? gd : gcap);
+    L.d = d;
+    L.bf16 = dtype == FA_BF16;
+    L.stream = static_cast<cudaStream_t>(stream);
+    cudaError_t e = slopes ? fa::launch_bwd_mask_bias(L) : fa::launch_bwd_mask(L);
+    if (e == cudaSuccess && dsinks) e = fa::launch_bwd_dsink(L.args, sinks, dsinks, L.stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 // ---- rotary positions ----
 
 // Whether rows of two packed tensors, `w` elements wide and `s` apart, share

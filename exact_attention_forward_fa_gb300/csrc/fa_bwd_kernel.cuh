@@ -42,6 +42,7 @@
 #include <cstdint>
 
 #include "fa_device.cuh"
+#include "fa_mask.cuh"
 
 namespace fa {
 
@@ -75,6 +76,10 @@ struct BwdArgs {
     // t = tanh(sc_pre s) with sc_pre = alpha / c, in log2 units sc_post t
     // with sc_post = c log2(e); dS picks up the factor 1 - t^2.
     float sc_pre, sc_post;
+    // Interval masks (kMask instantiations): the plan's lists and intervals;
+    // kBias: the score loses slopes[h] |i - j|.  chunk as for causal units.
+    MaskPlan plan;
+    const float *slopes;
 };
 
 // Visible keys [win_klo, win_khi) of query row i (0 <= i < N), and visible
@@ -193,6 +198,7 @@ struct BwdCfg {
 // first key tiles).
 struct BwdUnit {
     int b, h, m;
+    int lo, hi;     // interval masks: key (or query) tiles of the unit
 };
 
 // kWin: the window's loop bounds; longest-first when it has a right bound
@@ -203,11 +209,25 @@ __device__ __forceinline__ bool bwd_longest_first(const BwdArgs &a) {
     return kWin ? (a.wl < 0 && a.wr >= 0) : kCausal;
 }
 
-template <bool kCausal, bool kKeyTiles, bool kWin = false>
+template <bool kCausal, bool kKeyTiles, bool kWin = false, bool kMask = false>
 __device__ __forceinline__ BwdUnit make_bwd_unit(int u, const BwdArgs &a) {
     BwdUnit U;
     const int HH = kKeyTiles ? a.H / a.group : a.H;     // K/V heads for key tiles
     const int BH = a.B * HH;
+    if constexpr (kMask) {
+        // the dynamic order over the plan's lists, which have the longest first
+        int i, bh;
+        dynamic_order(u, BH, a.n_t, a.chunk, i, bh);
+        U.b = bh / HH;
+        U.h = bh - U.b * HH;
+        const int4 *list = kKeyTiles ? a.plan.ktiles : a.plan.qtiles;
+        const int4 rec = __ldg(list + static_cast<size_t>(U.b) * a.n_t + (a.n_t - 1 - i));
+        U.m = rec.x;
+        U.lo = rec.y;
+        U.hi = rec.z;
+        return U;
+    }
+    U.lo = U.hi = 0;
     int bh;
     if (kCausal && !kWin) {
         // the forward's dynamic order (fa_fwd_kernel.cuh): unit i of a head
@@ -237,7 +257,8 @@ __device__ __forceinline__ BwdUnit make_bwd_unit(int u, const BwdArgs &a) {
 // with 16-byte loads; each thread handles 4 rows per pass for memory
 // parallelism.
 // ---------------------------------------------------------------------------
-template <int D, bool kBF16>
+// kMask: rows outside every document may hold anything; their D is 0.
+template <int D, bool kBF16, bool kMask = false>
 __global__ void __launch_bounds__(256)
 fa_bwd_delta_kernel(const BwdArgs a) {
     constexpr int TPR = D / 8;                       // threads per row
@@ -282,6 +303,10 @@ fa_bwd_delta_kernel(const BwdArgs a) {
                 const long h = row % a.H;
                 const long bn = row / a.H;
                 const long n = bn % a.N, b = bn / a.N;
+                if constexpr (kMask) {
+                    const int4 lv = __ldg(a.plan.live + b);
+                    if (n < lv.x || n >= lv.y) acc = 0.f;
+                }
                 a.ws_d[(b * a.H + h) * a.NP + n] = acc;
             }
         }
@@ -351,6 +376,45 @@ __device__ __forceinline__ void gemm_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uin
                          (accumulate || kk > 0) ? 1u : 0u);
 }
 
+// Interval masks: a tile that reaches outside the documents [live_lo, live_hi)
+// has these rows set to 0 in shared memory, by the eight elementwise warps (row
+// `row` of the tile starting at token `first`, this thread's half of it), for
+// products that weigh them with 0 (0 x NaN is not 0).
+template <int NCH>
+__device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, int half, int live_lo, int live_hi) {
+    if (first + row < live_lo || first + row >= live_hi) {
+        constexpr int PER = NCH == 2 ? 8 : 4;          // 16-byte vectors of this half
+        uint8_t *at = tile + (NCH == 2 ? half * 128 * 128 : half * 64) + row * 128;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) *reinterpret_cast<uint4 *>(at + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+}
+
+// Distance bias -beta |i - j| of columns c = 0, 1, ... of a tile row, in pairs:
+// linear (b0 + bs c) in a tile beside the diagonal one, with |c - d0| there.
+struct BiasCols {
+    float b0, bs, d0;
+    bool diag;
+    // add: what else every column gets (-LSE2 in the dQ kernel)
+    __device__ __forceinline__ float2 at(int c, float add) const {
+        if (diag) return make_float2(__fmaf_rn(-bs, fabsf(d0 - c), add), __fmaf_rn(-bs, fabsf(d0 - (c + 1)), add));
+        return make_float2(__fmaf_rn(bs, static_cast<float>(c), b0 + add),
+                           __fmaf_rn(bs, static_cast<float>(c + 1), b0 + add));
+    }
+};
+// Row token `mine` (in tile tm), columns [first, ...) of tile tc; dir: +1 when the
+// rows are queries and the columns keys, -1 the other way round (the distance is
+// symmetric: which side a tile lies on is all that counts).
+__device__ __forceinline__ BiasCols bias_cols(float beta, int mine, int tm, int first, int tc) {
+    BiasCols b;
+    b.diag = tc == tm;
+    b.bs = b.diag || tc < tm ? beta : -beta;
+    b.b0 = b.bs * static_cast<float>(first - mine);
+    b.d0 = static_cast<float>(mine - first);
+    return b;
+}
+
 // Epilogue store: columns [col0, col0 + W) of one row, v * scale -> 16 bit.
 template <int D, int W, bool kBF16>
 __device__ __forceinline__ void store_cols(void *dst_base, const BwdArgs &a, int heads, int b,
@@ -381,7 +445,8 @@ __device__ __forceinline__ void store_cols(void *dst_base, const BwdArgs &a, int
 // and dP(t+1); dS is double-buffered so dQ(t) reads dS(t) while dS(t+1) is
 // written.
 // ---------------------------------------------------------------------------
-template <int D, bool kCausal, bool kBF16, bool kWin = false, bool kCap = false>
+template <int D, bool kCausal, bool kBF16, bool kWin = false, bool kCap = false, bool kMask = false,
+          bool kBias = false>
 __global__ void __launch_bounds__(320, 1)
 fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -396,16 +461,19 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto bar = [&](int i) -> uint32_t { return base + C::DQ_BAR_OFF + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::DQ_MISC_OFF);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + C::DQ_MISC_OFF + 4);
-    // Causal without a window: one CTA per unit, running CTAs take over those
+    // Causal without a window, interval masks: one CTA per unit, running CTAs take over those
     // not yet started (clc_try_cancel).  The producer asks for the next unit
     // once it has issued the current one's loads; the k-th answer goes to
     // slot k % CLC_DEPTH, the producer publishes its block index there (-1:
     // none left), and the MMA warp and the 8 elementwise warps read it.
-    constexpr bool kDyn = kCausal && !kWin;
+    constexpr bool kDyn = (kCausal && !kWin) || kMask;
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::DQ_UNIT_OFF);
     // key tiles [lo, hi) of query tile U.m, visited from hi - 1 down
     auto key_range = [&](const BwdUnit &U, int &lo, int &hi) {
-        if constexpr (kWin) {
+        if constexpr (kMask) {
+            lo = U.lo;
+            hi = U.hi;
+        } else if constexpr (kWin) {
             const int r0 = U.m * 128, r1 = min(a.N, r0 + 128) - 1;
             lo = tile_lo(win_klo(r0, a));
             hi = tile_hi(win_khi(r1, a));
@@ -480,7 +548,8 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             };
             for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                      u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const BwdUnit U = make_bwd_unit<kCausal, false, kWin>(u, a);
+                const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
+                if (kMask && U.lo >= U.hi) continue;         // sees nothing: dQ is 0
                 ok = mbar_wait(bar(C::DQB_QEMPTY), (qn & 1) ^ 1, w, 50);
                 if (!ok) break;
                 mbar_arrive_expect_tx(bar(C::DQB_QFULL), 2 * C::TILE);
@@ -544,10 +613,11 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         };
         for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                  u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, false, kWin>(u, a);
+            const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
             int klo_t, khi_t;
             key_range(U, klo_t, khi_t);
             const int T = khi_t - klo_t;
+            if (kMask && T <= 0) continue;
             ok = mbar_wait_warp(bar(C::DQB_QFULL), qph, w, 60);
             if (!ok) break;
             qph ^= 1;
@@ -614,6 +684,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         WaitCtx w{abort_flag, a.status, kRoleSoftmax0};
         const float sl2 = a.scale_log2;
         uint32_t sph = 0, dpph = 0, dqph = 0;
+        uint32_t kt = 0;                            // interval masks: K tiles of the units so far
         bool ok = true;
         uint32_t kq = 0;                            // causal: answers read
         auto next_dyn = [&]() __attribute__((always_inline)) -> int {
@@ -629,14 +700,34 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         };
         for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
                  u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, false, kWin>(u, a);
+            const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
             int klo_t, khi_t;
             key_range(U, klo_t, khi_t);
             const int T = khi_t - klo_t;
             const int grow = U.m * 128 + row;
+            if (kMask && T <= 0) {                           // no row of the tile sees a key
+                if (grow < a.N) {
+                    uint4 *z = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dq) +
+                               ((static_cast<size_t>(U.b) * a.N + grow) * a.H + U.h) * D + half * (D / 2));
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) z[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                continue;
+            }
             // this row's visible keys (rows past N: any range; their P is 0)
             int klo_r = 0, khi_r = a.N;
-            if constexpr (kWin) {
+            int live_lo = 0, live_hi = a.N;
+            float beta = 0.f;                                // the bias a key of distance, log2 units
+            if constexpr (kMask) {
+                const int2 kr = grow < a.N ? __ldg(a.plan.rows + static_cast<size_t>(U.b) * a.N + grow)
+                                           : make_int2(0, 0);
+                klo_r = kr.x;
+                khi_r = kr.y;
+                const int4 lv = __ldg(a.plan.live + U.b);
+                live_lo = lv.x;
+                live_hi = lv.y;
+                if constexpr (kBias) beta = a.slopes[U.h] * 1.44269504088896340736f;
+            } else if constexpr (kWin) {
                 const int gr = min(grow, a.N - 1);
                 klo_r = win_klo(gr, a);
                 khi_r = win_khi(gr, a);
@@ -666,15 +757,40 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 int lim = min(128, a.N - j * 128) - col0;        // keys beyond N
                 if (kCausal) lim = min(lim, grow - j * 128 + 1 - col0);
                 int llo = 0;                                     // window: first visible
-                if constexpr (kWin) {
+                if constexpr (kWin || kMask) {
                     lim = min(lim, khi_r - j * 128 - col0);
                     llo = klo_r - j * 128 - col0;
                 }
                 float *pf = reinterpret_cast<float *>(sv);
+                // interval masks: whether every row of the warp sees all its columns
+                const bool whole = kMask && __all_sync(0xffffffffu, lim >= 64 && llo <= 0);
+                if constexpr (kMask) {
+                    // (S(t) has been formed, dQ(t) waits for dS(t): K rows may change)
+                    if (j * 128 < live_lo || j * 128 + 128 > live_hi)
+                        zero_outside<C::NCH>(gbase + C::DQ_K_OFF + ((kt + t) % C::KN) * C::TILE, j * 128, row, half,
+                                             live_lo, live_hi);
+                }
                 if constexpr (kCap) {
                     // keep t = tanh(alpha s / c); P comes from t in the dS step
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pf[c] = tanh_approx(pf[c] * a.sc_pre);
+                } else if constexpr (kMask) {
+                    const BiasCols bc = bias_cols(beta, grow, U.m, j * 128 + col0, j);
+                    if (whole && !(kBias && bc.diag)) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.at(c, -lse2) : nl2);
+                            pf[c] = ex2_approx(x.x);
+                            pf[c + 1] = ex2_approx(x.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.at(c, -lse2) : nl2);
+                            pf[c] = c < lim && c >= llo ? ex2_approx(x.x) : 0.f;
+                            pf[c + 1] = c + 1 < lim && c + 1 >= llo ? ex2_approx(x.y) : 0.f;
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
@@ -707,7 +823,13 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         pp.x = (i < lim && (!kWin || i >= llo)) ? ex2_approx(x.x) * dt.x : 0.f;
                         pp.y = (i + 1 < lim && (!kWin || i + 1 >= llo)) ? ex2_approx(x.y) * dt.y : 0.f;
                     }
-                    const float2 ds = __fmul2_rn(pp, g);
+                    float2 ds = __fmul2_rn(pp, g);
+                    if constexpr (kMask) {       // (dP and D of a row or key outside may be NaN)
+                        if (!whole) {
+                            ds.x = i < lim && i >= llo ? ds.x : 0.f;
+                            ds.y = i + 1 < lim && i + 1 >= llo ? ds.y : 0.f;
+                        }
+                    }
                     pk[i / 2] = pack2<kBF16>(ds.x, ds.y);
                 }
                 tmem_st32(tbase + lane_off + C::DQ_COL_DS + (t & 1) * 64u + half * 32, pk);
@@ -717,6 +839,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (lane == 0) mbar_arrive(bar(C::DQB_DSFULL + (t & 1)));
             }
             if (!ok) break;
+            kt += static_cast<uint32_t>(T);
             // ---- epilogue: dQ * alpha -> global (this warp's half of the columns) ----
             ok = mbar_wait(bar(C::DQB_DQFULL), dqph, w, 72);
             if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
@@ -764,7 +887,8 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // workspace through L1 (the producer prefetches them, and the elementwise
 // warps touch the next tile's sectors a tile ahead).
 // ---------------------------------------------------------------------------
-template <int D, bool kCausal, bool kBF16, bool kWin = false, bool kCap = false>
+template <int D, bool kCausal, bool kBF16, bool kWin = false, bool kCap = false, bool kMask = false,
+          bool kBias = false>
 __global__ void __launch_bounds__(320, 1)
 fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -779,16 +903,19 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto bar = [&](int i) -> uint32_t { return base + C::KV_BAR_OFF + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::KV_MISC_OFF);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + C::KV_MISC_OFF + 4);
-    // Causal without a window: one CTA per unit, running CTAs take over those
+    // Causal without a window, interval masks: one CTA per unit, running CTAs take over those
     // not yet started (clc_try_cancel).  The producer asks for the next unit
     // once it has issued the current one's loads; the k-th answer goes to
     // slot k % CLC_DEPTH, the producer publishes its block index there (-1:
     // none left), and the MMA warp and the 8 elementwise warps read it.
-    constexpr bool kDyn = kCausal && !kWin;
+    constexpr bool kDyn = (kCausal && !kWin) || kMask;
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::KV_UNIT_OFF);
     // query tiles [lo, hi) that see key tile U.m
     auto query_range = [&](const BwdUnit &U, int &lo, int &hi) {
-        if constexpr (kWin) {
+        if constexpr (kMask) {
+            lo = U.lo;
+            hi = U.hi;
+        } else if constexpr (kWin) {
             const int k0 = U.m * 128, k1 = min(a.N, k0 + 128) - 1;
             lo = tile_lo(win_qlo(k0, a));
             hi = tile_hi(win_qhi(k1, a));
@@ -866,7 +993,8 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
                      u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const BwdUnit U = make_bwd_unit<kCausal, true, kWin>(u, a);
+                const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
+                if (kMask && U.lo >= U.hi) continue;         // nobody sees it: dK = dV = 0
                 ok = mbar_wait(bar(C::KVB_KVEMPTY), (kvn & 1) ^ 1, w, 80);
                 if (!ok) break;
                 mbar_arrive_expect_tx(bar(C::KVB_KVFULL), 2 * C::TILE);
@@ -934,10 +1062,11 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
                  u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, true, kWin>(u, a);
+            const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
             int qlo_t, qhi_t;
             query_range(U, qlo_t, qhi_t);
             const int Ti = a.group * (qhi_t - qlo_t);    // query tiles of all the group's heads
+            if (kMask && Ti <= 0) continue;
             ok = mbar_wait_warp(bar(C::KVB_KVFULL), kvph, w, 90);
             if (!ok) break;
             kvph ^= 1;
@@ -1028,14 +1157,36 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         };
         for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
                  u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, true, kWin>(u, a);
+            const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
             int i0, qhi_t;
             query_range(U, i0, qhi_t);
             const int Ti = qhi_t - i0;
             const int krow = U.m * 128 + row;
+            if (kMask && Ti <= 0) {
+                if (krow < a.N) {
+                    const size_t at = ((static_cast<size_t>(U.b) * a.N + krow) * (a.H / a.group) + U.h) * D + half * (D / 2);
+                    uint4 *zk = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dk) + at);
+                    uint4 *zv = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dv) + at);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        zk[i] = make_uint4(0u, 0u, 0u, 0u);
+                        zv[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                continue;
+            }
             // this key row's visible queries (rows past N: any range)
             int qlo_r = 0, qhi_r = a.N;
-            if constexpr (kWin) {
+            int live_lo = 0, live_hi = a.N;
+            if constexpr (kMask) {
+                const int2 qr = krow < a.N ? __ldg(a.plan.cols + static_cast<size_t>(U.b) * a.N + krow)
+                                           : make_int2(0, 0);
+                qlo_r = qr.x;
+                qhi_r = qr.y;
+                const int4 lv = __ldg(a.plan.live + U.b);
+                live_lo = lv.x;
+                live_hi = lv.y;
+            } else if constexpr (kWin) {
                 const int kr = min(krow, a.N - 1);
                 qlo_r = win_qlo(kr, a);
                 qhi_r = win_qhi(kr, a);
@@ -1083,6 +1234,19 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 uint32_t sv[64];
                 const uint32_t tST = tbase + lane_off + C::st_col(stn);
                 const int pbar = C::p_bar(stn);
+                if constexpr (kMask) {
+                    // a query tile that reaches outside the documents: its Q (S^T has been
+                    // formed) and dO rows there become 0; dP^T, which may read them
+                    // meanwhile, is masked in those columns
+                    if (i * 128 < live_lo || i * 128 + 128 > live_hi) {
+                        ok = mbar_wait(bar(C::KVB_DOFULL + RO::slot(stn)), RO::phase(stn), w, 104);
+                        if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                        zero_outside<C::NCH>(gbase + C::KV_Q_OFF + RQ::slot(stn) * C::TILE, i * 128, row, half, live_lo,
+                                             live_hi);
+                        zero_outside<C::NCH>(gbase + C::KV_DO_OFF + RO::slot(stn) * C::TILE, i * 128, row, half, live_lo,
+                                             live_hi);
+                    }
+                }
                 ++stn;
                 tmem_ld32(tST + col0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
                 tmem_ld32(tST + col0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
@@ -1090,9 +1254,17 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // causal: query column q sees this key row iff krow <= q
                 int lo = (kCausal ? krow - i * 128 : 0) - col0;         // first visible column
                 int hi = 1 << 30;                                       // one past the last
-                if constexpr (kWin) {
+                if constexpr (kWin || kMask) {
                     lo = qlo_r - i * 128 - col0;
                     hi = qhi_r - i * 128 - col0;
+                }
+                constexpr bool kHi = kWin || kMask;
+                // interval masks: whether every key of the warp is seen by all its columns
+                const bool whole = kMask && __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
+                BiasCols bc{};
+                if constexpr (kBias) {
+                    const float beta = __ldg(a.slopes + hq) * 1.44269504088896340736f;
+                    bc = bias_cols(beta, krow, U.m, i * 128 + col0, i);
                 }
                 float *pf = reinterpret_cast<float *>(sv);
                 uint32_t pk[32];
@@ -1104,14 +1276,18 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
                     const float4 l4 = kCap ? __ldg(lse4 + c / 4) : lse_v[c / 4];
-                    const float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2,
-                                                  make_float2(-l4.x, -l4.y));
-                    const float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2,
-                                                  make_float2(-l4.z, -l4.w));
-                    const float p0 = (c + 0 >= lo && (!kWin || c + 0 < hi)) ? ex2_approx(x01.x) : 0.f;
-                    const float p1 = (c + 1 >= lo && (!kWin || c + 1 < hi)) ? ex2_approx(x01.y) : 0.f;
-                    const float p2 = (c + 2 >= lo && (!kWin || c + 2 < hi)) ? ex2_approx(x23.x) : 0.f;
-                    const float p3 = (c + 3 >= lo && (!kWin || c + 3 < hi)) ? ex2_approx(x23.y) : 0.f;
+                    float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2,
+                                            make_float2(-l4.x, -l4.y));
+                    float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2,
+                                            make_float2(-l4.z, -l4.w));
+                    if constexpr (kBias) {
+                        x01 = __fadd2_rn(x01, bc.at(c, 0.f));
+                        x23 = __fadd2_rn(x23, bc.at(c + 2, 0.f));
+                    }
+                    const float p0 = (c + 0 >= lo && (!kHi || c + 0 < hi)) ? ex2_approx(x01.x) : 0.f;
+                    const float p1 = (c + 1 >= lo && (!kHi || c + 1 < hi)) ? ex2_approx(x01.y) : 0.f;
+                    const float p2 = (c + 2 >= lo && (!kHi || c + 2 < hi)) ? ex2_approx(x23.x) : 0.f;
+                    const float p3 = (c + 3 >= lo && (!kHi || c + 3 < hi)) ? ex2_approx(x23.y) : 0.f;
                     if constexpr (!kCap) {
                         pf[c + 0] = p0;
                         pf[c + 1] = p1;
@@ -1160,8 +1336,16 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         p23.x = (c + 2 >= lo && (!kWin || c + 2 < hi)) ? ex2_approx(x23.x) * t23.x : 0.f;
                         p23.y = (c + 3 >= lo && (!kWin || c + 3 < hi)) ? ex2_approx(x23.y) * t23.y : 0.f;
                     }
-                    const float2 ds01 = __fmul2_rn(p01, g01);
-                    const float2 ds23 = __fmul2_rn(p23, g23);
+                    float2 ds01 = __fmul2_rn(p01, g01);
+                    float2 ds23 = __fmul2_rn(p23, g23);
+                    if constexpr (kMask) {       // (dP and D of a row or key outside may be NaN)
+                        if (!whole) {
+                            ds01.x = c + 0 >= lo && c + 0 < hi ? ds01.x : 0.f;
+                            ds01.y = c + 1 >= lo && c + 1 < hi ? ds01.y : 0.f;
+                            ds23.x = c + 2 >= lo && c + 2 < hi ? ds23.x : 0.f;
+                            ds23.y = c + 3 >= lo && c + 3 < hi ? ds23.y : 0.f;
+                        }
+                    }
                     pk[c / 2] = pack2<kBF16>(ds01.x, ds01.y);
                     pk[c / 2 + 1] = pack2<kBF16>(ds23.x, ds23.y);
                 }

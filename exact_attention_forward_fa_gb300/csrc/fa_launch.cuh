@@ -66,6 +66,9 @@ cudaError_t launch_bwd_win(const BwdLaunch &L);
 cudaError_t launch_selftest_timeout(uint32_t *status, uint32_t *result, cudaStream_t stream);
 // The same with a softcap (L.args.sc_pre, L.args.sc_post).
 cudaError_t launch_bwd_win_softcap(const BwdLaunch &L);
+// A mask plan's intervals (L.args.plan), without and with the distance bias.
+cudaError_t launch_bwd_mask(const BwdLaunch &L);
+cudaError_t launch_bwd_mask_bias(const BwdLaunch &L);
 // Gradient of per-head sink logits: dsinks[h] = -sum_{b,i} 2^(sigma_h log2 e
 // - LSE2_i) D_i over the workspace rows of the backward (one CTA per head).
 cudaError_t launch_bwd_dsink(const BwdArgs &a, const float *sinks, float *dsinks,

@@ -568,6 +568,22 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
                         fa_dtype dtype, void *stream);
 
 /*
+ * fa_bwd_masked -- its gradients, as fa_bwd_ext's: P recomputed from the LSE, the
+ * three kernels of fa_bwd.
+ *   q, k, v, plan, slopes, sinks, alpha : the forward's; o, lse its outputs.
+ *   o, dout, dq : device, [B][N][H][d]; dk, dv : [B][N][H_kv][d], contiguous;
+ *          dk and dv sum the gradients of their group's query heads in FP32.
+ *   workspace : as fa_bwd.
+ *   dsinks : as fa_bwd_ext, or NULL.  The slopes are constants: no gradient.
+ */
+fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void *o,
+                        const void *dout, const float *lse, float *workspace,
+                        const void *plan, const float *slopes, const float *sinks, void *dq,
+                        void *dk, void *dv, float *dsinks, int B, int H, int H_kv, int N,
+                        int d, long long q_stride, long long k_stride, long long v_stride,
+                        float alpha, fa_dtype dtype, void *stream);
+
+/*
  * Rotary positions.  A head's first rot_dim elements are pairs that turn by an
  * angle proportional to the token's position p:
  *     y0 = scale (x0 cos t - x1 sin t),  y1 = scale (x1 cos t + x0 sin t),

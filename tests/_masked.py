@@ -101,3 +101,17 @@ def check_forward(o, lse, r, dt, d, alpha, slopes):
     lim = (e + 2.0 ** -22 * r["lse"].abs())[~dead]
     assert (err <= lim).all(), ("LSE", float((err / lim).max()))
     assert (o.double().abs().amax(-1)[dead.transpose(1, 2)] == 0).all()
+
+
+def check_backward(got, r, dt, d, slopes):
+    """Tolerances in test_masked_bwd_gpu.py."""
+    u = U[dt]
+    far = 0.0 if slopes is None else 48 * 2.0 ** -24 * float((r["far"] + r["lse"].abs().nan_to_num(posinf=0.0)).max() + 8)
+    e = 2 * d * 2.0 ** -23 * float(r["dot"].max()) + 2.0 ** -18 + far
+    worst = {}
+    for name, x, size, rounds in (("dq", got[0], r["eq"], 2), ("dk", got[1], r["ek"], 2), ("dv", got[2], r["ev"], 1)):
+        tol = 1.05 * (rounds * u + e) * size + u * r[name].abs() + 2.0 ** -24
+        off = (x.double() - r[name]).abs()
+        assert not (off > tol).any(), (name, int((off > tol).sum()), float((off / tol).max()))
+        worst[name] = float((off / tol).max())
+    return worst
