@@ -37,7 +37,7 @@ FA_SCALE_TENSOR = 2
 # Every symbol include/fa.h declares (checked by the tests).
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_gqa_packed", "fa_fwd_ext", "fa_fwd_splitkv", "fa_splitkv_workspace_floats",
            "fa_splitkv_auto", "fa_quantize_fp8", "fa_quantize_fp8_granular", "fa_fwd_fp8", "fa_fwd_fp8_gqa", "fa_bwd", "fa_bwd_ext", "fa_bwd_noalloc",
-           "fa_paged_append", "fa_fwd_paged", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
+           "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_bias", "fa_paged_workspace_bytes", "fa_paged_scores", "fa_paged_evict",
            "fa_mask_plan", "fa_mask_plan_bytes", "fa_fwd_masked", "fa_bwd_masked", "fa_rope", "fa_paged_rope_append",
            "fa_check_status", "fa_status_detail", "fa_selftest_wait_timeout",
            "fa_status_string", "fa_version")
@@ -96,6 +96,8 @@ def load():
     lib.fa_paged_append.restype = i
     lib.fa_fwd_paged.argtypes = [vp] * 9 + [i] * 9 + [ll, ll, f, i, i, i, i, vp]
     lib.fa_fwd_paged.restype = i
+    lib.fa_fwd_paged_bias.argtypes = [vp] * 10 + [i] * 9 + [ll, ll, f, i, i, i, i, vp]
+    lib.fa_fwd_paged_bias.restype = i
     lib.fa_paged_workspace_bytes.argtypes = [i]
     lib.fa_paged_workspace_bytes.restype = ll
     lib.fa_paged_scores.argtypes = [vp] * 8 + [i] * 10 + [ll, ll, f, i, i, i, i, vp]
@@ -439,6 +441,18 @@ def fa_fwd_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, o, lse, workspa
                                _stream(stream))
 
 
+def fa_fwd_paged_bias(q, k_pages, v_pages, block_table, kv_len, cu_q, o, lse, workspace, slopes, B: int,
+                      H: int, H_kv: int, total_q: int, max_q: int, d: int, page_size: int,
+                      n_pages: int, table_width: int, q_stride: int, page_stride: int, alpha: float,
+                      window_left: int, window_right: int, first: int, dtype: int, stream=None) -> int:
+    """Direct call of the C entry point (see include/fa.h); ``lse`` may be None."""
+    return load().fa_fwd_paged_bias(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(kv_len), _ptr(cu_q), _ptr(o),
+        _ptr(lse), _ptr(workspace), _ptr(slopes), B, H, H_kv, total_q, max_q, d, page_size, n_pages,
+        table_width, q_stride, page_stride, alpha, window_left, window_right, first, dtype,
+        _stream(stream))
+
+
 def fa_paged_workspace_bytes(d: int) -> int:
     return load().fa_paged_workspace_bytes(int(d))
 
@@ -624,12 +638,14 @@ def paged_append(k, v, k_pages, v_pages, block_table, kv_len, cu_q, stream=None)
 
 def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, window=(-1, 0),
                     first: int = 0, alpha: float | None = None, out=None, lse=None,
-                    want_lse: bool = True, workspace=None, stream=None):
+                    want_lse: bool = True, workspace=None, stream=None, slopes=None):
     """Attention of the new tokens (packed q [T, H, d], sequence b's in rows
     cu_q[b] .. cu_q[b + 1]) over the cache that holds them: causal by default,
     window = (left, right) key bounds around a token's position (-1: none),
     the first ``first`` tokens visible beside a left bound.  ``max_q``: the
-    most new tokens of one sequence.  Returns (O [T, H, d], LSE [H, T] or
+    most new tokens of one sequence.  slopes float32 [H]: the scores lose
+    slopes[h] times the distance (then ``paged_scores``, which knows no bias, has
+    nothing to add up).  Returns (O [T, H, d], LSE [H, T] or
     None); rows behind cu_q[B] (a padded batch) are left as they were,
     uninitialised where O and LSE are allocated here."""
     torch = _torch or _use_torch()
@@ -637,7 +653,7 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
     if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
         with _launch_on(q.device, stream):
             return attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q, window, first,
-                                   alpha, out, lse, want_lse, workspace)
+                                   alpha, out, lse, want_lse, workspace, None, slopes)
     T, H, d = q.shape
     B, W = block_table.shape
     left, right = window
@@ -660,6 +676,8 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
         _check_float(lse, (H, T), at)
     elif want_lse:
         lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    if slopes is not None:
+        _check_float(slopes, (H,), at)
     raw = torch._C._cuda_getCurrentRawStream(at)
     shared = workspace is None and raw == 0
     if shared:
@@ -673,11 +691,13 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
             or workspace.numel() * workspace.element_size() < fa_paged_workspace_bytes(d)):
         raise ValueError(f"the workspace is {fa_paged_workspace_bytes(d)} bytes on {q.device}")
     try:
-        rc = load().fa_fwd_paged(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-            kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-            workspace.data_ptr(), B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha,
-            left, right, first, FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
+        head = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                workspace.data_ptr())
+        tail = (B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha, left, right, first,
+                FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
+        rc = (load().fa_fwd_paged(*head, *tail) if slopes is None
+              else load().fa_fwd_paged_bias(*head, slopes.data_ptr(), *tail))
     finally:
         if shared:
             _paged_ws_lock.release()

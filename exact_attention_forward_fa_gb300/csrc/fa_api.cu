@@ -889,12 +889,14 @@ static fa_status encode_packed_q(CUtensorMap *m, CUtensorMapDataType dt, const f
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
-fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
-                       const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q,
-                       void *o, float *lse, void *workspace, int B, int H, int H_kv, int total_q,
-                       int max_q, int d, int page_size, int n_pages, int table_width,
-                       long long q_stride, long long page_stride, float alpha, int window_left,
-                       int window_right, int first, fa_dtype dtype, void *stream) {
+static fa_status fwd_paged_impl(const void *q, const void *k_pages, const void *v_pages,
+                                const int32_t *block_table, const int32_t *kv_len,
+                                const int32_t *cu_q, void *o, float *lse, void *workspace,
+                                const float *slopes, int B, int H, int H_kv, int total_q, int max_q,
+                                int d, int page_size, int n_pages, int table_width,
+                                long long q_stride, long long page_stride, float alpha,
+                                int window_left, int window_right, int first, fa_dtype dtype,
+                                void *stream) {
     if (!v_pages || !workspace || (total_q > 0 && !o)) return FA_ERR_INVALID_ARG;
     fa::PagedFwdLaunch L;
     std::memset(&L, 0, sizeof(L));
@@ -911,6 +913,7 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     a.v_pages = v_pages;
     a.o = o;
     a.lse = lse;
+    a.slopes = slopes;
     a.status = dev->status;
     L.d = d;
     L.bf16 = dtype == FA_BF16;
@@ -936,8 +939,35 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
     L.w.desc = static_cast<int *>(workspace);
     L.w.lse = reinterpret_cast<float *>(L.w.desc + 8 * dev->sm_count);
     L.w.o = L.w.lse + static_cast<size_t>(dev->sm_count) * 2 * 256;
-    const cudaError_t e = d == 64 ? fa::launch_fwd_paged_d64(L) : fa::launch_fwd_paged_d128(L);
+    const cudaError_t e = slopes ? fa::launch_fwd_paged_bias(L)
+                          : d == 64 ? fa::launch_fwd_paged_d64(L) : fa::launch_fwd_paged_d128(L);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
+                       const int32_t *block_table, const int32_t *kv_len, const int32_t *cu_q,
+                       void *o, float *lse, void *workspace, int B, int H, int H_kv, int total_q,
+                       int max_q, int d, int page_size, int n_pages, int table_width,
+                       long long q_stride, long long page_stride, float alpha, int window_left,
+                       int window_right, int first, fa_dtype dtype, void *stream) {
+    return fwd_paged_impl(q, k_pages, v_pages, block_table, kv_len, cu_q, o, lse, workspace, nullptr, B, H,
+                          H_kv, total_q, max_q, d, page_size, n_pages, table_width, q_stride,
+                          page_stride, alpha, window_left, window_right, first, dtype, stream);
+}
+
+fa_status fa_fwd_paged_bias(const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *block_table, const int32_t *kv_len,
+                            const int32_t *cu_q, void *o, float *lse, void *workspace,
+                            const float *slopes, int B, int H, int H_kv, int total_q, int max_q,
+                            int d, int page_size, int n_pages, int table_width,
+                            long long q_stride, long long page_stride, float alpha,
+                            int window_left, int window_right, int first, fa_dtype dtype,
+                            void *stream) {
+    if (!slopes) return FA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_MISALIGNED;
+    return fwd_paged_impl(q, k_pages, v_pages, block_table, kv_len, cu_q, o, lse, workspace, slopes, B, H,
+                          H_kv, total_q, max_q, d, page_size, n_pages, table_width, q_stride,
+                          page_stride, alpha, window_left, window_right, first, dtype, stream);
 }
 
 fa_status fa_paged_scores(const void *q, const float *lse, const void *k_pages,

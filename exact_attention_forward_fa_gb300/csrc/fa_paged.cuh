@@ -37,6 +37,7 @@ struct PagedArgs {
     int ps_log2, n_pages;
     int wl, wr, first;
     float scale_log2;              // alpha * log2(e)
+    const float *slopes;           // [H] or nullptr: scores lose slopes[h] |p - j|
 };
 
 // Records an index out of range (the access itself is skipped).
@@ -188,6 +189,7 @@ struct PagedFwdLaunch {
 };
 cudaError_t launch_fwd_paged_d64(const PagedFwdLaunch &L);
 cudaError_t launch_fwd_paged_d128(const PagedFwdLaunch &L);
+cudaError_t launch_fwd_paged_bias(const PagedFwdLaunch &L);   // a.slopes set, d 64 or 128
 
 struct PagedScoresLaunch {
     CUtensorMap q, k;   // as in PagedFwdLaunch

@@ -99,7 +99,8 @@ struct PagedCfg {
     static constexpr float TAU = 8.0f, KEEP_SUM = 65504.0f;
 };
 
-template <int D, bool kBF16>
+// kBias: the scores lose beta |p - j|, beta = slopes of the row's head log2(e).
+template <int D, bool kBF16, bool kBias = false>
 __global__ void __launch_bounds__(384, 1)
 fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
@@ -296,6 +297,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             const int pos = p.pos + tile * R + my_pos;
             const int klo = paged_lo(pos, a.wl), khi = paged_hi(pos, p.n, a.wr), kf = min(a.first, khi);
             const int nf = min(a.first, p.vhi);            // first tokens that any row sees
+            const float beta = kBias && valid ? __ldg(a.slopes + p.h * a.group + my_head) * 1.44269504088896340736f : 0.f;
             // r: reference point (log2 units); le: row sum of the FP32
             // exponentials (LSE); lr: of the same rounded as P (normalises O).
             // Rows that hold no token never ask for a new reference.
@@ -340,6 +342,12 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 // P against the current reference first; the maximum only on the
                 // first tile or when a row's sum got too large (fa_fwd_kernel.cuh)
                 bool keep = __all_sync(0xffffffffu, r != -INFINITY);
+                // Distance bias: linear in the column, b0 + bs c, where all keys that a row
+                // sees here lie on one side of it; else with |k0 + c - pos|.
+                const bool left = khi <= pos + 1 || k0 + 127 <= pos;
+                const bool mixed = kBias && __any_sync(0xffffffffu, valid && !left && k0 < pos);
+                const float bs = left ? beta : -beta;
+                const float b0 = kBias ? bs * static_cast<float>(k0 - pos) : 0.f;
 #pragma unroll 1
                 for (;;) {
                     tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
@@ -358,6 +366,30 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 if (!(m & (1u << cc))) sf[32 * w32 + cc] = -INFINITY;
                         }
                     }
+                    // biased scores in log2 units, less the reference when it is kept
+                    if constexpr (kBias) {
+                        const float rk = keep ? r : 0.f;
+                        if (mixed) {
+                            const float d0 = static_cast<float>(pos - k0);
+#pragma unroll
+                            for (int cc = 0; cc < 128; ++cc)
+                                sf[cc] = __fmaf_rn(sf[cc], sl2, __fmaf_rn(-beta, fabsf(d0 - static_cast<float>(cc)), -rk));
+                        } else {
+                            const float2 step = make_float2(8.f * bs, 8.f * bs);
+                            float2 bc[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0 - rk), __fmaf_rn(bs, 2.f * q + 1.f, b0 - rk));
+#pragma unroll
+                            for (int cc = 0; cc < 128; cc += 2) {
+                                float2 &bq = bc[(cc >> 1) & 3];
+                                const float2 x = __ffma2_rn(make_float2(sf[cc], sf[cc + 1]), c2, bq);
+                                sf[cc] = x.x;
+                                sf[cc + 1] = x.y;
+                                bq = __fadd2_rn(bq, step);
+                            }
+                        }
+                    }
                     if (!keep) {
                         float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
 #pragma unroll
@@ -367,7 +399,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             m2 = max3(m2, sf[cc + 2], sf[cc + 6]);
                             m3 = max3(m3, sf[cc + 3], sf[cc + 7]);
                         }
-                        const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+                        const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * (kBias ? 1.f : sl2);
                         if (valid) {
                             if (r == -INFINITY) rn = bnew;
                             else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
@@ -378,10 +410,21 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const float2 nr2 = make_float2(-rs, -rs);
                     e_a = make_float2(0.f, 0.f);
                     e_b = e_a;
+                    if constexpr (kBias) {
+                        if (!keep) {
+#pragma unroll
+                            for (int cc = 0; cc < 128; cc += 2) {
+                                const float2 x = __fadd2_rn(make_float2(sf[cc], sf[cc + 1]), nr2);
+                                sf[cc] = x.x;
+                                sf[cc + 1] = x.y;
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int cc = 0; cc < 128; cc += 4) {
-                        const float2 x01 = __ffma2_rn(make_float2(sf[cc + 0], sf[cc + 1]), c2, nr2);
-                        const float2 x23 = __ffma2_rn(make_float2(sf[cc + 2], sf[cc + 3]), c2, nr2);
+                        const float2 s01 = make_float2(sf[cc + 0], sf[cc + 1]), s23 = make_float2(sf[cc + 2], sf[cc + 3]);
+                        const float2 x01 = kBias ? s01 : __ffma2_rn(s01, c2, nr2);
+                        const float2 x23 = kBias ? s23 : __ffma2_rn(s23, c2, nr2);
                         const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
                         const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
                         pk[cc / 2] = pack2<kBF16>(e01.x, e01.y);

@@ -10,13 +10,13 @@
 
 namespace fa {
 
-// kFew: the kernel for few rows, else the one for chunks.
-template <int D, bool kBF16, bool kFew>
+// kFew: the kernel for few rows, else the one for chunks; kBias: with a distance bias.
+template <int D, bool kBF16, bool kFew, bool kBias>
 cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
     using C = std::conditional_t<kFew, TokenCfg<D, kBF16>, PagedCfg<D, kBF16>>;
     void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedArgs, PagedWork, int);
-    if constexpr (kFew) kern = fa_paged_token_kernel<D, kBF16>;
-    else kern = fa_paged_fwd_kernel<D, kBF16>;
+    if constexpr (kFew) kern = fa_paged_token_kernel<D, kBF16, kBias>;
+    else kern = fa_paged_fwd_kernel<D, kBF16, kBias>;
     static unsigned long long configured = 0ull;   // bit per device id (< 64)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -50,11 +50,11 @@ cudaError_t launch_fwd_paged_inst(const PagedFwdLaunch &L) {
 // Up to kFewRows rows a tile: few rows against each K/V tile, bound by HBM.  64
 // single tokens of 4 heads a group (4 rows) on up to 8192 188 us, one on 777 tokens 11.8,
 // up to 4 rows of d = 64 with a window 60; the chunk kernel 197, 12.8 and 89 for the same.
-template <int D>
+template <int D, bool kBias = false>
 cudaError_t launch_fwd_paged_dispatch(const PagedFwdLaunch &L) {
     if (L.R * L.a.group <= kFewRows)
-        return L.bf16 ? launch_fwd_paged_inst<D, true, true>(L) : launch_fwd_paged_inst<D, false, true>(L);
-    return L.bf16 ? launch_fwd_paged_inst<D, true, false>(L) : launch_fwd_paged_inst<D, false, false>(L);
+        return L.bf16 ? launch_fwd_paged_inst<D, true, true, kBias>(L) : launch_fwd_paged_inst<D, false, true, kBias>(L);
+    return L.bf16 ? launch_fwd_paged_inst<D, true, false, kBias>(L) : launch_fwd_paged_inst<D, false, false, kBias>(L);
 }
 
 }  // namespace fa

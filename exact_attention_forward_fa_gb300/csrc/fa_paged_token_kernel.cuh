@@ -143,7 +143,8 @@ __device__ __forceinline__ bool group_any(int x, bool v) {
 // 535 of eight (32 rows), where the chunk kernel takes 190, and 22 to 26 us for
 // one sequence of 777 against 14: a thread's unrolled work on 32 rows, most of
 // it at the beginning and end of a piece, comes from L2 each time.
-template <int D, bool kBF16>
+// kBias: the scores lose beta_n |p_n - j|, beta_n = slopes of the row's head log2(e).
+template <int D, bool kBF16, bool kBias = false>
 __global__ void __launch_bounds__(416, 1)
 fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PagedArgs a, const PagedWork wk,
@@ -321,6 +322,16 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll
             for (int n = 0; n < kN; ++n) { le[n] = 0.f; lr[n] = 0.f; }
             uint32_t unseen = ~0u;                                           // rows without a reference yet
+            float beta[kBias ? kN : 1], place[kBias ? kN : 1];               // bias of a row, its place in the piece
+            if constexpr (kBias) {
+                int pl = 0, hd = 0;
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    beta[n] = n < nr ? __ldg(a.slopes + p.h * a.group + hd) * 1.44269504088896340736f : 0.f;
+                    place[n] = static_cast<float>(pl);
+                    if (++hd == a.group) { hd = 0; ++pl; }
+                }
+            }
 #pragma unroll 1
             for (int i = x; i < ns; i += 2) {
                 const int k0 = paged_tile(p, p.t0 + i) * 128, kk = k0 + row;
@@ -359,6 +370,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 }
                 // x - r; hidden scores are -inf, rows without a reference take r = 0
                 bool big = false;
+                const float ahead = kBias ? static_cast<float>(kk - p.pos) : 0.f;
 #pragma unroll
                 for (int n4 = 0; n4 < kN; n4 += 4) {
                     if (n4 >= nr) continue;
@@ -369,6 +381,7 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                         const int n = n4 + q;
                         const bool first_seen = (unseen & (1u << n)) != 0;
                         float v = fmaf(__uint_as_float(s[n]), sl2, first_seen ? 0.f : -rv[q]);
+                        if constexpr (kBias) v = fmaf(-beta[n], fabsf(ahead - place[n]), v);
                         v = n >= ca && n < cb ? v : -INFINITY;
                         big |= v > C::CAP || (first_seen && v != -INFINITY);
                         s[n] = __float_as_uint(v);

@@ -439,6 +439,22 @@ fa_status fa_fwd_paged(const void *q, const void *k_pages, const void *v_pages,
                        long long page_stride, float alpha, int window_left,
                        int window_right, int first, fa_dtype dtype, void *stream);
 
+/*
+ * fa_fwd_paged_bias -- fa_fwd_paged with a bias that depends on the distance: the
+ * score of the row at position p against key j loses slopes[h] |p - j| (h: the
+ * row's query head; the serving form of fa_fwd_masked's slopes).
+ *   slopes : device, float [H], finite.
+ * Other arguments, results and errors as fa_fwd_paged, its workspace too.
+ */
+fa_status fa_fwd_paged_bias(const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *block_table, const int32_t *kv_len,
+                            const int32_t *cu_q, void *o, float *lse, void *workspace,
+                            const float *slopes, int B, int H, int H_kv, int total_q,
+                            int max_q, int d, int page_size, int n_pages, int table_width,
+                            long long q_stride, long long page_stride, float alpha,
+                            int window_left, int window_right, int first, fa_dtype dtype,
+                            void *stream);
+
 /* fa_paged_workspace_bytes -- workspace of fa_fwd_paged on the current
  * device, whatever the problem's other sizes; -1 for a head dim without a
  * kernel or without an sm_103 device. */
