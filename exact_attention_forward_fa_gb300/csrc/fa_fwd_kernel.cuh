@@ -141,7 +141,9 @@ struct FwdCfg {
     static constexpr uint32_t CLC_OFF = (MISC_OFF + 16 + 15) & ~15u;
     static_assert(CLC_OFF % 16 == 0, "cluster launch control answers: 16-byte aligned");
     static constexpr uint32_t UNIT_OFF = CLC_OFF + CLC_DEPTH * 16;   // int per answer
-    static constexpr uint32_t SMEM_BYTES = UNIT_OFF + CLC_DEPTH * 4 + 1024;   // + align slack
+    // interval masks: a unit's record (MaskRec) for each answer
+    static constexpr uint32_t REC_OFF = (UNIT_OFF + CLC_DEPTH * 4 + 15) & ~15u;
+    static constexpr uint32_t SMEM_BYTES = REC_OFF + CLC_DEPTH * 48 + 1024;   // + align slack
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
     // TMEM columns
@@ -226,32 +228,47 @@ __device__ __forceinline__ constexpr bool dynamic_units() {
     return kVar >= 3 || (kCausal && !kSplit && !kVar && !kPack);
 }
 
+// Interval masks: unit u's batch row and head and its pair's record of the plan.
+// The producer reads it and hands it on through shared memory, so that the other
+// roles need neither the divisions nor the loads.
+struct MaskRec {
+    int4 id;       // u (-1: no more units), b, h, pair
+    int4 tiles;    // key tiles [x, y) of the pair's first Q tile, [z, w) of its second
+    int4 live;     // tokens [x, y) of the sequence belong to documents
+};
+__device__ __forceinline__ MaskRec mask_rec(int u, const FwdArgs &a) {
+    int i, bh;
+    dynamic_order(u, a.B * a.H, a.n_pairs, a.chunk, i, bh);
+    const int b = bh / a.H;
+    const int4 *rec = a.plan.pairs + 2 * (static_cast<size_t>(b) * a.n_pairs + (a.n_pairs - 1 - i));
+    const int4 r0 = __ldg(rec), r1 = __ldg(rec + 1);
+    return MaskRec{make_int4(u, b, bh - b * a.H, r0.x), make_int4(r0.y, r0.z, r1.y, r1.z), make_int4(r0.w, r1.w, 0, 0)};
+}
+__device__ __forceinline__ Unit mask_unit(const MaskRec &r) {
+    Unit U;
+    U.b = r.id.y;
+    U.h = r.id.z;
+    U.s = 0;
+    const int lo[2] = {r.tiles.x, r.tiles.z}, hi[2] = {r.tiles.y, r.tiles.w};
+    for (int x = 0; x < 2; ++x) {
+        U.m[x] = 2 * r.id.w + x;
+        U.act[x] = hi[x] > lo[x];
+    }
+    const int jlo = !U.act[1] ? lo[0] : !U.act[0] ? lo[1] : min(lo[0], lo[1]);
+    U.jhi = !U.act[1] ? hi[0] : !U.act[0] ? hi[1] : max(hi[0], hi[1]);
+    U.T = U.jhi - jlo;                             // 0: neither tile sees a key
+    for (int x = 0; x < 2; ++x) {
+        U.t0[x] = U.act[x] ? U.jhi - hi[x] : U.T;
+        U.t1[x] = U.act[x] ? U.jhi - lo[x] : U.T;
+    }
+    return U;
+}
+
 template <bool kCausal, bool kSplit, int kVar = 0, bool kPack = false>
 __device__ __forceinline__ Unit make_unit(int u, const FwdArgs &a) {
     Unit U;
     constexpr bool kExt = kVar != 0;
-    if constexpr (kVar >= 3) {
-        int i, bh;
-        dynamic_order(u, a.B * a.H, a.n_pairs, a.chunk, i, bh);
-        U.b = bh / a.H;
-        U.h = bh - U.b * a.H;
-        U.s = 0;
-        const int4 *rec = a.plan.pairs + 2 * (static_cast<size_t>(U.b) * a.n_pairs + (a.n_pairs - 1 - i));
-        const int4 r0 = __ldg(rec), r1 = __ldg(rec + 1);
-        const int lo[2] = {r0.y, r1.y}, hi[2] = {r0.z, r1.z};
-        for (int x = 0; x < 2; ++x) {
-            U.m[x] = 2 * r0.x + x;
-            U.act[x] = hi[x] > lo[x];
-        }
-        const int jlo = !U.act[1] ? lo[0] : !U.act[0] ? lo[1] : min(lo[0], lo[1]);
-        U.jhi = !U.act[1] ? hi[0] : !U.act[0] ? hi[1] : max(hi[0], hi[1]);
-        U.T = U.jhi - jlo;                         // 0: neither tile sees a key
-        for (int x = 0; x < 2; ++x) {
-            U.t0[x] = U.act[x] ? U.jhi - hi[x] : U.T;
-            U.t1[x] = U.act[x] ? U.jhi - lo[x] : U.T;
-        }
-        return U;
-    }
+    static_assert(kVar < 3, "interval masks: MaskRec");
     const int HH = kPack ? a.H / a.group : a.H;    // heads the units run over
     const int BH = a.B * HH;
     const int S = kSplit ? a.n_splits : 1;
@@ -366,6 +383,13 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     // Static order: the persistent stride walk.
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::UNIT_OFF);
     constexpr bool kDyn = dynamic_units<kCausal, kSplit, kVar, kPack>();
+    // Interval masks: every unit, the first too, comes through the slots, as the
+    // record that the producer publishes.
+    const volatile int4 *rec_slot = reinterpret_cast<const volatile int4 *>(gbase + C::REC_OFF);
+    auto read_rec = [&](uint32_t q) __attribute__((always_inline)) -> MaskRec {
+        auto get = [&](int i) { const volatile int4 &v = rec_slot[3 * q + i]; return make_int4(v.x, v.y, v.z, v.w); };
+        return MaskRec{get(0), get(1), get(2)};
+    };
 
     auto bar = [&](int i) -> uint32_t { return base + C::BAR_OFF + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::MISC_OFF);
@@ -463,9 +487,40 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 mbar_arrive(bar(C::B_UNIT + q));        // release: the index is visible
                 return nu;
             };
-            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                     u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
+            // Interval masks: publishes unit u (-1: the end) and asks for the one after
+            // it, whose answer is awaited behind this unit's loads (asked behind
+            // them it came 3000 cycles late).
+            auto publish = [&](int u, Unit &U) __attribute__((always_inline)) -> bool {
+                const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+                MaskRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                if (u >= 0) r = mask_rec(u, a);
+                U = mask_unit(r);
+                ++kq;
+                if (!mbar_wait(bar(C::B_CLCEMPTY + q), ph ^ 1u, w, 3)) { ok = false; return false; }
+                int4 *slot_r = reinterpret_cast<int4 *>(gbase + C::REC_OFF) + 3 * q;
+                slot_r[0] = r.id;
+                slot_r[1] = r.tiles;
+                slot_r[2] = r.live;
+                mbar_arrive(bar(C::B_UNIT + q));        // release: the record is visible
+                if (u < 0) return false;
+                mbar_arrive_expect_tx(bar(C::B_CLCFULL), 16u);
+                clc_try_cancel(base + C::CLC_OFF, bar(C::B_CLCFULL));
+                clc_pending = true;
+                return true;
+            };
+            auto answer = [&]() __attribute__((always_inline)) -> int {
+                if (!ok || !mbar_wait(bar(C::B_CLCFULL), (kq - 1) & 1u, w, 4)) { ok = false; return -1; }
+                clc_pending = false;
+                return clc_block(base + C::CLC_OFF);
+            };
+            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (kMask || ((!kDyn || u >= 0) && u < a.n_units));
+                     u = kMask ? answer() : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+                Unit U;
+                if constexpr (kMask) {
+                    if (!publish(u, U)) break;
+                } else {
+                    U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
+                }
                 if (U.act[0]) ok = ok && load_q(0, U);
                 if (U.act[1]) ok = ok && load_q(1, U);
                 const int hk = kPack ? U.h : U.h / a.group;   // K/V head of this query head
@@ -486,7 +541,9 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 }
             }
             // Let every copy this lane issued land before the CTA can exit.
-            if (kDyn && clc_pending)
+            if (kMask && clc_pending)
+                mbar_wait_quiet(bar(C::B_CLCFULL), (kq - 1) & 1u, 500000000ull);
+            else if (kDyn && clc_pending)
                 mbar_wait_quiet(bar(C::B_CLCFULL + (kq - 1) % C::CLC_DEPTH),
                                 ((kq - 1) / C::CLC_DEPTH) & 1u, 500000000ull);
             for (int s = 0; s < C::NSTAGE; ++s)
@@ -517,9 +574,22 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
                 return nu;
             };
-            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                     u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
+            auto next_rec = [&](Unit &U) __attribute__((always_inline)) -> int {
+                if (!ok) return -1;
+                const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+                ++kq;
+                if (!mbar_wait_warp(bar(C::B_UNIT + q), ph, w, 15)) { ok = false; return -1; }
+                const MaskRec r = read_rec(q);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
+                U = mask_unit(r);
+                return r.id.x;
+            };
+            Unit U;
+            for (int u = kMask ? next_rec(U) : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                     ok && (!kDyn || u >= 0) && u < a.n_units;
+                     u = kMask ? next_rec(U) : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+                if constexpr (!kMask) U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 uint32_t qs0 = 0, qp0 = 0, qs1 = 0, qp1 = 0;   // Q slot and parity per tile
                 if (U.act[0]) { qs0 = qc % C::NQ; qp0 = (qc / C::NQ) & 1u; ++qc; }
                 if (U.act[1]) { qs1 = qc % C::NQ; qp1 = (qc / C::NQ) & 1u; ++qc; }
@@ -639,15 +709,43 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
             return nu;
         };
-        for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                     u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const Unit U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
+        // Interval masks: the next unit's record, and this row's visible keys and bias
+        // in it, are read before the stores of the unit at hand (behind them these
+        // loads took 4000 cycles).
+        Unit Un;
+        int2 kr_n = make_int2(0, 0), live_n = make_int2(0, 0);
+        float beta_n = 0.f;
+        auto fetch = [&]() __attribute__((always_inline)) -> int {
+            const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+            ++kq;
+            ok = mbar_wait(bar(C::B_UNIT + q), ph, w, 23);
+            if (__any_sync(0xffffffffu, !ok)) { ok = false; return -1; }
+            const MaskRec r = read_rec(q);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
+            if (r.id.x < 0) return -1;
+            Un = mask_unit(r);
+            live_n = make_int2(r.live.x, r.live.y);
+            const int n = (x ? Un.m[1] : Un.m[0]) * 128 + row;
+            kr_n = n < a.N ? __ldg(a.plan.rows + static_cast<size_t>(Un.b) * a.N + n) : make_int2(0, 0);
+            if constexpr (kBias) beta_n = __ldg(a.slopes + Un.h) * 1.44269504088896340736f;
+            return r.id.x;
+        };
+        for (int u = kMask ? fetch() : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                     ok && (!kDyn || u >= 0) && u < a.n_units;
+                     u = kMask ? u : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+            Unit U;
+            if constexpr (kMask) U = Un;
+            else U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
             const bool act = x ? U.act[1] : U.act[0];
             const int mt = x ? U.m[1] : U.m[0];
             const uint32_t kv0 = kvc;                    // K and V tiles before this unit's
+            const int2 kr = kr_n, docs_at = live_n;
+            const float beta = beta_n;                   // the bias a key of distance, log2 units
             if constexpr (kMask) {
                 kvc += 2u * static_cast<uint32_t>(U.T);
                 if (!act) {                              // no row of the tile sees a key
+                    u = fetch();
                     const int n = mt * 128 + row;
                     if (n < a.N) {
                         uint4 *o4 = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) +
@@ -669,18 +767,9 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             const int t1 = kExt ? (x ? U.t1[1] : U.t1[0]) : U.T;
             // this row's visible keys (rows past N: any non-empty range)
             int klo = 0, khi = a.N;
-            int live_lo = 0, live_hi = a.N;
-            float beta = 0.f;                            // the bias a key of distance, log2 units
             if constexpr (kMask) {
-                const int2 kr = mt * 128 + row < a.N
-                                    ? __ldg(a.plan.rows + static_cast<size_t>(U.b) * a.N + mt * 128 + row)
-                                    : make_int2(0, 0);
                 klo = kr.x;
                 khi = kr.y;
-                const int4 lv = __ldg(a.plan.live + U.b);
-                live_lo = lv.x;
-                live_hi = lv.y;
-                if constexpr (kBias) beta = a.slopes[U.h] * 1.44269504088896340736f;
             } else if constexpr (kExt) {
                 const int gr = min(mt * 128 + row, a.N - 1);
                 klo = window_lo(gr, a);
@@ -739,12 +828,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     // ---- a tile that reaches outside the documents: those V rows
                     //      become 0 (P is 0 there, and 0 x NaN is not); both groups
                     //      may write them, each before its own P is published ----
-                    if (j * 128 < live_lo || j * 128 + 128 > live_hi) {
+                    if (j * 128 < docs_at.x || j * 128 + 128 > docs_at.y) {
                         const uint32_t idx = kv0 + 2u * static_cast<uint32_t>(t) + 1u, slot = idx % C::NSTAGE;
                         ok = mbar_wait(bar(C::B_KVFULL + slot), (idx / C::NSTAGE) & 1u, w, 22);
                         if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
                         const int key = j * 128 + row;
-                        if (key < live_lo || key >= live_hi) {
+                        if (key < docs_at.x || key >= docs_at.y) {
                             uint8_t *vr = gbase + C::KV_OFF + slot * C::TILE_BYTES + row * 128;
 #pragma unroll
                             for (int ch = 0; ch < C::NCH; ++ch)
@@ -782,7 +871,9 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
                     tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
                     tmem_ld_wait();
-                    if constexpr (kExt) {
+                    if constexpr (kMask) {
+                        // (masked below)
+                    } else if constexpr (kExt) {
                         if constexpr (kCap) {
 #pragma unroll
                             for (int c = 0; c < 128; ++c) sf[c] = tanh_approx(sf[c] * sc_pre);
@@ -799,7 +890,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         }
                     }
                 };
-                load_s();
+                if constexpr (!kMask) load_s();
                 auto row_max = [&]() __attribute__((always_inline)) -> float {
                     float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
 #pragma unroll
@@ -817,7 +908,110 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 bool need = false;
                 float2 e_a, e_b;
                 uint32_t p[kFP8 ? 32 : 64];
-                if constexpr (kFP8) {
+                if constexpr (kMask) {
+                    // ---- as for 16-bit P below: against the current reference where all
+                    //      rows of the warp see the whole tile; else, and where that
+                    //      fails, with the row maximum ----
+                    const float2 c2 = make_float2(sl2, sl2);
+                    const bool masked = __any_sync(0xffffffffu, lim < 128 || llo > 0);
+                    // Distance bias, -beta |i - j|: in a tile before or behind the
+                    // diagonal one it is linear in the column, b0 + bs c.
+                    const float bs = kBias ? (j < mt ? beta : -beta) : 0.f;
+                    const float b0 = kBias ? bs * static_cast<float>(j * 128 - qpos) : 0.f;
+                    bool done = !masked && !(kBias && j == mt) && __all_sync(0xffffffffu, r != -INFINITY);
+                    if (done) {
+                        load_s();
+                        e_a = make_float2(0.f, 0.f);
+                        e_b = e_a;
+                        const float2 nr2 = make_float2(-r, -r);
+                        const float2 step = make_float2(8.f * bs, 8.f * bs);
+                        float2 bc[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0 - r), __fmaf_rn(bs, 2.f * i + 1.f, b0 - r));
+#pragma unroll
+                        for (int c = 0; c < 128; c += 4) {
+                            float2 &b01 = bc[(c >> 1) & 3], &b23 = bc[((c >> 1) + 1) & 3];
+                            const float2 x01 = __ffma2_rn(make_float2(sf[c + 0], sf[c + 1]), c2, kBias ? b01 : nr2);
+                            const float2 x23 = __ffma2_rn(make_float2(sf[c + 2], sf[c + 3]), c2, kBias ? b23 : nr2);
+                            if constexpr (kBias) {
+                                b01 = __fadd2_rn(b01, step);
+                                b23 = __fadd2_rn(b23, step);
+                            }
+                            const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                            const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                            p[c / 2] = pack2<kBF16>(e01.x, e01.y);
+                            p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                            e_a = __fadd2_rn(e_a, e01);
+                            e_b = __fadd2_rn(e_b, e23);
+                        }
+                        const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                        done = __all_sync(0xffffffffu, ts <= C::KEEP_SUM);          // NaN: redo
+                    }
+                    if (!done) {
+                        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                        tmem_ld_wait();
+                        if (masked) {
+#pragma unroll
+                            for (int w32 = 0; w32 < 4; ++w32) {
+                                // bit c of m: column 32 w32 + c is visible
+                                auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                                const uint32_t m = below(lim - 32 * w32) & ~below(llo - 32 * w32);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(m & (1u << c))) sf[32 * w32 + c] = -INFINITY;
+                            }
+                        }
+                        if constexpr (kBias) {
+                            // biased scores in log2 units
+                            if (j == mt) {
+                                const float d0 = static_cast<float>(row);
+#pragma unroll
+                                for (int c = 0; c < 128; ++c)
+                                    sf[c] = __fmaf_rn(sf[c], sl2, -beta * fabsf(d0 - static_cast<float>(c)));
+                            } else {
+                                const float2 step = make_float2(8.f * bs, 8.f * bs);
+                                float2 bc[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0), __fmaf_rn(bs, 2.f * i + 1.f, b0));
+#pragma unroll
+                                for (int c = 0; c < 128; c += 2) {
+                                    float2 &bq = bc[(c >> 1) & 3];
+                                    const float2 v = __ffma2_rn(make_float2(sf[c], sf[c + 1]), c2, bq);
+                                    sf[c] = v.x;
+                                    sf[c + 1] = v.y;
+                                    bq = __fadd2_rn(bq, step);
+                                }
+                            }
+                        }
+                        const float bnew = kBias ? row_max() : row_max() * sl2;
+                        if (r == -INFINITY) rn = bnew;
+                        else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
+                        need = (r != -INFINITY) && (rn != r);
+                        const float rs = rn == -INFINITY ? 0.f : rn;
+                        const float2 nr2 = make_float2(-rs, -rs);
+                        e_a = make_float2(0.f, 0.f);
+                        e_b = e_a;
+#pragma unroll
+                        for (int c = 0; c < 128; c += 4) {
+                            const float2 s01 = make_float2(sf[c + 0], sf[c + 1]), s23 = make_float2(sf[c + 2], sf[c + 3]);
+                            const float2 x01 = kBias ? __fadd2_rn(s01, nr2) : __ffma2_rn(s01, c2, nr2);
+                            const float2 x23 = kBias ? __fadd2_rn(s23, nr2) : __ffma2_rn(s23, c2, nr2);
+                            const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                            const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                            p[c / 2] = pack2<kBF16>(e01.x, e01.y);
+                            p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                            e_a = __fadd2_rn(e_a, e01);
+                            e_b = __fadd2_rn(e_b, e23);
+                        }
+                    }
+                    tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
+                } else if constexpr (kFP8) {
                     const float sc = sc_c, voff = voff_c;
                     // e4m3 saturates above 448, so the row max comes first.
                     const float bnew = row_max() * sc;             // -inf stays -inf
@@ -846,76 +1040,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     //      the max is formed only on the first tile or when
                     //      the tile's sum exceeds KEEP_SUM ----
                     const float2 c2 = make_float2(sl2, sl2);
-                    // Distance bias, -beta |i - j|: in a tile before or behind the
-                    // diagonal one it is linear in the column, b0 + bs c.
-                    const float bs = kBias ? (j < mt ? beta : -beta) : 0.f;
-                    const float b0 = kBias ? bs * static_cast<float>(j * 128 - qpos) : 0.f;
-                    bool scaled = false;                // s holds biased scores in log2 units
-                    auto to_scaled = [&]() __attribute__((always_inline)) {
-                        scaled = true;
-                        if (j != mt) {
-                            const float2 step = make_float2(8.f * bs, 8.f * bs);
-                            float2 bc[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0), __fmaf_rn(bs, 2.f * i + 1.f, b0));
-#pragma unroll
-                            for (int c = 0; c < 128; c += 2) {
-                                float2 &b = bc[(c >> 1) & 3];
-                                const float2 x = __ffma2_rn(make_float2(sf[c], sf[c + 1]), c2, b);
-                                sf[c] = x.x;
-                                sf[c + 1] = x.y;
-                                b = __fadd2_rn(b, step);
-                            }
-                        } else {
-                            const float d0 = static_cast<float>(row);
-#pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                sf[c] = __fmaf_rn(sf[c], sl2, -beta * fabsf(d0 - static_cast<float>(c)));
-                        }
-                    };
                     auto exps = [&](const float rs) __attribute__((always_inline)) {
                         const float2 nr2 = make_float2(-rs, -rs);
-                        if constexpr (kBias) {
-                            // s is raw in a linear tile that keeps its reference, else scaled
-                            e_a = make_float2(0.f, 0.f);
-                            e_b = e_a;
-                            if (!scaled) {
-                                const float2 step = make_float2(8.f * bs, 8.f * bs);
-                                float2 bc[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0 - rs),
-                                                        __fmaf_rn(bs, 2.f * i + 1.f, b0 - rs));
-#pragma unroll
-                                for (int c = 0; c < 128; c += 4) {
-                                    float2 &b01 = bc[(c >> 1) & 3], &b23 = bc[((c >> 1) + 1) & 3];
-                                    const float2 x01 = __ffma2_rn(make_float2(sf[c + 0], sf[c + 1]), c2, b01);
-                                    const float2 x23 = __ffma2_rn(make_float2(sf[c + 2], sf[c + 3]), c2, b23);
-                                    b01 = __fadd2_rn(b01, step);
-                                    b23 = __fadd2_rn(b23, step);
-                                    const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
-                                    const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
-                                    p[c / 2] = pack2<kBF16>(e01.x, e01.y);
-                                    p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
-                                    e_a = __fadd2_rn(e_a, e01);
-                                    e_b = __fadd2_rn(e_b, e23);
-                                }
-                            } else {
-#pragma unroll
-                                for (int c = 0; c < 128; c += 4) {
-                                    const float2 x01 = __fadd2_rn(make_float2(sf[c + 0], sf[c + 1]), nr2);
-                                    const float2 x23 = __fadd2_rn(make_float2(sf[c + 2], sf[c + 3]), nr2);
-                                    const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
-                                    const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
-                                    p[c / 2] = pack2<kBF16>(e01.x, e01.y);
-                                    p[c / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
-                                    e_a = __fadd2_rn(e_a, e01);
-                                    e_b = __fadd2_rn(e_b, e23);
-                                }
-                            }
-                            return;
-                        }
                         e_a = make_float2(0.f, 0.f);
                         e_b = e_a;
 #pragma unroll
@@ -930,19 +1056,15 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             e_b = __fadd2_rn(e_b, e23);
                         }
                     };
-                    // (interval masks: a row without a reference that sees nothing
-                    // here needs none yet)
-                    bool keep = __all_sync(0xffffffffu, r != -INFINITY || (kMask && (lim <= 0 || llo >= 128)));
+                    bool keep = __all_sync(0xffffffffu, r != -INFINITY);
                     if (keep) {
-                        if (kBias && j == mt) to_scaled();
-                        exps(kMask && r == -INFINITY ? 0.f : r);
+                        exps(r);
                         const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
                         keep = __all_sync(0xffffffffu, ts <= C::KEEP_SUM);   // NaN: redo
                         if (!keep) load_s();
                     }
                     if (!keep) {
-                        if constexpr (kBias) to_scaled();
-                        const float bnew = kBias ? row_max() : row_max() * sl2;
+                        const float bnew = row_max() * sl2;
                         if (r == -INFINITY) rn = bnew;
                         else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
                         need = (r != -INFINITY) && (rn != r);
@@ -1028,6 +1150,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             };
             if constexpr (!C::kLMMA) normalise();
             const int grow = qpos;
+            if constexpr (kMask) {
+                u = fetch();
+                if (!ok) break;
+            }
             {
                 // ---- epilogue: O / l -> global ----
                 ok = mbar_wait(bar(C::B_OFULL + x), oph, w, 21);

@@ -23,7 +23,7 @@ namespace fa {
 // longest first.
 struct MaskPlan {
     const int4 *live;    // [B] {first token of a document, one past the last, 0, 0}
-    const int4 *pairs;   // [B][n_p][2] {pair p, lo, hi, 0} of tile 2p, {0, lo, hi, 0} of 2p + 1: key tiles
+    const int4 *pairs;   // [B][n_p][2] {pair p, lo, hi, live.x} of tile 2p, {0, lo, hi, live.y} of 2p + 1: key tiles
     const int4 *qtiles;  // [B][n_t] {query tile, lo, hi, 0}: key tiles
     const int4 *ktiles;  // [B][n_t] {key tile, lo, hi, 0}: query tiles
     const int2 *rows;    // [B][N] visible keys of a token

@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) fa_mask_plan_kernel(const MaskPlanAr
         }, [&](int p, int place) {
             int2 x, y;
             ranges(p, x, y);
-            out[2 * place] = make_int4(p, x.x, x.y, 0);
-            out[2 * place + 1] = make_int4(0, y.x, y.y, 0);
+            out[2 * place] = make_int4(p, x.x, x.y, live_lo);
+            out[2 * place + 1] = make_int4(0, y.x, y.y, live_hi);
         });
     } else if (blockIdx.x == 1) {                 // query tiles
         int4 *out = const_cast<int4 *>(a.plan.qtiles) + static_cast<size_t>(b) * n_t;
