@@ -1157,6 +1157,7 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
     if ((st = encode_bshd(&L.q, q, dt, B, H, N, d, 128, q_stride)) != FA_OK) return st;
     if ((st = encode_bshd(&L.k, k, dt, B, H_kv, N, d, 128, k_stride)) != FA_OK) return st;
     if ((st = encode_bshd(&L.v, v, dt, B, H_kv, N, d, 128, v_stride)) != FA_OK) return st;
+    if ((st = encode_bshd(&L.o, o, dt, B, H, N, d, 128)) != FA_OK) return st;
     const uint64_t n_qt = (static_cast<uint64_t>(N) + 127) / 128;
     const uint64_t units = static_cast<uint64_t>(B) * H * ((n_qt + 1) / 2);
     L.args.o = o;

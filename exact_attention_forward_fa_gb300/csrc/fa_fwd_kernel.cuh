@@ -39,6 +39,8 @@
 //   * TMEM (512 columns): S_L [0,128), S_H [128,256), O_L [256,256+D),
 //     O_H [256+D, 256+2D); P_X (64 columns of packed pairs) overlays the
 //     first half of S_X.
+//   * Interval masks (kVar 3 and 4) store O through the tile's Q slot and TMA,
+//     and hand units on as records in shared memory.
 // Every mbarrier wait is bounded (fa_device.cuh).
 #pragma once
 
@@ -145,6 +147,8 @@ struct FwdCfg {
     static constexpr uint32_t REC_OFF = (UNIT_OFF + CLC_DEPTH * 4 + 15) & ~15u;
     static constexpr uint32_t SMEM_BYTES = REC_OFF + CLC_DEPTH * 48 + 1024;   // + align slack
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+    // Interval masks at d = 128: O leaves through the tile's Q slot and TMA.
+    static constexpr bool kOStage = D == 128 && !kFP8;
 
     // TMEM columns
     static constexpr uint32_t TMEM_COLS = 512;
@@ -358,7 +362,8 @@ template <int D, bool kCausal, bool kBF16, bool kFP8 = false, bool kSplit = fals
 __global__ void __launch_bounds__(384, 1)
 fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
               const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
+              const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ CUtensorMap tm_o, const FwdArgs a) {   // tm_o: kVar >= 3
     using C = FwdCfg<D, kCausal, kBF16, kFP8>;
     constexpr bool kExt = kVar != 0;
     constexpr bool kCap = kVar == 2;
@@ -656,7 +661,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                      C::IDESC_QK, kk > 0 ? 1u : 0u);
                             }
                             mma_commit_elect(bar(C::B_SFULL + x));
-                            if (t == t1x - 1) mma_commit_elect(bar(C::B_QEMPTY + qs));
+                            // (interval masks: the slot becomes O's stage)
+                            if ((!kMask || !C::kOStage) && t == t1x - 1) mma_commit_elect(bar(C::B_QEMPTY + qs));
                         }
                         return true;
                     };
@@ -697,7 +703,15 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             ((reinterpret_cast<uintptr_t>(kSplit ? static_cast<const void *>(a.o_part) : a.o) & 31u) == 0);
         bool ok = true;
         uint32_t kq = 0;                            // dynamic order: answers read
-        uint32_t kvc = 0;                           // interval masks: K and V tiles of the units so far
+        int staged = -1;                            // interval masks: Q slot that O leaves through
+        auto unstage = [&]() __attribute__((always_inline)) {
+            if (staged >= 0 && (tid & 127) == 0) {
+                bulk_wait_read();
+                mbar_arrive(bar(C::B_QEMPTY + staged));
+            }
+            staged = -1;
+        };
+        uint32_t kvc = 0, qc = 0;                   // interval masks: K and V tiles, Q tiles of the units so far
         // (a failed wait leaves this loop by break, so ok holds here)
         auto next_dyn = [&]() __attribute__((always_inline)) -> int {
             const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
@@ -742,8 +756,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             const uint32_t kv0 = kvc;                    // K and V tiles before this unit's
             const int2 kr = kr_n, docs_at = live_n;
             const float beta = beta_n;                   // the bias a key of distance, log2 units
+            uint32_t q_slot = 0;
             if constexpr (kMask) {
                 kvc += 2u * static_cast<uint32_t>(U.T);
+                q_slot = (qc + (x == 1 && U.act[0] ? 1u : 0u)) % C::NQ;
+                qc += (U.act[0] ? 1u : 0u) + (U.act[1] ? 1u : 0u);
+                unstage();       // (before this unit's first S: its Q tiles may wait for the slot)
                 if (!act) {                              // no row of the tile sees a key
                     u = fetch();
                     const int n = mt * 128 + row;
@@ -1179,7 +1197,30 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + x));
-                if (grow < a.N) {
+                if constexpr (kMask && C::kOStage) {
+                    // into the tile's Q slot, as TMA's 128-byte swizzle has it
+                    uint8_t *orow = gbase + C::Q_OFF + q_slot * C::TILE_BYTES + row * 128;
+#pragma unroll
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            pk[i] = pack2<kBF16>(__uint_as_float(ov[8 * ch + 2 * i]) * inv,
+                                                 __uint_as_float(ov[8 * ch + 2 * i + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(orow + (ch >> 3) * C::CHUNK_BYTES + (((ch & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                    fence_proxy_async_smem();
+                    asm volatile("barrier.sync %0, 128;" :: "r"(1 + x) : "memory");
+                    if ((tid & 127) == 0) {
+#pragma unroll
+                        for (int c = 0; c < C::NCH; ++c)
+                            tma_store_4d(&tm_o, base + C::Q_OFF + q_slot * C::TILE_BYTES + c * C::CHUNK_BYTES, c * 64,
+                                         qh, mt * 128, U.b);
+                        bulk_commit();
+                    }
+                    staged = static_cast<int>(q_slot);
+                } else if (grow < a.N) {
                     if constexpr (kSplit) {
                         // split key range: FP32 partial O
                         float *prow = a.o_part +
@@ -1242,6 +1283,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     }
 
     // ---- teardown ----
+    if (kMask && warp < 8 && (tid & 127) == 0) bulk_wait_all();
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {

@@ -14,6 +14,7 @@ namespace fa {
 
 struct FwdLaunch {
     CUtensorMap q, k, v;   // 4-D maps {d, H, N, B}, box {64, 1, 128, 1}, 128-B swizzle
+    CUtensorMap o;         // interval masks: the same for O
     FwdArgs args;
     int grid;              // persistent CTAs (<= SM count)
     cudaStream_t stream;
@@ -113,7 +114,7 @@ cudaError_t launch_fwd_inst(const FwdLaunch &L) {
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&configured, bit, __ATOMIC_ACQ_REL);
     }
-    kern<<<L.grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, L.stream>>>(L.q, L.k, L.v, L.args);
+    kern<<<L.grid, Cfg::NTHREADS, Cfg::SMEM_BYTES, L.stream>>>(L.q, L.k, L.v, L.o, L.args);
     return cudaGetLastError();
 }
 
