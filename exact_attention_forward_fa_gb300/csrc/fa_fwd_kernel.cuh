@@ -1007,8 +1007,19 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             }
                         }
                         const float bnew = kBias ? row_max() : row_max() * sl2;
-                        if (r == -INFINITY) rn = bnew;
-                        else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
+                        // A bias that rises towards the tiles that follow would move the
+                        // reference every few of them: it goes ahead by what is left of
+                        // the rise, up to what P's type bears below 1 (bf16 has FP32's
+                        // exponents; fp16 is subnormal below 2^-14).
+                        float lead = 0.f;
+                        if constexpr (kBias) {
+                            constexpr float most = kBF16 ? 64.f : 4.f;
+                            const float to_go = j > mt ? static_cast<float>(j * 128 - qpos)
+                                                       : static_cast<float>(klo - j * 128);
+                            lead = fminf(fmaxf(beta * to_go, 0.f), most);
+                        }
+                        if (r == -INFINITY) rn = bnew + lead;
+                        else { rn = (bnew > r + C::TAU) ? bnew + lead : r; corr = ex2_approx(r - rn); }
                         need = (r != -INFINITY) && (rn != r);
                         const float rs = rn == -INFINITY ? 0.f : rn;
                         const float2 nr2 = make_float2(-rs, -rs);
