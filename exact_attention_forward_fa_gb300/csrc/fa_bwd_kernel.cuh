@@ -391,29 +391,24 @@ __device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, 
     fence_proxy_async_smem();
 }
 
-// Distance bias -beta |i - j| of columns c = 0, 1, ... of a tile row, in pairs:
-// linear (b0 + bs c) in a tile beside the diagonal one, with |c - d0| there.
+// Bits of the columns [lo, hi) of 32.
+__device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
+    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+    return below(hi) & ~below(lo);
+}
+
+// Distance bias -beta |i - j| of a tile row's columns c = 0, 1, ..., d0 = the row's
+// token less the first column's.  In a tile beside the diagonal one it is linear,
+// b0 + bs c.
 struct BiasCols {
-    float b0, bs, d0;
-    bool diag;
-    // add: what else every column gets (-LSE2 in the dQ kernel)
+    float b0, bs;
+    __device__ __forceinline__ BiasCols(float beta, float d0, bool before) : b0(before ? -beta * d0 : beta * d0),
+                                                                             bs(before ? beta : -beta) {}
     __device__ __forceinline__ float2 at(int c, float add) const {
-        if (diag) return make_float2(__fmaf_rn(-bs, fabsf(d0 - c), add), __fmaf_rn(-bs, fabsf(d0 - (c + 1)), add));
         return make_float2(__fmaf_rn(bs, static_cast<float>(c), b0 + add),
                            __fmaf_rn(bs, static_cast<float>(c + 1), b0 + add));
     }
 };
-// Row token `mine` (in tile tm), columns [first, ...) of tile tc; dir: +1 when the
-// rows are queries and the columns keys, -1 the other way round (the distance is
-// symmetric: which side a tile lies on is all that counts).
-__device__ __forceinline__ BiasCols bias_cols(float beta, int mine, int tm, int first, int tc) {
-    BiasCols b;
-    b.diag = tc == tm;
-    b.bs = b.diag || tc < tm ? beta : -beta;
-    b.b0 = b.bs * static_cast<float>(first - mine);
-    b.d0 = static_cast<float>(mine - first);
-    return b;
-}
 
 // Epilogue store: columns [col0, col0 + W) of one row, v * scale -> 16 bit.
 template <int D, int W, bool kBF16>
@@ -717,6 +712,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // this row's visible keys (rows past N: any range; their P is 0)
             int klo_r = 0, khi_r = a.N;
             int live_lo = 0, live_hi = a.N;
+            bool row_edge = false;                           // the query tile reaches outside the documents
             float beta = 0.f;                                // the bias a key of distance, log2 units
             if constexpr (kMask) {
                 const int2 kr = grow < a.N ? __ldg(a.plan.rows + static_cast<size_t>(U.b) * a.N + grow)
@@ -726,6 +722,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int4 lv = __ldg(a.plan.live + U.b);
                 live_lo = lv.x;
                 live_hi = lv.y;
+                row_edge = U.m * 128 < live_lo || U.m * 128 + 128 > live_hi;
                 if constexpr (kBias) beta = a.slopes[U.h] * 1.44269504088896340736f;
             } else if constexpr (kWin) {
                 const int gr = min(grow, a.N - 1);
@@ -762,8 +759,18 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     llo = klo_r - j * 128 - col0;
                 }
                 float *pf = reinterpret_cast<float *>(sv);
-                // interval masks: whether every row of the warp sees all its columns
-                const bool whole = kMask && __all_sync(0xffffffffu, lim >= 64 && llo <= 0);
+                // interval masks: the visible columns, whether every row of the warp sees
+                // them all, whether hidden ones may hold anything
+                uint32_t seen[2] = {~0u, ~0u};
+                bool whole = true, edge = false;
+                if constexpr (kMask) {
+                    whole = __all_sync(0xffffffffu, lim >= 64 && llo <= 0) && !(kBias && j == U.m);
+                    edge = row_edge || j * 128 < live_lo || j * 128 + 128 > live_hi;
+                    if (!whole) {
+                        seen[0] = column_bits(llo, lim);
+                        seen[1] = column_bits(llo - 32, lim - 32);
+                    }
+                }
                 if constexpr (kMask) {
                     // (S(t) has been formed, dQ(t) waits for dS(t): K rows may change)
                     if (j * 128 < live_lo || j * 128 + 128 > live_hi)
@@ -775,8 +782,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pf[c] = tanh_approx(pf[c] * a.sc_pre);
                 } else if constexpr (kMask) {
-                    const BiasCols bc = bias_cols(beta, grow, U.m, j * 128 + col0, j);
-                    if (whole && !(kBias && bc.diag)) {
+                    const float d0 = static_cast<float>(grow - j * 128 - col0);
+                    if (whole) {
+                        const BiasCols bc(beta, d0, j < U.m);
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
                             const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.at(c, -lse2) : nl2);
@@ -785,10 +793,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
-                            const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.at(c, -lse2) : nl2);
-                            pf[c] = c < lim && c >= llo ? ex2_approx(x.x) : 0.f;
-                            pf[c + 1] = c + 1 < lim && c + 1 >= llo ? ex2_approx(x.y) : 0.f;
+                        for (int c = 0; c < 64; ++c) {
+                            const float x = __fmaf_rn(pf[c], sl2, kBias ? __fmaf_rn(-beta, fabsf(d0 - c), -lse2) : -lse2);
+                            pf[c] = (seen[c >> 5] & (1u << (c & 31))) ? ex2_approx(x) : 0.f;
                         }
                     }
                 } else {
@@ -809,6 +816,13 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
                 tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[32]));
                 tmem_ld_wait();
+                if constexpr (kMask) {
+                    if (edge) {                  // dP of a row or key outside may be NaN
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (!(seen[c >> 5] & (1u << (c & 31)))) dp[c] = 0u;
+                    }
+                }
                 uint32_t pk[32];
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) {
@@ -823,13 +837,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         pp.x = (i < lim && (!kWin || i >= llo)) ? ex2_approx(x.x) * dt.x : 0.f;
                         pp.y = (i + 1 < lim && (!kWin || i + 1 >= llo)) ? ex2_approx(x.y) * dt.y : 0.f;
                     }
-                    float2 ds = __fmul2_rn(pp, g);
-                    if constexpr (kMask) {       // (dP and D of a row or key outside may be NaN)
-                        if (!whole) {
-                            ds.x = i < lim && i >= llo ? ds.x : 0.f;
-                            ds.y = i + 1 < lim && i + 1 >= llo ? ds.y : 0.f;
-                        }
-                    }
+                    const float2 ds = __fmul2_rn(pp, g);
                     pk[i / 2] = pack2<kBF16>(ds.x, ds.y);
                 }
                 tmem_st32(tbase + lane_off + C::DQ_COL_DS + (t & 1) * 64u + half * 32, pk);
@@ -1178,6 +1186,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // this key row's visible queries (rows past N: any range)
             int qlo_r = 0, qhi_r = a.N;
             int live_lo = 0, live_hi = a.N;
+            bool key_edge = false;                           // the key tile reaches outside the documents
             if constexpr (kMask) {
                 const int2 qr = krow < a.N ? __ldg(a.plan.cols + static_cast<size_t>(U.b) * a.N + krow)
                                            : make_int2(0, 0);
@@ -1186,6 +1195,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int4 lv = __ldg(a.plan.live + U.b);
                 live_lo = lv.x;
                 live_hi = lv.y;
+                key_edge = U.m * 128 < live_lo || U.m * 128 + 128 > live_hi;
             } else if constexpr (kWin) {
                 const int kr = min(krow, a.N - 1);
                 qlo_r = win_qlo(kr, a);
@@ -1258,13 +1268,19 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     lo = qlo_r - i * 128 - col0;
                     hi = qhi_r - i * 128 - col0;
                 }
-                constexpr bool kHi = kWin || kMask;
-                // interval masks: whether every key of the warp is seen by all its columns
-                const bool whole = kMask && __all_sync(0xffffffffu, lo <= 0 && hi >= 64);
-                BiasCols bc{};
-                if constexpr (kBias) {
-                    const float beta = __ldg(a.slopes + hq) * 1.44269504088896340736f;
-                    bc = bias_cols(beta, krow, U.m, i * 128 + col0, i);
+                // interval masks: as in the dQ kernel
+                uint32_t seen[2] = {~0u, ~0u};
+                bool whole = true, edge = false;
+                float beta = 0.f;
+                const float d0 = static_cast<float>(krow - i * 128 - col0);
+                if constexpr (kMask) {
+                    whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64) && !(kBias && i == U.m);
+                    edge = key_edge || i * 128 < live_lo || i * 128 + 128 > live_hi;
+                    if (!whole) {
+                        seen[0] = column_bits(lo, hi);
+                        seen[1] = column_bits(lo - 32, hi - 32);
+                    }
+                    if constexpr (kBias) beta = __ldg(a.slopes + hq) * 1.44269504088896340736f;
                 }
                 float *pf = reinterpret_cast<float *>(sv);
                 uint32_t pk[32];
@@ -1273,29 +1289,60 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int c = 0; c < 64; ++c) pf[c] = tanh_approx(pf[c] * a.sc_pre);
                 }
+                if constexpr (kMask) {
+                    // (two copies: the rare one does without packed arithmetic)
+                    if (whole) {
+                        const BiasCols bc(beta, d0, i < U.m);
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const float4 l4 = kCap ? __ldg(lse4 + c / 4) : lse_v[c / 4];
-                    float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2,
-                                            make_float2(-l4.x, -l4.y));
-                    float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2,
-                                            make_float2(-l4.z, -l4.w));
-                    if constexpr (kBias) {
-                        x01 = __fadd2_rn(x01, bc.at(c, 0.f));
-                        x23 = __fadd2_rn(x23, bc.at(c + 2, 0.f));
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 l4 = lse_v[c / 4];
+                            float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, make_float2(-l4.x, -l4.y));
+                            float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2, make_float2(-l4.z, -l4.w));
+                            if constexpr (kBias) {
+                                x01 = __fadd2_rn(x01, bc.at(c, 0.f));
+                                x23 = __fadd2_rn(x23, bc.at(c + 2, 0.f));
+                            }
+                            pf[c + 0] = ex2_approx(x01.x);
+                            pf[c + 1] = ex2_approx(x01.y);
+                            pf[c + 2] = ex2_approx(x23.x);
+                            pf[c + 3] = ex2_approx(x23.y);
+                            pk[c / 2] = pack2<kBF16>(pf[c], pf[c + 1]);
+                            pk[c / 2 + 1] = pack2<kBF16>(pf[c + 2], pf[c + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float4 l4 = lse_v[c / 4];
+#pragma unroll
+                            for (int e = c; e < c + 2; ++e) {
+                                const float l = (e & 3) == 0 ? l4.x : (e & 3) == 1 ? l4.y : (e & 3) == 2 ? l4.z : l4.w;
+                                const float x = __fmaf_rn(pf[e], sl2, kBias ? __fmaf_rn(-beta, fabsf(d0 - e), -l) : -l);
+                                pf[e] = (seen[e >> 5] & (1u << (e & 31))) ? ex2_approx(x) : 0.f;
+                            }
+                            pk[c / 2] = pack2<kBF16>(pf[c], pf[c + 1]);
+                        }
                     }
-                    const float p0 = (c + 0 >= lo && (!kHi || c + 0 < hi)) ? ex2_approx(x01.x) : 0.f;
-                    const float p1 = (c + 1 >= lo && (!kHi || c + 1 < hi)) ? ex2_approx(x01.y) : 0.f;
-                    const float p2 = (c + 2 >= lo && (!kHi || c + 2 < hi)) ? ex2_approx(x23.x) : 0.f;
-                    const float p3 = (c + 3 >= lo && (!kHi || c + 3 < hi)) ? ex2_approx(x23.y) : 0.f;
-                    if constexpr (!kCap) {
-                        pf[c + 0] = p0;
-                        pf[c + 1] = p1;
-                        pf[c + 2] = p2;
-                        pf[c + 3] = p3;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 l4 = kCap ? __ldg(lse4 + c / 4) : lse_v[c / 4];
+                        const float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2,
+                                                make_float2(-l4.x, -l4.y));
+                        const float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2,
+                                                make_float2(-l4.z, -l4.w));
+                        const float p0 = (c + 0 >= lo && (!kWin || c + 0 < hi)) ? ex2_approx(x01.x) : 0.f;
+                        const float p1 = (c + 1 >= lo && (!kWin || c + 1 < hi)) ? ex2_approx(x01.y) : 0.f;
+                        const float p2 = (c + 2 >= lo && (!kWin || c + 2 < hi)) ? ex2_approx(x23.x) : 0.f;
+                        const float p3 = (c + 3 >= lo && (!kWin || c + 3 < hi)) ? ex2_approx(x23.y) : 0.f;
+                        if constexpr (!kCap) {
+                            pf[c + 0] = p0;
+                            pf[c + 1] = p1;
+                            pf[c + 2] = p2;
+                            pf[c + 3] = p3;
+                        }
+                        pk[c / 2] = pack2<kBF16>(p0, p1);
+                        pk[c / 2 + 1] = pack2<kBF16>(p2, p3);
                     }
-                    pk[c / 2] = pack2<kBF16>(p0, p1);
-                    pk[c / 2 + 1] = pack2<kBF16>(p2, p3);
                 }
                 // 16-bit P^T of query columns [col0, col0+64) -> S^T columns
                 // 32 + col0/2 .. +32: columns this warp has read itself
@@ -1314,6 +1361,13 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_ld32(tDPT + col0, *reinterpret_cast<uint32_t(*)[32]>(&dp[0]));
                 tmem_ld32(tDPT + col0 + 32, *reinterpret_cast<uint32_t(*)[32]>(&dp[32]));
                 tmem_ld_wait();
+                if constexpr (kMask) {
+                    if (edge) {                  // dP of a row or key outside may be NaN
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (!(seen[c >> 5] & (1u << (c & 31)))) dp[c] = 0u;
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
                     const float4 d4 = __ldg(dd4 + c / 4);
@@ -1336,16 +1390,8 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         p23.x = (c + 2 >= lo && (!kWin || c + 2 < hi)) ? ex2_approx(x23.x) * t23.x : 0.f;
                         p23.y = (c + 3 >= lo && (!kWin || c + 3 < hi)) ? ex2_approx(x23.y) * t23.y : 0.f;
                     }
-                    float2 ds01 = __fmul2_rn(p01, g01);
-                    float2 ds23 = __fmul2_rn(p23, g23);
-                    if constexpr (kMask) {       // (dP and D of a row or key outside may be NaN)
-                        if (!whole) {
-                            ds01.x = c + 0 >= lo && c + 0 < hi ? ds01.x : 0.f;
-                            ds01.y = c + 1 >= lo && c + 1 < hi ? ds01.y : 0.f;
-                            ds23.x = c + 2 >= lo && c + 2 < hi ? ds23.x : 0.f;
-                            ds23.y = c + 3 >= lo && c + 3 < hi ? ds23.y : 0.f;
-                        }
-                    }
+                    const float2 ds01 = __fmul2_rn(p01, g01);
+                    const float2 ds23 = __fmul2_rn(p23, g23);
                     pk[c / 2] = pack2<kBF16>(ds01.x, ds01.y);
                     pk[c / 2 + 1] = pack2<kBF16>(ds23.x, ds23.y);
                 }
