@@ -134,7 +134,8 @@ struct BwdCfg {
     static constexpr uint32_t DQ_MISC_OFF = DQ_BAR_OFF + DQ_NBAR * 8;
     static constexpr uint32_t DQ_CLC_OFF = (DQ_MISC_OFF + 16 + 15) & ~15u;   // 16-byte aligned
     static constexpr uint32_t DQ_UNIT_OFF = DQ_CLC_OFF + 4 * 16;
-    static constexpr uint32_t DQ_SMEM = DQ_UNIT_OFF + 4 * 4 + 1024;
+    static constexpr uint32_t DQ_REC_OFF = (DQ_UNIT_OFF + 4 * 4 + 15) & ~15u;   // interval masks: BwdRec per answer
+    static constexpr uint32_t DQ_SMEM = DQ_REC_OFF + 4 * 32 + 1024;
     // TMEM: S [0,128), dP [128,256), dQ [256,256+D), dS0, dS1 (64 columns each)
     static constexpr uint32_t DQ_COL_S = 0, DQ_COL_DP = 128, DQ_COL_DQ = 256,
                               DQ_COL_DS = 256 + D;
@@ -156,7 +157,8 @@ struct BwdCfg {
     static constexpr uint32_t KV_MISC_OFF = KV_BAR_OFF + KV_NBAR * 8;
     static constexpr uint32_t KV_CLC_OFF = (KV_MISC_OFF + 16 + 15) & ~15u;   // 16-byte aligned
     static constexpr uint32_t KV_UNIT_OFF = KV_CLC_OFF + 4 * 16;
-    static constexpr uint32_t KV_SMEM = KV_UNIT_OFF + 4 * 4 + 1024;
+    static constexpr uint32_t KV_REC_OFF = (KV_UNIT_OFF + 4 * 4 + 15) & ~15u;   // interval masks: BwdRec per answer
+    static constexpr uint32_t KV_SMEM = KV_REC_OFF + 4 * 32 + 1024;
     // TMEM: S^T [0,128) (P^T over its first 64), dP^T [128,256) (dS^T over
     // its first 64), dV [256,256+D), dK [256+D,256+2D); at d = 64 a second
     // S^T buffer [384,512), so the S^T of query tile i+2 is computed while
@@ -209,24 +211,35 @@ __device__ __forceinline__ bool bwd_longest_first(const BwdArgs &a) {
     return kWin ? (a.wl < 0 && a.wr >= 0) : kCausal;
 }
 
-template <bool kCausal, bool kKeyTiles, bool kWin = false, bool kMask = false>
+// Interval masks: a unit as the producer reads it from the plan's lists (the dynamic
+// order over tiles sorted longest first) and hands it on through shared memory.
+struct BwdRec {
+    int4 id;       // u (-1: no more units), b, h, tile
+    int4 range;    // its tiles [x, y); z: the sequence has tokens outside documents
+};
+template <bool kKeyTiles>
+__device__ __forceinline__ BwdRec bwd_rec(int u, const BwdArgs &a) {
+    const int HH = kKeyTiles ? a.H / a.group : a.H;
+    int i, bh;
+    dynamic_order(u, a.B * HH, a.n_t, a.chunk, i, bh);
+    const int b = bh / HH;
+    const int4 *list = kKeyTiles ? a.plan.ktiles : a.plan.qtiles;
+    const int4 rec = __ldg(list + static_cast<size_t>(b) * a.n_t + (a.n_t - 1 - i)), lv = __ldg(a.plan.live + b);
+    return BwdRec{make_int4(u, b, bh - b * HH, rec.x), make_int4(rec.y, rec.z, lv.x > 0 || lv.y < a.N, 0)};
+}
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdRec &r) {
+    return BwdUnit{r.id.y, r.id.z, r.id.w, r.range.x, r.range.y};
+}
+__device__ __forceinline__ BwdRec read_bwd_rec(const uint8_t *slots, uint32_t q) {
+    const volatile int *v = reinterpret_cast<const volatile int *>(slots) + 8 * q;
+    return BwdRec{make_int4(v[0], v[1], v[2], v[3]), make_int4(v[4], v[5], v[6], v[7])};
+}
+
+template <bool kCausal, bool kKeyTiles, bool kWin = false>
 __device__ __forceinline__ BwdUnit make_bwd_unit(int u, const BwdArgs &a) {
     BwdUnit U;
     const int HH = kKeyTiles ? a.H / a.group : a.H;     // K/V heads for key tiles
     const int BH = a.B * HH;
-    if constexpr (kMask) {
-        // the dynamic order over the plan's lists, which have the longest first
-        int i, bh;
-        dynamic_order(u, BH, a.n_t, a.chunk, i, bh);
-        U.b = bh / HH;
-        U.h = bh - U.b * HH;
-        const int4 *list = kKeyTiles ? a.plan.ktiles : a.plan.qtiles;
-        const int4 rec = __ldg(list + static_cast<size_t>(U.b) * a.n_t + (a.n_t - 1 - i));
-        U.m = rec.x;
-        U.lo = rec.y;
-        U.hi = rec.z;
-        return U;
-    }
     U.lo = U.hi = 0;
     int bh;
     if (kCausal && !kWin) {
@@ -376,13 +389,17 @@ __device__ __forceinline__ void gemm_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uin
                          (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// Interval masks: a tile that reaches outside the documents [live_lo, live_hi)
-// has these rows set to 0 in shared memory, by the eight elementwise warps (row
+// Whether tile t reaches outside the documents [live.x, live.y).
+__device__ __forceinline__ bool tile_outside(int t, const int4 &live) {
+    return t * 128 < live.x || t * 128 + 128 > live.y;
+}
+
+// Interval masks: a tile that does has these rows set to 0 in shared memory, by the eight elementwise warps (row
 // `row` of the tile starting at token `first`, this thread's half of it), for
 // products that weigh them with 0 (0 x NaN is not 0).
 template <int NCH>
-__device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, int half, int live_lo, int live_hi) {
-    if (first + row < live_lo || first + row >= live_hi) {
+__device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, int half, const int4 &live) {
+    if (first + row < live.x || first + row >= live.y) {
         constexpr int PER = NCH == 2 ? 8 : 4;          // 16-byte vectors of this half
         uint8_t *at = tile + (NCH == 2 ? half * 128 * 128 : half * 64) + row * 128;
 #pragma unroll
@@ -541,9 +558,38 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive(bar(C::DQB_UNIT + q));    // release: the index is visible
                 return nu;
             };
-            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                     u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
+            // Interval masks: publishes unit u (-1: the end) and asks for the one after
+            // it, whose answer is awaited behind this unit's loads.
+            auto publish = [&](int u, BwdUnit &U) __attribute__((always_inline)) -> bool {
+                const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+                BwdRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                if (u >= 0) r = bwd_rec<false>(u, a);
+                U = bwd_unit(r);
+                ++kq;
+                if (!mbar_wait(bar(C::DQB_CLCEMPTY + q), ph ^ 1u, w, 55)) { ok = false; return false; }
+                int4 *slot_r = reinterpret_cast<int4 *>(gbase + C::DQ_REC_OFF) + 2 * q;
+                slot_r[0] = r.id;
+                slot_r[1] = r.range;
+                mbar_arrive(bar(C::DQB_UNIT + q));      // release: the record is visible
+                if (u < 0) return false;
+                mbar_arrive_expect_tx(bar(C::DQB_CLCFULL), 16u);
+                clc_try_cancel(base + C::DQ_CLC_OFF, bar(C::DQB_CLCFULL));
+                clc_pending = true;
+                return true;
+            };
+            auto answer = [&]() __attribute__((always_inline)) -> int {
+                if (!ok || !mbar_wait(bar(C::DQB_CLCFULL), (kq - 1) & 1u, w, 56)) { ok = false; return -1; }
+                clc_pending = false;
+                return clc_block(base + C::DQ_CLC_OFF);
+            };
+            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (kMask || ((!kDyn || u >= 0) && u < a.n_units));
+                     u = kMask ? answer() : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+                BwdUnit U;
+                if constexpr (kMask) {
+                    if (!publish(u, U)) break;
+                } else {
+                    U = make_bwd_unit<kCausal, false, kWin>(u, a);
+                }
                 if (kMask && U.lo >= U.hi) continue;         // sees nothing: dQ is 0
                 ok = mbar_wait(bar(C::DQB_QEMPTY), (qn & 1) ^ 1, w, 50);
                 if (!ok) break;
@@ -571,7 +617,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ++nv;
                 }
             }
-            if (kDyn && clc_pending)
+            if (kMask && clc_pending)
+                mbar_wait_quiet(bar(C::DQB_CLCFULL), (kq - 1) & 1u, 500000000ull);
+            else if (kDyn && clc_pending)
                 mbar_wait_quiet(bar(C::DQB_CLCFULL + (kq - 1) % C::CLC_DEPTH),
                                 ((kq - 1) / C::CLC_DEPTH) & 1u, 500000000ull);
             RK::drain(nk, C::DQB_KFULL, base + C::DQ_BAR_OFF);
@@ -606,9 +654,22 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (lane == 0) mbar_arrive(bar(C::DQB_CLCEMPTY + q));
             return nu;
         };
-        for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                 u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
+        auto next_rec = [&](BwdUnit &U) __attribute__((always_inline)) -> int {
+            if (!ok) return -1;
+            const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+            ++kq;
+            if (!mbar_wait_warp(bar(C::DQB_UNIT + q), ph, w, 66)) { ok = false; return -1; }
+            const BwdRec r = read_bwd_rec(gbase + C::DQ_REC_OFF, q);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::DQB_CLCEMPTY + q));
+            U = bwd_unit(r);
+            return r.id.x;
+        };
+        BwdUnit U;
+        for (int u = kMask ? next_rec(U) : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                 ok && (!kDyn || u >= 0) && u < a.n_units;
+                 u = kMask ? next_rec(U) : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+            if constexpr (!kMask) U = make_bwd_unit<kCausal, false, kWin>(u, a);
             int klo_t, khi_t;
             key_range(U, klo_t, khi_t);
             const int T = khi_t - klo_t;
@@ -693,14 +754,42 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (lane == 0) mbar_arrive(bar(C::DQB_CLCEMPTY + q));
             return nu;
         };
-        for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units;
-                 u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, false, kWin, kMask>(u, a);
+        // Interval masks: the next unit's record, and this row's keys and statistics in
+        // it, are read before the stores of the unit at hand.
+        BwdRec rec_n{};
+        int2 vis_n = make_int2(0, 0);
+        float lse2_n = 0.f, drow_n = 0.f, beta_n = 0.f;
+        auto fetch = [&]() __attribute__((always_inline)) -> int {
+            const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+            ++kq;
+            ok = mbar_wait(bar(C::DQB_UNIT + q), ph, w, 73);
+            if (__any_sync(0xffffffffu, !ok)) { ok = false; return -1; }
+            rec_n = read_bwd_rec(gbase + C::DQ_REC_OFF, q);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::DQB_CLCEMPTY + q));
+            if (rec_n.id.x < 0) return -1;
+            const int n = rec_n.id.w * 128 + row;
+            const size_t at = (static_cast<size_t>(rec_n.id.y) * a.H + rec_n.id.z) * a.NP + n;
+            vis_n = n < a.N ? __ldg(a.plan.rows + static_cast<size_t>(rec_n.id.y) * a.N + n) : make_int2(0, 0);
+            lse2_n = __ldg(a.ws_l + at);
+            drow_n = __ldg(a.ws_d + at);
+            if constexpr (kBias) beta_n = __ldg(a.slopes + rec_n.id.z) * 1.44269504088896340736f;
+            return rec_n.id.x;
+        };
+        for (int u = kMask ? fetch() : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                 ok && (!kDyn || u >= 0) && u < a.n_units;
+                 u = kMask ? u : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+            BwdUnit U;
+            const bool padded = rec_n.range.z != 0;
+            const int2 vis = vis_n;
+            if constexpr (kMask) U = bwd_unit(rec_n);
+            else U = make_bwd_unit<kCausal, false, kWin>(u, a);
             int klo_t, khi_t;
             key_range(U, klo_t, khi_t);
             const int T = khi_t - klo_t;
             const int grow = U.m * 128 + row;
             if (kMask && T <= 0) {                           // no row of the tile sees a key
+                u = fetch();
                 if (grow < a.N) {
                     uint4 *z = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dq) +
                                ((static_cast<size_t>(U.b) * a.N + grow) * a.H + U.h) * D + half * (D / 2));
@@ -711,19 +800,11 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             // this row's visible keys (rows past N: any range; their P is 0)
             int klo_r = 0, khi_r = a.N;
-            int live_lo = 0, live_hi = a.N;
-            bool row_edge = false;                           // the query tile reaches outside the documents
             float beta = 0.f;                                // the bias a key of distance, log2 units
             if constexpr (kMask) {
-                const int2 kr = grow < a.N ? __ldg(a.plan.rows + static_cast<size_t>(U.b) * a.N + grow)
-                                           : make_int2(0, 0);
-                klo_r = kr.x;
-                khi_r = kr.y;
-                const int4 lv = __ldg(a.plan.live + U.b);
-                live_lo = lv.x;
-                live_hi = lv.y;
-                row_edge = U.m * 128 < live_lo || U.m * 128 + 128 > live_hi;
-                if constexpr (kBias) beta = a.slopes[U.h] * 1.44269504088896340736f;
+                klo_r = vis.x;
+                khi_r = vis.y;
+                if constexpr (kBias) beta = beta_n;
             } else if constexpr (kWin) {
                 const int gr = min(grow, a.N - 1);
                 klo_r = win_klo(gr, a);
@@ -732,7 +813,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // log2-domain LSE of this row (+inf for rows beyond N and empty
             // rows: their P is 0) and D of this row, from the workspace
             const size_t widx = (static_cast<size_t>(U.b) * a.H + U.h) * a.NP + grow;
-            const float lse2 = a.ws_l[widx], drow = a.ws_d[widx];
+            const float lse2 = kMask ? lse2_n : a.ws_l[widx], drow = kMask ? drow_n : a.ws_d[widx];
             const float2 c2 = kCap ? make_float2(a.sc_post, a.sc_post) : make_float2(sl2, sl2);
             const float2 nl2 = make_float2(-lse2, -lse2);
             const float2 nd2 = make_float2(-drow, -drow);
@@ -765,17 +846,21 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 bool whole = true, edge = false;
                 if constexpr (kMask) {
                     whole = __all_sync(0xffffffffu, lim >= 64 && llo <= 0) && !(kBias && j == U.m);
-                    edge = row_edge || j * 128 < live_lo || j * 128 + 128 > live_hi;
                     if (!whole) {
                         seen[0] = column_bits(llo, lim);
                         seen[1] = column_bits(llo - 32, lim - 32);
                     }
                 }
                 if constexpr (kMask) {
-                    // (S(t) has been formed, dQ(t) waits for dS(t): K rows may change)
-                    if (j * 128 < live_lo || j * 128 + 128 > live_hi)
-                        zero_outside<C::NCH>(gbase + C::DQ_K_OFF + ((kt + t) % C::KN) * C::TILE, j * 128, row, half,
-                                             live_lo, live_hi);
+                    if (padded) {
+                        const int4 live = __ldg(a.plan.live + U.b);
+                        const bool outside = tile_outside(j, live);
+                        edge = outside || tile_outside(U.m, live);
+                        // (S(t) has been formed, dQ(t) waits for dS(t): K rows may change)
+                        if (outside)
+                            zero_outside<C::NCH>(gbase + C::DQ_K_OFF + ((kt + t) % C::KN) * C::TILE, j * 128, row, half,
+                                                 live);
+                    }
                 }
                 if constexpr (kCap) {
                     // keep t = tanh(alpha s / c); P comes from t in the dS step
@@ -848,6 +933,10 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             if (!ok) break;
             kt += static_cast<uint32_t>(T);
+            if constexpr (kMask) {
+                u = fetch();
+                if (!ok) break;
+            }
             // ---- epilogue: dQ * alpha -> global (this warp's half of the columns) ----
             ok = mbar_wait(bar(C::DQB_DQFULL), dqph, w, 72);
             if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
@@ -999,9 +1088,38 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mbar_arrive(bar(C::KVB_UNIT + q));    // release: the index is visible
                 return nu;
             };
-            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
-                     u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-                const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
+            // Interval masks: publishes unit u (-1: the end) and asks for the one after
+            // it, whose answer is awaited behind this unit's loads.
+            auto publish = [&](int u, BwdUnit &U) __attribute__((always_inline)) -> bool {
+                const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+                BwdRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
+                if (u >= 0) r = bwd_rec<true>(u, a);
+                U = bwd_unit(r);
+                ++kq;
+                if (!mbar_wait(bar(C::KVB_CLCEMPTY + q), ph ^ 1u, w, 55)) { ok = false; return false; }
+                int4 *slot_r = reinterpret_cast<int4 *>(gbase + C::KV_REC_OFF) + 2 * q;
+                slot_r[0] = r.id;
+                slot_r[1] = r.range;
+                mbar_arrive(bar(C::KVB_UNIT + q));      // release: the record is visible
+                if (u < 0) return false;
+                mbar_arrive_expect_tx(bar(C::KVB_CLCFULL), 16u);
+                clc_try_cancel(base + C::KV_CLC_OFF, bar(C::KVB_CLCFULL));
+                clc_pending = true;
+                return true;
+            };
+            auto answer = [&]() __attribute__((always_inline)) -> int {
+                if (!ok || !mbar_wait(bar(C::KVB_CLCFULL), (kq - 1) & 1u, w, 56)) { ok = false; return -1; }
+                clc_pending = false;
+                return clc_block(base + C::KV_CLC_OFF);
+            };
+            for (int u = blockIdx.x, st = unit_stride0(snake); ok && (kMask || ((!kDyn || u >= 0) && u < a.n_units_kv));
+                     u = kMask ? answer() : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+                BwdUnit U;
+                if constexpr (kMask) {
+                    if (!publish(u, U)) break;
+                } else {
+                    U = make_bwd_unit<kCausal, true, kWin>(u, a);
+                }
                 if (kMask && U.lo >= U.hi) continue;         // nobody sees it: dK = dV = 0
                 ok = mbar_wait(bar(C::KVB_KVEMPTY), (kvn & 1) ^ 1, w, 80);
                 if (!ok) break;
@@ -1012,9 +1130,8 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 int qlo_t, qhi_t;
                 query_range(U, qlo_t, qhi_t);
                 // the query heads of this K/V head, each over its query tiles
-                for (int k = 0; ok && k < a.group * (qhi_t - qlo_t); ++k, ++nq) {
-                    const int hq = U.h * a.group + k / (qhi_t - qlo_t);
-                    const int i = qlo_t + k % (qhi_t - qlo_t);
+                for (int k = 0, hq = U.h * a.group, i = qlo_t; ok && k < a.group * (qhi_t - qlo_t);
+                     ++k, ++nq, i = i + 1 < qhi_t ? i + 1 : qlo_t, hq += i == qlo_t ? 1 : 0) {
                     const size_t wrow = (static_cast<size_t>(U.b) * a.H + hq) * a.NP;
                     // the elementwise warps read LSE2 and D of these 128
                     // columns: 2 x 512 B, four 128-byte lines each.  Measured:
@@ -1038,7 +1155,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++n_dc;
                 }
             }
-            if (kDyn && clc_pending)
+            if (kMask && clc_pending)
+                mbar_wait_quiet(bar(C::KVB_CLCFULL), (kq - 1) & 1u, 500000000ull);
+            else if (kDyn && clc_pending)
                 mbar_wait_quiet(bar(C::KVB_CLCFULL + (kq - 1) % C::CLC_DEPTH),
                                 ((kq - 1) / C::CLC_DEPTH) & 1u, 500000000ull);
             RQ::drain(n_qc, C::KVB_QFULL, base + C::KV_BAR_OFF);
@@ -1068,9 +1187,22 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) mbar_arrive(bar(C::KVB_CLCEMPTY + q));
             return nu;
         };
-        for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
-                 u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
+        auto next_rec = [&](BwdUnit &U) __attribute__((always_inline)) -> int {
+            if (!ok) return -1;
+            const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+            ++kq;
+            if (!mbar_wait_warp(bar(C::KVB_UNIT + q), ph, w, 66)) { ok = false; return -1; }
+            const BwdRec r = read_bwd_rec(gbase + C::KV_REC_OFF, q);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::KVB_CLCEMPTY + q));
+            U = bwd_unit(r);
+            return r.id.x;
+        };
+        BwdUnit U;
+        for (int u = kMask ? next_rec(U) : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                 ok && (!kDyn || u >= 0) && u < a.n_units_kv;
+                 u = kMask ? next_rec(U) : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+            if constexpr (!kMask) U = make_bwd_unit<kCausal, true, kWin>(u, a);
             int qlo_t, qhi_t;
             query_range(U, qlo_t, qhi_t);
             const int Ti = a.group * (qhi_t - qlo_t);    // query tiles of all the group's heads
@@ -1163,14 +1295,37 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) mbar_arrive(bar(C::KVB_CLCEMPTY + q));
             return nu;
         };
-        for (int u = blockIdx.x, st = unit_stride0(snake); ok && (!kDyn || u >= 0) && u < a.n_units_kv;
-                 u = kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
-            const BwdUnit U = make_bwd_unit<kCausal, true, kWin, kMask>(u, a);
+        // Interval masks: the next unit's record, and this key's queries in it, are read
+        // before the stores of the unit at hand.
+        BwdRec rec_n{};
+        int2 vis_n = make_int2(0, 0);
+        auto fetch = [&]() __attribute__((always_inline)) -> int {
+            const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
+            ++kq;
+            ok = mbar_wait(bar(C::KVB_UNIT + q), ph, w, 103);
+            if (__any_sync(0xffffffffu, !ok)) { ok = false; return -1; }
+            rec_n = read_bwd_rec(gbase + C::KV_REC_OFF, q);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::KVB_CLCEMPTY + q));
+            if (rec_n.id.x < 0) return -1;
+            const int n = rec_n.id.w * 128 + row;
+            vis_n = n < a.N ? __ldg(a.plan.cols + static_cast<size_t>(rec_n.id.y) * a.N + n) : make_int2(0, 0);
+            return rec_n.id.x;
+        };
+        for (int u = kMask ? fetch() : static_cast<int>(blockIdx.x), st = unit_stride0(snake);
+                 ok && (!kDyn || u >= 0) && u < a.n_units_kv;
+                 u = kMask ? u : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
+            BwdUnit U;
+            const bool padded = rec_n.range.z != 0;
+            const int2 vis = vis_n;
+            if constexpr (kMask) U = bwd_unit(rec_n);
+            else U = make_bwd_unit<kCausal, true, kWin>(u, a);
             int i0, qhi_t;
             query_range(U, i0, qhi_t);
             const int Ti = qhi_t - i0;
             const int krow = U.m * 128 + row;
             if (kMask && Ti <= 0) {
+                u = fetch();
                 if (krow < a.N) {
                     const size_t at = ((static_cast<size_t>(U.b) * a.N + krow) * (a.H / a.group) + U.h) * D + half * (D / 2);
                     uint4 *zk = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dk) + at);
@@ -1185,17 +1340,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             // this key row's visible queries (rows past N: any range)
             int qlo_r = 0, qhi_r = a.N;
-            int live_lo = 0, live_hi = a.N;
-            bool key_edge = false;                           // the key tile reaches outside the documents
             if constexpr (kMask) {
-                const int2 qr = krow < a.N ? __ldg(a.plan.cols + static_cast<size_t>(U.b) * a.N + krow)
-                                           : make_int2(0, 0);
-                qlo_r = qr.x;
-                qhi_r = qr.y;
-                const int4 lv = __ldg(a.plan.live + U.b);
-                live_lo = lv.x;
-                live_hi = lv.y;
-                key_edge = U.m * 128 < live_lo || U.m * 128 + 128 > live_hi;
+                qlo_r = vis.x;
+                qhi_r = vis.y;
             } else if constexpr (kWin) {
                 const int kr = min(krow, a.N - 1);
                 qlo_r = win_qlo(kr, a);
@@ -1212,17 +1359,15 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // the host rules out keeps alive), when the load has long landed.
             // Not with a softcap: its registers are spent (the loads spilled).
             float touched = 0.f, touched_sum = 0.f;
-            for (int k = 0; k < a.group * Ti; ++k) {
-                // query head of the group, then its query tile
-                const int hq = U.h * a.group + k / Ti;
-                const int i = i0 + k % Ti;
+            // query head of the group, then its query tile
+            for (int k = 0, hq = U.h * a.group, i = i0; k < a.group * Ti;
+                 ++k, i = i + 1 < qhi_t ? i + 1 : i0, hq += i == i0 ? 1 : 0) {
                 const size_t wrow = (static_cast<size_t>(U.b) * a.H + hq) * a.NP;
                 const float4 *lse4 = reinterpret_cast<const float4 *>(a.ws_l + wrow + i * 128 + col0);
                 const float4 *dd4 = reinterpret_cast<const float4 *>(a.ws_d + wrow + i * 128 + col0);
                 touched_sum += touched;
                 if (!kCap && k + 1 < a.group * Ti && lane < 16) {
-                    const int hq1 = U.h * a.group + (k + 1) / Ti;
-                    const int i1 = i0 + (k + 1) % Ti;
+                    const int i1 = i + 1 < qhi_t ? i + 1 : i0, hq1 = i1 == i0 ? hq + 1 : hq;
                     const size_t w1 = (static_cast<size_t>(U.b) * a.H + hq1) * a.NP + i1 * 128 + col0 +
                                       (lane & 7) * 8;
                     touched = __ldg((lane < 8 ? a.ws_l : a.ws_d) + w1);
@@ -1244,17 +1389,21 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 uint32_t sv[64];
                 const uint32_t tST = tbase + lane_off + C::st_col(stn);
                 const int pbar = C::p_bar(stn);
+                bool edge = false;               // interval masks: hidden columns may hold anything
                 if constexpr (kMask) {
                     // a query tile that reaches outside the documents: its Q (S^T has been
                     // formed) and dO rows there become 0; dP^T, which may read them
                     // meanwhile, is masked in those columns
-                    if (i * 128 < live_lo || i * 128 + 128 > live_hi) {
-                        ok = mbar_wait(bar(C::KVB_DOFULL + RO::slot(stn)), RO::phase(stn), w, 104);
-                        if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
-                        zero_outside<C::NCH>(gbase + C::KV_Q_OFF + RQ::slot(stn) * C::TILE, i * 128, row, half, live_lo,
-                                             live_hi);
-                        zero_outside<C::NCH>(gbase + C::KV_DO_OFF + RO::slot(stn) * C::TILE, i * 128, row, half, live_lo,
-                                             live_hi);
+                    if (padded) {
+                        const int4 live = __ldg(a.plan.live + U.b);
+                        const bool outside = tile_outside(i, live);
+                        edge = outside || tile_outside(U.m, live);
+                        if (outside) {
+                            ok = mbar_wait(bar(C::KVB_DOFULL + RO::slot(stn)), RO::phase(stn), w, 104);
+                            if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+                            zero_outside<C::NCH>(gbase + C::KV_Q_OFF + RQ::slot(stn) * C::TILE, i * 128, row, half, live);
+                            zero_outside<C::NCH>(gbase + C::KV_DO_OFF + RO::slot(stn) * C::TILE, i * 128, row, half, live);
+                        }
                     }
                 }
                 ++stn;
@@ -1270,12 +1419,11 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 // interval masks: as in the dQ kernel
                 uint32_t seen[2] = {~0u, ~0u};
-                bool whole = true, edge = false;
+                bool whole = true;
                 float beta = 0.f;
                 const float d0 = static_cast<float>(krow - i * 128 - col0);
                 if constexpr (kMask) {
                     whole = __all_sync(0xffffffffu, lo <= 0 && hi >= 64) && !(kBias && i == U.m);
-                    edge = key_edge || i * 128 < live_lo || i * 128 + 128 > live_hi;
                     if (!whole) {
                         seen[0] = column_bits(lo, hi);
                         seen[1] = column_bits(lo - 32, hi - 32);
@@ -1402,6 +1550,10 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lane == 0) mbar_arrive(bar(C::KVB_DSFULL));
             }
             if (!ok) break;
+            if constexpr (kMask) {
+                u = fetch();
+                if (!ok) break;
+            }
             // ---- epilogue: dV, dK * alpha -> global (this warp's half of the columns) ----
             ok = mbar_wait(bar(C::KVB_ACCFULL), accph, w, 102);
             if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
