@@ -418,12 +418,19 @@ __device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
 // token less the first column's.  In a tile beside the diagonal one it is linear,
 // b0 + bs c.
 struct BiasCols {
-    float b0, bs;
-    __device__ __forceinline__ BiasCols(float beta, float d0, bool before) : b0(before ? -beta * d0 : beta * d0),
-                                                                             bs(before ? beta : -beta) {}
-    __device__ __forceinline__ float2 at(int c, float add) const {
-        return make_float2(__fmaf_rn(bs, static_cast<float>(c), b0 + add),
-                           __fmaf_rn(bs, static_cast<float>(c + 1), b0 + add));
+    float2 even, odd, step;     // columns (c, c + 1) and (c + 2, c + 3), four further on
+    __device__ __forceinline__ BiasCols(float beta, float d0, bool before, float add) {
+        const float bs = before ? beta : -beta, b0 = add - bs * d0;
+        even = make_float2(b0, b0 + bs);
+        odd = make_float2(__fmaf_rn(2.f, bs, b0), __fmaf_rn(3.f, bs, b0));
+        step = make_float2(4.f * bs, 4.f * bs);
+    }
+    // in the order of the columns
+    __device__ __forceinline__ float2 next(int c) {
+        float2 &b = c & 2 ? odd : even;
+        const float2 v = b;
+        b = __fadd2_rn(b, step);
+        return v;
     }
 };
 
@@ -869,10 +876,10 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 } else if constexpr (kMask) {
                     const float d0 = static_cast<float>(grow - j * 128 - col0);
                     if (whole) {
-                        const BiasCols bc(beta, d0, j < U.m);
+                        BiasCols bc(beta, d0, j < U.m, -lse2);
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
-                            const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.at(c, -lse2) : nl2);
+                            const float2 x = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, kBias ? bc.next(c) : nl2);
                             pf[c] = ex2_approx(x.x);
                             pf[c + 1] = ex2_approx(x.y);
                         }
@@ -1440,16 +1447,17 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if constexpr (kMask) {
                     // (two copies: the rare one does without packed arithmetic)
                     if (whole) {
-                        const BiasCols bc(beta, d0, i < U.m);
+                        BiasCols bc(beta, d0, i < U.m, 0.f);
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const float4 l4 = lse_v[c / 4];
-                            float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, make_float2(-l4.x, -l4.y));
-                            float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2, make_float2(-l4.z, -l4.w));
+                            float2 n01 = make_float2(-l4.x, -l4.y), n23 = make_float2(-l4.z, -l4.w);
                             if constexpr (kBias) {
-                                x01 = __fadd2_rn(x01, bc.at(c, 0.f));
-                                x23 = __fadd2_rn(x23, bc.at(c + 2, 0.f));
+                                n01 = __fadd2_rn(n01, bc.next(c));
+                                n23 = __fadd2_rn(n23, bc.next(c + 2));
                             }
+                            const float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, n01);
+                            const float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2, n23);
                             pf[c + 0] = ex2_approx(x01.x);
                             pf[c + 1] = ex2_approx(x01.y);
                             pf[c + 2] = ex2_approx(x23.x);
