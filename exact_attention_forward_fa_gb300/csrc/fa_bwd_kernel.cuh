@@ -565,8 +565,8 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive(bar(C::DQB_UNIT + q));    // release: the index is visible
                 return nu;
             };
-            // Interval masks: publishes unit u (-1: the end) and asks for the one after
-            // it, whose answer is awaited behind this unit's loads.
+            // Interval masks: publishes unit u (-1: the end); the next one is asked for
+            // ahead of this one's last tiles (fa_fwd_kernel.cuh).
             auto publish = [&](int u, BwdUnit &U) __attribute__((always_inline)) -> bool {
                 const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
                 BwdRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
@@ -578,11 +578,12 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 slot_r[0] = r.id;
                 slot_r[1] = r.range;
                 mbar_arrive(bar(C::DQB_UNIT + q));      // release: the record is visible
-                if (u < 0) return false;
+                return u >= 0;
+            };
+            auto ask = [&]() __attribute__((always_inline)) {
                 mbar_arrive_expect_tx(bar(C::DQB_CLCFULL), 16u);
                 clc_try_cancel(base + C::DQ_CLC_OFF, bar(C::DQB_CLCFULL));
                 clc_pending = true;
-                return true;
             };
             auto answer = [&]() __attribute__((always_inline)) -> int {
                 if (!ok || !mbar_wait(bar(C::DQB_CLCFULL), (kq - 1) & 1u, w, 56)) { ok = false; return -1; }
@@ -594,6 +595,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 BwdUnit U;
                 if constexpr (kMask) {
                     if (!publish(u, U)) break;
+                    if (U.lo >= U.hi) ask();
                 } else {
                     U = make_bwd_unit<kCausal, false, kWin>(u, a);
                 }
@@ -609,6 +611,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const int T = khi_t - klo_t;
                 for (int t = 0; ok && t < T; ++t) {
                     const int j = khi_t - 1 - t;
+                    if (kMask && t == max(0, T - 2)) ask();
                     const uint32_t ks = RK::slot(nk), vs = RV::slot(nv);
                     ok = mbar_wait(bar(C::DQB_KEMPTY + ks), RK::phase(nk) ^ 1, w, 51);
                     if (!ok) break;
@@ -1095,8 +1098,8 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mbar_arrive(bar(C::KVB_UNIT + q));    // release: the index is visible
                 return nu;
             };
-            // Interval masks: publishes unit u (-1: the end) and asks for the one after
-            // it, whose answer is awaited behind this unit's loads.
+            // Interval masks: publishes unit u (-1: the end); the next one is asked for
+            // ahead of this one's last tiles (fa_fwd_kernel.cuh).
             auto publish = [&](int u, BwdUnit &U) __attribute__((always_inline)) -> bool {
                 const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
                 BwdRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
@@ -1108,11 +1111,12 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 slot_r[0] = r.id;
                 slot_r[1] = r.range;
                 mbar_arrive(bar(C::KVB_UNIT + q));      // release: the record is visible
-                if (u < 0) return false;
+                return u >= 0;
+            };
+            auto ask = [&]() __attribute__((always_inline)) {
                 mbar_arrive_expect_tx(bar(C::KVB_CLCFULL), 16u);
                 clc_try_cancel(base + C::KV_CLC_OFF, bar(C::KVB_CLCFULL));
                 clc_pending = true;
-                return true;
             };
             auto answer = [&]() __attribute__((always_inline)) -> int {
                 if (!ok || !mbar_wait(bar(C::KVB_CLCFULL), (kq - 1) & 1u, w, 56)) { ok = false; return -1; }
@@ -1124,6 +1128,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 BwdUnit U;
                 if constexpr (kMask) {
                     if (!publish(u, U)) break;
+                    if (U.lo >= U.hi) ask();
                 } else {
                     U = make_bwd_unit<kCausal, true, kWin>(u, a);
                 }
@@ -1139,6 +1144,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // the query heads of this K/V head, each over its query tiles
                 for (int k = 0, hq = U.h * a.group, i = qlo_t; ok && k < a.group * (qhi_t - qlo_t);
                      ++k, ++nq, i = i + 1 < qhi_t ? i + 1 : qlo_t, hq += i == qlo_t ? 1 : 0) {
+                    if (kMask && k == max(0, a.group * (qhi_t - qlo_t) - 2)) ask();
                     const size_t wrow = (static_cast<size_t>(U.b) * a.H + hq) * a.NP;
                     // the elementwise warps read LSE2 and D of these 128
                     // columns: 2 x 512 B, four 128-byte lines each.  Measured:

@@ -492,9 +492,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 mbar_arrive(bar(C::B_UNIT + q));        // release: the index is visible
                 return nu;
             };
-            // Interval masks: publishes unit u (-1: the end) and asks for the one after
-            // it, whose answer is awaited behind this unit's loads (asked behind
-            // them it came 3000 cycles late).
+            // Interval masks: publishes unit u (-1: the end).  The next one is asked for
+            // ahead of this one's last tiles and the answer awaited behind them: asked
+            // behind them it came 3000 cycles late, asked at the unit's beginning
+            // it left the long units' CTAs with more than their share.
             auto publish = [&](int u, Unit &U) __attribute__((always_inline)) -> bool {
                 const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
                 MaskRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
@@ -507,11 +508,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 slot_r[1] = r.tiles;
                 slot_r[2] = r.live;
                 mbar_arrive(bar(C::B_UNIT + q));        // release: the record is visible
-                if (u < 0) return false;
+                return u >= 0;
+            };
+            auto ask = [&]() __attribute__((always_inline)) {
                 mbar_arrive_expect_tx(bar(C::B_CLCFULL), 16u);
                 clc_try_cancel(base + C::CLC_OFF, bar(C::B_CLCFULL));
                 clc_pending = true;
-                return true;
             };
             auto answer = [&]() __attribute__((always_inline)) -> int {
                 if (!ok || !mbar_wait(bar(C::B_CLCFULL), (kq - 1) & 1u, w, 4)) { ok = false; return -1; }
@@ -523,6 +525,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 Unit U;
                 if constexpr (kMask) {
                     if (!publish(u, U)) break;
+                    if (U.T == 0) ask();
                 } else {
                     U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 }
@@ -531,6 +534,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 const int hk = kPack ? U.h : U.h / a.group;   // K/V head of this query head
                 for (int t = 0; t < U.T && ok; ++t) {
                     const int j = U.jhi - 1 - t;
+                    if (kMask && t == max(0, U.T - 2)) ask();
                     for (int kv = 0; kv < 2; ++kv) {
                         ok = mbar_wait(bar(C::B_KVEMPTY + slot), phase ^ 1, w, 2);
                         if (!ok) break;
