@@ -66,36 +66,39 @@ __device__ __forceinline__ void turn8(uint4 &a, uint4 &b, bool interleaved, cons
     }
 }
 
-constexpr int kPasses = 4;      // heads in flight per lane: 8 loads of 16 bytes
+constexpr int kPasses = 2;      // heads in flight per lane: 4 loads of 16 bytes
+constexpr int kBlocks = 4;      // blocks of 8 warps an SM
 
 }  // namespace
 
-// Item (token t, part): passes [part * per, part * per + per) of the token's
-// heads, 32 / G heads a pass (G lanes a head).  A warp keeps its part.
+// All tokens' passes, 32 / G heads each (G lanes a head), in a row, cut into equal
+// runs for the warps: a run begins and ends within a token.
 template <bool kBF16, bool kPaged>
-__global__ void __launch_bounds__(256, 2)
-fa_rope_kernel(const RopeArgs a, const int G, const int parts, const int per) {
+__global__ void __launch_bounds__(256, kBlocks)
+fa_rope_kernel(const RopeArgs a, const int G, const int passes, const int warps) {
     if (kPaged && blockIdx.x == gridDim.x - 1)              // the last block only checks
         return paged_check_seqs(a.cu_q, a.kv_len, a.B, a.T, a.W, a.ps_log2, a.status);
+    const int warp = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+    if (warp >= warps) return;
     const int lane = threadIdx.x & 31;
     const int c = lane % G, sub = lane / G, hpp = 32 / G;   // task, head of a pass, heads a pass
-    const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const long long warps = (static_cast<long long>(gridDim.x - (kPaged ? 1 : 0)) * blockDim.x) >> 5;
-    const int part = static_cast<int>(warp % parts);
-    const long long step = warps / parts;                   // (the grid is a multiple of parts)
     const bool turns = c * 16 < a.rot;
     // the task's two vectors within a head
-    const int half = a.rot / 16;
-    const int v0 = !turns || a.interleaved ? 2 * c : c, v1 = !turns || a.interleaved ? 2 * c + 1 : c + half;
+    const int v0 = !turns || a.interleaved ? 2 * c : c, v1 = !turns || a.interleaved ? 2 * c + 1 : c + a.rot / 16;
     unsigned long long u[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = turns ? turns_of(a.inv_freq[8 * c + i]) : 0ull;
     const int heads = a.H + a.H_kv * (kPaged ? 2 : 1);
-    const int h_end = min(heads, (part + 1) * per * hpp);
     const uint4 *qs = reinterpret_cast<const uint4 *>(a.q), *ks = reinterpret_cast<const uint4 *>(a.k),
                 *vs = reinterpret_cast<const uint4 *>(a.v);
-    for (long long t = warp / parts; t < a.T; t += step) {
-        const int h0 = part * per * hpp + sub;
+    const long long total = static_cast<long long>(a.T) * passes;
+    const long long p0 = total * warp / warps;
+    int left = static_cast<int>(total * (warp + 1) / warps - p0);
+    int t = static_cast<int>(p0 / passes), pass = static_cast<int>(p0 - static_cast<long long>(t) * passes);
+    for (; left > 0; ++t, pass = 0) {
+        const int n = min(passes - pass, left);
+        left -= n;
+        const int h_end = min(heads, (pass + n) * hpp);
         const uint4 *qt = qs + t * a.q_stride, *kt = ks + t * a.k_stride, *vt = vs + t * a.v_stride;
         uint4 x0[kPasses], x1[kPasses];
         auto load = [&](int h) __attribute__((always_inline)) {
@@ -103,25 +106,24 @@ fa_rope_kernel(const RopeArgs a, const int G, const int parts, const int per) {
             for (int i = 0; i < kPasses; ++i) {
                 const int hh = h + i * hpp;
                 if (hh < h_end) {
-                    const uint4 *src = hh < a.H ? qt + hh * a.V
-                                       : hh < a.H + a.H_kv ? kt + (hh - a.H) * a.V
-                                                           : vt + (hh - a.H - a.H_kv) * a.V;
                     // (values keep their order: the whole head is copied, two vectors a lane)
                     const bool is_v = kPaged && hh >= a.H + a.H_kv;
+                    const uint4 *src = hh < a.H ? qt + hh * a.V : is_v ? vt + (hh - a.H - a.H_kv) * a.V : kt + (hh - a.H) * a.V;
                     x0[i] = src[is_v ? 2 * c : v0];
                     x1[i] = src[is_v ? 2 * c + 1 : v1];
                 }
             }
         };
-        load(h0);
+        int h = pass * hpp + sub;
+        load(h);
         long long pos;
         uint4 *kd = nullptr, *vd = nullptr;                  // paged: the token's slot
         if constexpr (kPaged) {
-            const int b = paged_find_seq(a.cu_q, a.B, static_cast<int>(t));
+            const int b = paged_find_seq(a.cu_q, a.B, t);
             if (b < 0) continue;                             // behind the last sequence
-            const long long n = a.kv_len[b], p = n - a.cu_q[b + 1] + t;
+            const long long len = a.kv_len[b], p = len - a.cu_q[b + 1] + t;
             pos = p + (a.offsets ? a.offsets[b] : 0);
-            if (p >= 0 && p < min(n, static_cast<long long>(a.W) << a.ps_log2)) {
+            if (p >= 0 && p < min(len, static_cast<long long>(a.W) << a.ps_log2)) {
                 const int page = paged_page(a.table + static_cast<long long>(b) * a.W, static_cast<int>(p), a.ps_log2,
                                             a.n_pages, a.status);
                 if (page >= 0) {
@@ -132,7 +134,7 @@ fa_rope_kernel(const RopeArgs a, const int G, const int parts, const int per) {
                 }
             }
         } else {
-            pos = a.positions ? a.positions[t] : static_cast<int>(t) % a.N;
+            pos = a.positions ? a.positions[t] : t % a.N;
             kd = reinterpret_cast<uint4 *>(a.k_out) + t * a.ko_stride;
         }
         uint4 *qd = reinterpret_cast<uint4 *>(a.q_out) + t * a.qo_stride;
@@ -145,7 +147,7 @@ fa_rope_kernel(const RopeArgs a, const int G, const int parts, const int per) {
             cs[i] = co * a.scale;
             sn[i] = a.inverse ? -s * a.scale : s * a.scale;
         }
-        for (int h = h0;;) {
+        for (;;) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int hh = h + i * hpp;
@@ -171,26 +173,14 @@ cudaError_t launch_rope(const RopeArgs &a, bool bf16, bool paged, int sm_count, 
     const int G = a.V / 2, hpp = 32 / G;
     const int heads = a.H + a.H_kv * (paged ? 2 : 1);
     const int passes = (heads + hpp - 1) / hpp;
-    // Passes a warp: all of a token's when there are tokens for 16 warps on every
-    // SM, else as few as spread the call over that many.
-    const long long want = 16ll * sm_count;
-    long long per = static_cast<long long>(a.T) * passes / want;
-    per = per < 1 ? 1 : per > passes ? passes : per;
-    const int parts = static_cast<int>((passes + per - 1) / per);
-    // blocks of 8 warps, two an SM (what the registers allow); their warps a multiple of parts
-    long long warps = static_cast<long long>(a.T) * parts;
-    const long long cap = 16ll * sm_count;
-    if (warps > cap) warps = cap > parts ? cap : parts;
-    long long blocks = (warps + 7) / 8;
-    blocks = (blocks + parts - 1) / parts * parts;
-    const unsigned grid = static_cast<unsigned>(blocks + (paged ? 1 : 0));
-    if (paged) {
-        if (bf16) fa_rope_kernel<true, true><<<grid, 256, 0, stream>>>(a, G, parts, static_cast<int>(per));
-        else fa_rope_kernel<false, true><<<grid, 256, 0, stream>>>(a, G, parts, static_cast<int>(per));
-    } else {
-        if (bf16) fa_rope_kernel<true, false><<<grid, 256, 0, stream>>>(a, G, parts, static_cast<int>(per));
-        else fa_rope_kernel<false, false><<<grid, 256, 0, stream>>>(a, G, parts, static_cast<int>(per));
-    }
+    // as many warps as the SMs hold, a pass each at least (single tokens: spread
+    // over all SMs)
+    const long long total = static_cast<long long>(a.T) * passes, most = 8ll * kBlocks * sm_count;
+    const int warps = static_cast<int>(total < most ? total : most);
+    const unsigned grid = static_cast<unsigned>((warps + 7) / 8 + (paged ? 1 : 0));
+    auto kern = paged ? (bf16 ? fa_rope_kernel<true, true> : fa_rope_kernel<false, true>)
+                      : (bf16 ? fa_rope_kernel<true, false> : fa_rope_kernel<false, false>);
+    kern<<<grid, 256, 0, stream>>>(a, G, passes, warps);
     return cudaGetLastError();
 }
 
