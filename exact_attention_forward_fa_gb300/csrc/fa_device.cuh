@@ -456,6 +456,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The largest of a row's N scores (N a multiple of 8), in four chains.
+template <int N>
+__device__ __forceinline__ float row_max_of(const float *s) {
+    static_assert(N % 8 == 0, "four chains of two a step, and four more");
+    float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+    for (int c = 4; c < N - 4; c += 8) {
+        m0 = max3(m0, s[c + 0], s[c + 4]);
+        m1 = max3(m1, s[c + 1], s[c + 5]);
+        m2 = max3(m2, s[c + 2], s[c + 6]);
+        m3 = max3(m3, s[c + 3], s[c + 7]);
+    }
+    m0 = fmaxf(m0, s[N - 4]);
+    m1 = fmaxf(m1, s[N - 3]);
+    m2 = fmaxf(m2, s[N - 2]);
+    m3 = fmaxf(m3, s[N - 1]);
+    return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+}
+
 // Two FP32 values -> packed pair of 16-bit floats (low half = a), RN.
 template <bool kBF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

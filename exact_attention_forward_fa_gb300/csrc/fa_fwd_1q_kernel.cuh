@@ -413,15 +413,7 @@ fa_fwd_1q_kernel(const __grid_constant__ CUtensorMap tm_q,
 #pragma unroll
                     for (int c = 0; c < BN; ++c) if (c >= lim) sf[c] = -INFINITY;
                 }
-                float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
-#pragma unroll
-                for (int c = 4; c < BN; c += 8) {
-                    m0 = max3(m0, sf[c + 0], sf[c + 4]);
-                    m1 = max3(m1, sf[c + 1], sf[c + 5]);
-                    m2 = max3(m2, sf[c + 2], sf[c + 6]);
-                    m3 = max3(m3, sf[c + 3], sf[c + 7]);
-                }
-                const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                const float mx = row_max_of<BN>(sf);
                 const float bnew = mx * sl2;
                 float rn, corr;
                 if (r == -INFINITY) { rn = bnew; corr = 1.f; }

@@ -460,15 +460,7 @@ fa_fwd_fp8_1q_kernel(const __grid_constant__ CUtensorMap tm_q,
                     for (int c = 0; c < 128; ++c) if (c >= lim) sf[c] = -INFINITY;
                 }
                 // ---- the row max first: e4m3 saturates above 448 ----
-                float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
-#pragma unroll
-                for (int c = 4; c < 128; c += 8) {
-                    m0 = max3(m0, sf[c + 0], sf[c + 4]);
-                    m1 = max3(m1, sf[c + 1], sf[c + 5]);
-                    m2 = max3(m2, sf[c + 2], sf[c + 6]);
-                    m3 = max3(m3, sf[c + 3], sf[c + 7]);
-                }
-                const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sc;   // -inf stays -inf
+                const float bnew = row_max_of<128>(sf) * sc;   // -inf stays -inf
                 float rn = r, corr = 1.f;
                 if (r == -INFINITY) rn = bnew;
                 else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }

@@ -914,15 +914,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 };
                 if constexpr (!kMask) load_s();
                 auto row_max = [&]() __attribute__((always_inline)) -> float {
-                    float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
-#pragma unroll
-                    for (int c = 4; c < 128; c += 8) {
-                        m0 = max3(m0, sf[c + 0], sf[c + 4]);
-                        m1 = max3(m1, sf[c + 1], sf[c + 5]);
-                        m2 = max3(m2, sf[c + 2], sf[c + 6]);
-                        m3 = max3(m3, sf[c + 3], sf[c + 7]);
-                    }
-                    return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                    return row_max_of<128>(sf);
                 };
                 // r: reference of this tile's P; corr = 2^(r_old - r) rescales O
                 // and the row sums when r moves.

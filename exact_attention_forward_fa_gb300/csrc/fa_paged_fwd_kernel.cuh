@@ -391,15 +391,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         }
                     }
                     if (!keep) {
-                        float m0 = sf[0], m1 = sf[1], m2 = sf[2], m3 = sf[3];
-#pragma unroll
-                        for (int cc = 4; cc < 128; cc += 8) {
-                            m0 = max3(m0, sf[cc + 0], sf[cc + 4]);
-                            m1 = max3(m1, sf[cc + 1], sf[cc + 5]);
-                            m2 = max3(m2, sf[cc + 2], sf[cc + 6]);
-                            m3 = max3(m3, sf[cc + 3], sf[cc + 7]);
-                        }
-                        const float bnew = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * (kBias ? 1.f : sl2);
+                        const float bnew = row_max_of<128>(sf) * (kBias ? 1.f : sl2);
                         if (valid) {
                             if (r == -INFINITY) rn = bnew;
                             else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
