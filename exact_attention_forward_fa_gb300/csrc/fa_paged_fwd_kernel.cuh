@@ -342,12 +342,104 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 // P against the current reference first; the maximum only on the
                 // first tile or when a row's sum got too large (fa_fwd_kernel.cuh)
                 bool keep = __all_sync(0xffffffffu, r != -INFINITY);
-                // Distance bias: linear in the column, b0 + bs c, where all keys that a row
-                // sees here lie on one side of it; else with |k0 + c - pos|.
-                const bool left = khi <= pos + 1 || k0 + 127 <= pos;
-                const bool mixed = kBias && __any_sync(0xffffffffu, valid && !left && k0 < pos);
-                const float bs = left ? beta : -beta;
-                const float b0 = kBias ? bs * static_cast<float>(k0 - pos) : 0.f;
+                if constexpr (kBias) {
+                    // Distance bias: linear in the column, b0 + bs c, where all keys that a
+                    // row sees here lie on one side of it; else with |k0 + c - pos|.
+                    const bool left = khi <= pos + 1 || k0 + 127 <= pos;
+                    const bool mixed = __any_sync(0xffffffffu, valid && !left && k0 < pos);
+                    const float bs = left ? beta : -beta;
+                    const float b0 = bs * static_cast<float>(k0 - pos);
+                    const float2 step = make_float2(8.f * bs, 8.f * bs);
+                    float2 bc[4];
+                    // against the current reference where all rows see the whole tile
+                    bool done = keep && !masked && !mixed;
+                    if (done) {
+                        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                        tmem_ld_wait();
+                        e_a = make_float2(0.f, 0.f);
+                        e_b = e_a;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0 - r), __fmaf_rn(bs, 2.f * q + 1.f, b0 - r));
+#pragma unroll
+                        for (int cc = 0; cc < 128; cc += 4) {
+                            float2 &b01 = bc[(cc >> 1) & 3], &b23 = bc[((cc >> 1) + 1) & 3];
+                            const float2 x01 = __ffma2_rn(make_float2(sf[cc + 0], sf[cc + 1]), c2, b01);
+                            const float2 x23 = __ffma2_rn(make_float2(sf[cc + 2], sf[cc + 3]), c2, b23);
+                            b01 = __fadd2_rn(b01, step);
+                            b23 = __fadd2_rn(b23, step);
+                            const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                            const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                            pk[cc / 2] = pack2<kBF16>(e01.x, e01.y);
+                            pk[cc / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                            e_a = __fadd2_rn(e_a, e01);
+                            e_b = __fadd2_rn(e_b, e23);
+                        }
+                        const float ts = (e_a.x + e_a.y) + (e_b.x + e_b.y);
+                        done = __all_sync(0xffffffffu, !valid || ts <= C::KEEP_SUM);
+                    }
+                    if (!done) {
+                        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                        tmem_ld_wait();
+                        if (masked) {
+#pragma unroll
+                            for (int w32 = 0; w32 < 4; ++w32) {
+                                // bit c of m: column 32 w32 + c is visible
+                                auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                                const uint32_t m = below(lim - 32 * w32) & (~below(llo - 32 * w32) | below(lf - 32 * w32));
+#pragma unroll
+                                for (int cc = 0; cc < 32; ++cc)
+                                    if (!(m & (1u << cc))) sf[32 * w32 + cc] = -INFINITY;
+                            }
+                        }
+                        // biased scores in log2 units, their maximum
+                        if (mixed) {
+                            const float d0 = static_cast<float>(pos - k0);
+#pragma unroll
+                            for (int cc = 0; cc < 128; ++cc)
+                                sf[cc] = __fmaf_rn(sf[cc], sl2, -beta * fabsf(d0 - static_cast<float>(cc)));
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0), __fmaf_rn(bs, 2.f * q + 1.f, b0));
+#pragma unroll
+                            for (int cc = 0; cc < 128; cc += 2) {
+                                float2 &bq = bc[(cc >> 1) & 3];
+                                const float2 v = __ffma2_rn(make_float2(sf[cc], sf[cc + 1]), c2, bq);
+                                sf[cc] = v.x;
+                                sf[cc + 1] = v.y;
+                                bq = __fadd2_rn(bq, step);
+                            }
+                        }
+                        const float bnew = row_max_of<128>(sf);
+                        if (valid) {
+                            if (r == -INFINITY) rn = bnew;
+                            else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
+                            need = (r != -INFINITY) && (rn != r);
+                        }
+                        const float rs = rn == -INFINITY ? 0.f : rn;
+                        const float2 nr2 = make_float2(-rs, -rs);
+                        e_a = make_float2(0.f, 0.f);
+                        e_b = e_a;
+#pragma unroll
+                        for (int cc = 0; cc < 128; cc += 4) {
+                            const float2 x01 = __fadd2_rn(make_float2(sf[cc + 0], sf[cc + 1]), nr2);
+                            const float2 x23 = __fadd2_rn(make_float2(sf[cc + 2], sf[cc + 3]), nr2);
+                            const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
+                            const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
+                            pk[cc / 2] = pack2<kBF16>(e01.x, e01.y);
+                            pk[cc / 2 + 1] = pack2<kBF16>(e23.x, e23.y);
+                            e_a = __fadd2_rn(e_a, e01);
+                            e_b = __fadd2_rn(e_b, e23);
+                        }
+                    }
+                } else
 #pragma unroll 1
                 for (;;) {
                     tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
@@ -366,32 +458,8 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 if (!(m & (1u << cc))) sf[32 * w32 + cc] = -INFINITY;
                         }
                     }
-                    // biased scores in log2 units, less the reference when it is kept
-                    if constexpr (kBias) {
-                        const float rk = keep ? r : 0.f;
-                        if (mixed) {
-                            const float d0 = static_cast<float>(pos - k0);
-#pragma unroll
-                            for (int cc = 0; cc < 128; ++cc)
-                                sf[cc] = __fmaf_rn(sf[cc], sl2, __fmaf_rn(-beta, fabsf(d0 - static_cast<float>(cc)), -rk));
-                        } else {
-                            const float2 step = make_float2(8.f * bs, 8.f * bs);
-                            float2 bc[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0 - rk), __fmaf_rn(bs, 2.f * q + 1.f, b0 - rk));
-#pragma unroll
-                            for (int cc = 0; cc < 128; cc += 2) {
-                                float2 &bq = bc[(cc >> 1) & 3];
-                                const float2 x = __ffma2_rn(make_float2(sf[cc], sf[cc + 1]), c2, bq);
-                                sf[cc] = x.x;
-                                sf[cc + 1] = x.y;
-                                bq = __fadd2_rn(bq, step);
-                            }
-                        }
-                    }
                     if (!keep) {
-                        const float bnew = row_max_of<128>(sf) * (kBias ? 1.f : sl2);
+                        const float bnew = row_max_of<128>(sf) * sl2;
                         if (valid) {
                             if (r == -INFINITY) rn = bnew;
                             else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
@@ -402,21 +470,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const float2 nr2 = make_float2(-rs, -rs);
                     e_a = make_float2(0.f, 0.f);
                     e_b = e_a;
-                    if constexpr (kBias) {
-                        if (!keep) {
-#pragma unroll
-                            for (int cc = 0; cc < 128; cc += 2) {
-                                const float2 x = __fadd2_rn(make_float2(sf[cc], sf[cc + 1]), nr2);
-                                sf[cc] = x.x;
-                                sf[cc + 1] = x.y;
-                            }
-                        }
-                    }
 #pragma unroll
                     for (int cc = 0; cc < 128; cc += 4) {
-                        const float2 s01 = make_float2(sf[cc + 0], sf[cc + 1]), s23 = make_float2(sf[cc + 2], sf[cc + 3]);
-                        const float2 x01 = kBias ? s01 : __ffma2_rn(s01, c2, nr2);
-                        const float2 x23 = kBias ? s23 : __ffma2_rn(s23, c2, nr2);
+                        const float2 x01 = __ffma2_rn(make_float2(sf[cc + 0], sf[cc + 1]), c2, nr2);
+                        const float2 x23 = __ffma2_rn(make_float2(sf[cc + 2], sf[cc + 3]), c2, nr2);
                         const float2 e01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
                         const float2 e23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
                         pk[cc / 2] = pack2<kBF16>(e01.x, e01.y);
