@@ -1109,6 +1109,29 @@ fa_status fa_mask_plan(const int32_t *docs, const int32_t *prefix, void *plan, i
                                                                                      : FA_ERR_CUDA;
 }
 
+// Whether rows of two packed tensors, `w` elements wide and `s` apart, share
+// memory: T rows each; equal strides may interleave (slices of wider rows).
+static bool rows_overlap(const void *x, long long wx, long long sx, const void *y, long long wy,
+                         long long sy, long long T) {
+    if (!x || !y || T < 1) return false;
+    const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
+    if (a >= b + 2 * ((T - 1) * sy + wy) || b >= a + 2 * ((T - 1) * sx + wx)) return false;
+    if (sx != sy) return true;
+    const long long row = 2 * sx, off = ((b - a) % row + row) % row;     // y's columns begin at off
+    return off < 2 * wx || off + 2 * wy > row;
+}
+
+// Whether the contiguous output o [B][N][heads][d] shares memory with q, k or v
+// (a kernel reads them while another CTA writes).
+static bool masked_overlap(const void *o, int heads, const void *q, long long q_stride, const void *k,
+                           long long k_stride, const void *v, long long v_stride, int B, int H,
+                           int H_kv, int N, int d) {
+    const long long T = static_cast<long long>(B) * N, w = static_cast<long long>(heads) * d;
+    const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d;
+    return rows_overlap(o, w, w, q, wq, q_stride, T) || rows_overlap(o, w, w, k, wk, k_stride, T) ||
+           rows_overlap(o, w, w, v, wk, v_stride, T);
+}
+
 // What the forward and the backward on a mask plan check of their sizes.
 static fa_status masked_checks(const void *plan, const float *slopes, const float *sinks, int B, int H,
                                int H_kv, int N, int d, long long q_stride, long long k_stride,
@@ -1147,6 +1170,7 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return FA_ERR_MISALIGNED;
+    if (masked_overlap(o, H, q, q_stride, k, k_stride, v, v_stride, B, H, H_kv, N, d)) return FA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
 
@@ -1199,6 +1223,19 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
         !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(dsinks) & 3u))
         return FA_ERR_MISALIGNED;
+    const long long T = static_cast<long long>(B) * N, wq = static_cast<long long>(H) * d,
+                    wk = static_cast<long long>(H_kv) * d;
+    const struct { const void *p; int heads; } outs[3] = {{dq, H}, {dk, H_kv}, {dv, H_kv}};
+    for (int i = 0; i < 3; ++i) {
+        const long long w = i == 0 ? wq : wk;
+        if (masked_overlap(outs[i].p, outs[i].heads, q, q_stride, k, k_stride, v, v_stride, B, H, H_kv, N, d) ||
+            rows_overlap(outs[i].p, w, w, o, wq, wq, T) || rows_overlap(outs[i].p, w, w, dout, wq, wq, T))
+            return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j) {
+            const long long wj = j == 0 ? wq : wk;
+            if (rows_overlap(outs[i].p, w, w, outs[j].p, wj, wj, T)) return FA_ERR_INVALID_ARG;
+        }
+    }
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
 
@@ -1255,18 +1292,6 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
 }
 
 // ---- rotary positions ----
-
-// Whether rows of two packed tensors, `w` elements wide and `s` apart, share
-// memory: T rows each; equal strides may interleave (slices of wider rows).
-static bool rows_overlap(const void *x, long long wx, long long sx, const void *y, long long wy,
-                         long long sy, long long T) {
-    if (!x || !y || T < 1) return false;
-    const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
-    if (a >= b + 2 * ((T - 1) * sy + wy) || b >= a + 2 * ((T - 1) * sx + wx)) return false;
-    if (sx != sy) return true;
-    const long long row = 2 * sx, off = ((b - a) % row + row) % row;     // y's columns begin at off
-    return off < 2 * wx || off + 2 * wy > row;
-}
 
 // What both rotary entry points check of sizes and pointers, laid out.
 static fa_status rope_args(fa::RopeArgs *a, const void *q, const void *k, void *q_out,

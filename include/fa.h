@@ -541,6 +541,8 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
  *     O = softmax(S) V, LSE = log sum exp(S)      (over the visible keys)
  *
  * A row that sees nothing gives O = 0, LSE = -inf, and its gradients are 0.
+ * Outputs share no memory with q, k, v, o, dout or one another
+ * (FA_ERR_INVALID_ARG).
  */
 
 /*
