@@ -973,6 +973,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tbase, C::TMEM_COLS);
     }
+    // Interval masks: this grid may have begun before the dK/dV kernel's end, and what
+    // follows it on the stream waits for this one alone.
+    if constexpr (kMask) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -1069,6 +1072,10 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    // Interval masks: once every CTA of this grid has begun (or been taken over), the
+    // dQ kernel's may begin on SMs that run out of key tiles; it reads nothing that
+    // this one writes.
+    if constexpr (kMask) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 8) {
         // =================== TMA producer (one lane) ===================

@@ -44,6 +44,21 @@ cudaError_t launch_bwd_inst(const BwdLaunch &L) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     kkv<<<L.grid_kv, C::NTHREADS, C::KV_SMEM, L.stream>>>(L.q, L.k, L.v, L.dout, L.args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if constexpr (kMask) {
+        // Its CTAs fill the SMs that the longest key tiles leave idle at the end:
+        // measured with few units of unlike length (d = 64, 288 of up to 72 steps).
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(L.grid));
+        cfg.blockDim = dim3(C::NTHREADS);
+        cfg.dynamicSmemBytes = C::DQ_SMEM;
+        cfg.stream = L.stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kdq, L.q, L.k, L.v, L.dout, L.args);
+    }
     kdq<<<L.grid, C::NTHREADS, C::DQ_SMEM, L.stream>>>(L.q, L.k, L.v, L.dout, L.args);
     return cudaGetLastError();
 }
