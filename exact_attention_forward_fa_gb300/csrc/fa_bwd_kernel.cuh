@@ -324,6 +324,7 @@ fa_bwd_delta_kernel(const BwdArgs a) {
             }
         }
     }
+    if constexpr (kMask) grid_launch_dependents();
     const long n_pad = static_cast<long>(a.B) * a.H * a.NP;
     for (long idx = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n_pad;
          idx += static_cast<long>(gridDim.x) * blockDim.x) {
@@ -975,7 +976,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     // Interval masks: this grid may have begun before the dK/dV kernel's end, and what
     // follows it on the stream waits for this one alone.
-    if constexpr (kMask) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (kMask) grid_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -1072,10 +1073,6 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    // Interval masks: once every CTA of this grid has begun (or been taken over), the
-    // dQ kernel's may begin on SMs that run out of key tiles; it reads nothing that
-    // this one writes.
-    if constexpr (kMask) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 8) {
         // =================== TMA producer (one lane) ===================
@@ -1146,6 +1143,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 load_tile<C::NCH>(&tm_k, base + C::KV_K_OFF, bar(C::KVB_KVFULL), U.h, U.m * 128, U.b);
                 load_tile<C::NCH>(&tm_v, base + C::KV_V_OFF, bar(C::KVB_KVFULL), U.h, U.m * 128, U.b);
                 ++kvn;
+                if (kMask && kvn == 1) grid_wait();          // (the first rows' statistics)
                 int qlo_t, qhi_t;
                 query_range(U, qlo_t, qhi_t);
                 // the query heads of this K/V head, each over its query tiles
@@ -1294,6 +1292,14 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         __syncwarp();
     } else {
         // =================== elementwise group (warps 0-7) ===================
+        if constexpr (kMask) {
+            // This grid may have begun before the statistics' kernel ended.  Once it
+            // has, and every CTA of this grid has begun (or been taken over), the dQ
+            // kernel's may begin on SMs that run out of key tiles; it reads nothing that
+            // this one writes.
+            grid_wait();
+            if (warp == 0) grid_launch_dependents();
+        }
         const int quarter = warp & 3, half = warp >> 2;
         const int row = quarter * 32 + lane;                 // key row of the tile
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;

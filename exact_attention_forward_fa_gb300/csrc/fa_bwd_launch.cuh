@@ -42,23 +42,27 @@ cudaError_t launch_bwd_inst(const BwdLaunch &L) {
     if (e != cudaSuccess) return e;
     fa_bwd_delta_kernel<D, kBF16, kMask><<<L.grid_delta, 256, 0, L.stream>>>(L.args);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kkv<<<L.grid_kv, C::NTHREADS, C::KV_SMEM, L.stream>>>(L.q, L.k, L.v, L.dout, L.args);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if constexpr (kMask) {
-        // Its CTAs fill the SMs that the longest key tiles leave idle at the end:
-        // measured with few units of unlike length (d = 64, 288 of up to 72 steps).
+        // The dK/dV kernel begins behind the statistics' last CTAs, the dQ kernel's CTAs
+        // on the SMs that the longest key tiles leave idle at the end (288 units of up
+        // to 72 steps, d = 64: 296 us one after the other, 272 so).
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(L.grid));
+        cfg.gridDim = dim3(static_cast<unsigned>(L.grid_kv));
         cfg.blockDim = dim3(C::NTHREADS);
-        cfg.dynamicSmemBytes = C::DQ_SMEM;
+        cfg.dynamicSmemBytes = C::KV_SMEM;
         cfg.stream = L.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, kkv, L.q, L.k, L.v, L.dout, L.args)) != cudaSuccess) return e;
+        cfg.gridDim = dim3(static_cast<unsigned>(L.grid));
+        cfg.dynamicSmemBytes = C::DQ_SMEM;
         return cudaLaunchKernelEx(&cfg, kdq, L.q, L.k, L.v, L.dout, L.args);
     }
+    kkv<<<L.grid_kv, C::NTHREADS, C::KV_SMEM, L.stream>>>(L.q, L.k, L.v, L.dout, L.args);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     kdq<<<L.grid, C::NTHREADS, C::DQ_SMEM, L.stream>>>(L.q, L.k, L.v, L.dout, L.args);
     return cudaGetLastError();
 }

@@ -223,6 +223,16 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch: a grid launched so may begin once every CTA of the
+// one before it has said so (or ended), and waits for that one's end and its writes
+// where it needs them.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // tcgen05
 // ---------------------------------------------------------------------------
 // Whole-warp TMEM allocation; the base address is written to `dst_smem`.
