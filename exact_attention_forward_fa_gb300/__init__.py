@@ -691,13 +691,19 @@ def attention_paged(q, k_pages, v_pages, block_table, kv_len, cu_q, max_q: int, 
             or workspace.numel() * workspace.element_size() < fa_paged_workspace_bytes(d)):
         raise ValueError(f"the workspace is {fa_paged_workspace_bytes(d)} bytes on {q.device}")
     try:
-        head = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        if slopes is None:
+            rc = load().fa_fwd_paged(
+                q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                 kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                workspace.data_ptr())
-        tail = (B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha, left, right, first,
+                workspace.data_ptr(), B, H, hk, T, max_q, d, ps, n, W, qs, k_pages.stride(0), alpha,
+                left, right, first, FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
+        else:
+            rc = load().fa_fwd_paged_bias(
+                q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                workspace.data_ptr(), slopes.data_ptr(), B, H, hk, T, max_q, d, ps, n, W, qs,
+                k_pages.stride(0), alpha, left, right, first,
                 FA_BF16 if dtype is torch.bfloat16 else FA_FP16, raw)
-        rc = (load().fa_fwd_paged(*head, *tail) if slopes is None
-              else load().fa_fwd_paged_bias(*head, slopes.data_ptr(), *tail))
     finally:
         if shared:
             _paged_ws_lock.release()
@@ -888,25 +894,34 @@ def mask_plan(docs, N: int, prefix=None, window=(-1, 0), out: MaskPlan | None = 
 def _check_masked(q, k, v, plan, slopes, sinks):
     """What the forward and the backward on a plan are told by sizes and
     strides: (dtype code, B, N, H, H_kv, d, strides of q, k, v)."""
-    at = q.get_device()
-    dt = _dtype_of(q)
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+    at, dtype, shape, kv_shape = q.get_device(), q.dtype, q.shape, k.shape
+    if dtype is _torch.bfloat16:
+        dt = FA_BF16
+    elif dtype is _torch.float16:
+        dt = FA_FP16
+    else:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if len(shape) != 4 or len(kv_shape) != 4 or kv_shape != v.shape:
         raise ValueError("q is [B, N, H, d], k and v are [B, N, H_kv, d]")
-    B, N, H, d = q.shape
-    if k.shape[:2] != (B, N) or k.shape[3] != d:
+    B, N, H, d = shape
+    kv_B, kv_N, hk, kv_d = kv_shape
+    if kv_B != B or kv_N != N or kv_d != d:
         raise ValueError("q, k and v differ in tokens or head dim")
-    if (plan.B, plan.N) != (B, N):
+    if plan.B != B or plan.N != N:
         raise ValueError(f"a plan of [{plan.B}, {plan.N}] for sequences of [{B}, {N}]")
-    _like(k, q, "k")
-    _like(v, q, "v")
-    if plan.data.get_device() != at:
-        raise ValueError("tensors on different devices")
-    for x in (slopes, sinks):
-        if x is not None:
-            _check_float(x, (H,), at)
+    if (k.dtype is not dtype or v.dtype is not dtype or k.get_device() != at or v.get_device() != at
+            or plan.data.get_device() != at):
+        raise ValueError("q, k, v and the plan differ in type or device")
+    if slopes is not None:
+        _check_float(slopes, (H,), at)
+    if sinks is not None:
+        _check_float(sinks, (H,), at)
     if at < 0:
         raise ValueError("tensors must be on the GPU")
-    return dt, B, N, H, k.shape[2], d, _rows_stride(q, "q"), _rows_stride(k, "k"), _rows_stride(v, "v")
+    wide, wide_kv = H * d, hk * d
+    return (dt, B, N, H, hk, d, wide if q.is_contiguous() else _rows_stride(q, "q"),
+            wide_kv if k.is_contiguous() else _rows_stride(k, "k"),
+            wide_kv if v.is_contiguous() else _rows_stride(v, "v"))
 
 
 def _check_out(x, shape, ref, name: str) -> None:
@@ -1044,7 +1059,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return w.to(device), scale
 
 
-def _check_turns(inv_freq, d: int, at: int) -> int:
+def _check_turns(inv_freq, at: int) -> int:
     """rot_dim of a frequency tensor."""
     if inv_freq.dtype is not _torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq is a contiguous float64 [rot_dim / 2]")
@@ -1057,29 +1072,16 @@ def _rows_stride(x, name: str) -> int:
     """The elements between the tokens of a [B, N, heads, d] or [T, heads, d]
     tensor whose tokens follow one another at one distance."""
     s, shape = x.stride(), x.shape
-    heads, d = shape[-2:]
-    if x.numel() and (s[-1] != 1 or (s[-2] != d and heads > 1)):
+    heads, d = shape[-2], shape[-1]
+    if (s[-1] != 1 or (s[-2] != d and heads > 1)) and x.numel():
         raise ValueError(f"{name} has contiguous [heads, d] rows")
     if len(shape) == 3:
         return s[0] if shape[0] > 1 else heads * d
-    B, N = shape[:2]
+    B, N = shape[0], shape[1]
     step = s[1] if N > 1 else s[0] if B > 1 else heads * d
     if B > 1 and N > 1 and s[0] != N * step:
         raise ValueError(f"{name}: the tokens of all sequences follow at one distance")
     return step
-
-
-def _dtype_of(x) -> int:
-    if x.dtype is _torch.bfloat16:
-        return FA_BF16
-    if x.dtype is _torch.float16:
-        return FA_FP16
-    raise TypeError(f"unsupported dtype {x.dtype}")
-
-
-def _like(x, ref, name: str) -> None:
-    if x.dtype is not ref.dtype or x.get_device() != ref.get_device():
-        raise ValueError(f"{name} differs in type or device")
 
 
 def rope(q, k, inv_freq, positions=None, scale: float = 1.0, interleaved: bool = False,
@@ -1096,44 +1098,49 @@ def rope(q, k, inv_freq, positions=None, scale: float = 1.0, interleaved: bool =
     if stream is not None or (at >= 0 and at != torch._C._cuda_getDevice()):
         with _launch_on(q.device, stream):
             return rope(q, k, inv_freq, positions, scale, interleaved, inverse, q_out, k_out)
-    dt = _dtype_of(q)
-    shape = q.shape
-    if len(shape) not in (3, 4):
+    dtype, shape = q.dtype, q.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if len(shape) == 4:
+        B, N, H, d = shape
+    elif len(shape) == 3:
+        B, (N, H, d) = 1, shape
+    else:
         raise ValueError("q is [B, N, H, d] or [T, H, d]")
-    lead, (H, d) = shape[:-2], shape[-2:]
-    rot = _check_turns(inv_freq, d, at)
+    rot = _check_turns(inv_freq, at)
     if positions is not None:
-        _check_int(positions, lead, at)
-    qs, ks, kos, hk = _rows_stride(q, "q"), 0, 0, 0
+        _check_int(positions, shape[:-2], at)
+    qs, ks, kos, hk, wide = _rows_stride(q, "q"), 0, 0, 0, H * d
     if q_out is None:
-        q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
-    elif q_out.shape != shape:
-        raise ValueError("q_out differs from q in shape")
-    _like(q_out, q, "q_out")
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif q_out.shape != shape or q_out.dtype is not dtype or q_out.get_device() != at:
+        raise ValueError("q_out differs from q in shape, type or device")
     if k is not None:
-        hk = k.shape[-2]
-        if k.shape != (*lead, hk, d):
+        kv_shape = k.shape
+        hk = kv_shape[-2] if len(kv_shape) == len(shape) else -1
+        if kv_shape[:-2] != shape[:-2] or kv_shape[-1] != d or hk < 0:
             raise ValueError("q and k differ in tokens or head dim")
-        _like(k, q, "k")
+        if k.dtype is not dtype or k.get_device() != at:
+            raise ValueError("q and k differ in type or device")
         ks = _rows_stride(k, "k")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out differs from k in shape")
-        _like(k_out, q, "k_out")
-        kos = _rows_stride(k_out, "k_out")
+            k_out = torch.empty(kv_shape, dtype=dtype, device=k.device)
+        elif k_out.shape != kv_shape or k_out.dtype is not dtype or k_out.get_device() != at:
+            raise ValueError("k_out differs from k in shape, type or device")
+        kos = hk * d if k_out.is_contiguous() else _rows_stride(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
     if at < 0:
         raise ValueError("tensors must be on the GPU")
-    if 0 in lead:
+    if B == 0 or N == 0:
         return q_out, k_out
-    B, N = lead if len(lead) == 2 else (1, lead[0])
     rc = load().fa_rope(
         q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
         None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
-        inv_freq.data_ptr(), B, N, H, hk, d, rot, qs, ks, _rows_stride(q_out, "q_out"), kos, scale,
-        int(bool(interleaved)), int(bool(inverse)), dt, torch._C._cuda_getCurrentRawStream(at))
+        inv_freq.data_ptr(), B, N, H, hk, d, rot, qs, ks,
+        wide if q_out.is_contiguous() else _rows_stride(q_out, "q_out"), kos, scale, 1 if interleaved else 0,
+        1 if inverse else 0, FA_BF16 if dtype is torch.bfloat16 else FA_FP16,
+        torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_rope")
     return q_out, k_out
@@ -1159,12 +1166,12 @@ def paged_rope_append(q, k, v, k_pages, v_pages, block_table, kv_len, cu_q, inv_
     _check_paged(at, dtype, k_pages, v_pages, block_table, kv_len, cu_q, (B + 1,))
     n, ps, hk, dp = k_pages.shape
     qs, ks = _packed_stride(q, "q"), _packed_stride(k, "k")
-    if (k.shape != v.shape or k.dtype is not dtype or v.dtype is not dtype or k.get_device() != at
-            or v.get_device() != at or _packed_stride(v, "v") != ks):
-        raise ValueError("k and v differ in type, shape, strides or device")
-    if k.shape != (T, hk, d) or d != dp:
+    if (k.dtype is not dtype or v.dtype is not dtype or k.get_device() != at or v.get_device() != at
+            or _packed_stride(v, "v") != ks):
+        raise ValueError("k and v differ in type, strides or device")
+    if d != dp or k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError("q, k, v and the pages differ in tokens, heads or head dim")
-    rot = _check_turns(inv_freq, d, at)
+    rot = _check_turns(inv_freq, at)
     if offsets is not None:
         _check_int(offsets, (B,), at)
     if q_out is None:
@@ -1175,8 +1182,8 @@ def paged_rope_append(q, k, v, k_pages, v_pages, block_table, kv_len, cu_q, inv_
         q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(),
         None if offsets is None else offsets.data_ptr(), inv_freq.data_ptr(), B, H, hk, d, rot, T, ps,
-        n, W, qs, ks, _packed_stride(q_out, "q_out"), k_pages.stride(0), scale,
-        int(bool(interleaved)), FA_BF16 if dtype is torch.bfloat16 else FA_FP16,
+        n, W, qs, ks, H * d if q_out.is_contiguous() else _packed_stride(q_out, "q_out"), k_pages.stride(0),
+        scale, 1 if interleaved else 0, FA_BF16 if dtype is torch.bfloat16 else FA_FP16,
         torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_paged_rope_append")
