@@ -283,7 +283,16 @@ fa_bwd_delta_kernel(const BwdArgs a) {
     const int sub = lane / TPR, part = lane % TPR;
     const uint4 *o4 = reinterpret_cast<const uint4 *>(a.o);
     const uint4 *d4 = reinterpret_cast<const uint4 *>(a.dout);
+    // x / y, in 32 bits where they suffice (a 64-bit division is a hundred instructions)
+    auto divide = [](long x, int y) -> long {
+        return x >> 32 ? x / y : static_cast<long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+    };
     for (long base = warp_g * RPW * 4; base < n_rows; base += n_warps * RPW * 4) {
+        // row = (b * N + n) * H + h: the pass's first one
+        const long bn0 = divide(base, a.H);
+        const int h0 = static_cast<int>(base - bn0 * a.H);
+        const long b0 = divide(bn0, a.N);
+        const int n0 = static_cast<int>(bn0 - b0 * a.N);
         uint4 ov[4], dv[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -301,21 +310,20 @@ fa_bwd_delta_kernel(const BwdArgs a) {
             const uint32_t dw[4] = {dv[r].x, dv[r].y, dv[r].z, dv[r].w};
             float acc = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float o0, o1, g0, g1;
-                unpack2<kBF16>(ow[i], o0, o1);
-                unpack2<kBF16>(dw[i], g0, g1);
-                acc = fmaf(o0, g0, acc);
-                acc = fmaf(o1, g1, acc);
-            }
+            for (int i = 0; i < 4; ++i) acc = fma_pair<kBF16>(acc, ow[i], dw[i]);
 #pragma unroll
             for (int m = TPR / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
             const long row = base + r * RPW + sub;
             if (part == 0 && row < n_rows) {
-                // row = (b * N + n) * H + h
-                const long h = row % a.H;
-                const long bn = row / a.H;
-                const long n = bn % a.N, b = bn / a.N;
+                int h = h0 + r * RPW + sub, n = n0;      // (a few steps on: no division)
+                long b = b0;
+                while (h >= a.H) {
+                    h -= a.H;
+                    if (++n == a.N) {
+                        n = 0;
+                        ++b;
+                    }
+                }
                 if constexpr (kMask) {
                     const int4 lv = __ldg(a.plan.live + b);
                     if (n < lv.x || n >= lv.y) acc = 0.f;
@@ -328,7 +336,7 @@ fa_bwd_delta_kernel(const BwdArgs a) {
     const long n_pad = static_cast<long>(a.B) * a.H * a.NP;
     for (long idx = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n_pad;
          idx += static_cast<long>(gridDim.x) * blockDim.x) {
-        const long bh = idx / a.NP, n = idx % a.NP;
+        const long bh = divide(idx, a.NP), n = idx - bh * a.NP;
         float l2 = INFINITY;
         if (n < a.N) {
             const float l = a.lse[bh * a.N + n];

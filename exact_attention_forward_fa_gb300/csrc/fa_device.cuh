@@ -512,6 +512,21 @@ __device__ __forceinline__ void add_pair(float &acc0, float &acc1, uint32_t pk) 
     }
 }
 
+// acc + a0 b0, then + a1 b1, of two packed pairs of 16-bit floats (exact products).
+template <bool kBF16>
+__device__ __forceinline__ float fma_pair(float acc, uint32_t a, uint32_t b) {
+    if constexpr (kBF16) {
+        asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %1;\n\tmov.b32 {b0, b1}, %2;\n\t"
+            "fma.rn.f32.bf16 %0, a0, b0, %0;\n\tfma.rn.f32.bf16 %0, a1, b1, %0;\n\t}"
+            : "+f"(acc) : "r"(a), "r"(b));
+    } else {
+        asm("{\n\t.reg .b16 a0, a1, b0, b1;\n\tmov.b32 {a0, a1}, %1;\n\tmov.b32 {b0, b1}, %2;\n\t"
+            "fma.rn.f32.f16 %0, a0, b0, %0;\n\tfma.rn.f32.f16 %0, a1, b1, %0;\n\t}"
+            : "+f"(acc) : "r"(a), "r"(b));
+    }
+    return acc;
+}
+
 // Four FP32 values -> four e4m3 bytes (RN, saturating at +-448), a first.
 __device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d) {
     uint16_t lo, hi;

@@ -69,13 +69,30 @@ __device__ void sort_units(int n, int most, Cost &&cost, Out &&out) {
     };
     for (int u = threadIdx.x; u < n; u += kThreads) atomicAdd(&count[bucket(u)], 1);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int at = 0;
-        for (int i = 0; i < kBuckets; ++i) {
-            const int c = count[i];
-            count[i] = at;
-            at += c;
-        }
+    // each thread's buckets, then the threads' sums over lanes and warps
+    constexpr int kEach = kBuckets / kThreads;
+    __shared__ int warp_sum[kThreads / 32];
+    int c[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        c[i] = count[threadIdx.x * kEach + i];
+        mine += c[i];
+    }
+    const int lane = threadIdx.x & 31;
+    int upto = mine;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, upto, w);
+        if (lane >= w) upto += below;
+    }
+    if (lane == 31) warp_sum[threadIdx.x / 32] = upto;
+    __syncthreads();
+    int at = upto - mine;
+    for (int w = 0; w < static_cast<int>(threadIdx.x) / 32; ++w) at += warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        count[threadIdx.x * kEach + i] = at;
+        at += c[i];
     }
     __syncthreads();
     for (int u = threadIdx.x; u < n; u += kThreads) out(u, atomicAdd(&count[bucket(u)], 1));
