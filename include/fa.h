@@ -21,6 +21,8 @@
  *     FP8 scales : [B][H][ceil(N/128)] float32, one per 128-row tile of a head
  *     paged cache: pools of pages with their own strides (see "Paged
  *                  key/value cache" below)
+ *     masked attention and rotary positions: rows that follow one another
+ *                  at a stride of their own
  *
  * Conventions for every entry point:
  *   * Pointers named q, k, v, o, lse, x, x8, *_scale, *_pages, *_table,

@@ -152,3 +152,103 @@ def test_many_units(gpu_lib):
     assert fa.fa_check_status() == fa.FA_OK
     r = reference(q, k, v, seen, slopes, None, 1 / math.sqrt(d), do)
     check_backward(got, r, "bf16", d, slopes)
+
+
+def test_training_layer(gpu_lib):
+    """A layer's attention as a training step runs it -- plan, rotation of slices of a fused projection, attention,
+    gradients, rotation back -- against automatic differentiation in float64, eager and captured.
+
+    Tolerance: the chain's steps as above, taken together in the norm: q and k are rounded after the rotation (u
+    each of the scores' arguments), the gradients' errors (at most 3 u of their size, independent from element
+    to element) pass the rotation and are rounded again; 8 u of the norm bounds them with the scores' errors, which
+    move P by alpha |q| |k| u ~ sqrt(d) u."""
+    B, N, H, Hk, d = 2, 333, 4, 2, 64
+    docs, prefix = [[0, 100, 101, 320], [5, 200, 333, 333]], [[40, 0, 100], [0, 133, 0]]
+    g = torch.Generator("cuda").manual_seed(11)
+    rows = torch.randn(B, N, H + 2 * Hk, d, generator=g, device="cuda").bfloat16()
+    dout = gradient(rows[:, :, :H], docs, "bf16", nan=False)
+    slopes, alpha = slopes_of(H), 1 / math.sqrt(d)
+    w, scale = fa.rope_frequencies(d // 2, scaling="yarn", factor=4.0, original=64)
+    offsets = torch.tensor(docs, dtype=torch.int32, device="cuda")
+    plan = fa.mask_plan(offsets, N, prefix=torch.tensor(prefix, dtype=torch.int32, device="cuda"))
+
+    def step():
+        q, k, v = rows[:, :, :H], rows[:, :, H:H + Hk], rows[:, :, H + Hk:]
+        qr, kr = fa.rope(q, k, w, positions=plan.positions, scale=scale)
+        o, lse = fa.attention_masked(qr, kr, v, plan, slopes=slopes)
+        dq, dk, dv, _ = fa.attention_backward_masked(qr, kr, v, o, lse, dout, plan, slopes=slopes)
+        dq, dk = fa.rope(dq, dk, w, positions=plan.positions, scale=scale, inverse=True, q_out=dq, k_out=dk)
+        return o, dq, dk, dv
+
+    got = step()
+    # float64: the same mathematics on leaves of its own
+    from tests._masked import visible
+    leaf = [x.double().requires_grad_() for x in (rows[:, :, :H], rows[:, :, H:H + Hk], rows[:, :, H + Hk:])]
+    a = plan.positions.double()[..., None, None] * w
+
+    def turn(x):
+        u, v = x[..., :d // 4], x[..., d // 4:d // 2]
+        c, s = torch.cos(a) * scale, torch.sin(a) * scale
+        return torch.cat([u * c - v * s, v * c + u * s, x[..., d // 2:]], -1)
+
+    q, k = turn(leaf[0]), turn(leaf[1])
+    dist = (torch.arange(N)[:, None] - torch.arange(N)[None]).abs().double().cuda()
+    outs = []
+    for b in range(B):
+        seen = visible(docs[b], prefix[b], N, -1, 0)
+        alive = seen.any(1)[:, None]
+        for h in range(H):
+            x = alpha * q[b, :, h] @ k[b, :, h // 2].T - slopes[h].double() * dist
+            p = torch.softmax(x.masked_fill(~seen & alive, -math.inf), -1) * alive
+            outs.append(p @ leaf[2][b, :, h // 2])
+    o = torch.stack(outs).reshape(B, H, N, d).transpose(1, 2)
+    (o * dout.double()).sum().backward()
+    for x, y in zip(got, [o.detach()] + [x.grad for x in leaf]):
+        assert float((x.double() - y).norm() / y.norm()) <= 8 * 2.0 ** -8
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            captured = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, captured))
+    assert fa.fa_check_status() == fa.FA_OK
+
+
+def test_two_streams_and_threads(gpu_lib):
+    """Calls on two streams at once, and from two host threads, give the bits of calls one after the other."""
+    import threading
+    cases = []
+    for seed, (N, d) in enumerate([(1100, 64), (700, 128)]):
+        docs = [pack(N, [300, 390])]
+        q, k, v, plan, _ = make(1, N, 8, 4, d, "bf16", docs, None, -1, -1, seed=seed, nan=False)
+        do = gradient(q, docs, "bf16", nan=False)
+        cases.append((q, k, v, plan, do, slopes_of(8)))
+
+    def step(c):
+        q, k, v, plan, do, slopes = c
+        o, lse = fa.attention_masked(q, k, v, plan, slopes=slopes)
+        return (o, lse) + fa.attention_backward_masked(q, k, v, o, lse, do, plan, slopes=slopes)[:3]
+
+    alone = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got[i] = step(cases[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert fa.fa_check_status() == fa.FA_OK
