@@ -1154,7 +1154,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             bool live = false;
             float inv = 0.f, lse2 = -INFINITY;      // LSE in log2 units
             auto normalise = [&]() __attribute__((always_inline)) {
-                live = (le > 0.f) && (kFP8 || lr > 0.f);
+                // (interval masks: a NaN that the row sees stays one)
+                live = kMask ? !(le <= 0.f) : (le > 0.f) && (kFP8 || lr > 0.f);
                 inv = live ? (kFP8 ? vmax / le : 1.f / lr) : 0.f;
                 lse2 = live ? r - C::P_OFFSET + log2f(le) : -INFINITY;
                 if constexpr (kExt) {

@@ -536,8 +536,10 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
  * prefix too; without a right bound a prefix changes nothing.)  Tokens before
  * docs[b][0] and from docs[b][n_docs] on are padding: they see nothing, nobody
  * sees them, and q, k, v and dout may hold anything there (NaN included).
- * Within the documents, an infinity or NaN in a value, key, query or gradient
- * reaches, as 0 times it, also rows of its 128-token tile that do not see it.
+ * Within the documents, a NaN in q or in a key that a row sees makes its O and
+ * LSE NaN and those of no other row; an infinity or NaN in a value, and in the
+ * backward in any input, reaches, as 0 times it, also rows whose tile of 128
+ * sees its tile.
  *
  *     S_ij = alpha q_i . k_j - slopes[h] |i - j|
  *     O = softmax(S) V, LSE = log sum exp(S)      (over the visible keys)
@@ -678,8 +680,8 @@ fa_status fa_check_status(void *stream);
  * that returned FA_ERR_TIMEOUT or FA_ERR_BAD_INDEX: out[0] code, out[1] role
  * that gave up (1/2 softmax group L/H, 3 producer, 4 MMA issuer, 6 FP8
  * pre-pass, 7 self-test, 8 paged cache),
- * out[2] wait site (bad index: 1 kv_len or cu_q, 2 page id, 3 kv_len beyond
- * the scores),
+ * out[2] wait site (bad index, role 8 for the mask plan too: 1 kv_len or cu_q,
+ * 2 page id, 3 kv_len beyond the scores, 4 document offset, 5 prefix),
  * out[3] block index.  Zeros if nothing was ever reported.
  */
 void fa_status_detail(uint32_t out[4]);

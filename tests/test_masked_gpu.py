@@ -175,3 +175,28 @@ def test_many_units(gpu_lib):
     for h in (0, 13, 47):
         r = reference(q[:, :, h:h + 1], k[:, :, h // 12:h // 12 + 1], v[:, :, h // 12:h // 12 + 1], seen, slopes[h:h + 1], None, 0.125)
         check_forward(o[:, :, h:h + 1], lse[:, h:h + 1], r, "bf16", d, 0.125, slopes[h:h + 1])
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_reaches_the_rows_that_see_it(gpu_lib, d, bias):
+    """A NaN key makes the rows that see it NaN, a NaN query its own row, and no others."""
+    N, H = 700, 2
+    docs = [pack(N, [100, 450, 140])]
+    q, k, v, plan, seen = make(1, N, H, H, d, "bf16", docs, None, 200, 0, seed=21)
+    slopes = slopes_of(H) if bias else None
+    clean = fa.attention_masked(q, k, v, plan, slopes=slopes)
+    q, k = q.clone(), k.clone()
+    k[0, 300, 1, 5] = math.nan
+    q[0, 610, 1, 0] = math.nan
+    o, lse = fa.attention_masked(q, k, v, plan, slopes=slopes)
+    hit = seen[0][:, 300].clone()
+    hit[610] = True
+    assert torch.isnan(o[0, hit, 1]).all() and torch.isnan(lse[0, 1, hit]).all()
+    # the other rows: their maximum may have been taken at another tile, nothing else
+    assert torch.equal(o[0, :, 0], clean[0][0, :, 0]) and torch.equal(lse[0, 0], clean[1][0, 0])
+    rest = ~hit
+    assert torch.isfinite(o[0, rest, 1]).all()
+    assert (o[0, rest, 1].float() - clean[0][0, rest, 1].float()).abs().max() <= 2 * U["bf16"] * 4
+    same = lse[0, 1, rest], clean[1][0, 1, rest]
+    assert ((same[0] - same[1]).abs().nan_to_num() < 1e-5).all()
