@@ -478,11 +478,9 @@ __device__ __forceinline__ float row_max_of(const float *s) {
         m2 = max3(m2, s[c + 2], s[c + 6]);
         m3 = max3(m3, s[c + 3], s[c + 7]);
     }
-    m0 = fmaxf(m0, s[N - 4]);
-    m1 = fmaxf(m1, s[N - 3]);
-    m2 = fmaxf(m2, s[N - 2]);
-    m3 = fmaxf(m3, s[N - 1]);
-    return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+    m0 = max3(m0, s[N - 4], s[N - 3]);
+    m1 = max3(m1, s[N - 2], s[N - 1]);
+    return max3(fmaxf(m0, m1), m2, m3);
 }
 
 // Two FP32 values -> packed pair of 16-bit floats (low half = a), RN.
