@@ -238,7 +238,8 @@ __device__ __forceinline__ constexpr bool dynamic_units() {
 struct MaskRec {
     int4 id;       // u (-1: no more units), b, h, pair
     int4 tiles;    // key tiles [x, y) of the pair's first Q tile, [z, w) of its second
-    int4 live;     // tokens [x, y) of the sequence belong to documents
+    int4 live;     // tokens [x, y) of the sequence belong to documents;
+                   // kSlots: Q slot of the first tile (z) and of the second (w), 2 slot + parity
 };
 __device__ __forceinline__ MaskRec mask_rec(int u, const FwdArgs &a) {
     int i, bh;
@@ -388,6 +389,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     // Static order: the persistent stride walk.
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::UNIT_OFF);
     constexpr bool kDyn = dynamic_units<kCausal, kSplit, kVar, kPack>();
+    // Interval masks at d = 128: O leaves through Q's slots, so that a slot is free
+    // again when its tile's softmax warps have stored, and take_slots chooses among
+    // them.  With a bias the plain rotation is as fast or faster (documents of 512
+    // tokens, causal, N8192 B2 H32: 129 us, chosen slots 134).
+    constexpr bool kStaged = kMask && C::kOStage;
+    constexpr bool kSlots = kStaged && !kBias;
     // Interval masks: every unit, the first too, comes through the slots, as the
     // record that the producer publishes.
     const volatile int4 *rec_slot = reinterpret_cast<const volatile int4 *>(gbase + C::REC_OFF);
@@ -456,10 +463,31 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             uint32_t slot = 0, phase = 0;
             uint32_t armed = 0, armed_par = 0;      // per-slot: ever armed / parity
             bool ok = true;
+            // kSlots: the slots of the last tile 0 and tile 1, and every slot's
+            // parity.  The tile that starts first takes the free slot and the other one
+            // that of the last tile 0, which is the first to finish: with slots that
+            // only rotated, units of two key tiles waited 3000 cycles for their Q.
+            uint32_t q_of0 = 0, q_of1 = 1, q_par = 0, q_mine0 = 0, q_mine1 = 0;
+            auto take_slots = [&](const Unit &U) __attribute__((always_inline)) {
+                const bool one_first = !U.act[0] || (U.act[1] && U.t0[1] < U.t0[0]);
+                const uint32_t f = 3u - q_of0 - q_of1, p0 = q_of0;
+                if (U.act[0] && U.act[1]) {
+                    q_of0 = one_first ? p0 : f;
+                    q_of1 = one_first ? f : p0;
+                } else if (U.act[0]) {
+                    q_of0 = f;
+                } else if (U.act[1]) {
+                    q_of1 = f;
+                }
+                q_mine0 = 2u * q_of0 + ((q_par >> q_of0) & 1u);
+                q_mine1 = 2u * q_of1 + ((q_par >> q_of1) & 1u);
+                q_par ^= (U.act[0] ? 1u << q_of0 : 0u) ^ (U.act[1] ? 1u << q_of1 : 0u);
+            };
             // Tile x of U into the next Q slot, once the slot's previous
-            // tile has had its last QK.
+            // tile has had its last QK (interval masks: its O has left).
             auto load_q = [&](const int x, const Unit &U) __attribute__((always_inline)) -> bool {
-                const uint32_t qs = qc % C::NQ, qph = (qc / C::NQ) & 1u;
+                const uint32_t mine = x ? q_mine1 : q_mine0;
+                const uint32_t qs = kSlots ? mine >> 1 : qc % C::NQ, qph = kSlots ? mine & 1u : (qc / C::NQ) & 1u;
                 if (!mbar_wait(bar(C::B_QEMPTY + qs), qph ^ 1u, w, 1)) return false;
                 mbar_arrive_expect_tx(bar(C::B_QFULL + qs), C::TILE_BYTES);
 #pragma unroll
@@ -501,12 +529,13 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 MaskRec r{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
                 if (u >= 0) r = mask_rec(u, a);
                 U = mask_unit(r);
+                if constexpr (kSlots) take_slots(U);
                 ++kq;
                 if (!mbar_wait(bar(C::B_CLCEMPTY + q), ph ^ 1u, w, 3)) { ok = false; return false; }
                 int4 *slot_r = reinterpret_cast<int4 *>(gbase + C::REC_OFF) + 3 * q;
                 slot_r[0] = r.id;
                 slot_r[1] = r.tiles;
-                slot_r[2] = r.live;
+                slot_r[2] = make_int4(r.live.x, r.live.y, static_cast<int>(q_mine0), static_cast<int>(q_mine1));
                 mbar_arrive(bar(C::B_UNIT + q));        // release: the record is visible
                 return u >= 0;
             };
@@ -529,8 +558,11 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 } else {
                     U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 }
-                if (U.act[0]) ok = ok && load_q(0, U);
-                if (U.act[1]) ok = ok && load_q(1, U);
+                // (kSlots: the tile that starts second goes behind the first K tile that
+                // it multiplies, since its slot is what this unit waits for)
+                const int second = !kSlots || !U.act[0] || !U.act[1] ? -1 : U.t0[1] < U.t0[0] ? 0 : 1;
+                if (U.act[0] && second != 0) ok = ok && load_q(0, U);
+                if (U.act[1] && second != 1) ok = ok && load_q(1, U);
                 const int hk = kPack ? U.h : U.h / a.group;   // K/V head of this query head
                 for (int t = 0; t < U.T && ok; ++t) {
                     const int j = U.jhi - 1 - t;
@@ -546,6 +578,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         armed |= 1u << slot;
                         armed_par = (armed_par & ~(1u << slot)) | (phase << slot);
                         if (++slot == C::NSTAGE) { slot = 0; phase ^= 1; }
+                        if (kSlots && kv == 0 && second >= 0 && t == (second ? U.t0[1] : U.t0[0]) &&
+                            !(ok = second ? load_q(1, U) : load_q(0, U))) break;
                     }
                 }
             }
@@ -583,6 +617,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
                 return nu;
             };
+            uint2 q_at = make_uint2(0, 0);          // kSlots: the unit's Q slots (MaskRec)
             auto next_rec = [&](Unit &U) __attribute__((always_inline)) -> int {
                 if (!ok) return -1;
                 const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
@@ -592,6 +627,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_CLCEMPTY + q));
                 U = mask_unit(r);
+                q_at = make_uint2(static_cast<uint32_t>(r.live.z), static_cast<uint32_t>(r.live.w));
                 return r.id.x;
             };
             Unit U;
@@ -600,8 +636,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                      u = kMask ? next_rec(U) : kDyn ? next_dyn() : u + st, st = 2 * static_cast<int>(gridDim.x) - st) {
                 if constexpr (!kMask) U = make_unit<kCausal, kSplit, kVar, kPack>(u, a);
                 uint32_t qs0 = 0, qp0 = 0, qs1 = 0, qp1 = 0;   // Q slot and parity per tile
-                if (U.act[0]) { qs0 = qc % C::NQ; qp0 = (qc / C::NQ) & 1u; ++qc; }
-                if (U.act[1]) { qs1 = qc % C::NQ; qp1 = (qc / C::NQ) & 1u; ++qc; }
+                if constexpr (kSlots) {
+                    qs0 = q_at.x >> 1; qp0 = q_at.x & 1u; qs1 = q_at.y >> 1; qp1 = q_at.y & 1u;
+                } else {
+                    if (U.act[0]) { qs0 = qc % C::NQ; qp0 = (qc / C::NQ) & 1u; ++qc; }
+                    if (U.act[1]) { qs1 = qc % C::NQ; qp1 = (qc / C::NQ) & 1u; ++qc; }
+                }
                 for (int t = 0; t <= U.T && ok; ++t) {
                     const bool has_v = t > 0, has_k = t < U.T;
                     uint32_t vslot = 0, vph = 0, kslot = 0, kph = 0;
@@ -666,7 +706,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             }
                             mma_commit_elect(bar(C::B_SFULL + x));
                             // (interval masks: the slot becomes O's stage)
-                            if ((!kMask || !C::kOStage) && t == t1x - 1) mma_commit_elect(bar(C::B_QEMPTY + qs));
+                            if (!kStaged && t == t1x - 1) mma_commit_elect(bar(C::B_QEMPTY + qs));
                         }
                         return true;
                     };
@@ -733,6 +773,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
         Unit Un;
         int2 kr_n = make_int2(0, 0), live_n = make_int2(0, 0);
         float beta_n = 0.f;
+        uint32_t q_slot_n = 0;
         auto fetch = [&]() __attribute__((always_inline)) -> int {
             const uint32_t q = kq % C::CLC_DEPTH, ph = (kq / C::CLC_DEPTH) & 1u;
             ++kq;
@@ -744,6 +785,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             if (r.id.x < 0) return -1;
             Un = mask_unit(r);
             live_n = make_int2(r.live.x, r.live.y);
+            if constexpr (kSlots) q_slot_n = static_cast<uint32_t>(x ? r.live.w : r.live.z) >> 1;
             const int n = (x ? Un.m[1] : Un.m[0]) * 128 + row;
             kr_n = n < a.N ? __ldg(a.plan.rows + static_cast<size_t>(Un.b) * a.N + n) : make_int2(0, 0);
             if constexpr (kBias) beta_n = __ldg(a.slopes + Un.h) * 1.44269504088896340736f;
@@ -763,8 +805,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             uint32_t q_slot = 0;
             if constexpr (kMask) {
                 kvc += 2u * static_cast<uint32_t>(U.T);
-                q_slot = (qc + (x == 1 && U.act[0] ? 1u : 0u)) % C::NQ;
-                qc += (U.act[0] ? 1u : 0u) + (U.act[1] ? 1u : 0u);
+                if constexpr (kSlots) {
+                    q_slot = q_slot_n;
+                } else {
+                    q_slot = (qc + (x == 1 && U.act[0] ? 1u : 0u)) % C::NQ;
+                    qc += (U.act[0] ? 1u : 0u) + (U.act[1] ? 1u : 0u);
+                }
                 unstage();       // (before this unit's first S: its Q tiles may wait for the slot)
                 if (!act) {                              // no row of the tile sees a key
                     u = fetch();
@@ -1205,7 +1251,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + x));
-                if constexpr (kMask && C::kOStage) {
+                if constexpr (kStaged) {
                     // into the tile's Q slot, as TMA's 128-byte swizzle has it
                     uint8_t *orow = gbase + C::Q_OFF + q_slot * C::TILE_BYTES + row * 128;
 #pragma unroll
