@@ -22,11 +22,14 @@
 //
 // Measured (GB300): 16384 tokens of 16 + 16 heads of 128, slices of wider rows
 // (268 MB in and out), 48 us, 5.6 TB/s; half of 40 heads at 6002 tokens, interleaved
-// (123 MB), 26 us; chunks of 11921 tokens into pages (293 MB) 56 us; 64 single
+// (123 MB), 26 us; chunks of 11921 tokens into pages (293 MB) 54 us; plain copies of as
+// many bytes 47, 25 and 50 us; 64 single
 // tokens 4.8 us, a launch and the chain offsets, length, page, store.  Runs of equal
 // length took the place of whole tokens a warp (2.5 and 4.2 rounds of them: 27.4 and
 // 61.6 us).  2 to 4 blocks of 8 warps an SM and 2 to 6 passes in flight lie within
 // 5 % of one another; packed FP32 arithmetic changed nothing.
+#include <climits>
+
 #include "fa_paged.cuh"
 #include "fa_rope.cuh"
 
@@ -103,6 +106,10 @@ fa_rope_kernel(const RopeArgs a, const int G, const int passes, const int warps)
     const long long p0 = total * warp / warps;
     int left = static_cast<int>(total * (warp + 1) / warps - p0);
     int t = static_cast<int>(p0 / passes), pass = static_cast<int>(p0 - static_cast<long long>(t) * passes);
+    // paged: what the run's tokens of one sequence and of one page share (looked up
+    // for each token, the chain of loads cost chunks 3 us of 56)
+    int b = -1, end = INT_MIN, index = -1, page = -1;        // tokens of b end there; page number `index`
+    long long len = 0;
     for (; left > 0; ++t, pass = 0) {
         const int n = min(passes - pass, left);
         left -= n;
@@ -127,13 +134,21 @@ fa_rope_kernel(const RopeArgs a, const int G, const int passes, const int warps)
         long long pos;
         uint4 *kd = nullptr, *vd = nullptr;                  // paged: the token's slot
         if constexpr (kPaged) {
-            const int b = paged_find_seq(a.cu_q, a.B, t);
-            if (b < 0) continue;                             // behind the last sequence
-            const long long len = a.kv_len[b], p = len - a.cu_q[b + 1] + t;
+            if (t >= end) {
+                b = paged_find_seq(a.cu_q, a.B, t);
+                if (b < 0) continue;                         // behind the last sequence
+                end = a.cu_q[b + 1];
+                len = a.kv_len[b];
+                index = -1;
+            }
+            const long long p = len - end + t;
             pos = p + (a.offsets ? a.offsets[b] : 0);
             if (p >= 0 && p < min(len, static_cast<long long>(a.W) << a.ps_log2)) {
-                const int page = paged_page(a.table + static_cast<long long>(b) * a.W, static_cast<int>(p), a.ps_log2,
-                                            a.n_pages, a.status);
+                if (static_cast<int>(p >> a.ps_log2) != index) {
+                    index = static_cast<int>(p >> a.ps_log2);
+                    page = paged_page(a.table + static_cast<long long>(b) * a.W, static_cast<int>(p), a.ps_log2,
+                                      a.n_pages, a.status);
+                }
                 if (page >= 0) {
                     const long long at = static_cast<long long>(page) * a.page_stride +
                                          (p & ((1 << a.ps_log2) - 1)) * (static_cast<long long>(a.H_kv) * a.V);

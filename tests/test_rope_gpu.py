@@ -224,6 +224,27 @@ def test_paged_equals_rope_then_append(gpu_lib):
     assert torch.equal(out, q1) and torch.equal(kp, kp1) and torch.equal(vp, vp1)
 
 
+@pytest.mark.parametrize("q_len", [[1] * 5000 + [0, 7] + [2] * 1500, [3, 0, 1, 4000, 0, 0, 1, 65, 4100, 2, 129]])
+def test_runs_over_sequences_and_pages(gpu_lib, q_len):
+    """More tokens than warps: a warp's tokens go on into the next page and sequence,
+    past empty ones, to rows behind the last."""
+    kv = [n + (17 * b) % 23 for b, n in enumerate(q_len)]
+    q, k, v, kp, vp, table, kv_len, cu = paged(q_len, kv, 2, 1, 64, 8, "bf16")
+    w, _ = fa.rope_frequencies(64)
+    off = torch.tensor([(31 * b) % 1001 for b in range(len(kv))], dtype=torch.int32, device="cuda")
+    pos = torch.cat([torch.arange(n - m, n) + (31 * b) % 1001 for b, (m, n) in enumerate(zip(q_len, kv))]).int().cuda()
+    q1, k1 = fa.rope(q, k, w, positions=pos)
+    kp1, vp1 = kp.clone(), vp.clone()
+    fa.paged_append(k1, v.contiguous(), kp1, vp1, table, kv_len, cu)
+    q, k, v = (torch.cat([x, x[:3000]]).contiguous() for x in (q, k, v))
+    out = torch.full_like(q, 7.0)
+    fa.paged_rope_append(q, k, v, kp, vp, table, kv_len, cu, w, offsets=off, q_out=out)
+    T = sum(q_len)
+    assert torch.equal(out[:T], q1) and (out[T:] == 7).all()
+    assert torch.equal(kp, kp1) and torch.equal(vp, vp1)
+    assert fa.fa_check_status() == fa.FA_OK
+
+
 def test_paged_behind_and_full(gpu_lib):
     """Rows behind cu_q[B] stay; tokens without a slot are dropped and reported."""
     q, k, v, kp, vp, table, kv_len, cu = paged([2, 3], [10, 12], 2, 1, 64, 8, "bf16")
