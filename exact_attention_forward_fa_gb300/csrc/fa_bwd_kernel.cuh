@@ -374,28 +374,44 @@ struct Ring {
     }
 };
 
-// 16-bit A x B^T over the full K = D: both tiles K-major (S = Q K^T style).
-template <int D>
+// 16-bit A x B^T over the full K = D: both tiles K-major (S = Q K^T style).  kBatch:
+// one election for four steps, or eight, instead of one each.  Interval masks at d = 64
+// (4 x 4096, 12 heads over 4: 739 us with one each, 730); at d = 128 long documents
+// lose 3 %, short ones nothing.
+template <int D, bool kBatch = false>
 __device__ __forceinline__ void gemm_ss_kmajor(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem,
                                                uint32_t idesc) {
     const uint64_t ad = smem_desc_sw128(a_smem, 16u, 1024u);
     const uint64_t bd = smem_desc_sw128(b_smem, 16u, 1024u);
+    if constexpr (kBatch) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk >> 2) * 128u * 128u + (kk & 3) * 32u) >> 4;
-        mma_ss_f16_elect(d_tmem, ad + off, bd + off, idesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; kk += 4) {
+            const uint32_t off = ((kk >> 2) * 128u * 128u) >> 4;
+            mma_ss_f16_elect4<2, 2>(d_tmem, ad + off, bd + off, idesc, kk > 0 ? 1u : 0u);
+        }
+    } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 128u * 128u + (kk & 3) * 32u) >> 4;
+            mma_ss_f16_elect(d_tmem, ad + off, bd + off, idesc, kk > 0 ? 1u : 0u);
+        }
     }
 }
 
 // D += A B with A (128 x 128, 16-bit) in TMEM and B (128 rows x D) an
 // MN-major shared-memory tile (P V style).
+template <bool kBatch = false>
 __device__ __forceinline__ void gemm_ts_mn(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem,
                                            uint32_t idesc, bool accumulate) {
     const uint64_t bd = smem_desc_sw128(b_smem, 128u * 128u, 1024u);
+    if constexpr (kBatch) {
+        mma_ts_f16_elect8<8, 128>(d_tmem, a_tmem, bd, idesc, accumulate ? 1u : 0u);
+    } else {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_ts_f16_elect(d_tmem, a_tmem + kk * 8u, bd + ((kk * 2048u) >> 4), idesc,
-                         (accumulate || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk)
+            mma_ts_f16_elect(d_tmem, a_tmem + kk * 8u, bd + ((kk * 2048u) >> 4), idesc,
+                             (accumulate || kk > 0) ? 1u : 0u);
+    }
 }
 
 // Whether tile t reaches outside the documents [live.x, live.y).
@@ -495,6 +511,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // slot k % CLC_DEPTH, the producer publishes its block index there (-1:
     // none left), and the MMA warp and the 8 elementwise warps read it.
     constexpr bool kDyn = (kCausal && !kWin) || kMask;
+    constexpr bool kBatch = kMask && D == 64;               // (gemm_ss_kmajor)
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::DQ_UNIT_OFF);
     // key tiles [lo, hi) of query tile U.m, visited from hi - 1 down
     auto key_range = [&](const BwdUnit &U, int &lo, int &hi) {
@@ -700,9 +717,9 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ok = wait_k(k0) && wait_v(k0);
             if (!ok) break;
             tc_fence_after();
-            gemm_ss_kmajor<D>(tbase + C::DQ_COL_S, base + C::DQ_Q_OFF, k_tile(k0), C::IDESC_SS);
+            gemm_ss_kmajor<D, kBatch>(tbase + C::DQ_COL_S, base + C::DQ_Q_OFF, k_tile(k0), C::IDESC_SS);
             mma_commit_elect(bar(C::DQB_SFULL));
-            gemm_ss_kmajor<D>(tbase + C::DQ_COL_DP, base + C::DQ_DO_OFF, v_tile(k0), C::IDESC_SS);
+            gemm_ss_kmajor<D, kBatch>(tbase + C::DQ_COL_DP, base + C::DQ_DO_OFF, v_tile(k0), C::IDESC_SS);
             mma_commit_elect(bar(C::DQB_DPFULL));
             mma_commit_elect(bar(C::DQB_VEMPTY + RV::slot(k0)));
             if (T == 1) mma_commit_elect(bar(C::DQB_QEMPTY));
@@ -716,7 +733,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ok = wait_k(it + 1);
                     if (!ok) break;
                     tc_fence_after();
-                    gemm_ss_kmajor<D>(tbase + C::DQ_COL_S, base + C::DQ_Q_OFF, k_tile(it + 1), C::IDESC_SS);
+                    gemm_ss_kmajor<D, kBatch>(tbase + C::DQ_COL_S, base + C::DQ_Q_OFF, k_tile(it + 1), C::IDESC_SS);
                     mma_commit_elect(bar(C::DQB_SFULL));
                 }
                 // ---- dS(t) ready: dP(t+1), then dQ += dS(t) K(t) ----
@@ -728,7 +745,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ok = wait_v(it + 1);
                     if (!ok) break;
                     tc_fence_after();
-                    gemm_ss_kmajor<D>(tbase + C::DQ_COL_DP, base + C::DQ_DO_OFF, v_tile(it + 1), C::IDESC_SS);
+                    gemm_ss_kmajor<D, kBatch>(tbase + C::DQ_COL_DP, base + C::DQ_DO_OFF, v_tile(it + 1), C::IDESC_SS);
                     mma_commit_elect(bar(C::DQB_DPFULL));
                     mma_commit_elect(bar(C::DQB_VEMPTY + RV::slot(it + 1)));
                     if (t + 2 == T) mma_commit_elect(bar(C::DQB_QEMPTY));   // last use of Q, dO
@@ -739,7 +756,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     dqe_ph ^= 1;
                 }
                 tc_fence_after();
-                gemm_ts_mn(tbase + C::DQ_COL_DQ, tbase + C::DQ_COL_DS + b2 * 64u, k_tile(it),
+                gemm_ts_mn<kBatch>(tbase + C::DQ_COL_DQ, tbase + C::DQ_COL_DS + b2 * 64u, k_tile(it),
                            C::IDESC_ACC, t > 0);
                 mma_commit_elect(bar(C::DQB_KEMPTY + RK::slot(it)));
             }
@@ -1028,6 +1045,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // slot k % CLC_DEPTH, the producer publishes its block index there (-1:
     // none left), and the MMA warp and the 8 elementwise warps read it.
     constexpr bool kDyn = (kCausal && !kWin) || kMask;
+    constexpr bool kBatch = kMask && D == 64;               // (gemm_ss_kmajor)
     volatile int *unit_slot = reinterpret_cast<volatile int *>(gbase + C::KV_UNIT_OFF);
     // query tiles [lo, hi) that see key tile U.m
     auto query_range = [&](const BwdUnit &U, int &lo, int &hi) {
@@ -1240,7 +1258,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             auto g1 = [&](uint32_t i) __attribute__((always_inline)) -> bool {
                 if (!wait_q(i)) return false;
                 tc_fence_after();
-                gemm_ss_kmajor<D>(tbase + C::st_col(i), base + C::KV_K_OFF, q_tile(i), C::IDESC_SS);
+                gemm_ss_kmajor<D, kBatch>(tbase + C::st_col(i), base + C::KV_K_OFF, q_tile(i), C::IDESC_SS);
                 mma_commit_elect(bar(C::st_bar(i)));
                 return true;
             };
@@ -1249,7 +1267,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = wait_do(q_item);
             if (!ok) break;
             tc_fence_after();
-            gemm_ss_kmajor<D>(tbase + C::KV_COL_DPT, base + C::KV_V_OFF, do_tile(q_item), C::IDESC_SS);
+            gemm_ss_kmajor<D, kBatch>(tbase + C::KV_COL_DPT, base + C::KV_V_OFF, do_tile(q_item), C::IDESC_SS);
             mma_commit_elect(bar(C::KVB_DPTFULL));
             if (C::KV_SDB && Ti > 1) {               // the second buffer starts one tile ahead
                 ok = g1(q_item + 1);
@@ -1264,7 +1282,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!ok) break;
                 if (k == 0) accph ^= 1;
                 tc_fence_after();
-                gemm_ts_mn(tbase + C::KV_COL_DV, tbase + C::st_col(ic) + 32, do_tile(ic), C::IDESC_ACC,
+                gemm_ts_mn<kBatch>(tbase + C::KV_COL_DV, tbase + C::st_col(ic) + 32, do_tile(ic), C::IDESC_ACC,
                            k > 0);
                 mma_commit_elect(bar(C::KVB_DOEMPTY + RO::slot(ic)));
                 // ---- G1 into the S^T buffer G3 has just read: tile i+2
@@ -1278,7 +1296,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!ok) break;
                 dsph ^= 1;
                 tc_fence_after();
-                gemm_ts_mn(tbase + C::KV_COL_DK, tbase + C::KV_COL_DPT + 32, q_tile(ic), C::IDESC_ACC,
+                gemm_ts_mn<kBatch>(tbase + C::KV_COL_DK, tbase + C::KV_COL_DPT + 32, q_tile(ic), C::IDESC_ACC,
                            k > 0);
                 mma_commit_elect(bar(C::KVB_QEMPTY + RQ::slot(ic)));
                 // ---- G2(i+1) ----
@@ -1286,7 +1304,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ok = wait_do(in);
                     if (!ok) break;
                     tc_fence_after();
-                    gemm_ss_kmajor<D>(tbase + C::KV_COL_DPT, base + C::KV_V_OFF, do_tile(in), C::IDESC_SS);
+                    gemm_ss_kmajor<D, kBatch>(tbase + C::KV_COL_DPT, base + C::KV_V_OFF, do_tile(in), C::IDESC_SS);
                     mma_commit_elect(bar(C::KVB_DPTFULL));
                 }
             }

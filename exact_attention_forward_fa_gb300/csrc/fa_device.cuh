@@ -304,6 +304,68 @@ __device__ __forceinline__ void mma_ts_f16_elect(uint32_t d_tmem, uint32_t a_tme
         : "memory");
 }
 
+// Four steps of a product with one election: descriptors (and A's TMEM columns) go on
+// by constants, and all but the first step accumulate.
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma_ss_f16_elect4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                  uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+        "add.s64 a2, a1, %5;\n\tadd.s64 b2, b1, %6;\n\t"
+        "add.s64 a3, a2, %5;\n\tadd.s64 b3, b2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+        : "memory");
+}
+
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma_ts_f16_elect4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                  uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s32 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+        "add.s32 a2, a1, %5;\n\tadd.s64 b2, b1, %6;\n\t"
+        "add.s32 a3, a2, %5;\n\tadd.s64 b3, b2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+        : "memory");
+}
+
+// Eight steps, A in TMEM.
+template <int kStepA, int kStepB>
+__device__ __forceinline__ void mma_ts_f16_elect8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                  uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a<8>;\n\t.reg .b64 b<8>;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s32 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+        "add.s32 a2, a1, %5;\n\tadd.s64 b2, b1, %6;\n\t"
+        "add.s32 a3, a2, %5;\n\tadd.s64 b3, b2, %6;\n\t"
+        "add.s32 a4, a3, %5;\n\tadd.s64 b4, b3, %6;\n\t"
+        "add.s32 a5, a4, %5;\n\tadd.s64 b5, b4, %6;\n\t"
+        "add.s32 a6, a5, %5;\n\tadd.s64 b6, b5, %6;\n\t"
+        "add.s32 a7, a6, %5;\n\tadd.s64 b7, b6, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t;\n\t}"
+        :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kStepA), "n"(kStepB)
+        : "memory");
+}
+
 // kind::f8f6f4 forms (e4m3 x e4m3 -> f32), same issue discipline.
 __device__ __forceinline__ void mma_ss_f8_elect(uint32_t d_tmem, uint64_t a_desc,
                                                 uint64_t b_desc, uint32_t idesc,

@@ -666,19 +666,38 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const uint64_t vd = smem_desc_sw128(base + C::KV_OFF + vslot * C::TILE_BYTES,
                                                                 C::CHUNK_BYTES, 1024u);
                             const uint32_t acc = (t - 1 > t0x) ? 1u : 0u;
+                            // Interval masks: one election for four or eight steps.  At d = 64
+                            // this warp's issue is on the critical path (4 x 4096, 32 heads:
+                            // 615 us with one each, 609; with a bias 753 and 735); O and L in
+                            // turn by fours (by eights 612 and 742).
+                            constexpr int kStepV = (C::PV_KEYS * 128) / 16;
+                            if constexpr (kMask && C::kLMMA) {
 #pragma unroll
-                            for (int kk = 0; kk < C::PV_STEPS; ++kk) {
-                                const uint64_t bd = vd + ((kk * C::PV_KEYS * 128u) >> 4);
-                                if constexpr (kFP8)
-                                    mma_ts_f8_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u,
-                                                    bd, C::IDESC_PV, (acc | kk) ? 1u : 0u);
-                                else
-                                    mma_ts_f16_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u,
-                                                     bd, C::IDESC_PV, (acc | kk) ? 1u : 0u);
-                                if constexpr (C::kLMMA)     // L_X += P_X 1 (row sums of P)
-                                    mma_ts_f16_elect(tbase + C::col_l(x), tbase + C::col_s(x) + kk * 8u,
-                                                     smem_desc_sw128(base + C::ONES_OFF, 16u, 1024u),
-                                                     C::IDESC_L, (acc | kk) ? 1u : 0u);
+                                for (int kk = 0; kk < C::PV_STEPS; kk += 4) {
+                                    mma_ts_f16_elect4<8, kStepV>(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u,
+                                                                 vd + kk * kStepV, C::IDESC_PV, (acc | kk) ? 1u : 0u);
+                                    mma_ts_f16_elect4<8, 0>(tbase + C::col_l(x), tbase + C::col_s(x) + kk * 8u,
+                                                            smem_desc_sw128(base + C::ONES_OFF, 16u, 1024u),
+                                                            C::IDESC_L, (acc | kk) ? 1u : 0u);
+                                }
+                            } else if constexpr (kMask) {
+                                mma_ts_f16_elect8<8, kStepV>(tbase + C::col_o(x), tbase + C::col_s(x), vd,
+                                                             C::IDESC_PV, acc);
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < C::PV_STEPS; ++kk) {
+                                    const uint64_t bd = vd + ((kk * C::PV_KEYS * 128u) >> 4);
+                                    if constexpr (kFP8)
+                                        mma_ts_f8_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u,
+                                                        bd, C::IDESC_PV, (acc | kk) ? 1u : 0u);
+                                    else
+                                        mma_ts_f16_elect(tbase + C::col_o(x), tbase + C::col_s(x) + kk * 8u,
+                                                         bd, C::IDESC_PV, (acc | kk) ? 1u : 0u);
+                                    if constexpr (C::kLMMA)     // L_X += P_X 1 (row sums of P)
+                                        mma_ts_f16_elect(tbase + C::col_l(x), tbase + C::col_s(x) + kk * 8u,
+                                                         smem_desc_sw128(base + C::ONES_OFF, 16u, 1024u),
+                                                         C::IDESC_L, (acc | kk) ? 1u : 0u);
+                                }
                             }
                             pph ^= 1;
                             if (t == t1x) mma_commit_elect(bar(C::B_OFULL + x));
@@ -694,15 +713,23 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             tc_fence_after();
                             const uint64_t qd = smem_desc_sw128(base + C::Q_OFF + qs * C::TILE_BYTES, 16u, 1024u);
                             const uint64_t kd = smem_desc_sw128(base + C::KV_OFF + kslot * C::TILE_BYTES, 16u, 1024u);
+                            if constexpr (kMask) {
 #pragma unroll
-                            for (int kk = 0; kk < C::QK_STEPS; ++kk) {
-                                const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
-                                if constexpr (kFP8)
-                                    mma_ss_f8_elect(tbase + C::col_s(x), qd + off, kd + off,
-                                                    C::IDESC_QK, kk > 0 ? 1u : 0u);
-                                else
-                                    mma_ss_f16_elect(tbase + C::col_s(x), qd + off, kd + off,
-                                                     C::IDESC_QK, kk > 0 ? 1u : 0u);
+                                for (int kk = 0; kk < C::QK_STEPS; kk += 4)
+                                    mma_ss_f16_elect4<2, 2>(tbase + C::col_s(x), qd + (kk >> 2) * (C::CHUNK_BYTES >> 4),
+                                                            kd + (kk >> 2) * (C::CHUNK_BYTES >> 4), C::IDESC_QK,
+                                                            kk > 0 ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+                                    const uint32_t off = ((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32u) >> 4;
+                                    if constexpr (kFP8)
+                                        mma_ss_f8_elect(tbase + C::col_s(x), qd + off, kd + off,
+                                                        C::IDESC_QK, kk > 0 ? 1u : 0u);
+                                    else
+                                        mma_ss_f16_elect(tbase + C::col_s(x), qd + off, kd + off,
+                                                         C::IDESC_QK, kk > 0 ? 1u : 0u);
+                                }
                             }
                             mma_commit_elect(bar(C::B_SFULL + x));
                             // (interval masks: the slot becomes O's stage)
