@@ -395,6 +395,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     // tokens, causal, N8192 B2 H32: 129 us, chosen slots 134).
     constexpr bool kStaged = kMask && C::kOStage;
     constexpr bool kSlots = kStaged && !kBias;
+    // Interval masks: one commit releases a step's K tile and the V tile before it, so
+    // a unit's last V tile with the next one's first K (N8192 B2 H32 d128, one document:
+    // 716 us with two commits, 705; documents of 256 in both directions 91 and 93).
+    constexpr bool kPairs = kMask;
     // Interval masks: every unit, the first too, comes through the slots, as the
     // record that the producer publishes.
     const volatile int4 *rec_slot = reinterpret_cast<const volatile int4 *>(gbase + C::REC_OFF);
@@ -568,7 +572,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const int j = U.jhi - 1 - t;
                     if (kMask && t == max(0, U.T - 2)) ask();
                     for (int kv = 0; kv < 2; ++kv) {
-                        ok = mbar_wait(bar(C::B_KVEMPTY + slot), phase ^ 1, w, 2);
+                        // (kPairs: V's slot is released with the K tile that follows it)
+                        if (kPairs && kv) ok = mbar_wait(bar(C::B_KVEMPTY + (slot + 1) % C::NSTAGE),
+                                                         slot + 1 == C::NSTAGE ? phase : phase ^ 1, w, 2);
+                        else ok = mbar_wait(bar(C::B_KVEMPTY + slot), phase ^ 1, w, 2);
                         if (!ok) break;
                         mbar_arrive_expect_tx(bar(C::B_KVFULL + slot), C::TILE_BYTES);
                         const CUtensorMap *tm = kv ? &tm_v : &tm_k;
@@ -741,7 +748,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                          step_x(1, U.t0[1], kExt ? U.t1[1] : U.T, qs1, qp1, un1, pph1);
                     if (!ok) break;
                     if (has_k) mma_commit_elect(bar(C::B_KVEMPTY + kslot));
-                    if (has_v) mma_commit_elect(bar(C::B_KVEMPTY + vslot));
+                    if (has_v && !kPairs) mma_commit_elect(bar(C::B_KVEMPTY + vslot));
                 }
                 un0 += U.act[0] ? 1 : 0;
                 un1 += U.act[1] ? 1 : 0;
