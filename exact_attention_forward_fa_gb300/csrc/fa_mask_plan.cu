@@ -3,7 +3,8 @@
 // all layers.  Each token finds its document by bisection of the offsets; three
 // further blocks a sequence sort the unit lists by their number of tiles (counting
 // sort: which of two equally long units comes first may vary, no result depends on
-// it).
+// it).  Measured (GB300): 6 us for 2 x 8192 tokens (8 under the profiler, cold), the
+// latency of the sorting blocks' dependent loads; it writes 16 bytes a token.
 #include "fa_mask.cuh"
 #include "fa_paged.cuh"
 
