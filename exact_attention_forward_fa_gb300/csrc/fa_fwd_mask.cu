@@ -5,7 +5,7 @@
 // intervals), and only tiles that some row of a warp sees in part pay for a mask, as bits of the
 // columns.  Bound by the tensor core and the softmax chain, at the ends of units by a
 // step's latency.  Measured (GB300, bf16): 2 x 8192 tokens, 32 heads of 128 over 8,
-// documents of 200 to 4000 tokens, causal: 237 us, 951 TFLOP/s of the visible pairs (83 %
+// documents of 200 to 4000 tokens, causal: 237 to 241 us, 935 to 951 TFLOP/s of the visible pairs (83 %
 // of the computed tiles' elements); one document 702 us, 1567; fp16, 4 x 4001, 32 heads
 // of 64, prefixes: 286 us, 684.
 #include "fa_launch.cuh"

@@ -2,7 +2,7 @@
 // In a tile beside the diagonal one the bias is linear in the column: four packed pairs
 // start at b0 + bs c and step by eight columns, one packed addition for two scores
 // (6 % of a long document's time); on the diagonal tile |i - j| is formed for each.
-// Measured (GB300, bf16): 16384 tokens, 16 heads of 128, causal: 710 to 735 us, 1500 to 1550
+// Measured (GB300, bf16): 16384 tokens, 16 heads of 128, causal: 710 to 748 us, 1470 to 1550
 // TFLOP/s, bound as the forward without a bias.
 #include "fa_launch.cuh"
 
