@@ -136,7 +136,9 @@ struct FwdCfg {
                          // dynamic order: the hardware's answer for the next
                          // unit landed, its block index published, slot free
                          B_CLCFULL = B_MMADONE + 1, B_UNIT = B_CLCFULL + 4,
-                         B_CLCEMPTY = B_UNIT + 4, NBAR = B_CLCEMPTY + 4;
+                         B_CLCEMPTY = B_UNIT + 4,
+                         // interval masks: a group's warps have written O to its stage
+                         B_STAGED = B_CLCEMPTY + 4, NBAR = B_STAGED + 2;
     static constexpr int CLC_DEPTH = 4;          // units the producer may run ahead
     static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;
     // 16 B per answer, 16-byte aligned (the answer's store and its 128-bit load)
@@ -424,6 +426,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
             mbar_init(bar(C::B_PFULL + x), 4);
             mbar_init(bar(C::B_OFULL + x), 1);
             mbar_init(bar(C::B_OEMPTY + x), 4);
+            if (kStaged) mbar_init(bar(C::B_STAGED + x), 4);
         }
         for (int s = 0; s < C::NSTAGE; ++s) {
             mbar_init(bar(C::B_KVFULL + s), 1);
@@ -773,7 +776,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
         // [-1, 1], scaled to log2 units by c log2(e).
         const float sc_pre = kCap ? a.sc_pre : 0.f;
         const float sl2 = kCap ? a.sc_post : a.scale_log2;
-        uint32_t sph = 0, oph = 0;
+        uint32_t sph = 0, oph = 0, stph = 0;
         // O rows are D * 2 (partials D * 4) bytes apart, a multiple of 32, so
         // 32-byte stores are aligned everywhere when the base is; the API
         // promises only 16 bytes, and 16-byte stores serve that case.
@@ -1298,8 +1301,17 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         *reinterpret_cast<uint4 *>(orow + (ch >> 3) * C::CHUNK_BYTES + (((ch & 7) ^ (row & 7)) << 4)) =
                             make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
+                    // The group's first warp stores what all four have written.  A bounded
+                    // wait: a warp that gave up (fetch, O above) arrives no more, and a
+                    // named barrier would hold the others for ever.
                     fence_proxy_async_smem();
-                    asm volatile("barrier.sync %0, 128;" :: "r"(1 + x) : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_STAGED + x));
+                    if ((warp & 3) == 0) {
+                        ok = mbar_wait_warp(bar(C::B_STAGED + x), stph, w, 24);
+                        if (!ok) break;
+                    }
+                    stph ^= 1;
                     if ((tid & 127) == 0) {
 #pragma unroll
                         for (int c = 0; c < C::NCH; ++c)
