@@ -433,6 +433,16 @@ __device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, 
     fence_proxy_async_smem();
 }
 
+// The rows' statistics, as the dK/dV kernel reads them.  Interval masks: it may begin
+// while the kernel that writes them still runs, and the read-only path (ld.global.nc)
+// is for data that nobody writes while a kernel runs; plain loads, which stay behind
+// grid_wait()'s memory clobber.
+template <bool kMask, class T>
+__device__ __forceinline__ T ws_load(const T *p) {
+    if constexpr (kMask) return *p;
+    else return __ldg(p);
+}
+
 // Bits of the columns [lo, hi) of 32.
 __device__ __forceinline__ uint32_t column_bits(int lo, int hi) {
     auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
@@ -1319,10 +1329,10 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else {
         // =================== elementwise group (warps 0-7) ===================
         if constexpr (kMask) {
-            // This grid may have begun before the statistics' kernel ended.  Once it
-            // has, and every CTA of this grid has begun (or been taken over), the dQ
-            // kernel's may begin on SMs that run out of key tiles; it reads nothing that
-            // this one writes.
+            // This grid may have begun before the statistics' kernel ended: nothing of the
+            // workspace is read ahead of this wait (ws_load).  Once it has ended, and every
+            // CTA of this grid has begun (or been taken over), the dQ kernel's may begin on
+            // SMs that run out of key tiles; it reads nothing that this one writes.
             grid_wait();
             if (warp == 0) grid_launch_dependents();
         }
@@ -1422,7 +1432,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const int i1 = i + 1 < qhi_t ? i + 1 : i0, hq1 = i1 == i0 ? hq + 1 : hq;
                     const size_t w1 = (static_cast<size_t>(U.b) * a.H + hq1) * a.NP + i1 * 128 + col0 +
                                       (lane & 7) * 8;
-                    touched = __ldg((lane < 8 ? a.ws_l : a.ws_d) + w1);
+                    touched = ws_load<kMask>((lane < 8 ? a.ws_l : a.ws_d) + w1);
                 }
                 // this tile's LSE2, loaded before the wait for S^T so the
                 // loads overlap it (D stays in the loop: 64 more registers
@@ -1432,7 +1442,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 float4 lse_v[16];
                 if constexpr (!kCap) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) lse_v[c] = __ldg(lse4 + c);
+                    for (int c = 0; c < 16; ++c) lse_v[c] = ws_load<kMask>(lse4 + c);
                 }
                 // ---- P^T = exp2(S^T c - LSE2[q]) ----
                 ok = mbar_wait(bar(C::st_bar(stn)), C::st_par(stn), w, 100);
@@ -1526,7 +1536,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 } else {
 #pragma unroll
                     for (int c = 0; c < 64; c += 4) {
-                        const float4 l4 = kCap ? __ldg(lse4 + c / 4) : lse_v[c / 4];
+                        const float4 l4 = kCap ? ws_load<kMask>(lse4 + c / 4) : lse_v[c / 4];
                         const float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2,
                                                 make_float2(-l4.x, -l4.y));
                         const float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2,
@@ -1571,7 +1581,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
-                    const float4 d4 = __ldg(dd4 + c / 4);
+                    const float4 d4 = ws_load<kMask>(dd4 + c / 4);
                     const float2 g01 = __fadd2_rn(
                         make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])),
                         make_float2(-d4.x, -d4.y));
@@ -1581,7 +1591,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     float2 p01 = make_float2(pf[c], pf[c + 1]), p23 = make_float2(pf[c + 2], pf[c + 3]);
                     if constexpr (kCap) {
                         // P again from t, times dS/du = 1 - t^2
-                        const float4 l4 = __ldg(lse4 + c / 4);
+                        const float4 l4 = ws_load<kMask>(lse4 + c / 4);
                         const float2 x01 = __ffma2_rn(p01, c2, make_float2(-l4.x, -l4.y));
                         const float2 x23 = __ffma2_rn(p23, c2, make_float2(-l4.z, -l4.w));
                         const float2 t01 = __ffma2_rn(make_float2(-p01.x, -p01.y), p01, make_float2(1.f, 1.f));

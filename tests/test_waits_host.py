@@ -40,3 +40,14 @@ def test_roles_meet_outside_their_branches(path):
     for line in code(path).splitlines():
         if "__syncthreads()" in line and "regs_" not in line:
             assert len(line) - len(line.lstrip()) <= 8, line
+
+
+def test_statistics_are_read_as_written_data():
+    """The masked dK/dV kernel may begin while the kernel that writes ws_l and ws_d runs: it reads them with plain loads
+    behind its wait (the read-only path is for data that nobody writes meanwhile)."""
+    text = code(os.path.join(_build.CSRC, "fa_bwd_kernel.cuh"))
+    kernel = text[text.index("fa_bwd_dkdv_kernel("):]
+    reads = re.findall(r"(\w+(?:<\w+>)?)\(\s*\(?(?:lse4|dd4|a\.ws_[ld]|lane < 8 \? a\.ws_l)", kernel)
+    assert len(reads) >= 4 and set(reads) == {"ws_load<kMask>"}, reads
+    body = text[text.index("T ws_load("):]
+    assert re.match(r"T ws_load\(const T \*p\) \{\s*if constexpr \(kMask\) return \*p;", body)
