@@ -401,6 +401,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
     // a unit's last V tile with the next one's first K (N8192 B2 H32 d128, one document:
     // 716 us with two commits, 705; documents of 256 in both directions 91 and 93).
     constexpr bool kPairs = kMask;
+    static_assert(!kPairs || C::NSTAGE % 2 == 0, "a K tile and the V tile behind it lie in neighbouring stages");
     // Interval masks: every unit, the first too, comes through the slots, as the
     // record that the producer publishes.
     const volatile int4 *rec_slot = reinterpret_cast<const volatile int4 *>(gbase + C::REC_OFF);
