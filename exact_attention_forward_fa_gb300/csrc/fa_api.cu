@@ -1077,6 +1077,13 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
 
 // ---- masks of documents and prefixes ----
 
+// Whether two ranges of bytes share some (NULL shares none).
+static bool ranges_meet(const void *x, long long nx, const void *y, long long ny) {
+    if (!x || !y || nx < 1 || ny < 1) return false;
+    const intptr_t a = reinterpret_cast<intptr_t>(x), b = reinterpret_cast<intptr_t>(y);
+    return a < b + ny && b < a + nx;
+}
+
 long long fa_mask_plan_bytes(int B, int N) {
     if (B < 1 || N < 1 || B > 65535 || N > (1 << 30)) return -1;
     return static_cast<long long>(fa::mask_plan_layout(B, N, nullptr, nullptr));
@@ -1094,6 +1101,12 @@ fa_status fa_mask_plan(const int32_t *docs, const int32_t *prefix, void *plan, i
     DeviceInfo *dev = nullptr;
     fa_status st = get_device(&dev);
     if (st != FA_OK) return st;
+    const long long bytes = static_cast<long long>(fa::mask_plan_layout(B, N, nullptr, nullptr)), at = 4ll * B * N,
+                    nd = 4ll * B * (n_docs + 1ll), np = 4ll * B * n_docs;
+    if (ranges_meet(plan, bytes, docs, nd) || ranges_meet(plan, bytes, prefix, np) ||
+        ranges_meet(plan, bytes, positions, at) || ranges_meet(positions, at, docs, nd) ||
+        ranges_meet(positions, at, prefix, np))
+        return FA_ERR_INVALID_ARG;
     fa::MaskPlanArgs a;
     a.docs = docs;
     a.prefix = prefix;
@@ -1121,15 +1134,26 @@ static bool rows_overlap(const void *x, long long wx, long long sx, const void *
     return off < 2 * wx || off + 2 * wy > row;
 }
 
-// Whether the contiguous output o [B][N][heads][d] shares memory with q, k or v
-// (a kernel reads them while another CTA writes).
-static bool masked_overlap(const void *o, int heads, const void *q, long long q_stride, const void *k,
-                           long long k_stride, const void *v, long long v_stride, int B, int H,
+// Whether an output of n bytes shares memory with q, k or v (a kernel reads them while
+// another CTA writes), or with the plan, the slopes or the sinks.  o: n = 0, the
+// contiguous [B][N][heads][d].
+static bool masked_overlap(const void *out, int heads, long long n, const void *q, long long q_stride,
+                           const void *k, long long k_stride, const void *v, long long v_stride,
+                           const void *plan, const float *slopes, const float *sinks, int B, int H,
                            int H_kv, int N, int d) {
     const long long T = static_cast<long long>(B) * N, w = static_cast<long long>(heads) * d;
     const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d;
-    return rows_overlap(o, w, w, q, wq, q_stride, T) || rows_overlap(o, w, w, k, wk, k_stride, T) ||
-           rows_overlap(o, w, w, v, wk, v_stride, T);
+    const long long bytes = n ? n : 2 * T * w;
+    const long long h4 = 4ll * H;
+    if (ranges_meet(out, bytes, plan, static_cast<long long>(fa::mask_plan_layout(B, N, nullptr, nullptr))) ||
+        ranges_meet(out, bytes, slopes, h4) || ranges_meet(out, bytes, sinks, h4))
+        return true;
+    if (n)
+        return ranges_meet(out, n, q, 2 * ((T - 1) * q_stride + wq)) ||
+               ranges_meet(out, n, k, 2 * ((T - 1) * k_stride + wk)) ||
+               ranges_meet(out, n, v, 2 * ((T - 1) * v_stride + wk));
+    return rows_overlap(out, w, w, q, wq, q_stride, T) || rows_overlap(out, w, w, k, wk, k_stride, T) ||
+           rows_overlap(out, w, w, v, wk, v_stride, T);
 }
 
 // What the forward and the backward on a mask plan check of their sizes.
@@ -1170,7 +1194,12 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
         (reinterpret_cast<uintptr_t>(lse) & 3u))
         return FA_ERR_MISALIGNED;
-    if (masked_overlap(o, H, q, q_stride, k, k_stride, v, v_stride, B, H, H_kv, N, d)) return FA_ERR_INVALID_ARG;
+    const long long lse_bytes = 4ll * B * H * N;
+    if (masked_overlap(o, H, 0, q, q_stride, k, k_stride, v, v_stride, plan, slopes, sinks, B, H, H_kv, N, d) ||
+        masked_overlap(lse, 0, lse_bytes, q, q_stride, k, k_stride, v, v_stride, plan, slopes, sinks, B, H, H_kv, N,
+                       d) ||
+        ranges_meet(lse, lse_bytes, o, 2ll * B * N * H * d))
+        return FA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
 
@@ -1225,19 +1254,27 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
         return FA_ERR_MISALIGNED;
     const long long T = static_cast<long long>(B) * N, wq = static_cast<long long>(H) * d,
                     wk = static_cast<long long>(H_kv) * d;
-    const struct { const void *p; int heads; } outs[3] = {{dq, H}, {dk, H_kv}, {dv, H_kv}};
-    for (int i = 0; i < 3; ++i) {
-        const long long w = i == 0 ? wq : wk;
-        if (masked_overlap(outs[i].p, outs[i].heads, q, q_stride, k, k_stride, v, v_stride, B, H, H_kv, N, d) ||
-            rows_overlap(outs[i].p, w, w, o, wq, wq, T) || rows_overlap(outs[i].p, w, w, dout, wq, wq, T))
-            return FA_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j) {
-            const long long wj = j == 0 ? wq : wk;
-            if (rows_overlap(outs[i].p, w, w, outs[j].p, wj, wj, T)) return FA_ERR_INVALID_ARG;
-        }
-    }
+    // what the call writes, in bytes (heads: a tensor of tokens): every part apart from
+    // the inputs and from the other parts
+    const long long n_t128 = (static_cast<long long>(N) + 127) / 128 * 128;
+    const struct { const void *p; int heads; long long n; } outs[5] = {
+        {dq, H, 2 * T * wq}, {dk, H_kv, 2 * T * wk}, {dv, H_kv, 2 * T * wk}, {dsinks, 0, 4ll * H},
+        {workspace, 0, 8 * n_t128 * B * H}};
+    auto shares = [&](int i) {
+        if (masked_overlap(outs[i].p, outs[i].heads, outs[i].heads ? 0 : outs[i].n, q, q_stride, k, k_stride, v,
+                           v_stride, plan, slopes, sinks, B, H, H_kv, N, d) ||
+            ranges_meet(outs[i].p, outs[i].n, o, 2 * T * wq) || ranges_meet(outs[i].p, outs[i].n, dout, 2 * T * wq) ||
+            ranges_meet(outs[i].p, outs[i].n, lse, 4 * T * H))
+            return true;
+        for (int j = 0; j < i; ++j)
+            if (ranges_meet(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+        return false;
+    };
+    for (int i = 0; i < 4; ++i)
+        if (shares(i)) return FA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
+    if (shares(4)) return FA_ERR_INVALID_ARG;                // (the workspace)
 
     fa::BwdLaunch L;
     std::memset(&L, 0, sizeof(L));
@@ -1394,11 +1431,20 @@ fa_status fa_paged_rope_append(const void *q, const void *k, const void *v, void
     if (!aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
         (reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
         return FA_ERR_MISALIGNED;
-    if (rows_overlap(q_out, static_cast<long long>(H) * d, q_out_stride, v, static_cast<long long>(H_kv) * d,
-                     kv_stride, total_q))
+    // the pages are outputs: apart from the rows and from one another
+    const long long wq = static_cast<long long>(H) * d, wk = static_cast<long long>(H_kv) * d,
+                    wp = wk * page_size, pool = 2 * ((n_pages - 1) * page_stride + wp);
+    auto pages_meet = [&](const void *rows, long long w, long long stride) {
+        const long long n = 2 * ((total_q - 1) * stride + w);
+        return total_q > 0 && (ranges_meet(rows, n, k_pages, pool) || ranges_meet(rows, n, v_pages, pool));
+    };
+    if (rows_overlap(q_out, wq, q_out_stride, v, wk, kv_stride, total_q) || pages_meet(q_out, wq, q_out_stride) ||
+        pages_meet(k, wk, kv_stride) || pages_meet(v, wk, kv_stride))
         return FA_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if ((st = get_device(&dev)) != FA_OK) return st;
+    if (pages_meet(q, wq, q_stride) || rows_overlap(k_pages, wp, page_stride, v_pages, wp, page_stride, n_pages))
+        return FA_ERR_INVALID_ARG;
     if (total_q == 0) return FA_OK;
     a.v = v;
     a.v_stride = kv_stride / 8;

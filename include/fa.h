@@ -545,8 +545,8 @@ fa_status fa_paged_evict(void *k_pages, void *v_pages, const float *scores,
  *     O = softmax(S) V, LSE = log sum exp(S)      (over the visible keys)
  *
  * A row that sees nothing gives O = 0, LSE = -inf, and its gradients are 0.
- * Outputs share no memory with q, k, v, o, dout or one another
- * (FA_ERR_INVALID_ARG).
+ * What a call writes (the workspace too) shares no memory with what it reads or
+ * with the rest that it writes (FA_ERR_INVALID_ARG).
  */
 
 /*
@@ -622,8 +622,8 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
  *   FA_ERR_UNSUPPORTED).  Strides are elements between tokens, multiples of 8,
  *   at least the row's width; a token's [heads][d] is contiguous.  Pointers
  *   16-byte aligned.  An output is its input itself (same pointer and stride)
- *   or shares no element with any input or other output, else
- *   FA_ERR_INVALID_ARG.
+ *   or shares no element with q, k, v or any other output (the pages are
+ *   outputs), else FA_ERR_INVALID_ARG.
  */
 
 /*
