@@ -1502,14 +1502,21 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if constexpr (kMask) {
                     // (two copies: the rare one does without packed arithmetic)
                     if (whole) {
-                        BiasCols bc(beta, d0, i < U.m, 0.f);
+                        // (the columns step by their distances, which are exact, and the
+                        // bias joins the LSE in one FMA: both may be large, each column
+                        // with an LSE of its own)
+                        const float bs = i < U.m ? -beta : beta;
+                        const float2 bs2 = make_float2(bs, bs), four = make_float2(-4.f, -4.f);
+                        float2 even = make_float2(d0, d0 - 1.f), odd = make_float2(d0 - 2.f, d0 - 3.f);
 #pragma unroll
                         for (int c = 0; c < 64; c += 4) {
                             const float4 l4 = lse_v[c / 4];
                             float2 n01 = make_float2(-l4.x, -l4.y), n23 = make_float2(-l4.z, -l4.w);
                             if constexpr (kBias) {
-                                n01 = __fadd2_rn(n01, bc.next(c));
-                                n23 = __fadd2_rn(n23, bc.next(c + 2));
+                                n01 = __ffma2_rn(even, bs2, n01);
+                                n23 = __ffma2_rn(odd, bs2, n23);
+                                even = __fadd2_rn(even, four);
+                                odd = __fadd2_rn(odd, four);
                             }
                             const float2 x01 = __ffma2_rn(make_float2(pf[c], pf[c + 1]), c2, n01);
                             const float2 x23 = __ffma2_rn(make_float2(pf[c + 2], pf[c + 3]), c2, n23);

@@ -1013,9 +1013,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const float2 c2 = make_float2(sl2, sl2);
                     const bool masked = __any_sync(0xffffffffu, lim < 128 || llo > 0);
                     // Distance bias, -beta |i - j|: in a tile before or behind the
-                    // diagonal one it is linear in the column, b0 + bs c.
+                    // diagonal one it is linear in the column, bs (ahead + c).  What
+                    // the distance of the tile adds joins the reference in one FMA,
+                    // so that the score less the reference is rounded at its own size,
+                    // not at that of a far tile's bias (or of a negative slope's LSE).
                     const float bs = kBias ? (j < mt ? beta : -beta) : 0.f;
-                    const float b0 = kBias ? bs * static_cast<float>(j * 128 - qpos) : 0.f;
+                    const float ahead = kBias && j != mt ? static_cast<float>(j * 128 - qpos) : 0.f;
                     bool done = !masked && !(kBias && j == mt) && __all_sync(0xffffffffu, r != -INFINITY);
                     if (done) {
                         load_s();
@@ -1023,10 +1026,11 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         e_b = e_a;
                         const float2 nr2 = make_float2(-r, -r);
                         const float2 step = make_float2(8.f * bs, 8.f * bs);
+                        const float b0 = __fmaf_rn(bs, ahead, -r);
                         float2 bc[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0 - r), __fmaf_rn(bs, 2.f * i + 1.f, b0 - r));
+                            bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0), __fmaf_rn(bs, 2.f * i + 1.f, b0));
 #pragma unroll
                         for (int c = 0; c < 128; c += 4) {
                             float2 &b01 = bc[(c >> 1) & 3], &b23 = bc[((c >> 1) + 1) & 3];
@@ -1064,7 +1068,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                             }
                         }
                         if constexpr (kBias) {
-                            // biased scores in log2 units
+                            // biased scores in log2 units, less bs ahead
                             if (j == mt) {
                                 const float d0 = static_cast<float>(row);
 #pragma unroll
@@ -1074,8 +1078,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                                 const float2 step = make_float2(8.f * bs, 8.f * bs);
                                 float2 bc[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    bc[i] = make_float2(__fmaf_rn(bs, 2.f * i, b0), __fmaf_rn(bs, 2.f * i + 1.f, b0));
+                                for (int i = 0; i < 4; ++i) bc[i] = make_float2(bs * (2.f * i), bs * (2.f * i + 1.f));
 #pragma unroll
                                 for (int c = 0; c < 128; c += 2) {
                                     float2 &bq = bc[(c >> 1) & 3];
@@ -1086,7 +1089,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                                 }
                             }
                         }
-                        const float bnew = kBias ? row_max() : row_max() * sl2;
+                        const float bnew = kBias ? __fmaf_rn(bs, ahead, row_max()) : row_max() * sl2;
                         // A bias that rises towards the tiles that follow would move the
                         // reference every few of them: it goes ahead by what is left of
                         // the rise, up to what P's type bears below 1 (bf16 has FP32's
@@ -1101,8 +1104,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                         if (r == -INFINITY) rn = bnew + lead;
                         else { rn = (bnew > r + C::TAU) ? bnew + lead : r; corr = ex2_approx(r - rn); }
                         need = (r != -INFINITY) && (rn != r);
-                        const float rs = rn == -INFINITY ? 0.f : rn;
-                        const float2 nr2 = make_float2(-rs, -rs);
+                        const float nrs = rn == -INFINITY ? 0.f : __fmaf_rn(bs, ahead, -rn);
+                        const float2 nr2 = make_float2(nrs, nrs);
                         e_a = make_float2(0.f, 0.f);
                         e_b = e_a;
 #pragma unroll

@@ -343,12 +343,13 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 // first tile or when a row's sum got too large (fa_fwd_kernel.cuh)
                 bool keep = __all_sync(0xffffffffu, r != -INFINITY);
                 if constexpr (kBias) {
-                    // Distance bias: linear in the column, b0 + bs c, where all keys that a
-                    // row sees here lie on one side of it; else with |k0 + c - pos|.
+                    // Distance bias: linear in the column, bs (ahead + c), where all keys that
+                    // a row sees here lie on one side of it; else with |k0 + c - pos|.  The
+                    // tile's distance joins the reference (fa_fwd_kernel.cuh).
                     const bool left = khi <= pos + 1 || k0 + 127 <= pos;
                     const bool mixed = __any_sync(0xffffffffu, valid && !left && k0 < pos);
                     const float bs = left ? beta : -beta;
-                    const float b0 = bs * static_cast<float>(k0 - pos);
+                    const float ahead = mixed ? 0.f : static_cast<float>(k0 - pos);
                     const float2 step = make_float2(8.f * bs, 8.f * bs);
                     float2 bc[4];
                     // against the current reference where all rows see the whole tile
@@ -361,9 +362,10 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         tmem_ld_wait();
                         e_a = make_float2(0.f, 0.f);
                         e_b = e_a;
+                        const float b0 = __fmaf_rn(bs, ahead, -r);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0 - r), __fmaf_rn(bs, 2.f * q + 1.f, b0 - r));
+                            bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0), __fmaf_rn(bs, 2.f * q + 1.f, b0));
 #pragma unroll
                         for (int cc = 0; cc < 128; cc += 4) {
                             float2 &b01 = bc[(cc >> 1) & 3], &b23 = bc[((cc >> 1) + 1) & 3];
@@ -398,7 +400,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                     if (!(m & (1u << cc))) sf[32 * w32 + cc] = -INFINITY;
                             }
                         }
-                        // biased scores in log2 units, their maximum
+                        // biased scores in log2 units, less bs ahead, and their maximum
                         if (mixed) {
                             const float d0 = static_cast<float>(pos - k0);
 #pragma unroll
@@ -406,8 +408,7 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 sf[cc] = __fmaf_rn(sf[cc], sl2, -beta * fabsf(d0 - static_cast<float>(cc)));
                         } else {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                bc[q] = make_float2(__fmaf_rn(bs, 2.f * q, b0), __fmaf_rn(bs, 2.f * q + 1.f, b0));
+                            for (int q = 0; q < 4; ++q) bc[q] = make_float2(bs * (2.f * q), bs * (2.f * q + 1.f));
 #pragma unroll
                             for (int cc = 0; cc < 128; cc += 2) {
                                 float2 &bq = bc[(cc >> 1) & 3];
@@ -417,14 +418,14 @@ fa_paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 bq = __fadd2_rn(bq, step);
                             }
                         }
-                        const float bnew = row_max_of<128>(sf);
+                        const float bnew = __fmaf_rn(bs, ahead, row_max_of<128>(sf));
                         if (valid) {
                             if (r == -INFINITY) rn = bnew;
                             else { rn = (bnew > r + C::TAU) ? bnew : r; corr = ex2_approx(r - rn); }
                             need = (r != -INFINITY) && (rn != r);
                         }
-                        const float rs = rn == -INFINITY ? 0.f : rn;
-                        const float2 nr2 = make_float2(-rs, -rs);
+                        const float nrs = rn == -INFINITY ? 0.f : __fmaf_rn(bs, ahead, -rn);
+                        const float2 nr2 = make_float2(nrs, nrs);
                         e_a = make_float2(0.f, 0.f);
                         e_b = e_a;
 #pragma unroll

@@ -380,8 +380,10 @@ fa_paged_token_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                     for (int q = 0; q < 4; ++q) {
                         const int n = n4 + q;
                         const bool first_seen = (unseen & (1u << n)) != 0;
-                        float v = fmaf(__uint_as_float(s[n]), sl2, first_seen ? 0.f : -rv[q]);
+                        // (the bias joins the reference first: both may be large)
+                        float v = first_seen ? 0.f : -rv[q];
                         if constexpr (kBias) v = fmaf(-beta[n], fabsf(ahead - place[n]), v);
+                        v = fmaf(__uint_as_float(s[n]), sl2, v);
                         v = n >= ca && n < cb ? v : -INFINITY;
                         big |= v > C::CAP || (first_seen && v != -INFINITY);
                         s[n] = __float_as_uint(v);
