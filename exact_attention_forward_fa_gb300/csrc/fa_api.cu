@@ -1320,11 +1320,14 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
     const uint64_t gd = (static_cast<uint64_t>(B) * H * N + rows_per_cta - 1) / rows_per_cta;
     const uint64_t gcap = 8ull * static_cast<uint64_t>(dev->sm_count);
     L.grid_delta = static_cast<int>(gd < gcap ? gd : gcap);
+    L.args.v = v;
+    L.args.v_stride = v_stride;
+    L.args.parts = L.grid_delta;
     L.d = d;
     L.bf16 = dtype == FA_BF16;
     L.stream = static_cast<cudaStream_t>(stream);
     cudaError_t e = slopes ? fa::launch_bwd_mask_bias(L) : fa::launch_bwd_mask(L);
-    if (e == cudaSuccess && dsinks) e = fa::launch_bwd_dsink(L.args, sinks, dsinks, L.stream);
+    if (e == cudaSuccess && dsinks) e = fa::launch_bwd_dsink(L.args, sinks, dsinks, L.stream, !L.bf16);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -18,6 +18,8 @@ cudaError_t launch_bwd_win(const BwdLaunch &L) {
 // logit's gradient sums that over the rows of every batch.  One CTA per head
 // reduces in a fixed order (thread partials, then a tree), so the result is
 // the same on every run.  Workspace padding rows have LSE2 = +inf: P = 0.
+// kLse: LSE from the forward's, the workspace's being less a scale (fa_bwd_kernel.cuh).
+template <bool kLse>
 __global__ void __launch_bounds__(512)
 fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
     const int h = blockIdx.x;
@@ -32,7 +34,18 @@ fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
         const float4 *d4 = reinterpret_cast<const float4 *>(a.ws_d + base);
 #pragma unroll 4
         for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-            const float4 l = __ldg(l4 + i), dd = __ldg(d4 + i);
+            const float4 dd = __ldg(d4 + i);
+            float4 l;
+            if constexpr (kLse) {
+                const float *row = a.lse + (static_cast<size_t>(b) * a.H + h) * a.N;
+                auto at = [&](int n) {
+                    const float x = n < a.N ? __ldg(row + n) : -INFINITY;
+                    return x == -INFINITY ? INFINITY : to_log2(x);
+                };
+                l = make_float4(at(4 * i), at(4 * i + 1), at(4 * i + 2), at(4 * i + 3));
+            } else {
+                l = __ldg(l4 + i);
+            }
             acc[0] = fmaf(-ex2_approx(sg - l.x), dd.x, acc[0]);
             acc[1] = fmaf(-ex2_approx(sg - l.y), dd.y, acc[1]);
             acc[2] = fmaf(-ex2_approx(sg - l.z), dd.z, acc[2]);
@@ -50,8 +63,9 @@ fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
 }
 
 cudaError_t launch_bwd_dsink(const BwdArgs &a, const float *sinks, float *dsinks,
-                             cudaStream_t stream) {
-    fa_bwd_dsink_kernel<<<a.H, 512, 0, stream>>>(a, sinks, dsinks);
+                             cudaStream_t stream, bool scaled) {
+    if (scaled) fa_bwd_dsink_kernel<true><<<a.H, 512, 0, stream>>>(a, sinks, dsinks);
+    else fa_bwd_dsink_kernel<false><<<a.H, 512, 0, stream>>>(a, sinks, dsinks);
     return cudaGetLastError();
 }
 

@@ -80,6 +80,11 @@ struct BwdArgs {
     // kBias: the score loses slopes[h] |i - j|.  chunk as for causal units.
     MaskPlan plan;
     const float *slopes;
+    // Interval masks in fp16 (kScale): V's tokens for the bound of dS, and the CTAs
+    // that form it
+    const void *v;
+    long long v_stride;
+    int parts;
 };
 
 // Visible keys [win_klo, win_khi) of query row i (0 <= i < N), and visible
@@ -261,6 +266,45 @@ __device__ __forceinline__ BwdUnit make_bwd_unit(int u, const BwdArgs &a) {
     return U;
 }
 
+// x / y, in 32 bits where they suffice (a 64-bit division is a hundred instructions).
+__device__ __forceinline__ long divide32(long x, int y) {
+    return x >> 32 ? x / y : static_cast<long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+
+// LSE in log2 units, as the main kernels take it; scale_undo gives back what e took off.
+__device__ __forceinline__ float to_log2(float lse) { return __fmul_rn(lse, 1.4426950408889634f); }
+
+// 2^-e for the e of a row whose LSE2 - e is given: the difference is e up to the rounding
+// of LSE2 - e, a fourth at most while |LSE2| < 2^22 (beyond, FP32 scores mean little).
+__device__ __forceinline__ float scale_undo(float lse, float lse2_less_e) {
+    const float d = rintf(__fsub_rn(to_log2(lse), lse2_less_e));
+    return d > 0.f && d <= 15.f ? __int_as_float((127 - static_cast<int>(d)) << 23) : 1.f;
+}
+
+// The larger of each half and the sizes of eight fp16 values, in packed pairs.
+__device__ __forceinline__ uint32_t max_abs_f16(uint32_t m, const uint4 &x) {
+    asm("{\n\t.reg .b32 a, b, c, d;\n\t"
+        "and.b32 a, %1, 0x7fff7fff;\n\tand.b32 b, %2, 0x7fff7fff;\n\t"
+        "and.b32 c, %3, 0x7fff7fff;\n\tand.b32 d, %4, 0x7fff7fff;\n\t"
+        "max.f16x2 a, a, b;\n\tmax.f16x2 c, c, d;\n\tmax.f16x2 a, a, c;\n\tmax.f16x2 %0, %0, a;\n\t}"
+        : "+r"(m) : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w));
+    return m;
+}
+
+// The maxima over a block of 256 threads, in all of them.
+__device__ __forceinline__ float2 cta_max(float2 m, float2 (&warps)[8]) {
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+        m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, w));
+        m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, w));
+    }
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = make_float2(fmaxf(m.x, warps[w].x), fmaxf(m.y, warps[w].y));
+    return m;
+}
+
 // ---------------------------------------------------------------------------
 // Preprocess ("FlashAttention-3 on Hopper", sec. 7.1.2, 7.1.3 and 7.3):
 //   ws_d[b][h][n] = sum_c dO[b][n][h][c] * O[b][n][h][c]   (FP32)
@@ -271,9 +315,22 @@ __device__ __forceinline__ BwdUnit make_bwd_unit(int u, const BwdArgs &a) {
 // parallelism.
 // ---------------------------------------------------------------------------
 // kMask: rows outside every document may hold anything; their D is 0.
+//
+// Interval masks in fp16 (kScale).  P and dS = P o (dP - D) are rounded to fp16 for the
+// products that consume them, and fp16 is spaced by 2^-24 below 2^-14: P of long
+// documents is there (1 / N), and dS falls with N, |dO| and |V| (dO of size 2^-10 and
+// N = 4096: dQ off by 0.5 % in its norm).  So P and with it dS are formed 2^e times as
+// large, e in [0, 15], with LSE2 - e in the place of LSE2 (no step of the tiles' loops),
+// and the gradients are scaled back as they are stored.  P <= 1 and |dP - D| <= 2 d
+// max|dO| max|V| (D is a mean of a row's dP): the largest e with 2^e times that below
+// 65504 / 1.01.  This kernel forms the maxima a CTA (a NaN drops out, an infinity leaves e
+// = 0); fa_bwd_scale_kernel joins them and writes LSE2 - e.  The maxima and e travel in
+// dq, which nobody writes before the dQ kernel: the dK/dV kernel's CTAs read e before they
+// let that one begin, and it has e from LSE2 and the LSE.
 template <int D, bool kBF16, bool kMask = false>
 __global__ void __launch_bounds__(256)
 fa_bwd_delta_kernel(const BwdArgs a) {
+    constexpr bool kScale = kMask && !kBF16;
     constexpr int TPR = D / 8;                       // threads per row
     constexpr int RPW = 32 / TPR;                    // rows per warp pass
     const long n_rows = static_cast<long>(a.B) * a.N * a.H;
@@ -283,15 +340,12 @@ fa_bwd_delta_kernel(const BwdArgs a) {
     const int sub = lane / TPR, part = lane % TPR;
     const uint4 *o4 = reinterpret_cast<const uint4 *>(a.o);
     const uint4 *d4 = reinterpret_cast<const uint4 *>(a.dout);
-    // x / y, in 32 bits where they suffice (a 64-bit division is a hundred instructions)
-    auto divide = [](long x, int y) -> long {
-        return x >> 32 ? x / y : static_cast<long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
-    };
+    uint32_t most_o = 0u, most_v = 0u;               // kScale: |dO|, |V|, as pairs
     for (long base = warp_g * RPW * 4; base < n_rows; base += n_warps * RPW * 4) {
         // row = (b * N + n) * H + h: the pass's first one
-        const long bn0 = divide(base, a.H);
+        const long bn0 = divide32(base, a.H);
         const int h0 = static_cast<int>(base - bn0 * a.H);
-        const long b0 = divide(bn0, a.N);
+        const long b0 = divide32(bn0, a.N);
         const int n0 = static_cast<int>(bn0 - b0 * a.N);
         uint4 ov[4], dv[4];
 #pragma unroll
@@ -314,7 +368,7 @@ fa_bwd_delta_kernel(const BwdArgs a) {
 #pragma unroll
             for (int m = TPR / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
             const long row = base + r * RPW + sub;
-            if (part == 0 && row < n_rows) {
+            if ((kScale || part == 0) && row < n_rows) {
                 int h = h0 + r * RPW + sub, n = n0;      // (a few steps on: no division)
                 long b = b0;
                 while (h >= a.H) {
@@ -327,24 +381,99 @@ fa_bwd_delta_kernel(const BwdArgs a) {
                 if constexpr (kMask) {
                     const int4 lv = __ldg(a.plan.live + b);
                     if (n < lv.x || n >= lv.y) acc = 0.f;
+                    else if constexpr (kScale) most_o = max_abs_f16(most_o, dv[r]);
                 }
-                a.ws_d[(b * a.H + h) * a.NP + n] = acc;
+                if (part == 0) a.ws_d[(b * a.H + h) * a.NP + n] = acc;
             }
         }
     }
     if constexpr (kMask) grid_launch_dependents();
-    const long n_pad = static_cast<long>(a.B) * a.H * a.NP;
-    for (long idx = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n_pad;
-         idx += static_cast<long>(gridDim.x) * blockDim.x) {
-        const long bh = divide(idx, a.NP), n = idx - bh * a.NP;
-        float l2 = INFINITY;
-        if (n < a.N) {
-            const float l = a.lse[bh * a.N + n];
-            l2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-        } else {
-            a.ws_d[idx] = 0.f;
+    if constexpr (kScale) {
+        // V's vectors within the documents, four in flight, then the CTA's maxima
+        const int per = a.H / a.group * TPR;         // vectors of a token
+        const long n_v = static_cast<long>(a.B) * a.N * per, step = n_warps * 32;
+        const uint4 *v4 = reinterpret_cast<const uint4 *>(a.v);
+        for (long idx = warp_g * 32 + lane; idx < n_v; idx += 4 * step) {
+            uint4 x[4];
+            long t[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const long i = idx + r * step;
+                t[r] = i < n_v ? divide32(i, per) : -1;
+                x[r] = t[r] < 0 ? make_uint4(0u, 0u, 0u, 0u) : v4[t[r] * (a.v_stride / 8) + (i - t[r] * per)];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (t[r] < 0) continue;
+                const long b = divide32(t[r], a.N), n = t[r] - b * a.N;
+                const int4 lv = __ldg(a.plan.live + b);
+                if (n >= lv.x && n < lv.y) most_v = max_abs_f16(most_v, x[r]);
+            }
         }
-        a.ws_l[idx] = l2;
+        __shared__ float2 most[8];
+        float o0, o1, v0, v1;
+        unpack2<false>(most_o, o0, o1);
+        unpack2<false>(most_v, v0, v1);
+        const float2 m = cta_max(make_float2(fmaxf(o0, o1), fmaxf(v0, v1)), most);
+        if (threadIdx.x == 0) reinterpret_cast<float2 *>(a.dq)[blockIdx.x] = m;
+    } else {
+        const long n_pad = static_cast<long>(a.B) * a.H * a.NP;
+        for (long idx = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n_pad;
+             idx += static_cast<long>(gridDim.x) * blockDim.x) {
+            const long bh = divide32(idx, a.NP), n = idx - bh * a.NP;
+            float l2 = INFINITY;
+            if (n < a.N) {
+                const float l = a.lse[bh * a.N + n];
+                l2 = l == -INFINITY ? INFINITY : to_log2(l);
+            } else {
+                a.ws_d[idx] = 0.f;
+            }
+            a.ws_l[idx] = l2;
+        }
+    }
+}
+
+// Joins the maxima (kScale, see above): e for the call, and LSE2 - e.  Measured (GB300, 4 x
+// 4096 tokens, 32 heads of 64, documents of 256: 280 us, in bf16 259): V's pass 14 us, at HBM
+// speed, this kernel 6; 2 x 8192, 32 heads of 128 over 8, of 1024: 478 and 470 together.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_scale_kernel(const BwdArgs a) {
+    grid_launch_dependents();
+    // four rows a thread, in one head: their LSE, an input, ahead of the wait
+    const long n4 = static_cast<long>(a.B) * a.H * a.NP / 4, step = static_cast<long>(gridDim.x) * blockDim.x;
+    long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    float l[4];
+    auto load = [&]() {
+        const long bh = divide32(4 * i, a.NP);
+        const int n = static_cast<int>(4 * i - bh * a.NP);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) l[r] = n + r < a.N ? a.lse[bh * a.N + n + r] : -INFINITY;
+        return n;
+    };
+    int n = i < n4 ? load() : 0;
+    grid_wait();
+    float2 *part = reinterpret_cast<float2 *>(a.dq);
+    float2 m = make_float2(0.f, 0.f);
+#pragma unroll 5
+    for (int p = threadIdx.x; p < a.parts; p += blockDim.x) {
+        const float2 x = part[p];
+        m = make_float2(fmaxf(m.x, x.x), fmaxf(m.y, x.y));
+    }
+    __shared__ float2 most[8];
+    m = cta_max(m, most);
+    // 2^e 2 D m.x m.y <= 65504 / 1.01 = 2^15.985; infinities leave 0, zeros 15
+    const float room = floorf((D == 64 ? 8.985f : 7.985f) - (log2f(m.x) + log2f(m.y)));
+    const float e = room > 0.f ? fminf(room, 15.f) : 0.f;    // (a NaN: 0)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int *>(part + a.parts) = static_cast<int>(e);
+    while (i < n4) {
+        float w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            w[r] = l[r] == -INFINITY ? INFINITY : __fsub_rn(to_log2(l[r]), e);
+            if (n + r >= a.N) a.ws_d[4 * i + r] = 0.f;
+        }
+        reinterpret_cast<float4 *>(a.ws_l)[i] = make_float4(w[0], w[1], w[2], w[3]);
+        if ((i += step) < n4) n = load();
     }
 }
 
@@ -436,7 +565,8 @@ __device__ __forceinline__ void zero_outside(uint8_t *tile, int first, int row, 
 // The rows' statistics, as the dK/dV kernel reads them.  Interval masks: it may begin
 // while the kernel that writes them still runs, and the read-only path (ld.global.nc)
 // is for data that nobody writes while a kernel runs; plain loads, which stay behind
-// grid_wait()'s memory clobber.
+// grid_wait()'s memory clobber.  (They cost 1 % on long documents at d = 64: 4 x 4096 tokens,
+// 32 heads, bf16, 1080 us and 1091.)
 template <bool kMask, class T>
 __device__ __forceinline__ T ws_load(const T *p) {
     if constexpr (kMask) return *p;
@@ -984,6 +1114,10 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!ok) break;
             }
             // ---- epilogue: dQ * alpha -> global (this warp's half of the columns) ----
+            float out_scale = a.alpha;
+            if constexpr (kMask && !kBF16)
+                if (grow < a.N)
+                    out_scale *= scale_undo(__ldg(a.lse + (static_cast<size_t>(U.b) * a.H + U.h) * a.N + grow), lse2);
             ok = mbar_wait(bar(C::DQB_DQFULL), dqph, w, 72);
             if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
             dqph ^= 1;
@@ -998,7 +1132,7 @@ fa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::DQB_DQEMPTY));
-            store_cols<D, W, kBF16>(a.dq, a, a.H, U.b, U.h, grow, half * W, dq, a.alpha);
+            store_cols<D, W, kBF16>(a.dq, a, a.H, U.b, U.h, grow, half * W, dq, out_scale);
         }
     }
 
@@ -1049,6 +1183,8 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto bar = [&](int i) -> uint32_t { return base + C::KV_BAR_OFF + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbase + C::KV_MISC_OFF);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(gbase + C::KV_MISC_OFF + 4);
+    constexpr bool kScale = kMask && !kBF16;                // (fa_bwd_delta_kernel)
+    volatile int *scale_slot = reinterpret_cast<volatile int *>(gbase + C::KV_MISC_OFF + 8);   // its e
     // Causal without a window, interval masks: one CTA per unit, running CTAs take over those
     // not yet started (clc_try_cancel).  The producer asks for the next unit
     // once it has issued the current one's loads; the k-th answer goes to
@@ -1179,7 +1315,16 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 load_tile<C::NCH>(&tm_k, base + C::KV_K_OFF, bar(C::KVB_KVFULL), U.h, U.m * 128, U.b);
                 load_tile<C::NCH>(&tm_v, base + C::KV_V_OFF, bar(C::KVB_KVFULL), U.h, U.m * 128, U.b);
                 ++kvn;
-                if (kMask && kvn == 1) grid_wait();          // (the first rows' statistics)
+                if (kMask && kvn == 1) {
+                    grid_wait();                             // (the first rows' statistics)
+                    if constexpr (kScale) {
+                        // e, ahead of the first Q tile, behind which the stores read it;
+                        // then dq may be written (below)
+                        *scale_slot =
+                            *reinterpret_cast<const volatile int *>(reinterpret_cast<const float2 *>(a.dq) + a.parts);
+                        grid_launch_dependents();
+                    }
+                }
                 int qlo_t, qhi_t;
                 query_range(U, qlo_t, qhi_t);
                 // the query heads of this K/V head, each over its query tiles
@@ -1332,9 +1477,10 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // This grid may have begun before the statistics' kernel ended: nothing of the
             // workspace is read ahead of this wait (ws_load).  Once it has ended, and every
             // CTA of this grid has begun (or been taken over), the dQ kernel's may begin on
-            // SMs that run out of key tiles; it reads nothing that this one writes.
+            // SMs that run out of key tiles; it reads nothing that this one writes.  (kScale:
+            // the producer says so, once it has read e from dq.)
             grid_wait();
-            if (warp == 0) grid_launch_dependents();
+            if (!kScale && warp == 0) grid_launch_dependents();
         }
         const int quarter = warp & 3, half = warp >> 2;
         const int row = quarter * 32 + lane;                 // key row of the tile
@@ -1629,6 +1775,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
             accph ^= 1;
             tc_fence_after();
+            const float undo = kScale ? __int_as_float((127 - *scale_slot) << 23) : 1.f;      // 2^-e
             constexpr int W = D / 2;
             uint32_t acc[W];
 #pragma unroll
@@ -1636,7 +1783,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 tmem_ld32(tbase + lane_off + C::KV_COL_DV + half * W + ch * 32,
                           *reinterpret_cast<uint32_t(*)[32]>(&acc[ch * 32]));
             tmem_ld_wait();
-            store_cols<D, W, kBF16>(a.dv, a, a.H / a.group, U.b, U.h, krow, half * W, acc, 1.f);
+            store_cols<D, W, kBF16>(a.dv, a, a.H / a.group, U.b, U.h, krow, half * W, acc, undo);
 #pragma unroll
             for (int ch = 0; ch < W / 32; ++ch)
                 tmem_ld32(tbase + lane_off + C::KV_COL_DK + half * W + ch * 32,
@@ -1645,7 +1792,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::KVB_ACCEMPTY));
-            store_cols<D, W, kBF16>(a.dk, a, a.H / a.group, U.b, U.h, krow, half * W, acc, a.alpha);
+            store_cols<D, W, kBF16>(a.dk, a, a.H / a.group, U.b, U.h, krow, half * W, acc, kScale ? a.alpha * undo : a.alpha);
             if constexpr (!kCap) {
                 if (a.N < 0 && touched_sum == 0.f) a.status[3] = 1u;    // never true: N >= 1
             }

@@ -47,15 +47,22 @@ cudaError_t launch_bwd_inst(const BwdLaunch &L) {
         // on the SMs that the longest key tiles leave idle at the end (288 units of up
         // to 72 steps, d = 64: 296 us one after the other, 272 so).
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(L.grid_kv));
-        cfg.blockDim = dim3(C::NTHREADS);
-        cfg.dynamicSmemBytes = C::KV_SMEM;
+        cfg.blockDim = dim3(256);
         cfg.stream = L.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
+        if constexpr (!kBF16) {
+            // four rows a thread, up to the 1216 CTAs of 256 that fit 152 SMs
+            const long n = (static_cast<long>(L.args.B) * L.args.H * L.args.NP + 1023) / 1024;
+            cfg.gridDim = dim3(static_cast<unsigned>(n < 1216 ? n : 1216));
+            if ((e = cudaLaunchKernelEx(&cfg, fa_bwd_scale_kernel<D>, L.args)) != cudaSuccess) return e;
+        }
+        cfg.gridDim = dim3(static_cast<unsigned>(L.grid_kv));
+        cfg.blockDim = dim3(C::NTHREADS);
+        cfg.dynamicSmemBytes = C::KV_SMEM;
         if ((e = cudaLaunchKernelEx(&cfg, kkv, L.q, L.k, L.v, L.dout, L.args)) != cudaSuccess) return e;
         cfg.gridDim = dim3(static_cast<unsigned>(L.grid));
         cfg.dynamicSmemBytes = C::DQ_SMEM;

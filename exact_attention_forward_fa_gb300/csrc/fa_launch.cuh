@@ -71,9 +71,10 @@ cudaError_t launch_bwd_win_softcap(const BwdLaunch &L);
 cudaError_t launch_bwd_mask(const BwdLaunch &L);
 cudaError_t launch_bwd_mask_bias(const BwdLaunch &L);
 // Gradient of per-head sink logits: dsinks[h] = -sum_{b,i} 2^(sigma_h log2 e
-// - LSE2_i) D_i over the workspace rows of the backward (one CTA per head).
+// - LSE2_i) D_i over the workspace rows of the backward (one CTA per head).  scaled:
+// the workspace holds LSE2 less a scale, and LSE2 comes from the LSE.
 cudaError_t launch_bwd_dsink(const BwdArgs &a, const float *sinks, float *dsinks,
-                             cudaStream_t stream);
+                             cudaStream_t stream, bool scaled = false);
 
 // FP8 pre-pass: persistent CTAs over (b, h, 128-row tile); x arrives by
 // TMA (map {d, H, N, B}, box {d, 1, 128, 1}, no swizzle, rows >= N zero).

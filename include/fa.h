@@ -597,6 +597,11 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
  *          dk and dv sum the gradients of their group's query heads in FP32.
  *   workspace : as fa_bwd.
  *   dsinks : as fa_bwd_ext, or NULL.  The slopes are constants: no gradient.
+ * In fp16, P and dS are formed 2^e times as large, e from 0 to 15 and so that no
+ * dS leaves the type (found on the device from the largest |dout| and |v|), so that
+ * small gradients, small values and long documents keep their digits; the gradients
+ * are scaled back before they are rounded.  (fa_bwd and fa_bwd_ext round P and dS
+ * as they are: below 2^-14 fp16 is spaced by 2^-24.)
  */
 fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void *o,
                         const void *dout, const float *lse, float *workspace,
