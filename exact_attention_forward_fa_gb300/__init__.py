@@ -882,12 +882,12 @@ def mask_plan(docs, N: int, prefix=None, window=(-1, 0), out: MaskPlan | None = 
     else:
         if (out.B, out.N) != (B, N) or out.data.get_device() != at:
             raise ValueError("out is a plan of another shape or device")
-        out.window = window
     rc = load().fa_mask_plan(docs.data_ptr(), None if prefix is None else prefix.data_ptr(),
                              out.data.data_ptr(), out.positions.data_ptr(), B, N, D, left, right,
                              torch._C._cuda_getCurrentRawStream(at))
     if rc != FA_OK:
         raise FaError(rc, "fa_mask_plan")
+    out.window = window
     return out
 
 

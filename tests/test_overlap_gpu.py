@@ -76,3 +76,18 @@ def test_rotated_append_refuses_queries_in_the_pages(gpu_lib):
     assert not pool.any()
     fa.paged_rope_append(q, k, k, k_pages, v_pages, table, kv_len, cu_q, w)
     assert fa.fa_check_status() == fa.FA_OK and pool.any()
+
+
+def test_a_refused_plan_stays_as_it_was(gpu_lib):
+    """A window that is refused leaves the plan's mask and what it says of its window."""
+    N = 300
+    docs = torch.tensor([[0, 120, 290]], dtype=torch.int32, device="cuda")
+    plan = fa.mask_plan(docs, N, window=(17, 3))
+    before = plan.data.clone()
+    for window in ((-2, 0), (5, -3)):
+        with pytest.raises(fa.FaError) as e:
+            fa.mask_plan(docs, N, window=window, out=plan)
+        assert e.value.code == fa.FA_ERR_INVALID_ARG and plan.window == (17, 3)
+    torch.cuda.synchronize()
+    assert torch.equal(plan.data, before)
+    assert fa.mask_plan(docs, N, window=(-1, 0), out=plan) is plan and plan.window == (-1, 0)
