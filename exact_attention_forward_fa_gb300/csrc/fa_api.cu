@@ -1323,6 +1323,7 @@ fa_status fa_bwd_masked(const void *q, const void *k, const void *v, const void 
     L.args.v = v;
     L.args.v_stride = v_stride;
     L.args.parts = L.grid_delta;
+    L.args.dsinks = dsinks;
     L.d = d;
     L.bf16 = dtype == FA_BF16;
     L.stream = static_cast<cudaStream_t>(stream);

@@ -18,8 +18,8 @@ cudaError_t launch_bwd_win(const BwdLaunch &L) {
 // logit's gradient sums that over the rows of every batch.  One CTA per head
 // reduces in a fixed order (thread partials, then a tree), so the result is
 // the same on every run.  Workspace padding rows have LSE2 = +inf: P = 0.
-// kLse: LSE from the forward's, the workspace's being less a scale (fa_bwd_kernel.cuh).
-template <bool kLse>
+// kScaled: the workspace holds LSE2 - e, and dsinks 2^-e (fa_bwd_kernel.cuh).
+template <bool kScaled>
 __global__ void __launch_bounds__(512)
 fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
     const int h = blockIdx.x;
@@ -34,18 +34,7 @@ fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
         const float4 *d4 = reinterpret_cast<const float4 *>(a.ws_d + base);
 #pragma unroll 4
         for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-            const float4 dd = __ldg(d4 + i);
-            float4 l;
-            if constexpr (kLse) {
-                const float *row = a.lse + (static_cast<size_t>(b) * a.H + h) * a.N;
-                auto at = [&](int n) {
-                    const float x = n < a.N ? __ldg(row + n) : -INFINITY;
-                    return x == -INFINITY ? INFINITY : to_log2(x);
-                };
-                l = make_float4(at(4 * i), at(4 * i + 1), at(4 * i + 2), at(4 * i + 3));
-            } else {
-                l = __ldg(l4 + i);
-            }
+            const float4 l = __ldg(l4 + i), dd = __ldg(d4 + i);
             acc[0] = fmaf(-ex2_approx(sg - l.x), dd.x, acc[0]);
             acc[1] = fmaf(-ex2_approx(sg - l.y), dd.y, acc[1]);
             acc[2] = fmaf(-ex2_approx(sg - l.z), dd.z, acc[2]);
@@ -59,7 +48,7 @@ fa_bwd_dsink_kernel(const BwdArgs a, const float *sinks, float *dsinks) {
         if (threadIdx.x < s) part[threadIdx.x] += part[threadIdx.x + s];
         __syncthreads();
     }
-    if (threadIdx.x == 0) dsinks[h] = part[0];
+    if (threadIdx.x == 0) dsinks[h] = kScaled ? part[0] * dsinks[h] : part[0];
 }
 
 cudaError_t launch_bwd_dsink(const BwdArgs &a, const float *sinks, float *dsinks,

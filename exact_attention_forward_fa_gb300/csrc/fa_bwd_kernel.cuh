@@ -85,6 +85,7 @@ struct BwdArgs {
     const void *v;
     long long v_stride;
     int parts;
+    float *dsinks;         // 2^-e goes there (or NULL), for the sinks' gradient
 };
 
 // Visible keys [win_klo, win_khi) of query row i (0 <= i < N), and visible
@@ -464,7 +465,11 @@ __global__ void __launch_bounds__(256) fa_bwd_scale_kernel(const BwdArgs a) {
     // 2^e 2 D m.x m.y <= 65504 / 1.01 = 2^15.985; infinities leave 0, zeros 15
     const float room = floorf((D == 64 ? 8.985f : 7.985f) - (log2f(m.x) + log2f(m.y)));
     const float e = room > 0.f ? fminf(room, 15.f) : 0.f;    // (a NaN: 0)
-    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<int *>(part + a.parts) = static_cast<int>(e);
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *reinterpret_cast<int *>(part + a.parts) = static_cast<int>(e);
+        if (a.dsinks != nullptr)
+            for (int h = threadIdx.x; h < a.H; h += blockDim.x) a.dsinks[h] = exp2f(-e);
+    }
     while (i < n4) {
         float w[4];
 #pragma unroll
@@ -505,7 +510,7 @@ struct Ring {
 
 // 16-bit A x B^T over the full K = D: both tiles K-major (S = Q K^T style).  kBatch:
 // one election for four steps, or eight, instead of one each.  Interval masks at d = 64
-// (4 x 4096, 12 heads over 4: 739 us with one each, 730); at d = 128 long documents
+// (4 x 4096, 12 heads over 4, both directions: 739 us with one each, 730); at d = 128 long documents
 // lose 3 %, short ones nothing.
 template <int D, bool kBatch = false>
 __device__ __forceinline__ void gemm_ss_kmajor(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem,

@@ -72,7 +72,7 @@ cudaError_t launch_bwd_mask(const BwdLaunch &L);
 cudaError_t launch_bwd_mask_bias(const BwdLaunch &L);
 // Gradient of per-head sink logits: dsinks[h] = -sum_{b,i} 2^(sigma_h log2 e
 // - LSE2_i) D_i over the workspace rows of the backward (one CTA per head).  scaled:
-// the workspace holds LSE2 less a scale, and LSE2 comes from the LSE.
+// the workspace holds LSE2 less a scale, whose 2^-e dsinks bring.
 cudaError_t launch_bwd_dsink(const BwdArgs &a, const float *sinks, float *dsinks,
                              cudaStream_t stream, bool scaled = false);
 
