@@ -326,8 +326,9 @@ __device__ __forceinline__ float2 cta_max(float2 m, float2 (&warps)[8]) {
 // max|dO| max|V| (D is a mean of a row's dP): the largest e with 2^e times that below
 // 65504 / 1.01.  This kernel forms the maxima a CTA (a NaN drops out, an infinity leaves e
 // = 0); fa_bwd_scale_kernel joins them and writes LSE2 - e.  The maxima and e travel in
-// dq, which nobody writes before the dQ kernel: the dK/dV kernel's CTAs read e before they
-// let that one begin, and it has e from LSE2 and the LSE.
+// dq (8 bytes a CTA and 4; a CTA's rows are 128 bytes of dq at least), which nobody writes
+// before the dQ kernel: the dK/dV kernel's CTAs read e before they let that one begin, and
+// it has e from LSE2 - e and the LSE.
 template <int D, bool kBF16, bool kMask = false>
 __global__ void __launch_bounds__(256)
 fa_bwd_delta_kernel(const BwdArgs a) {

@@ -28,7 +28,8 @@ inline cudaError_t set_smem_once(K kern, int bytes, unsigned long long &configur
 
 // The three kernels of one backward, in order on the caller's stream.
 // kWin: the window instantiations (kCausal false); kCap: with a softcap.
-// kMask, kBias: a mask plan's intervals, the distance bias.
+// kMask, kBias: a mask plan's intervals, the distance bias; in fp16 with the kernel that
+// joins the scale behind the first.
 template <int D, bool kCausal, bool kBF16, bool kWin = false, bool kCap = false, bool kMask = false,
           bool kBias = false>
 cudaError_t launch_bwd_inst(const BwdLaunch &L) {

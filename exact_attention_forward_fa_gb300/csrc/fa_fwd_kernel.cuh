@@ -678,9 +678,9 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                                 C::CHUNK_BYTES, 1024u);
                             const uint32_t acc = (t - 1 > t0x) ? 1u : 0u;
                             // Interval masks: one election for four or eight steps.  At d = 64
-                            // this warp's issue is on the critical path (4 x 4096, 32 heads:
-                            // 615 us with one each, 609; with a bias 753 and 735); O and L in
-                            // turn by fours (by eights 612 and 742).
+                            // this warp's issue is on the critical path (4 x 4096, 32 heads,
+                            // both directions: 615 us with one each, 609); O and L in turn by
+                            // fours (by eights 612).
                             constexpr int kStepV = (C::PV_KEYS * 128) / 16;
                             if constexpr (kMask && C::kLMMA) {
 #pragma unroll

@@ -4,7 +4,8 @@
 // further blocks a sequence sort the unit lists by their number of tiles (counting
 // sort: which of two equally long units comes first may vary, no result depends on
 // it).  Measured (GB300): 6 us for 2 x 8192 tokens (8 under the profiler, cold), the
-// latency of the sorting blocks' dependent loads; it writes 16 bytes a token.
+// latency of the sorting blocks' dependent loads; it writes 16 bytes a token, 20 with the
+// positions (which the torch wrapper always takes).
 #include "fa_mask.cuh"
 #include "fa_paged.cuh"
 

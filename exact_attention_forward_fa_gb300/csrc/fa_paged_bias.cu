@@ -2,7 +2,8 @@
 // q_i k_j - beta_h |p_i - j| for a row at place p_i.  Measured (GB300): 64 single tokens of
 // 32 heads over 8 on up to 8192 cached ones (bf16, d 128) 172 us and the joining kernel 3.3, as without
 // a bias (HBM, 6.3 TB/s; eight FMAs a key and thread); 24 sequences of 1 to 300 new tokens
-// on up to 4096 (fp16) 90 us and 8.6 (82 without), bound by each tile's chain.
+// on up to 4096 (fp16) 101 to 103 us with the joining kernel (10; without a bias 92 with it),
+// bound by each tile's chain and the code's footprint (d 128: spills of 184 bytes stored and 220 loaded).
 #include "fa_paged_launch.cuh"
 
 namespace fa {

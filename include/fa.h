@@ -579,9 +579,12 @@ long long fa_mask_plan_bytes(int B, int N);
  *   sinks : as fa_fwd_ext, or NULL (a row that sees nothing then has
  *          LSE = sink).
  *   alpha : positive.  d in {64, 128}.
- * Accumulation and rounding as fa_fwd.  Key tiles that no row of a Q tile sees
- * are neither loaded nor computed; units run in a dynamic order as fa_fwd's
- * causal launches do.
+ * Accumulation and rounding as fa_fwd: P is rounded to `dtype` beside a reference of
+ * the row.  In fp16, weights below 2^-14 of the row's largest are spaced by 2^-24 of
+ * it in O (below 2^-10 by 2^-20 where a bias rises towards the keys to come); LSE
+ * sums them in FP32.
+ * Key tiles that no row of a Q tile sees are neither loaded nor computed; units run
+ * in a dynamic order as fa_fwd's causal launches do.
  */
 fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, float *lse,
                         const void *plan, const float *slopes, const float *sinks, int B,
@@ -591,7 +594,7 @@ fa_status fa_fwd_masked(const void *q, const void *k, const void *v, void *o, fl
 
 /*
  * fa_bwd_masked -- its gradients, as fa_bwd_ext's: P recomputed from the LSE, the
- * three kernels of fa_bwd.
+ * three kernels of fa_bwd (in fp16 a small fourth).
  *   q, k, v, plan, slopes, sinks, alpha : the forward's; o, lse its outputs.
  *   o, dout, dq : device, [B][N][H][d]; dk, dv : [B][N][H_kv][d], contiguous;
  *          dk and dv sum the gradients of their group's query heads in FP32.
