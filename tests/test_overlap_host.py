@@ -8,7 +8,7 @@ from tests.test_masked_host import A, INV, LAUNCH, M, _bwd, _fwd, _rappend, lib 
 
 # sizes of these calls' tensors in bytes: q, o, dq and dout 2 x 300 x 4 x 64 x 2, k, v, dk, dv half of it,
 # lse 2 x 4 x 300 x 4, the plan's in fa_mask_plan_bytes; pages 4 x 2048 x 2
-WQ, WK, LSE, POOL = 307200, 153600, 9600, 16384
+WQ, WK, LSE, POOL = 2 * 300 * 4 * 64 * 2, 2 * 300 * 2 * 64 * 2, 2 * 4 * 300 * 4, 4 * 2048 * 2
 
 
 @pytest.mark.parametrize("lse", [A, A + 4, A + WQ - 4, A + M + WK - 4, A + 2 * M + 16, A + 3 * M, A + 3 * M + WQ - 4,
